@@ -195,11 +195,11 @@ def cost_key(name: str) -> str:
 
 def source_digest() -> str:
     """Digest of the sources the SSD kernels are built from (every csrc file but
-    the Mamba-3 kernels', which no SSD launch uses): `traffic.json` figures
-    apply while it matches."""
+    the Mamba-3, delta-rule and norm kernels', which no SSD launch uses):
+    `traffic.json` figures apply while it matches."""
     h = hashlib.sha256()
     for f in sorted(glob.glob(os.path.join(ROOT, "state_space_model_mamba_gb300", "csrc", "*"))):
-        if os.path.basename(f) == "mamba3.cu":
+        if os.path.basename(f).startswith(("mamba3", "delta_", "norm")):
             continue
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())

@@ -1,0 +1,172 @@
+// delta_api.cu -- the C ABI declared in include/delta.h: argument checks,
+// workspace carving and the launch sequences of the gated delta rule.
+#include <stdarg.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "delta_internal.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+ssd_status fail(ssd_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+ssd_status fail(ssd_status st, const char *fmt, ...) {
+    char msg[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof(msg), fmt, ap);
+    va_end(ap);
+    record_error(msg);
+    return st;
+}
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+ssd_status validate(const delta_dims *d, ssd_dtype dt) {
+    if (!d) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    if (dt != SSD_F32 && dt != SSD_BF16) return fail(SSD_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (d->reserved != 0) return fail(SSD_ERR_INVALID_ARG, "dims.reserved must be 0");
+    if (d->flags & ~(uint32_t)DELTA_FLAG_SIMT) return fail(SSD_ERR_INVALID_ARG, "unknown flags 0x%x", d->flags);
+    if (d->batch < 1 || d->seqlen < 1 || d->nheads < 1 || d->headdim < 1 || d->dstate < 1 || d->ngroups < 1)
+        return fail(SSD_ERR_INVALID_ARG, "every dimension must be >= 1");
+    if (d->nheads % d->ngroups != 0)
+        return fail(SSD_ERR_INVALID_ARG, "nheads (%lld) must be a multiple of ngroups (%lld)", (long long)d->nheads,
+                    (long long)d->ngroups);
+    if (d->headdim > 128 || d->headdim % 4 != 0)
+        return fail(SSD_ERR_UNSUPPORTED, "headdim %lld: need a multiple of 4 <= 128", (long long)d->headdim);
+    if (d->dstate > 256 || d->dstate % 4 != 0)
+        return fail(SSD_ERR_UNSUPPORTED, "dstate %lld: need a multiple of 4 <= 256", (long long)d->dstate);
+    // index and grid limits
+    if (d->seqlen > (1LL << 30) || d->batch > (1LL << 24) || d->nheads > (1LL << 20) ||
+        (double)d->batch * d->nheads * ((d->seqlen + 63) / 64) > 2.0e9 || (double)d->batch * d->nheads > 2.0e8 ||
+        (double)d->batch * d->seqlen * d->nheads * 256.0 > 4.0e11)
+        return fail(SSD_ERR_UNSUPPORTED, "problem too large");
+    return SSD_OK;
+}
+
+ssd_status check_pointers(const void *const *req, const char *const *names, int nreq, const void *const *opt, int nopt) {
+    for (int i = 0; i < nreq; ++i) {
+        if (!req[i]) return fail(SSD_ERR_INVALID_ARG, "%s is NULL", names[i]);
+        if (!aligned16(req[i])) return fail(SSD_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+    }
+    for (int i = 0; i < nopt; ++i)
+        if (opt[i] && !aligned16(opt[i])) return fail(SSD_ERR_INVALID_ARG, "state pointers must be 16-byte aligned");
+    return SSD_OK;
+}
+
+ssd_status cuda_status(cudaError_t e) {
+    return e == cudaSuccess ? SSD_OK : fail(SSD_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+}
+
+constexpr size_t kStatusBytes = 256;  // status words, then the paths' own buffers
+
+DeltaParams base_params(const delta_dims &d, const void *q, const void *k, const void *v, const float *g,
+                        const float *beta, float scale, const float *init, const int32_t *valid_len, void *ws) {
+    DeltaParams p;
+    memset(&p, 0, sizeof(p));
+    p.b = (int)d.batch;
+    p.L = (int)d.seqlen;
+    p.H = (int)d.nheads;
+    p.P = (int)d.headdim;
+    p.N = (int)d.dstate;
+    p.G = (int)d.ngroups;
+    p.hpg = p.H / p.G;
+    p.scale = scale;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.init = init;
+    p.valid_len = valid_len;
+    p.status = (int *)ws;
+    return p;
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace ssd
+
+using namespace ssd;
+using namespace ssd::delta;
+
+extern "C" {
+
+ssd_status delta_supported(const delta_dims *dims, ssd_dtype dtype) {
+    record_error("");
+    return validate(dims, dtype);
+}
+
+size_t delta_workspace_bytes(const delta_dims *dims, ssd_dtype dtype, int backward) {
+    record_error("");
+    if (validate(dims, dtype) != SSD_OK) return 0;
+    return kStatusBytes + (backward ? simt_backward_bytes(*dims) : 0);
+}
+
+ssd_status delta_forward(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
+                         const float *g, const float *beta, float scale, const float *init_state,
+                         const int32_t *valid_len, void *o, float *final_state, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    record_error("");
+    ssd_status st = validate(dims, dtype);
+    if (st != SSD_OK) return st;
+    const void *req[] = {q, k, v, g, beta, o, workspace};
+    static const char *const names[] = {"q", "k", "v", "g", "beta", "o", "workspace"};
+    const void *opt[] = {init_state, final_state};
+    if ((st = check_pointers(req, names, 7, opt, 2)) != SSD_OK) return st;
+    const size_t need = delta_workspace_bytes(dims, dtype, 0);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    DeltaParams p = base_params(*dims, q, k, v, g, beta, scale, init_state, valid_len, workspace);
+    p.o = o;
+    p.final_state = final_state;
+    return cuda_status(launch_simt_forward(p, dtype == SSD_BF16, (cudaStream_t)stream));
+}
+
+ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
+                          const float *g, const float *beta, float scale, const float *init_state,
+                          const int32_t *valid_len, const void *d_o, const float *d_final_state, void *dq, void *dk,
+                          void *dv, float *dg, float *dbeta, float *d_init_state, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    record_error("");
+    ssd_status st = validate(dims, dtype);
+    if (st != SSD_OK) return st;
+    const void *req[] = {q, k, v, g, beta, d_o, dq, dk, dv, dg, dbeta, workspace};
+    static const char *const names[] = {"q", "k", "v", "g", "beta", "do", "dq", "dk", "dv", "dg", "dbeta", "workspace"};
+    const void *opt[] = {init_state, d_final_state, d_init_state};
+    if ((st = check_pointers(req, names, 12, opt, 3)) != SSD_OK) return st;
+    const size_t need = delta_workspace_bytes(dims, dtype, 1);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    DeltaParams p = base_params(*dims, q, k, v, g, beta, scale, init_state, valid_len, workspace);
+    p.d_o = d_o;
+    p.d_final = d_final_state;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dg = dg;
+    p.dbeta = dbeta;
+    p.d_init = d_init_state;
+    return cuda_status(launch_simt_backward(p, dtype == SSD_BF16, (char *)workspace + kStatusBytes, (cudaStream_t)stream));
+}
+
+ssd_status delta_step(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
+                      const float *g, const float *beta, float scale, float *state, int64_t slots,
+                      const int32_t *state_index, void *o, void *stream) {
+    record_error("");
+    ssd_status st = validate(dims, dtype);
+    if (st != SSD_OK) return st;
+    if (dims->seqlen != 1) return fail(SSD_ERR_INVALID_ARG, "delta_step takes one token: seqlen must be 1");
+    const void *req[] = {q, k, v, g, beta, state, o};
+    static const char *const names[] = {"q", "k", "v", "g", "beta", "state", "o"};
+    if ((st = check_pointers(req, names, 7, nullptr, 0)) != SSD_OK) return st;
+    if (slots < 1 || slots > (1LL << 31)) return fail(SSD_ERR_INVALID_ARG, "slots %lld out of range", (long long)slots);
+    if (!state_index && slots < dims->batch)
+        return fail(SSD_ERR_INVALID_ARG, "%lld slots for a batch of %lld without state_index", (long long)slots,
+                    (long long)dims->batch);
+    DeltaParams p = base_params(*dims, q, k, v, g, beta, scale, nullptr, nullptr, nullptr);
+    p.o = o;
+    return cuda_status(launch_step(p, dtype == SSD_BF16, state, slots, state_index, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,451 @@
+// delta_simt.cu -- the gated delta rule token by token on CUDA cores: the fp32
+// path, shapes outside the tensor-core kernels, and the one-token step.
+//
+// Every row p of the state S [P, N] is a recurrence of its own,
+//     s <- a s + beta (v_p - a s.k) k,   o_p = scale s.q,
+// so rows are spread over the grid: 8 lanes hold one row (N / 8 elements each
+// in registers, 4-element pieces interleaved over the lanes so that a row's
+// load is one 128-byte line per piece), 32 rows a block.  What bounds the
+// sequence kernels is the latency of one token (two dependent 8-lane sums),
+// about 150 cycles; the step kernel reads and writes each state once and is
+// bound by HBM.
+#include <stdio.h>
+
+#include "delta_internal.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+constexpr int kRows = 32;   // state rows per block
+constexpr int kLanes = 8;   // lanes per row
+constexpr int kThreads = kRows * kLanes;
+// Tokens staged in shared memory at a time, also the tokens between kept states of the backward
+// (8 for wide keys: the backward's stage and reduction buffers stay within 48 KB).
+constexpr int tok_of(int nc) { return nc > 4 ? 8 : 16; }
+
+__device__ __forceinline__ float sum8(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    return x;
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+__device__ __forceinline__ float4 axpy4(float a, float4 x, float4 y) {
+    return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+}
+__device__ __forceinline__ float4 scale4(float a, float4 x) { return make_float4(a * x.x, a * x.y, a * x.z, a * x.w); }
+
+// Tokens [t0, t0 + nt) of one (b, h, row block) in shared memory: q and k rows
+// (N, zero-padded to 32 NC), v (and do) of the block's rows, decay and beta.
+template <int NC, bool BWD>
+struct Stage {
+    static constexpr int kTok = tok_of(NC);
+    float4 q[kTok][NC * kLanes], k[kTok][NC * kLanes];
+    float v[kTok][kRows];
+    float dO[BWD ? kTok : 1][kRows];
+    float a[kTok], beta[kTok];
+};
+
+template <typename T, int NC, bool BWD>
+__device__ __forceinline__ void load_stage(Stage<NC, BWD> &s, const DeltaParams &p, int bi, int h, int row0, int t0,
+                                           int nt) {
+    const int g = h / p.hpg, nq = p.N / 4;
+    const T *q = (const T *)p.q, *k = (const T *)p.k, *v = (const T *)p.v;
+    for (int i = threadIdx.x; i < nt * NC * kLanes; i += kThreads) {
+        const int t = i / (NC * kLanes), c = i % (NC * kLanes);
+        const long long at = (((long long)bi * p.L + t0 + t) * p.G + g) * p.N + 4 * c;
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        s.q[t][c] = c < nq ? load4(q + at) : z;
+        s.k[t][c] = c < nq ? load4(k + at) : z;
+    }
+    for (int i = threadIdx.x; i < nt * kRows; i += kThreads) {
+        const int t = i / kRows, r = i % kRows;
+        const long long at = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r;
+        const bool in = row0 + r < p.P;
+        s.v[t][r] = in ? load1(v + at) : 0.f;
+        if (BWD) s.dO[t][r] = in ? p.scale * load1((const T *)p.d_o + at) : 0.f;
+    }
+    if (threadIdx.x < nt) {
+        const long long at = ((long long)bi * p.H + h) * p.L + t0 + threadIdx.x;
+        s.a[threadIdx.x] = expf(clamp_log_decay(p.g[at]));
+        s.beta[threadIdx.x] = p.beta[at];
+    }
+}
+
+template <int NC>
+__device__ __forceinline__ void load_row(float4 (&s)[NC], const float *src, bool in, int N, int lane) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 4 * (i * kLanes + lane);
+        s[i] = (src && in && c < N) ? *(const float4 *)(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+template <int NC>
+__device__ __forceinline__ void store_row(const float4 (&s)[NC], float *dst, bool in, int N, int lane) {
+    if (!dst || !in) return;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 4 * (i * kLanes + lane);
+        if (c < N) *(float4 *)(dst + c) = s[i];
+    }
+}
+
+// ------------------------------------------------------------------ forward
+// Grid: one block per (b, h, row block).  `kept`, when given, gets the state before
+// every segment of tok_of(NC) tokens ([b, H, segments, P, N]), for the backward.
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float *kept, int nseg) {
+    constexpr int kTok = tok_of(NC);
+    __shared__ Stage<NC, false> st;
+    __shared__ float out[kTok][kRows];
+    const int nblk = (p.P + kRows - 1) / kRows, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H;
+    const int row0 = (blockIdx.x % nblk) * kRows;
+    const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const bool in = row0 + row < p.P;
+    const int V = valid_tokens(p, bi);
+    if (blockIdx.x == 0) write_status(p);
+    const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
+    float4 s[NC];
+    load_row(s, p.init ? p.init + srow : nullptr, in, p.N, lane);
+    for (int t0 = 0; t0 < V; t0 += kTok) {
+        const int nt = min(kTok, V - t0);
+        __syncthreads();
+        load_stage<T>(st, p, bi, h, row0, t0, nt);
+        if (kept)
+            store_row(s, kept + (((long long)bh * nseg + t0 / kTok) * p.P + row0 + row) * p.N, in, p.N, lane);
+        __syncthreads();
+        for (int t = 0; t < nt; ++t) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) d += dot4(s[i], st.k[t][i * kLanes + lane]);
+            const float a = st.a[t];
+            const float u = st.beta[t] * (st.v[t][row] - a * sum8(d));
+            float od = 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                s[i] = axpy4(u, st.k[t][i * kLanes + lane], scale4(a, s[i]));
+                od += dot4(s[i], st.q[t][i * kLanes + lane]);
+            }
+            od = sum8(od);
+            if (lane == 0) out[t][row] = p.scale * od;
+        }
+        __syncthreads();
+        if (p.o)
+            for (int i = threadIdx.x; i < nt * kRows; i += kThreads) {
+                const int t = i / kRows, r = i % kRows;
+                if (row0 + r < p.P)
+                    store1((T *)p.o + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r, out[t][r]);
+            }
+    }
+    if (p.o)
+        for (int i = threadIdx.x; i < (p.L - V) * kRows; i += kThreads) {
+            const int t = V + i / kRows, r = i % kRows;
+            if (row0 + r < p.P) store1((T *)p.o + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
+        }
+    store_row(s, p.final_state ? p.final_state + srow : nullptr, in, p.N, lane);
+}
+
+// ------------------------------------------------------------------ backward
+// Reverse over the tokens with the adjoint D of the state in registers.  With
+// Sd = a S_{t-1}, z = v - Sd k and S_t = Sd + beta z k^T:
+//     D += do q^T;   dbeta = (D k).z;   dz = beta D k = dv;
+//     dk = beta z^T D - dz^T Sd;   dq = do^T S_t;   D -= dz k^T;
+//     dg = <D, Sd>;   D *= a.
+// The states inside a segment are formed again from the kept one and stored
+// per block in `hist` (each element written and read by one thread).  Sums over
+// the rows (dq, dk, dbeta, dg) go to per-row-block partials, which
+// delta_rows_reduce adds in a fixed order.
+struct BwdBuffers {
+    float *kept, *hist, *part_q, *part_k, *part_g, *part_b;
+    int nseg, nblk, items;
+};
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
+    constexpr int kSegTok = tok_of(NC);
+    __shared__ Stage<NC, true> st;
+    __shared__ float zs[kSegTok][kRows];
+    __shared__ float4 red[2][kThreads / 32][NC * kLanes];
+    __shared__ float red1[2][kThreads / 32];
+    const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, warp = threadIdx.x / 32;
+    float4 *hist = (float4 *)w.hist + (size_t)blockIdx.x * kSegTok * NC * kThreads + threadIdx.x;
+    for (int item = blockIdx.x; item < w.items; item += gridDim.x) {
+        const int bh = item / w.nblk, blk = item % w.nblk, bi = bh / p.H, h = bh % p.H, row0 = blk * kRows;
+        const bool in = row0 + row < p.P;
+        const int V = valid_tokens(p, bi);
+        const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
+        float4 D[NC], s[NC];
+        load_row(D, p.d_final ? p.d_final + srow : nullptr, in, p.N, lane);
+        for (int seg = (V + kSegTok - 1) / kSegTok - 1; seg >= 0; --seg) {
+            const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
+            __syncthreads();
+            load_stage<T>(st, p, bi, h, row0, t0, nt);
+            load_row(s, w.kept + (((long long)bh * w.nseg + seg) * p.P + row0 + row) * p.N, in, p.N, lane);
+            __syncthreads();
+            for (int t = 0; t < nt; ++t) {
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    s[i] = scale4(st.a[t], s[i]);
+                    hist[(t * NC + i) * kThreads] = s[i];
+                    d += dot4(s[i], st.k[t][i * kLanes + lane]);
+                }
+                const float z = st.v[t][row] - sum8(d);
+                if (lane == 0) zs[t][row] = z;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) s[i] = axpy4(st.beta[t] * z, st.k[t][i * kLanes + lane], s[i]);
+            }
+            __syncwarp();
+            for (int t = nt - 1; t >= 0; --t) {
+                const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = zs[t][row];
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    D[i] = axpy4(dO, st.q[t][i * kLanes + lane], D[i]);
+                    d += dot4(D[i], st.k[t][i * kLanes + lane]);
+                }
+                d = sum8(d);
+                const float dz = be * d, bz = be * z;
+                if (lane == 0 && in)
+                    store1((T *)p.dv + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + row, dz);
+                float dg = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const float4 sd = hist[(t * NC + i) * kThreads], kk = st.k[t][i * kLanes + lane];
+                    float4 dq = scale4(dO, axpy4(bz, kk, sd));
+                    float4 dk = axpy4(bz, D[i], scale4(-dz, sd));
+                    D[i] = axpy4(-dz, kk, D[i]);
+                    dg += dot4(D[i], sd);
+                    D[i] = scale4(a, D[i]);
+                    // the warp's four rows
+#pragma unroll
+                    for (int o = 8; o <= 16; o <<= 1) {
+                        dq.x += __shfl_xor_sync(0xffffffffu, dq.x, o);
+                        dq.y += __shfl_xor_sync(0xffffffffu, dq.y, o);
+                        dq.z += __shfl_xor_sync(0xffffffffu, dq.z, o);
+                        dq.w += __shfl_xor_sync(0xffffffffu, dq.w, o);
+                        dk.x += __shfl_xor_sync(0xffffffffu, dk.x, o);
+                        dk.y += __shfl_xor_sync(0xffffffffu, dk.y, o);
+                        dk.z += __shfl_xor_sync(0xffffffffu, dk.z, o);
+                        dk.w += __shfl_xor_sync(0xffffffffu, dk.w, o);
+                    }
+                    if ((threadIdx.x & 31) < kLanes) {
+                        red[0][warp][i * kLanes + lane] = dq;
+                        red[1][warp][i * kLanes + lane] = dk;
+                    }
+                }
+                // over the warp: every lane has its share of dg, lane 0 of each row its dbeta
+                float db = lane == 0 ? d * z : 0.f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    dg += __shfl_xor_sync(0xffffffffu, dg, o);
+                    db += __shfl_xor_sync(0xffffffffu, db, o);
+                }
+                if ((threadIdx.x & 31) == 0) {
+                    red1[0][warp] = dg;
+                    red1[1][warp] = db;
+                }
+                __syncthreads();
+                const long long tok = ((long long)blk * p.b * p.H + bh) * p.L + t0 + t;
+                for (int i = threadIdx.x; i < 2 * NC * kLanes; i += kThreads) {
+                    const int which = i / (NC * kLanes), c = i % (NC * kLanes);
+                    float4 acc = red[which][0][c];
+                    for (int x = 1; x < kThreads / 32; ++x) {
+                        const float4 r = red[which][x][c];
+                        acc = make_float4(acc.x + r.x, acc.y + r.y, acc.z + r.z, acc.w + r.w);
+                    }
+                    if (4 * c < p.N) *(float4 *)((which ? w.part_k : w.part_q) + tok * p.N + 4 * c) = acc;
+                }
+                if (threadIdx.x >= kThreads - 2) {
+                    const int which = threadIdx.x - (kThreads - 2);
+                    float acc = 0.f;
+                    for (int x = 0; x < kThreads / 32; ++x) acc += red1[which][x];
+                    (which ? w.part_b : w.part_g)[tok] = acc;
+                }
+                __syncthreads();
+            }
+        }
+        store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
+        for (int i = threadIdx.x; i < (p.L - V) * kRows; i += kThreads) {
+            const int t = V + i / kRows, r = i % kRows;
+            if (row0 + r < p.P) store1((T *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
+        }
+    }
+}
+
+// dq, dk: the partials of a group's heads and their row blocks; dg, dbeta: of
+// the row blocks.  One thread per output element, a fixed order of addition.
+template <typename T>
+__global__ void delta_rows_reduce(DeltaParams p, BwdBuffers w) {
+    const long long nqk = (long long)p.b * p.L * p.G * p.N, ngt = (long long)p.b * p.H * p.L;
+    const long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x;
+    const long long per = (long long)p.b * p.H * p.L;
+    if (i < nqk) {
+        const int n = i % p.N, g = (i / p.N) % p.G;
+        const long long bt = i / ((long long)p.N * p.G);
+        const int t = bt % p.L, bi = bt / p.L;
+        float aq = 0.f, ak = 0.f;
+        if (t < valid_tokens(p, bi))
+            for (int h = g * p.hpg; h < (g + 1) * p.hpg; ++h)
+                for (int x = 0; x < w.nblk; ++x) {
+                    const long long at = (x * per + ((long long)bi * p.H + h) * p.L + t) * p.N + n;
+                    aq += w.part_q[at];
+                    ak += w.part_k[at];
+                }
+        store1((T *)p.dq + i, aq);
+        store1((T *)p.dk + i, ak);
+    }
+    if (i < ngt) {
+        const int t = i % p.L, bi = i / ((long long)p.L * p.H);
+        float ag = 0.f, ab = 0.f;
+        if (t < valid_tokens(p, bi))
+            for (int x = 0; x < w.nblk; ++x) {
+                ag += w.part_g[x * per + i];
+                ab += w.part_b[x * per + i];
+            }
+        p.dg[i] = ag;
+        p.dbeta[i] = ab;
+    }
+}
+
+// ------------------------------------------------------------------ one token
+// Grid: one block per (b, h, row block).  Each state element is read and written once, in
+// 16-byte pieces, NC of them in flight per thread.
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaParams p, float *state, long long slots,
+                                                              const int32_t *index) {
+    const int nblk = (p.P + kRows - 1) / kRows, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H, g = h / p.hpg;
+    const int row = (blockIdx.x % nblk) * kRows + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const bool in = row < p.P;
+    const long long slot = index ? (long long)index[bi] : (long long)bi;
+    const long long vat = ((long long)bi * p.H + h) * p.P + row;
+    if (slot < 0 || slot >= slots) {
+        if (in && lane == 0) store1((T *)p.o + vat, 0.f);
+        return;
+    }
+    float *srow = state + ((slot * p.H + h) * p.P + row) * (long long)p.N;
+    float4 s[NC], k[NC], q[NC];
+    load_row(s, srow, in, p.N, lane);
+    const long long kat = ((long long)bi * p.G + g) * p.N;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 4 * (i * kLanes + lane);
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        k[i] = c < p.N ? load4((const T *)p.k + kat + c) : zero;
+        q[i] = c < p.N ? load4((const T *)p.q + kat + c) : zero;
+    }
+    const float a = expf(clamp_log_decay(p.g[bi * (long long)p.H + h])), be = p.beta[bi * (long long)p.H + h];
+    const float v = in ? load1((const T *)p.v + vat) : 0.f;
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) d += dot4(s[i], k[i]);
+    const float u = be * (v - a * sum8(d));
+    float od = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        s[i] = axpy4(u, k[i], scale4(a, s[i]));
+        od += dot4(s[i], q[i]);
+    }
+    od = sum8(od);
+    store_row(s, srow, in, p.N, lane);
+    if (in && lane == 0) store1((T *)p.o + vat, p.scale * od);
+}
+
+int row_blocks(int P) { return (P + kRows - 1) / kRows; }
+constexpr int kBwdBlocks = 304;  // two per SM: bounds the history buffer
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+struct BwdSizes {
+    size_t kept, hist, part, gate, total;
+    int nseg, nblk, grid;
+};
+BwdSizes bwd_sizes(long long b, long long L, long long H, long long P, long long N) {
+    BwdSizes z;
+    const size_t nc = (size_t)(N + 31) / 32;
+    const int seg = tok_of((int)nc);
+    z.nseg = (int)((L + seg - 1) / seg);
+    z.nblk = row_blocks((int)P);
+    const long long items = b * H * z.nblk;
+    z.grid = (int)(items < kBwdBlocks ? items : kBwdBlocks);
+    z.kept = up256(4ull * b * H * z.nseg * P * N);
+    z.hist = up256(16ull * z.grid * seg * nc * kThreads);
+    z.part = up256(4ull * z.nblk * b * H * L * N);
+    z.gate = up256(4ull * z.nblk * b * H * L);
+    z.total = z.kept + z.hist + 2 * z.part + 2 * z.gate;
+    return z;
+}
+
+#define DELTA_BY_NC(CALL)              \
+    switch ((p.N + 31) / 32) {         \
+        case 1: CALL(1); break;        \
+        case 2: CALL(2); break;        \
+        case 3: CALL(3); break;        \
+        case 4: CALL(4); break;        \
+        case 5: CALL(5); break;        \
+        case 6: CALL(6); break;        \
+        case 7: CALL(7); break;        \
+        default: CALL(8); break;       \
+    }
+
+template <typename T>
+cudaError_t fwd(const DeltaParams &p, float *kept, int nseg, cudaStream_t s) {
+    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P));
+#define CALL(NC) delta_rows_fwd<T, NC><<<grid, kThreads, 0, s>>>(p, kept, nseg)
+    DELTA_BY_NC(CALL)
+#undef CALL
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
+    const BwdSizes z = bwd_sizes(p.b, p.L, p.H, p.P, p.N);
+    BwdBuffers w;
+    w.kept = (float *)ws;
+    w.hist = (float *)(ws + z.kept);
+    w.part_q = (float *)(ws + z.kept + z.hist);
+    w.part_k = (float *)(ws + z.kept + z.hist + z.part);
+    w.part_g = (float *)(ws + z.kept + z.hist + 2 * z.part);
+    w.part_b = (float *)(ws + z.kept + z.hist + 2 * z.part + z.gate);
+    w.nseg = z.nseg;
+    w.nblk = z.nblk;
+    w.items = p.b * p.H * z.nblk;
+    DeltaParams f = p;
+    f.o = nullptr;
+    f.final_state = nullptr;
+    cudaError_t e = fwd<T>(f, w.kept, w.nseg, s);
+    if (e != cudaSuccess) return e;
+#define CALL(NC) delta_rows_bwd<T, NC><<<z.grid, kThreads, 0, s>>>(p, w)
+    DELTA_BY_NC(CALL)
+#undef CALL
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long nqk = (long long)p.b * p.L * p.G * p.N, ngt = (long long)p.b * p.H * p.L;
+    const long long most = nqk > ngt ? nqk : ngt;
+    delta_rows_reduce<T><<<(unsigned)((most + 255) / 256), 256, 0, s>>>(p, w);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t step(const DeltaParams &p, float *state, long long slots, const int32_t *index, cudaStream_t s) {
+    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P));
+#define CALL(NC) delta_step_kernel<T, NC><<<grid, kThreads, 0, s>>>(p, state, slots, index)
+    DELTA_BY_NC(CALL)
+#undef CALL
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t simt_backward_bytes(const delta_dims &d) { return bwd_sizes(d.batch, d.seqlen, d.nheads, d.headdim, d.dstate).total; }
+
+cudaError_t launch_simt_forward(const DeltaParams &p, bool is_bf16, cudaStream_t s) {
+    return is_bf16 ? fwd<bf16>(p, nullptr, 0, s) : fwd<float>(p, nullptr, 0, s);
+}
+cudaError_t launch_simt_backward(const DeltaParams &p, bool is_bf16, char *ws, cudaStream_t s) {
+    return is_bf16 ? bwd<bf16>(p, ws, s) : bwd<float>(p, ws, s);
+}
+cudaError_t launch_step(const DeltaParams &p, bool is_bf16, float *state, long long slots, const int32_t *index,
+                        cudaStream_t s) {
+    return is_bf16 ? step<bf16>(p, state, slots, index, s) : step<float>(p, state, slots, index, s);
+}
+
+}  // namespace delta
+}  // namespace ssd

@@ -1,0 +1,269 @@
+"""GPU parity of the gated delta rule (include/delta.h), through the C ABI,
+against the token-by-token fp64 oracle (oracle/delta.py).
+
+Bars, as normwise relative errors of whole outputs:
+  * fp32 storage: a handful of fp32 roundings (2^-24) a token over the at most
+    ~100 tokens that a contracting state remembers, and sums over N <= 256: 1e-5;
+  * bf16 storage, bf16 outputs: one rounding at the end (2^-8 at most, 1.7e-3
+    root-mean-square) and operands rounded once on the way (as much again, in
+    quadrature): 2^-8;
+  * bf16 storage, fp32 outputs (final_state, dg, dbeta, d_init): operands held
+    as two bf16 (2^-17 off at most) through three chained products: 3 * 2^-17.
+Slices along the leading axes are held to four times the bar, their norms
+floored at a tenth of the tensor's RMS slice norm."""
+import numpy as np
+import pytest
+
+from oracle import delta as od
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F32_BAR, BF16_BAR, SPLIT_BAR = 1e-5, 2.0 ** -8, 3 * 2.0 ** -17
+
+
+@pytest.fixture(scope="module")
+def dl():
+    from state_space_model_mamba_gb300 import delta
+    return delta
+
+
+def draw(b, L, H, P, N, G, seed, dt_mu=-3.0, bf16=True, relu_keys=False):
+    r = np.random.default_rng(seed)
+
+    def store(x):
+        t = torch.from_numpy(np.ascontiguousarray(x, np.float32))
+        return t.bfloat16().float().numpy() if bf16 else t.numpy()
+
+    def unit(x):
+        x = np.maximum(x, 0.05) if relu_keys else x / (1 + np.exp(-x))
+        return store(x / np.linalg.norm(x, axis=-1, keepdims=True))
+
+    f = np.float32
+    return dict(q=unit(r.standard_normal((b, L, G, N))), k=unit(r.standard_normal((b, L, G, N))),
+                v=store(r.standard_normal((b, L, H, P))),
+                g=(-np.exp(r.uniform(0, np.log(16), H))[None, :, None]
+                   * np.logaddexp(0, r.standard_normal((b, H, L)) + dt_mu)).astype(f),
+                beta=(1 / (1 + np.exp(-r.standard_normal((b, H, L))))).astype(f),
+                init=(0.3 * r.standard_normal((b, H, P, N))).astype(f), do=store(r.standard_normal((b, L, H, P))),
+                d_final=r.standard_normal((b, H, P, N)).astype(f))
+
+
+def dev(x, bf16):
+    T = torch.bfloat16 if bf16 else torch.float32
+    return {k: torch.from_numpy(a).cuda().to(T if k in ("q", "k", "v", "do") else torch.float32) for k, a in x.items()}
+
+
+def check(got, ref, bar, what, axes):
+    got = got.double().cpu().numpy()
+    assert got.shape == ref.shape and np.isfinite(got).all(), what
+    d = got - ref
+    n = np.linalg.norm(ref)
+    whole = np.linalg.norm(d) / n if n else np.linalg.norm(d)
+    assert whole <= bar, f"{what}: {whole:.3e} > {bar:.3e}"
+    m = int(np.prod(ref.shape[:axes]))
+    rn = np.linalg.norm(ref.reshape(m, -1), axis=1)
+    floor = max(0.1 * np.sqrt(np.mean(rn ** 2)), 1e-30)
+    worst = np.max(np.linalg.norm(d.reshape(m, -1), axis=1) / np.maximum(rn, floor))
+    assert worst <= 4 * bar, f"{what}, worst slice: {worst:.3e} > {4 * bar:.3e}"
+
+
+def run(dl, x, bf16, scale, init=True, valid=None, backward=True, simt=False, d_final=True):
+    d = dev(x, bf16)
+    vl = None if valid is None else torch.tensor(valid, dtype=torch.int32, device="cuda")
+    a = (d["q"], d["k"], d["v"], d["g"], d["beta"])
+    out = dict(zip(("o", "final"), dl.delta_forward(*a, scale=scale, init_state=d["init"] if init else None,
+                                                    valid_len=vl, simt=simt)))
+    if backward:
+        out.update(dl.delta_backward(*a, d["do"], scale=scale, d_final_state=d["d_final"] if d_final else None,
+                                     init_state=d["init"] if init else None, valid_len=vl, simt=simt))
+    torch.cuda.synchronize()
+    return out
+
+
+def compare(out, x, bf16, scale, init=True, valid=None, d_final=True, split=True):
+    ini = x["init"] if init else None
+    o, S = od.delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], scale, ini, valid)
+    ref = dict(o=o, final=S)
+    if "dq" in out:
+        ref.update(od.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], scale, x["do"],
+                                     x["d_final"] if d_final else None, ini, valid))
+    for name, r in ref.items():
+        stored = name in ("o", "dq", "dk", "dv")
+        bar = F32_BAR if not bf16 else (BF16_BAR if stored else SPLIT_BAR)
+        check(out[name], r, bar, name, 2 if not stored else 3)
+
+
+# one token, chunk edges, ragged tails; padded and full key and value widths; shared and own keys
+SHAPES = [(1, 1, 1, 64, 128, 1), (2, 63, 2, 64, 64, 1), (1, 64, 4, 128, 128, 2), (2, 65, 2, 64, 128, 2),
+          (1, 130, 6, 96, 80, 2), (3, 200, 2, 8, 8, 1), (1, 257, 3, 128, 64, 3), (1, 700, 2, 64, 128, 1)]
+
+
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_bf16_forward_backward(dl, shape, simt):
+    x = draw(*shape, seed=sum(shape))
+    scale = shape[4] ** -0.5
+    compare(run(dl, x, True, scale, simt=simt), x, True, scale)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 4, 4, 1), (2, 37, 4, 12, 20, 2), (1, 100, 2, 128, 256, 1), (2, 70, 3, 36, 132, 3),
+                                   (1, 300, 2, 64, 128, 2), (2, 33, 2, 100, 196, 1)])
+@pytest.mark.parametrize("init", [True, False])
+def test_f32_forward_backward(dl, shape, init):
+    x = draw(*shape, seed=7 + sum(shape), bf16=False)
+    compare(run(dl, x, False, 0.5, init=init), x, False, 0.5, init=init)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("valid", [[150, 0, 1], [64, 128, 149], [63, 65, 2]])
+def test_valid_len_and_garbage_past_it(dl, bf16, valid):
+    x = draw(3, 150, 4, 64, 128, 2, seed=3, bf16=bf16)
+    y = {k: a.copy() for k, a in x.items()}
+    for i, n in enumerate(valid):  # absent tokens hold what must not be read into anything
+        for k in ("q", "k", "v", "do"):
+            y[k][i, n:] = np.nan
+        y["g"][i, :, n:], y["beta"][i, :, n:] = np.inf, np.nan
+    out = run(dl, y, bf16, 0.3, valid=valid)
+    compare(out, x, bf16, 0.3, valid=valid)
+    for i, n in enumerate(valid):
+        for k in ("o", "dq", "dk", "dv"):
+            assert torch.all(out[k][i, n:] == 0), k
+        for k in ("dg", "dbeta"):
+            assert torch.all(out[k][i, :, n:] == 0), k
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_no_state_no_final_gradient(dl, bf16):
+    x = draw(2, 129, 2, 64, 128, 1, seed=5, bf16=bf16)
+    compare(run(dl, x, bf16, 1.0, init=False, d_final=False), x, bf16, 1.0, init=False, d_final=False)
+
+
+@pytest.mark.parametrize("kind", ["no_decay", "reset", "minus_inf", "beta_zero", "beta_one", "same_key", "long_memory"])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_gates_and_keys_at_their_ends(dl, kind, bf16):
+    x = draw(2, 190, 2, 64, 128, 2, seed=11, bf16=bf16, relu_keys=kind == "same_key")
+    r = np.random.default_rng(1)
+    if kind == "no_decay":
+        x["g"][:] = 0.0
+    elif kind == "reset":        # a decay that forgets everything, at single tokens
+        x["g"][r.uniform(size=x["g"].shape) < 0.05] = -300.0
+    elif kind == "minus_inf":
+        x["g"][:, :, 70] = -np.inf
+        x["g"][:, 0, 64] = -np.inf
+    elif kind == "beta_zero":
+        x["beta"][r.uniform(size=x["beta"].shape) < 0.5] = 0.0
+        x["beta"][0, 0] = 0.0
+    elif kind == "beta_one":
+        x["beta"][:] = 1.0
+    elif kind == "same_key":     # strongly correlated keys
+        x["g"][:] *= 0.01
+    elif kind == "long_memory":
+        x["g"][:] = -1e-4
+        x["beta"][:] = 0.01
+    out = run(dl, x, bf16, 0.4)
+    with np.errstate(invalid="ignore"):
+        compare(out, x, bf16, 0.4)
+
+
+def test_step_matches_sequence_and_pool(dl):
+    for bf16 in (True, False):
+        for (b, H, P, N, G) in ((1, 4, 64, 128, 2), (5, 3, 40, 72, 1), (3, 2, 128, 256, 2), (2, 2, 4, 4, 1)):
+            x = draw(b, 6, H, P, N, G, seed=b + H, bf16=bf16)
+            d = dev(x, bf16)
+            r = np.random.default_rng(2)
+            pool = r.standard_normal((b + 4, H, P, N)).astype(np.float32)
+            idx = r.permutation(b + 4)[:b].astype(np.int32)
+            if b > 2:
+                idx[1], idx[2] = -1, b + 4  # absent requests
+            state, ref = torch.from_numpy(pool).cuda(), pool.astype(np.float64)
+            for t in range(6):
+                o = dl.delta_step(d["q"][:, t].contiguous(), d["k"][:, t].contiguous(), d["v"][:, t].contiguous(),
+                                  d["g"][:, :, t].contiguous(), d["beta"][:, :, t].contiguous(), state, scale=0.6,
+                                  state_index=torch.from_numpy(idx).cuda())
+                ro = od.delta_step(x["q"][:, t], x["k"][:, t], x["v"][:, t], x["g"][:, :, t], x["beta"][:, :, t], 0.6, ref, idx)
+                check(o, ro, BF16_BAR if bf16 else F32_BAR, "o", 1)
+            check(state, ref, F32_BAR, "state", 1)
+            if b > 2:
+                assert torch.all(o[1] == 0) and torch.all(o[2] == 0)
+            untouched = [i for i in range(b + 4) if i not in idx]
+            assert torch.equal(state[untouched].cpu(), torch.from_numpy(pool[untouched]))
+
+
+def test_prefill_then_steps(dl):
+    # the chunked forward's state continues token by token
+    x = draw(2, 150, 4, 64, 128, 2, seed=21)
+    d = dev(x, True)
+    cut = 133
+    part = [d[k][:, :cut].contiguous() for k in ("q", "k", "v")] + [d[k][:, :, :cut].contiguous() for k in ("g", "beta")]
+    o, state = dl.delta_forward(*part, scale=0.5, init_state=d["init"])
+    outs = [o]
+    for t in range(cut, 150):
+        outs.append(dl.delta_step(d["q"][:, t].contiguous(), d["k"][:, t].contiguous(), d["v"][:, t].contiguous(),
+                                  d["g"][:, :, t].contiguous(), d["beta"][:, :, t].contiguous(), state, scale=0.5)[:, None])
+    ro, rS = od.delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.5, x["init"])
+    check(torch.cat(outs, 1), ro, BF16_BAR, "o", 2)
+    check(state, rS, SPLIT_BAR, "state", 2)
+
+
+def test_same_inputs_same_bits_and_other_streams(dl):
+    x = draw(2, 300, 8, 64, 128, 2, seed=31)
+    first = run(dl, x, True, 0.2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = run(dl, x, True, 0.2)
+    for k in first:
+        assert torch.equal(first[k], second[k]), k
+
+
+def test_backward_against_differences_of_the_forward(dl):
+    # fp32: the gradient along a direction, against central differences of the GPU's own forward in fp32.
+    # The loss is O(1) per term over ~1e4 terms; a step of 1e-2 leaves rounding ~1e-5 and curvature ~1e-3 relative.
+    x = draw(1, 80, 2, 16, 32, 1, seed=41, bf16=False)
+    d = dev(x, False)
+    gr = dl.delta_backward(d["q"], d["k"], d["v"], d["g"], d["beta"], d["do"], scale=0.5, d_final_state=d["d_final"],
+                           init_state=d["init"])
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def loss(e):
+        o, S = dl.delta_forward(e["q"], e["k"], e["v"], e["g"], e["beta"], scale=0.5, init_state=e["init"])
+        return float((o.double() * d["do"]).sum() + (S.double() * d["d_final"]).sum())
+
+    for name, g in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("init", "d_init")):
+        u = torch.randn(d[name].shape, generator=gen, device="cuda")
+        u /= u.norm()
+        h = 1e-2
+        num = (loss(dict(d, **{name: d[name] + h * u})) - loss(dict(d, **{name: d[name] - h * u}))) / (2 * h)
+        ana = float((gr[g].double() * u).sum())
+        assert abs(num - ana) <= 1e-3 * float(gr[g].norm()) + 1e-3, (name, num, ana)
+
+
+def test_clamped_valid_len_is_reported(dl):
+    from state_space_model_mamba_gb300 import ssd
+    x = draw(2, 20, 2, 64, 128, 1, seed=51)
+    d = dev(x, True)
+    vl = torch.tensor([25, -3], dtype=torch.int32, device="cuda")
+    for simt in (False, True):
+        with pytest.raises(ssd.SsdError, match="2 valid_len entries"):
+            dl.delta_forward(d["q"], d["k"], d["v"], d["g"], d["beta"], valid_len=vl, simt=simt, check_status=True)
+        with pytest.raises(ssd.SsdError, match="2 valid_len entries"):
+            dl.delta_backward(d["q"], d["k"], d["v"], d["g"], d["beta"], d["do"], valid_len=vl, simt=simt,
+                              check_status=True)
+
+
+def test_refusals(dl):
+    x = dev(draw(1, 20, 4, 64, 128, 2, seed=61), True)
+    a = dict(q=x["q"], k=x["k"], v=x["v"], g=x["g"], beta=x["beta"])
+    for name, bad in (("q", x["q"].float()), ("k", x["k"][:, :-1]), ("g", x["g"].bfloat16()), ("beta", x["beta"][:, :2]),
+                      ("q", x["q"].transpose(1, 2)), ("v", x["v"].half())):
+        with pytest.raises((ValueError, TypeError)):
+            dl.delta_forward(**dict(a, **{name: bad}))
+    with pytest.raises(ValueError):
+        dl.delta_forward(**a, init_state=x["init"].bfloat16())
+    with pytest.raises(ValueError):
+        dl.delta_forward(**a, valid_len=torch.tensor([20], device="cuda"))  # int64
+    with pytest.raises(ValueError):
+        dl.delta_backward(**a, do=x["do"].float())
+    with pytest.raises(ValueError):
+        dl.delta_step(x["q"][:, 0], x["k"][:, 0], x["v"][:, 0].contiguous(), x["g"][:, :, 0], x["beta"][:, :, 0], x["init"])

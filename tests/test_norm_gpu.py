@@ -1,0 +1,126 @@
+"""GPU parity of the entry norm (include/norm.h) against fp64.
+
+Bars (normwise): fp32 outputs 1e-6 (a few roundings of 2^-24 and sums of up to
+16384 terms in fp32, pairwise over threads); bf16 outputs 2^-9 against the fp64
+value rounded to bf16 (only values within fp32 noise of a tie may differ); dweight 1e-5 (up to a few thousand rows added in fp32)."""
+import numpy as np
+import pytest
+
+from oracle import delta as od
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BAR = {torch.float32: 1e-6, torch.bfloat16: 2.0 ** -9}
+
+
+@pytest.fixture(scope="module")
+def nm():
+    from state_space_model_mamba_gb300 import norm
+    return norm
+
+
+def rel(got, ref):
+    bf16 = got.dtype == torch.bfloat16
+    got = got.double().cpu().numpy()
+    assert got.shape == ref.shape and np.isfinite(got).all()
+    if bf16:
+        ref = torch.from_numpy(ref).bfloat16().double().numpy()
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+def make(rows, D, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, r, dy, ds = (torch.randn(rows, D, generator=g, device="cuda").to(dtype) for _ in range(4))
+    return x, r, dy, ds, 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+
+
+# every thread count and vector width: multiples of 8, even, odd; one column; the largest row
+SHAPES = [(1, 8), (5, 1), (3, 7), (4, 250), (2, 256), (130, 264), (3, 1000), (7, 1026), (2, 2051), (300, 2560), (2, 3000),
+          (3, 4096), (2, 4100), (2, 5121), (2, 8192), (2, 10008), (1, 16384), (1, 16383), (1, 16382)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,D", SHAPES)
+def test_forward_backward(nm, rows, D, dtype):
+    x, r, dy, ds, w = make(rows, D, dtype, rows + D)
+    y, stream = nm.add_rms_norm(x, w, 1e-5, residual=r)
+    assert torch.equal(stream, (x.float() + r.float()).to(dtype))
+    h = stream.double().cpu().numpy()
+    assert rel(y, od.add_rms_norm(h, w.double().cpu().numpy(), 1e-5)) <= BAR[dtype]
+    y0, s0 = nm.add_rms_norm(stream, w, 1e-5)
+    assert s0 is stream and torch.equal(y0, y)
+    for d_stream in (None, ds):
+        dx, dw = nm.add_rms_norm_backward(dy, stream, w, 1e-5, d_stream=d_stream)
+        rx, rw = od.add_rms_norm_backward(dy.double().cpu().numpy(), h, w.double().cpu().numpy(), 1e-5,
+                                          None if d_stream is None else ds.double().cpu().numpy())
+        # one column: y = sign(h) w up to eps, the two terms of dx cancel to ~eps of either
+        bar = BAR[dtype] if D > 1 or d_stream is not None else 1.0
+        assert rel(dx, rx) <= bar
+        assert rel(dw, rw) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,D,group", [(3, 128, 0), (5, 256, 32), (4, 2560, 128), (300, 2560, 64), (2, 96, 32), (3, 250, 0),
+                                          (2, 2051, 0), (1, 16384, 128), (7, 10240, 0), (129, 512, 128), (1, 1, 0)])
+def test_fp8(nm, rows, D, group, dtype):
+    x, r, _, _, w = make(rows, D, dtype, rows + D + group)
+    y8, scales, stream = nm.add_rms_norm_fp8(x, w, 1e-5, residual=r, group=group)
+    assert y8.dtype == torch.float8_e4m3fn and y8.shape == x.shape and scales.shape == (rows, D // group if group else 1)
+    assert torch.equal(stream, (x.float() + r.float()).to(dtype))
+    y = od.add_rms_norm(stream.double().cpu().numpy(), w.double().cpu().numpy(), 1e-5).reshape(rows, scales.shape[1], -1)
+    ref = np.abs(y).max(-1) / 448.0
+    assert rel(scales, ref) <= 1e-6
+    q = y8.float().double().cpu().numpy().reshape(y.shape)
+    # nearest e4m3: half a step of 2^-3 of the value's power of two, at least half of 2^-9; fp32 noise on ties
+    err = np.abs(q - y / ref[..., None])
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(y / ref[..., None]), 2.0 ** -6))) - 3)
+    assert np.all(err <= 0.5 * step * (1 + 1e-4)) and np.abs(q).max() <= 448
+
+
+def test_zero_rows_and_non_finite_rows(nm):
+    x, r, _, _, w = make(6, 512, torch.bfloat16, 1)
+    x[1] = 0
+    r[1] = 0
+    x[2, 5] = float("nan")
+    x[3, 7] = float("inf")
+    x[4, :128] = 0
+    r[4, :128] = 0
+    for group in (0, 128):
+        y8, s, _ = nm.add_rms_norm_fp8(x, w, 1e-5, residual=r, group=group)
+        assert torch.all(y8[1].float() == 0) and torch.all(s[1] == 0)
+        assert torch.isnan(y8[2].float()).all() and torch.isnan(s[2]).all()
+        assert torch.isnan(y8[3].float()[7])
+        assert torch.all(y8[4, :128].float() == 0) and torch.isfinite(y8[4].float()).all()
+        assert torch.isfinite(y8[[0, 4, 5]].float()).all() and torch.isfinite(s[[0, 4, 5]]).all()
+    y, _ = nm.add_rms_norm(x, w, 1e-5, residual=r)
+    assert torch.all(y[1] == 0) and torch.isnan(y[2]).all() and torch.isnan(y[3, 7])
+    assert torch.isfinite(y[[0, 1, 4, 5]]).all()
+
+
+def test_in_place_stream_and_fixed_order(nm):
+    import ctypes
+    from state_space_model_mamba_gb300 import ssd
+    x, r, dy, _, w = make(1000, 2560, torch.bfloat16, 2)
+    y, stream = nm.add_rms_norm(x, w, 1e-5, residual=r)
+    y2, r2 = torch.empty_like(y), r.clone()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert nm._lib().norm_add_rms(1, p(x), p(r2), p(w), 1e-5, p(y2), p(r2), 1000, 2560, ssd._stream_ptr(x.device)) == 0
+    assert torch.equal(y, y2) and torch.equal(stream, r2)
+    first = nm.add_rms_norm_backward(dy, stream, w)
+    for a, b in zip(first, nm.add_rms_norm_backward(dy, stream, w)):
+        assert torch.equal(a, b)
+
+
+def test_refusals(nm):
+    x, r, dy, _, w = make(4, 64, torch.bfloat16, 3)
+    for bad in (dict(residual=r.float()), dict(residual=r[:2]), dict(weight=w.bfloat16()), dict(weight=w[:-1])):
+        with pytest.raises(ValueError):
+            nm.add_rms_norm(**dict(dict(x=x, weight=w), **bad))
+    with pytest.raises(TypeError):
+        nm.add_rms_norm(x.half(), w)
+    with pytest.raises(ValueError):
+        nm.add_rms_norm(x.t(), w)
+    from state_space_model_mamba_gb300 import ssd
+    with pytest.raises(ssd.SsdError):
+        nm.add_rms_norm_fp8(x, w, group=48)
