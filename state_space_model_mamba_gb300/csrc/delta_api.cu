@@ -4,7 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "delta_internal.cuh"
+#include "delta_chunk.cuh"
 
 namespace ssd {
 namespace delta {
@@ -83,6 +83,10 @@ DeltaParams base_params(const delta_dims &d, const void *q, const void *k, const
     return p;
 }
 
+size_t image_bytes(const delta_dims &d) {
+    return (size_t)d.batch * d.nheads * chunk_count(d.seqlen) * kImgBytes;
+}
+
 }  // namespace
 }  // namespace delta
 }  // namespace ssd
@@ -100,6 +104,7 @@ ssd_status delta_supported(const delta_dims *dims, ssd_dtype dtype) {
 size_t delta_workspace_bytes(const delta_dims *dims, ssd_dtype dtype, int backward) {
     record_error("");
     if (validate(dims, dtype) != SSD_OK) return 0;
+    if (!backward && chunk_supported(*dims, dtype)) return kStatusBytes + image_bytes(*dims);
     return kStatusBytes + (backward ? simt_backward_bytes(*dims) : 0);
 }
 
@@ -120,7 +125,11 @@ ssd_status delta_forward(const delta_dims *dims, ssd_dtype dtype, const void *q,
     DeltaParams p = base_params(*dims, q, k, v, g, beta, scale, init_state, valid_len, workspace);
     p.o = o;
     p.final_state = final_state;
-    return cuda_status(launch_simt_forward(p, dtype == SSD_BF16, (cudaStream_t)stream));
+    cudaStream_t cs = (cudaStream_t)stream;
+    if (!chunk_supported(*dims, dtype)) return cuda_status(launch_simt_forward(p, dtype == SSD_BF16, cs));
+    const ChunkParams c{p, chunk_count(dims->seqlen), (char *)workspace + kStatusBytes};
+    st = cuda_status(launch_chunk_prep(c, cs));
+    return st != SSD_OK ? st : cuda_status(launch_chunk_forward(c, cs));
 }
 
 ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
