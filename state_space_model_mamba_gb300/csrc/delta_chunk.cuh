@@ -12,21 +12,37 @@
 //     Z = X0 + Tt (beta o X0)  for X0 = V - e^gamma o (K S),
 // and, in the backward, X = dU + Tt^T (beta o dU), dV = beta o X.
 //
-// The chunk image of one (b, h, chunk): lower triangles of 16x16 bf16 blocks
-// (10 of 64; blk_at, blk_swz) of Tt and A, each as hi and lo parts, and the gate
-// vectors in fp32.
+// The forward takes A through the inverse, so that one operand (beta o X0) gives both
+// the errors and the outputs:  A U = At (beta o X0),  At = A (I + diag(beta) Tt).
+//
+// The chunk image of one (b, h, chunk) is what the scan copies to shared memory: the
+// gate vectors in fp32, then Tt and At as hi and lo bf16 parts.  Each is kept as the
+// tensor core reads it without swizzle, in 8x8 matrices of 128 contiguous bytes:
+// columns 16 ks + 8 kc .. + 7 are one run of the row octets from 2 ks on (the octets
+// above are zero and not stored).
 #pragma once
+#include <cuda.h>
+
 #include "delta_internal.cuh"
 
 namespace ssd {
 namespace delta {
 
 constexpr int kChunk = 64;
-constexpr int kTri = 10 * 512;                 // bytes of one lower triangle of blocks
-constexpr int kGates = 3 * kChunk * 4;         // e^gamma, e^(gamma_C - gamma), beta
-// image layout: gates, Tt hi, Tt lo, A hi, A lo.  The forward reads all but A lo.
-constexpr int kImgGates = 0, kImgT = kGates, kImgA = kGates + 2 * kTri;
-constexpr int kImgFwd = kGates + 3 * kTri, kImgBytes = kGates + 4 * kTri;
+constexpr int kTri = 2 * 128 * (8 + 6 + 4 + 2);  // bytes of one lower triangle (5120)
+constexpr int kGates = 3 * kChunk * 4;           // e^gamma, e^(gamma_C - gamma), beta
+// image: gates, then [hi, lo][Tt, At]
+constexpr int kImgTri = kGates, kImgBytes = kGates + 4 * kTri;
+// run (ks, kc) of a triangle: its first byte and its length
+__host__ __device__ constexpr int tri_run_bytes(int ks) { return (8 - 2 * ks) * 128; }
+__host__ __device__ constexpr int tri_run(int ks, int kc) {
+    return 2048 * ks - 256 * ks * (ks - 1) + kc * tri_run_bytes(ks);
+}
+// the 16-byte piece of row i, columns 8 c .. 8 c + 7 (c / 2 <= i / 16)
+__host__ __device__ constexpr int tri_piece(int i, int c) {
+    return tri_run(c >> 1, c & 1) + ((i >> 3) - (c & ~1)) * 128 + (i & 7) * 16;
+}
+static_assert(tri_run(1, 0) == 2048 && tri_run(2, 0) == 3584 && tri_run(3, 1) + tri_run_bytes(3) == kTri, "triangle runs");
 
 struct ChunkParams {
     DeltaParams p;
@@ -39,6 +55,10 @@ inline bool chunk_supported(const delta_dims &d, ssd_dtype t) {
            d.headdim <= 128 && d.dstate <= 128;
 }
 inline int chunk_count(long long L) { return (int)((L + kChunk - 1) / kChunk); }
+
+// Tensor map of bf16 tiles in the 128-byte swizzle, zeros outside (delta_maps.cu).
+cudaError_t encode_tiles(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                         const cuuint32_t *box);
 
 cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s);
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s);

@@ -28,13 +28,18 @@ struct PrepSmem {
             __align__(16) unsigned char q[kChunk * 256], k[kChunk * 256];
         };
         struct {
-            float E[kChunk * kLd];
-            float T[kChunk * kLd];
-            float W[3][16 * 20];
-            __align__(16) unsigned char img[kImgBytes];
+            union {
+                struct {
+                    float E[kChunk * kLd];
+                    float W[3][16 * 20];
+                };
+                __align__(16) unsigned char tri[4 * kTri];  // written once E is done with
+            };
+            float T[kChunk * kLd], A[kChunk * kLd];
         };
     };
     float ghi[kChunk], glo[kChunk], beta[kChunk];
+    __align__(16) float gates[kGates / 4];
 };
 
 // d += a (16x16 at A, columns scaled by sc) times b (16x16 at B), fp32 rows of lda / ldb floats
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const ChunkPara
     const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * kHeadsPer);
     for (int h = grp * p.hpg + slice * kHeadsPer; h < h_end; ++h) {
         const long long bh = (long long)bi * p.H + h;
-        float *gates = (float *)(s.img + kImgGates);
+        float *gates = s.gates;
         __syncthreads();  // the tiles, or the image of the head before, have been read
         if (warp == 0) {
             // gamma in fp64, kept as hi + lo: differences of it stay exact to fp32 after strong decays
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const ChunkPara
             gates[2 * kChunk + i0 + 1] = b1;
         }
         __syncthreads();
-        // E (fp32) and A (hi, lo blocks)
+        // E and A
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
             if (nt / 2 <= warp) {
@@ -185,12 +190,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const ChunkPara
                     const float d1 = j + 1 <= i ? expf((gi - s.ghi[j + 1]) + (li - s.glo[j + 1])) : 0.f;
                     *(float2 *)(s.E + i * kLd + j) = make_float2(j < i ? d0 * kk[nt][2 * half] : 0.f,
                                                                  j + 1 < i ? d1 * kk[nt][2 * half + 1] : 0.f);
-                    uint32_t hi, lo;
-                    split2(j <= i ? p.scale * d0 * qk[nt][2 * half] : 0.f,
-                           j + 1 <= i ? p.scale * d1 * qk[nt][2 * half + 1] : 0.f, hi, lo);
-                    unsigned char *dst = s.img + kImgA + blk_at(warp, nt / 2) * 512 + blk_swz(g + 8 * half, nt & 1) + 4 * t;
-                    *(uint32_t *)dst = hi;
-                    *(uint32_t *)(dst + kTri) = lo;
+                    *(float2 *)(s.A + i * kLd + j) = make_float2(j <= i ? p.scale * d0 * qk[nt][2 * half] : 0.f,
+                                                                 j + 1 <= i ? p.scale * d1 * qk[nt][2 * half + 1] : 0.f);
                 }
             }
         __syncthreads();
@@ -227,21 +228,44 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const ChunkPara
             }
             __syncthreads();
         }
-        // Tt as hi, lo blocks: a thread takes 8 neighbouring columns (one 16-byte piece)
-        for (int i = tid; i < 10 * 32; i += kThreads) {
-            const int blk = i >> 5, r = (i >> 1) & 15, c8 = i & 1;
-            const int bi_ = blk >= 6 ? 3 : (blk >= 3 ? 2 : (blk >= 1 ? 1 : 0)), bj = blk - bi_ * (bi_ + 1) / 2;
-            const float *src = s.T + (16 * bi_ + r) * kLd + 16 * bj + 8 * c8;
+        // Tt as hi and lo parts, a thread per 16-byte piece
+        for (int x = tid; x < 10 * 32; x += kThreads) {
+            const int blk = x >> 5, br = blk >= 6 ? 3 : (blk >= 3 ? 2 : (blk >= 1 ? 1 : 0)), bc = blk - br * (br + 1) / 2;
+            const int i = 16 * br + ((x >> 1) & 15), c = 2 * bc + (x & 1);
+            const float *src = s.T + i * kLd + 8 * c;
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) split2(src[2 * e], src[2 * e + 1], hi[e], lo[e]);
-            unsigned char *dst = s.img + kImgT + blk * 512 + blk_swz(r, c8);
-            *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *(uint4 *)(dst + kTri) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *(uint4 *)(s.tri + tri_piece(i, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *(uint4 *)(s.tri + 2 * kTri + tri_piece(i, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        // At = A + A diag(beta) Tt: five block products a warp
+        {
+            constexpr int nblk[4] = {2, 2, 2, 4};
+            constexpr int rows[4][4] = {{3, 0, 0, 0}, {2, 1, 0, 0}, {3, 2, 0, 0}, {3, 1, 2, 3}};
+            constexpr int cols[4][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {1, 1, 0, 0}, {2, 1, 2, 3}};
+            for (int x = 0; x < nblk[warp]; ++x) {
+                const int i = rows[warp][x], j = cols[warp][x];
+                float w[2][4];
+                load_block(w, s.A + 16 * i * kLd + 16 * j, kLd, lane);
+                for (int k = j; k <= i; ++k)
+                    block_product(w, s.A + 16 * i * kLd + 16 * k, kLd, s.beta + 16 * k, s.T + 16 * k * kLd + 16 * j, kLd, lane);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t hi, lo;
+                        split2(w[nt][2 * half], w[nt][2 * half + 1], hi, lo);
+                        unsigned char *dst = s.tri + kTri + tri_piece(16 * i + g + 8 * half, 2 * j + nt) + 4 * t;
+                        *(uint32_t *)dst = hi;
+                        *(uint32_t *)(dst + 2 * kTri) = lo;
+                    }
+            }
         }
         __syncthreads();
         uint4 *out = (uint4 *)(cp.img + (bh * cp.n + chunk) * (long long)kImgBytes);
-        for (int i = tid; i < kImgBytes / 16; i += kThreads) out[i] = ((const uint4 *)s.img)[i];
+        for (int i = tid; i < kGates / 16; i += kThreads) out[i] = ((const uint4 *)s.gates)[i];
+        for (int i = tid; i < 4 * kTri / 16; i += kThreads) out[kImgTri / 16 + i] = ((const uint4 *)s.tri)[i];
     }
 }
 

@@ -1,14 +1,26 @@
 // delta_scan.cu -- the serial pass of the chunked gated delta rule
-// (delta_chunk.cuh): one block per (b, h, 64 rows of P) walks the chunks in
-// order with the state in registers.
+// (delta_chunk.cuh): one block per (b, h, 64 columns of P) walks the chunks in
+// order.  Per chunk, three products on the tensor cores, each waiting for the
+// one before:
+//   1.  [K; Q] S       M = 64 + 64 tokens, K index = N      -> K S and Q S
+//   2.  [Tt; At] X     M = 64 + 64 tokens, K index = 64     -> Z = X0 + Tt X,  O = scale e^gamma Q S + At X
+//   3.  K^T W          M = N, K index = 64 tokens           -> S' = e^gamma_C S + K^T W
+// with X0 = V - e^gamma K S, X = beta X0 and W = beta e^(gamma_C - gamma) Z formed by
+// the threads between them.  Stacking K on Q and Tt on At fills the 128 rows of the
+// instruction, and the output's rows ride along with the chain's.
 //
-// Everything is computed transposed, a warp owning 16 rows of S^T [P, N]:
-//     X0^T = V^T - (S^T K^T) e^gamma,   Z^T = X0^T + (X0 beta)^T Tt^T,
-//     O^T = (S^T Q^T) scale e^gamma + U^T A^T,   S'^T = e^gamma_C S^T + (U e^(gamma_C-gamma))^T K,
-// so that the accumulators of one product are the register operand of the next
-// (rows stay in the lane that holds them): state, X0, Z and U never pass through
-// shared memory, and the warps of a block share nothing but the loaded tiles.
-// The fp32 operands go to the tensor cores as hi + lo bf16 parts (delta_mma.cuh).
+// Precision: q, k, v are exact in bf16; S, X, W, Tt, At are fp32 values fed as hi + lo
+// bf16 parts (2^-17), the hi and lo parts of S and W side by side as one operand of
+// twice the columns, so that the left operand is read once.  The state itself stays
+// in fp32 registers (thread (n, half) holds row n, 32 columns) and is added to with
+// rounding to nearest.
+//
+// What bounds it is the latency of the chain of three products and three passes of
+// the threads.  A block needs 97 KB of shared memory with one set of K, Q tiles, so
+// that two chains share an SM and hide in each other's waits; with few chains (one
+// block per SM) a second set of K, Q tiles takes the load latency out of the chain.
+#include <cuda.h>
+
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -16,246 +28,347 @@ namespace ssd {
 namespace delta {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace tc;
 
-template <int NP>
-struct ScanStage {
-    unsigned char k[kChunk * NP * 2], q[kChunk * NP * 2];
-    unsigned char v[kChunk * 128];  // 64 columns; o is staged over it once it has been read
-    unsigned char img[kImgFwd];
+constexpr int kCompute = 256;              // eight warps: TMEM lane quarter w % 4, column half w / 4
+constexpr int kScanThreads = kCompute + 32;  // and a warp that issues copies and products
+constexpr uint32_t kAccCols = 128;
+
+// shared memory from a 1024-byte aligned base
+constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128; X (16 KB) and W (16 KB) in their place
+constexpr uint32_t kOffX = 0, kOffW = 16384;
+constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][kc][16 row octets][128 bytes]: Tt rows, then At rows
+constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
+constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
+constexpr uint32_t kKQBytes = 32768;
+
+// descriptor of K-step ks of the unswizzled [Tt; At] operand
+__device__ __forceinline__ uint64_t sdesc_tri(uint32_t base, int ks) {
+    const uint32_t a = base + (uint32_t)ks * 4096u;
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(2048 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// 32 floats as 64 bytes of each of a SW128 tile's hi and lo parts: row `row`, 16-byte pieces c0 .. c0 + 3
+__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float *x) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
+    st_shared_v4(hi_tile + sw128_chunk(row, piece), h[0], h[1], h[2], h[3]);
+    st_shared_v4(lo_tile + sw128_chunk(row, piece), l[0], l[1], l[2], l[3]);
+}
+
+struct ScanMaps {
+    CUtensorMap k, q, v;
 };
 
-template <int NP>
-__device__ __forceinline__ void load_scan_stage(ScanStage<NP> &s, const ChunkParams &cp, int bi, int h, int slice,
-                                                int chunk, int V) {
+template <int NB>
+__global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
+    delta_scan_fwd(const ChunkParams cp, const __grid_constant__ ScanMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar_kq[2], bar_tri, bar_v;               // copies have landed
+    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (8 warps each)
+    __shared__ uint64_t bar_m[3];                                // products are done
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_err;
     const DeltaParams &p = cp.p;
-    constexpr int LINE = NP * 2;
-    const int t0 = chunk * kChunk, grp = h / p.hpg, tid = threadIdx.x;
-    const uint32_t ks = smem_u32(s.k), qs = smem_u32(s.q), vs = smem_u32(s.v), is = smem_u32(s.img);
-#pragma unroll
-    for (int x = 0; x < kChunk * (NP / 8) / kThreads; ++x) {
-        const int i = x * kThreads + tid, r = i / (NP / 8), c = i % (NP / 8);
-        const bool real = t0 + r < V && c * 8 < p.N;
-        const long long at = real ? (((long long)bi * p.L + t0 + r) * p.G + grp) * p.N + c * 8 : 0;
-        cp_async16(ks + swz<LINE>(r, c), (const bf16 *)p.k + at, real);
-        cp_async16(qs + swz<LINE>(r, c), (const bf16 *)p.q + at, real);
-    }
-#pragma unroll
-    for (int x = 0; x < kChunk * 8 / kThreads; ++x) {
-        const int i = x * kThreads + tid, r = i / 8, c = i % 8;
-        const bool real = t0 + r < V && slice * 64 + c * 8 < p.P;
-        const long long at = real ? (((long long)bi * p.L + t0 + r) * p.H + h) * p.P + slice * 64 + c * 8 : 0;
-        cp_async16(vs + swz<128>(r, c), (const bf16 *)p.v + at, real);
-    }
-    const char *img = cp.img + (((long long)bi * p.H + h) * cp.n + chunk) * (long long)kImgBytes;
-#pragma unroll
-    for (int x = 0; x < (kImgFwd / 16 + kThreads - 1) / kThreads; ++x) {
-        const int i = x * kThreads + tid;
-        if (i < kImgFwd / 16) cp_async16(is + 16 * i, img + 16 * i, true);
-    }
-}
-
-// Rows of fp32 state in accumulator layout: tile nt holds columns 8 nt + 2 t, +1 of rows r and r + 8.
-template <int NP>
-__device__ __forceinline__ void load_state(float (&s)[NP / 8][4], const float *src, int row, int P, int N, int t) {
-#pragma unroll
-    for (int nt = 0; nt < NP / 8; ++nt) {
-        const int c = 8 * nt + 2 * t;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = row + 8 * half;
-            const float2 x = (src && r < P && c < N) ? *(const float2 *)(src + (long long)r * N + c) : make_float2(0.f, 0.f);
-            s[nt][2 * half] = x.x;
-            s[nt][2 * half + 1] = x.y;
-        }
-    }
-}
-template <int NP>
-__device__ __forceinline__ void store_state(const float (&s)[NP / 8][4], float *dst, int row, int P, int N, int t) {
-    if (!dst) return;
-#pragma unroll
-    for (int nt = 0; nt < NP / 8; ++nt) {
-        const int c = 8 * nt + 2 * t;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = row + 8 * half;
-            if (r < P && c < N) *(float2 *)(dst + (long long)r * N + c) = make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
-        }
-    }
-}
-
-template <int NP>
-__global__ void __launch_bounds__(kThreads, 2) delta_scan_fwd(const ChunkParams cp) {
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    ScanStage<NP> *stage = (ScanStage<NP> *)smem_raw;
-    constexpr int LINE = NP * 2;
-    const DeltaParams &p = cp.p;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int nsl = (p.P + 63) / 64, slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk;
-    const int row = slice * 64 + 16 * warp + g;
-    const long long sbase = (long long)bh * p.P * p.N;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
+    const char *img0 = cp.img + (long long)bh * cp.n * (long long)kImgBytes;
+    if (tid == 0) {
+        mbar_init(&bar_kq[0], 1);
+        mbar_init(&bar_kq[1], 1);
+        mbar_init(&bar_tri, 1);
+        mbar_init(&bar_v, 1);
+        mbar_init(&bar_s, kCompute / 32);
+        mbar_init(&bar_x, kCompute / 32);
+        mbar_init(&bar_w, kCompute / 32);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_fence_init();
+        s_err = 0;
+    }
+    if (warp == 0) tmem_alloc(&s_tmem, kAccCols);
+    // the row octets of the triangles that no copy writes are zero
+    for (int i = tid; i < 32768 / 16; i += kScanThreads) st_shared_v4(base + kOffTri + 16 * i, 0, 0, 0, 0);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
 
-    float s[NP / 8][4];
-    load_state<NP>(s, p.init ? p.init + sbase : nullptr, row, p.P, p.N, t);
-    if (nv > 0) load_scan_stage<NP>(stage[0], cp, bi, h, slice, 0, V);
-    cp_async_commit();
+    if (warp == kCompute / 32) {
+        // ---- copies and products
+        const int grp = h / p.hpg;
+        const uint32_t half_k = p.N > 64 ? 2u : 1u;
+        int kq_issued = 0, tri_issued = 0, v_issued = 0, done = 0;
+        // tma_load_* take generic pointers; shared addresses are passed through this one
+        auto tma = [&](uint32_t dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1, int c2, int c3) {
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                : "memory");
+        };
+        auto expect_kq = [&](int c) {
+            if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], half_k * 16384u);
+            kq_issued = c + 1;
+        };
+        auto load_half = [&](int c, const CUtensorMap *m, uint32_t off) {
+            if (lane == 0)
+                for (uint32_t kb = 0; kb < half_k; ++kb)
+                    tma(base + kOffKQ + (c % NB) * kKQBytes + kb * 16384u + off, m, &bar_kq[c % NB], 64 * kb, grp, c * kChunk, bi);
+        };
+        auto load_tri = [&](int c) {
+            if (lane == 0) mbar_arrive_expect_tx(&bar_tri, 4 * kTri);
+            __syncwarp();
+            const int part = lane >> 4, which = (lane >> 3) & 1, ks = (lane >> 1) & 3, kc = lane & 1;
+            bulk_load(base + kOffTri + part * 16384 + ks * 4096 + kc * 2048 + which * 1024 + 2 * ks * 128,
+                      img0 + (long long)c * kImgBytes + kImgTri + (2 * part + which) * kTri + tri_run(ks, kc),
+                      tri_run_bytes(ks), &bar_tri);
+            tri_issued = c + 1;
+        };
+        auto load_v = [&](int c) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar_v, 8192);
+                tma(base + kOffV, &maps.v, &bar_v, 64 * slice, h, c * kChunk, bi);
+            }
+            v_issued = c + 1;
+        };
+        for (int c = 0; c < NB && c < nv; ++c) {
+            expect_kq(c);
+            load_half(c, &maps.k, 0);
+            load_half(c, &maps.q, 8192);
+        }
+        if (nv > 0) {
+            load_tri(0);
+            load_v(0);
+        }
+        const uint32_t i1 = idesc_bf16(128, 128, false, true), i2 = idesc_bf16(128, 64, false, true),
+                       i3 = idesc_bf16(128, 128, true, true);
+        bool ok = true;
+        for (int c = 0; c < nv; ++c) {
+            const uint32_t ph = c & 1, kq = base + kOffKQ + (c % NB) * kKQBytes;
+            ok = mbar_wait(&bar_kq[c % NB], (c / NB) & 1) && mbar_wait(&bar_s, ph);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int ks = 0; ks < nks; ++ks)
+                    mma_bf16(tm, sdesc_kmajor(kq, ks, 16384), sdesc_mnmajor(base + kOffS, ks, 16384), i1, ks > 0);
+                mma_commit(&bar_m[0]);
+            }
+            ok = mbar_wait(&bar_tri, ph) && mbar_wait(&bar_x, ph);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int pass = 0; pass < 3; ++pass)
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tm, sdesc_tri(base + kOffTri + (pass == 2 ? 16384 : 0), ks),
+                                 sdesc_mnmajor(base + kOffX + (pass == 1 ? 8192 : 0), ks, 8192), i2, true);
+                mma_commit(&bar_m[1]);
+            }
+            __syncwarp();
+            // V has been read, and Q by the first product
+            if (c + 1 < nv) load_v(c + 1);
+            if (NB == 1 && c + 1 < nv) {
+                expect_kq(c + 1);
+                load_half(c + 1, &maps.q, 8192);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tm, sdesc_mnmajor(kq, ks, 16384), sdesc_mnmajor(base + kOffW, ks, 8192), i3, ks > 0);
+                mma_commit(&bar_m[2]);
+            }
+            __syncwarp();
+            done = c + 1;
+            if (c + 1 < nv) load_tri(c + 1);
+            if (c + NB < nv) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
+                if (!ok) break;
+                if (NB > 1) {
+                    expect_kq(c + NB);
+                    load_half(c + NB, &maps.q, 8192);
+                }
+                load_half(c + NB, &maps.k, 0);
+            }
+        }
+        if (!ok) s_err = 1;
+        // every copy has to land and every product to complete before the block may end
+        for (int c = max(0, kq_issued - NB); c < kq_issued; ++c) mbar_wait(&bar_kq[c % NB], (c / NB) & 1);
+        if (tri_issued) mbar_wait(&bar_tri, (tri_issued - 1) & 1);
+        if (v_issued) mbar_wait(&bar_v, (v_issued - 1) & 1);
+        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const bool keys = quarter < 2;       // rows 0 .. 63: K tokens, 64 .. 127: Q tokens
+        const int i = row & 63;              // the row's token
+        const uint32_t my = tmem_addr(tm, 32 * quarter, 32 * half);
+        float S[32];
+        {
+            const float *src = p.init ? p.init + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row : nullptr;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                S[j] = (src && row < p.N && slice * 64 + 32 * half + j < p.P) ? src[(long long)j * p.N] : 0.f;
+        }
+        bool ok = true;
+        // S as an operand; before the last chunk, K rows of absent tokens are made zero
+        auto publish_s = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 8 * j);
+            const int live = V - c * kChunk;
+            if (live < kChunk) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[c % NB], (c / NB) & 1));
+                const uint32_t kq = base + kOffKQ + (c % NB) * kKQBytes;
+                for (int x = tid; x < 2 * kChunk * 8; x += kCompute)
+                    if (((x >> 3) & 63) >= live) st_shared_v4(kq + (x >> 9) * 16384u + (x & 511) * 16u, 0, 0, 0, 0);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_s);
+        };
+        if (nv > 0) publish_s(0);
+        for (int c = 0; c < nv && ok; ++c) {
+            const uint32_t ph = c & 1;
+            const float *gates = (const float *)(img0 + (long long)c * kImgBytes);
+            const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
+            const float ec = __ldg(gates + kChunk - 1);
+            const bool live = c * kChunk + i < V;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float a[16], b[16];
+                tmem_ld16(my + 16 * j, a);
+                tmem_ld16(my + 64 + 16 * j, b);
+                if (keys) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + 2 * j + u));
+                        const uint32_t vv[4] = {w.x, w.y, w.z, w.w};
+                        float xb[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float v = (e & 1) ? bf_hi(vv[e >> 1]) : bf_lo(vv[e >> 1]);
+                            const float x = live ? v - eg * (a[8 * u + e] + b[8 * u + e]) : 0.f;
+                            a[8 * u + e] = x;
+                            xb[e] = be * x;
+                        }
+                        store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + 2 * j + u, xb);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) a[e] = p.scale * eg * (a[e] + b[e]);
+                }
+                uint32_t r[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(a[e]);
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t" ::"r"(
+                        my + 16 * j),
+                    "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                    : "memory");
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_x);
 
-    for (int c = 0; c < nv; ++c) {
-        cp_async_wait<0>();
-        __syncthreads();  // this chunk's tiles are complete, the other stage is free
-        if (c + 1 < nv) load_scan_stage<NP>(stage[(c + 1) & 1], cp, bi, h, slice, c + 1, V);
-        cp_async_commit();
-        ScanStage<NP> &st = stage[c & 1];
-        const uint32_t ks = smem_u32(st.k), qs = smem_u32(st.q), vs = smem_u32(st.v);
-        const uint32_t th = smem_u32(st.img + kImgT), ah_ = smem_u32(st.img + kImgA);
-        const float *gates = (const float *)(st.img + kImgGates);
-
-        // S^T K^T and S^T Q^T
-        float x[8][4], o[8][4];
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+            if (!ok) break;
+            tc_fence_after();
+            {
+                float a[32];
+                tmem_ld32(my, a);
+                if (keys) {
+                    const float f = be * et;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+                    for (int e = 0; e < 32; ++e) a[e] = live ? f * a[e] : 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = o[i][e] = 0.f;
-        const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
+                    for (int j = 0; j < 4; ++j) store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, a + 8 * j);
+                    fence_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_w);
+                if (!keys) {
+                    const int tok = c * kChunk + i;
+                    bf16 *dst = (bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + 32 * half;
 #pragma unroll
-        for (int kst = 0; kst < NP / 16; ++kst) {
-            uint32_t hi[4], lo[4];
-            split_frag(s[2 * kst], s[2 * kst + 1], hi, lo);
-            uint32_t b[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ldsm4(b[j], ks + swz<LINE>(16 * j + brow, 2 * kst + bcol));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma16(x[2 * j], hi, b[j][0], b[j][1]);
-                mma16(x[2 * j + 1], hi, b[j][2], b[j][3]);
+                    for (int j = 0; j < 4; ++j)
+                        if (tok < p.L && slice * 64 + 32 * half + 8 * j < p.P)
+                            *(uint4 *)(dst + 8 * j) =
+                                live ? make_uint4(pack_bf2(a[8 * j], a[8 * j + 1]), pack_bf2(a[8 * j + 2], a[8 * j + 3]),
+                                                  pack_bf2(a[8 * j + 4], a[8 * j + 5]), pack_bf2(a[8 * j + 6], a[8 * j + 7]))
+                                     : make_uint4(0, 0, 0, 0);
+                }
             }
-            uint32_t bq[4][4];
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ldsm4(bq[j], qs + swz<LINE>(16 * j + brow, 2 * kst + bcol));
+            for (int j = 0; j < 2; ++j) {
+                float a[16], b[16];
+                tmem_ld16(my + 16 * j, a);
+                tmem_ld16(my + 64 + 16 * j, b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma16(o[2 * j], hi, bq[j][0], bq[j][1]);
-                mma16(o[2 * j + 1], hi, bq[j][2], bq[j][3]);
+                for (int e = 0; e < 16; ++e) S[16 * j + e] = fmaf(ec, S[16 * j + e], a[e] + b[e]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma16(x[2 * j], lo, b[j][0], b[j][1]);
-                mma16(x[2 * j + 1], lo, b[j][2], b[j][3]);
-                mma16(o[2 * j], lo, bq[j][0], bq[j][1]);
-                mma16(o[2 * j + 1], lo, bq[j][2], bq[j][3]);
-            }
+            if (c + 1 < nv) publish_s(c + 1);
         }
-        // X0 = V - e^gamma (K S)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t r[4];
-            ldsm4t(r, vs + swz<128>(16 * j + brow, 2 * warp + bcol));
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float(&d)[4] = x[2 * j + u];
-                const float2 eg = *(const float2 *)(gates + 8 * (2 * j + u) + 2 * t);
-                d[0] = __uint_as_float(r[2 * u] << 16) - eg.x * d[0];
-                d[1] = __uint_as_float(r[2 * u] & 0xFFFF0000u) - eg.y * d[1];
-                d[2] = __uint_as_float(r[2 * u + 1] << 16) - eg.x * d[2];
-                d[3] = __uint_as_float(r[2 * u + 1] & 0xFFFF0000u) - eg.y * d[3];
-                float(&oo)[4] = o[2 * j + u];
-                oo[0] *= p.scale * eg.x;
-                oo[1] *= p.scale * eg.y;
-                oo[2] *= p.scale * eg.x;
-                oo[3] *= p.scale * eg.y;
-            }
+        if (!ok) s_err = 1;
+        // absent tokens past the last chunk
+        for (int x = nv * kChunk * 8 + tid; x < p.L * 8; x += kCompute) {
+            const int tok = x / 8, cc = x % 8;
+            if (slice * 64 + cc * 8 < p.P)
+                *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
         }
-        // Z = X0 + Tt (beta X0): token blocks from the last, so that a block is an operand before it is added to
-        const float *be = gates + 2 * kChunk;
+        if (ok && p.final_state && row < p.N) {
+            float *dst = p.final_state + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row;
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
-            uint32_t hi[4], lo[4];
-            split_frag(x[2 * j], x[2 * j + 1], *(const float2 *)(be + 16 * j + 2 * t),
-                       *(const float2 *)(be + 16 * j + 8 + 2 * t), hi, lo);
-#pragma unroll
-            for (int i = j; i < 4; ++i) {
-                uint32_t bh_[4], bl_[4];
-                const uint32_t at = th + blk_at(i, j) * 512 + blk_swz(brow, bcol);
-                ldsm4(bh_, at);
-                ldsm4(bl_, at + kTri);
-                mma16(x[2 * i], hi, bh_[0], bh_[1]);
-                mma16(x[2 * i + 1], hi, bh_[2], bh_[3]);
-                mma16(x[2 * i], lo, bh_[0], bh_[1]);
-                mma16(x[2 * i + 1], lo, bh_[2], bh_[3]);
-                mma16(x[2 * i], hi, bl_[0], bl_[1]);
-                mma16(x[2 * i + 1], hi, bl_[2], bl_[3]);
-            }
-        }
-        // U = beta Z;  O += U A^T;  S = e^gamma_C S + (U e^(gamma_C - gamma))^T K
-        const float ec = gates[kChunk - 1];
-#pragma unroll
-        for (int nt = 0; nt < NP / 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] *= ec;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t hi[4], lo[4];
-            const float2 b0 = *(const float2 *)(be + 16 * j + 2 * t), b1 = *(const float2 *)(be + 16 * j + 8 + 2 * t);
-            split_frag(x[2 * j], x[2 * j + 1], b0, b1, hi, lo);
-#pragma unroll
-            for (int i = j; i < 4; ++i) {
-                uint32_t b[4];
-                ldsm4(b, ah_ + blk_at(i, j) * 512 + blk_swz(brow, bcol));
-                mma16(o[2 * i], hi, b[0], b[1]);
-                mma16(o[2 * i + 1], hi, b[2], b[3]);
-                mma16(o[2 * i], lo, b[0], b[1]);
-                mma16(o[2 * i + 1], lo, b[2], b[3]);
-            }
-            const float2 e0 = *(const float2 *)(gates + kChunk + 16 * j + 2 * t);
-            const float2 e1 = *(const float2 *)(gates + kChunk + 16 * j + 8 + 2 * t);
-            split_frag(x[2 * j], x[2 * j + 1], make_float2(b0.x * e0.x, b0.y * e0.y), make_float2(b1.x * e1.x, b1.y * e1.y),
-                       hi, lo);
-#pragma unroll
-            for (int np = 0; np < NP / 16; ++np) {
-                uint32_t b[4];
-                ldsm4t(b, ks + swz<LINE>(16 * j + (lane & 15), 2 * np + (lane >> 4)));
-                mma16(s[2 * np], hi, b[0], b[1]);
-                mma16(s[2 * np + 1], hi, b[2], b[3]);
-                mma16(s[2 * np], lo, b[0], b[1]);
-                mma16(s[2 * np + 1], lo, b[2], b[3]);
-            }
-        }
-        // o: transposed through the warp's own columns of the v tile
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            stsm4t(vs + swz<128>(16 * j + brow, 2 * warp + bcol), tc::pack_bf2(o[2 * j][0], o[2 * j][1]),
-                   tc::pack_bf2(o[2 * j][2], o[2 * j][3]), tc::pack_bf2(o[2 * j + 1][0], o[2 * j + 1][1]),
-                   tc::pack_bf2(o[2 * j + 1][2], o[2 * j + 1][3]));
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 16 * i + (lane >> 1), cc = 2 * warp + (lane & 1), tok = c * kChunk + r;
-            if (tok < p.L && slice * 64 + cc * 8 < p.P)
-                *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) =
-                    *(const uint4 *)(st.v + swz<128>(r, cc));
+            for (int j = 0; j < 32; ++j)
+                if (slice * 64 + 32 * half + j < p.P) dst[(long long)j * p.N] = S[j];
         }
     }
-    // absent tokens past the last chunk
-    for (int i = nv * kChunk * 8 + threadIdx.x; i < p.L * 8; i += kThreads) {
-        const int tok = i / 8, cc = i % 8;
-        if (slice * 64 + cc * 8 < p.P)
-            *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
-    }
-    store_state<NP>(s, p.final_state ? p.final_state + sbase : nullptr, row, p.P, p.N, t);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
+    if (warp == 0) tmem_dealloc(tm, kAccCols);
+}
+
+// [b, L, heads, width] bf16: boxes of 64 columns x 64 tokens, zeros outside
+cudaError_t map_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width) {
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)b};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)heads * width * 2, (cuuint64_t)L * heads * width * 2};
+    const cuuint32_t box[4] = {64, 1, kChunk, 1};
+    return encode_tiles(m, ptr, 4, dims, strides, box);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     const DeltaParams &p = c.p;
+    ScanMaps maps;
+    cudaError_t e;
+    if ((e = map_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * ((p.P + 63) / 64));
-    const int bytes = 2 * (int)(p.N <= 64 ? sizeof(ScanStage<64>) : sizeof(ScanStage<128>));
-    auto kernel = p.N <= 64 ? delta_scan_fwd<64> : delta_scan_fwd<128>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, s>>>(c);
+    const bool one_per_sm = grid <= 152;
+    auto kernel = one_per_sm ? delta_scan_fwd<2> : delta_scan_fwd<1>;
+    const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    kernel<<<grid, kScanThreads, bytes, s>>>(c, maps);
     return cudaGetLastError();
 }
 
