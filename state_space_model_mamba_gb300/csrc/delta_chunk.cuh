@@ -18,8 +18,8 @@
 // The chunk image of one (b, h, chunk) is what the scan copies to shared memory: the
 // gate vectors in fp32, then Tt and At as hi and lo bf16 parts.  Each is kept as the
 // tensor core reads it without swizzle, in 8x8 matrices of 128 contiguous bytes:
-// columns 16 ks + 8 kc .. + 7 are one run of the row octets from 2 ks on (the octets
-// above are zero and not stored).
+// columns 16 ks .. 16 ks + 15 are one run of the row octets from 2 ks on, two matrices
+// an octet (the octets above are zero and not stored).
 #pragma once
 #include <cuda.h>
 
@@ -33,16 +33,14 @@ constexpr int kTri = 2 * 128 * (8 + 6 + 4 + 2);  // bytes of one lower triangle 
 constexpr int kGates = 3 * kChunk * 4;           // e^gamma, e^(gamma_C - gamma), beta
 // image: gates, then [hi, lo][Tt, At]
 constexpr int kImgTri = kGates, kImgBytes = kGates + 4 * kTri;
-// run (ks, kc) of a triangle: its first byte and its length
-__host__ __device__ constexpr int tri_run_bytes(int ks) { return (8 - 2 * ks) * 128; }
-__host__ __device__ constexpr int tri_run(int ks, int kc) {
-    return 2048 * ks - 256 * ks * (ks - 1) + kc * tri_run_bytes(ks);
-}
+// run ks of a triangle: its first byte and its length
+__host__ __device__ constexpr int tri_run_bytes(int ks) { return (8 - 2 * ks) * 256; }
+__host__ __device__ constexpr int tri_run(int ks) { return 2048 * ks - 256 * ks * (ks - 1); }
 // the 16-byte piece of row i, columns 8 c .. 8 c + 7 (c / 2 <= i / 16)
 __host__ __device__ constexpr int tri_piece(int i, int c) {
-    return tri_run(c >> 1, c & 1) + ((i >> 3) - (c & ~1)) * 128 + (i & 7) * 16;
+    return tri_run(c >> 1) + ((i >> 3) - (c & ~1)) * 256 + (c & 1) * 128 + (i & 7) * 16;
 }
-static_assert(tri_run(1, 0) == 2048 && tri_run(2, 0) == 3584 && tri_run(3, 1) + tri_run_bytes(3) == kTri, "triangle runs");
+static_assert(tri_run(1) == 2048 && tri_run(2) == 3584 && tri_run(3) + tri_run_bytes(3) == kTri, "triangle runs");
 
 struct ChunkParams {
     DeltaParams p;
@@ -59,6 +57,13 @@ inline int chunk_count(long long L) { return (int)((L + kChunk - 1) / kChunk); }
 // Tensor map of bf16 tiles in the 128-byte swizzle, zeros outside (delta_maps.cu).
 cudaError_t encode_tiles(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                          const cuuint32_t *box);
+// [b, L, heads, width] bf16: boxes of 64 columns of one head x a chunk's tokens
+inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width) {
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)b};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)heads * width * 2, (cuuint64_t)L * heads * width * 2};
+    const cuuint32_t box[4] = {64, 1, kChunk, 1};
+    return encode_tiles(m, ptr, 4, dims, strides, box);
+}
 
 cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s);
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s);

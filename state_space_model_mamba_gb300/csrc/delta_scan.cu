@@ -31,32 +31,22 @@ namespace {
 using namespace tc;
 
 constexpr int kCompute = 256;              // eight warps: TMEM lane quarter w % 4, column half w / 4
-constexpr int kScanThreads = kCompute + 32;  // and a warp that issues copies and products
+constexpr int kScanThreads = kCompute + 64;  // and a warp that issues the products, one that issues the copies
 constexpr uint32_t kAccCols = 128;
 
 // shared memory from a 1024-byte aligned base
 constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128; X (16 KB) and W (16 KB) in their place
 constexpr uint32_t kOffX = 0, kOffW = 16384;
-constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][kc][16 row octets][128 bytes]: Tt rows, then At rows
+constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][16 row octets][2][128 bytes]: Tt rows, then At rows
 constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
 constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
 constexpr uint32_t kKQBytes = 32768;
 
-// descriptor of K-step ks of the unswizzled [Tt; At] operand
-__device__ __forceinline__ uint64_t sdesc_tri(uint32_t base, int ks) {
-    const uint32_t a = base + (uint32_t)ks * 4096u;
-    return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(2048 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-// 32 floats as 64 bytes of each of a SW128 tile's hi and lo parts: row `row`, 16-byte pieces c0 .. c0 + 3
-__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float *x) {
+// 8 values as one 16-byte piece of row `row` of a hi and of a lo tile (SW128)
+__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float2 *x) {
     uint32_t h[4], l[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
+    for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
     st_shared_v4(hi_tile + sw128_chunk(row, piece), h[0], h[1], h[2], h[3]);
     st_shared_v4(lo_tile + sw128_chunk(row, piece), l[0], l[1], l[2], l[3]);
 }
@@ -102,125 +92,135 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     const uint32_t tm = s_tmem;
 
     if (warp == kCompute / 32) {
-        // ---- copies and products
-        const int grp = h / p.hpg;
-        const uint32_t half_k = p.N > 64 ? 2u : 1u;
-        int kq_issued = 0, tri_issued = 0, v_issued = 0, done = 0;
-        // tma_load_* take generic pointers; shared addresses are passed through this one
-        auto tma = [&](uint32_t dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1, int c2, int c3) {
-            asm volatile(
-                "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-                "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-                : "memory");
-        };
-        auto expect_kq = [&](int c) {
-            if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], half_k * 16384u);
-            kq_issued = c + 1;
-        };
-        auto load_half = [&](int c, const CUtensorMap *m, uint32_t off) {
-            if (lane == 0)
-                for (uint32_t kb = 0; kb < half_k; ++kb)
-                    tma(base + kOffKQ + (c % NB) * kKQBytes + kb * 16384u + off, m, &bar_kq[c % NB], 64 * kb, grp, c * kChunk, bi);
-        };
-        auto load_tri = [&](int c) {
-            if (lane == 0) mbar_arrive_expect_tx(&bar_tri, 4 * kTri);
-            __syncwarp();
-            const int part = lane >> 4, which = (lane >> 3) & 1, ks = (lane >> 1) & 3, kc = lane & 1;
-            bulk_load(base + kOffTri + part * 16384 + ks * 4096 + kc * 2048 + which * 1024 + 2 * ks * 128,
-                      img0 + (long long)c * kImgBytes + kImgTri + (2 * part + which) * kTri + tri_run(ks, kc),
-                      tri_run_bytes(ks), &bar_tri);
-            tri_issued = c + 1;
-        };
-        auto load_v = [&](int c) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar_v, 8192);
-                tma(base + kOffV, &maps.v, &bar_v, 64 * slice, h, c * kChunk, bi);
-            }
-            v_issued = c + 1;
-        };
-        for (int c = 0; c < NB && c < nv; ++c) {
-            expect_kq(c);
-            load_half(c, &maps.k, 0);
-            load_half(c, &maps.q, 8192);
-        }
-        if (nv > 0) {
-            load_tri(0);
-            load_v(0);
-        }
+        // ---- products
         const uint32_t i1 = idesc_bf16(128, 128, false, true), i2 = idesc_bf16(128, 64, false, true),
                        i3 = idesc_bf16(128, 128, true, true);
+        const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
+                       dW = sdesc(base + kOffW, 8192, 1024), dT = sdesc_tri(base + kOffTri);
         bool ok = true;
+        int done = 0;
         for (int c = 0; c < nv; ++c) {
             const uint32_t ph = c & 1, kq = base + kOffKQ + (c % NB) * kKQBytes;
+            const uint64_t dK = sdesc(kq, 16, 1024), dKt = sdesc(kq, 16384, 1024);
             ok = mbar_wait(&bar_kq[c % NB], (c / NB) & 1) && mbar_wait(&bar_s, ph);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
-                for (int ks = 0; ks < nks; ++ks)
-                    mma_bf16(tm, sdesc_kmajor(kq, ks, 16384), sdesc_mnmajor(base + kOffS, ks, 16384), i1, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    if (ks < nks) mma_bf16(tm, sdesc_add(dK, (ks >> 2) * 16384 + (ks & 3) * 32), sdesc_add(dS, ks * 2048), i1, ks > 0);
                 mma_commit(&bar_m[0]);
             }
             ok = mbar_wait(&bar_tri, ph) && mbar_wait(&bar_x, ph);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
+#pragma unroll
                 for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm, sdesc_tri(base + kOffTri + (pass == 2 ? 16384 : 0), ks),
-                                 sdesc_mnmajor(base + kOffX + (pass == 1 ? 8192 : 0), ks, 8192), i2, true);
+                        mma_bf16(tm, sdesc_add(dT, (pass == 2 ? 16384 : 0) + ks * 4096),
+                                 sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i2, true);
                 mma_commit(&bar_m[1]);
-            }
-            __syncwarp();
-            // V has been read, and Q by the first product
-            if (c + 1 < nv) load_v(c + 1);
-            if (NB == 1 && c + 1 < nv) {
-                expect_kq(c + 1);
-                load_half(c + 1, &maps.q, 8192);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph));
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tm, sdesc_mnmajor(kq, ks, 16384), sdesc_mnmajor(base + kOffW, ks, 8192), i3, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, ks > 0);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
             done = c + 1;
-            if (c + 1 < nv) load_tri(c + 1);
+        }
+        if (!ok) s_err = 1;
+        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);  // every product has to complete before the block may end
+    } else if (warp == kCompute / 32 + 1) {
+        // ---- copies
+        const int grp = h / p.hpg;
+        const uint32_t halves = p.N > 64 ? 2u : 1u;
+        int kq_issued = 0, tri_issued = 0, v_issued = 0;
+        auto expect_kq = [&](int c) {
+            if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], halves * 16384u);
+            kq_issued = c + 1;
+        };
+        auto load_rows = [&](int c, const CUtensorMap *m, uint32_t off) {
+            if (lane == 0)
+                for (uint32_t kb = 0; kb < halves; ++kb)
+                    tma_tile(base + kOffKQ + (c % NB) * kKQBytes + kb * 16384u + off, m, &bar_kq[c % NB], 64 * kb, grp, c * kChunk, bi);
+        };
+        auto load_tri = [&](int c) {
+            if (lane == 0) mbar_arrive_expect_tx(&bar_tri, 4 * kTri);
+            __syncwarp();
+            if (lane < 16) {
+                const int part = lane >> 3, which = (lane >> 2) & 1, ks = lane & 3;
+                bulk_load(base + kOffTri + part * 16384 + ks * 4096 + which * 2048 + 2 * ks * 256,
+                          img0 + (long long)c * kImgBytes + kImgTri + (2 * part + which) * kTri + tri_run(ks), tri_run_bytes(ks),
+                          &bar_tri);
+            }
+            tri_issued = c + 1;
+        };
+        auto load_v = [&](int c) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar_v, 8192);
+                tma_tile(base + kOffV, &maps.v, &bar_v, 64 * slice, h, c * kChunk, bi);
+            }
+            v_issued = c + 1;
+        };
+        for (int c = 0; c < NB && c < nv; ++c) {
+            expect_kq(c);
+            load_rows(c, &maps.k, 0);
+            load_rows(c, &maps.q, 8192);
+        }
+        if (nv > 0) {
+            load_v(0);
+            load_tri(0);
+        }
+        bool ok = true;
+        for (int c = 0; c + 1 < nv; ++c) {
+            const uint32_t ph = c & 1;
+            // V and, by the first product, Q have been read
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
+            if (NB == 1) {
+                expect_kq(c + 1);
+                load_rows(c + 1, &maps.q, 8192);
+            }
+            load_v(c + 1);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph)))) break;
+            load_tri(c + 1);
             if (c + NB < nv) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
-                if (!ok) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
                 if (NB > 1) {
                     expect_kq(c + NB);
-                    load_half(c + NB, &maps.q, 8192);
+                    load_rows(c + NB, &maps.q, 8192);
                 }
-                load_half(c + NB, &maps.k, 0);
+                load_rows(c + NB, &maps.k, 0);
             }
         }
         if (!ok) s_err = 1;
-        // every copy has to land and every product to complete before the block may end
+        // every copy has to land before the block may end
         for (int c = max(0, kq_issued - NB); c < kq_issued; ++c) mbar_wait(&bar_kq[c % NB], (c / NB) & 1);
         if (tri_issued) mbar_wait(&bar_tri, (tri_issued - 1) & 1);
         if (v_issued) mbar_wait(&bar_v, (v_issued - 1) & 1);
-        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);
     } else {
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // rows 0 .. 63: K tokens, 64 .. 127: Q tokens
         const int i = row & 63;              // the row's token
         const uint32_t my = tmem_addr(tm, 32 * quarter, 32 * half);
-        float S[32];
+        const float2 one = make_float2(1.f, 1.f);
+        float2 S[16];
         {
             const float *src = p.init ? p.init + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row : nullptr;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                S[j] = (src && row < p.N && slice * 64 + 32 * half + j < p.P) ? src[(long long)j * p.N] : 0.f;
+                ((float *)S)[j] = (src && row < p.N && slice * 64 + 32 * half + j < p.P) ? src[(long long)j * p.N] : 0.f;
         }
         bool ok = true;
         // S as an operand; before the last chunk, K rows of absent tokens are made zero
         auto publish_s = [&](int c) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 8 * j);
+            for (int j = 0; j < 4; ++j) store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 4 * j);
             const int live = V - c * kChunk;
             if (live < kChunk) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[c % NB], (c / NB) & 1));
@@ -239,45 +239,39 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             const float *gates = (const float *)(img0 + (long long)c * kImgBytes);
             const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
             const float ec = __ldg(gates + kChunk - 1);
-            const bool live = c * kChunk + i < V;
+            const bool live = c * kChunk + i < V, partial = V - c * kChunk < kChunk;
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float a[16], b[16];
-                tmem_ld16(my + 16 * j, a);
-                tmem_ld16(my + 64 + 16 * j, b);
+                float2 a[8], b[8];
+                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
                 if (keys) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + 2 * j + u));
                         const uint32_t vv[4] = {w.x, w.y, w.z, w.w};
-                        float xb[8];
+                        float2 xb[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float v = (e & 1) ? bf_hi(vv[e >> 1]) : bf_lo(vv[e >> 1]);
-                            const float x = live ? v - eg * (a[8 * u + e] + b[8 * u + e]) : 0.f;
-                            a[8 * u + e] = x;
-                            xb[e] = be * x;
+                        for (int e = 0; e < 4; ++e) {
+                            float2 x = ffma2(a[4 * u + e], make_float2(-eg, -eg), bf2_to_f2(vv[e]));
+                            if (partial && !live) x = make_float2(0.f, 0.f);
+                            a[4 * u + e] = x;
+                            xb[e] = fmul2(x, make_float2(be, be));
                         }
                         store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + 2 * j + u, xb);
                     }
                 } else {
+                    const float f = p.scale * eg;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) a[e] = p.scale * eg * (a[e] + b[e]);
+                    for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
                 }
-                uint32_t r[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(a[e]);
-                asm volatile(
-                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t" ::"r"(
-                        my + 16 * j),
-                    "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                    : "memory");
+                tmem_st16(my + 16 * j, (const float *)a);
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tmem_wait_st();
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
@@ -287,14 +281,17 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             if (!ok) break;
             tc_fence_after();
             {
-                float a[32];
-                tmem_ld32(my, a);
+                float2 a[16];
+                tmem_ld32(my, (float *)a);
                 if (keys) {
                     const float f = be * et;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) a[e] = live ? f * a[e] : 0.f;
+                    for (int e = 0; e < 16; ++e) {
+                        a[e] = fmul2(a[e], make_float2(f, f));
+                        if (partial && !live) a[e] = make_float2(0.f, 0.f);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, a + 8 * j);
+                    for (int j = 0; j < 4; ++j) store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, a + 4 * j);
                     fence_async_smem();
                 }
                 tc_fence_before();
@@ -307,8 +304,8 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                     for (int j = 0; j < 4; ++j)
                         if (tok < p.L && slice * 64 + 32 * half + 8 * j < p.P)
                             *(uint4 *)(dst + 8 * j) =
-                                live ? make_uint4(pack_bf2(a[8 * j], a[8 * j + 1]), pack_bf2(a[8 * j + 2], a[8 * j + 3]),
-                                                  pack_bf2(a[8 * j + 4], a[8 * j + 5]), pack_bf2(a[8 * j + 6], a[8 * j + 7]))
+                                live ? make_uint4(pack_bf2(a[4 * j].x, a[4 * j].y), pack_bf2(a[4 * j + 1].x, a[4 * j + 1].y),
+                                                  pack_bf2(a[4 * j + 2].x, a[4 * j + 2].y), pack_bf2(a[4 * j + 3].x, a[4 * j + 3].y))
                                      : make_uint4(0, 0, 0, 0);
                 }
             }
@@ -317,11 +314,11 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float a[16], b[16];
-                tmem_ld16(my + 16 * j, a);
-                tmem_ld16(my + 64 + 16 * j, b);
+                float2 a[8], b[8];
+                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[16 * j + e] = fmaf(ec, S[16 * j + e], a[e] + b[e]);
+                for (int e = 0; e < 8; ++e)
+                    S[8 * j + e] = ffma2(S[8 * j + e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
             }
             if (c + 1 < nv) publish_s(c + 1);
         }
@@ -336,7 +333,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             float *dst = p.final_state + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (slice * 64 + 32 * half + j < p.P) dst[(long long)j * p.N] = S[j];
+                if (slice * 64 + 32 * half + j < p.P) dst[(long long)j * p.N] = ((const float *)S)[j];
         }
     }
     tc_fence_before();
@@ -346,23 +343,15 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     if (warp == 0) tmem_dealloc(tm, kAccCols);
 }
 
-// [b, L, heads, width] bf16: boxes of 64 columns x 64 tokens, zeros outside
-cudaError_t map_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width) {
-    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)b};
-    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)heads * width * 2, (cuuint64_t)L * heads * width * 2};
-    const cuuint32_t box[4] = {64, 1, kChunk, 1};
-    return encode_tiles(m, ptr, 4, dims, strides, box);
-}
-
 }  // namespace
 
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     const DeltaParams &p = c.p;
     ScanMaps maps;
     cudaError_t e;
-    if ((e = map_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * ((p.P + 63) / 64));
     const bool one_per_sm = grid <= 152;
     auto kernel = one_per_sm ? delta_scan_fwd<2> : delta_scan_fwd<1>;
