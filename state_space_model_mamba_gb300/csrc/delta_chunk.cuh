@@ -57,11 +57,12 @@ inline int chunk_count(long long L) { return (int)((L + kChunk - 1) / kChunk); }
 // Tensor map of bf16 tiles in the 128-byte swizzle, zeros outside (delta_maps.cu).
 cudaError_t encode_tiles(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                          const cuuint32_t *box);
-// [b, L, heads, width] bf16: boxes of 64 columns of one head x a chunk's tokens
-inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width) {
+// [b, L, heads, width] bf16: boxes of 64 columns of one head x a chunk's (or fewer) tokens
+inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width,
+                                    int tokens = kChunk) {
     const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)b};
     const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)heads * width * 2, (cuuint64_t)L * heads * width * 2};
-    const cuuint32_t box[4] = {64, 1, kChunk, 1};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)tokens, 1};
     return encode_tiles(m, ptr, 4, dims, strides, box);
 }
 

@@ -7,14 +7,17 @@
 //     Tt (I + diag(beta) E) = -E      and      At (I + diag(beta) E) = A,
 // so both matrices are rows of one right-hand solve with a unit lower triangle, and
 // every row is independent: thread i of 128 holds row i of [E; A] as it comes out of
-// tensor memory and substitutes from its last column to its first in fp32
-// registers,
-//     y_j = r_j - sum_{m > j} y_m beta_m E_mj,
-// reading diag(beta) E from shared memory as broadcasts.  Substitution stays accurate for
-// repeated keys, where a power series of the triangle would lose every digit.
-// What bounds it are the 5000 warp-wide multiply-adds of the two solves a head and
-// chunk (rows 0 - 31 stop at column 31); a matrix instruction on the 16x16 pieces
-// needs fp32 operands in three parts and was slower.
+// tensor memory and substitutes from its last column to its first in fp32,
+//     y_j = r_j - sum_{m > j} (beta_m y_m) E_mj,
+// 16 columns at a time: first the columns already solved (beta y from shared memory,
+// column m of all threads side by side; E rows as broadcasts), then the 16 x 16 triangle
+// in registers.  Substitution stays accurate for repeated keys, where a power series
+// of the triangle would lose every digit.
+// What bounds it are the multiply-adds of the two solves, 2000 for each of the rows
+// 32 .. 63 and 500 for the others.  Rolled over the blocks: the whole substitution
+// unrolled (40 KB of code) waited for instructions half of the time.  The rows are
+// swapped by halves in every other block, so that the long ones do not always land on
+// the same two schedulers.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -26,38 +29,19 @@ using namespace tc;
 
 constexpr int kThreads = 128;
 constexpr int kHeadsPer = 4;          // heads of a group per block
-constexpr int kLdG = 68;              // floats per column of diag(beta) E: 16-byte rows, four banks apart
+constexpr int kLdE = 68;              // floats per row of E: 16-byte pieces, rows four banks apart
 constexpr uint32_t kAccCols = 64;
 
 struct PrepMaps {
     CUtensorMap k, q;
 };
 
-// y_j = r_j - sum_{m > j} y_m g[j][m] for j = M-1 .. 0
-template <int M>
-__device__ __forceinline__ void solve_row(float (&y)[kChunk], const float *g) {
-#pragma unroll
-    for (int j = M - 2; j >= 0; --j) {
-        float a0 = y[j], a1 = 0.f, a2 = 0.f, a3 = 0.f;
-        // the newest value, y[j + 1], comes last
-#pragma unroll
-        for (int m4 = (M - 1) / 4; m4 >= (j + 1) / 4; --m4) {
-            const float4 w = *(const float4 *)(g + j * kLdG + 4 * m4);
-            if (4 * m4 + 3 > j) a3 = fmaf(-y[4 * m4 + 3], w.w, a3);
-            if (4 * m4 + 2 > j) a2 = fmaf(-y[4 * m4 + 2], w.z, a2);
-            if (4 * m4 + 1 > j) a1 = fmaf(-y[4 * m4 + 1], w.y, a1);
-            if (4 * m4 > j) a0 = fmaf(-y[4 * m4], w.x, a0);
-        }
-        y[j] = (a0 + a1) + (a2 + a3);
-    }
-}
-
 // Grid: one block per (b, group, slice of the group's heads, chunk).
 __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_load, bar_mma;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_g[kChunk * kLdG];
+    __shared__ __align__(16) float s_e[kChunk * kLdE];
     __shared__ float2 s_gam[kChunk];   // gamma log2(e), hi and lo
     __shared__ float s_beta[kChunk];
     const DeltaParams &p = cp.p;
@@ -70,15 +54,18 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
     if (t0 >= V) return;
     const uint32_t kq = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t halves = p.N > 64 ? 2u : 1u;
+    const int flip = (blockIdx.x * 0x9E3779B1u) >> 31;  // tokens 32 .. 63 in rows (and columns) 0 .. 31
     if (tid == 0) {
         mbar_init(&bar_load, 1);
         mbar_init(&bar_mma, 1);
         mbar_fence_init();
         mbar_arrive_expect_tx(&bar_load, halves * 16384u);
-        for (uint32_t kb = 0; kb < halves; ++kb) {
-            tma_tile(kq + kb * 16384u, &maps.k, &bar_load, 64 * kb, grp, t0, bi);
-            tma_tile(kq + kb * 16384u + 8192u, &maps.q, &bar_load, 64 * kb, grp, t0, bi);
-        }
+        for (uint32_t kb = 0; kb < halves; ++kb)
+            for (int x = 0; x < 2; ++x) {
+                const int tok = t0 + 32 * (x ^ flip);
+                tma_tile(kq + kb * 16384u + 4096u * x, &maps.k, &bar_load, 64 * kb, grp, tok, bi);
+                tma_tile(kq + kb * 16384u + 8192u + 4096u * x, &maps.q, &bar_load, 64 * kb, grp, tok, bi);
+            }
     }
     if (warp == 0) tmem_alloc(&s_tmem, kAccCols);
     tc_fence_before();
@@ -96,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         }
         __syncwarp();
     }
-    const int i = tid & 63;               // the row's token
+    const int i = (tid & 63) ^ (32 * flip);  // the row's token
     const bool keys = tid < kChunk, live = t0 + i < V;  // rows of absent tokens may hold anything: made zero
     const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * kHeadsPer);
     for (int h = grp * p.hpg + slice * kHeadsPer; h < h_end; ++h) {
@@ -131,52 +118,85 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
             tc_fence_after();
         }
         if (__syncthreads_and(ok) == 0) break;
-        // rows of -E (the key rows) or A
-        float y[kChunk];
         const float2 gi = s_gam[i];
-        const float f = keys ? -1.f : p.scale;
-        const bool low = warp & 1;        // rows 32 .. 63
+        const int last = i >> 4 | 1;      // warps of rows 0 .. 31 stop after two blocks of columns
+        // 16 columns of D o (row of K K^T or Q K^T), zero where j >= i (keys) or j > i
+        auto decayed = [&](int jb, float f, float (&r)[16]) {
+            float a[16];
+            tmem_ld16(tmem_addr(tm, 32 * warp, (16 * jb) ^ (32 * flip)), a);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (q < 2 || low) {
-                float a[16];
-                tmem_ld16(tmem_addr(tm, 32 * warp, 16 * q), a);
+            for (int e = 0; e < 16; ++e) {
+                const int j = 16 * jb + e;
+                const float2 gj = s_gam[j];
+                const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y));
+                r[e] = live && (j < i || (j == i && !keys)) ? f * d * a[e] : 0.f;
+            }
+        };
+        if (keys)
+            for (int jb = 0; jb <= (last | 1); ++jb) {
+                float r[16];
+                decayed(jb, 1.f, r);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = 16 * q + e;
-                    const float2 gj = s_gam[j];
-                    const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y));
-                    y[j] = live && (j < i || (j == i && !keys)) ? f * d * a[e] : 0.f;
+                for (int e = 0; e < 4; ++e)
+                    *(float4 *)(s_e + i * kLdE + 16 * jb + 4 * e) = make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+            }
+        __syncthreads();
+        // z[m][row] = beta_m y_m of this thread's row, over the tiles (which the products have read)
+        float *z = (float *)(smem_raw + (kq - smem_u32(smem_raw))) + tid;
+        char *tri = img + kImgTri + (keys ? 0 : kTri);
+        for (int jb = last; jb >= 0; --jb) {
+            float2 y[8];
+            if (keys) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 v = *(const float4 *)(s_e + i * kLdE + 16 * jb + 4 * e);
+                    y[2 * e] = make_float2(-v.x, -v.y);
+                    y[2 * e + 1] = make_float2(-v.z, -v.w);
                 }
             } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[16 * q + e] = 0.f;
+                decayed(jb, p.scale, (float(&)[16])y);
             }
-        }
-        if (keys) {  // diag(beta) E by columns
-            const float b = -s_beta[i];
+            const float *e0 = s_e + 16 * jb;
+#pragma unroll 4
+            for (int m = 16 * last + 15; m >= 16 * (jb + 1); --m) {
+                const float zm = -z[m * kThreads];
+                const float4 *w = (const float4 *)(e0 + m * kLdE);
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j)
-                if (j < 32 || low) s_g[j * kLdG + i] = b * y[j];
-        }
-        __syncthreads();
-        if (low)
-            solve_row<64>(y, s_g);
-        else
-            solve_row<32>(y, s_g);
-        // hi and lo parts: 16-byte pieces, neighbouring rows on neighbouring addresses
-        char *tri = img + kImgTri + (keys ? 0 : kTri);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if ((c >> 1) <= (i >> 4)) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) split2(y[8 * c + 2 * e], y[8 * c + 2 * e + 1], hi[e], lo[e]);
-                char *dst = tri + tri_piece(i, c);
-                *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *(uint4 *)(dst + 2 * kTri) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const float4 v = w[e];
+                    y[2 * e] = ffma2(make_float2(v.x, v.y), make_float2(zm, zm), y[2 * e]);
+                    y[2 * e + 1] = ffma2(make_float2(v.z, v.w), make_float2(zm, zm), y[2 * e + 1]);
+                }
             }
-        __syncthreads();  // s_g and the gates may be written for the next head
+            // the triangle of the block: from the last column, each solved one taken off those before it
+            float *yy = (float *)y;
+#pragma unroll
+            for (int m = 15; m >= 0; --m) {
+                const float zm = -s_beta[16 * jb + m] * yy[m];
+                z[(16 * jb + m) * kThreads] = -zm;
+                const float4 *w = (const float4 *)(e0 + (16 * jb + m) * kLdE);
+#pragma unroll
+                for (int e = 0; e < (m + 3) / 4; ++e) {
+                    const float4 v = w[e];
+                    yy[4 * e] = fmaf(zm, v.x, yy[4 * e]);
+                    if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(zm, v.y, yy[4 * e + 1]);
+                    if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(zm, v.z, yy[4 * e + 2]);
+                    if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
+                }
+            }
+            // hi and lo parts: 16-byte pieces, neighbouring rows on neighbouring addresses
+            if (jb <= (i >> 4))
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2(y[4 * c + e].x, y[4 * c + e].y, hi[e], lo[e]);
+                    char *dst = tri + tri_piece(i, 2 * jb + c);
+                    *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4 *)(dst + 2 * kTri) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+        }
+        __syncthreads();  // s_e and the gates may be written for the next head
     }
     if (tid == 0) {
         if (!ok) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
@@ -195,9 +215,9 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
     const DeltaParams &p = c.p;
     PrepMaps maps;
     cudaError_t e;
-    if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    const int bytes = 1024 + (p.N > 64 ? 32768 : 16384);
+    if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
+    const int bytes = 1024 + 32768;  // the tiles, then z
     const unsigned grid = (unsigned)c.n * ((p.hpg + kHeadsPer - 1) / kHeadsPer) * p.b * p.G;
     if ((e = cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     delta_prep_kernel<<<grid, kThreads, bytes, s>>>(c, maps);
