@@ -58,7 +58,7 @@ ssd_status cuda_status(cudaError_t e) {
     return e == cudaSuccess ? SSD_OK : fail(SSD_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 }
 
-constexpr size_t kStatusBytes = 256;  // status words, then the paths' own buffers
+constexpr size_t kStatusBytes = 1024;  // status words, then the paths' own buffers
 
 DeltaParams base_params(const delta_dims &d, const void *q, const void *k, const void *v, const float *g,
                         const float *beta, float scale, const float *init, const int32_t *valid_len, void *ws) {
@@ -83,8 +83,35 @@ DeltaParams base_params(const delta_dims &d, const void *q, const void *k, const
     return p;
 }
 
-size_t image_bytes(const delta_dims &d) {
-    return (size_t)d.batch * d.nheads * chunk_count(d.seqlen) * kImgBytes;
+// The chunked path's buffers behind the status words: the images, then what the backward keeps.
+size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
+    const size_t n = chunk_count(d.seqlen), chains = (size_t)d.batch * d.nheads, nsl = (d.headdim + 63) / 64, cs = chains * nsl;
+    size_t off = kStatusBytes;
+    auto take = [&](size_t bytes) {
+        char *at = ws + off;
+        off += (bytes + 1023) / 1024 * 1024;
+        return at;
+    };
+    char *img = take(chains * n * kImgBytes);
+    ChunkBackward w;
+    memset(&w, 0, sizeof(w));
+    if (backward) {
+        w.rev = take(chains * n * kRevBytes);
+        w.states = take(cs * (n + 1) * kStateTile);
+        w.dstates = take(cs * n * kDStateTile);
+        w.errs = take(cs * n * kErrTile);
+        w.reads = take(cs * n * kErrTile);
+        w.dv_lo = take(cs * n * kDvLoTile);
+        w.ss = (float *)take(cs * n * 8 * 4);
+        for (float **x : {&w.ww, &w.fq, &w.fk, &w.zx}) *x = (float *)take(cs * 2 * n * kChunk * 4);
+        w.pe = (float *)take(cs * n * kChunk * 4);
+    }
+    if (c) {
+        c->n = (int)n;
+        c->img = img;
+        c->w = w;
+    }
+    return off;
 }
 
 }  // namespace
@@ -104,7 +131,7 @@ ssd_status delta_supported(const delta_dims *dims, ssd_dtype dtype) {
 size_t delta_workspace_bytes(const delta_dims *dims, ssd_dtype dtype, int backward) {
     record_error("");
     if (validate(dims, dtype) != SSD_OK) return 0;
-    if (!backward && chunk_supported(*dims, dtype)) return kStatusBytes + image_bytes(*dims);
+    if (chunk_supported(*dims, dtype)) return carve(*dims, backward != 0, nullptr, nullptr);
     return kStatusBytes + (backward ? simt_backward_bytes(*dims) : 0);
 }
 
@@ -127,7 +154,9 @@ ssd_status delta_forward(const delta_dims *dims, ssd_dtype dtype, const void *q,
     p.final_state = final_state;
     cudaStream_t cs = (cudaStream_t)stream;
     if (!chunk_supported(*dims, dtype)) return cuda_status(launch_simt_forward(p, dtype == SSD_BF16, cs));
-    const ChunkParams c{p, chunk_count(dims->seqlen), (char *)workspace + kStatusBytes};
+    ChunkParams c;
+    c.p = p;
+    carve(*dims, false, (char *)workspace, &c);
     st = cuda_status(launch_chunk_prep(c, cs));
     return st != SSD_OK ? st : cuda_status(launch_chunk_forward(c, cs));
 }
@@ -156,7 +185,16 @@ ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q
     p.dg = dg;
     p.dbeta = dbeta;
     p.d_init = d_init_state;
-    return cuda_status(launch_simt_backward(p, dtype == SSD_BF16, (char *)workspace + kStatusBytes, (cudaStream_t)stream));
+    cudaStream_t cs = (cudaStream_t)stream;
+    if (!chunk_supported(*dims, dtype))
+        return cuda_status(launch_simt_backward(p, dtype == SSD_BF16, (char *)workspace + kStatusBytes, cs));
+    ChunkParams c;
+    c.p = p;
+    carve(*dims, true, (char *)workspace, &c);
+    if ((st = cuda_status(launch_chunk_prep(c, cs))) != SSD_OK) return st;
+    if ((st = cuda_status(launch_chunk_forward(c, cs))) != SSD_OK) return st;
+    if ((st = cuda_status(launch_chunk_reverse(c, cs))) != SSD_OK) return st;
+    return cuda_status(launch_chunk_grads(c, cs));
 }
 
 ssd_status delta_step(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,

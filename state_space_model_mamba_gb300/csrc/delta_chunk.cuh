@@ -30,7 +30,8 @@ namespace delta {
 
 constexpr int kChunk = 64;
 constexpr int kTri = 2 * 128 * (8 + 6 + 4 + 2);  // bytes of one lower triangle (5120)
-constexpr int kGates = 3 * kChunk * 4;           // e^gamma, e^(gamma_C - gamma), beta
+// e^gamma, e^(gamma_C - gamma), beta; then pairs gamma log2(e) as hi and lo
+constexpr int kGates = 5 * kChunk * 4;
 // image: gates, then [hi, lo][Tt, At]
 constexpr int kImgTri = kGates, kImgBytes = kGates + 4 * kTri;
 // run ks of a triangle: its first byte and its length
@@ -42,11 +43,35 @@ __host__ __device__ constexpr int tri_piece(int i, int c) {
 }
 static_assert(tri_run(1) == 2048 && tri_run(2) == 3584 && tri_run(3) + tri_run_bytes(3) == kTri, "triangle runs");
 
+// What the backward's kernels keep, per (b, h) chain and slice of 64 columns of P (chain-slice
+// cs = bh * nsl + slice).  Tiles are in the 128-byte swizzle, ready as operands.
+//   rev    [b, H, n]        Tt hi, A hi, Tt lo, A lo, each [64 rows][64 columns] (32 KB)
+//   states [cs, n + 1]      S before every chunk and after the last: hi, lo parts [128 n][64] (32 KB)
+//   dstates [cs, n]         dS after every chunk: [128 n][64] (16 KB)
+//   errs, reads [cs, n]     Z and e^gamma o (K S): hi, lo parts [64 tokens][64] (16 KB each)
+//   dv_lo  [cs, n]          what dV lost to its rounding: [64 tokens][64] (8 KB)
+// dg is the sum of everything that crosses its token inside the chunk, so that no term carries
+// less decay than the result (products of whole rows, do.o - dv.v and <S, dS>, would be the same sum
+// but cancel where a head forgets fast):
+//     dg_t = ss + sum_{j < t} ww_j + sum_{i >= t} (fq_i + fk_i + pe_i)
+//     ss = e^gamma_C <S, dS>            S before, dS after the chunk    [cs, n, 8], a share of each warp
+//     ww = beta Z.(e^(gamma_C - gamma) K dS)                            the next four [cs, 2, n * 64]:
+//     fq = dO.(scale e^gamma Q S),  fk = -dV.(e^gamma K S),  zx = Z.X   sums of rows of 32 columns
+//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n * 64]   (delta_grad.cu)
+// and dbeta = zx.
+struct ChunkBackward {
+    char *rev, *states, *dstates, *errs, *reads, *dv_lo;
+    float *ss, *ww, *fq, *fk, *zx, *pe;
+};
+
 struct ChunkParams {
     DeltaParams p;
     int n;           // chunks
     char *img;       // [b, H, n] images
+    ChunkBackward w; // pointers are null in the forward
 };
+constexpr int kRevBytes = 32768, kStateTile = 32768, kDStateTile = 16384, kErrTile = 16384, kDvLoTile = 8192;
+__host__ __device__ __forceinline__ int slices_of(const DeltaParams &p) { return (p.P + 63) / 64; }
 
 inline bool chunk_supported(const delta_dims &d, ssd_dtype t) {
     return t == SSD_BF16 && !(d.flags & DELTA_FLAG_SIMT) && d.headdim % 8 == 0 && d.dstate % 8 == 0 &&
@@ -67,7 +92,9 @@ inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int 
 }
 
 cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s);
-cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s);
+cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s);   // with c.w: the backward's recompute
+cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s);   // dS, dv and the gates' sums
+cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s);     // dq, dk, dg, dbeta
 
 }  // namespace delta
 }  // namespace ssd

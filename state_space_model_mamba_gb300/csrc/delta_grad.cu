@@ -1,0 +1,398 @@
+// delta_grad.cu -- dq and dk of the chunked gated delta rule, all chunks in
+// parallel, and the gates' gradients from the sums that the two scans left.
+//
+// Per chunk and head, with D_ij = exp(gamma_i - gamma_j), the forward's S (before the
+// chunk) and Z, the reverse pass's dS (after the chunk) and dV:
+//     Nm_ij = scale D_ij beta_j (dO_i . Z_j), j <= i;    M_ij = -D_ij beta_j (dV_i . Z_j), j < i
+//     dQ = scale e^gamma o (dO S^T) + Nm K
+//     dK = -e^gamma o (dV S^T) + M K + Nm^T Q + M^T K + (beta e^(gamma_C - gamma) o Z) dS^T
+// in three groups of products: [Q; K] K^T, and [dO; dV] on S and Z at once (128 rows,
+// 192 columns); then [Nm; M] K, whose rows 0 .. 63 complete dQ; then, onto the same
+// accumulator, W dS^T with W = beta e^(gamma_C - gamma) o Z, and (Nm; M)^T [Q; K], whose
+// rows 64 .. 127 complete dK (the upper rows are spent by then and take what falls on
+// them).  The heads of a key group are walked by one block, which adds them up in
+// registers: dq and dk are written once, in a fixed order.  Z, S, Nm and M come as hi + lo
+// parts: what a token reads of S and what the chunk has written over it cancel, and the
+// share of dg that passes between tokens of the chunk is made here,
+//     pe_i = sum_j P_ij - sum_j P_ji,   P = Nm o Q K^T + M o K K^T;
+// dV (beside dO Z^T and dV Z^T), W and dS are rounded once, as dk is.
+// Two blocks share an SM and hide each other's copies and passes.
+#include "delta_chunk.cuh"
+#include "delta_mma.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+using namespace tc;
+
+constexpr int kCompute = 256, kThreads = kCompute + 32;
+// shared memory: 64 rows of zeros; dV lo, then W; S hi (then [Nm; M] hi) and Z hi; Z lo, then sums;
+// S lo, then dS; dO and dV (then [Nm; M] lo); Q and K
+constexpr uint32_t kOffZero = 0, kOffW = 8192, kOffSZ = 16384, kOffZ = kOffSZ + 16384, kOffP = kOffSZ, kOffZlo = 40960,
+                   kOffDS = 49152, kOffDV = 65536, kOffPlo = kOffDV, kOffQK = 81920, kOffSmall = 114688;
+struct Small {
+    float2 gam[kChunk];
+    float beta[kChunk];
+    uint64_t qk, in, ds, p, out, q, m[3];
+    uint32_t tmem;
+    int err;
+};
+constexpr uint32_t kBytes = kOffSmall + sizeof(Small);
+static_assert(2 * (kBytes + 1024) <= 233472, "two blocks per SM");
+struct GradMaps {
+    CUtensorMap k, q, d_o, dv;
+};
+
+// Grid: one block per (b, group, chunk).
+__global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkParams cp, const __grid_constant__ GradMaps maps) {
+    // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Small &sm = *(Small *)(smem_raw + kOffSmall);
+    uint64_t &bar_qk = sm.qk, &bar_in = sm.in, &bar_ds = sm.ds, &bar_p = sm.p, &bar_out = sm.out, &bar_q = sm.q;
+    uint64_t(&bar_m)[3] = sm.m;
+    const DeltaParams &p = cp.p;
+    const uint32_t base = smem_u32(smem_raw);
+    const int chunk = blockIdx.x % cp.n, grp = blockIdx.x / cp.n % p.G, bi = blockIdx.x / cp.n / p.G;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int V = valid_tokens(p, bi), t0 = chunk * kChunk, live_n = V - t0, nsl = slices_of(p);
+    if (live_n <= 0) {
+        for (int x = tid; x < kChunk * (p.N / 8); x += kThreads) {
+            const int tok = t0 + x / (p.N / 8);
+            if (tok < p.L) {
+                const long long at = (((long long)bi * p.L + tok) * p.G + grp) * p.N + 8 * (x % (p.N / 8));
+                *(uint4 *)((bf16 *)p.dq + at) = make_uint4(0, 0, 0, 0);
+                *(uint4 *)((bf16 *)p.dk + at) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        return;
+    }
+    const int items = p.hpg * nsl;
+    if (tid == 0) {
+        mbar_init(&bar_qk, 1);
+        mbar_init(&bar_in, 1);
+        mbar_init(&bar_ds, 1);
+        mbar_init(&bar_p, kCompute / 32);
+        mbar_init(&bar_out, kCompute / 32);
+        mbar_init(&bar_q, kCompute / 64);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_fence_init();
+        sm.err = (base & 1023u) ? 1 : 0;
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, 256);
+    for (int i = tid; i < 8192 / 16; i += kThreads) st_shared_v4(base + kOffZero + 16 * i, 0, 0, 0, 0);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    const uint32_t halves = p.N > 64 ? 2u : 1u;
+
+    if (warp == kCompute / 32) {
+        // ---- copies and products
+        auto head = [&](int it) { return grp * p.hpg + it / nsl; };
+        auto load_in = [&](int it) {
+            if (lane == 0) {
+                const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
+                const char *state = cp.w.states + (cs * (cp.n + 1) + chunk) * kStateTile;
+                mbar_arrive_expect_tx(&bar_in, 16384 + kStateTile + kErrTile + kDvLoTile);
+                bulk_load(base + kOffSZ, state, 16384, &bar_in);
+                bulk_load(base + kOffZ, cp.w.errs + (cs * cp.n + chunk) * kErrTile, kErrTile, &bar_in);
+                tma_tile(base + kOffDV, &maps.d_o, &bar_in, 64 * (it % nsl), head(it), t0, bi);
+                tma_tile(base + kOffDV + 8192, &maps.dv, &bar_in, 64 * (it % nsl), head(it), t0, bi);
+                bulk_load(base + kOffDS, state + 16384, 16384, &bar_in);
+                bulk_load(base + kOffW, cp.w.dv_lo + (cs * cp.n + chunk) * kDvLoTile, kDvLoTile, &bar_in);
+                prefetch_bulk(cp.w.dstates + (cs * cp.n + chunk) * kDStateTile, kDStateTile);
+            }
+        };
+        auto load_ds = [&](int it) {
+            if (lane == 0) {
+                const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
+                mbar_arrive_expect_tx(&bar_ds, kDStateTile);
+                bulk_load(base + kOffDS, cp.w.dstates + (cs * cp.n + chunk) * kDStateTile, kDStateTile, &bar_ds);
+            }
+        };
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_qk, halves * 16384u);
+            for (uint32_t kb = 0; kb < halves; ++kb) {
+                tma_tile(base + kOffQK + kb * 16384u, &maps.q, &bar_qk, 64 * kb, grp, t0, bi);
+                tma_tile(base + kOffQK + kb * 16384u + 8192u, &maps.k, &bar_qk, 64 * kb, grp, t0, bi);
+            }
+        }
+        load_in(0);
+        const uint32_t i_ac = idesc_bf16(128, 192, false, false), i_c = idesc_bf16(128, 64, false, false),
+                       i_b = idesc_bf16(128, 128, false, false), i_d = idesc_bf16(128, 64 * halves, false, true),
+                       i_e = idesc_bf16(128, 64 * halves, true, true);
+        const uint64_t dDV = sdesc(base + kOffDV, 16, 1024), dSZ = sdesc(base + kOffSZ, 16, 1024),
+                       dZ = sdesc(base + kOffZ, 16, 1024), dZlo = sdesc(base + kOffZlo, 16, 1024),
+                       dVlo = sdesc(base + kOffZero, 16, 1024), dDS = sdesc(base + kOffDS, 16, 1024),
+                       dP = sdesc(base + kOffP, 16, 1024), dK = sdesc(base + kOffQK + 8192, 16384, 1024),
+                       // the 64 columns before P's transpose are what lies before it: rows 0 .. 63 take anything
+                       dPt = sdesc(base + kOffP - 16384, 16384, 1024), dPlo = sdesc(base + kOffPlo, 16, 1024),
+                       dPlot = sdesc(base + kOffPlo - 16384, 16384, 1024), dSlo = sdesc(base + kOffDS, 16, 1024), dQKt = sdesc(base + kOffQK, 16384, 1024),
+                       dQK = sdesc(base + kOffQK, 16, 1024), dKk = sdesc(base + kOffQK + 8192, 16, 1024);
+        const int nks = (p.N + 15) / 16;
+        bool ok = true;
+        int done = 0, in_issued = 1, ds_issued = 0;
+        for (int it = 0; it < items; ++it) {
+            const uint32_t ph = it & 1;
+            ok = mbar_wait(&bar_in, ph) && mbar_wait(&bar_qk, 0) && (it == 0 || mbar_wait(&bar_out, (it - 1) & 1));
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int ks = 0; ks < nks; ++ks)
+                    mma_bf16(tm + 192, sdesc_add(dQK, (ks >> 2) * 16384 + (ks & 3) * 32),
+                             sdesc_add(dKk, (ks >> 2) * 16384 + (ks & 3) * 32), i_c, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSlo, ks * 32), i_b, true);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dDV, ks * 32), sdesc_add(dZlo, ks * 32), i_c, true);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dVlo, ks * 32), sdesc_add(dZ, ks * 32), i_c, true);
+                mma_commit(&bar_m[0]);
+            }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph)))) break;
+            load_ds(it);
+            ds_issued = it + 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_p, ph));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dP, ks * 32), sdesc_add(dK, ks * 2048), i_d, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dPlo, ks * 32), sdesc_add(dK, ks * 2048), i_d, true);
+                mma_commit(&bar_m[1]);
+            }
+            ok = mbar_wait(&bar_q, ph) && mbar_wait(&bar_ds, ph);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, sdesc_add(dPt, ks * 2048), sdesc_add(dQKt, ks * 2048), i_e, true);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, sdesc_add(dPlot, ks * 2048), sdesc_add(dQKt, ks * 2048), i_e, true);
+                // W, where dV lo was, below the zeros
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dVlo, ks * 32), sdesc_add(dDS, ks * 32), i_b, true);
+                mma_commit(&bar_m[2]);
+            }
+            __syncwarp();
+            done = it + 1;
+            if (it + 1 < items) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
+                load_in(it + 1);
+                in_issued = it + 2;
+            }
+        }
+        if (!ok) sm.err = 1;
+        mbar_wait(&bar_qk, 0);
+        mbar_wait(&bar_in, (in_issued - 1) & 1);
+        if (ds_issued) mbar_wait(&bar_ds, (ds_issued - 1) & 1);
+        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const bool keys = row >= kChunk;     // rows 64 .. 127: dV, M, dK
+        const int i = row & 63, tok = t0 + i;
+        const bool live = i < live_n;
+        float2 acc[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = make_float2(0.f, 0.f);
+        bool ok = true;
+        if (live_n < kChunk) {  // q and k rows of absent tokens are made zero
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_qk, 0));
+            for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
+                if (((x >> 3) & 63) >= live_n) st_shared_v4(base + kOffQK + x * 16u, 0, 0, 0, 0);
+        }
+        for (int it = 0; it < items && ok; ++it) {
+            const uint32_t ph = it & 1;
+            const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
+            const float *gates = (const float *)(cp.img + (bh * cp.n + chunk) * (long long)kImgBytes);
+            if (tid < kChunk) {
+                sm.gam[tid] = __ldg((const float2 *)(gates + 3 * kChunk) + tid);
+                sm.beta[tid] = __ldg(gates + 2 * kChunk + tid);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph));
+            if (!ok) break;
+            tc_fence_after();
+            // W, in place of what dV lost, from both parts of Z (16 columns of row tid % 64): kept in shared memory
+            const int wr = tid & 63, wc = 2 * (tid >> 6);
+            const float wf = __ldg(gates + 2 * kChunk + wr) * __ldg(gates + kChunk + wr), eg = __ldg(gates + i);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float2 w[4];
+                const uint32_t off = sw128_chunk(wr, wc + c);
+                join8(ld_shared_v4(base + kOffZ + off), ld_shared_v4(base + kOffZlo + off), w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = fmul2(w[e], make_float2(wf, wf));
+                const uint4 o = pack8(w);
+                st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");  // Z lo has been read: the sums may take its place
+            float *rsum = (float *)(smem_raw + kOffZlo), *csum = rsum + 256;  // [half][128 rows], [quarter][64 columns]
+            const float2 gi = sm.gam[i];
+            const float f = keys ? -1.f : p.scale;
+            float rs = 0.f, cs_[32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float a[16], b[16];
+                tmem_ld16x2(tmem_addr(tm, 32 * quarter, 128 + 32 * half + 16 * q), tmem_addr(tm, 32 * quarter, 192 + 32 * half + 16 * q), a, b);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = 32 * half + 16 * q + e;
+                    const float2 gj = sm.gam[j];
+                    const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y)) * sm.beta[j];
+                    const bool in = live && (j < i || (j == i && !keys));
+                    a[e] = in ? f * d * a[e] : 0.f;
+                    cs_[16 * q + e] = in ? a[e] * b[e] : 0.f;
+                    rs += cs_[16 * q + e];
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    store_parts8(base + kOffP, base + kOffPlo, row, 4 * half + 2 * q + c, (const float2 *)a + 4 * c);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_p);
+            // column sums over the warp's rows: halves of the columns change hands until lane l has column l
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < o) {
+                        const float give = up ? cs_[e] : cs_[e + o], keep = up ? cs_[e + o] : cs_[e];
+                        cs_[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+            }
+            rsum[half * 128 + row] = rs;
+            csum[quarter * 64 + 32 * half + lane] = cs_[0];
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (tid < kChunk) {
+                float e = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) e += rsum[(x >> 1) * 128 + (x & 1) * 64 + tid] - csum[x * 64 + tid];
+                cp.w.pe[cs * cp.n * kChunk + t0 + tid] = e;
+            }
+            const float fa = f * eg;
+            auto add = [&]() {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (half < (int)halves) {
+                        float2 a[8], b[8];
+                        const uint32_t at = tmem_addr(tm, 32 * quarter, 64 * half + 16 * q);
+                        tmem_ld16x2(at, at + 128, (float *)a, (float *)b);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 &x = acc[8 * q + e];
+                            x = ffma2(b[e], make_float2(1.f, 1.f), ffma2(a[e], make_float2(fa, fa), x));
+                        }
+                    }
+            };
+            if (!keys) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+                if (!ok) break;
+                tc_fence_after();
+                add();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_q);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
+            if (!ok) break;
+            tc_fence_after();
+            if (keys) add();
+            fence_async_smem();  // the sums, before the copies that come in their place
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_out);
+        }
+        if (!ok) sm.err = 1;
+        if (tok < p.L) {
+            bf16 *dst = (bf16 *)(keys ? p.dk : p.dq) + (((long long)bi * p.L + tok) * p.G + grp) * p.N + 64 * half;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (64 * half + 8 * c < p.N) *(uint4 *)(dst + 8 * c) = live ? pack8(acc + 4 * c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && sm.err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
+    if (warp == 0) tmem_dealloc(tm, 256);
+}
+
+// dg and dbeta from the sums (delta_chunk.cuh): a warp per (b, h, chunk), lane l tokens 2 l and 2 l + 1.
+__global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
+    const DeltaParams &p = cp.p;
+    const long long w = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    if (w >= (long long)p.b * p.H * cp.n) return;
+    const int lane = threadIdx.x & 31, chunk = (int)(w % cp.n), nsl = slices_of(p);
+    const long long bh = w / cp.n;
+    const int V = valid_tokens(p, (int)(bh / p.H)), t = chunk * kChunk + 2 * lane;
+    float2 from = make_float2(0.f, 0.f), to = from, db = from;  // what tokens read, what they write
+    float ss = 0.f;
+    if (chunk * kChunk < V) {
+        for (int x = 0; x < 2 * nsl; ++x) {
+            const long long at = (bh * nsl * 2 + x) * cp.n * kChunk + t;
+            const float2 fq = *(const float2 *)(cp.w.fq + at), fk = *(const float2 *)(cp.w.fk + at);
+            const float2 ww = *(const float2 *)(cp.w.ww + at), zx = *(const float2 *)(cp.w.zx + at);
+            from.x += fq.x + fk.x;
+            from.y += fq.y + fk.y;
+            to.x += ww.x;
+            to.y += ww.y;
+            db.x += zx.x;
+            db.y += zx.y;
+        }
+        for (int x = 0; x < nsl; ++x) {
+            const float2 pe = *(const float2 *)(cp.w.pe + (bh * nsl + x) * cp.n * kChunk + t);
+            from.x += pe.x;
+            from.y += pe.y;
+            if (lane < 8) ss += cp.w.ss[((bh * nsl + x) * cp.n + chunk) * 8 + lane];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    float suffix = from.x + from.y, prefix = to.x + to.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float dn = __shfl_down_sync(0xffffffffu, suffix, o), up = __shfl_up_sync(0xffffffffu, prefix, o);
+        if (lane + o < 32) suffix += dn;
+        if (lane >= o) prefix += up;
+    }
+    prefix -= to.x + to.y;  // before token 2 l
+    const long long at = bh * p.L + t;
+    if (t < p.L) {
+        p.dg[at] = t < V ? ss + prefix + suffix : 0.f;
+        p.dbeta[at] = t < V ? db.x : 0.f;
+    }
+    if (t + 1 < p.L) {
+        p.dg[at + 1] = t + 1 < V ? ss + (prefix + to.x) + (suffix - from.x) : 0.f;
+        p.dbeta[at + 1] = t + 1 < V ? db.y : 0.f;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s) {
+    const DeltaParams &p = c.p;
+    GradMaps maps;
+    cudaError_t e;
+    if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.dv, p.dv, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    const int bytes = (int)kBytes;
+    if ((e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    delta_grad_kernel<<<(unsigned)c.n * p.G * p.b, kThreads, bytes, s>>>(c, maps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    delta_gate_grads<<<(unsigned)(((long long)p.b * p.H * c.n + 7) / 8), 256, 0, s>>>(c);
+    return cudaGetLastError();
+}
+
+}  // namespace delta
+}  // namespace ssd

@@ -25,6 +25,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// the same into the L2 cache only, ahead of their use
+__device__ __forceinline__ void prefetch_tile(const void *map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(c0), "r"(c1),
+                 "r"(c2), "r"(c3)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ---- descriptor of an operand kept without swizzle: 8x8 matrices of 128 contiguous bytes, the two
 // column octets of a K-step next to each other, row octets 256 bytes apart; K-steps 4096 (128 rows)
 __device__ __forceinline__ uint64_t sdesc_tri(uint32_t base) {
@@ -75,6 +85,42 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     hi = tc::pack_bf2(x, y);
     const float2 r = tc::ffma2(tc::bf2_to_f2(hi), make_float2(-1.f, -1.f), make_float2(x, y));
     lo = tc::pack_bf2(r.x, r.y);
+}
+
+// 8 values as one 16-byte piece of row `row` of a hi and of a lo tile (SW128)
+__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float2 *x) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
+    tc::st_shared_v4(hi_tile + tc::sw128_chunk(row, piece), h[0], h[1], h[2], h[3]);
+    tc::st_shared_v4(lo_tile + tc::sw128_chunk(row, piece), l[0], l[1], l[2], l[3]);
+}
+// the same to global memory, the lo tile `lo_off` bytes behind the hi one
+__device__ __forceinline__ void store_parts8(char *tile, int lo_off, int row, int piece, const float2 *x) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
+    char *dst = tile + tc::sw128_chunk(row, piece);
+    *(uint4 *)dst = make_uint4(h[0], h[1], h[2], h[3]);
+    *(uint4 *)(dst + lo_off) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// the sum of hi and lo parts
+__device__ __forceinline__ void join8(const uint4 hi, const uint4 lo, float2 *x) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = tc::ffma2(tc::bf2_to_f2(l[e]), make_float2(1.f, 1.f), tc::bf2_to_f2(h[e]));
+}
+// sum of products with 8 bf16 values
+__device__ __forceinline__ float dot8(const uint4 w, const float2 *x, float acc) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    float2 a = make_float2(acc, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a = tc::ffma2(tc::bf2_to_f2(v[e]), x[e], a);
+    return a.x + a.y;
+}
+__device__ __forceinline__ uint4 pack8(const float2 *x) {
+    return make_uint4(tc::pack_bf2(x[0].x, x[0].y), tc::pack_bf2(x[1].x, x[1].y), tc::pack_bf2(x[2].x, x[2].y),
+                      tc::pack_bf2(x[3].x, x[3].y));
 }
 
 }  // namespace delta

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
             *(float2 *)(gates + i0) = make_float2(expf((float)c0), expf((float)c1));
             *(float2 *)(gates + kChunk + i0) = make_float2(expf((float)(total - c0)), expf((float)(total - c1)));
             *(float2 *)(gates + 2 * kChunk + i0) = make_float2(b0, b1);
+            *(float4 *)(gates + 3 * kChunk + 2 * i0) = make_float4(h0, (float)(l0 - (double)h0), h1, (float)(l1 - (double)h1));
         }
         if (h == grp * p.hpg + slice * kHeadsPer) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_mma, 0));
@@ -144,6 +145,16 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         // z[m][row] = beta_m y_m of this thread's row, over the tiles (which the products have read)
         float *z = (float *)(smem_raw + (kq - smem_u32(smem_raw))) + tid;
         char *tri = img + kImgTri + (keys ? 0 : kTri);
+        // the reverse pass's full squares (Tt hi, A hi, Tt lo, A lo)
+        char *rev = cp.w.rev ? cp.w.rev + (bh * cp.n + chunk) * (long long)kRevBytes : nullptr;
+        auto store_rev = [&](char *sq, int jb, const float2 *y) {
+            store_parts8(sq, 16384, i, 2 * jb, y);
+            store_parts8(sq, 16384, i, 2 * jb + 1, y + 4);
+        };
+        if (rev && last == 1) {
+            const float2 zero[8] = {};
+            for (int jb = 2; jb < 4; ++jb) store_rev(rev + (keys ? 0 : 8192), jb, zero);
+        }
         for (int jb = last; jb >= 0; --jb) {
             float2 y[8];
             if (keys) {
@@ -155,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 }
             } else {
                 decayed(jb, p.scale, (float(&)[16])y);
+                if (rev) store_rev(rev + 8192, jb, y);  // A itself
             }
             const float *e0 = s_e + 16 * jb;
 #pragma unroll 4
@@ -184,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                     if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
                 }
             }
+            if (rev && keys) store_rev(rev, jb, y);
             // hi and lo parts: 16-byte pieces, neighbouring rows on neighbouring addresses
             if (jb <= (i >> 4))
 #pragma unroll

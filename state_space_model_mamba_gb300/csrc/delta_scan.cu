@@ -42,20 +42,11 @@ constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
 constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
 constexpr uint32_t kKQBytes = 32768;
 
-// 8 values as one 16-byte piece of row `row` of a hi and of a lo tile (SW128)
-__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float2 *x) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
-    st_shared_v4(hi_tile + sw128_chunk(row, piece), h[0], h[1], h[2], h[3]);
-    st_shared_v4(lo_tile + sw128_chunk(row, piece), l[0], l[1], l[2], l[3]);
-}
-
 struct ScanMaps {
-    CUtensorMap k, q, v;
+    CUtensorMap k, q, v, d_o;
 };
 
-template <int NB>
+template <int NB, bool BWD>
 __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     delta_scan_fwd(const ChunkParams cp, const __grid_constant__ ScanMaps maps) {
     extern __shared__ uint8_t smem_raw[];
@@ -66,7 +57,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     __shared__ int s_err;
     const DeltaParams &p = cp.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int nsl = (p.P + 63) / 64, slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
+    const int nsl = slices_of(p), slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
     const char *img0 = cp.img + (long long)bh * cp.n * (long long)kImgBytes;
@@ -180,6 +171,16 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         bool ok = true;
         for (int c = 0; c + 1 < nv; ++c) {
             const uint32_t ph = c & 1;
+            if (lane == 0) {  // what the next chunk reads, into L2
+                prefetch_bulk(img0 + (long long)(c + 1) * kImgBytes, kImgBytes);
+                if (c + NB < nv)
+                    for (uint32_t kb = 0; kb < halves; ++kb) {
+                        prefetch_tile(&maps.k, 64 * kb, grp, (c + NB) * kChunk, bi);
+                        prefetch_tile(&maps.q, 64 * kb, grp, (c + NB) * kChunk, bi);
+                    }
+                prefetch_tile(&maps.v, 64 * slice, h, (c + 1) * kChunk, bi);
+                if (BWD) prefetch_tile(&maps.d_o, 64 * slice, h, (c + 1) * kChunk, bi);
+            }
             // V and, by the first product, Q have been read
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
             if (NB == 1) {
@@ -217,10 +218,17 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 ((float *)S)[j] = (src && row < p.N && slice * 64 + 32 * half + j < p.P) ? src[(long long)j * p.N] : 0.f;
         }
         bool ok = true;
+        // the backward's copy of S before chunk c
+        auto keep_state = [&](int c) {
+            char *tile = cp.w.states + ((long long)blockIdx.x * (cp.n + 1) + c) * kStateTile;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) store_parts8(tile, 16384, row, 4 * half + j, S + 4 * j);
+        };
         // S as an operand; before the last chunk, K rows of absent tokens are made zero
         auto publish_s = [&](int c) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 4 * j);
+            if (BWD) keep_state(c);
             const int live = V - c * kChunk;
             if (live < kChunk) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[c % NB], (c / NB) & 1));
@@ -240,6 +248,15 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
             const float ec = __ldg(gates + kChunk - 1);
             const bool live = c * kChunk + i < V, partial = V - c * kChunk < kChunk;
+            const int tok = c * kChunk + i, col = slice * 64 + 32 * half;
+            const long long at = (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
+            uint4 dov[BWD ? 4 : 1];
+            float fq = 0.f;
+            if (BWD && !keys) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dov[j] = live && col + 8 * j < p.P ? __ldg((const uint4 *)((const bf16 *)p.d_o + at + 8 * j)) : make_uint4(0, 0, 0, 0);
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph));
             if (!ok) break;
             tc_fence_after();
@@ -250,6 +267,16 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
                 if (keys) {
+                    if (BWD) {
+                        char *tile = cp.w.reads + ((long long)blockIdx.x * cp.n + c) * kErrTile;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float2 rd[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) rd[e] = live ? fmul2(a[4 * u + e], make_float2(eg, eg)) : make_float2(0.f, 0.f);
+                            store_parts8(tile, 8192, i, 4 * half + 2 * j + u, rd);
+                        }
+                    }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + 2 * j + u));
@@ -268,6 +295,10 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                     const float f = p.scale * eg;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
+                    if (BWD) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) fq = dot8(dov[2 * j + u], a + 4 * u, fq);
+                    }
                 }
                 tmem_st16(my + 16 * j, (const float *)a);
             }
@@ -284,29 +315,33 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 float2 a[16];
                 tmem_ld32(my, (float *)a);
                 if (keys) {
-                    const float f = be * et;
+                    const float f = live ? be * et : 0.f;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        a[e] = fmul2(a[e], make_float2(f, f));
-                        if (partial && !live) a[e] = make_float2(0.f, 0.f);
+                    for (int j = 0; j < 4; ++j) {
+                        float2 w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (partial && !live) a[4 * j + e] = make_float2(0.f, 0.f);
+                            w[e] = fmul2(a[4 * j + e], make_float2(f, f));
+                        }
+                        store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, w);
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, a + 4 * j);
                     fence_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_w);
-                if (!keys) {
-                    const int tok = c * kChunk + i;
-                    bf16 *dst = (bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + 32 * half;
+                if (BWD && keys) {
+                    char *tile = cp.w.errs + ((long long)blockIdx.x * cp.n + c) * kErrTile;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) store_parts8(tile, 8192, i, 4 * half + j, a + 4 * j);
+                }
+                if (BWD && !keys) cp.w.fq[((long long)blockIdx.x * 2 + half) * cp.n * kChunk + tok] = live ? fq : 0.f;
+                if (!BWD && !keys) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (tok < p.L && slice * 64 + 32 * half + 8 * j < p.P)
-                            *(uint4 *)(dst + 8 * j) =
-                                live ? make_uint4(pack_bf2(a[4 * j].x, a[4 * j].y), pack_bf2(a[4 * j + 1].x, a[4 * j + 1].y),
-                                                  pack_bf2(a[4 * j + 2].x, a[4 * j + 2].y), pack_bf2(a[4 * j + 3].x, a[4 * j + 3].y))
-                                     : make_uint4(0, 0, 0, 0);
+                        if (tok < p.L && col + 8 * j < p.P)
+                            *(uint4 *)((bf16 *)p.o + at + 8 * j) = live ? pack8(a + 4 * j) : make_uint4(0, 0, 0, 0);
                 }
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
@@ -323,9 +358,12 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             if (c + 1 < nv) publish_s(c + 1);
         }
         if (!ok) s_err = 1;
+        if (BWD) {
+            if (ok) keep_state(nv);
+        }
         // absent tokens past the last chunk
-        for (int x = nv * kChunk * 8 + tid; x < p.L * 8; x += kCompute) {
-            const int tok = x / 8, cc = x % 8;
+        for (long long x = (long long)nv * kChunk * 8 + tid; !BWD && x < (long long)p.L * 8; x += kCompute) {
+            const int tok = (int)(x / 8), cc = (int)(x % 8);
             if (slice * 64 + cc * 8 < p.P)
                 *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
         }
@@ -343,6 +381,373 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     if (warp == 0) tmem_dealloc(tm, kAccCols);
 }
 
+// ------------------------------------------------------------------ reverse
+// The adjoint of the scan, chunks in reverse, with dS after the chunk in registers as S
+// is in the forward.  With D = s e^gamma dO,
+//   0.  A^T dO                          (does not wait for the chain)
+//   1.  K dS                            -> dU = A^T dO + e^(gamma_C - gamma) K dS
+//   2.  Tt^T (beta dU)                  -> X = dU + Tt^T (beta dU),  dV = beta X
+//   3.  K^T (-e^gamma dV) + Q^T D       -> dS = e^gamma_C dS + ...
+// and, with what the forward kept, the sums that the gates' gradients are made of
+// (delta_chunk.cuh).
+constexpr uint32_t kOffRev = 32768;        // Tt hi, A hi, Tt lo, A lo: [64][64] SW128 each
+struct RevMaps {
+    CUtensorMap k, q, d_o;
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
+    delta_scan_rev(const ChunkParams cp, const __grid_constant__ RevMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar_kq[2], bar_rev, bar_do;              // copies have landed
+    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (8 warps each)
+    __shared__ uint64_t bar_m[3];                                // products are done
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_err;
+    const DeltaParams &p = cp.p;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int nsl = slices_of(p), slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
+    if (tid == 0) {
+        mbar_init(&bar_kq[0], 1);
+        mbar_init(&bar_kq[1], 1);
+        mbar_init(&bar_rev, 1);
+        mbar_init(&bar_do, 1);
+        mbar_init(&bar_s, kCompute / 32);
+        mbar_init(&bar_x, kCompute / 32);
+        mbar_init(&bar_w, kCompute / 32);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_fence_init();
+        s_err = 0;
+    }
+    if (warp == 0) tmem_alloc(&s_tmem, 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    if (warp == kCompute / 32) {
+        // ---- products; step r is chunk nv - 1 - r
+        const uint32_t i0 = idesc_bf16(128, 64, true, true), i1 = idesc_bf16(128, 128, false, true),
+                       i3 = idesc_bf16(128, 128, true, true);
+        const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
+                       dW = sdesc(base + kOffW, 8192, 1024), dR = sdesc(base + kOffRev, 8192, 1024),
+                       dO = sdesc(base + kOffV, 8192, 1024);
+        bool ok = true;
+        int done = 0;
+        for (int r = 0; r < nv; ++r) {
+            const uint32_t ph = r & 1, kq = base + kOffKQ + (r % NB) * kKQBytes;
+            const uint64_t dK = sdesc(kq, 16, 1024), dKt = sdesc(kq, 16384, 1024), dQt = sdesc(kq + 8192, 16384, 1024);
+            ok = mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_rev, ph) && mbar_wait(&bar_do, ph) &&
+                 mbar_wait(&bar_s, ph);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    if (ks < nks) mma_bf16(tm, sdesc_add(dK, (ks >> 2) * 16384 + (ks & 3) * 32), sdesc_add(dS, ks * 2048), i1, ks > 0);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tm + 128, sdesc_add(dR, 8192 + part * 16384 + ks * 2048), sdesc_add(dO, ks * 2048), i0,
+                                 part > 0 || ks > 0);
+                mma_commit(&bar_m[0]);
+            }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tm, sdesc_add(dR, (pass == 2 ? 16384 : 0) + ks * 2048),
+                                 sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i0, true);
+                mma_commit(&bar_m[1]);
+            }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph)))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dQt, ks * 2048), sdesc_add(dX, ks * 2048), i3, true);
+                mma_commit(&bar_m[2]);
+            }
+            __syncwarp();
+            done = r + 1;
+        }
+        if (!ok) s_err = 1;
+        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);  // every product has to complete before the block may end
+    } else if (warp == kCompute / 32 + 1) {
+        // ---- copies
+        const int grp = h / p.hpg;
+        const uint32_t halves = p.N > 64 ? 2u : 1u;
+        int kq_issued = 0, do_issued = 0, rev_issued = 0;
+        auto load_kq = [&](int r) {
+            if (lane == 0) {
+                uint64_t *bar = &bar_kq[r % NB];
+                const uint32_t dst = base + kOffKQ + (r % NB) * kKQBytes;
+                const int t0 = (nv - 1 - r) * kChunk;
+                mbar_arrive_expect_tx(bar, halves * 16384u);
+                for (uint32_t kb = 0; kb < halves; ++kb) {
+                    tma_tile(dst + kb * 16384u, &maps.k, bar, 64 * kb, grp, t0, bi);
+                    tma_tile(dst + kb * 16384u + 8192u, &maps.q, bar, 64 * kb, grp, t0, bi);
+                }
+            }
+            kq_issued = r + 1;
+        };
+        auto load_rev = [&](int r) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar_rev, kRevBytes);
+                bulk_load(base + kOffRev, cp.w.rev + ((long long)bh * cp.n + nv - 1 - r) * kRevBytes, kRevBytes, &bar_rev);
+            }
+            rev_issued = r + 1;
+        };
+        auto load_do = [&](int r) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar_do, 8192);
+                tma_tile(base + kOffV, &maps.d_o, &bar_do, 64 * slice, h, (nv - 1 - r) * kChunk, bi);
+            }
+            do_issued = r + 1;
+        };
+        for (int r = 0; r < NB && r < nv; ++r) load_kq(r);
+        if (nv > 0) {
+            load_rev(0);
+            load_do(0);
+        }
+        bool ok = true;
+        for (int r = 0; r + 1 < nv; ++r) {
+            const uint32_t ph = r & 1;
+            if (lane == 0) {  // what the next step reads, into L2
+                const int c = nv - 2 - r;
+                const long long at = (long long)blockIdx.x * cp.n + c;
+                prefetch_bulk(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes, kGates);
+                prefetch_bulk(cp.w.rev + ((long long)bh * cp.n + c) * kRevBytes, kRevBytes);
+                prefetch_bulk(cp.w.states + (at + blockIdx.x) * kStateTile, kStateTile);
+                prefetch_bulk(cp.w.errs + at * kErrTile, kErrTile);
+                prefetch_bulk(cp.w.reads + at * kErrTile, kErrTile);
+                prefetch_tile(&maps.d_o, 64 * slice, h, c * kChunk, bi);
+                if (r + NB < nv)
+                    for (uint32_t kb = 0; kb < halves; ++kb) {
+                        prefetch_tile(&maps.k, 64 * kb, grp, (nv - 1 - r - NB) * kChunk, bi);
+                        prefetch_tile(&maps.q, 64 * kb, grp, (nv - 1 - r - NB) * kChunk, bi);
+                    }
+            }
+            // dO, and by the products the matrices, have been read
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph)))) break;
+            load_rev(r + 1);
+            load_do(r + 1);
+            if (r + NB < nv) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
+                load_kq(r + NB);
+            }
+        }
+        if (!ok) s_err = 1;
+        // every copy has to land before the block may end
+        for (int r = max(0, kq_issued - NB); r < kq_issued; ++r) mbar_wait(&bar_kq[r % NB], (r / NB) & 1);
+        if (rev_issued) mbar_wait(&bar_rev, (rev_issued - 1) & 1);
+        if (do_issued) mbar_wait(&bar_do, (do_issued - 1) & 1);
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const bool keys = quarter < 2;       // these threads form dU and X; the others D
+        const int i = row & 63;              // the row's token
+        const uint32_t my = tmem_addr(tm, 32 * quarter, 32 * half);
+        const int col = slice * 64 + 32 * half;
+        const float2 one = make_float2(1.f, 1.f);
+        float2 S[16];
+        {
+            const float *src = p.d_final ? p.d_final + ((long long)bh * p.P + col) * p.N + row : nullptr;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                ((float *)S)[j] = (src && row < p.N && col + j < p.P) ? src[(long long)j * p.N] : 0.f;
+        }
+        bool ok = true;
+        // dS after chunk nv - 1 - r as an operand, kept for the gradients of q and k
+        auto publish_s = [&](int r) {
+            char *tile = cp.w.dstates + ((long long)blockIdx.x * cp.n + nv - 1 - r) * kDStateTile;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 4 * j);
+                *(uint4 *)(tile + sw128_chunk(row, 4 * half + j)) = pack8(S + 4 * j);
+            }
+            const int live = V - (nv - 1 - r) * kChunk;
+            if (live < kChunk) {  // the last chunk: K, Q and dO rows of absent tokens are made zero
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_do, r & 1));
+                const uint32_t kq = base + kOffKQ + (r % NB) * kKQBytes;
+                for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
+                    if (((x >> 3) & 63) >= live) st_shared_v4(kq + x * 16u, 0, 0, 0, 0);
+                for (int x = tid; x < kChunk * 8; x += kCompute)
+                    if ((x >> 3) >= live) st_shared_v4(base + kOffV + x * 16u, 0, 0, 0, 0);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_s);
+        };
+        if (nv > 0) publish_s(0);
+        for (int r = 0; r < nv && ok; ++r) {
+            const int c = nv - 1 - r;
+            const uint32_t ph = r & 1;
+            const float *gates = (const float *)(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes);
+            const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
+            const float ec = __ldg(gates + kChunk - 1);
+            const int tok = c * kChunk + i;
+            // e^gamma_C <S, dS>, while the products run
+            {
+                const char *tile = cp.w.states + ((long long)blockIdx.x * (cp.n + 1) + c) * kStateTile;
+                float sum = 0.f;
+                if (row < p.N) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const char *src = tile + sw128_chunk(row, 4 * half + j);
+                        sum = dot8(__ldg((const uint4 *)src), S + 4 * j, sum);
+                        sum = dot8(__ldg((const uint4 *)(src + 16384)), S + 4 * j, sum);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) cp.w.ss[((long long)blockIdx.x * cp.n + c) * 8 + warp] = ec * sum;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph));
+            if (!ok) break;
+            tc_fence_after();
+            const char *err = cp.w.errs + ((long long)blockIdx.x * cp.n + c) * kErrTile;
+            float2 ww = make_float2(0.f, 0.f);
+            if (keys) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float2 a[8], b[8], u[8];
+                    tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
+                    tmem_ld16(my + 128 + 16 * j, (float *)u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = fmul2(ffma2(b[e], one, a[e]), make_float2(et, et));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float2 z[4];
+                        const char *src = err + sw128_chunk(i, 4 * half + 2 * j + x);
+                        join8(__ldg((const uint4 *)src), __ldg((const uint4 *)(src + 8192)), z);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ww = ffma2(z[e], a[4 * x + e], ww);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = ffma2(u[e], one, a[e]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float2 xb[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) xb[e] = fmul2(a[4 * x + e], make_float2(be, be));
+                        store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + 2 * j + x, xb);
+                    }
+                    tmem_st16(my + 16 * j, (const float *)a);
+                }
+                tmem_wait_st();
+                fence_async_smem();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_x);
+
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+            if (!ok) break;
+            tc_fence_after();
+            if (keys) {
+                float2 a[16];
+                tmem_ld32(my, (float *)a);
+                const float f = -eg * be;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * j + e], make_float2(f, f));
+                    store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, w);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_w);
+                const char *read = cp.w.reads + ((long long)blockIdx.x * cp.n + c) * kErrTile;
+                char *lo_tile = cp.w.dv_lo + ((long long)blockIdx.x * cp.n + c) * kDvLoTile;
+                const long long at = (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
+                float2 zx = make_float2(0.f, 0.f), fk = zx;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t off = sw128_chunk(i, 4 * half + j);
+                    float2 z[4];
+                    join8(__ldg((const uint4 *)(err + off)), __ldg((const uint4 *)(err + off + 8192)), z);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        zx = ffma2(z[e], a[4 * j + e], zx);
+                        a[4 * j + e] = fmul2(a[4 * j + e], make_float2(be, be));
+                    }
+                    join8(__ldg((const uint4 *)(read + off)), __ldg((const uint4 *)(read + off + 8192)), z);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        fk = ffma2(z[e], a[4 * j + e], fk);
+                        split2(a[4 * j + e].x, a[4 * j + e].y, hi[e], lo[e]);
+                    }
+                    *(uint4 *)(lo_tile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (tok < p.L && col + 8 * j < p.P)
+                        *(uint4 *)((bf16 *)p.dv + at + 8 * j) = tok < V ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0, 0, 0, 0);
+                }
+                const long long sat = ((long long)blockIdx.x * 2 + half) * cp.n * kChunk + tok;
+                cp.w.zx[sat] = zx.x + zx.y;
+                cp.w.fk[sat] = -(fk.x + fk.y);
+                cp.w.ww[sat] = be * (ww.x + ww.y);
+            } else {
+                // D = scale e^gamma dO in place of beta dU
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_do, ph));
+                const float f = p.scale * eg;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + j));
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    float2 d[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = fmul2(bf2_to_f2(v[e]), make_float2(f, f));
+                    store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + j, d);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_w);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float2 a[8], b[8];
+                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    S[8 * j + e] = ffma2(S[8 * j + e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
+            }
+            if (r + 1 < nv) publish_s(r + 1);
+        }
+        if (!ok) s_err = 1;
+        // absent tokens past the last chunk
+        for (long long x = (long long)nv * kChunk * 8 + tid; x < (long long)p.L * 8; x += kCompute) {
+            const int t = (int)(x / 8), cc = (int)(x % 8);
+            if (slice * 64 + cc * 8 < p.P)
+                *(uint4 *)((bf16 *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
+        }
+        if (ok && p.d_init && row < p.N) {
+            float *dst = p.d_init + ((long long)bh * p.P + col) * p.N + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < p.P) dst[(long long)j * p.N] = ((const float *)S)[j];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
+    if (warp == 0) tmem_dealloc(tm, 256);
+}
+
 }  // namespace
 
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
@@ -352,9 +757,27 @@ cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    if (c.w.states && (e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * ((p.P + 63) / 64));
     const bool one_per_sm = grid <= 152;
-    auto kernel = one_per_sm ? delta_scan_fwd<2> : delta_scan_fwd<1>;
+    auto kernel = c.w.states ? (one_per_sm ? delta_scan_fwd<2, true> : delta_scan_fwd<1, true>)
+                             : (one_per_sm ? delta_scan_fwd<2, false> : delta_scan_fwd<1, false>);
+    const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    kernel<<<grid, kScanThreads, bytes, s>>>(c, maps);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s) {
+    const DeltaParams &p = c.p;
+    RevMaps maps;
+    cudaError_t e;
+    if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    const unsigned grid = (unsigned)(p.b * p.H * slices_of(p));
+    const bool one_per_sm = grid <= 152;
+    auto kernel = one_per_sm ? delta_scan_rev<2> : delta_scan_rev<1>;
     const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     kernel<<<grid, kScanThreads, bytes, s>>>(c, maps);
