@@ -97,13 +97,13 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
     memset(&w, 0, sizeof(w));
     if (backward) {
         w.rev = take(chains * n * kRevBytes);
-        w.states = take(cs * (n + 1) * kStateTile);
+        w.states = take(cs * n * kStateTile);
         w.dstates = take(cs * n * kDStateTile);
         w.errs = take(cs * n * kErrTile);
-        w.reads = take(cs * n * kErrTile);
         w.dv_lo = take(cs * n * kDvLoTile);
-        w.ss = (float *)take(cs * n * 8 * 4);
-        for (float **x : {&w.ww, &w.fq, &w.fk, &w.zx}) *x = (float *)take(cs * 2 * n * kChunk * 4);
+        w.ss = (float *)take(cs * n * 16 * 4);
+        for (float **x : {&w.ww, &w.zx}) *x = (float *)take(cs * 4 * n * kChunk * 4);
+        for (float **x : {&w.fq, &w.fk}) *x = (float *)take(cs * 2 * n * kChunk * 4);
         w.pe = (float *)take(cs * n * kChunk * 4);
     }
     if (c) {

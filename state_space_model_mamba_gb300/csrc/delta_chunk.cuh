@@ -46,22 +46,22 @@ static_assert(tri_run(1) == 2048 && tri_run(2) == 3584 && tri_run(3) + tri_run_b
 // What the backward's kernels keep, per (b, h) chain and slice of 64 columns of P (chain-slice
 // cs = bh * nsl + slice).  Tiles are in the 128-byte swizzle, ready as operands.
 //   rev    [b, H, n]        Tt hi, A hi, Tt lo, A lo, each [64 rows][64 columns] (32 KB)
-//   states [cs, n + 1]      S before every chunk and after the last: hi, lo parts [128 n][64] (32 KB)
+//   states [cs, n]          S before every chunk: hi, lo parts [128 n][64] (32 KB)
 //   dstates [cs, n]         dS after every chunk: [128 n][64] (16 KB)
-//   errs, reads [cs, n]     Z and e^gamma o (K S): hi, lo parts [64 tokens][64] (16 KB each)
+//   errs   [cs, n]          Z: hi, lo parts [64 tokens][64] (16 KB)
 //   dv_lo  [cs, n]          what dV lost to its rounding: [64 tokens][64] (8 KB)
 // dg is the sum of everything that crosses its token inside the chunk, so that no term carries
 // less decay than the result (products of whole rows, do.o - dv.v and <S, dS>, would be the same sum
 // but cancel where a head forgets fast):
 //     dg_t = ss + sum_{j < t} ww_j + sum_{i >= t} (fq_i + fk_i + pe_i)
-//     ss = e^gamma_C <S, dS>            S before, dS after the chunk    [cs, n, 8], a share of each warp
-//     ww = beta Z.(e^(gamma_C - gamma) K dS)                            the next four [cs, 2, n * 64]:
-//     fq = dO.(scale e^gamma Q S),  fk = -dV.(e^gamma K S),  zx = Z.X   sums of rows of 32 columns
-//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n * 64]   (delta_grad.cu)
+//     ss = e^gamma_C <S, dS>            S before, dS after the chunk    [cs, n, 16], a share of each warp
+//     ww = beta Z.(e^(gamma_C - gamma) K dS),  zx = Z.X                 [cs, 4, n * 64], sums over 16 columns
+//     fq = q.(scale e^gamma dO S^T),  fk = -k.(e^gamma dV S^T)          [cs, 2, n * 64], over 64 of the keys' columns
+//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n * 64]
 // and dbeta = zx.
 struct ChunkBackward {
-    char *rev, *states, *dstates, *errs, *reads, *dv_lo;
-    float *ss, *ww, *fq, *fk, *zx, *pe;
+    char *rev, *states, *dstates, *errs, *dv_lo;
+    float *ss, *ww, *zx, *fq, *fk, *pe;
 };
 
 struct ChunkParams {

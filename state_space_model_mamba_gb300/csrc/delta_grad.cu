@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         auto load_in = [&](int it) {
             if (lane == 0) {
                 const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
-                const char *state = cp.w.states + (cs * (cp.n + 1) + chunk) * kStateTile;
+                const char *state = cp.w.states + (cs * cp.n + chunk) * kStateTile;
                 mbar_arrive_expect_tx(&bar_in, 16384 + kStateTile + kErrTile + kDvLoTile);
                 bulk_load(base + kOffSZ, state, 16384, &bar_in);
                 bulk_load(base + kOffZ, cp.w.errs + (cs * cp.n + chunk) * kErrTile, kErrTile, &bar_in);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                        i_b = idesc_bf16(128, 128, false, false), i_d = idesc_bf16(128, 64 * halves, false, true),
                        i_e = idesc_bf16(128, 64 * halves, true, true);
         const uint64_t dDV = sdesc(base + kOffDV, 16, 1024), dSZ = sdesc(base + kOffSZ, 16, 1024),
-                       dZ = sdesc(base + kOffZ, 16, 1024), dZlo = sdesc(base + kOffZlo, 16, 1024),
+                       dZlo = sdesc(base + kOffZlo, 16, 1024),
                        dVlo = sdesc(base + kOffZero, 16, 1024), dDS = sdesc(base + kOffDS, 16, 1024),
                        dP = sdesc(base + kOffP, 16, 1024), dK = sdesc(base + kOffQK + 8192, 16384, 1024),
                        // the 64 columns before P's transpose are what lies before it: rows 0 .. 63 take anything
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dDV, ks * 32), sdesc_add(dZlo, ks * 32), i_c, true);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dVlo, ks * 32), sdesc_add(dZ, ks * 32), i_c, true);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dVlo, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, true);
                 mma_commit(&bar_m[0]);
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph)))) break;
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 cp.w.pe[cs * cp.n * kChunk + t0 + tid] = e;
             }
             const float fa = f * eg;
+            float read = 0.f;
             auto add = [&]() {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -291,7 +292,12 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                             float2 &x = acc[8 * q + e];
                             x = ffma2(b[e], make_float2(1.f, 1.f), ffma2(a[e], make_float2(fa, fa), x));
                         }
+                        // with the row's own q or k: what it reads of S
+                        const uint32_t own = base + kOffQK + half * 16384;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) read = dot8(ld_shared_v4(own + sw128_chunk(row, 2 * q + u)), a + 4 * u, read);
                     }
+                (keys ? cp.w.fk : cp.w.fq)[(cs * 2 + half) * cp.n * kChunk + tok] = live ? fa * read : 0.f;
             };
             if (!keys) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
@@ -337,22 +343,25 @@ __global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
     float2 from = make_float2(0.f, 0.f), to = from, db = from;  // what tokens read, what they write
     float ss = 0.f;
     if (chunk * kChunk < V) {
-        for (int x = 0; x < 2 * nsl; ++x) {
-            const long long at = (bh * nsl * 2 + x) * cp.n * kChunk + t;
-            const float2 fq = *(const float2 *)(cp.w.fq + at), fk = *(const float2 *)(cp.w.fk + at);
+        for (int x = 0; x < 4 * nsl; ++x) {
+            const long long at = (bh * nsl * 4 + x) * cp.n * kChunk + t;
             const float2 ww = *(const float2 *)(cp.w.ww + at), zx = *(const float2 *)(cp.w.zx + at);
-            from.x += fq.x + fk.x;
-            from.y += fq.y + fk.y;
             to.x += ww.x;
             to.y += ww.y;
             db.x += zx.x;
             db.y += zx.y;
         }
+        for (int x = 0; x < 2 * nsl; ++x) {
+            const long long at = (bh * nsl * 2 + x) * cp.n * kChunk + t;
+            const float2 fq = *(const float2 *)(cp.w.fq + at), fk = *(const float2 *)(cp.w.fk + at);
+            from.x += fq.x + fk.x;
+            from.y += fq.y + fk.y;
+        }
         for (int x = 0; x < nsl; ++x) {
             const float2 pe = *(const float2 *)(cp.w.pe + (bh * nsl + x) * cp.n * kChunk + t);
             from.x += pe.x;
             from.y += pe.y;
-            if (lane < 8) ss += cp.w.ss[((bh * nsl + x) * cp.n + chunk) * 8 + lane];
+            if (lane < 16) ss += cp.w.ss[((bh * nsl + x) * cp.n + chunk) * 16 + lane];
         }
     }
 #pragma unroll

@@ -10,14 +10,16 @@
 // instruction, and the output's rows ride along with the chain's.
 //
 // Precision: q, k, v are exact in bf16; S, X, W, Tt, At are fp32 values fed as hi + lo
-// bf16 parts (2^-17), the hi and lo parts of S and W side by side as one operand of
-// twice the columns, so that the left operand is read once.  The state itself stays
-// in fp32 registers (thread (n, half) holds row n, 32 columns) and is added to with
-// rounding to nearest.
+// bf16 parts, the hi and lo parts of S and W side by side as one operand of twice the
+// columns, so that the left operand is read once.  The state itself stays in fp32, in
+// tensor memory beside the accumulators, and is added to by the threads with rounding to
+// nearest.
 //
 // What bounds it is the latency of the chain of three products and three passes of
-// the threads.  A block needs 97 KB of shared memory with one set of K, Q tiles, so
-// that two chains share an SM and hide in each other's waits; with few chains (one
+// the threads.  The rows that carry the chain (K tokens) lie in two of the four lane
+// quarters, which only half of the warps may read: 16 warps of 16 columns each hide one
+// another's waits there.  A block needs 106 KB of shared memory with one set of K, Q tiles,
+// so that two chains share an SM and hide in each other's waits; with few chains (one
 // block per SM) a second set of K, Q tiles takes the load latency out of the chain.
 #include <cuda.h>
 
@@ -30,9 +32,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kCompute = 256;              // eight warps: TMEM lane quarter w % 4, column half w / 4
+constexpr int kCompute = 512;              // 16 warps: TMEM lane quarter w % 4, columns 16 (w / 4) .. + 15
 constexpr int kScanThreads = kCompute + 64;  // and a warp that issues the products, one that issues the copies
-constexpr uint32_t kAccCols = 128;
+constexpr uint32_t kTmemCols = 256;
 
 // shared memory from a 1024-byte aligned base
 constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128; X (16 KB) and W (16 KB) in their place
@@ -42,8 +44,25 @@ constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
 constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
 constexpr uint32_t kKQBytes = 32768;
 
+// One piece of the state: 16 columns of row `row` at TMEM address ts; its parts as an operand
+__device__ __forceinline__ void publish_piece(uint32_t planes, int row, int group, const float2 *S) {
+    store_parts8(planes, planes + 16384, row, 2 * group, S);
+    store_parts8(planes, planes + 16384, row, 2 * group + 1, S + 4);
+}
+// fp32 rows of a state [P, N] in global memory: element (p, n) at p N + n, lanes along n
+__device__ __forceinline__ void load_piece(float2 *S, const float *src, int row, int col, int P, int N) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) ((float *)S)[j] = (src && row < N && col + j < P) ? src[(long long)(col + j) * N + row] : 0.f;
+}
+__device__ __forceinline__ void store_piece(const float2 *S, float *dst, int row, int col, int P, int N) {
+    if (!dst || row >= N) return;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (col + j < P) dst[(long long)(col + j) * N + row] = ((const float *)S)[j];
+}
+
 struct ScanMaps {
-    CUtensorMap k, q, v, d_o;
+    CUtensorMap k, q, v;
 };
 
 template <int NB, bool BWD>
@@ -51,8 +70,9 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     delta_scan_fwd(const ChunkParams cp, const __grid_constant__ ScanMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_kq[2], bar_tri, bar_v;               // copies have landed
-    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (8 warps each)
+    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (by every compute warp)
     __shared__ uint64_t bar_m[3];                                // products are done
+    __shared__ uint64_t bar_kept;                                // the backward's copy of S has been taken
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     const DeltaParams &p = cp.p;
@@ -70,10 +90,11 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         mbar_init(&bar_x, kCompute / 32);
         mbar_init(&bar_w, kCompute / 32);
         for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_init(&bar_kept, 1);
         mbar_fence_init();
         s_err = 0;
     }
-    if (warp == 0) tmem_alloc(&s_tmem, kAccCols);
+    if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
     // the row octets of the triangles that no copy writes are zero
     for (int i = tid; i < 32768 / 16; i += kScanThreads) st_shared_v4(base + kOffTri + 16 * i, 0, 0, 0, 0);
     fence_async_smem();
@@ -169,8 +190,21 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             load_tri(0);
         }
         bool ok = true;
+        auto keep = [&](int c) {  // S before chunk c, from the operand
+            if (!BWD) return true;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar_s, c & 1))) return false;
+            if (lane == 0) {
+                bulk_store(cp.w.states + ((long long)blockIdx.x * cp.n + c) * kStateTile, base + kOffS, kStateTile);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(&bar_kept);
+            }
+            __syncwarp();
+            return true;
+        };
         for (int c = 0; c + 1 < nv; ++c) {
             const uint32_t ph = c & 1;
+            if (!(ok = keep(c))) break;
             if (lane == 0) {  // what the next chunk reads, into L2
                 prefetch_bulk(img0 + (long long)(c + 1) * kImgBytes, kImgBytes);
                 if (c + NB < nv)
@@ -179,7 +213,6 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                         prefetch_tile(&maps.q, 64 * kb, grp, (c + NB) * kChunk, bi);
                     }
                 prefetch_tile(&maps.v, 64 * slice, h, (c + 1) * kChunk, bi);
-                if (BWD) prefetch_tile(&maps.d_o, 64 * slice, h, (c + 1) * kChunk, bi);
             }
             // V and, by the first product, Q have been read
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
@@ -199,36 +232,22 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 load_rows(c + NB, &maps.k, 0);
             }
         }
+        if (ok && nv > 0) ok = keep(nv - 1);
+        if (BWD && lane == 0) bulk_wait_all();
         if (!ok) s_err = 1;
         // every copy has to land before the block may end
         for (int c = max(0, kq_issued - NB); c < kq_issued; ++c) mbar_wait(&bar_kq[c % NB], (c / NB) & 1);
         if (tri_issued) mbar_wait(&bar_tri, (tri_issued - 1) & 1);
         if (v_issued) mbar_wait(&bar_v, (v_issued - 1) & 1);
     } else {
-        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // rows 0 .. 63: K tokens, 64 .. 127: Q tokens
-        const int i = row & 63;              // the row's token
-        const uint32_t my = tmem_addr(tm, 32 * quarter, 32 * half);
+        const int i = row & 63, col = slice * 64 + 16 * group;
+        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + 64, ts = ta + 128;
         const float2 one = make_float2(1.f, 1.f);
-        float2 S[16];
-        {
-            const float *src = p.init ? p.init + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row : nullptr;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                ((float *)S)[j] = (src && row < p.N && slice * 64 + 32 * half + j < p.P) ? src[(long long)j * p.N] : 0.f;
-        }
         bool ok = true;
-        // the backward's copy of S before chunk c
-        auto keep_state = [&](int c) {
-            char *tile = cp.w.states + ((long long)blockIdx.x * (cp.n + 1) + c) * kStateTile;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store_parts8(tile, 16384, row, 4 * half + j, S + 4 * j);
-        };
-        // S as an operand; before the last chunk, K rows of absent tokens are made zero
-        auto publish_s = [&](int c) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 4 * j);
-            if (BWD) keep_state(c);
+        // the state operand of chunk c is written; before the last chunk, K rows of absent tokens are made zero
+        auto published = [&](int c) {
             const int live = V - c * kChunk;
             if (live < kChunk) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[c % NB], (c / NB) & 1));
@@ -241,45 +260,33 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_s);
         };
-        if (nv > 0) publish_s(0);
+        {
+            float2 S[8];
+            load_piece(S, p.init ? p.init + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
+            tmem_st16(ts, (const float *)S);
+            if (nv > 0) publish_piece(base + kOffS, row, group, S);
+            tmem_wait_st();
+            if (nv > 0) published(0);
+        }
         for (int c = 0; c < nv && ok; ++c) {
             const uint32_t ph = c & 1;
             const float *gates = (const float *)(img0 + (long long)c * kImgBytes);
             const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
             const float ec = __ldg(gates + kChunk - 1);
-            const bool live = c * kChunk + i < V, partial = V - c * kChunk < kChunk;
-            const int tok = c * kChunk + i, col = slice * 64 + 32 * half;
-            const long long at = (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
-            uint4 dov[BWD ? 4 : 1];
-            float fq = 0.f;
-            if (BWD && !keys) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    dov[j] = live && col + 8 * j < p.P ? __ldg((const uint4 *)((const bf16 *)p.d_o + at + 8 * j)) : make_uint4(0, 0, 0, 0);
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph));
+            const int tok = c * kChunk + i;
+            const bool live = tok < V, partial = V - c * kChunk < kChunk;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph) && (!BWD || mbar_wait(&bar_kept, ph)));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            {
                 float2 a[8], b[8];
-                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
+                tmem_ld16x2(ta, tb, (float *)a, (float *)b);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
                 if (keys) {
-                    if (BWD) {
-                        char *tile = cp.w.reads + ((long long)blockIdx.x * cp.n + c) * kErrTile;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float2 rd[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) rd[e] = live ? fmul2(a[4 * u + e], make_float2(eg, eg)) : make_float2(0.f, 0.f);
-                            store_parts8(tile, 8192, i, 4 * half + 2 * j + u, rd);
-                        }
-                    }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + 2 * j + u));
+                        const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 2 * group + u));
                         const uint32_t vv[4] = {w.x, w.y, w.z, w.w};
                         float2 xb[4];
 #pragma unroll
@@ -289,18 +296,14 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                             a[4 * u + e] = x;
                             xb[e] = fmul2(x, make_float2(be, be));
                         }
-                        store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + 2 * j + u, xb);
+                        store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + u, xb);
                     }
                 } else {
                     const float f = p.scale * eg;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
-                    if (BWD) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) fq = dot8(dov[2 * j + u], a + 4 * u, fq);
-                    }
                 }
-                tmem_st16(my + 16 * j, (const float *)a);
+                tmem_st16(ta, (const float *)a);
             }
             tmem_wait_st();
             fence_async_smem();
@@ -312,19 +315,19 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             if (!ok) break;
             tc_fence_after();
             {
-                float2 a[16];
-                tmem_ld32(my, (float *)a);
+                float2 a[8];
+                tmem_ld16(ta, (float *)a);
                 if (keys) {
-                    const float f = live ? be * et : 0.f;
+                    const float f = be * et;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int u = 0; u < 2; ++u) {
                         float2 w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (partial && !live) a[4 * j + e] = make_float2(0.f, 0.f);
-                            w[e] = fmul2(a[4 * j + e], make_float2(f, f));
+                            if (partial && !live) a[4 * u + e] = make_float2(0.f, 0.f);
+                            w[e] = fmul2(a[4 * u + e], make_float2(f, f));
                         }
-                        store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, w);
+                        store_parts8(base + kOffW, base + kOffW + 8192, i, 2 * group + u, w);
                     }
                     fence_async_smem();
                 }
@@ -333,52 +336,48 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 if (lane == 0) mbar_arrive(&bar_w);
                 if (BWD && keys) {
                     char *tile = cp.w.errs + ((long long)blockIdx.x * cp.n + c) * kErrTile;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) store_parts8(tile, 8192, i, 4 * half + j, a + 4 * j);
+                    store_parts8(tile, 8192, i, 2 * group, a);
+                    store_parts8(tile, 8192, i, 2 * group + 1, a + 4);
                 }
-                if (BWD && !keys) cp.w.fq[((long long)blockIdx.x * 2 + half) * cp.n * kChunk + tok] = live ? fq : 0.f;
                 if (!BWD && !keys) {
+                    bf16 *dst = (bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (tok < p.L && col + 8 * j < p.P)
-                            *(uint4 *)((bf16 *)p.o + at + 8 * j) = live ? pack8(a + 4 * j) : make_uint4(0, 0, 0, 0);
+                    for (int u = 0; u < 2; ++u)
+                        if (tok < p.L && col + 8 * u < p.P) *(uint4 *)(dst + 8 * u) = live ? pack8(a + 4 * u) : make_uint4(0, 0, 0, 0);
                 }
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
             if (!ok) break;
             tc_fence_after();
+            {
+                float2 a[8], b[8], S[8];
+                tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float2 a[8], b[8];
-                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    S[8 * j + e] = ffma2(S[8 * j + e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
+                for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
+                if (c + 1 < nv) publish_piece(base + kOffS, row, group, S);
+                tmem_st16(ts, (const float *)S);
+                tmem_wait_st();
+                if (c + 1 < nv) published(c + 1);
             }
-            if (c + 1 < nv) publish_s(c + 1);
         }
         if (!ok) s_err = 1;
-        if (BWD) {
-            if (ok) keep_state(nv);
-        }
         // absent tokens past the last chunk
         for (long long x = (long long)nv * kChunk * 8 + tid; !BWD && x < (long long)p.L * 8; x += kCompute) {
             const int tok = (int)(x / 8), cc = (int)(x % 8);
             if (slice * 64 + cc * 8 < p.P)
                 *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
         }
-        if (ok && p.final_state && row < p.N) {
-            float *dst = p.final_state + ((long long)bh * p.P + slice * 64 + 32 * half) * p.N + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (slice * 64 + 32 * half + j < p.P) dst[(long long)j * p.N] = ((const float *)S)[j];
+        if (ok && p.final_state) {
+            float2 S[8];
+            tmem_ld16(ts, (float *)S);
+            store_piece(S, p.final_state + (long long)bh * p.P * p.N, row, col, p.P, p.N);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, kAccCols);
+    if (warp == 0) tmem_dealloc(tm, kTmemCols);
 }
 
 // ------------------------------------------------------------------ reverse
@@ -400,8 +399,9 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     delta_scan_rev(const ChunkParams cp, const __grid_constant__ RevMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_kq[2], bar_rev, bar_do;              // copies have landed
-    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (8 warps each)
+    __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (by every compute warp)
     __shared__ uint64_t bar_m[3];                                // products are done
+    __shared__ uint64_t bar_kept;                                // the backward's copy of S has been taken
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     const DeltaParams &p = cp.p;
@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         mbar_init(&bar_x, kCompute / 32);
         mbar_init(&bar_w, kCompute / 32);
         for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_init(&bar_kept, 1);
         mbar_fence_init();
         s_err = 0;
     }
-    if (warp == 0) tmem_alloc(&s_tmem, 256);
+    if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -436,23 +437,26 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                        dO = sdesc(base + kOffV, 8192, 1024);
         bool ok = true;
         int done = 0;
+        auto own = [&](int r) {  // A^T dO of step r
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_rev, r & 1) && mbar_wait(&bar_do, r & 1));
+            if (!ok || lane) return;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tm + 128, sdesc_add(dR, 8192 + part * 16384 + ks * 2048), sdesc_add(dO, ks * 2048), i0, part > 0 || ks > 0);
+        };
         for (int r = 0; r < nv; ++r) {
             const uint32_t ph = r & 1, kq = base + kOffKQ + (r % NB) * kKQBytes;
             const uint64_t dK = sdesc(kq, 16, 1024), dKt = sdesc(kq, 16384, 1024), dQt = sdesc(kq + 8192, 16384, 1024);
-            ok = mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_rev, ph) && mbar_wait(&bar_do, ph) &&
-                 mbar_wait(&bar_s, ph);
+            ok = mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_s, ph);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
+            if (r == 0) own(0);  // after the rows of absent tokens have been made zero
             if (lane == 0) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                     if (ks < nks) mma_bf16(tm, sdesc_add(dK, (ks >> 2) * 16384 + (ks & 3) * 32), sdesc_add(dS, ks * 2048), i1, ks > 0);
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm + 128, sdesc_add(dR, 8192 + part * 16384 + ks * 2048), sdesc_add(dO, ks * 2048), i0,
-                                 part > 0 || ks > 0);
                 mma_commit(&bar_m[0]);
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
@@ -477,6 +481,9 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             }
             __syncwarp();
             done = r + 1;
+            // the next step's A^T dO, whose accumulator the threads have read
+            if (r + 1 < nv) own(r + 1);
+            if (!ok) break;
         }
         if (!ok) s_err = 1;
         if (done) mbar_wait(&bar_m[2], (done - 1) & 1);  // every product has to complete before the block may end
@@ -518,16 +525,27 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             load_do(0);
         }
         bool ok = true;
+        auto keep = [&](int r) {  // the hi part of dS after the chunk, from the operand
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar_s, r & 1))) return false;
+            if (lane == 0) {
+                bulk_store(cp.w.dstates + ((long long)blockIdx.x * cp.n + nv - 1 - r) * kDStateTile, base + kOffS, kDStateTile);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(&bar_kept);
+            }
+            __syncwarp();
+            return true;
+        };
         for (int r = 0; r + 1 < nv; ++r) {
             const uint32_t ph = r & 1;
+            if (!(ok = keep(r))) break;
             if (lane == 0) {  // what the next step reads, into L2
                 const int c = nv - 2 - r;
                 const long long at = (long long)blockIdx.x * cp.n + c;
                 prefetch_bulk(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes, kGates);
                 prefetch_bulk(cp.w.rev + ((long long)bh * cp.n + c) * kRevBytes, kRevBytes);
-                prefetch_bulk(cp.w.states + (at + blockIdx.x) * kStateTile, kStateTile);
+                prefetch_bulk(cp.w.states + at * kStateTile, kStateTile);
                 prefetch_bulk(cp.w.errs + at * kErrTile, kErrTile);
-                prefetch_bulk(cp.w.reads + at * kErrTile, kErrTile);
                 prefetch_tile(&maps.d_o, 64 * slice, h, c * kChunk, bi);
                 if (r + NB < nv)
                     for (uint32_t kb = 0; kb < halves; ++kb) {
@@ -544,36 +562,24 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 load_kq(r + NB);
             }
         }
+        if (ok && nv > 0) ok = keep(nv - 1);
+        if (lane == 0) bulk_wait_all();
         if (!ok) s_err = 1;
         // every copy has to land before the block may end
         for (int r = max(0, kq_issued - NB); r < kq_issued; ++r) mbar_wait(&bar_kq[r % NB], (r / NB) & 1);
         if (rev_issued) mbar_wait(&bar_rev, (rev_issued - 1) & 1);
         if (do_issued) mbar_wait(&bar_do, (do_issued - 1) & 1);
     } else {
-        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // these threads form dU and X; the others D
-        const int i = row & 63;              // the row's token
-        const uint32_t my = tmem_addr(tm, 32 * quarter, 32 * half);
-        const int col = slice * 64 + 32 * half;
+        const int i = row & 63, col = slice * 64 + 16 * group;
+        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + 64, tu = ta + 128, ts = ta + 192;
         const float2 one = make_float2(1.f, 1.f);
-        float2 S[16];
-        {
-            const float *src = p.d_final ? p.d_final + ((long long)bh * p.P + col) * p.N + row : nullptr;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                ((float *)S)[j] = (src && row < p.N && col + j < p.P) ? src[(long long)j * p.N] : 0.f;
-        }
         bool ok = true;
-        // dS after chunk nv - 1 - r as an operand, kept for the gradients of q and k
-        auto publish_s = [&](int r) {
-            char *tile = cp.w.dstates + ((long long)blockIdx.x * cp.n + nv - 1 - r) * kDStateTile;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                store_parts8(base + kOffS, base + kOffS + 16384, row, 4 * half + j, S + 4 * j);
-                *(uint4 *)(tile + sw128_chunk(row, 4 * half + j)) = pack8(S + 4 * j);
-            }
+        // the operand of step r is written; in the first, K, Q and dO rows of absent tokens are made zero
+        auto published = [&](int r) {
             const int live = V - (nv - 1 - r) * kChunk;
-            if (live < kChunk) {  // the last chunk: K, Q and dO rows of absent tokens are made zero
+            if (live < kChunk) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_do, r & 1));
                 const uint32_t kq = base + kOffKQ + (r % NB) * kKQBytes;
                 for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
@@ -586,62 +592,69 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_s);
         };
-        if (nv > 0) publish_s(0);
+        {
+            float2 S[8];
+            load_piece(S, p.d_final ? p.d_final + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
+            tmem_st16(ts, (const float *)S);
+            if (nv > 0) publish_piece(base + kOffS, row, group, S);
+            tmem_wait_st();
+            if (nv > 0) published(0);
+        }
         for (int r = 0; r < nv && ok; ++r) {
             const int c = nv - 1 - r;
             const uint32_t ph = r & 1;
+            const long long cc = (long long)blockIdx.x * cp.n + c;
             const float *gates = (const float *)(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes);
             const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
             const float ec = __ldg(gates + kChunk - 1);
             const int tok = c * kChunk + i;
+            float2 z[8];  // Z, for the rows of the chain
+            if (keys) {
+                const char *err = cp.w.errs + cc * kErrTile;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const char *src = err + sw128_chunk(i, 2 * group + u);
+                    join8(__ldg((const uint4 *)src), __ldg((const uint4 *)(src + 8192)), z + 4 * u);
+                }
+            }
             // e^gamma_C <S, dS>, while the products run
             {
-                const char *tile = cp.w.states + ((long long)blockIdx.x * (cp.n + 1) + c) * kStateTile;
+                const char *tile = cp.w.states + cc * kStateTile;
+                float2 S[8];
+                tmem_ld16(ts, (float *)S);
                 float sum = 0.f;
-                if (row < p.N) {
+                if (row < p.N)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const char *src = tile + sw128_chunk(row, 4 * half + j);
-                        sum = dot8(__ldg((const uint4 *)src), S + 4 * j, sum);
-                        sum = dot8(__ldg((const uint4 *)(src + 16384)), S + 4 * j, sum);
+                    for (int u = 0; u < 2; ++u) {
+                        const char *src = tile + sw128_chunk(row, 2 * group + u);
+                        sum = dot8(__ldg((const uint4 *)src), S + 4 * u, sum);
+                        sum = dot8(__ldg((const uint4 *)(src + 16384)), S + 4 * u, sum);
                     }
-                }
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) cp.w.ss[((long long)blockIdx.x * cp.n + c) * 8 + warp] = ec * sum;
+                if (lane == 0) cp.w.ss[cc * 16 + warp] = ec * sum;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_kept, ph));
             if (!ok) break;
             tc_fence_after();
-            const char *err = cp.w.errs + ((long long)blockIdx.x * cp.n + c) * kErrTile;
             float2 ww = make_float2(0.f, 0.f);
             if (keys) {
+                float2 a[8], b[8], u[8];
+                tmem_ld16x3(ta, tb, tu, (float *)a, (float *)b, (float *)u);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float2 a[8], b[8], u[8];
-                    tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
-                    tmem_ld16(my + 128 + 16 * j, (float *)u);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) a[e] = fmul2(ffma2(b[e], one, a[e]), make_float2(et, et));
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float2 z[4];
-                        const char *src = err + sw128_chunk(i, 4 * half + 2 * j + x);
-                        join8(__ldg((const uint4 *)src), __ldg((const uint4 *)(src + 8192)), z);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) ww = ffma2(z[e], a[4 * x + e], ww);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) a[e] = ffma2(u[e], one, a[e]);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float2 xb[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) xb[e] = fmul2(a[4 * x + e], make_float2(be, be));
-                        store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + 2 * j + x, xb);
-                    }
-                    tmem_st16(my + 16 * j, (const float *)a);
+                for (int e = 0; e < 8; ++e) {
+                    a[e] = fmul2(ffma2(b[e], one, a[e]), make_float2(et, et));
+                    ww = ffma2(z[e], a[e], ww);
+                    a[e] = ffma2(u[e], one, a[e]);
                 }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float2 xb[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xb[e] = fmul2(a[4 * x + e], make_float2(be, be));
+                    store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + x, xb);
+                }
+                tmem_st16(ta, (const float *)a);
                 tmem_wait_st();
                 fence_async_smem();
             }
@@ -649,65 +662,54 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_x);
 
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph) && mbar_wait(&bar_do, ph));
             if (!ok) break;
             tc_fence_after();
             if (keys) {
-                float2 a[16];
-                tmem_ld32(my, (float *)a);
+                float2 a[8];
+                tmem_ld16(ta, (float *)a);
                 const float f = -eg * be;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int x = 0; x < 2; ++x) {
                     float2 w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * j + e], make_float2(f, f));
-                    store_parts8(base + kOffW, base + kOffW + 8192, i, 4 * half + j, w);
+                    for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * x + e], make_float2(f, f));
+                    store_parts8(base + kOffW, base + kOffW + 8192, i, 2 * group + x, w);
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_w);
-                const char *read = cp.w.reads + ((long long)blockIdx.x * cp.n + c) * kErrTile;
-                char *lo_tile = cp.w.dv_lo + ((long long)blockIdx.x * cp.n + c) * kDvLoTile;
-                const long long at = (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
-                float2 zx = make_float2(0.f, 0.f), fk = zx;
+                char *lo_tile = cp.w.dv_lo + cc * kDvLoTile;
+                bf16 *dst = (bf16 *)p.dv + (((long long)bi * p.L + tok) * p.H + h) * p.P + col;
+                float2 zx = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t off = sw128_chunk(i, 4 * half + j);
-                    float2 z[4];
-                    join8(__ldg((const uint4 *)(err + off)), __ldg((const uint4 *)(err + off + 8192)), z);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        zx = ffma2(z[e], a[4 * j + e], zx);
-                        a[4 * j + e] = fmul2(a[4 * j + e], make_float2(be, be));
-                    }
-                    join8(__ldg((const uint4 *)(read + off)), __ldg((const uint4 *)(read + off + 8192)), z);
+                for (int x = 0; x < 2; ++x) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        fk = ffma2(z[e], a[4 * j + e], fk);
-                        split2(a[4 * j + e].x, a[4 * j + e].y, hi[e], lo[e]);
+                        zx = ffma2(z[4 * x + e], a[4 * x + e], zx);
+                        const float2 d = fmul2(a[4 * x + e], make_float2(be, be));
+                        split2(d.x, d.y, hi[e], lo[e]);
                     }
-                    *(uint4 *)(lo_tile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    if (tok < p.L && col + 8 * j < p.P)
-                        *(uint4 *)((bf16 *)p.dv + at + 8 * j) = tok < V ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0, 0, 0, 0);
+                    *(uint4 *)(lo_tile + sw128_chunk(i, 2 * group + x)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (tok < p.L && col + 8 * x < p.P)
+                        *(uint4 *)(dst + 8 * x) = tok < V ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0, 0, 0, 0);
                 }
-                const long long sat = ((long long)blockIdx.x * 2 + half) * cp.n * kChunk + tok;
+                const long long sat = ((long long)blockIdx.x * 4 + group) * cp.n * kChunk + tok;
                 cp.w.zx[sat] = zx.x + zx.y;
-                cp.w.fk[sat] = -(fk.x + fk.y);
                 cp.w.ww[sat] = be * (ww.x + ww.y);
             } else {
                 // D = scale e^gamma dO in place of beta dU
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar_do, ph));
                 const float f = p.scale * eg;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 4 * half + j));
+                for (int x = 0; x < 2; ++x) {
+                    const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 2 * group + x));
                     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
                     float2 d[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) d[e] = fmul2(bf2_to_f2(v[e]), make_float2(f, f));
-                    store_parts8(base + kOffX, base + kOffX + 8192, i, 4 * half + j, d);
+                    store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + x, d);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -717,15 +719,16 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
             if (!ok) break;
             tc_fence_after();
+            {
+                float2 a[8], b[8], S[8];
+                tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float2 a[8], b[8];
-                tmem_ld16x2(my + 16 * j, my + 64 + 16 * j, (float *)a, (float *)b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    S[8 * j + e] = ffma2(S[8 * j + e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
+                for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
+                if (r + 1 < nv) publish_piece(base + kOffS, row, group, S);
+                tmem_st16(ts, (const float *)S);
+                tmem_wait_st();
+                if (r + 1 < nv) published(r + 1);
             }
-            if (r + 1 < nv) publish_s(r + 1);
         }
         if (!ok) s_err = 1;
         // absent tokens past the last chunk
@@ -734,18 +737,17 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             if (slice * 64 + cc * 8 < p.P)
                 *(uint4 *)((bf16 *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
         }
-        if (ok && p.d_init && row < p.N) {
-            float *dst = p.d_init + ((long long)bh * p.P + col) * p.N + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col + j < p.P) dst[(long long)j * p.N] = ((const float *)S)[j];
+        if (ok && p.d_init) {
+            float2 S[8];
+            tmem_ld16(ts, (float *)S);
+            store_piece(S, p.d_init + (long long)bh * p.P * p.N, row, col, p.P, p.N);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, 256);
+    if (warp == 0) tmem_dealloc(tm, kTmemCols);
 }
 
 }  // namespace
@@ -757,7 +759,6 @@ cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
-    if (c.w.states && (e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * ((p.P + 63) / 64));
     const bool one_per_sm = grid <= 152;
     auto kernel = c.w.states ? (one_per_sm ? delta_scan_fwd<2, true> : delta_scan_fwd<1, true>)
