@@ -1,5 +1,5 @@
 // delta_scan.cu -- the serial pass of the chunked gated delta rule
-// (delta_chunk.cuh): one block per (b, h, 64 columns of P) walks the chunks in
+// (delta_chunk.cuh): one block per (b, h, W columns of P) walks the chunks in
 // order.  Per chunk, three products on the tensor cores, each waiting for the
 // one before:
 //   1.  [K; Q] S       M = 64 + 64 tokens, K index = N      -> K S and Q S
@@ -20,7 +20,10 @@
 // quarters, which only half of the warps may read: 16 warps of 16 columns each hide one
 // another's waits there.  A block needs 106 KB of shared memory with one set of K, Q tiles,
 // so that two chains share an SM and hide in each other's waits; with few chains (one
-// block per SM) a second set of K, Q tiles takes the load latency out of the chain.
+// block per SM) a second set of K, Q tiles takes the load latency out of the chain, and
+// narrower slices of P (W = 32 or 16 for 64) put more SMs on a chain, each with shorter
+// passes and products: they repeat the loads of K and Q and waste part of the
+// instruction, so they are taken only where every slice still has an SM of its own.
 #include <cuda.h>
 
 #include "delta_chunk.cuh"
@@ -32,22 +35,38 @@ namespace {
 
 using namespace tc;
 
-constexpr int kCompute = 512;              // 16 warps: TMEM lane quarter w % 4, columns 16 (w / 4) .. + 15
-constexpr int kScanThreads = kCompute + 64;  // and a warp that issues the products, one that issues the copies
+// 4 warps for every 16 columns of the slice (TMEM lane quarter w % 4, columns 16 (w / 4) .. + 15),
+// a warp that issues the products, one that issues the copies
+constexpr int compute_threads(int W) { return 8 * W; }
+constexpr int scan_threads(int W) { return compute_threads(W) + 64; }
 constexpr uint32_t kTmemCols = 256;
+constexpr int kSMs = 152;
 
 // shared memory from a 1024-byte aligned base
-constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128; X (16 KB) and W (16 KB) in their place
+constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128 each; X and W in their place
 constexpr uint32_t kOffX = 0, kOffW = 16384;
+// narrow slices: hi and lo parts side by side in the rows of one tile
 constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][16 row octets][2][128 bytes]: Tt rows, then At rows
 constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
 constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
 constexpr uint32_t kKQBytes = 32768;
 
-// One piece of the state: 16 columns of row `row` at TMEM address ts; its parts as an operand
+// 8 values as hi and lo parts of an operand tile with W columns: piece `piece` of row `row`; the lo
+// tile lies `lo` bytes behind (W = 64), or the lo columns behind the hi ones
+template <int W>
+__device__ __forceinline__ void store_operand8(uint32_t tile, uint32_t lo, int row, int piece, const float2 *x) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
+    const uint32_t at = tile + sw128_chunk(row, piece), al = W == 64 ? at + lo : tile + sw128_chunk(row, piece + W / 8);
+    st_shared_v4(at, h[0], h[1], h[2], h[3]);
+    st_shared_v4(al, l[0], l[1], l[2], l[3]);
+}
+// 16 columns of row `row` of the state
+template <int W>
 __device__ __forceinline__ void publish_piece(uint32_t planes, int row, int group, const float2 *S) {
-    store_parts8(planes, planes + 16384, row, 2 * group, S);
-    store_parts8(planes, planes + 16384, row, 2 * group + 1, S + 4);
+    store_operand8<W>(planes, 16384, row, 2 * group, S);
+    store_operand8<W>(planes, 16384, row, 2 * group + 1, S + 4);
 }
 // fp32 rows of a state [P, N] in global memory: element (p, n) at p N + n, lanes along n
 __device__ __forceinline__ void load_piece(float2 *S, const float *src, int row, int col, int P, int N) {
@@ -65,8 +84,8 @@ struct ScanMaps {
     CUtensorMap k, q, v;
 };
 
-template <int NB, bool BWD>
-__global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
+template <int NB, bool BWD, int W>
+__global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     delta_scan_fwd(const ChunkParams cp, const __grid_constant__ ScanMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_kq[2], bar_tri, bar_v;               // copies have landed
@@ -77,7 +96,9 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     __shared__ int s_err;
     const DeltaParams &p = cp.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int nsl = slices_of(p), slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
+    constexpr int kCompute = compute_threads(W), kScanThreads = scan_threads(W);
+    static_assert(!BWD || W == 64, "the backward's tiles have 64 columns");
+    const int nsl = (p.P + W - 1) / W, slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
     const char *img0 = cp.img + (long long)bh * cp.n * (long long)kImgBytes;
@@ -105,8 +126,8 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
 
     if (warp == kCompute / 32) {
         // ---- products
-        const uint32_t i1 = idesc_bf16(128, 128, false, true), i2 = idesc_bf16(128, 64, false, true),
-                       i3 = idesc_bf16(128, 128, true, true);
+        const uint32_t i1 = idesc_bf16(128, 2 * W, false, true), i2 = idesc_bf16(128, W, false, true),
+                       i3 = idesc_bf16(128, 2 * W, true, true);
         const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
                        dW = sdesc(base + kOffW, 8192, 1024), dT = sdesc_tri(base + kOffTri);
         bool ok = true;
@@ -127,12 +148,20 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
+                if (W == 64) {
 #pragma unroll
-                for (int pass = 0; pass < 3; ++pass)
+                    for (int pass = 0; pass < 3; ++pass)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm, sdesc_add(dT, (pass == 2 ? 16384 : 0) + ks * 4096),
-                                 sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i2, true);
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_bf16(tm, sdesc_add(dT, (pass == 2 ? 16384 : 0) + ks * 4096),
+                                     sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i2, true);
+                } else {  // the products with X lo in the columns behind
+#pragma unroll
+                    for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_bf16(tm, sdesc_add(dT, pass * 16384 + ks * 4096), sdesc_add(dX, ks * 2048), pass ? i2 : i1, true);
+                }
                 mma_commit(&bar_m[1]);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph));
@@ -152,6 +181,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         // ---- copies
         const int grp = h / p.hpg;
         const uint32_t halves = p.N > 64 ? 2u : 1u;
+        const int vcol = slice * W / 64 * 64;  // V comes in tiles of 64 columns
         int kq_issued = 0, tri_issued = 0, v_issued = 0;
         auto expect_kq = [&](int c) {
             if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], halves * 16384u);
@@ -176,7 +206,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         auto load_v = [&](int c) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bar_v, 8192);
-                tma_tile(base + kOffV, &maps.v, &bar_v, 64 * slice, h, c * kChunk, bi);
+                tma_tile(base + kOffV, &maps.v, &bar_v, vcol, h, c * kChunk, bi);
             }
             v_issued = c + 1;
         };
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                         prefetch_tile(&maps.k, 64 * kb, grp, (c + NB) * kChunk, bi);
                         prefetch_tile(&maps.q, 64 * kb, grp, (c + NB) * kChunk, bi);
                     }
-                prefetch_tile(&maps.v, 64 * slice, h, (c + 1) * kChunk, bi);
+                prefetch_tile(&maps.v, vcol, h, (c + 1) * kChunk, bi);
             }
             // V and, by the first product, Q have been read
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
@@ -242,8 +272,8 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     } else {
         const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // rows 0 .. 63: K tokens, 64 .. 127: Q tokens
-        const int i = row & 63, col = slice * 64 + 16 * group;
-        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + 64, ts = ta + 128;
+        const int i = row & 63, col = slice * W + 16 * group;
+        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + W, ts = ta + 128;
         const float2 one = make_float2(1.f, 1.f);
         bool ok = true;
         // the state operand of chunk c is written; before the last chunk, K rows of absent tokens are made zero
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             float2 S[8];
             load_piece(S, p.init ? p.init + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
             tmem_st16(ts, (const float *)S);
-            if (nv > 0) publish_piece(base + kOffS, row, group, S);
+            if (nv > 0) publish_piece<W>(base + kOffS, row, group, S);
             tmem_wait_st();
             if (nv > 0) published(0);
         }
@@ -286,7 +316,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 if (keys) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 2 * group + u));
+                        const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, (col & 63) / 8 + u));
                         const uint32_t vv[4] = {w.x, w.y, w.z, w.w};
                         float2 xb[4];
 #pragma unroll
@@ -296,7 +326,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                             a[4 * u + e] = x;
                             xb[e] = fmul2(x, make_float2(be, be));
                         }
-                        store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + u, xb);
+                        store_operand8<W>(base + kOffX, 8192, i, 2 * group + u, xb);
                     }
                 } else {
                     const float f = p.scale * eg;
@@ -304,6 +334,10 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                     for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
                 }
                 tmem_st16(ta, (const float *)a);
+                if (W < 64) {
+                    const float zero[16] = {};
+                    tmem_st16(tb, zero);
+                }
             }
             tmem_wait_st();
             fence_async_smem();
@@ -316,7 +350,14 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             tc_fence_after();
             {
                 float2 a[8];
-                tmem_ld16(ta, (float *)a);
+                if (W < 64) {
+                    float2 b[8];
+                    tmem_ld16x2(ta, tb, (float *)a, (float *)b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
+                } else {
+                    tmem_ld16(ta, (float *)a);
+                }
                 if (keys) {
                     const float f = be * et;
 #pragma unroll
@@ -327,7 +368,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                             if (partial && !live) a[4 * u + e] = make_float2(0.f, 0.f);
                             w[e] = fmul2(a[4 * u + e], make_float2(f, f));
                         }
-                        store_parts8(base + kOffW, base + kOffW + 8192, i, 2 * group + u, w);
+                        store_operand8<W>(base + kOffW, 8192, i, 2 * group + u, w);
                     }
                     fence_async_smem();
                 }
@@ -354,7 +395,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
-                if (c + 1 < nv) publish_piece(base + kOffS, row, group, S);
+                if (c + 1 < nv) publish_piece<W>(base + kOffS, row, group, S);
                 tmem_st16(ts, (const float *)S);
                 tmem_wait_st();
                 if (c + 1 < nv) published(c + 1);
@@ -362,10 +403,9 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
         }
         if (!ok) s_err = 1;
         // absent tokens past the last chunk
-        for (long long x = (long long)nv * kChunk * 8 + tid; !BWD && x < (long long)p.L * 8; x += kCompute) {
-            const int tok = (int)(x / 8), cc = (int)(x % 8);
-            if (slice * 64 + cc * 8 < p.P)
-                *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + slice * 64 + cc * 8) = make_uint4(0, 0, 0, 0);
+        for (long long x = (long long)nv * kChunk * (W / 8) + tid; !BWD && x < (long long)p.L * (W / 8); x += kCompute) {
+            const int tok = (int)(x / (W / 8)), at = slice * W + 8 * (int)(x % (W / 8));
+            if (at < p.P) *(uint4 *)((bf16 *)p.o + (((long long)bi * p.L + tok) * p.H + h) * p.P + at) = make_uint4(0, 0, 0, 0);
         }
         if (ok && p.final_state) {
             float2 S[8];
@@ -395,7 +435,7 @@ struct RevMaps {
 };
 
 template <int NB>
-__global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
+__global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
     delta_scan_rev(const ChunkParams cp, const __grid_constant__ RevMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar_kq[2], bar_rev, bar_do;              // copies have landed
@@ -406,6 +446,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
     __shared__ int s_err;
     const DeltaParams &p = cp.p;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    constexpr int kCompute = compute_threads(64);
     const int nsl = slices_of(p), slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
@@ -596,7 +637,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
             float2 S[8];
             load_piece(S, p.d_final ? p.d_final + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
             tmem_st16(ts, (const float *)S);
-            if (nv > 0) publish_piece(base + kOffS, row, group, S);
+            if (nv > 0) publish_piece<64>(base + kOffS, row, group, S);
             tmem_wait_st();
             if (nv > 0) published(0);
         }
@@ -724,7 +765,7 @@ __global__ void __launch_bounds__(kScanThreads, NB == 1 ? 2 : 1)
                 tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
-                if (r + 1 < nv) publish_piece(base + kOffS, row, group, S);
+                if (r + 1 < nv) publish_piece<64>(base + kOffS, row, group, S);
                 tmem_st16(ts, (const float *)S);
                 tmem_wait_st();
                 if (r + 1 < nv) published(r + 1);
@@ -759,14 +800,22 @@ cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(p.b * p.H * ((p.P + 63) / 64));
-    const bool one_per_sm = grid <= 152;
-    auto kernel = c.w.states ? (one_per_sm ? delta_scan_fwd<2, true> : delta_scan_fwd<1, true>)
-                             : (one_per_sm ? delta_scan_fwd<2, false> : delta_scan_fwd<1, false>);
-    const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    kernel<<<grid, kScanThreads, bytes, s>>>(c, maps);
-    return cudaGetLastError();
+    // the narrowest slices that all have an SM of their own; two blocks of full slices per SM where not even those do
+    const long long chains = (long long)p.b * p.H;
+    int W = 64;
+    if (!c.w.states)
+        while (W > 16 && chains * ((p.P + W / 2 - 1) / (W / 2)) <= kSMs) W /= 2;
+    const long long grid = chains * ((p.P + W - 1) / W);
+    const int nb = grid <= kSMs ? 2 : 1, bytes = 1024 + (int)kOffKQ + nb * (int)kKQBytes;
+    auto launch = [&](auto kernel, int threads) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        kernel<<<(unsigned)grid, threads, bytes, s>>>(c, maps);
+        return cudaGetLastError();
+    };
+    if (c.w.states) return nb == 2 ? launch(delta_scan_fwd<2, true, 64>, scan_threads(64)) : launch(delta_scan_fwd<1, true, 64>, scan_threads(64));
+    if (nb == 1) return launch(delta_scan_fwd<1, false, 64>, scan_threads(64));
+    if (W == 64) return launch(delta_scan_fwd<2, false, 64>, scan_threads(64));
+    return W == 32 ? launch(delta_scan_fwd<2, false, 32>, scan_threads(32)) : launch(delta_scan_fwd<2, false, 16>, scan_threads(16));
 }
 
 cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s) {
@@ -777,11 +826,11 @@ cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * slices_of(p));
-    const bool one_per_sm = grid <= 152;
+    const bool one_per_sm = grid <= kSMs;
     auto kernel = one_per_sm ? delta_scan_rev<2> : delta_scan_rev<1>;
     const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    kernel<<<grid, kScanThreads, bytes, s>>>(c, maps);
+    kernel<<<grid, scan_threads(64), bytes, s>>>(c, maps);
     return cudaGetLastError();
 }
 
