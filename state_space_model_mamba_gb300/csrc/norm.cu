@@ -2,12 +2,13 @@
 // root-mean-square norm in one pass over the row, the output in the stream's
 // type or in e4m3 with scales, and the backward.
 //
-// All three are streams bound by HBM: a row is read once into registers, its
-// sum of squares reduced over the block, and the outputs written from the
-// registers.  A row is held by TPR threads with NV vectors of VEC columns
-// each, vector j of thread t at columns (j TPR + t) VEC, so that every load of
-// a warp is contiguous (512 bytes at VEC = 8 in bf16).  VEC is 8 where D is a
-// multiple of 8, else 2 or 1: rows then start on the vector's alignment.
+// All three are streams bound by HBM.  A row is held by TPR threads with NV vectors of
+// VEC columns each, vector j of thread t at columns (j TPR + t) VEC, so that every load
+// of a warp is contiguous (512 bytes at VEC = 8 in bf16).  VEC is 8 where D is a multiple of
+// 8, else 2 or 1: rows then start on the vector's alignment.  Blocks walk the rows: the
+// weight stays in registers (read again for every row it is as much L2 traffic as half
+// the row), and the next row is loaded, as it is stored, before the sums of this one are
+// waited for.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdio.h>
@@ -20,64 +21,63 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 
-// ---- VEC consecutive elements of a row as floats (aligned to the vector's size, or to 16 bytes)
+// ---- VEC consecutive elements of a row, in 32-bit words as they are stored (VEC sizeof(T) bytes, at most 16 a load)
 template <typename T, int VEC>
-struct Vec;
-template <>
-struct Vec<bf16, 8> {
-    static __device__ __forceinline__ void ld(const bf16 *p, float *f) {
-        const uint4 u = __ldg((const uint4 *)p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Vec {
+    static constexpr int BYTES = VEC * (int)sizeof(T), WORDS = (BYTES + 3) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (BYTES == 32) {
+            const uint4 a = __ldg((const uint4 *)p), b = __ldg((const uint4 *)p + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        } else if constexpr (BYTES == 16) {
+            const uint4 a = __ldg((const uint4 *)p);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else if constexpr (BYTES == 8) {
+            const uint2 a = __ldg((const uint2 *)p);
+            w[0] = a.x, w[1] = a.y;
+        } else if constexpr (BYTES == 4) {
+            w[0] = __ldg((const uint32_t *)p);
+        } else {
+            w[0] = __ldg((const unsigned short *)p);
         }
     }
-    static __device__ __forceinline__ void st(bf16 *p, const float *f) {
-        uint32_t w[4];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *(const uint32_t *)&v;
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void set(const float *f) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], VEC > 1 ? f[2 * i + 1] : 0.f);
+                w[i] = *(const uint32_t *)&v;
+            }
         }
-        *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
     }
-};
-template <>
-struct Vec<float, 8> {
-    static __device__ __forceinline__ void ld(const float *p, float *f) {
-        const float4 a = __ldg((const float4 *)p), b = __ldg((const float4 *)p + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (BYTES == 32) {
+            ((uint4 *)p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            ((uint4 *)p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if constexpr (BYTES == 16) {
+            *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if constexpr (BYTES == 8) {
+            *(uint2 *)p = make_uint2(w[0], w[1]);
+        } else if constexpr (BYTES == 4) {
+            *(uint32_t *)p = w[0];
+        } else {
+            *(unsigned short *)p = (unsigned short)w[0];
+        }
     }
-    static __device__ __forceinline__ void st(float *p, const float *f) {
-        ((float4 *)p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        ((float4 *)p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-};
-template <>
-struct Vec<bf16, 2> {
-    static __device__ __forceinline__ void ld(const bf16 *p, float *f) {
-        const uint32_t u = __ldg((const uint32_t *)p);
-        f[0] = __uint_as_float(u << 16);
-        f[1] = __uint_as_float(u & 0xFFFF0000u);
-    }
-    static __device__ __forceinline__ void st(bf16 *p, const float *f) {
-        *(__nv_bfloat162 *)p = __floats2bfloat162_rn(f[0], f[1]);
-    }
-};
-template <>
-struct Vec<float, 2> {
-    static __device__ __forceinline__ void ld(const float *p, float *f) {
-        const float2 a = __ldg((const float2 *)p);
-        f[0] = a.x, f[1] = a.y;
-    }
-    static __device__ __forceinline__ void st(float *p, const float *f) { *(float2 *)p = make_float2(f[0], f[1]); }
-};
-template <typename T>
-struct Vec<T, 1> {
-    static __device__ __forceinline__ void ld(const T *p, float *f) { f[0] = (float)*p; }
-    static __device__ __forceinline__ void st(T *p, const float *f) { *p = (T)f[0]; }
 };
 
 // e4m3 bytes of VEC floats
@@ -109,21 +109,29 @@ struct Sum {
 struct Max {
     static __device__ __forceinline__ float op(float a, float b) { return max_nan(a, b); }
 };
-// Reduction over the TPR threads of a row; every thread gets the result.  `buf` has a float per warp.
-template <typename Op, int TPR>
-__device__ __forceinline__ float row_reduce(float x, float *buf) {
+// Reduction of K values over the TPR threads of a row; every thread gets the results.  `buf` holds K floats
+// per warp, twice: `turn` alternates between reductions, so that one barrier each is enough.
+template <typename Op, int TPR, int K>
+__device__ __forceinline__ void row_reduce(float (&x)[K], float (*buf)[32][K], int &turn) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x = Op::op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = Op::op(x[k], __shfl_xor_sync(0xffffffffu, x[k], o));
     if constexpr (TPR > 32) {
         const int warp = threadIdx.x / 32, w0 = warp / (TPR / 32) * (TPR / 32);
-        __syncthreads();  // buf may still be read from the reduction before
-        if ((threadIdx.x & 31) == 0) buf[warp] = x;
-        __syncthreads();
-        x = buf[w0];
+        float(*b)[K] = buf[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int i = 1; i < TPR / 32; ++i) x = Op::op(x, buf[w0 + i]);
+            for (int k = 0; k < K; ++k) b[warp][k] = x[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = b[w0][k];
+#pragma unroll
+        for (int i = 1; i < TPR / 32; ++i)
+#pragma unroll
+            for (int k = 0; k < K; ++k) x[k] = Op::op(x[k], b[w0 + i][k]);
     }
-    return x;
 }
 
 struct NormArgs {
@@ -140,130 +148,155 @@ struct NormArgs {
 // ------------------------------------------------------------------ forward
 template <typename T, int VEC, int TPR, int NV, bool FP8>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs a) {
-    __shared__ float buf[32];
+    __shared__ float buf[2][32][1];
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
-    const long long row = blockIdx.x * (long long)RPB + threadIdx.x / TPR;
     const int t = threadIdx.x % TPR;
-    const bool live = row < a.rows;
-    const long long at = row * a.D;
-    float f[NV][VEC];
-    float ss = 0.f;
+    int turn = 0;
+    Vec<float, VEC> w[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + t) * VEC;
-        if (live && c < a.D) {
-            Vec<T, VEC>::ld((const T *)a.x + at + c, f[j]);
-            if (a.residual) {
-                float r[VEC];
-                Vec<T, VEC>::ld((const T *)a.residual + at + c, r);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[j][i] = (float)(T)(f[j][i] + r[i]);  // the stream as it is stored
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[j][i] = 0.f;
-        }
+        w[j].zero();
+        if (c < a.D) w[j].load(a.weight + c);
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + t) * VEC;
-        if (a.stream && live && c < a.D) Vec<T, VEC>::st((T *)a.stream + at + c, f[j]);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ss += f[j][i] * f[j][i];
-    }
-    ss = row_reduce<Sum, TPR>(ss, buf);
-    const float rstd = rsqrtf(ss / (float)a.D + a.eps);
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + t) * VEC;
-        if (c < a.D) {
-            float w[VEC];
-            Vec<float, VEC>::ld(a.weight + c, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                f[j][i] = f[j][i] * rstd * w[i];
-                if (FP8) amax = max_nan(amax, fabsf(f[j][i]));
-            }
-            if (!FP8 && live) Vec<T, VEC>::st((T *)a.y + at + c, f[j]);
-        }
-        if constexpr (FP8 && VEC == 8) {
-            if (a.group) {  // group / 8 neighbouring lanes hold a group's columns of vector j
-                float m = amax;
-                for (int o = a.group / 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                amax = 0.f;
-                const float s = m / kE4m3Max;
-                if (live && c < a.D) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[j][i] = m == 0.f ? 0.f : f[j][i] / s;
-                    st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
-                    if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = s;
-                }
-            }
-        }
-    }
-    if constexpr (FP8) {
-        if (a.group) return;
-        const float m = row_reduce<Max, TPR>(amax, buf), s = m / kE4m3Max;
+    Vec<T, VEC> x[NV], r[NV];
+    const long long first = blockIdx.x * (long long)RPB, step = gridDim.x * (long long)RPB;
+    auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
-            if (live && c < a.D) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[j][i] = m == 0.f ? 0.f : f[j][i] / s;
-                st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
+            x[j].zero();
+            r[j].zero();
+            if (row < a.rows && c < a.D) {
+                x[j].load((const T *)a.x + row * a.D + c);
+                if (a.residual) r[j].load((const T *)a.residual + row * a.D + c);
             }
         }
-        if (live && t == 0) a.scales[row] = s;
+    };
+    load(first + threadIdx.x / TPR);
+    for (long long base = first; base < a.rows; base += step) {
+        const long long row = base + threadIdx.x / TPR, at = row * a.D;
+        const bool live = row < a.rows;
+        float f[NV][VEC], ss[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + t) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[j][i] = a.residual ? x[j].get(i) + r[j].get(i) : x[j].get(i);
+            x[j].set(f[j]);  // the stream as it is stored is what is normalised
+            if (a.stream && live && c < a.D) x[j].store((T *)a.stream + at + c);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                f[j][i] = x[j].get(i);
+                ss[0] += f[j][i] * f[j][i];
+            }
+        }
+        load(row + step);
+        row_reduce<Sum, TPR, 1>(ss, buf, turn);
+        const float rstd = rsqrtf(ss[0] / (float)a.D + a.eps);
+        float amax[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + t) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                f[j][i] = f[j][i] * rstd * w[j].get(i);
+                if (FP8 && c < a.D) amax[0] = max_nan(amax[0], fabsf(f[j][i]));
+            }
+            if (!FP8 && live && c < a.D) {
+                Vec<T, VEC> y;
+                y.set(f[j]);
+                y.store((T *)a.y + at + c);
+            }
+            if constexpr (FP8 && VEC == 8) {
+                if (a.group) {  // group / 8 neighbouring lanes hold a group's columns of vector j
+                    float m = amax[0];
+                    for (int o = a.group / 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    amax[0] = 0.f;
+                    const float inv = m == 0.f ? 0.f : kE4m3Max / m;
+                    if (live && c < a.D) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) f[j][i] *= inv;
+                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
+                        if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = m / kE4m3Max;
+                    }
+                }
+            }
+        }
+        if constexpr (FP8) {
+            if (!a.group) {
+                row_reduce<Max, TPR, 1>(amax, buf, turn);
+                const float m = amax[0], inv = m == 0.f ? 0.f : kE4m3Max / m;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * TPR + t) * VEC;
+                    if (live && c < a.D) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) f[j][i] *= inv;
+                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
+                    }
+                }
+                if (live && t == 0) a.scales[row] = m / kE4m3Max;
+            }
+        }
     }
 }
 
 // ------------------------------------------------------------------ backward
-// Blocks walk rows blockIdx.x, + gridDim.x, ...; a thread's columns are the
-// same in every row, so its share of dweight stays in registers and leaves as
-// one partial row per block, which a second kernel adds in the blocks' order.
+// A thread's columns are the same in every row, so its share of dweight stays in
+// registers and leaves as one partial row per block, which a second kernel adds in
+// the blocks' order.
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const T *dy, const T *h, const float *weight, float eps,
                                                       const T *d_stream, T *dx, float *part, long long rows, int D) {
-    __shared__ float buf[2][32];
+    __shared__ float buf[2][32][2];
     const int t = threadIdx.x;
-    float w[NV][VEC], dw[NV][VEC];
+    int turn = 0;
+    Vec<float, VEC> w[NV];
+    float dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + t) * VEC;
-        if (c < D) Vec<float, VEC>::ld(weight + c, w[j]);
+        w[j].zero();
+        if (c < D) w[j].load(weight + c);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            dw[j][i] = 0.f;
-            if (c >= D) w[j][i] = 0.f;
-        }
+        for (int i = 0; i < VEC; ++i) dw[j][i] = 0.f;
     }
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-        const long long at = row * D;
-        float hv[NV][VEC], dv[NV][VEC], sv[NV][VEC];
+    Vec<T, VEC> hv[NV], dv[NV], sv[NV], hn[NV], dn[NV], sn[NV];
+    auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) hv[j][i] = dv[j][i] = sv[j][i] = 0.f;
-            if (c < D) {
-                Vec<T, VEC>::ld(h + at + c, hv[j]);
-                Vec<T, VEC>::ld(dy + at + c, dv[j]);
-                if (d_stream) Vec<T, VEC>::ld(d_stream + at + c, sv[j]);
+            hn[j].zero();
+            dn[j].zero();
+            sn[j].zero();
+            if (row < rows && c < D) {
+                hn[j].load(h + row * D + c);
+                dn[j].load(dy + row * D + c);
+                if (d_stream) sn[j].load(d_stream + row * D + c);
             }
         }
-        float ss = 0.f, th = 0.f;
+    };
+    load(blockIdx.x);
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        float sum[2] = {0.f, 0.f};  // h^2 and dy w h
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            hv[j] = hn[j];
+            dv[j] = dn[j];
+            sv[j] = sn[j];
+        }
+        load(row + gridDim.x);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                ss += hv[j][i] * hv[j][i];
-                th += dv[j][i] * w[j][i] * hv[j][i];
+                sum[0] += hv[j].get(i) * hv[j].get(i);
+                sum[1] += dv[j].get(i) * w[j].get(i) * hv[j].get(i);
             }
-        ss = row_reduce<Sum, TPR>(ss, buf[0]);
-        th = row_reduce<Sum, TPR>(th, buf[1]);
-        const float rstd = rsqrtf(ss / (float)D + eps);
-        const float coef = rstd * rstd * (th / (float)D);
+        row_reduce<Sum, TPR, 2>(sum, buf, turn);
+        const float rstd = rsqrtf(sum[0] / (float)D + eps);
+        const float coef = rstd * rstd * (sum[1] / (float)D);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
@@ -271,10 +304,13 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const T *dy, const T *h, c
                 float out[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    out[i] = sv[j][i] + rstd * (dv[j][i] * w[j][i] - hv[j][i] * coef);
-                    dw[j][i] += dv[j][i] * hv[j][i] * rstd;
+                    const float d = dv[j].get(i), x = hv[j].get(i);
+                    out[i] = sv[j].get(i) + rstd * (d * w[j].get(i) - x * coef);
+                    dw[j][i] += d * x * rstd;
                 }
-                Vec<T, VEC>::st(dx + at + c, out);
+                Vec<T, VEC> o;
+                o.set(out);
+                o.store(dx + row * D + c);
             }
         }
     }
@@ -282,23 +318,27 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const T *dy, const T *h, c
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
-            if (c < D) Vec<float, VEC>::st(part + (long long)blockIdx.x * D + c, dw[j]);
+            Vec<float, VEC> o;
+            o.set(dw[j]);
+            if (c < D) o.store(part + (long long)blockIdx.x * D + c);
         }
     }
 }
 
-// dweight[c] = the sum over the blocks' partial rows: 32 columns a block, 8 rows of threads, fixed order.
-__global__ void __launch_bounds__(256) rms_dweight_reduce(const float *part, float *dweight, int blocks, int D) {
-    __shared__ float red[8][33];
+// dweight[c] = the sum over the blocks' partial rows: 32 columns a block, 32 rows of threads, fixed order.
+__global__ void __launch_bounds__(1024) rms_dweight_reduce(const float *part, float *dweight, int blocks, int D) {
+    __shared__ float red[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
     float a = 0.f;
-    if (c < D)
-        for (int i = r; i < blocks; i += 8) a += part[(long long)i * D + c];
+    if (c < D) {
+#pragma unroll 4
+        for (int i = r; i < blocks; i += 32) a += part[(long long)i * D + c];
+    }
     red[r][threadIdx.x & 31] = a;
     __syncthreads();
     if (r == 0 && c < D) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) a += red[i][threadIdx.x];
+        for (int i = 1; i < 32; ++i) a += red[i][threadIdx.x];
         dweight[c] = a;
     }
 }
@@ -306,6 +346,7 @@ __global__ void __launch_bounds__(256) rms_dweight_reduce(const float *part, flo
 // ------------------------------------------------------------------ host side
 constexpr long long kMaxD = 16384;
 constexpr int kBwdBlocks = 608;  // four per SM
+constexpr int kFwdThreads = 152 * 1280;  // threads that walk the rows
 
 ssd_status norm_fail(ssd_status st, const char *msg) {
     record_error(msg);
@@ -358,6 +399,10 @@ int vec_of(int64_t D) { return D % 8 == 0 ? 8 : (D % 2 == 0 ? 2 : 1); }
         }                                                                    \
     } while (0)
 
+unsigned fwd_blocks(long long rows, int rows_per_block, int threads) {
+    const long long all = (rows + rows_per_block - 1) / rows_per_block, most = kFwdThreads / threads;
+    return (unsigned)(all < most ? all : most);
+}
 template <typename T, bool FP8>
 cudaError_t forward(const NormArgs &a, cudaStream_t s) {
     const int64_t D = a.D;
@@ -365,7 +410,7 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s) {
     do {                                                                                    \
         constexpr int rpb = TPR < 128 ? 128 / TPR : 1;                                      \
         add_rms_kernel<T, V, TPR, NV, FP8>                                                  \
-            <<<(unsigned)((a.rows + rpb - 1) / rpb), TPR * rpb, 0, s>>>(a);                 \
+            <<<fwd_blocks(a.rows, rpb, TPR * rpb), TPR * rpb, 0, s>>>(a);                   \
     } while (0)
     NORM_BY_D(F);
 #undef F
@@ -383,7 +428,7 @@ cudaError_t backward(const void *dy, const void *h, const float *weight, float e
 #undef F
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !dw) return e;
-    rms_dweight_reduce<<<(unsigned)((D + 31) / 32), 256, 0, s>>>(part, dw, blocks, (int)D);
+    rms_dweight_reduce<<<(unsigned)((D + 31) / 32), 1024, 0, s>>>(part, dw, blocks, (int)D);
     return cudaGetLastError();
 }
 

@@ -49,33 +49,43 @@ def _lib():
     return _bound
 
 
-_ptr = ssd._ptr
+# One decoded token is a few microseconds of GPU work, so the calls below keep the host's
+# part short: addresses go to ctypes as plain integers, the stream comes from the raw
+# query, and what a check would print is only formed when it fails.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _want(name, t, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+    if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
 
 
 def _check_tokens(q, k, v, g, beta, lead):
     """Shapes and types of the per-token tensors; `lead` leading axes (2: [b, L], 1: [b])."""
-    if v.dim() != lead + 2 or q.dim() != lead + 2:
+    vs, qs = v.shape, q.shape
+    if len(vs) != lead + 2 or len(qs) != lead + 2:
         raise ValueError("q, k [.., G, N] and v [.., H, P] need the same leading axes")
     if not v.is_cuda or not v.is_contiguous():
         raise ValueError("v must be a contiguous CUDA tensor")
-    code = ssd._dtype_code(v)
-    G, N = q.shape[-2:]
-    H, P = v.shape[-2:]
+    dtype, device = v.dtype, v.device
+    code = ssd.SSD_BF16 if dtype is _BF16 else ssd._dtype_code(v)
+    G, N = qs[-2:]
+    H, P = vs[-2:]
     if G < 1 or H % G:
         raise ValueError(f"heads ({H}) must be a multiple of key groups ({G})")
-    head = tuple(v.shape[:lead])
-    gate = (head[0], H) if lead == 1 else (head[0], H, head[1])
-    for name, t in (("q", q), ("k", k)):
-        _want(name, t, head + (G, N), v.dtype, v.device)
-    for name, t in (("g", g), ("beta", beta)):
-        _want(name, t, gate, torch.float32, v.device)
+    keys = vs[:lead] + (G, N)
+    gate = (vs[0], H) if lead == 1 else (vs[0], H, vs[1])
+    _want("q", q, keys, dtype, device)
+    _want("k", k, keys, dtype, device)
+    _want("g", g, gate, _F32, device)
+    _want("beta", beta, gate, _F32, device)
     return code, G, N, H, P
 
 
@@ -93,9 +103,9 @@ def workspace_bytes(dims: DeltaDims, dtype_code: int, backward: bool) -> int:
 def _check_sequence(v, N, init_state, valid_len):
     b, _, H, P = v.shape
     if init_state is not None:
-        _want("init_state", init_state, (b, H, P, N), torch.float32, v.device)
+        _want("init_state", init_state, (b, H, P, N), _F32, v.device)
     if valid_len is not None:
-        _want("valid_len", valid_len, (b,), torch.int32, v.device)
+        _want("valid_len", valid_len, (b,), _I32, v.device)
 
 
 def delta_forward(q, k, v, g, beta, scale=None, init_state=None, valid_len=None, return_final_state=True,
@@ -113,11 +123,11 @@ def delta_forward(q, k, v, g, beta, scale=None, init_state=None, valid_len=None,
     b, L = v.shape[:2]
     dims = _dims(b, L, H, P, N, G, simt)
     o = torch.empty_like(v)
-    fin = torch.empty(b, H, P, N, device=v.device, dtype=torch.float32) if return_final_state else None
+    fin = torch.empty(b, H, P, N, device=v.device, dtype=_F32) if return_final_state else None
     ws = torch.empty(workspace_bytes(dims, code, False), dtype=torch.uint8, device=v.device)
     ssd._check(_lib().delta_forward(
         ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
-        _ptr(init_state), _ptr(valid_len), _ptr(o), _ptr(fin), _ptr(ws), ws.numel(), ssd._stream_ptr(v.device)))
+        _ptr(init_state), _ptr(valid_len), _ptr(o), _ptr(fin), _ptr(ws), ws.numel(), _raw_stream(v.device.index)))
     if check_status:
         ssd.workspace_status(ws)
     return o, fin
@@ -132,17 +142,17 @@ def delta_backward(q, k, v, g, beta, do, scale=None, d_final_state=None, init_st
     b, L = v.shape[:2]
     _want("do", do, v.shape, v.dtype, v.device)
     if d_final_state is not None:
-        _want("d_final_state", d_final_state, (b, H, P, N), torch.float32, v.device)
+        _want("d_final_state", d_final_state, (b, H, P, N), _F32, v.device)
     dims = _dims(b, L, H, P, N, G, simt)
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dg=torch.empty_like(g),
                dbeta=torch.empty_like(beta),
-               d_init=torch.empty(b, H, P, N, device=v.device, dtype=torch.float32) if want_d_init else None)
+               d_init=torch.empty(b, H, P, N, device=v.device, dtype=_F32) if want_d_init else None)
     ws = torch.empty(workspace_bytes(dims, code, True), dtype=torch.uint8, device=v.device)
     ssd._check(_lib().delta_backward(
         ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
         _ptr(init_state), _ptr(valid_len), _ptr(do), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
         _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["d_init"]), _ptr(ws), ws.numel(),
-        ssd._stream_ptr(v.device)))
+        _raw_stream(v.device.index)))
     if check_status:
         ssd.workspace_status(ws)
     return out
@@ -160,12 +170,12 @@ def delta_step(q, k, v, g, beta, state, scale=None, state_index=None):
     b = v.shape[0]
     if state.dim() != 4:
         raise ValueError("state must be [slots, H, P, N]")
-    _want("state", state, (state.shape[0], H, P, N), torch.float32, v.device)
+    _want("state", state, (state.shape[0], H, P, N), _F32, v.device)
     if state_index is not None:
-        _want("state_index", state_index, (b,), torch.int32, v.device)
+        _want("state_index", state_index, (b,), _I32, v.device)
     dims = _dims(b, 1, H, P, N, G)
     o = torch.empty_like(v)
     ssd._check(_lib().delta_step(
         ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
-        _ptr(state), state.shape[0], _ptr(state_index), _ptr(o), ssd._stream_ptr(v.device)))
+        _ptr(state), state.shape[0], _ptr(state_index), _ptr(o), _raw_stream(v.device.index)))
     return o

@@ -38,20 +38,26 @@ def _lib():
     return _bound
 
 
-_ptr = ssd._ptr
+# as in delta.py: addresses as plain integers, the raw stream query, messages only on failure
+_BF16, _F32 = torch.bfloat16, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check(x, weight, **same):
-    code = ssd._dtype_code(x)
+    code = ssd.SSD_BF16 if x.dtype is _BF16 else ssd._dtype_code(x)
     if x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor")
     D = x.shape[-1]
-    if tuple(weight.shape) != (D,) or weight.dtype != torch.float32:
+    if weight.shape != (D,) or weight.dtype is not _F32:
         raise ValueError(f"weight: expected ({D},) float32, got {tuple(weight.shape)} {weight.dtype}")
     if weight.device != x.device or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous tensor on {x.device}")
     for name, t in same.items():
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
+        if t is not None and (t.shape != x.shape or t.dtype is not x.dtype or t.device != x.device or not t.is_contiguous()):
             raise ValueError(f"{name} must match x in shape, dtype and device and be contiguous")
     return code, x.numel() // max(D, 1), D
 
@@ -63,7 +69,7 @@ def add_rms_norm(x, weight, eps=1e-5, residual=None):
     y = torch.empty_like(x)
     stream = x if residual is None else torch.empty_like(x)
     ssd._check(_lib().norm_add_rms(code, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(y),
-                                   None if residual is None else _ptr(stream), rows, D, ssd._stream_ptr(x.device)))
+                                   None if residual is None else _ptr(stream), rows, D, _raw_stream(x.device.index)))
     return y, stream
 
 
@@ -76,7 +82,7 @@ def add_rms_norm_fp8(x, weight, eps=1e-5, residual=None, group=0):
     stream = x if residual is None else torch.empty_like(x)
     ssd._check(_lib().norm_add_rms_fp8(code, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(y8), _ptr(scales),
                                        None if residual is None else _ptr(stream), rows, D, group,
-                                       ssd._stream_ptr(x.device)))
+                                       _raw_stream(x.device.index)))
     return y8, scales, stream
 
 
@@ -90,5 +96,5 @@ def add_rms_norm_backward(dy, stream, weight, eps=1e-5, d_stream=None):
     lib = _lib()
     ws = torch.empty(lib.norm_backward_workspace_bytes(rows, D), dtype=torch.uint8, device=stream.device)
     ssd._check(lib.norm_add_rms_backward(code, _ptr(dy), _ptr(stream), _ptr(weight), eps, _ptr(d_stream), _ptr(dx),
-                                         _ptr(dw), rows, D, _ptr(ws), ws.numel(), ssd._stream_ptr(stream.device)))
+                                         _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(stream.device.index)))
     return dx, dw
