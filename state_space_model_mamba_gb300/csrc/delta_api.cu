@@ -92,11 +92,11 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
         off += (bytes + 1023) / 1024 * 1024;
         return at;
     };
-    char *img = take(chains * n * kImgBytes);
+    const int img_bytes = backward ? kImgBwd : kImgFwd;
+    char *img = take(chains * n * img_bytes);
     ChunkBackward w;
     memset(&w, 0, sizeof(w));
     if (backward) {
-        w.rev = take(chains * n * kRevBytes);
         w.states = take(cs * n * kStateTile);
         w.dstates = take(cs * n * kDStateTile);
         w.errs = take(cs * n * kErrTile);
@@ -108,6 +108,7 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
     }
     if (c) {
         c->n = (int)n;
+        c->img_bytes = img_bytes;
         c->img = img;
         c->w = w;
     }

@@ -15,11 +15,15 @@
 // The forward takes A through the inverse, so that one operand (beta o X0) gives both
 // the errors and the outputs:  A U = At (beta o X0),  At = A (I + diag(beta) Tt).
 //
-// The chunk image of one (b, h, chunk) is what the scan copies to shared memory: the
-// gate vectors in fp32, then Tt and At as hi and lo bf16 parts.  Each is kept as the
-// tensor core reads it without swizzle, in 8x8 matrices of 128 contiguous bytes:
-// columns 16 ks .. 16 ks + 15 are one run of the row octets from 2 ks on, two matrices
-// an octet (the octets above are zero and not stored).
+// The chunk image of one (b, h, chunk) is what the scans copy to shared memory: the
+// gate vectors in fp32, then two matrices as hi and lo bf16 parts, kept as the tensor
+// core reads them without swizzle, in 8x8 matrices of 128 contiguous bytes.
+//   forward:  Tt rows stacked on At rows.  Columns 16 ks .. 16 ks + 15 are one run of the 16 row
+//     octets, two matrices each, from octet 2 ks on (the first 2 ks octets of Tt are zero and
+//     not stored; those of At are stored, as the run goes on over them): few copies of some
+//     kilobytes, for a copy costs its issuing warp some 70 cycles whatever its size.
+//   backward: Tt, A as full squares, column octet by column octet, so that the same bytes serve
+//     as Tt and, read along the other axis, as Tt^T.
 #pragma once
 #include <cuda.h>
 
@@ -29,23 +33,24 @@ namespace ssd {
 namespace delta {
 
 constexpr int kChunk = 64;
-constexpr int kTri = 2 * 128 * (8 + 6 + 4 + 2);  // bytes of one lower triangle (5120)
 // e^gamma, e^(gamma_C - gamma), beta; then pairs gamma log2(e) as hi and lo
 constexpr int kGates = 5 * kChunk * 4;
-// image: gates, then [hi, lo][Tt, At]
-constexpr int kImgTri = kGates, kImgBytes = kGates + 4 * kTri;
-// run ks of a triangle: its first byte and its length
-__host__ __device__ constexpr int tri_run_bytes(int ks) { return (8 - 2 * ks) * 256; }
-__host__ __device__ constexpr int tri_run(int ks) { return 2048 * ks - 256 * ks * (ks - 1); }
-// the 16-byte piece of row i, columns 8 c .. 8 c + 7 (c / 2 <= i / 16)
-__host__ __device__ constexpr int tri_piece(int i, int c) {
-    return tri_run(c >> 1) + ((i >> 3) - (c & ~1)) * 256 + (c & 1) * 128 + (i & 7) * 16;
+// forward: run ks of a part: its first byte and its length; the 16-byte piece of row i (0 .. 127), columns 8 c .. + 7
+__host__ __device__ constexpr int run_bytes(int ks) { return (16 - 2 * ks) * 256; }
+__host__ __device__ constexpr int run_at(int ks) { return 4096 * ks - 256 * ks * (ks - 1); }
+constexpr int kPart = run_at(4);
+__host__ __device__ constexpr int run_piece(int i, int c) {
+    return run_at(c >> 1) + ((i >> 3) - (c & ~1)) * 256 + (c & 1) * 128 + (i & 7) * 16;
 }
-static_assert(tri_run(1) == 2048 && tri_run(2) == 3584 && tri_run(3) + tri_run_bytes(3) == kTri, "triangle runs");
+static_assert(kPart == 13312 && run_at(3) + run_bytes(3) == kPart, "runs");
+// backward: [Tt hi, Tt lo, A hi, A lo][8 column octets][8 row octets][128 bytes]
+constexpr int kSquare = 8192;
+__host__ __device__ constexpr int square_piece(int i, int c) { return c * 1024 + (i >> 3) * 128 + (i & 7) * 16; }
+// image: gates, then the parts or the squares
+constexpr int kImgMat = kGates, kImgFwd = kGates + 2 * kPart, kImgBwd = kGates + 4 * kSquare;
 
 // What the backward's kernels keep, per (b, h) chain and slice of 64 columns of P (chain-slice
 // cs = bh * nsl + slice).  Tiles are in the 128-byte swizzle, ready as operands.
-//   rev    [b, H, n]        Tt hi, A hi, Tt lo, A lo, each [64 rows][64 columns] (32 KB)
 //   states [cs, n]          S before every chunk: hi, lo parts [128 n][64] (32 KB)
 //   dstates [cs, n]         dS after every chunk: [128 n][64] (16 KB)
 //   errs   [cs, n]          Z: hi, lo parts [64 tokens][64] (16 KB)
@@ -60,17 +65,19 @@ static_assert(tri_run(1) == 2048 && tri_run(2) == 3584 && tri_run(3) + tri_run_b
 //     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n * 64]
 // and dbeta = zx.
 struct ChunkBackward {
-    char *rev, *states, *dstates, *errs, *dv_lo;
+    char *states, *dstates, *errs, *dv_lo;
     float *ss, *ww, *zx, *fq, *fk, *pe;
 };
 
 struct ChunkParams {
     DeltaParams p;
     int n;           // chunks
+    int img_bytes;   // kImgFwd or kImgBwd
     char *img;       // [b, H, n] images
     ChunkBackward w; // pointers are null in the forward
+    __host__ __device__ char *image(long long bh, int chunk) const { return img + (bh * n + chunk) * (long long)img_bytes; }
 };
-constexpr int kRevBytes = 32768, kStateTile = 32768, kDStateTile = 16384, kErrTile = 16384, kDvLoTile = 8192;
+constexpr int kStateTile = 32768, kDStateTile = 16384, kErrTile = 16384, kDvLoTile = 8192;
 __host__ __device__ __forceinline__ int slices_of(const DeltaParams &p) { return (p.P + 63) / 64; }
 
 inline bool chunk_supported(const delta_dims &d, ssd_dtype t) {

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         for (int it = 0; it < items && ok; ++it) {
             const uint32_t ph = it & 1;
             const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
-            const float *gates = (const float *)(cp.img + (bh * cp.n + chunk) * (long long)kImgBytes);
+            const float *gates = (const float *)cp.image(bh, chunk);
             if (tid < kChunk) {
                 sm.gam[tid] = __ldg((const float2 *)(gates + 3 * kChunk) + tid);
                 sm.beta[tid] = __ldg(gates + 2 * kChunk + tid);

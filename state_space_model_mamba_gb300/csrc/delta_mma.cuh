@@ -39,10 +39,10 @@ __device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// ---- descriptor of an operand kept without swizzle: 8x8 matrices of 128 contiguous bytes, the two
-// column octets of a K-step next to each other, row octets 256 bytes apart; K-steps 4096 (128 rows)
-__device__ __forceinline__ uint64_t sdesc_tri(uint32_t base) {
-    return (uint64_t)((base & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+// ---- descriptors of operands kept without swizzle (8x8 matrices of 128 contiguous bytes): lbo is the distance of
+// neighbouring matrices along K, sbo along M
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t base, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((base & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46;
 }
 // a descriptor moved by `bytes`
 __device__ __forceinline__ uint64_t sdesc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }

@@ -14,10 +14,9 @@
 // in registers.  Substitution stays accurate for repeated keys, where a power series
 // of the triangle would lose every digit.
 // What bounds it are the multiply-adds of the two solves, 2000 for each of the rows
-// 32 .. 63 and 500 for the others.  Rolled over the blocks: the whole substitution
-// unrolled (40 KB of code) waited for instructions half of the time.  The rows are
-// swapped by halves in every other block, so that the long ones do not always land on
-// the same two schedulers.
+// 32 .. 63 and 500 for the others (the backward needs A, not At, and solves half).  Rolled over the blocks: the whole substitution
+// unrolled (40 KB of code) waited for instructions half of the time.  Which
+// warps get the long rows changes from block to block.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -54,7 +53,10 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
     if (t0 >= V) return;
     const uint32_t kq = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t halves = p.N > 64 ? 2u : 1u;
-    const int flip = (blockIdx.x * 0x9E3779B1u) >> 31;  // tokens 32 .. 63 in rows (and columns) 0 .. 31
+    // where rows lie changes from block to block, so that the long solves do not always land on the same schedulers
+    const uint32_t hash = blockIdx.x * 0x9E3779B1u;
+    const int flip = hash >> 31;                          // tokens 32 .. 63 in rows (and columns) 0 .. 31
+    const uint32_t k_off = (hash >> 30 & 1) * 8192u;      // K rows behind the Q rows
     if (tid == 0) {
         mbar_init(&bar_load, 1);
         mbar_init(&bar_mma, 1);
@@ -63,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         for (uint32_t kb = 0; kb < halves; ++kb)
             for (int x = 0; x < 2; ++x) {
                 const int tok = t0 + 32 * (x ^ flip);
-                tma_tile(kq + kb * 16384u + 4096u * x, &maps.k, &bar_load, 64 * kb, grp, tok, bi);
-                tma_tile(kq + kb * 16384u + 8192u + 4096u * x, &maps.q, &bar_load, 64 * kb, grp, tok, bi);
+                tma_tile(kq + kb * 16384u + k_off + 4096u * x, &maps.k, &bar_load, 64 * kb, grp, tok, bi);
+                tma_tile(kq + kb * 16384u + (k_off ^ 8192u) + 4096u * x, &maps.q, &bar_load, 64 * kb, grp, tok, bi);
             }
     }
     if (warp == 0) tmem_alloc(&s_tmem, kAccCols);
@@ -78,17 +80,17 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         if (ok && lane == 0) {
             const int nks = (p.N + 15) / 16;
             for (int ks = 0; ks < nks; ++ks)
-                mma_bf16(tm, sdesc_kmajor(kq, ks, 16384), sdesc_kmajor(kq, ks, 16384), idesc_bf16(128, 64, false, false), ks > 0);
+                mma_bf16(tm, sdesc_kmajor(kq, ks, 16384), sdesc_kmajor(kq + k_off, ks, 16384), idesc_bf16(128, 64, false, false), ks > 0);
             mma_commit(&bar_mma);
         }
         __syncwarp();
     }
     const int i = (tid & 63) ^ (32 * flip);  // the row's token
-    const bool keys = tid < kChunk, live = t0 + i < V;  // rows of absent tokens may hold anything: made zero
+    const bool keys = (tid < kChunk) == (k_off == 0), live = t0 + i < V;  // rows of absent tokens may hold anything: made zero
     const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * kHeadsPer);
     for (int h = grp * p.hpg + slice * kHeadsPer; h < h_end; ++h) {
         const long long bh = (long long)bi * p.H + h;
-        char *img = cp.img + (bh * cp.n + chunk) * (long long)kImgBytes;
+        char *img = cp.image(bh, chunk);
         if (warp == 0) {
             // gamma in fp64, kept as hi + lo: differences of it stay exact to fp32 after strong decays
             const int i0 = 2 * lane;
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         // 16 columns of D o (row of K K^T or Q K^T), zero where j >= i (keys) or j > i
         auto decayed = [&](int jb, float f, float (&r)[16]) {
             float a[16];
+            __syncwarp();  // the lanes' rows end at different columns
             tmem_ld16(tmem_addr(tm, 32 * warp, (16 * jb) ^ (32 * flip)), a);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -144,17 +147,32 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         __syncthreads();
         // z[m][row] = beta_m y_m of this thread's row, over the tiles (which the products have read)
         float *z = (float *)(smem_raw + (kq - smem_u32(smem_raw))) + tid;
-        char *tri = img + kImgTri + (keys ? 0 : kTri);
-        // the reverse pass's full squares (Tt hi, A hi, Tt lo, A lo)
-        char *rev = cp.w.rev ? cp.w.rev + (bh * cp.n + chunk) * (long long)kRevBytes : nullptr;
-        auto store_rev = [&](char *sq, int jb, const float2 *y) {
-            store_parts8(sq, 16384, i, 2 * jb, y);
-            store_parts8(sq, 16384, i, 2 * jb + 1, y + 4);
+        const bool bwd = cp.w.states != nullptr;
+        char *mat = img + kImgMat + (bwd && !keys ? 2 * kSquare : 0);
+        auto store_block = [&](int jb, const float2 *y) {  // hi and lo parts, neighbouring rows on neighbouring addresses
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(y[4 * c + e].x, y[4 * c + e].y, hi[e], lo[e]);
+                char *dst = mat + (bwd ? square_piece(i, 2 * jb + c) : run_piece(i + (keys ? 0 : kChunk), 2 * jb + c));
+                *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(dst + (bwd ? kSquare : kPart)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         };
-        if (rev && last == 1) {
-            const float2 zero[8] = {};
-            for (int jb = 2; jb < 4; ++jb) store_rev(rev + (keys ? 0 : 8192), jb, zero);
-        }
+        // blocks above the diagonal that are stored: zeros
+        for (int jb = (i >> 4) + 1; jb < 4; ++jb)
+            if (bwd || !keys) {
+                const float2 zero[8] = {};
+                store_block(jb, zero);
+            }
+        if (bwd && !keys) {  // the backward takes A itself
+            for (int jb = 0; jb <= last; ++jb) {
+                float2 y[8];
+                decayed(jb, p.scale, (float(&)[16])y);
+                if (jb <= (i >> 4)) store_block(jb, y);
+            }
+        } else
         for (int jb = last; jb >= 0; --jb) {
             float2 y[8];
             if (keys) {
@@ -166,7 +184,6 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 }
             } else {
                 decayed(jb, p.scale, (float(&)[16])y);
-                if (rev) store_rev(rev + 8192, jb, y);  // A itself
             }
             const float *e0 = s_e + 16 * jb;
 #pragma unroll 4
@@ -196,18 +213,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                     if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
                 }
             }
-            if (rev && keys) store_rev(rev, jb, y);
-            // hi and lo parts: 16-byte pieces, neighbouring rows on neighbouring addresses
-            if (jb <= (i >> 4))
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(y[4 * c + e].x, y[4 * c + e].y, hi[e], lo[e]);
-                    char *dst = tri + tri_piece(i, 2 * jb + c);
-                    *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *(uint4 *)(dst + 2 * kTri) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
+            if (jb <= (i >> 4)) store_block(jb, y);
         }
         __syncthreads();  // s_e and the gates may be written for the next head
     }

@@ -46,7 +46,7 @@ constexpr int kSMs = 152;
 constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128 each; X and W in their place
 constexpr uint32_t kOffX = 0, kOffW = 16384;
 // narrow slices: hi and lo parts side by side in the rows of one tile
-constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][16 row octets][2][128 bytes]: Tt rows, then At rows
+constexpr uint32_t kOffTri = 32768;        // [hi, lo][ks][16 row octets][2][128 bytes]: Tt rows, then At rows; or squares
 constexpr uint32_t kOffV = 65536;          // [64 tokens][64] SW128
 constexpr uint32_t kOffKQ = 73728;         // NB x [2 column halves][K 64 rows, Q 64 rows][64] SW128
 constexpr uint32_t kKQBytes = 32768;
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     constexpr int kCompute = compute_threads(W), kScanThreads = scan_threads(W);
     static_assert(!BWD || W == 64, "the backward's tiles have 64 columns");
+    constexpr bool kBeside = NB > 1;
     const int nsl = (p.P + W - 1) / W, slice = blockIdx.x % nsl, bh = blockIdx.x / nsl, bi = bh / p.H, h = bh % p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
-    const char *img0 = cp.img + (long long)bh * cp.n * (long long)kImgBytes;
     if (tid == 0) {
         mbar_init(&bar_kq[0], 1);
         mbar_init(&bar_kq[1], 1);
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         s_err = 0;
     }
     if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
-    // the row octets of the triangles that no copy writes are zero
-    for (int i = tid; i < 32768 / 16; i += kScanThreads) st_shared_v4(base + kOffTri + 16 * i, 0, 0, 0, 0);
+    // the row octets of Tt that no copy writes are zero
+    for (int i = tid; !BWD && i < 32768 / 16; i += kScanThreads) st_shared_v4(base + kOffTri + 16 * i, 0, 0, 0, 0);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         const uint32_t i1 = idesc_bf16(128, 2 * W, false, true), i2 = idesc_bf16(128, W, false, true),
                        i3 = idesc_bf16(128, 2 * W, true, true);
         const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
-                       dW = sdesc(base + kOffW, 8192, 1024), dT = sdesc_tri(base + kOffTri);
+                       dW = sdesc(base + kOffW, 8192, 1024), dT = BWD ? sdesc_plain(base + kOffTri, 1024, 128) : sdesc_plain(base + kOffTri, 128, 256);
         bool ok = true;
         int done = 0;
         for (int c = 0; c < nv; ++c) {
@@ -148,20 +148,17 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
-                if (W == 64) {
+                // Tt hi X hi and Tt hi X lo (side by side where the threads have the registers to add them), Tt lo X hi
 #pragma unroll
-                    for (int pass = 0; pass < 3; ++pass)
+                for (int pass = kBeside ? 1 : 0; pass < 3; ++pass)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16(tm, sdesc_add(dT, (pass == 2 ? 16384 : 0) + ks * 4096),
-                                     sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i2, true);
-                } else {  // the products with X lo in the columns behind
-#pragma unroll
-                    for (int pass = 0; pass < 2; ++pass)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16(tm, sdesc_add(dT, pass * 16384 + ks * 4096), sdesc_add(dX, ks * 2048), pass ? i2 : i1, true);
-                }
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t at = BWD ? (pass == 2) * kSquare + ks * 2048 : (pass == 2) * 16384 + ks * 4096;
+                        if (kBeside)
+                            mma_bf16(tm, sdesc_add(dT, at), sdesc_add(dX, ks * 2048), pass == 2 ? i2 : i1, true);
+                        else
+                            mma_bf16(tm, sdesc_add(dT, at), sdesc_add(dX, (pass == 1) * 8192 + ks * 2048), i2, true);
+                    }
                 mma_commit(&bar_m[1]);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph));
@@ -184,22 +181,27 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         const int vcol = slice * W / 64 * 64;  // V comes in tiles of 64 columns
         int kq_issued = 0, tri_issued = 0, v_issued = 0;
         auto expect_kq = [&](int c) {
-            if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], halves * 16384u);
+            if (lane == 0) mbar_arrive_expect_tx(&bar_kq[c % NB], halves * (BWD ? 8192u : 16384u));
             kq_issued = c + 1;
         };
         auto load_rows = [&](int c, const CUtensorMap *m, uint32_t off) {
-            if (lane == 0)
+            if (lane == 0 && !(BWD && off))  // the backward needs no outputs, hence no Q
                 for (uint32_t kb = 0; kb < halves; ++kb)
                     tma_tile(base + kOffKQ + (c % NB) * kKQBytes + kb * 16384u + off, m, &bar_kq[c % NB], 64 * kb, grp, c * kChunk, bi);
         };
         auto load_tri = [&](int c) {
-            if (lane == 0) mbar_arrive_expect_tx(&bar_tri, 4 * kTri);
-            __syncwarp();
-            if (lane < 16) {
-                const int part = lane >> 3, which = (lane >> 2) & 1, ks = lane & 3;
-                bulk_load(base + kOffTri + part * 16384 + ks * 4096 + which * 2048 + 2 * ks * 256,
-                          img0 + (long long)c * kImgBytes + kImgTri + (2 * part + which) * kTri + tri_run(ks), tri_run_bytes(ks),
-                          &bar_tri);
+            const char *mat = cp.image(bh, c) + kImgMat;
+            if (BWD) {  // both parts of Tt; its rows 64 .. 127, of which nothing is read, are what comes behind
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar_tri, 2 * kSquare);
+                    bulk_load(base + kOffTri, mat, 2 * kSquare, &bar_tri);
+                }
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(&bar_tri, 2 * kPart);
+                __syncwarp();
+                const int part = lane >> 2, ks = lane & 3;
+                if (lane < 8)
+                    bulk_load(base + kOffTri + part * 16384 + ks * 4096 + ks * 512, mat + part * kPart + run_at(ks), run_bytes(ks), &bar_tri);
             }
             tri_issued = c + 1;
         };
@@ -236,11 +238,11 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             const uint32_t ph = c & 1;
             if (!(ok = keep(c))) break;
             if (lane == 0) {  // what the next chunk reads, into L2
-                prefetch_bulk(img0 + (long long)(c + 1) * kImgBytes, kImgBytes);
+                prefetch_bulk(cp.image(bh, c + 1), BWD ? kImgMat + 2 * kSquare : kImgFwd);
                 if (c + NB < nv)
                     for (uint32_t kb = 0; kb < halves; ++kb) {
                         prefetch_tile(&maps.k, 64 * kb, grp, (c + NB) * kChunk, bi);
-                        prefetch_tile(&maps.q, 64 * kb, grp, (c + NB) * kChunk, bi);
+                        if (!BWD) prefetch_tile(&maps.q, 64 * kb, grp, (c + NB) * kChunk, bi);
                     }
                 prefetch_tile(&maps.v, vcol, h, (c + 1) * kChunk, bi);
             }
@@ -293,22 +295,32 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         {
             float2 S[8];
             load_piece(S, p.init ? p.init + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
+            __syncwarp();
             tmem_st16(ts, (const float *)S);
             if (nv > 0) publish_piece<W>(base + kOffS, row, group, S);
             tmem_wait_st();
             if (nv > 0) published(0);
         }
+        float gn[4] = {0.f, 0.f, 0.f, 0.f};  // the next chunk's gates
+        auto load_gates = [&](int c) {
+            const float *gates = (const float *)cp.image(bh, c);
+            gn[0] = __ldg(gates + i);
+            gn[1] = __ldg(gates + 2 * kChunk + i);
+            gn[2] = __ldg(gates + kChunk + i);
+            gn[3] = __ldg(gates + kChunk - 1);
+        };
+        if (NB > 1 && nv > 0) load_gates(0);
         for (int c = 0; c < nv && ok; ++c) {
             const uint32_t ph = c & 1;
-            const float *gates = (const float *)(img0 + (long long)c * kImgBytes);
-            const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
-            const float ec = __ldg(gates + kChunk - 1);
+            if (NB == 1) load_gates(c);  // (ahead they would take registers that two blocks per SM do not have)
+            const float eg = gn[0], be = gn[1], et = gn[2], ec = gn[3];
+            if (NB > 1 && c + 1 < nv) load_gates(c + 1);
             const int tok = c * kChunk + i;
             const bool live = tok < V, partial = V - c * kChunk < kChunk;
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph) && (!BWD || mbar_wait(&bar_kept, ph)));
             if (!ok) break;
             tc_fence_after();
-            {
+            if (keys || !BWD) {
                 float2 a[8], b[8];
                 tmem_ld16x2(ta, tb, (float *)a, (float *)b);
 #pragma unroll
@@ -334,13 +346,13 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
                     for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
                 }
                 tmem_st16(ta, (const float *)a);
-                if (W < 64) {
+                if (kBeside) {
                     const float zero[16] = {};
                     tmem_st16(tb, zero);
                 }
+                tmem_wait_st();
+                if (keys) fence_async_smem();
             }
-            tmem_wait_st();
-            fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_x);
@@ -350,12 +362,12 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             tc_fence_after();
             {
                 float2 a[8];
-                if (W < 64) {
+                if (kBeside) {
                     float2 b[8];
-                    tmem_ld16x2(ta, tb, (float *)a, (float *)b);
+                    if (keys || !BWD) tmem_ld16x2(ta, tb, (float *)a, (float *)b);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
-                } else {
+                } else if (keys || !BWD) {
                     tmem_ld16(ta, (float *)a);
                 }
                 if (keys) {
@@ -396,6 +408,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
                 if (c + 1 < nv) publish_piece<W>(base + kOffS, row, group, S);
+                __syncwarp();
                 tmem_st16(ts, (const float *)S);
                 tmem_wait_st();
                 if (c + 1 < nv) published(c + 1);
@@ -409,6 +422,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         }
         if (ok && p.final_state) {
             float2 S[8];
+            __syncwarp();
             tmem_ld16(ts, (float *)S);
             store_piece(S, p.final_state + (long long)bh * p.P * p.N, row, col, p.P, p.N);
         }
@@ -429,18 +443,25 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 //   3.  K^T (-e^gamma dV) + Q^T D       -> dS = e^gamma_C dS + ...
 // and, with what the forward kept, the sums that the gates' gradients are made of
 // (delta_chunk.cuh).
-constexpr uint32_t kOffRev = 32768;        // Tt hi, A hi, Tt lo, A lo: [64][64] SW128 each
+// One block per SM, with everything that a step reads in flight a step ahead: two sets of
+// every tile, D in a place of its own, and Q^T D in an accumulator of its own, formed
+// while the chain waits for its threads.  Two blocks per SM (single tiles, 56 registers a
+// thread) took as long for two chains as this takes for two in turn.  The forward's S and Z
+// read where they are used cost 2 us of a step's 5: Z comes by copy, S into registers, a step ahead.
+constexpr uint32_t kOffX2 = 0, kOffW2 = 16384;                   // in the state's place, as in the forward
+constexpr uint32_t kRevTri = 32768, kRevDO = kRevTri + 2 * 32768, kRevD = kRevDO + 2 * 8192, kRevKQ = kRevD + 16384,
+                   kRevZ = kRevKQ + 2 * kKQBytes, kRevBytes = kRevZ + kErrTile;
+static_assert(kRevBytes + 2048 <= 232448, "shared memory of the reverse scan");
 struct RevMaps {
     CUtensorMap k, q, d_o;
 };
 
-template <int NB>
-__global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
+__global__ void __launch_bounds__(scan_threads(64), 1)
     delta_scan_rev(const ChunkParams cp, const __grid_constant__ RevMaps maps) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_kq[2], bar_rev, bar_do;              // copies have landed
+    __shared__ uint64_t bar_in[2], bar_z;                        // a step's copies have landed
     __shared__ uint64_t bar_s, bar_x, bar_w;                     // operands are written (by every compute warp)
-    __shared__ uint64_t bar_m[3];                                // products are done
+    __shared__ uint64_t bar_m[3], bar_d;                         // products are done; D is written
     __shared__ uint64_t bar_kept;                                // the backward's copy of S has been taken
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
@@ -451,19 +472,20 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = valid_tokens(p, bi), nv = (V + kChunk - 1) / kChunk, nks = (p.N + 15) / 16;
     if (tid == 0) {
-        mbar_init(&bar_kq[0], 1);
-        mbar_init(&bar_kq[1], 1);
-        mbar_init(&bar_rev, 1);
-        mbar_init(&bar_do, 1);
+        mbar_init(&bar_in[0], 1);
+        mbar_init(&bar_in[1], 1);
+        mbar_init(&bar_z, 1);
         mbar_init(&bar_s, kCompute / 32);
         mbar_init(&bar_x, kCompute / 32);
         mbar_init(&bar_w, kCompute / 32);
         for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
         mbar_init(&bar_kept, 1);
+        mbar_init(&bar_d, kCompute / 64);
         mbar_fence_init();
         s_err = 0;
     }
-    if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
+    constexpr uint32_t kCols = 512, kAcc3 = 256;
+    if (warp == 0) tmem_alloc(&s_tmem, kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -473,24 +495,26 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
         // ---- products; step r is chunk nv - 1 - r
         const uint32_t i0 = idesc_bf16(128, 64, true, true), i1 = idesc_bf16(128, 128, false, true),
                        i3 = idesc_bf16(128, 128, true, true);
-        const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
-                       dW = sdesc(base + kOffW, 8192, 1024), dR = sdesc(base + kOffRev, 8192, 1024),
-                       dO = sdesc(base + kOffV, 8192, 1024);
+        const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX2, 8192, 1024),
+                       dW = sdesc(base + kOffW2, 8192, 1024), dD = sdesc(base + kRevD, 8192, 1024);
         bool ok = true;
         int done = 0;
         auto own = [&](int r) {  // A^T dO of step r
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_rev, r & 1) && mbar_wait(&bar_do, r & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_in[r & 1], (r >> 1) & 1));
             if (!ok || lane) return;
+            const uint64_t dA = sdesc_plain(base + kRevTri + (r & 1) * 32768 + 2 * kSquare, 128, 1024),
+                           dO = sdesc(base + kRevDO + (r & 1) * 8192, 8192, 1024);
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tm + 128, sdesc_add(dR, 8192 + part * 16384 + ks * 2048), sdesc_add(dO, ks * 2048), i0, part > 0 || ks > 0);
+                    mma_bf16(tm + 128, sdesc_add(dA, part * kSquare + ks * 256), sdesc_add(dO, ks * 2048), i0, part > 0 || ks > 0);
         };
         for (int r = 0; r < nv; ++r) {
-            const uint32_t ph = r & 1, kq = base + kOffKQ + (r % NB) * kKQBytes;
-            const uint64_t dK = sdesc(kq, 16, 1024), dKt = sdesc(kq, 16384, 1024), dQt = sdesc(kq + 8192, 16384, 1024);
-            ok = mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_s, ph);
+            const uint32_t ph = r & 1, kq = base + kRevKQ + (r & 1) * kKQBytes;
+            const uint64_t dK = sdesc(kq, 16, 1024), dKt = sdesc(kq, 16384, 1024), dQt = sdesc(kq + 8192, 16384, 1024),
+                           dT = sdesc_plain(base + kRevTri + (r & 1) * 32768, 128, 1024);
+            ok = mbar_wait(&bar_in[r & 1], (r >> 1) & 1) && mbar_wait(&bar_s, ph);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (r == 0) own(0);  // after the rows of absent tokens have been made zero
@@ -500,24 +524,28 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
                     if (ks < nks) mma_bf16(tm, sdesc_add(dK, (ks >> 2) * 16384 + (ks & 3) * 32), sdesc_add(dS, ks * 2048), i1, ks > 0);
                 mma_commit(&bar_m[0]);
             }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_d, ph)))) break;
+            tc_fence_after();
+            if (lane == 0)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + kAcc3, sdesc_add(dQt, ks * 2048), sdesc_add(dD, ks * 2048), i3, ks > 0);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
             tc_fence_after();
             if (lane == 0) {
+                // the products with (beta dU) lo in the columns behind
 #pragma unroll
-                for (int pass = 0; pass < 3; ++pass)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm, sdesc_add(dR, (pass == 2 ? 16384 : 0) + ks * 2048),
-                                 sdesc_add(dX, (pass == 1 ? 8192 : 0) + ks * 2048), i0, true);
+                        mma_bf16(tm, sdesc_add(dT, part * kSquare + ks * 256), sdesc_add(dX, ks * 2048), part ? i0 : i3, true);
                 mma_commit(&bar_m[1]);
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph)))) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, ks > 0);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dQt, ks * 2048), sdesc_add(dX, ks * 2048), i3, true);
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tm + kAcc3, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, true);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
@@ -532,39 +560,31 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
         // ---- copies
         const int grp = h / p.hpg;
         const uint32_t halves = p.N > 64 ? 2u : 1u;
-        int kq_issued = 0, do_issued = 0, rev_issued = 0;
-        auto load_kq = [&](int r) {
+        int issued = 0, z_issued = 0;
+        auto load_z = [&](int r) {
             if (lane == 0) {
-                uint64_t *bar = &bar_kq[r % NB];
-                const uint32_t dst = base + kOffKQ + (r % NB) * kKQBytes;
-                const int t0 = (nv - 1 - r) * kChunk;
-                mbar_arrive_expect_tx(bar, halves * 16384u);
+                mbar_arrive_expect_tx(&bar_z, kErrTile);
+                bulk_load(base + kRevZ, cp.w.errs + ((long long)blockIdx.x * cp.n + nv - 1 - r) * kErrTile, kErrTile, &bar_z);
+            }
+            z_issued = r + 1;
+        };
+        auto load = [&](int r) {
+            if (lane == 0) {
+                uint64_t *bar = &bar_in[r & 1];
+                const int c = nv - 1 - r, t0 = c * kChunk;
+                const uint32_t kq = base + kRevKQ + (r & 1) * kKQBytes;
+                mbar_arrive_expect_tx(bar, halves * 16384u + 4 * kSquare + 8192);
+                tma_tile(base + kRevDO + (r & 1) * 8192, &maps.d_o, bar, 64 * slice, h, t0, bi);
+                bulk_load(base + kRevTri + (r & 1) * 32768, cp.image(bh, c) + kImgMat, 4 * kSquare, bar);
                 for (uint32_t kb = 0; kb < halves; ++kb) {
-                    tma_tile(dst + kb * 16384u, &maps.k, bar, 64 * kb, grp, t0, bi);
-                    tma_tile(dst + kb * 16384u + 8192u, &maps.q, bar, 64 * kb, grp, t0, bi);
+                    tma_tile(kq + kb * 16384u, &maps.k, bar, 64 * kb, grp, t0, bi);
+                    tma_tile(kq + kb * 16384u + 8192u, &maps.q, bar, 64 * kb, grp, t0, bi);
                 }
             }
-            kq_issued = r + 1;
+            issued = r + 1;
         };
-        auto load_rev = [&](int r) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar_rev, kRevBytes);
-                bulk_load(base + kOffRev, cp.w.rev + ((long long)bh * cp.n + nv - 1 - r) * kRevBytes, kRevBytes, &bar_rev);
-            }
-            rev_issued = r + 1;
-        };
-        auto load_do = [&](int r) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar_do, 8192);
-                tma_tile(base + kOffV, &maps.d_o, &bar_do, 64 * slice, h, (nv - 1 - r) * kChunk, bi);
-            }
-            do_issued = r + 1;
-        };
-        for (int r = 0; r < NB && r < nv; ++r) load_kq(r);
-        if (nv > 0) {
-            load_rev(0);
-            load_do(0);
-        }
+        for (int r = 0; r < 2 && r < nv; ++r) load(r);
+        if (nv > 0) load_z(0);
         bool ok = true;
         auto keep = [&](int r) {  // the hi part of dS after the chunk, from the operand
             if (!__all_sync(0xffffffffu, mbar_wait(&bar_s, r & 1))) return false;
@@ -583,50 +603,51 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
             if (lane == 0) {  // what the next step reads, into L2
                 const int c = nv - 2 - r;
                 const long long at = (long long)blockIdx.x * cp.n + c;
-                prefetch_bulk(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes, kGates);
-                prefetch_bulk(cp.w.rev + ((long long)bh * cp.n + c) * kRevBytes, kRevBytes);
-                prefetch_bulk(cp.w.states + at * kStateTile, kStateTile);
-                prefetch_bulk(cp.w.errs + at * kErrTile, kErrTile);
-                prefetch_tile(&maps.d_o, 64 * slice, h, c * kChunk, bi);
-                if (r + NB < nv)
+                prefetch_bulk(cp.image(bh, c), kGates);
+                if (r + 2 < nv) {
+                    prefetch_bulk(cp.w.states + (at - 1) * kStateTile, kStateTile);
+                    prefetch_bulk(cp.w.errs + (at - 1) * kErrTile, kErrTile);
+                }
+                if (r + 3 < nv) {
+                    const int c3 = c - 2;
+                    prefetch_bulk(cp.image(bh, c3), kImgBwd);
+                    prefetch_tile(&maps.d_o, 64 * slice, h, c3 * kChunk, bi);
                     for (uint32_t kb = 0; kb < halves; ++kb) {
-                        prefetch_tile(&maps.k, 64 * kb, grp, (nv - 1 - r - NB) * kChunk, bi);
-                        prefetch_tile(&maps.q, 64 * kb, grp, (nv - 1 - r - NB) * kChunk, bi);
+                        prefetch_tile(&maps.k, 64 * kb, grp, c3 * kChunk, bi);
+                        prefetch_tile(&maps.q, 64 * kb, grp, c3 * kChunk, bi);
                     }
+                }
             }
-            // dO, and by the products the matrices, have been read
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph)))) break;
-            load_rev(r + 1);
-            load_do(r + 1);
-            if (r + NB < nv) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
+            load_z(r + 1);  // Z has been read
+            if (r + 2 < nv) {  // the products of this step have read its tiles
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
-                load_kq(r + NB);
+                load(r + 2);
             }
         }
         if (ok && nv > 0) ok = keep(nv - 1);
         if (lane == 0) bulk_wait_all();
         if (!ok) s_err = 1;
         // every copy has to land before the block may end
-        for (int r = max(0, kq_issued - NB); r < kq_issued; ++r) mbar_wait(&bar_kq[r % NB], (r / NB) & 1);
-        if (rev_issued) mbar_wait(&bar_rev, (rev_issued - 1) & 1);
-        if (do_issued) mbar_wait(&bar_do, (do_issued - 1) & 1);
+        for (int r = max(0, issued - 2); r < issued; ++r) mbar_wait(&bar_in[r & 1], (r >> 1) & 1);
+        if (z_issued) mbar_wait(&bar_z, (z_issued - 1) & 1);
     } else {
         const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // these threads form dU and X; the others D
         const int i = row & 63, col = slice * 64 + 16 * group;
-        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + 64, tu = ta + 128, ts = ta + 192;
+        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + 64, tu = ta + 128, ts = ta + 192, t3 = ta + kAcc3;
         const float2 one = make_float2(1.f, 1.f);
         bool ok = true;
         // the operand of step r is written; in the first, K, Q and dO rows of absent tokens are made zero
         auto published = [&](int r) {
             const int live = V - (nv - 1 - r) * kChunk;
             if (live < kChunk) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar_kq[r % NB], (r / NB) & 1) && mbar_wait(&bar_do, r & 1));
-                const uint32_t kq = base + kOffKQ + (r % NB) * kKQBytes;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_in[r & 1], (r >> 1) & 1));
+                const uint32_t kq = base + kRevKQ + (r & 1) * kKQBytes;
                 for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
                     if (((x >> 3) & 63) >= live) st_shared_v4(kq + x * 16u, 0, 0, 0, 0);
                 for (int x = tid; x < kChunk * 8; x += kCompute)
-                    if ((x >> 3) >= live) st_shared_v4(base + kOffV + x * 16u, 0, 0, 0, 0);
+                    if ((x >> 3) >= live) st_shared_v4(base + kRevDO + (r & 1) * 8192 + x * 16u, 0, 0, 0, 0);
             }
             fence_async_smem();
             tc_fence_before();
@@ -636,48 +657,82 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
         {
             float2 S[8];
             load_piece(S, p.d_final ? p.d_final + (long long)bh * p.P * p.N : nullptr, row, col, p.P, p.N);
+            __syncwarp();
             tmem_st16(ts, (const float *)S);
             if (nv > 0) publish_piece<64>(base + kOffS, row, group, S);
             tmem_wait_st();
             if (nv > 0) published(0);
         }
+        float gn[4] = {0.f, 0.f, 0.f, 0.f};  // the next step's gates
+        auto load_gates = [&](int c) {
+            if (c < 0) return;
+            const float *gates = (const float *)cp.image(bh, c);
+            gn[0] = __ldg(gates + i);
+            gn[1] = __ldg(gates + 2 * kChunk + i);
+            gn[2] = __ldg(gates + kChunk + i);
+            gn[3] = __ldg(gates + kChunk - 1);
+        };
+        load_gates(nv - 1);
+        uint4 sr[4];                         // and S before its chunk, this thread's 16 columns: hi, lo parts
+        auto load_s = [&](int c) {
+            if (c < 0) return;
+            const char *tile = cp.w.states + ((long long)blockIdx.x * cp.n + c) * kStateTile;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const char *src = tile + sw128_chunk(row, 2 * group + u);
+                sr[u] = __ldg((const uint4 *)src);
+                sr[2 + u] = __ldg((const uint4 *)(src + 16384));
+            }
+        };
+        load_s(nv - 1);
         for (int r = 0; r < nv && ok; ++r) {
             const int c = nv - 1 - r;
             const uint32_t ph = r & 1;
             const long long cc = (long long)blockIdx.x * cp.n + c;
-            const float *gates = (const float *)(cp.img + ((long long)bh * cp.n + c) * (long long)kImgBytes);
-            const float eg = __ldg(gates + i), be = __ldg(gates + 2 * kChunk + i), et = __ldg(gates + kChunk + i);
-            const float ec = __ldg(gates + kChunk - 1);
+            const float eg = gn[0], be = gn[1], et = gn[2], ec = gn[3];
+            load_gates(c - 1);
             const int tok = c * kChunk + i;
-            float2 z[8];  // Z, for the rows of the chain
-            if (keys) {
-                const char *err = cp.w.errs + cc * kErrTile;
+            if (!keys) {  // D = scale e^gamma dO (bar_s: the rows of absent tokens are zero)
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_in[r & 1], (r >> 1) & 1) && mbar_wait(&bar_s, ph));
+                const float f = p.scale * eg;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const char *src = err + sw128_chunk(i, 2 * group + u);
-                    join8(__ldg((const uint4 *)src), __ldg((const uint4 *)(src + 8192)), z + 4 * u);
+                for (int x = 0; x < 2; ++x) {
+                    const uint4 w = ld_shared_v4(base + kRevDO + (r & 1) * 8192 + sw128_chunk(i, 2 * group + x));
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    float2 d[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = fmul2(bf2_to_f2(v[e]), make_float2(f, f));
+                    store_parts8(base + kRevD, base + kRevD + 8192, i, 2 * group + x, d);
                 }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_d);
             }
             // e^gamma_C <S, dS>, while the products run
             {
-                const char *tile = cp.w.states + cc * kStateTile;
                 float2 S[8];
+                __syncwarp();  // lane 0 has announced the operand
                 tmem_ld16(ts, (float *)S);
                 float sum = 0.f;
-                if (row < p.N)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const char *src = tile + sw128_chunk(row, 2 * group + u);
-                        sum = dot8(__ldg((const uint4 *)src), S + 4 * u, sum);
-                        sum = dot8(__ldg((const uint4 *)(src + 16384)), S + 4 * u, sum);
-                    }
+                for (int u = 0; u < 4; ++u) sum = dot8(sr[u], S + 4 * (u & 1), sum);
+                load_s(c - 1);
+                if (row >= p.N) sum = 0.f;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (lane == 0) cp.w.ss[cc * 16 + warp] = ec * sum;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_kept, ph));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_kept, ph) && mbar_wait(&bar_z, ph));
             if (!ok) break;
             tc_fence_after();
+            float2 z[8];
+            if (keys) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t at = base + kRevZ + sw128_chunk(i, 2 * group + u);
+                    join8(ld_shared_v4(at), ld_shared_v4(at + 8192), z + 4 * u);
+                }
+            }
             float2 ww = make_float2(0.f, 0.f);
             if (keys) {
                 float2 a[8], b[8], u[8];
@@ -693,9 +748,11 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
                     float2 xb[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) xb[e] = fmul2(a[4 * x + e], make_float2(be, be));
-                    store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + x, xb);
+                    store_parts8(base + kOffX2, base + kOffX2 + 8192, i, 2 * group + x, xb);
                 }
                 tmem_st16(ta, (const float *)a);
+                const float zero[16] = {};
+                tmem_st16(tb, zero);
                 tmem_wait_st();
                 fence_async_smem();
             }
@@ -703,19 +760,21 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_x);
 
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph) && mbar_wait(&bar_do, ph));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
             if (!ok) break;
             tc_fence_after();
             if (keys) {
-                float2 a[8];
-                tmem_ld16(ta, (float *)a);
+                float2 a[8], b[8];
+                tmem_ld16x2(ta, tb, (float *)a, (float *)b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[e] = ffma2(b[e], one, a[e]);
                 const float f = -eg * be;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float2 w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * x + e], make_float2(f, f));
-                    store_parts8(base + kOffW, base + kOffW + 8192, i, 2 * group + x, w);
+                    store_parts8(base + kOffW2, base + kOffW2 + 8192, i, 2 * group + x, w);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -741,18 +800,6 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
                 cp.w.zx[sat] = zx.x + zx.y;
                 cp.w.ww[sat] = be * (ww.x + ww.y);
             } else {
-                // D = scale e^gamma dO in place of beta dU
-                const float f = p.scale * eg;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint4 w = ld_shared_v4(base + kOffV + sw128_chunk(i, 2 * group + x));
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                    float2 d[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = fmul2(bf2_to_f2(v[e]), make_float2(f, f));
-                    store_parts8(base + kOffX, base + kOffX + 8192, i, 2 * group + x, d);
-                }
-                fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_w);
@@ -762,10 +809,11 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
             tc_fence_after();
             {
                 float2 a[8], b[8], S[8];
-                tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
+                tmem_ld16x3(t3, t3 + 64, ts, (float *)a, (float *)b, (float *)S);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
                 if (r + 1 < nv) publish_piece<64>(base + kOffS, row, group, S);
+                __syncwarp();
                 tmem_st16(ts, (const float *)S);
                 tmem_wait_st();
                 if (r + 1 < nv) published(r + 1);
@@ -780,6 +828,7 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
         }
         if (ok && p.d_init) {
             float2 S[8];
+            __syncwarp();
             tmem_ld16(ts, (float *)S);
             store_piece(S, p.d_init + (long long)bh * p.P * p.N, row, col, p.P, p.N);
         }
@@ -788,7 +837,7 @@ __global__ void __launch_bounds__(scan_threads(64), NB == 1 ? 2 : 1)
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, kTmemCols);
+    if (warp == 0) tmem_dealloc(tm, kCols);
 }
 
 }  // namespace
@@ -826,11 +875,9 @@ cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * slices_of(p));
-    const bool one_per_sm = grid <= kSMs;
-    auto kernel = one_per_sm ? delta_scan_rev<2> : delta_scan_rev<1>;
-    const int bytes = 1024 + (int)kOffKQ + (one_per_sm ? 2 : 1) * (int)kKQBytes;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    kernel<<<grid, scan_threads(64), bytes, s>>>(c, maps);
+    const int bytes = 1024 + (int)kRevBytes;
+    if ((e = cudaFuncSetAttribute(delta_scan_rev, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    delta_scan_rev<<<grid, scan_threads(64), bytes, s>>>(c, maps);
     return cudaGetLastError();
 }
 
