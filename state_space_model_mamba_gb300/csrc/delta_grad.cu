@@ -105,6 +105,25 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 prefetch_bulk(cp.w.dstates + (cs * cp.n + chunk) * kDStateTile, kDStateTile);
             }
         };
+        // into L2, ahead: the block's next item, or the first of the block that will follow here
+        auto prefetch_in = [&](int it) {
+            long long cs, ck = chunk;
+            if (it < items) {
+                cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
+            } else {
+                const long long blk = blockIdx.x + 2LL * 152;
+                if (blk >= (long long)gridDim.x) return;
+                ck = blk % cp.n;
+                const long long hd = blk / cp.n / p.G * p.H + blk / cp.n % p.G * p.hpg;
+                if (ck * kChunk >= valid_tokens(p, (int)(hd / p.H))) return;
+                cs = hd * nsl;
+            }
+            if (lane == 0) {
+                prefetch_bulk(cp.w.states + (cs * cp.n + ck) * kStateTile, kStateTile);
+                prefetch_bulk(cp.w.errs + (cs * cp.n + ck) * kErrTile, kErrTile);
+                prefetch_bulk(cp.w.dv_lo + (cs * cp.n + ck) * kDvLoTile, kDvLoTile);
+            }
+        };
         auto load_ds = [&](int it) {
             if (lane == 0) {
                 const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
@@ -156,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph)))) break;
             load_ds(it);
             ds_issued = it + 1;
+            prefetch_in(it + 1);
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_p, ph));
             if (!ok) break;
             tc_fence_after();

@@ -7,16 +7,17 @@
 //     Tt (I + diag(beta) E) = -E      and      At (I + diag(beta) E) = A,
 // so both matrices are rows of one right-hand solve with a unit lower triangle, and
 // every row is independent: thread i of 128 holds row i of [E; A] as it comes out of
-// tensor memory and substitutes from its last column to its first in fp32,
+// tensor memory and substitutes from its last column to its first,
 //     y_j = r_j - sum_{m > j} (beta_m y_m) E_mj,
-// 16 columns at a time: first the columns already solved (beta y from shared memory,
-// column m of all threads side by side; E rows as broadcasts), then the 16 x 16 triangle
-// in registers.  Substitution stays accurate for repeated keys, where a power series
-// of the triangle would lose every digit.
-// What bounds it are the multiply-adds of the two solves, 2000 for each of the rows
-// 32 .. 63 and 500 for the others (the backward needs A, not At, and solves half).  Rolled over the blocks: the whole substitution
-// unrolled (40 KB of code) waited for instructions half of the time.  Which
-// warps get the long rows changes from block to block.
+// 16 columns at a time: the 16 x 16 triangle in fp32 registers, its columns' share of all
+// columns before them on the tensor cores (beta y and E as hi + lo bf16 parts), where it
+// adds up beside the products.  Substitution stays accurate for repeated keys, where a
+// power series of the triangle would lose every digit.
+// What bounds it are the 5000 (backward, which takes A itself: 3500) warp instructions a
+// head and chunk of the decays, triangles and stores, and the latency of the three
+// steps; four blocks share an SM.  With the shares in fp32 registers too a head took
+// twice the instructions; the whole substitution unrolled waited for instructions
+// half of the time.  Which warps get the long rows changes from block to block.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -28,19 +29,35 @@ using namespace tc;
 
 constexpr int kThreads = 128;
 constexpr int kHeadsPer = 4;          // heads of a group per block
-constexpr int kLdE = 68;              // floats per row of E: 16-byte pieces, rows four banks apart
-constexpr uint32_t kAccCols = 64;
+constexpr int kLdD = 20;              // floats per row of E's diagonal blocks: 16-byte pieces
+constexpr uint32_t kAccCols = 128;    // the products; from column 64 the solved columns' shares
+// over the tiles, once the products have read them: E hi, E lo [64][64] SW128, beta y hi, lo [2 column octets][16 row octets][128]
+constexpr uint32_t kOffE = 0, kOffZ = 16384;
 
 struct PrepMaps {
     CUtensorMap k, q;
 };
 
+// a sum kept as hi + lo, and its product with log2(e)
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    const float s = a.hi + b.hi, t = s - a.hi, e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    return Pair{s + e, e - ((s + e) - s)};
+}
+__device__ __forceinline__ Pair times_log2e(Pair a) {
+    constexpr float c = 1.44269504f, c_lo = (float)(1.4426950408889634 - (double)1.44269504f);
+    const float p = a.hi * c, e = fmaf(a.hi, c, -p) + fmaf(a.hi, c_lo, a.lo * c);
+    return Pair{p + e, e - ((p + e) - p)};
+}
+
 // Grid: one block per (b, group, slice of the group's heads, chunk).
 __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_load, bar_mma;
+    __shared__ uint64_t bar_load, bar_mma, bar_step;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_e[kChunk * kLdE];
+    __shared__ __align__(16) float s_d[kChunk * kLdD];
     __shared__ float2 s_gam[kChunk];   // gamma log2(e), hi and lo
     __shared__ float s_beta[kChunk];
     const DeltaParams &p = cp.p;
@@ -60,6 +77,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
     if (tid == 0) {
         mbar_init(&bar_load, 1);
         mbar_init(&bar_mma, 1);
+        mbar_init(&bar_step, 1);
         mbar_fence_init();
         mbar_arrive_expect_tx(&bar_load, halves * 16384u);
         for (uint32_t kb = 0; kb < halves; ++kb)
@@ -85,36 +103,44 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         }
         __syncwarp();
     }
+    int steps = 0;                        // groups of shares issued
     const int i = (tid & 63) ^ (32 * flip);  // the row's token
     const bool keys = (tid < kChunk) == (k_off == 0), live = t0 + i < V;  // rows of absent tokens may hold anything: made zero
     const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * kHeadsPer);
+    float2 next_g = make_float2(0.f, 0.f), next_b = next_g;  // the next head's gates of tokens 2 lane, 2 lane + 1
+    auto fetch = [&](int h) {
+        const long long at = ((long long)bi * p.H + h) * p.L + t0 + 2 * lane;
+        const bool r0 = t0 + 2 * lane < V, r1 = t0 + 2 * lane + 1 < V;
+        next_g = make_float2(r0 ? clamp_log_decay(p.g[at]) : 0.f, r1 ? clamp_log_decay(p.g[at + 1]) : 0.f);
+        next_b = make_float2(r0 ? p.beta[at] : 0.f, r1 ? p.beta[at + 1] : 0.f);
+    };
+    if (warp == 0) fetch(grp * p.hpg + slice * kHeadsPer);
     for (int h = grp * p.hpg + slice * kHeadsPer; h < h_end; ++h) {
         const long long bh = (long long)bi * p.H + h;
         char *img = cp.image(bh, chunk);
         if (warp == 0) {
-            // gamma in fp64, kept as hi + lo: differences of it stay exact to fp32 after strong decays
+            // gamma as hi + lo: differences of it stay exact to fp32 after strong decays
             const int i0 = 2 * lane;
-            const long long at = bh * p.L + t0 + i0;
-            const bool r0 = t0 + i0 < V, r1 = t0 + i0 + 1 < V;
-            const float g0 = r0 ? clamp_log_decay(p.g[at]) : 0.f, g1 = r1 ? clamp_log_decay(p.g[at + 1]) : 0.f;
-            const float b0 = r0 ? p.beta[at] : 0.f, b1 = r1 ? p.beta[at + 1] : 0.f;
-            double sum = (double)g0 + (double)g1;
+            const float g1 = next_g.y;
+            const float2 beta = next_b;
+            Pair sum = add(Pair{next_g.x, 0.f}, Pair{g1, 0.f});
+            if (h + 1 < h_end) fetch(h + 1);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double up = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += up;
+                const Pair up{__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
+                if (lane >= o) sum = add(up, sum);
             }
-            const double c0 = sum - (double)g1, c1 = sum, total = __shfl_sync(0xffffffffu, sum, 31);
-            const double l0 = c0 * 1.4426950408889634, l1 = c1 * 1.4426950408889634;
-            const float h0 = (float)l0, h1 = (float)l1;
-            s_gam[i0] = make_float2(h0, (float)(l0 - (double)h0));
-            s_gam[i0 + 1] = make_float2(h1, (float)(l1 - (double)h1));
-            *(float2 *)(s_beta + i0) = make_float2(b0, b1);
+            const Pair c0 = add(sum, Pair{-g1, 0.f}), c1 = sum;
+            const Pair total{__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+            const Pair l0 = times_log2e(c0), l1 = times_log2e(c1);
+            s_gam[i0] = make_float2(l0.hi, l0.lo);
+            s_gam[i0 + 1] = make_float2(l1.hi, l1.lo);
+            *(float2 *)(s_beta + i0) = beta;
             float *gates = (float *)img;
-            *(float2 *)(gates + i0) = make_float2(expf((float)c0), expf((float)c1));
-            *(float2 *)(gates + kChunk + i0) = make_float2(expf((float)(total - c0)), expf((float)(total - c1)));
-            *(float2 *)(gates + 2 * kChunk + i0) = make_float2(b0, b1);
-            *(float4 *)(gates + 3 * kChunk + 2 * i0) = make_float4(h0, (float)(l0 - (double)h0), h1, (float)(l1 - (double)h1));
+            *(float2 *)(gates + i0) = make_float2(expf(c0.hi), expf(c1.hi));
+            *(float2 *)(gates + kChunk + i0) = make_float2(expf((total.hi - c0.hi) + (total.lo - c0.lo)), expf((total.hi - c1.hi) + (total.lo - c1.lo)));
+            *(float2 *)(gates + 2 * kChunk + i0) = beta;
+            *(float4 *)(gates + 3 * kChunk + 2 * i0) = make_float4(l0.hi, l0.lo, l1.hi, l1.lo);
         }
         if (h == grp * p.hpg + slice * kHeadsPer) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_mma, 0));
@@ -122,31 +148,35 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
         }
         if (__syncthreads_and(ok) == 0) break;
         const float2 gi = s_gam[i];
-        const int last = i >> 4 | 1;      // warps of rows 0 .. 31 stop after two blocks of columns
+        const int last = i >> 4 | 1;      // warps of rows 0 .. 31 have two blocks of columns
         // 16 columns of D o (row of K K^T or Q K^T), zero where j >= i (keys) or j > i
         auto decayed = [&](int jb, float f, float (&r)[16]) {
             float a[16];
             __syncwarp();  // the lanes' rows end at different columns
             tmem_ld16(tmem_addr(tm, 32 * warp, (16 * jb) ^ (32 * flip)), a);
+            const bool whole = 16 * jb + 15 < (i & ~31);  // the same for the warp
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int j = 16 * jb + e;
                 const float2 gj = s_gam[j];
                 const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y));
-                r[e] = live && (j < i || (j == i && !keys)) ? f * d * a[e] : 0.f;
+                r[e] = whole || j < i || (j == i && !keys) ? f * d * a[e] : 0.f;
+                if (!live) r[e] = 0.f;
             }
         };
         if (keys)
-            for (int jb = 0; jb <= (last | 1); ++jb) {
-                float r[16];
-                decayed(jb, 1.f, r);
+            for (int jb = 0; jb <= last; ++jb) {
+                float2 r[8];
+                decayed(jb, 1.f, (float(&)[16])r);
+                store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb, r);
+                store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb + 1, r + 4);
+                if (jb == i >> 4) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *(float4 *)(s_e + i * kLdE + 16 * jb + 4 * e) = make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                    for (int e = 0; e < 4; ++e)
+                        *(float4 *)(s_d + i * kLdD + 4 * e) = make_float4(r[2 * e].x, r[2 * e].y, r[2 * e + 1].x, r[2 * e + 1].y);
+                }
             }
         __syncthreads();
-        // z[m][row] = beta_m y_m of this thread's row, over the tiles (which the products have read)
-        float *z = (float *)(smem_raw + (kq - smem_u32(smem_raw))) + tid;
         const bool bwd = cp.w.states != nullptr;
         char *mat = img + kImgMat + (bwd && !keys ? 2 * kSquare : 0);
         auto store_block = [&](int jb, const float2 *y) {  // hi and lo parts, neighbouring rows on neighbouring addresses
@@ -166,61 +196,100 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 const float2 zero[8] = {};
                 store_block(jb, zero);
             }
-        if (bwd && !keys) {  // the backward takes A itself
+        if (bwd && !keys)                 // the backward takes A itself
             for (int jb = 0; jb <= last; ++jb) {
                 float2 y[8];
                 decayed(jb, p.scale, (float(&)[16])y);
                 if (jb <= (i >> 4)) store_block(jb, y);
             }
-        } else
-        for (int jb = last; jb >= 0; --jb) {
+        const bool solves = keys || !bwd;
+        const uint32_t zt = kq + kOffZ + (tid >> 3) * 128 + (tid & 7) * 16;
+        for (int jb = 3; jb >= 0; --jb) {
             float2 y[8];
-            if (keys) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 v = *(const float4 *)(s_e + i * kLdE + 16 * jb + 4 * e);
-                    y[2 * e] = make_float2(-v.x, -v.y);
-                    y[2 * e + 1] = make_float2(-v.z, -v.w);
+            for (int e = 0; e < 8; ++e) y[e] = make_float2(0.f, 0.f);
+            if (solves && jb <= last) {
+                if (keys) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t at = kq + kOffE + sw128_chunk(i, 2 * jb + c);
+                        join8(ld_shared_v4(at), ld_shared_v4(at + 8192), y + 4 * c);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = make_float2(-y[e].x, -y[e].y);
+                } else {
+                    decayed(jb, p.scale, (float(&)[16])y);
                 }
-            } else {
-                decayed(jb, p.scale, (float(&)[16])y);
-            }
-            const float *e0 = s_e + 16 * jb;
-#pragma unroll 4
-            for (int m = 16 * last + 15; m >= 16 * (jb + 1); --m) {
-                const float zm = -z[m * kThreads];
-                const float4 *w = (const float4 *)(e0 + m * kLdE);
+                if (jb < 3) {
+                    float2 g[8];
+                    __syncwarp();
+                    tmem_ld16(tmem_addr(tm, 32 * warp, 64 + 16 * jb), (float *)g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 v = w[e];
-                    y[2 * e] = ffma2(make_float2(v.x, v.y), make_float2(zm, zm), y[2 * e]);
-                    y[2 * e + 1] = ffma2(make_float2(v.z, v.w), make_float2(zm, zm), y[2 * e + 1]);
+                    for (int e = 0; e < 8; ++e) y[e] = ffma2(g[e], make_float2(-1.f, -1.f), y[e]);
+                }
+                // the triangle of the block: from the last column, each solved one taken off those before it
+                float *yy = (float *)y;
+                const float *e0 = s_d + 16 * jb * kLdD;
+                float2 z[8];
+                float *zz = (float *)z;
+#pragma unroll
+                for (int m = 15; m >= 0; --m) {
+                    const float zm = s_beta[16 * jb + m] * yy[m];
+                    zz[m] = zm;
+                    const float4 *w = (const float4 *)(e0 + m * kLdD);
+#pragma unroll
+                    for (int e = 0; e < (m + 3) / 4; ++e) {
+                        const float4 v = w[e];
+                        yy[4 * e] = fmaf(-zm, v.x, yy[4 * e]);
+                        if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(-zm, v.y, yy[4 * e + 1]);
+                        if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(-zm, v.z, yy[4 * e + 2]);
+                        if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(-zm, v.w, yy[4 * e + 3]);
+                    }
+                }
+                if (jb > 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split2(z[4 * c + e].x, z[4 * c + e].y, hi[e], lo[e]);
+                        st_shared_v4(zt + c * 2048, hi[0], hi[1], hi[2], hi[3]);
+                        st_shared_v4(zt + 4096 + c * 2048, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+            } else if (jb > 0) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) st_shared_v4(zt + c * 2048, 0, 0, 0, 0);
+            }
+            if (jb > 0) {  // the block's share of the columns before it: K = 16, N = 16 jb
+                fence_async_smem();
+                tc_fence_before();
+                __syncthreads();
+                if (tid == 0) {
+                    tc_fence_after();
+                    const uint32_t idesc = idesc_bf16(128, 16 * jb, false, true);
+                    const uint64_t dZ = sdesc_plain(kq + kOffZ, 2048, 128), dE = sdesc_mnmajor(kq + kOffE, jb, 8192);
+                    mma_bf16(tm + 64, dZ, dE, idesc, jb < 3);
+                    mma_bf16(tm + 64, dZ, sdesc_add(dE, 8192), idesc, true);
+                    mma_bf16(tm + 64, sdesc_add(dZ, 4096), dE, idesc, true);
+                    mma_commit(&bar_step);
                 }
             }
-            // the triangle of the block: from the last column, each solved one taken off those before it
-            float *yy = (float *)y;
-#pragma unroll
-            for (int m = 15; m >= 0; --m) {
-                const float zm = -s_beta[16 * jb + m] * yy[m];
-                z[(16 * jb + m) * kThreads] = -zm;
-                const float4 *w = (const float4 *)(e0 + (16 * jb + m) * kLdE);
-#pragma unroll
-                for (int e = 0; e < (m + 3) / 4; ++e) {
-                    const float4 v = w[e];
-                    yy[4 * e] = fmaf(zm, v.x, yy[4 * e]);
-                    if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(zm, v.y, yy[4 * e + 1]);
-                    if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(zm, v.z, yy[4 * e + 2]);
-                    if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
-                }
+            if (solves && jb <= (i >> 4)) store_block(jb, y);
+            if (jb > 0) {
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_step, steps & 1));
+                ++steps;
+                tc_fence_after();
             }
-            if (jb <= (i >> 4)) store_block(jb, y);
         }
-        __syncthreads();  // s_e and the gates may be written for the next head
+        tc_fence_before();
+        __syncthreads();  // E and the gates may be written for the next head
     }
     if (tid == 0) {
         if (!ok) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
         mbar_wait(&bar_load, 0);
         mbar_wait(&bar_mma, 0);
+        if (steps) mbar_wait(&bar_step, (steps - 1) & 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -236,7 +305,7 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
-    const int bytes = 1024 + 32768;  // the tiles, then z
+    const int bytes = 1024 + 32768;  // the tiles, then E and beta y
     const unsigned grid = (unsigned)c.n * ((p.hpg + kHeadsPer - 1) / kHeadsPer) * p.b * p.G;
     if ((e = cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     delta_prep_kernel<<<grid, kThreads, bytes, s>>>(c, maps);

@@ -309,12 +309,11 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             gn[2] = __ldg(gates + kChunk + i);
             gn[3] = __ldg(gates + kChunk - 1);
         };
-        if (NB > 1 && nv > 0) load_gates(0);
+        if (nv > 0) load_gates(0);
         for (int c = 0; c < nv && ok; ++c) {
             const uint32_t ph = c & 1;
-            if (NB == 1) load_gates(c);  // (ahead they would take registers that two blocks per SM do not have)
             const float eg = gn[0], be = gn[1], et = gn[2], ec = gn[3];
-            if (NB > 1 && c + 1 < nv) load_gates(c + 1);
+            if (c + 1 < nv) load_gates(c + 1);
             const int tok = c * kChunk + i;
             const bool live = tok < V, partial = V - c * kChunk < kChunk;
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_v, ph) && (!BWD || mbar_wait(&bar_kept, ph)));
