@@ -104,7 +104,7 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
         w.ss = (float *)take(cs * n * 16 * 4);
         for (float **x : {&w.ww, &w.zx}) *x = (float *)take(cs * 4 * n * kChunk * 4);
         for (float **x : {&w.fq, &w.fk}) *x = (float *)take(cs * 2 * n * kChunk * 4);
-        w.pe = (float *)take(cs * n * kChunk * 4);
+        w.pe = (float *)take(cs * n * 512 * 4);
     }
     if (c) {
         c->n = (int)n;

@@ -33,6 +33,7 @@ namespace ssd {
 namespace delta {
 
 constexpr int kChunk = 64;
+constexpr int kSMs = 152;
 // e^gamma, e^(gamma_C - gamma), beta; then pairs gamma log2(e) as hi and lo
 constexpr int kGates = 5 * kChunk * 4;
 // forward: run ks of a part: its first byte and its length; the 16-byte piece of row i (0 .. 127), columns 8 c .. + 7
@@ -62,7 +63,7 @@ constexpr int kImgMat = kGates, kImgFwd = kGates + 2 * kPart, kImgBwd = kGates +
 //     ss = e^gamma_C <S, dS>            S before, dS after the chunk    [cs, n, 16], a share of each warp
 //     ww = beta Z.(e^(gamma_C - gamma) K dS),  zx = Z.X                 [cs, 4, n * 64], sums over 16 columns
 //     fq = q.(scale e^gamma dO S^T),  fk = -k.(e^gamma dV S^T)          [cs, 2, n * 64], over 64 of the keys' columns
-//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n * 64]
+//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n, 512], the sums in pieces
 // and dbeta = zx.
 struct ChunkBackward {
     char *states, *dstates, *errs, *dv_lo;

@@ -6,17 +6,18 @@
 //     Nm_ij = scale D_ij beta_j (dO_i . Z_j), j <= i;    M_ij = -D_ij beta_j (dV_i . Z_j), j < i
 //     dQ = scale e^gamma o (dO S^T) + Nm K
 //     dK = -e^gamma o (dV S^T) + M K + Nm^T Q + M^T K + (beta e^(gamma_C - gamma) o Z) dS^T
-// in three groups of products: [Q; K] K^T, and [dO; dV] on S and Z at once (128 rows,
-// 192 columns); then [Nm; M] K, whose rows 0 .. 63 complete dQ; then, onto the same
-// accumulator, W dS^T with W = beta e^(gamma_C - gamma) o Z, and (Nm; M)^T [Q; K], whose
-// rows 64 .. 127 complete dK (the upper rows are spent by then and take what falls on
-// them).  The heads of a key group are walked by one block, which adds them up in
-// registers: dq and dk are written once, in a fixed order.  Z, S, Nm and M come as hi + lo
-// parts: what a token reads of S and what the chunk has written over it cancel, and the
-// share of dg that passes between tokens of the chunk is made here,
+// in two groups of products: [Q; K] K^T, and [dO; dV] on S and Z at once (128 rows,
+// 192 columns); then, into one accumulator whose rows 0 .. 63 are dQ and 64 .. 127 dK,
+// [Nm; M] K, [0; W] dS^T with W = beta e^(gamma_C - gamma) o Z, and [0 | (Nm; M)]^T [Q; K] (the
+// zero blocks keep the products that are dK's alone off the dQ rows).  The heads of a key
+// group are walked by one block, which adds them up in registers: dq and dk are written
+// once, in a fixed order.  Z, S, Nm and M come as hi + lo parts: what a token reads of S and
+// what the chunk has written over it cancel, and the share of dg that passes between tokens
+// of the chunk is made here,
 //     pe_i = sum_j P_ij - sum_j P_ji,   P = Nm o Q K^T + M o K K^T;
 // dV (beside dO Z^T and dV Z^T), W and dS are rounded once, as dk is.
-// Two blocks share an SM and hide each other's copies and passes.
+// Two blocks share an SM, hide each other's copies and passes, and stay for the whole
+// pass.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -27,14 +28,14 @@ namespace {
 using namespace tc;
 
 constexpr int kCompute = 256, kThreads = kCompute + 32;
-// shared memory: 64 rows of zeros; dV lo, then W; S hi (then [Nm; M] hi) and Z hi; Z lo, then sums;
+// shared memory: 64 rows of zeros; dV lo, then W; S hi (then [Nm; M] hi) and Z hi; Z lo;
 // S lo, then dS; dO and dV (then [Nm; M] lo); Q and K
 constexpr uint32_t kOffZero = 0, kOffW = 8192, kOffSZ = 16384, kOffZ = kOffSZ + 16384, kOffP = kOffSZ, kOffZlo = 40960,
                    kOffDS = 49152, kOffDV = 65536, kOffPlo = kOffDV, kOffQK = 81920, kOffSmall = 114688;
 struct Small {
     float2 gam[kChunk];
     float beta[kChunk];
-    uint64_t qk, in, ds, p, out, q, m[3];
+    uint64_t qk, in, ds, p, out, m[2];
     uint32_t tmem;
     int err;
 };
@@ -44,38 +45,25 @@ struct GradMaps {
     CUtensorMap k, q, d_o, dv;
 };
 
-// Grid: one block per (b, group, chunk).
+// Blocks walk the units (b, group, chunk); within a unit the items (head, slice of 64 columns of P).
 __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkParams cp, const __grid_constant__ GradMaps maps) {
     // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Small &sm = *(Small *)(smem_raw + kOffSmall);
-    uint64_t &bar_qk = sm.qk, &bar_in = sm.in, &bar_ds = sm.ds, &bar_p = sm.p, &bar_out = sm.out, &bar_q = sm.q;
-    uint64_t(&bar_m)[3] = sm.m;
+    uint64_t &bar_qk = sm.qk, &bar_in = sm.in, &bar_ds = sm.ds, &bar_p = sm.p, &bar_out = sm.out;
+    uint64_t(&bar_m)[2] = sm.m;
     const DeltaParams &p = cp.p;
     const uint32_t base = smem_u32(smem_raw);
-    const int chunk = blockIdx.x % cp.n, grp = blockIdx.x / cp.n % p.G, bi = blockIdx.x / cp.n / p.G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int V = valid_tokens(p, bi), t0 = chunk * kChunk, live_n = V - t0, nsl = slices_of(p);
-    if (live_n <= 0) {
-        for (int x = tid; x < kChunk * (p.N / 8); x += kThreads) {
-            const int tok = t0 + x / (p.N / 8);
-            if (tok < p.L) {
-                const long long at = (((long long)bi * p.L + tok) * p.G + grp) * p.N + 8 * (x % (p.N / 8));
-                *(uint4 *)((bf16 *)p.dq + at) = make_uint4(0, 0, 0, 0);
-                *(uint4 *)((bf16 *)p.dk + at) = make_uint4(0, 0, 0, 0);
-            }
-        }
-        return;
-    }
-    const int items = p.hpg * nsl;
+    const int nsl = slices_of(p), items = p.hpg * nsl, units = cp.n * p.G * p.b;
     if (tid == 0) {
         mbar_init(&bar_qk, 1);
         mbar_init(&bar_in, 1);
         mbar_init(&bar_ds, 1);
         mbar_init(&bar_p, kCompute / 32);
         mbar_init(&bar_out, kCompute / 32);
-        mbar_init(&bar_q, kCompute / 64);
-        for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
+        mbar_init(&bar_m[0], 1);
+        mbar_init(&bar_m[1], 1);
         mbar_fence_init();
         sm.err = (base & 1023u) ? 1 : 0;
     }
@@ -87,75 +75,89 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
     tc_fence_after();
     const uint32_t tm = sm.tmem;
     const uint32_t halves = p.N > 64 ? 2u : 1u;
+    bool ok = sm.err == 0;
+    int u = 0, n = 0;  // live units and items so far: the barriers' phases
 
     if (warp == kCompute / 32) {
         // ---- copies and products
-        auto head = [&](int it) { return grp * p.hpg + it / nsl; };
-        auto load_in = [&](int it) {
+        struct Item {
+            int chunk, bi, grp, h, slice;
+            long long cs;
+        };
+        // item `it` of unit `unit`; of the next unit that is not all absent, where `it` is past its end
+        auto item = [&](int &unit, int it, Item &x) {
+            if (it >= items) {
+                unit += gridDim.x;
+                it = 0;
+                while (unit < units && unit % cp.n * kChunk >= valid_tokens(p, unit / cp.n / p.G)) unit += gridDim.x;
+            }
+            if (unit >= units) return false;
+            x.chunk = unit % cp.n;
+            x.grp = unit / cp.n % p.G;
+            x.bi = unit / cp.n / p.G;
+            x.h = x.grp * p.hpg + it / nsl;
+            x.slice = it % nsl;
+            x.cs = ((long long)x.bi * p.H + x.h) * nsl + x.slice;
+            return true;
+        };
+        auto load_qk = [&](const Item &x) {
             if (lane == 0) {
-                const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
-                const char *state = cp.w.states + (cs * cp.n + chunk) * kStateTile;
+                mbar_arrive_expect_tx(&bar_qk, halves * 16384u);
+                for (uint32_t kb = 0; kb < halves; ++kb) {
+                    tma_tile(base + kOffQK + kb * 16384u, &maps.q, &bar_qk, 64 * kb, x.grp, x.chunk * kChunk, x.bi);
+                    tma_tile(base + kOffQK + kb * 16384u + 8192u, &maps.k, &bar_qk, 64 * kb, x.grp, x.chunk * kChunk, x.bi);
+                }
+            }
+        };
+        auto load_in = [&](const Item &x) {
+            if (lane == 0) {
+                const char *state = cp.w.states + (x.cs * cp.n + x.chunk) * kStateTile;
                 mbar_arrive_expect_tx(&bar_in, 16384 + kStateTile + kErrTile + kDvLoTile);
                 bulk_load(base + kOffSZ, state, 16384, &bar_in);
-                bulk_load(base + kOffZ, cp.w.errs + (cs * cp.n + chunk) * kErrTile, kErrTile, &bar_in);
-                tma_tile(base + kOffDV, &maps.d_o, &bar_in, 64 * (it % nsl), head(it), t0, bi);
-                tma_tile(base + kOffDV + 8192, &maps.dv, &bar_in, 64 * (it % nsl), head(it), t0, bi);
+                bulk_load(base + kOffZ, cp.w.errs + (x.cs * cp.n + x.chunk) * kErrTile, kErrTile, &bar_in);
+                tma_tile(base + kOffDV, &maps.d_o, &bar_in, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
+                tma_tile(base + kOffDV + 8192, &maps.dv, &bar_in, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
                 bulk_load(base + kOffDS, state + 16384, 16384, &bar_in);
-                bulk_load(base + kOffW, cp.w.dv_lo + (cs * cp.n + chunk) * kDvLoTile, kDvLoTile, &bar_in);
-                prefetch_bulk(cp.w.dstates + (cs * cp.n + chunk) * kDStateTile, kDStateTile);
+                bulk_load(base + kOffW, cp.w.dv_lo + (x.cs * cp.n + x.chunk) * kDvLoTile, kDvLoTile, &bar_in);
             }
         };
-        // into L2, ahead: the block's next item, or the first of the block that will follow here
-        auto prefetch_in = [&](int it) {
-            long long cs, ck = chunk;
-            if (it < items) {
-                cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
-            } else {
-                const long long blk = blockIdx.x + 2LL * 152;
-                if (blk >= (long long)gridDim.x) return;
-                ck = blk % cp.n;
-                const long long hd = blk / cp.n / p.G * p.H + blk / cp.n % p.G * p.hpg;
-                if (ck * kChunk >= valid_tokens(p, (int)(hd / p.H))) return;
-                cs = hd * nsl;
-            }
+        auto prefetch = [&](const Item &x) {  // into L2
             if (lane == 0) {
-                prefetch_bulk(cp.w.states + (cs * cp.n + ck) * kStateTile, kStateTile);
-                prefetch_bulk(cp.w.errs + (cs * cp.n + ck) * kErrTile, kErrTile);
-                prefetch_bulk(cp.w.dv_lo + (cs * cp.n + ck) * kDvLoTile, kDvLoTile);
+                prefetch_bulk(cp.w.states + (x.cs * cp.n + x.chunk) * kStateTile, kStateTile);
+                prefetch_bulk(cp.w.errs + (x.cs * cp.n + x.chunk) * kErrTile, kErrTile);
+                prefetch_bulk(cp.w.dv_lo + (x.cs * cp.n + x.chunk) * kDvLoTile, kDvLoTile);
+                prefetch_bulk(cp.w.dstates + (x.cs * cp.n + x.chunk) * kDStateTile, kDStateTile);
+                prefetch_bulk(cp.image((long long)x.bi * p.H + x.h, x.chunk), kGates);
+                prefetch_tile(&maps.d_o, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
+                prefetch_tile(&maps.dv, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
             }
         };
-        auto load_ds = [&](int it) {
-            if (lane == 0) {
-                const long long cs = ((long long)bi * p.H + head(it)) * nsl + it % nsl;
-                mbar_arrive_expect_tx(&bar_ds, kDStateTile);
-                bulk_load(base + kOffDS, cp.w.dstates + (cs * cp.n + chunk) * kDStateTile, kDStateTile, &bar_ds);
-            }
-        };
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_qk, halves * 16384u);
-            for (uint32_t kb = 0; kb < halves; ++kb) {
-                tma_tile(base + kOffQK + kb * 16384u, &maps.q, &bar_qk, 64 * kb, grp, t0, bi);
-                tma_tile(base + kOffQK + kb * 16384u + 8192u, &maps.k, &bar_qk, 64 * kb, grp, t0, bi);
-            }
-        }
-        load_in(0);
         const uint32_t i_ac = idesc_bf16(128, 192, false, false), i_c = idesc_bf16(128, 64, false, false),
                        i_b = idesc_bf16(128, 128, false, false), i_d = idesc_bf16(128, 64 * halves, false, true),
                        i_e = idesc_bf16(128, 64 * halves, true, true);
         const uint64_t dDV = sdesc(base + kOffDV, 16, 1024), dSZ = sdesc(base + kOffSZ, 16, 1024),
-                       dZlo = sdesc(base + kOffZlo, 16, 1024),
-                       dVlo = sdesc(base + kOffZero, 16, 1024), dDS = sdesc(base + kOffDS, 16, 1024),
-                       dP = sdesc(base + kOffP, 16, 1024), dK = sdesc(base + kOffQK + 8192, 16384, 1024),
-                       // the 64 columns before P's transpose are what lies before it: rows 0 .. 63 take anything
-                       dPt = sdesc(base + kOffP - 16384, 16384, 1024), dPlo = sdesc(base + kOffPlo, 16, 1024),
-                       dPlot = sdesc(base + kOffPlo - 16384, 16384, 1024), dSlo = sdesc(base + kOffDS, 16, 1024), dQKt = sdesc(base + kOffQK, 16384, 1024),
-                       dQK = sdesc(base + kOffQK, 16, 1024), dKk = sdesc(base + kOffQK + 8192, 16, 1024);
+                       dZlo = sdesc(base + kOffZlo, 16, 1024), dVlo = sdesc(base + kOffZero, 16, 1024),
+                       dDS = sdesc(base + kOffDS, 16, 1024), dP = sdesc(base + kOffP, 16, 1024),
+                       dPlo = sdesc(base + kOffPlo, 16, 1024), dK = sdesc(base + kOffQK + 8192, 16384, 1024),
+                       dQKt = sdesc(base + kOffQK, 16384, 1024), dQK = sdesc(base + kOffQK, 16, 1024),
+                       dKk = sdesc(base + kOffQK + 8192, 16, 1024);
+        // (zeros | part of P)^T: the 64 zero rows serve both halves of the K index, the second with P 8 KB further away
+        auto zeros_p = [&](uint32_t part, int ks) {
+            return sdesc(base + kOffZero + (ks & 3) * 2048, part - kOffZero + (ks >> 2) * 8192, 1024);
+        };
         const int nks = (p.N + 15) / 16;
-        bool ok = true;
-        int done = 0, in_issued = 1, ds_issued = 0;
-        for (int it = 0; it < items; ++it) {
-            const uint32_t ph = it & 1;
-            ok = mbar_wait(&bar_in, ph) && mbar_wait(&bar_qk, 0) && (it == 0 || mbar_wait(&bar_out, (it - 1) & 1));
+        int unit = (int)blockIdx.x - (int)gridDim.x, loaded = 0;
+        Item x;
+        bool more = ok && item(unit, items, x);
+        if (more) {
+            load_qk(x);
+            load_in(x);
+            loaded = 1;
+        }
+        int qk_loaded = loaded, ds_loaded = 0, done = 0, it = 0;
+        while (more) {
+            const uint32_t ph = n & 1;
+            ok = mbar_wait(&bar_in, ph) && mbar_wait(&bar_qk, u & 1) && (n == 0 || mbar_wait(&bar_out, (n - 1) & 1));
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -165,185 +167,184 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, ks > 0);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSlo, ks * 32), i_b, true);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dDS, ks * 32), i_b, true);  // S lo
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dDV, ks * 32), sdesc_add(dZlo, ks * 32), i_c, true);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dVlo, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, true);
                 mma_commit(&bar_m[0]);
             }
+            // the item after this one
+            int next_unit = unit, next_it = it + 1;
+            Item y;
+            const bool next = item(next_unit, next_it, y);
+            if (next_it >= items) next_it = 0;
+            if (next) prefetch(y);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph)))) break;
-            load_ds(it);
-            ds_issued = it + 1;
-            prefetch_in(it + 1);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_p, ph));
-            if (!ok) break;
+            if (lane == 0) {  // dS in place of S lo
+                mbar_arrive_expect_tx(&bar_ds, kDStateTile);
+                bulk_load(base + kOffDS, cp.w.dstates + (x.cs * cp.n + x.chunk) * kDStateTile, kDStateTile, &bar_ds);
+            }
+            ds_loaded = n + 1;
+            ok = mbar_wait(&bar_p, ph) && mbar_wait(&bar_ds, ph);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dP, ks * 32), sdesc_add(dK, ks * 2048), i_d, ks > 0);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dPlo, ks * 32), sdesc_add(dK, ks * 2048), i_d, true);
-                mma_commit(&bar_m[1]);
-            }
-            ok = mbar_wait(&bar_q, ph) && mbar_wait(&bar_ds, ph);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-            if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, sdesc_add(dPt, ks * 2048), sdesc_add(dQKt, ks * 2048), i_e, true);
+                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, zeros_p(kOffP, ks), sdesc_add(dQKt, ks * 2048), i_e, true);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, sdesc_add(dPlot, ks * 2048), sdesc_add(dQKt, ks * 2048), i_e, true);
+                for (int ks = 0; ks < 8; ++ks) mma_bf16(tm + 128, zeros_p(kOffPlo, ks), sdesc_add(dQKt, ks * 2048), i_e, true);
                 // W, where dV lo was, below the zeros
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dVlo, ks * 32), sdesc_add(dDS, ks * 32), i_b, true);
-                mma_commit(&bar_m[2]);
+                mma_commit(&bar_m[1]);
             }
             __syncwarp();
-            done = it + 1;
-            if (it + 1 < items) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
-                load_in(it + 1);
-                in_issued = it + 2;
-            }
-        }
-        if (!ok) sm.err = 1;
-        mbar_wait(&bar_qk, 0);
-        mbar_wait(&bar_in, (in_issued - 1) & 1);
-        if (ds_issued) mbar_wait(&bar_ds, (ds_issued - 1) & 1);
-        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);
-    } else {
-        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-        const bool keys = row >= kChunk;     // rows 64 .. 127: dV, M, dK
-        const int i = row & 63, tok = t0 + i;
-        const bool live = i < live_n;
-        float2 acc[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] = make_float2(0.f, 0.f);
-        bool ok = true;
-        if (live_n < kChunk) {  // q and k rows of absent tokens are made zero
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_qk, 0));
-            for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
-                if (((x >> 3) & 63) >= live_n) st_shared_v4(base + kOffQK + x * 16u, 0, 0, 0, 0);
-        }
-        for (int it = 0; it < items && ok; ++it) {
-            const uint32_t ph = it & 1;
-            const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
-            const float *gates = (const float *)cp.image(bh, chunk);
-            if (tid < kChunk) {
-                sm.gam[tid] = __ldg((const float2 *)(gates + 3 * kChunk) + tid);
-                sm.beta[tid] = __ldg(gates + 2 * kChunk + tid);
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph));
-            if (!ok) break;
-            tc_fence_after();
-            // W, in place of what dV lost, from both parts of Z (16 columns of row tid % 64): kept in shared memory
-            const int wr = tid & 63, wc = 2 * (tid >> 6);
-            const float wf = __ldg(gates + 2 * kChunk + wr) * __ldg(gates + kChunk + wr), eg = __ldg(gates + i);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float2 w[4];
-                const uint32_t off = sw128_chunk(wr, wc + c);
-                join8(ld_shared_v4(base + kOffZ + off), ld_shared_v4(base + kOffZlo + off), w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = fmul2(w[e], make_float2(wf, wf));
-                const uint4 o = pack8(w);
-                st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");  // Z lo has been read: the sums may take its place
-            float *rsum = (float *)(smem_raw + kOffZlo), *csum = rsum + 256;  // [half][128 rows], [quarter][64 columns]
-            const float2 gi = sm.gam[i];
-            const float f = keys ? -1.f : p.scale;
-            float rs = 0.f, cs_[32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float a[16], b[16];
-                tmem_ld16x2(tmem_addr(tm, 32 * quarter, 128 + 32 * half + 16 * q), tmem_addr(tm, 32 * quarter, 192 + 32 * half + 16 * q), a, b);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = 32 * half + 16 * q + e;
-                    const float2 gj = sm.gam[j];
-                    const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y)) * sm.beta[j];
-                    const bool in = live && (j < i || (j == i && !keys));
-                    a[e] = in ? f * d * a[e] : 0.f;
-                    cs_[16 * q + e] = in ? a[e] * b[e] : 0.f;
-                    rs += cs_[16 * q + e];
+            done = n + 1;
+            if (next) {  // all but Q and K is done with; those, too, once the threads have read their rows
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph)))) break;
+                load_in(y);
+                ++loaded;
+                if (next_unit != unit) {
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_out, ph)))) break;
+                    load_qk(y);
+                    ++qk_loaded;
+                    ++u;
                 }
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    store_parts8(base + kOffP, base + kOffPlo, row, 4 * half + 2 * q + c, (const float2 *)a + 4 * c);
             }
-            fence_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_p);
-            // column sums over the warp's rows: halves of the columns change hands until lane l has column l
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const bool up = lane & o;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < o) {
-                        const float give = up ? cs_[e] : cs_[e + o], keep = up ? cs_[e + o] : cs_[e];
-                        cs_[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                    }
-            }
-            rsum[half * 128 + row] = rs;
-            csum[quarter * 64 + 32 * half + lane] = cs_[0];
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (tid < kChunk) {
-                float e = 0.f;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) e += rsum[(x >> 1) * 128 + (x & 1) * 64 + tid] - csum[x * 64 + tid];
-                cp.w.pe[cs * cp.n * kChunk + t0 + tid] = e;
-            }
-            const float fa = f * eg;
-            float read = 0.f;
-            auto add = [&]() {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (half < (int)halves) {
-                        float2 a[8], b[8];
-                        const uint32_t at = tmem_addr(tm, 32 * quarter, 64 * half + 16 * q);
-                        tmem_ld16x2(at, at + 128, (float *)a, (float *)b);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float2 &x = acc[8 * q + e];
-                            x = ffma2(b[e], make_float2(1.f, 1.f), ffma2(a[e], make_float2(fa, fa), x));
-                        }
-                        // with the row's own q or k: what it reads of S
-                        const uint32_t own = base + kOffQK + half * 16384;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) read = dot8(ld_shared_v4(own + sw128_chunk(row, 2 * q + u)), a + 4 * u, read);
-                    }
-                (keys ? cp.w.fk : cp.w.fq)[(cs * 2 + half) * cp.n * kChunk + tok] = live ? fa * read : 0.f;
-            };
-            if (!keys) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
-                if (!ok) break;
-                tc_fence_after();
-                add();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_q);
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
-            if (!ok) break;
-            tc_fence_after();
-            if (keys) add();
-            fence_async_smem();  // the sums, before the copies that come in their place
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_out);
+            more = next;
+            unit = next_unit;
+            it = next_it;
+            x = y;
+            ++n;
         }
         if (!ok) sm.err = 1;
-        if (tok < p.L) {
-            bf16 *dst = (bf16 *)(keys ? p.dk : p.dq) + (((long long)bi * p.L + tok) * p.G + grp) * p.N + 64 * half;
+        if (qk_loaded) mbar_wait(&bar_qk, (qk_loaded - 1) & 1);
+        if (loaded) mbar_wait(&bar_in, (loaded - 1) & 1);
+        if (ds_loaded) mbar_wait(&bar_ds, (ds_loaded - 1) & 1);
+        if (done) mbar_wait(&bar_m[1], (done - 1) & 1);
+    } else {
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane, i = row & 63;
+        const bool keys = row >= kChunk;     // rows 64 .. 127: dV, M, dK
+        for (int unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
+            const int chunk = unit % cp.n, grp = unit / cp.n % p.G, bi = unit / cp.n / p.G;
+            const int V = valid_tokens(p, bi), t0 = chunk * kChunk, live_n = V - t0, tok = t0 + i;
+            const bool live = i < live_n;
+            float2 acc[32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (64 * half + 8 * c < p.N) *(uint4 *)(dst + 8 * c) = live ? pack8(acc + 4 * c) : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 32; ++e) acc[e] = make_float2(0.f, 0.f);
+            if (live_n > 0) {
+                if (live_n < kChunk) {  // q and k rows of absent tokens are made zero
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_qk, u & 1));
+                    for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
+                        if (((x >> 3) & 63) >= live_n) st_shared_v4(base + kOffQK + x * 16u, 0, 0, 0, 0);
+                }
+                for (int it = 0; it < items && ok; ++it, ++n) {
+                    const uint32_t ph = n & 1;
+                    const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
+                    const float *gates = (const float *)cp.image(bh, chunk);
+                    const int wr = tid & 63, wc = 2 * (tid >> 6);
+                    const float wf = __ldg(gates + 2 * kChunk + wr) * __ldg(gates + kChunk + wr), eg = __ldg(gates + i);
+                    if (tid < kChunk) {
+                        sm.gam[tid] = __ldg((const float2 *)(gates + 3 * kChunk) + tid);
+                        sm.beta[tid] = __ldg(gates + 2 * kChunk + tid);
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph));
+                    if (!ok) break;
+                    tc_fence_after();
+                    // W, in place of what dV lost, from both parts of Z (16 columns of row tid % 64)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float2 w[4];
+                        const uint32_t off = sw128_chunk(wr, wc + c);
+                        join8(ld_shared_v4(base + kOffZ + off), ld_shared_v4(base + kOffZlo + off), w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = fmul2(w[e], make_float2(wf, wf));
+                        const uint4 o = pack8(w);
+                        st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
+                    }
+                    const float2 gi = sm.gam[i];
+                    const float f = keys ? -1.f : p.scale;
+                    float rs = 0.f, cs_[32];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float a[16], b[16];
+                        tmem_ld16x2(tmem_addr(tm, 32 * quarter, 128 + 32 * half + 16 * q),
+                                    tmem_addr(tm, 32 * quarter, 192 + 32 * half + 16 * q), a, b);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int j = 32 * half + 16 * q + e;
+                            const float2 gj = sm.gam[j];
+                            const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y)) * sm.beta[j];
+                            const bool in = live && (j < i || (j == i && !keys));
+                            a[e] = in ? f * d * a[e] : 0.f;
+                            cs_[16 * q + e] = in ? a[e] * b[e] : 0.f;
+                            rs += cs_[16 * q + e];
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            store_parts8(base + kOffP, base + kOffPlo, row, 4 * half + 2 * q + c, (const float2 *)a + 4 * c);
+                    }
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_p);
+                    // column sums over the warp's rows: halves of the columns change hands until lane l has column l
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e < o) {
+                                const float give = up ? cs_[e] : cs_[e + o], keep = up ? cs_[e + o] : cs_[e];
+                                cs_[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                            }
+                    }
+                    float *pe = cp.w.pe + (cs * cp.n + chunk) * 512;
+                    pe[half * 128 + row] = rs;
+                    pe[256 + quarter * 64 + 32 * half + lane] = cs_[0];
+                    const float fa = f * eg;
+                    float read = 0.f;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (half < (int)halves) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float2 a[8], b[8];
+                            const uint32_t at = tmem_addr(tm, 32 * quarter, 64 * half + 16 * q);
+                            tmem_ld16x2(at, at + 128, (float *)a, (float *)b);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float2 &x = acc[8 * q + e];
+                                x = ffma2(b[e], make_float2(1.f, 1.f), ffma2(a[e], make_float2(fa, fa), x));
+                            }
+                            // with the row's own q or k: what it reads of S
+                            const uint32_t own = base + kOffQK + half * 16384;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) read = dot8(ld_shared_v4(own + sw128_chunk(row, 2 * q + c)), a + 4 * c, read);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_out);
+                    (keys ? cp.w.fk : cp.w.fq)[(cs * 2 + half) * cp.n * kChunk + tok] = live ? fa * read : 0.f;
+                }
+                ++u;
+            }
+            if (tok < p.L && ok) {
+                bf16 *dst = (bf16 *)(keys ? p.dk : p.dq) + (((long long)bi * p.L + tok) * p.G + grp) * p.N + 64 * half;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (64 * half + 8 * c < p.N) *(uint4 *)(dst + 8 * c) = live ? pack8(acc + 4 * c) : make_uint4(0, 0, 0, 0);
+            }
         }
+        if (!ok) sm.err = 1;
     }
     tc_fence_before();
     __syncthreads();
@@ -378,9 +379,14 @@ __global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
             from.y += fq.y + fk.y;
         }
         for (int x = 0; x < nsl; ++x) {
-            const float2 pe = *(const float2 *)(cp.w.pe + (bh * nsl + x) * cp.n * kChunk + t);
-            from.x += pe.x;
-            from.y += pe.y;
+            // row sums of Nm and of M, each over two halves of the columns; column sums, over four quarters of the rows
+            const float *pe = cp.w.pe + ((bh * nsl + x) * cp.n + chunk) * 512 + 2 * lane;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float2 r = *(const float2 *)(pe + 64 * y), c = *(const float2 *)(pe + 256 + 64 * y);
+                from.x += r.x - c.x;
+                from.y += r.y - c.y;
+            }
             if (lane < 16) ss += cp.w.ss[((bh * nsl + x) * cp.n + chunk) * 16 + lane];
         }
     }
@@ -417,7 +423,8 @@ cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.dv, p.dv, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const int bytes = (int)kBytes;
     if ((e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    delta_grad_kernel<<<(unsigned)c.n * p.G * p.b, kThreads, bytes, s>>>(c, maps);
+    const int units = c.n * p.G * p.b;
+    delta_grad_kernel<<<units < 2 * kSMs ? units : 2 * kSMs, kThreads, bytes, s>>>(c, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     delta_gate_grads<<<(unsigned)(((long long)p.b * p.H * c.n + 7) / 8), 256, 0, s>>>(c);
     return cudaGetLastError();

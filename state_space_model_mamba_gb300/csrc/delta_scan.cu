@@ -40,7 +40,6 @@ using namespace tc;
 constexpr int compute_threads(int W) { return 8 * W; }
 constexpr int scan_threads(int W) { return compute_threads(W) + 64; }
 constexpr uint32_t kTmemCols = 256;
-constexpr int kSMs = 152;
 
 // shared memory from a 1024-byte aligned base
 constexpr uint32_t kOffS = 0;              // S hi, S lo: [128 n][64] SW128 each; X and W in their place
