@@ -5,19 +5,30 @@
 // All three are streams bound by HBM.  A row is held by TPR threads with NV vectors of
 // VEC columns each, vector j of thread t at columns (j TPR + t) VEC, so that every load
 // of a warp is contiguous (512 bytes at VEC = 8 in bf16).  VEC is 8 where D is a multiple of
-// 8, else 2 or 1: rows then start on the vector's alignment.  Blocks walk the rows: the
-// weight stays in registers (read again for every row it is as much L2 traffic as half
-// the row), and the next row is loaded, as it is stored, before the sums of this one are
-// waited for.
+// 8, else 2 or 1: rows then start on the vector's alignment.  The blocks that the SMs hold at
+// once walk the rows: the weight stays in registers (read again for every row it is as much L2
+// traffic as half the row), and the next row is loaded, as it is stored, before the sums of this
+// one are waited for.  The arithmetic is in pairs, and the residual is added in bf16 itself: at
+// 36 instructions a column (scalar, IEEE divisions) the e4m3 form took 63 us where the
+// bf16 one, which writes more, took 57.
+//
+// Measured at 16384 x 2560 in bf16, of a measured copy's 6.69 TB/s:
+//   bf16 output 52.6 us (6.4 TB/s), e4m3 with a scale per 128 columns 47.8 us (6.2 TB/s),
+//   backward 59 us (5.7 TB/s), of which the second kernel is 4;
+// 24 x 2560: 2 us, below a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdio.h>
 
 #include "norm.h"
 #include "ssd_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace {
+
+using tc::ffma2;
+using tc::fmul2;
 
 constexpr float kE4m3Max = 448.f;
 
@@ -26,40 +37,65 @@ template <typename T, int VEC>
 struct Vec {
     static constexpr int BYTES = VEC * (int)sizeof(T), WORDS = (BYTES + 3) / 4;
     uint32_t w[WORDS];
+    // ONCE: evicted from the caches first, as a row that is read once may be
+    template <typename W, bool ONCE>
+    static __device__ __forceinline__ W ld(const W *p) {
+        if constexpr (ONCE)
+            return __ldcs(p);
+        else
+            return __ldg(p);
+    }
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (BYTES == 32) {
-            const uint4 a = __ldg((const uint4 *)p), b = __ldg((const uint4 *)p + 1);
+            const uint4 a = ld<uint4, ONCE>((const uint4 *)p), b = ld<uint4, ONCE>((const uint4 *)p + 1);
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
         } else if constexpr (BYTES == 16) {
-            const uint4 a = __ldg((const uint4 *)p);
+            const uint4 a = ld<uint4, ONCE>((const uint4 *)p);
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         } else if constexpr (BYTES == 8) {
-            const uint2 a = __ldg((const uint2 *)p);
+            const uint2 a = ld<uint2, ONCE>((const uint2 *)p);
             w[0] = a.x, w[1] = a.y;
         } else if constexpr (BYTES == 4) {
-            w[0] = __ldg((const uint32_t *)p);
+            w[0] = ld<uint32_t, ONCE>((const uint32_t *)p);
         } else {
-            w[0] = __ldg((const unsigned short *)p);
+            w[0] = ld<unsigned short, ONCE>((const unsigned short *)p);
         }
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
-    __device__ __forceinline__ float get(int i) const {
+    // elements 2 i and 2 i + 1 (VEC = 1: the element and 0)
+    static constexpr int PAIRS = (VEC + 1) / 2;
+    __device__ __forceinline__ float2 get(int i) const {
         if constexpr (sizeof(T) == 4)
-            return __uint_as_float(w[i]);
+            return make_float2(__uint_as_float(w[2 * i]), VEC > 1 ? __uint_as_float(w[2 * i + (VEC > 1)]) : 0.f);
         else
-            return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+            return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    __device__ __forceinline__ void set(const float *f) {
+    __device__ __forceinline__ void set(int i, float2 f) {
         if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(f[i]);
+            w[2 * i] = __float_as_uint(f.x);
+            if (VEC > 1) w[2 * i + (VEC > 1)] = __float_as_uint(f.y);
         } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+            w[i] = *(const uint32_t *)&v;
+        }
+    }
+    // what added leaves every value as it is
+    __device__ __forceinline__ void minus_zero() {
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], VEC > 1 ? f[2 * i + 1] : 0.f);
+        for (int i = 0; i < WORDS; ++i) w[i] = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
+    }
+    // the sum rounded to T (in bf16 the same as the fp32 sum rounded: 24 bits are more than twice 8 and two)
+    __device__ __forceinline__ void add(const Vec &o) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(o.w[i]));
+            else {
+                const __nv_bfloat162 v = __hadd2(*(const __nv_bfloat162 *)&w[i], *(const __nv_bfloat162 *)&o.w[i]);
                 w[i] = *(const uint32_t *)&v;
             }
         }
@@ -80,16 +116,16 @@ struct Vec {
     }
 };
 
-// e4m3 bytes of VEC floats
+// e4m3 bytes of VEC floats times `inv`
 template <int VEC>
-__device__ __forceinline__ void st_e4m3(uint8_t *p, const float *f) {
+__device__ __forceinline__ void st_e4m3(uint8_t *p, const float2 *f, float inv) {
     if constexpr (VEC == 1) {
-        *p = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+        *p = __nv_cvt_float_to_fp8(f[0].x * inv, __NV_SATFINITE, __NV_E4M3);
     } else {
         uint16_t h[VEC / 2];
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i)
-            h[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            h[i] = __nv_cvt_float2_to_fp8x2(fmul2(f[i], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
         if constexpr (VEC == 2)
             *(uint16_t *)p = h[0];
         else
@@ -102,6 +138,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
+}
+// what brings a maximum of m to e4m3's largest value.  The reciprocal is off by one unit in the last place at most;
+// for m too small to have one in range it stops at the largest float, so that zeros stay zeros.
+__device__ __forceinline__ float e4m3_gain(float m) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
+    r *= kE4m3Max;
+    return m == 0.f ? 0.f : (r > 3.4e38f ? 3.4e38f : r);
 }
 struct Sum {
     static __device__ __forceinline__ float op(float a, float b) { return a + b; }
@@ -160,16 +204,17 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
         if (c < a.D) w[j].load(a.weight + c);
     }
     Vec<T, VEC> x[NV], r[NV];
+    constexpr int PAIRS = Vec<T, VEC>::PAIRS;
     const long long first = blockIdx.x * (long long)RPB, step = gridDim.x * (long long)RPB;
     auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
             x[j].zero();
-            r[j].zero();
+            r[j].minus_zero();
             if (row < a.rows && c < a.D) {
-                x[j].load((const T *)a.x + row * a.D + c);
-                if (a.residual) r[j].load((const T *)a.residual + row * a.D + c);
+                x[j].template load<true>((const T *)a.x + row * a.D + c);
+                if (a.residual) r[j].template load<true>((const T *)a.residual + row * a.D + c);
             }
         }
     };
@@ -177,21 +222,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
     for (long long base = first; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / TPR, at = row * a.D;
         const bool live = row < a.rows;
-        float f[NV][VEC], ss[1] = {0.f};
+        float2 f[NV][PAIRS], s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[j][i] = a.residual ? x[j].get(i) + r[j].get(i) : x[j].get(i);
-            x[j].set(f[j]);  // the stream as it is stored is what is normalised
+            x[j].add(r[j]);  // the stream as it is stored is what is normalised
             if (a.stream && live && c < a.D) x[j].store((T *)a.stream + at + c);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
+            for (int i = 0; i < PAIRS; ++i) {
                 f[j][i] = x[j].get(i);
-                ss[0] += f[j][i] * f[j][i];
+                s2 = ffma2(f[j][i], f[j][i], s2);
             }
         }
         load(row + step);
+        float ss[1] = {s2.x + s2.y};
         row_reduce<Sum, TPR, 1>(ss, buf, turn);
         const float rstd = rsqrtf(ss[0] / (float)a.D + a.eps);
         float amax[1] = {0.f};
@@ -199,13 +243,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                f[j][i] = f[j][i] * rstd * w[j].get(i);
-                if (FP8 && c < a.D) amax[0] = max_nan(amax[0], fabsf(f[j][i]));
+            for (int i = 0; i < PAIRS; ++i) {
+                f[j][i] = fmul2(fmul2(f[j][i], make_float2(rstd, rstd)), w[j].get(i));
+                if (FP8 && c < a.D) amax[0] = max_nan(amax[0], max_nan(fabsf(f[j][i].x), fabsf(f[j][i].y)));
             }
             if (!FP8 && live && c < a.D) {
                 Vec<T, VEC> y;
-                y.set(f[j]);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) y.set(i, f[j][i]);
                 y.store((T *)a.y + at + c);
             }
             if constexpr (FP8 && VEC == 8) {
@@ -213,12 +258,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
                     float m = amax[0];
                     for (int o = a.group / 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     amax[0] = 0.f;
-                    const float inv = m == 0.f ? 0.f : kE4m3Max / m;
                     if (live && c < a.D) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) f[j][i] *= inv;
-                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
-                        if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = m / kE4m3Max;
+                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], e4m3_gain(m));
+                        if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = m * (1.f / kE4m3Max);
                     }
                 }
             }
@@ -226,17 +268,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
         if constexpr (FP8) {
             if (!a.group) {
                 row_reduce<Max, TPR, 1>(amax, buf, turn);
-                const float m = amax[0], inv = m == 0.f ? 0.f : kE4m3Max / m;
+                const float m = amax[0], inv = e4m3_gain(m);
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int c = (j * TPR + t) * VEC;
-                    if (live && c < a.D) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) f[j][i] *= inv;
-                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j]);
-                    }
+                    if (live && c < a.D) st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], inv);
                 }
-                if (live && t == 0) a.scales[row] = m / kE4m3Max;
+                if (live && t == 0) a.scales[row] = m * (1.f / kE4m3Max);
             }
         }
     }
@@ -244,24 +282,36 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
 
 // ------------------------------------------------------------------ backward
 // A thread's columns are the same in every row, so its share of dweight stays in
-// registers and leaves as one partial row per block, which a second kernel adds in
-// the blocks' order.
+// registers; the rows of threads of a block add theirs up in order, and one partial row per block
+// leaves, which a second kernel adds in the blocks' order.
+constexpr int kBwdThreads = 512;  // on an SM at least: 128 registers a thread (at 96 they spill: 78 us for 59; at 140 two blocks of 160: 67)
+template <int TPR>
+constexpr int kBlock = TPR < 128 ? 128 : TPR;
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(TPR) rms_bwd_kernel(const T *dy, const T *h, const float *weight, float eps,
-                                                      const T *d_stream, T *dx, float *part, long long rows, int D) {
+__global__ void __launch_bounds__(kBlock<TPR>, kBwdThreads / kBlock<TPR> > 1 ? kBwdThreads / kBlock<TPR> : 1)
+    rms_bwd_kernel(const T *dy, const T *h, const float *weight, float eps, const T *d_stream, T *dx, float *part,
+                   long long rows, int D) {
+    constexpr int RPB = kBlock<TPR> / TPR, PAIRS = Vec<T, VEC>::PAIRS;
+    constexpr bool kAhead = TPR < 1024;  // registers for the weight and for the next row
     __shared__ float buf[2][32][2];
-    const int t = threadIdx.x;
+    __shared__ float2 shares[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NV * PAIRS : 1];
+    const int t = threadIdx.x % TPR;
     int turn = 0;
     Vec<float, VEC> w[NV];
-    float dw[NV][VEC];
+    float2 dw[NV][PAIRS];
+    auto load_weight = [&]() {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + t) * VEC;
-        w[j].zero();
-        if (c < D) w[j].load(weight + c);
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + t) * VEC;
+            w[j].zero();
+            if (c < D) w[j].load(weight + c);
+        }
+    };
+    load_weight();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dw[j][i] = 0.f;
-    }
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) dw[j][i] = make_float2(0.f, 0.f);
     Vec<T, VEC> hv[NV], dv[NV], sv[NV], hn[NV], dn[NV], sn[NV];
     auto load = [&](long long row) {
 #pragma unroll
@@ -271,55 +321,78 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const T *dy, const T *h, c
             dn[j].zero();
             sn[j].zero();
             if (row < rows && c < D) {
-                hn[j].load(h + row * D + c);
-                dn[j].load(dy + row * D + c);
-                if (d_stream) sn[j].load(d_stream + row * D + c);
+                hn[j].template load<true>(h + row * D + c);
+                dn[j].template load<true>(dy + row * D + c);
+                if (d_stream) sn[j].template load<true>(d_stream + row * D + c);
             }
         }
     };
-    load(blockIdx.x);
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-        float sum[2] = {0.f, 0.f};  // h^2 and dy w h
+    const long long first = blockIdx.x * (long long)RPB, step = gridDim.x * (long long)RPB;
+    if (kAhead) load(first + threadIdx.x / TPR);
+    for (long long base = first; base < rows; base += step) {
+        const long long row = base + threadIdx.x / TPR;
+        if (!kAhead) load(row);
+        float2 s0 = make_float2(0.f, 0.f), s1 = s0;  // h^2 and dy w h
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             hv[j] = hn[j];
             dv[j] = dn[j];
             sv[j] = sn[j];
         }
-        load(row + gridDim.x);
+        if (kAhead)
+            load(row + step);
+        else
+            load_weight();
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                sum[0] += hv[j].get(i) * hv[j].get(i);
-                sum[1] += dv[j].get(i) * w[j].get(i) * hv[j].get(i);
+            for (int i = 0; i < PAIRS; ++i) {
+                s0 = ffma2(hv[j].get(i), hv[j].get(i), s0);
+                s1 = ffma2(fmul2(dv[j].get(i), w[j].get(i)), hv[j].get(i), s1);
             }
+        float sum[2] = {s0.x + s0.y, s1.x + s1.y};
         row_reduce<Sum, TPR, 2>(sum, buf, turn);
         const float rstd = rsqrtf(sum[0] / (float)D + eps);
-        const float coef = rstd * rstd * (sum[1] / (float)D);
+        const float coef = -rstd * rstd * (sum[1] / (float)D);
+        const float2 r2 = make_float2(rstd, rstd), c2 = make_float2(coef, coef);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
-            if (c < D) {
-                float out[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = dv[j].get(i), x = hv[j].get(i);
-                    out[i] = sv[j].get(i) + rstd * (d * w[j].get(i) - x * coef);
-                    dw[j][i] += d * x * rstd;
-                }
+            if (row < rows && c < D) {
                 Vec<T, VEC> o;
-                o.set(out);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const float2 d = dv[j].get(i), x = hv[j].get(i);
+                    o.set(i, ffma2(ffma2(x, c2, fmul2(d, w[j].get(i))), r2, sv[j].get(i)));
+                    dw[j][i] = ffma2(fmul2(d, x), r2, dw[j][i]);
+                }
                 o.store(dx + row * D + c);
             }
         }
     }
     if (part) {
+        if constexpr (RPB > 1) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) shares[threadIdx.x / TPR][(j * PAIRS + i) * TPR + t] = dw[j][i];
+            __syncthreads();
+            if (threadIdx.x >= TPR) return;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i)
+                    for (int y = 1; y < RPB; ++y) {
+                        const float2 o = shares[y][(j * PAIRS + i) * TPR + t];
+                        dw[j][i] = make_float2(dw[j][i].x + o.x, dw[j][i].y + o.y);
+                    }
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + t) * VEC;
             Vec<float, VEC> o;
-            o.set(dw[j]);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) o.set(i, dw[j][i]);
             if (c < D) o.store(part + (long long)blockIdx.x * D + c);
         }
     }
@@ -345,8 +418,20 @@ __global__ void __launch_bounds__(1024) rms_dweight_reduce(const float *part, fl
 
 // ------------------------------------------------------------------ host side
 constexpr long long kMaxD = 16384;
-constexpr int kBwdBlocks = 608;  // four per SM
-constexpr int kFwdThreads = 152 * 1280;  // threads that walk the rows
+constexpr int kSMs = 152;
+constexpr int kBwdBlocks = 4 * kSMs;  // the most whose partial rows the workspace holds
+
+// Blocks of a kernel that the SMs hold at once.  A grid of just these walks the rows: one of 8 blocks per SM where
+// 5 fit leaves the last 3 to run by themselves (56 us for 48 at 16384 x 2560 in e4m3).
+template <auto Kernel, int THREADS>
+int resident_blocks() {
+    static const int n = [] {
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, Kernel, THREADS, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+        return per_sm * kSMs;
+    }();
+    return n;
+}
 
 ssd_status norm_fail(ssd_status st, const char *msg) {
     record_error(msg);
@@ -399,18 +484,15 @@ int vec_of(int64_t D) { return D % 8 == 0 ? 8 : (D % 2 == 0 ? 2 : 1); }
         }                                                                    \
     } while (0)
 
-unsigned fwd_blocks(long long rows, int rows_per_block, int threads) {
-    const long long all = (rows + rows_per_block - 1) / rows_per_block, most = kFwdThreads / threads;
-    return (unsigned)(all < most ? all : most);
-}
 template <typename T, bool FP8>
 cudaError_t forward(const NormArgs &a, cudaStream_t s) {
     const int64_t D = a.D;
-#define F(V, TPR, NV)                                                                       \
-    do {                                                                                    \
-        constexpr int rpb = TPR < 128 ? 128 / TPR : 1;                                      \
-        add_rms_kernel<T, V, TPR, NV, FP8>                                                  \
-            <<<fwd_blocks(a.rows, rpb, TPR * rpb), TPR * rpb, 0, s>>>(a);                   \
+#define F(V, TPR, NV)                                                                              \
+    do {                                                                                           \
+        constexpr int rpb = TPR < 128 ? 128 / TPR : 1;                                             \
+        const long long all = (a.rows + rpb - 1) / rpb;                                            \
+        const int most = resident_blocks<add_rms_kernel<T, V, TPR, NV, FP8>, TPR * rpb>();         \
+        add_rms_kernel<T, V, TPR, NV, FP8><<<(unsigned)(all < most ? all : most), TPR * rpb, 0, s>>>(a); \
     } while (0)
     NORM_BY_D(F);
 #undef F
@@ -420,10 +502,15 @@ int bwd_blocks(int64_t rows) { return (int)(rows < kBwdBlocks ? rows : kBwdBlock
 template <typename T>
 cudaError_t backward(const void *dy, const void *h, const float *weight, float eps, const void *ds, void *dx, float *dw,
                      int64_t rows, int64_t D, float *part, cudaStream_t s) {
-    const int blocks = bwd_blocks(rows);
+    int blocks = bwd_blocks(rows);
 #define F(V, TPR, NV)                                                                                     \
-    rms_bwd_kernel<T, V, TPR, NV><<<blocks, TPR, 0, s>>>((const T *)dy, (const T *)h, weight, eps,        \
-                                                         (const T *)ds, (T *)dx, dw ? part : nullptr, rows, (int)D)
+    do {                                                                                                  \
+        const int most = resident_blocks<rms_bwd_kernel<T, V, TPR, NV>, kBlock<TPR>>();                   \
+        if (blocks > most) blocks = most;                                                                 \
+        rms_bwd_kernel<T, V, TPR, NV><<<blocks, kBlock<TPR>, 0, s>>>((const T *)dy, (const T *)h, weight, eps,    \
+                                                             (const T *)ds, (T *)dx, dw ? part : nullptr, \
+                                                             rows, (int)D);                               \
+    } while (0)
     NORM_BY_D(F);
 #undef F
     cudaError_t e = cudaGetLastError();

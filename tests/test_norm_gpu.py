@@ -98,6 +98,22 @@ def test_zero_rows_and_non_finite_rows(nm):
     assert torch.isfinite(y[[0, 1, 4, 5]]).all()
 
 
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("top", [1e-38, 1e-44, 2e38])
+def test_fp8_scales_at_the_ends_of_fp32(nm, group, top):
+    """Largest values with no reciprocal in fp32: what is zero stays zero, nothing becomes NaN."""
+    x = torch.ones(2, 256, device="cuda")
+    x[:, ::2] = 0
+    w = torch.full((256,), top, device="cuda")
+    y8, s, _ = nm.add_rms_norm_fp8(x, w, 1e-5, group=group)
+    q = y8.float()
+    assert torch.all(q[:, ::2] == 0) and torch.isfinite(q).all() and torch.isfinite(s).all() and q.abs().max() <= 448
+    if top > 1e-40:  # a normal maximum: the scale times e4m3's largest value gives it back
+        assert torch.all(q[:, 1::2] > 0)
+    if top > 1:
+        assert torch.all(q[:, 1::2] == 448)
+
+
 def test_in_place_stream_and_fixed_order(nm):
     import ctypes
     from state_space_model_mamba_gb300 import ssd
