@@ -33,12 +33,13 @@ constexpr int kCompute = 256, kThreads = kCompute + 32;
 constexpr uint32_t kOffZero = 0, kOffW = 8192, kOffSZ = 16384, kOffZ = kOffSZ + 16384, kOffP = kOffSZ, kOffZlo = 40960,
                    kOffDS = 49152, kOffDV = 65536, kOffPlo = kOffDV, kOffQK = 81920, kOffSmall = 114688;
 struct Small {
+    float beta[kChunk];  // as the image has them, one copy
     float2 gam[kChunk];
-    float beta[kChunk];
     uint64_t qk, in, ds, p, out, m[2];
     uint32_t tmem;
     int err;
 };
+constexpr uint32_t kGateBytes = 3 * kChunk * 4, kGateAt = 2 * kChunk * 4;
 constexpr uint32_t kBytes = kOffSmall + sizeof(Small);
 static_assert(2 * (kBytes + 1024) <= 233472, "two blocks per SM");
 struct GradMaps {
@@ -112,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         auto load_in = [&](const Item &x) {
             if (lane == 0) {
                 const char *state = cp.w.states + (x.cs * cp.n + x.chunk) * kStateTile;
-                mbar_arrive_expect_tx(&bar_in, 16384 + kStateTile + kErrTile + kDvLoTile);
+                mbar_arrive_expect_tx(&bar_in, 16384 + kStateTile + kErrTile + kDvLoTile + kGateBytes);
+                bulk_load(smem_u32(sm.beta), cp.image((long long)x.bi * p.H + x.h, x.chunk) + kGateAt, kGateBytes, &bar_in);
                 bulk_load(base + kOffSZ, state, 16384, &bar_in);
                 bulk_load(base + kOffZ, cp.w.errs + (x.cs * cp.n + x.chunk) * kErrTile, kErrTile, &bar_in);
                 tma_tile(base + kOffDV, &maps.d_o, &bar_in, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
@@ -246,17 +248,12 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 for (int it = 0; it < items && ok; ++it, ++n) {
                     const uint32_t ph = n & 1;
                     const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
-                    const float *gates = (const float *)cp.image(bh, chunk);
                     const int wr = tid & 63, wc = 2 * (tid >> 6);
-                    const float wf = __ldg(gates + 2 * kChunk + wr) * __ldg(gates + kChunk + wr), eg = __ldg(gates + i);
-                    if (tid < kChunk) {
-                        sm.gam[tid] = __ldg((const float2 *)(gates + 3 * kChunk) + tid);
-                        sm.beta[tid] = __ldg(gates + 2 * kChunk + tid);
-                    }
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph));
                     if (!ok) break;
                     tc_fence_after();
+                    const float2 gi = sm.gam[i], gr = sm.gam[wr], gc = sm.gam[kChunk - 1];
+                    const float wf = sm.beta[wr] * exp2_approx((gc.x - gr.x) + (gc.y - gr.y)), eg = exp2_approx(gi.x + gi.y);
                     // W, in place of what dV lost, from both parts of Z (16 columns of row tid % 64)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -268,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                         const uint4 o = pack8(w);
                         st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
                     }
-                    const float2 gi = sm.gam[i];
                     const float f = keys ? -1.f : p.scale;
                     float rs = 0.f, cs_[32];
 #pragma unroll
