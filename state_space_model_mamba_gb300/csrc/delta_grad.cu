@@ -6,11 +6,12 @@
 //     Nm_ij = scale D_ij beta_j (dO_i . Z_j), j <= i;    M_ij = -D_ij beta_j (dV_i . Z_j), j < i
 //     dQ = scale e^gamma o (dO S^T) + Nm K
 //     dK = -e^gamma o (dV S^T) + M K + Nm^T Q + M^T K + (beta e^(gamma_C - gamma) o Z) dS^T
-// in two groups of products: [Q; K] K^T, and [dO; dV] on S and Z at once (128 rows,
-// 192 columns); then, into one accumulator whose rows 0 .. 63 are dQ and 64 .. 127 dK,
+// in three groups of products: [dO; dV] S^T (128 rows); [dO; dV] Z^T and [Q; K] K^T in its
+// place, once the threads have added it, times its gate, to the sums; then, on top of the sums,
+// whose rows 0 .. 63 are dQ and 64 .. 127 dK,
 // [Nm; M] K, [0; W] dS^T with W = beta e^(gamma_C - gamma) o Z, and [0 | (Nm; M)]^T [Q; K] (the
 // zero blocks keep the products that are dK's alone off the dQ rows).  The heads of a key
-// group are walked by one block, which adds them up in registers: dq and dk are written
+// group are walked by one block, which adds them up in tensor memory: dq and dk are written
 // once, in a fixed order.  Z, S, Nm and M come as hi + lo parts: what a token reads of S and
 // what the chunk has written over it cancel, and the share of dg that passes between tokens
 // of the chunk is made here,
@@ -35,7 +36,7 @@ constexpr uint32_t kOffZero = 0, kOffW = 8192, kOffSZ = 16384, kOffZ = kOffSZ + 
 struct Small {
     float beta[kChunk];  // as the image has them, one copy
     float2 gam[kChunk];
-    uint64_t qk, in, ds, p, out, m[2];
+    uint64_t qk, in, ds, x, p, m[3];
     uint32_t tmem;
     int err;
 };
@@ -51,8 +52,8 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
     // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Small &sm = *(Small *)(smem_raw + kOffSmall);
-    uint64_t &bar_qk = sm.qk, &bar_in = sm.in, &bar_ds = sm.ds, &bar_p = sm.p, &bar_out = sm.out;
-    uint64_t(&bar_m)[2] = sm.m;
+    uint64_t &bar_qk = sm.qk, &bar_in = sm.in, &bar_ds = sm.ds, &bar_x = sm.x, &bar_p = sm.p;
+    uint64_t(&bar_m)[3] = sm.m;
     const DeltaParams &p = cp.p;
     const uint32_t base = smem_u32(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -62,9 +63,8 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         mbar_init(&bar_in, 1);
         mbar_init(&bar_ds, 1);
         mbar_init(&bar_p, kCompute / 32);
-        mbar_init(&bar_out, kCompute / 32);
-        mbar_init(&bar_m[0], 1);
-        mbar_init(&bar_m[1], 1);
+        mbar_init(&bar_x, kCompute / 32);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_m[i], 1);
         mbar_fence_init();
         sm.err = (base & 1023u) ? 1 : 0;
     }
@@ -134,11 +134,11 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 prefetch_tile(&maps.dv, 64 * x.slice, x.h, x.chunk * kChunk, x.bi);
             }
         };
-        const uint32_t i_ac = idesc_bf16(128, 192, false, false), i_c = idesc_bf16(128, 64, false, false),
+        const uint32_t i_c = idesc_bf16(128, 64, false, false),
                        i_b = idesc_bf16(128, 128, false, false), i_d = idesc_bf16(128, 64 * halves, false, true),
                        i_e = idesc_bf16(128, 64 * halves, true, true);
         const uint64_t dDV = sdesc(base + kOffDV, 16, 1024), dSZ = sdesc(base + kOffSZ, 16, 1024),
-                       dZlo = sdesc(base + kOffZlo, 16, 1024), dVlo = sdesc(base + kOffZero, 16, 1024),
+                       dZ = sdesc(base + kOffZ, 16, 1024), dZlo = sdesc(base + kOffZlo, 16, 1024), dVlo = sdesc(base + kOffZero, 16, 1024),
                        dDS = sdesc(base + kOffDS, 16, 1024), dP = sdesc(base + kOffP, 16, 1024),
                        dPlo = sdesc(base + kOffPlo, 16, 1024), dK = sdesc(base + kOffQK + 8192, 16384, 1024),
                        dQKt = sdesc(base + kOffQK, 16384, 1024), dQK = sdesc(base + kOffQK, 16, 1024),
@@ -159,21 +159,15 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         int qk_loaded = loaded, ds_loaded = 0, done = 0, it = 0;
         while (more) {
             const uint32_t ph = n & 1;
-            ok = mbar_wait(&bar_in, ph) && mbar_wait(&bar_qk, u & 1) && (n == 0 || mbar_wait(&bar_out, (n - 1) & 1));
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_in, ph)))) break;
             tc_fence_after();
             if (lane == 0) {
-                for (int ks = 0; ks < nks; ++ks)
-                    mma_bf16(tm + 192, sdesc_add(dQK, (ks >> 2) * 16384 + (ks & 3) * 32),
-                             sdesc_add(dKk, (ks >> 2) * 16384 + (ks & 3) * 32), i_c, ks > 0);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dSZ, ks * 32), i_b, ks > 0);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dDS, ks * 32), i_b, true);  // S lo
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dDV, ks * 32), sdesc_add(dZlo, ks * 32), i_c, true);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dVlo, ks * 32), sdesc_add(dSZ, ks * 32), i_ac, true);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dVlo, ks * 32), sdesc_add(dSZ, ks * 32), i_b, true);
                 mma_commit(&bar_m[0]);
             }
             // the item after this one
@@ -188,12 +182,27 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 bulk_load(base + kOffDS, cp.w.dstates + (x.cs * cp.n + x.chunk) * kDStateTile, kDStateTile, &bar_ds);
             }
             ds_loaded = n + 1;
+            ok = mbar_wait(&bar_x, ph) && mbar_wait(&bar_qk, u & 1);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dZ, ks * 32), i_c, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dDV, ks * 32), sdesc_add(dZlo, ks * 32), i_c, true);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dVlo, ks * 32), sdesc_add(dZ, ks * 32), i_c, true);
+                for (int ks = 0; ks < nks; ++ks)
+                    mma_bf16(tm + 64, sdesc_add(dQK, (ks >> 2) * 16384 + (ks & 3) * 32),
+                             sdesc_add(dKk, (ks >> 2) * 16384 + (ks & 3) * 32), i_c, ks > 0);
+                mma_commit(&bar_m[1]);
+            }
             ok = mbar_wait(&bar_p, ph) && mbar_wait(&bar_ds, ph);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dP, ks * 32), sdesc_add(dK, ks * 2048), i_d, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dP, ks * 32), sdesc_add(dK, ks * 2048), i_d, true);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dPlo, ks * 32), sdesc_add(dK, ks * 2048), i_d, true);
 #pragma unroll
@@ -203,16 +212,15 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 // W, where dV lo was, below the zeros
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + 128, sdesc_add(dVlo, ks * 32), sdesc_add(dDS, ks * 32), i_b, true);
-                mma_commit(&bar_m[1]);
+                mma_commit(&bar_m[2]);
             }
             __syncwarp();
             done = n + 1;
-            if (next) {  // all but Q and K is done with; those, too, once the threads have read their rows
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph)))) break;
+            if (next) {  // everything has been read
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph)))) break;
                 load_in(y);
                 ++loaded;
                 if (next_unit != unit) {
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_out, ph)))) break;
                     load_qk(y);
                     ++qk_loaded;
                     ++u;
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         if (qk_loaded) mbar_wait(&bar_qk, (qk_loaded - 1) & 1);
         if (loaded) mbar_wait(&bar_in, (loaded - 1) & 1);
         if (ds_loaded) mbar_wait(&bar_ds, (ds_loaded - 1) & 1);
-        if (done) mbar_wait(&bar_m[1], (done - 1) & 1);
+        if (done) mbar_wait(&bar_m[2], (done - 1) & 1);
     } else {
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane, i = row & 63;
         const bool keys = row >= kChunk;     // rows 64 .. 127: dV, M, dK
@@ -236,9 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
             const int chunk = unit % cp.n, grp = unit / cp.n % p.G, bi = unit / cp.n / p.G;
             const int V = valid_tokens(p, bi), t0 = chunk * kChunk, live_n = V - t0, tok = t0 + i;
             const bool live = i < live_n;
-            float2 acc[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = make_float2(0.f, 0.f);
+            const uint32_t tx = tmem_addr(tm, 32 * quarter, 64 * half), tr = tx + 128;  // 64 columns of dO S^T and of the sums
             if (live_n > 0) {
                 if (live_n < kChunk) {  // q and k rows of absent tokens are made zero
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar_qk, u & 1));
@@ -248,12 +254,43 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                 for (int it = 0; it < items && ok; ++it, ++n) {
                     const uint32_t ph = n & 1;
                     const long long bh = (long long)bi * p.H + grp * p.hpg + it / nsl, cs = bh * nsl + it % nsl;
-                    const int wr = tid & 63, wc = 2 * (tid >> 6);
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph));
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[0], ph) && mbar_wait(&bar_in, ph) && mbar_wait(&bar_qk, u & 1));
                     if (!ok) break;
                     tc_fence_after();
+                    const int wr = tid & 63, wc = 2 * (tid >> 6);
                     const float2 gi = sm.gam[i], gr = sm.gam[wr], gc = sm.gam[kChunk - 1];
                     const float wf = sm.beta[wr] * exp2_approx((gc.x - gr.x) + (gc.y - gr.y)), eg = exp2_approx(gi.x + gi.y);
+                    const float f = keys ? -1.f : p.scale, fa = f * eg;
+                    float read = 0.f;
+                    if (half < (int)halves) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float2 a[8], b[8];
+                            if (it > 0) {
+                                tmem_ld16x2(tx + 16 * q, tr + 16 * q, (float *)a, (float *)b);
+                            } else {
+                                tmem_ld16(tx + 16 * q, (float *)a);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) b[e] = make_float2(0.f, 0.f);
+                            }
+                            // with the row's own q or k: what it reads of S
+                            const uint32_t own = base + kOffQK + half * 16384;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) read = dot8(ld_shared_v4(own + sw128_chunk(row, 2 * q + c)), a + 4 * c, read);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) b[e] = ffma2(a[e], make_float2(fa, fa), b[e]);
+                            __syncwarp();
+                            tmem_st16(tr + 16 * q, (const float *)b);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_x);
+                    (keys ? cp.w.fk : cp.w.fq)[(cs * 2 + half) * cp.n * kChunk + tok] = live ? fa * read : 0.f;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
+                    if (!ok) break;
+                    tc_fence_after();
                     // W, in place of what dV lost, from both parts of Z (16 columns of row tid % 64)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -265,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                         const uint4 o = pack8(w);
                         st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
                     }
-                    const float f = keys ? -1.f : p.scale;
                     float rs = 0.f, cs_[32];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float a[16], b[16];
-                        tmem_ld16x2(tmem_addr(tm, 32 * quarter, 128 + 32 * half + 16 * q),
-                                    tmem_addr(tm, 32 * quarter, 192 + 32 * half + 16 * q), a, b);
+                        __syncwarp();
+                        tmem_ld16x2(tmem_addr(tm, 32 * quarter, 32 * half + 16 * q),
+                                    tmem_addr(tm, 32 * quarter, 64 + 32 * half + 16 * q), a, b);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int j = 32 * half + 16 * q + e;
@@ -304,40 +341,25 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                     float *pe = cp.w.pe + (cs * cp.n + chunk) * 512;
                     pe[half * 128 + row] = rs;
                     pe[256 + quarter * 64 + 32 * half + lane] = cs_[0];
-                    const float fa = f * eg;
-                    float read = 0.f;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[1], ph));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (half < (int)halves) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float2 a[8], b[8];
-                            const uint32_t at = tmem_addr(tm, 32 * quarter, 64 * half + 16 * q);
-                            tmem_ld16x2(at, at + 128, (float *)a, (float *)b);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float2 &x = acc[8 * q + e];
-                                x = ffma2(b[e], make_float2(1.f, 1.f), ffma2(a[e], make_float2(fa, fa), x));
-                            }
-                            // with the row's own q or k: what it reads of S
-                            const uint32_t own = base + kOffQK + half * 16384;
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) read = dot8(ld_shared_v4(own + sw128_chunk(row, 2 * q + c)), a + 4 * c, read);
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_out);
-                    (keys ? cp.w.fk : cp.w.fq)[(cs * 2 + half) * cp.n * kChunk + tok] = live ? fa * read : 0.f;
                 }
                 ++u;
             }
-            if (tok < p.L && ok) {
-                bf16 *dst = (bf16 *)(keys ? p.dk : p.dq) + (((long long)bi * p.L + tok) * p.G + grp) * p.N + 64 * half;
+            if (live_n > 0 && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], (n - 1) & 1));
+                tc_fence_after();
+            }
+            bf16 *dst = (bf16 *)(keys ? p.dk : p.dq) + (((long long)bi * p.L + tok) * p.G + grp) * p.N + 64 * half;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (64 * half + 8 * c < p.N) *(uint4 *)(dst + 8 * c) = live ? pack8(acc + 4 * c) : make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < 4; ++q) {
+                float2 r[8];
+                if (live_n > 0) {
+                    __syncwarp();
+                    tmem_ld16(tr + 16 * q, (float *)r);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (ok && tok < p.L && 64 * half + 16 * q + 8 * c < p.N)
+                        *(uint4 *)(dst + 16 * q + 8 * c) = live ? pack8(r + 4 * c) : make_uint4(0, 0, 0, 0);
             }
         }
         if (!ok) sm.err = 1;
