@@ -29,10 +29,18 @@ using namespace tc;
 
 constexpr int kThreads = 128;
 constexpr int kHeadsPer = 4;          // heads of a group per block
-constexpr int kLdD = 20;              // floats per row of E's diagonal blocks: 16-byte pieces
-constexpr uint32_t kAccCols = 128;    // the products; from column 64 the solved columns' shares
+constexpr int kLdD = 16;              // floats per row of E's diagonal blocks
 // over the tiles, once the products have read them: E hi, E lo [64][64] SW128, beta y hi, lo [2 column octets][16 row octets][128]
-constexpr uint32_t kOffE = 0, kOffZ = 16384;
+constexpr uint32_t kOffE = 0, kOffZ = 16384, kOffSmall = 32768;
+struct Small {
+    float d[kChunk * kLdD];
+    float2 gam[kChunk];   // gamma log2(e), hi and lo
+    float beta[kChunk];
+    uint64_t load, mma, step;
+    uint32_t tmem;
+};
+constexpr uint32_t kBytes = kOffSmall + sizeof(Small);
+static_assert(6 * (kBytes + 1024) <= 233472, "six blocks per SM");
 
 struct PrepMaps {
     CUtensorMap k, q;
@@ -53,13 +61,17 @@ __device__ __forceinline__ Pair times_log2e(Pair a) {
 }
 
 // Grid: one block per (b, group, slice of the group's heads, chunk).
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bar_load, bar_mma, bar_step;
-    __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_d[kChunk * kLdD];
-    __shared__ float2 s_gam[kChunk];   // gamma log2(e), hi and lo
-    __shared__ float s_beta[kChunk];
+// ALONE: the group has one head, whose right-hand sides take the products' place in tensor memory.
+template <bool ALONE>
+__global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps) {
+    // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Small &sm = *(Small *)(smem_raw + kOffSmall);
+    uint64_t &bar_load = sm.load, &bar_mma = sm.mma, &bar_step = sm.step;
+    float *const s_d = sm.d, *const s_beta = sm.beta;
+    float2 *const s_gam = sm.gam;
+    // the products, then the right-hand sides
+    constexpr uint32_t kAccCols = ALONE ? 64 : 128, kRhs = ALONE ? 0 : 64;
     const DeltaParams &p = cp.p;
     const int slices = (p.hpg + kHeadsPer - 1) / kHeadsPer;
     const int chunk = blockIdx.x % cp.n, slice = blockIdx.x / cp.n % slices;
@@ -68,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
     if (blockIdx.x == 0) write_status(p);
     const int V = valid_tokens(p, bi), t0 = chunk * kChunk;
     if (t0 >= V) return;
-    const uint32_t kq = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t kq = smem_u32(smem_raw);
     const uint32_t halves = p.N > 64 ? 2u : 1u;
     // where rows lie changes from block to block, so that the long solves do not always land on the same schedulers
     const uint32_t hash = blockIdx.x * 0x9E3779B1u;
@@ -87,14 +99,14 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 tma_tile(kq + kb * 16384u + (k_off ^ 8192u) + 4096u * x, &maps.q, &bar_load, 64 * kb, grp, tok, bi);
             }
     }
-    if (warp == 0) tmem_alloc(&s_tmem, kAccCols);
+    if (warp == 0) tmem_alloc(&sm.tmem, kAccCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = s_tmem;
-    bool ok = true;
+    const uint32_t tm = sm.tmem;
+    bool ok = !(kq & 1023u);
     if (warp == 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar_load, 0));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_load, 0));
         if (ok && lane == 0) {
             const int nks = (p.N + 15) / 16;
             for (int ks = 0; ks < nks; ++ks)
@@ -164,20 +176,29 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 if (!live) r[e] = 0.f;
             }
         };
-        if (keys)
+        const bool bwd = cp.w.states != nullptr, solves = keys || !bwd;
+        // where columns 16 jb of a right-hand side lie: in place of the products they come from, or behind them
+        auto rhs = [&](int jb) { return tm + kRhs + (uint32_t)(ALONE ? (16 * jb) ^ (32 * flip) : 16 * jb); };
+        if (solves)
             for (int jb = 0; jb <= last; ++jb) {
                 float2 r[8];
-                decayed(jb, 1.f, (float(&)[16])r);
-                store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb, r);
-                store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb + 1, r + 4);
-                if (jb == i >> 4) {
+                decayed(jb, keys ? -1.f : p.scale, (float(&)[16])r);
+                __syncwarp();
+                tmem_st16(tmem_addr(rhs(jb), 32 * warp, 0), (const float *)r);
+                if (keys) {  // -E
+                    store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb, r);
+                    store_parts8(kq + kOffE, kq + kOffE + 8192, i, 2 * jb + 1, r + 4);
+                    if (jb == i >> 4) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *(float4 *)(s_d + i * kLdD + 4 * e) = make_float4(r[2 * e].x, r[2 * e].y, r[2 * e + 1].x, r[2 * e + 1].y);
+                        for (int e = 0; e < 4; ++e)
+                            *(float4 *)(s_d + i * kLdD + 4 * e) = make_float4(r[2 * e].x, r[2 * e].y, r[2 * e + 1].x, r[2 * e + 1].y);
+                    }
                 }
             }
+        __syncwarp();
+        tmem_wait_st();
+        tc_fence_before();
         __syncthreads();
-        const bool bwd = cp.w.states != nullptr;
         char *mat = img + kImgMat + (bwd && !keys ? 2 * kSquare : 0);
         auto store_block = [&](int jb, const float2 *y) {  // hi and lo parts, neighbouring rows on neighbouring addresses
 #pragma unroll
@@ -202,31 +223,12 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 decayed(jb, p.scale, (float(&)[16])y);
                 if (jb <= (i >> 4)) store_block(jb, y);
             }
-        const bool solves = keys || !bwd;
         const uint32_t zt = kq + kOffZ + (tid >> 3) * 128 + (tid & 7) * 16;
         for (int jb = 3; jb >= 0; --jb) {
             float2 y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = make_float2(0.f, 0.f);
             if (solves && jb <= last) {
-                if (keys) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t at = kq + kOffE + sw128_chunk(i, 2 * jb + c);
-                        join8(ld_shared_v4(at), ld_shared_v4(at + 8192), y + 4 * c);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = make_float2(-y[e].x, -y[e].y);
-                } else {
-                    decayed(jb, p.scale, (float(&)[16])y);
-                }
-                if (jb < 3) {
-                    float2 g[8];
-                    __syncwarp();
-                    tmem_ld16(tmem_addr(tm, 32 * warp, 64 + 16 * jb), (float *)g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = ffma2(g[e], make_float2(-1.f, -1.f), y[e]);
-                }
+                __syncwarp();
+                tmem_ld16(tmem_addr(rhs(jb), 32 * warp, 0), (float *)y);
                 // the triangle of the block: from the last column, each solved one taken off those before it
                 float *yy = (float *)y;
                 const float *e0 = s_d + 16 * jb * kLdD;
@@ -240,10 +242,10 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
 #pragma unroll
                     for (int e = 0; e < (m + 3) / 4; ++e) {
                         const float4 v = w[e];
-                        yy[4 * e] = fmaf(-zm, v.x, yy[4 * e]);
-                        if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(-zm, v.y, yy[4 * e + 1]);
-                        if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(-zm, v.z, yy[4 * e + 2]);
-                        if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(-zm, v.w, yy[4 * e + 3]);
+                        yy[4 * e] = fmaf(zm, v.x, yy[4 * e]);
+                        if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(zm, v.y, yy[4 * e + 1]);
+                        if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(zm, v.z, yy[4 * e + 2]);
+                        if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
                     }
                 }
                 if (jb > 0) {
@@ -266,11 +268,14 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const ChunkParams 
                 __syncthreads();
                 if (tid == 0) {
                     tc_fence_after();
-                    const uint32_t idesc = idesc_bf16(128, 16 * jb, false, true);
                     const uint64_t dZ = sdesc_plain(kq + kOffZ, 2048, 128), dE = sdesc_mnmajor(kq + kOffE, jb, 8192);
-                    mma_bf16(tm + 64, dZ, dE, idesc, jb < 3);
-                    mma_bf16(tm + 64, dZ, sdesc_add(dE, 8192), idesc, true);
-                    mma_bf16(tm + 64, sdesc_add(dZ, 4096), dE, idesc, true);
+                    // columns 0 .. 31, then those behind: apart, where the products lie in the other order
+                    for (int c = 0; c < 16 * jb; c += 32) {
+                        const uint32_t d = rhs(c / 16), idesc = idesc_bf16(128, min(32, 16 * jb - c), false, true);
+                        mma_bf16(d, dZ, sdesc_add(dE, 2 * c), idesc, true);
+                        mma_bf16(d, dZ, sdesc_add(dE, 8192 + 2 * c), idesc, true);
+                        mma_bf16(d, sdesc_add(dZ, 4096), sdesc_add(dE, 2 * c), idesc, true);
+                    }
                     mma_commit(&bar_step);
                 }
             }
@@ -305,11 +310,13 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
-    const int bytes = 1024 + 32768;  // the tiles, then E and beta y
     const unsigned grid = (unsigned)c.n * ((p.hpg + kHeadsPer - 1) / kHeadsPer) * p.b * p.G;
-    if ((e = cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    delta_prep_kernel<<<grid, kThreads, bytes, s>>>(c, maps);
-    return cudaGetLastError();
+    auto launch = [&](auto kernel) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes)) != cudaSuccess) return e;
+        kernel<<<grid, kThreads, kBytes, s>>>(c, maps);
+        return cudaGetLastError();
+    };
+    return p.hpg == 1 ? launch(delta_prep_kernel<true>) : launch(delta_prep_kernel<false>);
 }
 
 }  // namespace delta
