@@ -28,7 +28,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 128;
-constexpr int kHeadsPer = 4;          // heads of a group per block
+constexpr int kHeadsPer = 6;          // heads of a group per block at most
 constexpr int kLdD = 16;              // floats per row of E's diagonal blocks
 // over the tiles, once the products have read them: E hi, E lo [64][64] SW128, beta y hi, lo [2 column octets][16 row octets][128]
 constexpr uint32_t kOffE = 0, kOffZ = 16384, kOffSmall = 32768;
@@ -60,10 +60,10 @@ __device__ __forceinline__ Pair times_log2e(Pair a) {
     return Pair{p + e, e - ((p + e) - p)};
 }
 
-// Grid: one block per (b, group, slice of the group's heads, chunk).
-// ALONE: the group has one head, whose right-hand sides take the products' place in tensor memory.
+// Grid: one block per (b, group, `per` of the group's heads, chunk).
+// ALONE: per is 1, and the head's right-hand sides take the products' place in tensor memory.
 template <bool ALONE>
-__global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps) {
+__global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps, int per) {
     // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Small &sm = *(Small *)(smem_raw + kOffSmall);
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
     // the products, then the right-hand sides
     constexpr uint32_t kAccCols = ALONE ? 64 : 128, kRhs = ALONE ? 0 : 64;
     const DeltaParams &p = cp.p;
-    const int slices = (p.hpg + kHeadsPer - 1) / kHeadsPer;
+    const int slices = (p.hpg + per - 1) / per;
     const int chunk = blockIdx.x % cp.n, slice = blockIdx.x / cp.n % slices;
     const int bg = blockIdx.x / cp.n / slices, bi = bg / p.G, grp = bg % p.G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
     int steps = 0;                        // groups of shares issued
     const int i = (tid & 63) ^ (32 * flip);  // the row's token
     const bool keys = (tid < kChunk) == (k_off == 0), live = t0 + i < V;  // rows of absent tokens may hold anything: made zero
-    const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * kHeadsPer);
+    const int h_end = min((grp + 1) * p.hpg, grp * p.hpg + (slice + 1) * per);
     float2 next_g = make_float2(0.f, 0.f), next_b = next_g;  // the next head's gates of tokens 2 lane, 2 lane + 1
     auto fetch = [&](int h) {
         const long long at = ((long long)bi * p.H + h) * p.L + t0 + 2 * lane;
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
         next_g = make_float2(r0 ? clamp_log_decay(p.g[at]) : 0.f, r1 ? clamp_log_decay(p.g[at + 1]) : 0.f);
         next_b = make_float2(r0 ? p.beta[at] : 0.f, r1 ? p.beta[at + 1] : 0.f);
     };
-    if (warp == 0) fetch(grp * p.hpg + slice * kHeadsPer);
-    for (int h = grp * p.hpg + slice * kHeadsPer; h < h_end; ++h) {
+    if (warp == 0) fetch(grp * p.hpg + slice * per);
+    for (int h = grp * p.hpg + slice * per; h < h_end; ++h) {
         const long long bh = (long long)bi * p.H + h;
         char *img = cp.image(bh, chunk);
         if (warp == 0) {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
             *(float2 *)(gates + 2 * kChunk + i0) = beta;
             *(float4 *)(gates + 3 * kChunk + 2 * i0) = make_float4(l0.hi, l0.lo, l1.hi, l1.lo);
         }
-        if (h == grp * p.hpg + slice * kHeadsPer) {
+        if (h == grp * p.hpg + slice * per) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_mma, 0));
             tc_fence_after();
         }
@@ -310,13 +310,18 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
-    const unsigned grid = (unsigned)c.n * ((p.hpg + kHeadsPer - 1) / kHeadsPer) * p.b * p.G;
+    // A block's heads share the two products: equal shares of a group, up to 6 heads (80 heads in 16 groups: one block of
+    // 5 took 275 us where blocks of 4 and 1 took 292; 64 heads in 8 groups: 281 us in fours, 284 in eights,
+    // 329 alone), but one by one while all of them have a place at once.
+    const int shares = (p.hpg + kHeadsPer - 1) / kHeadsPer;
+    const int per = (long long)c.n * p.b * p.H <= 6 * kSMs ? 1 : (p.hpg + shares - 1) / shares;
+    const unsigned grid = (unsigned)c.n * ((p.hpg + per - 1) / per) * p.b * p.G;
     auto launch = [&](auto kernel) {
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes)) != cudaSuccess) return e;
-        kernel<<<grid, kThreads, kBytes, s>>>(c, maps);
+        kernel<<<grid, kThreads, kBytes, s>>>(c, maps, per);
         return cudaGetLastError();
     };
-    return p.hpg == 1 ? launch(delta_prep_kernel<true>) : launch(delta_prep_kernel<false>);
+    return per == 1 ? launch(delta_prep_kernel<true>) : launch(delta_prep_kernel<false>);
 }
 
 }  // namespace delta

@@ -134,7 +134,8 @@ def test_valid_len_and_garbage_past_it(dl, bf16, valid):
 
 
 @pytest.mark.parametrize("shape, valid", [((5, 300, 40, 64, 64, 8), None), ((4, 420, 48, 40, 128, 16), [420, 0, 65, 192]),
-                                          ((2, 190, 90, 128, 32, 90), [1, 190]), ((200, 70, 1, 64, 64, 1), None)])
+                                          ((2, 190, 90, 128, 32, 90), [1, 190]), ((200, 70, 1, 64, 64, 1), None),
+                                          ((2, 130, 160, 8, 16, 2), None)])
 def test_more_chains_than_blocks_run_at_once(dl, shape, valid):
     x = draw(*shape, seed=sum(shape))
     compare(run(dl, x, True, 0.3, valid=valid), x, True, 0.3, valid=valid)
