@@ -4,6 +4,12 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <map>
+#include <memory>
+#include <mutex>
+#include <type_traits>
+#include <utility>
+
 #include "delta_chunk.cuh"
 
 namespace ssd {
@@ -115,6 +121,85 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
     return off;
 }
 
+// The same problem, batch rows b0 .. b0 + nb - 1 of it.
+ChunkParams batch_part(const ChunkParams &all, int b0, int nb) {
+    ChunkParams c = all;
+    DeltaParams &p = c.p;
+    const size_t keys = (size_t)b0 * p.L * p.G * p.N, values = (size_t)b0 * p.L * p.H * p.P, gates = (size_t)b0 * p.H * p.L,
+                 state = (size_t)b0 * p.H * p.P * p.N, cs = (size_t)b0 * p.H * slices_of(p);
+    auto move = [](auto *&x, size_t bytes) {
+        if (x) x = (std::remove_reference_t<decltype(x)>)((char *)x + bytes);
+    };
+    p.b = nb;
+    move(p.q, 2 * keys), move(p.k, 2 * keys), move(p.dq, 2 * keys), move(p.dk, 2 * keys);
+    move(p.v, 2 * values), move(p.o, 2 * values), move(p.d_o, 2 * values), move(p.dv, 2 * values);
+    move(p.g, 4 * gates), move(p.beta, 4 * gates), move(p.dg, 4 * gates), move(p.dbeta, 4 * gates);
+    move(p.init, 4 * state), move(p.final_state, 4 * state), move(p.d_final, 4 * state), move(p.d_init, 4 * state);
+    move(p.valid_len, 4 * (size_t)b0);
+    move(c.img, (size_t)b0 * p.H * c.n * c.img_bytes);
+    ChunkBackward &w = c.w;
+    move(w.states, cs * c.n * kStateTile), move(w.dstates, cs * c.n * kDStateTile);
+    move(w.errs, cs * c.n * kErrTile), move(w.dv_lo, cs * c.n * kDvLoTile);
+    move(w.ss, cs * c.n * 16 * 4);
+    move(w.ww, cs * 4 * c.n * kChunk * 4), move(w.zx, cs * 4 * c.n * kChunk * 4);
+    move(w.fq, cs * 2 * c.n * kChunk * 4), move(w.fk, cs * 2 * c.n * kChunk * 4);
+    move(w.pe, cs * c.n * 512 * 4);
+    return c;
+}
+
+// A second stream per (device, caller stream), as the scan's backward has one (include/ssd.h): created at the
+// first call that takes it, kept until the process exits, with a lock from the fork to the join.
+struct SideStream {
+    cudaStream_t st = nullptr;
+    cudaEvent_t fork = nullptr, join = nullptr;
+    std::mutex mu;
+};
+std::mutex g_side_mu;
+std::map<std::pair<int, cudaStream_t>, std::unique_ptr<SideStream>> g_side;
+cudaError_t side_stream(cudaStream_t caller, SideStream **out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_side_mu);
+    std::unique_ptr<SideStream> &slot = g_side[std::make_pair(dev, caller)];
+    if (!slot) {
+        std::unique_ptr<SideStream> sd(new SideStream);
+        if ((e = cudaStreamCreateWithFlags(&sd->st, cudaStreamNonBlocking)) != cudaSuccess) return e;
+        if ((e = cudaEventCreateWithFlags(&sd->fork, cudaEventDisableTiming)) != cudaSuccess) return e;
+        if ((e = cudaEventCreateWithFlags(&sd->join, cudaEventDisableTiming)) != cudaSuccess) return e;
+        slot = std::move(sd);
+    }
+    *out = slot.get();
+    return cudaSuccess;
+}
+
+// The backward of two halves of the batch, each on its own stream.  The scans are serial in the chunks, so a last
+// wave of few chains leaves most SMs to themselves for as long as a full one; the other half's kernels fill them,
+// those of the gradients above all.  2 x 8192 x 80 heads (160 chains on 152 SMs): 2.11 ms for 2.54; 3 x 4096 x 64: 1.28 for
+// 1.39; 4 x 8192 x 80: 4.28 for 4.45.  Chains that all run at once anyway gain nothing (4 x 2048 x 24: 453 us for
+// 440), short ones not the launches.
+bool halves(const ChunkParams &c) {
+    return c.p.b >= 2 && (long long)c.p.b * c.p.H * slices_of(c.p) > kSMs && c.n >= 16;
+}
+cudaError_t backward_halves(const ChunkParams &c, cudaStream_t s) {
+    const int b0 = (c.p.b + 1) / 2;
+    const ChunkParams part[2] = {batch_part(c, 0, b0), batch_part(c, b0, c.p.b - b0)};
+    SideStream *sd = nullptr;
+    cudaError_t e = side_stream(s, &sd);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(sd->mu);
+    const cudaStream_t on[2] = {s, sd->st};
+    if ((e = launch_chunk_prep(part[0], c.p.b, s)) != cudaSuccess) return e;
+    if ((e = cudaEventRecord(sd->fork, s)) != cudaSuccess) return e;
+    if ((e = cudaStreamWaitEvent(sd->st, sd->fork, 0)) != cudaSuccess) return e;
+    e = launch_chunk_prep(part[1], 0, sd->st);
+    for (auto step : {launch_chunk_forward, launch_chunk_reverse, launch_chunk_grads})
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = step(part[i], on[i]);
+    // joined whatever failed: the caller's stream waits for all that runs
+    const cudaError_t j = cudaEventRecord(sd->join, sd->st), w = j == cudaSuccess ? cudaStreamWaitEvent(s, sd->join, 0) : j;
+    return e != cudaSuccess ? e : w;
+}
+
 }  // namespace
 }  // namespace delta
 }  // namespace ssd
@@ -158,7 +243,7 @@ ssd_status delta_forward(const delta_dims *dims, ssd_dtype dtype, const void *q,
     ChunkParams c;
     c.p = p;
     carve(*dims, false, (char *)workspace, &c);
-    st = cuda_status(launch_chunk_prep(c, cs));
+    st = cuda_status(launch_chunk_prep(c, p.b, cs));
     return st != SSD_OK ? st : cuda_status(launch_chunk_forward(c, cs));
 }
 
@@ -192,7 +277,8 @@ ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q
     ChunkParams c;
     c.p = p;
     carve(*dims, true, (char *)workspace, &c);
-    if ((st = cuda_status(launch_chunk_prep(c, cs))) != SSD_OK) return st;
+    if (halves(c)) return cuda_status(backward_halves(c, cs));
+    if ((st = cuda_status(launch_chunk_prep(c, p.b, cs))) != SSD_OK) return st;
     if ((st = cuda_status(launch_chunk_forward(c, cs))) != SSD_OK) return st;
     if ((st = cuda_status(launch_chunk_reverse(c, cs))) != SSD_OK) return st;
     return cuda_status(launch_chunk_grads(c, cs));

@@ -99,7 +99,8 @@ inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int 
     return encode_tiles(m, ptr, 4, dims, strides, box);
 }
 
-cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s);
+// and the status words, over status_rows of valid_len (0: left alone)
+cudaError_t launch_chunk_prep(const ChunkParams &c, int status_rows, cudaStream_t s);
 cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s);   // with c.w: the backward's recompute
 cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s);   // dS, dv and the gates' sums
 cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s);     // dq, dk, dg, dbeta

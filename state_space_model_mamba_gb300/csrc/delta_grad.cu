@@ -441,8 +441,10 @@ cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s) {
     if ((e = map_chunk_tokens(&maps.dv, p.dv, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const int bytes = (int)kBytes;
     if ((e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    // two blocks per SM run at once; as many again for the SMs that other kernels give up later (2.04 ms for 2.11 of the
+    // whole backward at 2 x 8192 x 80 heads, where the other half's scan holds SMs; no change elsewhere)
     const int units = c.n * p.G * p.b;
-    delta_grad_kernel<<<units < 2 * kSMs ? units : 2 * kSMs, kThreads, bytes, s>>>(c, maps);
+    delta_grad_kernel<<<units < 4 * kSMs ? units : 4 * kSMs, kThreads, bytes, s>>>(c, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     delta_gate_grads<<<(unsigned)(((long long)p.b * p.H * c.n + 7) / 8), 256, 0, s>>>(c);
     return cudaGetLastError();

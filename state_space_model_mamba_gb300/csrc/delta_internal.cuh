@@ -38,11 +38,11 @@ __device__ __forceinline__ int valid_tokens(const DeltaParams &p, int bi) {
     return v < 0 ? 0 : (v > p.L ? p.L : v);
 }
 // One block writes the call's status words: nothing timed out, how many valid_len entries were clamped.
-__device__ __forceinline__ void write_status(const DeltaParams &p) {
+__device__ __forceinline__ void write_status(const DeltaParams &p, int rows) {
     if (threadIdx.x == 0) {
         int bad = 0;
         if (p.valid_len)
-            for (int i = 0; i < p.b; ++i) bad += p.valid_len[i] < 0 || p.valid_len[i] > p.L;
+            for (int i = 0; i < rows; ++i) bad += p.valid_len[i] < 0 || p.valid_len[i] > p.L;
         for (int i = 0; i < kStatusWords; ++i) p.status[i] = i == kStatusValidLen ? bad : 0;
     }
 }

@@ -63,7 +63,8 @@ __device__ __forceinline__ Pair times_log2e(Pair a) {
 // Grid: one block per (b, group, `per` of the group's heads, chunk).
 // ALONE: per is 1, and the head's right-hand sides take the products' place in tensor memory.
 template <bool ALONE>
-__global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps, int per) {
+__global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(const ChunkParams cp, const __grid_constant__ PrepMaps maps, int per,
+                                                                                        int status_rows) {
     // no static shared memory and no slack for alignment: the window starts on a 1024-byte boundary
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Small &sm = *(Small *)(smem_raw + kOffSmall);
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
     const int chunk = blockIdx.x % cp.n, slice = blockIdx.x / cp.n % slices;
     const int bg = blockIdx.x / cp.n / slices, bi = bg / p.G, grp = bg % p.G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (blockIdx.x == 0) write_status(p);
+    if (blockIdx.x == 0 && status_rows > 0) write_status(p, status_rows);
     const int V = valid_tokens(p, bi), t0 = chunk * kChunk;
     if (t0 >= V) return;
     const uint32_t kq = smem_u32(smem_raw);
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
 
 }  // namespace
 
-cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
+cudaError_t launch_chunk_prep(const ChunkParams &c, int status_rows, cudaStream_t s) {
     const DeltaParams &p = c.p;
     PrepMaps maps;
     cudaError_t e;
@@ -318,7 +319,7 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, cudaStream_t s) {
     const unsigned grid = (unsigned)c.n * ((p.hpg + per - 1) / per) * p.b * p.G;
     auto launch = [&](auto kernel) {
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes)) != cudaSuccess) return e;
-        kernel<<<grid, kThreads, kBytes, s>>>(c, maps, per);
+        kernel<<<grid, kThreads, kBytes, s>>>(c, maps, per, status_rows);
         return cudaGetLastError();
     };
     return per == 1 ? launch(delta_prep_kernel<true>) : launch(delta_prep_kernel<false>);

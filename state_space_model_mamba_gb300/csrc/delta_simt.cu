@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float 
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const bool in = row0 + row < p.P;
     const int V = valid_tokens(p, bi);
-    if (blockIdx.x == 0) write_status(p);
+    if (blockIdx.x == 0) write_status(p, p.b);
     const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
     float4 s[NC];
     load_row(s, p.init ? p.init + srow : nullptr, in, p.N, lane);

@@ -141,6 +141,38 @@ def test_more_chains_than_blocks_run_at_once(dl, shape, valid):
     compare(run(dl, x, True, 0.3, valid=valid), x, True, 0.3, valid=valid)
 
 
+def test_halves_of_the_batch_on_two_streams(dl):
+    """More chains than SMs over 16 chunks and more: the backward forks.  Ordered on the caller's stream, the
+    same bits when captured and replayed."""
+    valid = [1030, 0, 700]
+    x = draw(3, 1030, 64, 8, 8, 2, seed=8)
+    out = run(dl, x, True, 0.3, valid=valid)
+    compare(out, x, True, 0.3, valid=valid)
+    d = dev(x, True)
+    vl = torch.tensor(valid, dtype=torch.int32, device="cuda")
+    a = (d["q"], d["k"], d["v"], d["g"], d["beta"], d["do"])
+    kw = dict(scale=0.3, d_final_state=d["d_final"], init_state=d["init"], valid_len=vl)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        late = torch.empty_like(d["do"])
+        torch.cuda._sleep(2_000_000)
+        late.copy_(d["do"])  # the fork has to come after this, the join before the copies below
+        got = dl.delta_backward(*a[:5], late, **kw)
+        copies = {k: t.clone() for k, t in got.items()}
+    torch.cuda.current_stream().wait_stream(other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=other):
+        captured = dl.delta_backward(*a, **kw)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k in copies:
+        assert torch.equal(copies[k], got[k]) and torch.equal(captured[k], got[k]), k
+        if k in out:
+            assert torch.equal(out[k], got[k]), k
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_no_state_no_final_gradient(dl, bf16):
     x = draw(2, 129, 2, 64, 128, 1, seed=5, bf16=bf16)
