@@ -32,7 +32,11 @@
  * ssd_last_error() describes the last failure.  valid_len entries outside
  * [0, seqlen] are clamped; ssd_workspace_status() on the call's workspace
  * reports how many (SSD_ERR_INVALID_ARG).  Results do not depend on the order
- * in which blocks run: the same inputs give the same bits. */
+ * in which blocks run: the same inputs give the same bits.  A chunked backward
+ * of several rows whose chains outnumber the SMs runs half of the batch on a
+ * second stream that the library keeps per (device, caller stream) pair,
+ * forked from `stream` and joined back into it before the call returns, as the
+ * scan's backward does (ssd.h); make a first such call before any capture. */
 #ifndef DELTA_GB300_H
 #define DELTA_GB300_H
 

@@ -8,7 +8,7 @@
 // load is one 128-byte line per piece), 32 rows a block.  What bounds the
 // sequence kernels is the latency of one token (two dependent 8-lane sums),
 // about 150 cycles; the step kernel reads and writes each state once and is
-// bound by HBM.
+// bound by HBM: 192 requests of 80 heads, 64 x 128, 1.01 GB in 151 us, 6.7 TB/s, as a copy.
 #include <stdio.h>
 
 #include "delta_internal.cuh"
