@@ -439,11 +439,11 @@ cudaError_t launch_chunk_grads(const ChunkParams &c, cudaStream_t s) {
     GradMaps maps;
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = same_tiles(&maps.q, maps.k, p.q)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.dv, p.dv, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
+    if ((e = same_tiles(&maps.dv, maps.d_o, p.dv)) != cudaSuccess) return e;
     const int bytes = (int)kBytes;
-    if ((e = cudaFuncSetAttribute(delta_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    if ((e = allow_shared((const void *)delta_grad_kernel, bytes)) != cudaSuccess) return e;
     // two blocks per SM run at once; as many again for the SMs that other kernels give up later (2.04 ms for 2.11 of the
     // whole backward at 2 x 8192 x 80 heads, where the other half's scan holds SMs; no change elsewhere)
     const int units = c.n * p.G * p.b;

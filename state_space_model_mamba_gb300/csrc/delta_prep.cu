@@ -312,7 +312,7 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, int status_rows, cudaStream_
     PrepMaps maps;
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N, 32)) != cudaSuccess) return e;
+    if ((e = same_tiles(&maps.q, maps.k, p.q)) != cudaSuccess) return e;
     // A block's heads share the two products: equal shares of a group, up to 6 heads (80 heads in 16 groups: one block of
     // 5 took 275 us where blocks of 4 and 1 took 292; 64 heads in 8 groups: 281 us in fours, 284 in eights,
     // 329 alone), but one by one while all of them have a place at once.
@@ -320,7 +320,7 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, int status_rows, cudaStream_
     const int per = (long long)c.n * p.b * p.H <= 6 * kSMs ? 1 : (p.hpg + shares - 1) / shares;
     const unsigned grid = (unsigned)c.n * ((p.hpg + per - 1) / per) * p.b * p.G;
     auto launch = [&](auto kernel) {
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes)) != cudaSuccess) return e;
+        if ((e = allow_shared((const void *)kernel, (int)kBytes)) != cudaSuccess) return e;
         kernel<<<grid, kThreads, kBytes, s>>>(c, maps, per, status_rows);
         return cudaGetLastError();
     };

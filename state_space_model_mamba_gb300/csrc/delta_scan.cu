@@ -869,7 +869,7 @@ cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     ScanMaps maps;
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = same_tiles(&maps.q, maps.k, p.q)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.v, p.v, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     // the narrowest slices that all have an SM of their own; two blocks of full slices per SM where not even those do
     const long long chains = (long long)p.b * p.H;
@@ -879,7 +879,7 @@ cudaError_t launch_chunk_forward(const ChunkParams &c, cudaStream_t s) {
     const long long grid = chains * ((p.P + W - 1) / W);
     const int nb = grid <= kSMs ? 2 : 1, bytes = 1024 + (int)kOffKQ + nb * (int)kKQBytes;
     auto launch = [&](auto kernel, int threads) {
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        if ((e = allow_shared((const void *)kernel, bytes)) != cudaSuccess) return e;
         kernel<<<(unsigned)grid, threads, bytes, s>>>(c, maps);
         return cudaGetLastError();
     };
@@ -894,11 +894,11 @@ cudaError_t launch_chunk_reverse(const ChunkParams &c, cudaStream_t s) {
     RevMaps maps;
     cudaError_t e;
     if ((e = map_chunk_tokens(&maps.k, p.k, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
-    if ((e = map_chunk_tokens(&maps.q, p.q, p.b, p.L, p.G, p.N)) != cudaSuccess) return e;
+    if ((e = same_tiles(&maps.q, maps.k, p.q)) != cudaSuccess) return e;
     if ((e = map_chunk_tokens(&maps.d_o, p.d_o, p.b, p.L, p.H, p.P)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(p.b * p.H * slices_of(p));
     const int bytes = 1024 + (int)kRevBytes;
-    if ((e = cudaFuncSetAttribute(delta_scan_rev, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    if ((e = allow_shared((const void *)delta_scan_rev, bytes)) != cudaSuccess) return e;
     delta_scan_rev<<<grid, scan_threads(64), bytes, s>>>(c, maps);
     return cudaGetLastError();
 }

@@ -30,6 +30,8 @@ class DeltaDims(ctypes.Structure):
 
 def _lib():
     global _bound
+    if _bound is not None:
+        return _bound
     with _lock:
         if _bound is None:
             lib = ssd.load_library()

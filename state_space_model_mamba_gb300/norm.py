@@ -22,6 +22,8 @@ _bound = None
 
 def _lib():
     global _bound
+    if _bound is not None:
+        return _bound
     with _lock:
         if _bound is None:
             lib = ssd.load_library()
@@ -47,42 +49,43 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check(x, weight, **same):
-    code = ssd.SSD_BF16 if x.dtype is _BF16 else ssd._dtype_code(x)
-    if x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
+def _check(x, weight, names, *same):
+    dtype, shape, device = x.dtype, x.shape, x.device
+    code = ssd.SSD_BF16 if dtype is _BF16 else ssd._dtype_code(x)
+    if not shape or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor")
-    D = x.shape[-1]
+    D = shape[-1]
     if weight.shape != (D,) or weight.dtype is not _F32:
         raise ValueError(f"weight: expected ({D},) float32, got {tuple(weight.shape)} {weight.dtype}")
-    if weight.device != x.device or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous tensor on {x.device}")
-    for name, t in same.items():
-        if t is not None and (t.shape != x.shape or t.dtype is not x.dtype or t.device != x.device or not t.is_contiguous()):
-            raise ValueError(f"{name} must match x in shape, dtype and device and be contiguous")
-    return code, x.numel() // max(D, 1), D
+    if weight.device != device or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous tensor on {device}")
+    for i, t in enumerate(same):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
+            raise ValueError(f"{names[i]} must match x in shape, dtype and device and be contiguous")
+    return code, x.numel() // max(D, 1), D, device.index
 
 
 def add_rms_norm(x, weight, eps=1e-5, residual=None):
     """Returns ``(y, stream)``: stream = x + residual (x itself without a
     residual), y = stream / sqrt(mean(stream^2) + eps) * weight, both in x's type."""
-    code, rows, D = _check(x, weight, residual=residual)
+    code, rows, D, index = _check(x, weight, ("residual",), residual)
     y = torch.empty_like(x)
     stream = x if residual is None else torch.empty_like(x)
     ssd._check(_lib().norm_add_rms(code, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(y),
-                                   None if residual is None else _ptr(stream), rows, D, _raw_stream(x.device.index)))
+                                   None if residual is None else _ptr(stream), rows, D, _raw_stream(index)))
     return y, stream
 
 
 def add_rms_norm_fp8(x, weight, eps=1e-5, residual=None, group=0):
     """Returns ``(y8, scales, stream)``: y8 float8_e4m3fn shaped like x, scales
     fp32 [..., D / group] (group 0: one per row), y = y8 * scale."""
-    code, rows, D = _check(x, weight, residual=residual)
+    code, rows, D, index = _check(x, weight, ("residual",), residual)
     y8 = torch.empty(x.shape, device=x.device, dtype=torch.float8_e4m3fn)
     scales = torch.empty(*x.shape[:-1], D // group if group else 1, device=x.device, dtype=torch.float32)
     stream = x if residual is None else torch.empty_like(x)
     ssd._check(_lib().norm_add_rms_fp8(code, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(y8), _ptr(scales),
                                        None if residual is None else _ptr(stream), rows, D, group,
-                                       _raw_stream(x.device.index)))
+                                       _raw_stream(index)))
     return y8, scales, stream
 
 
@@ -90,11 +93,11 @@ def add_rms_norm_backward(dy, stream, weight, eps=1e-5, d_stream=None):
     """Gradients for dy at the stored stream, with the gradient ``d_stream`` that
     reaches the stream from behind added: ``(dx, dweight)``; dx is the gradient
     of both x and residual."""
-    code, rows, D = _check(stream, weight, dy=dy, d_stream=d_stream)
+    code, rows, D, index = _check(stream, weight, ("dy", "d_stream"), dy, d_stream)
     dx = torch.empty_like(stream)
     dw = torch.empty_like(weight)
     lib = _lib()
     ws = torch.empty(lib.norm_backward_workspace_bytes(rows, D), dtype=torch.uint8, device=stream.device)
     ssd._check(lib.norm_add_rms_backward(code, _ptr(dy), _ptr(stream), _ptr(weight), eps, _ptr(d_stream), _ptr(dx),
-                                         _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(stream.device.index)))
+                                         _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(index)))
     return dx, dw
