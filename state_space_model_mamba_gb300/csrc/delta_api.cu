@@ -64,6 +64,16 @@ ssd_status cuda_status(cudaError_t e) {
     return e == cudaSuccess ? SSD_OK : fail(SSD_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
 }
 
+// Nothing thrown below (locks, the table of streams) leaves a C entry.
+template <class F>
+ssd_status guarded(F launches) {
+    try {
+        return cuda_status(launches());
+    } catch (...) {
+        return fail(SSD_ERR_CUDA, "launch failed: a host resource could not be had");
+    }
+}
+
 constexpr size_t kStatusBytes = 1024;  // status words, then the paths' own buffers
 
 DeltaParams base_params(const delta_dims &d, const void *q, const void *k, const void *v, const float *g,
@@ -243,8 +253,10 @@ ssd_status delta_forward(const delta_dims *dims, ssd_dtype dtype, const void *q,
     ChunkParams c;
     c.p = p;
     carve(*dims, false, (char *)workspace, &c);
-    st = cuda_status(launch_chunk_prep(c, p.b, cs));
-    return st != SSD_OK ? st : cuda_status(launch_chunk_forward(c, cs));
+    return guarded([&] {
+        const cudaError_t e = launch_chunk_prep(c, p.b, cs);
+        return e != cudaSuccess ? e : launch_chunk_forward(c, cs);
+    });
 }
 
 ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
@@ -277,11 +289,13 @@ ssd_status delta_backward(const delta_dims *dims, ssd_dtype dtype, const void *q
     ChunkParams c;
     c.p = p;
     carve(*dims, true, (char *)workspace, &c);
-    if (halves(c)) return cuda_status(backward_halves(c, cs));
-    if ((st = cuda_status(launch_chunk_prep(c, p.b, cs))) != SSD_OK) return st;
-    if ((st = cuda_status(launch_chunk_forward(c, cs))) != SSD_OK) return st;
-    if ((st = cuda_status(launch_chunk_reverse(c, cs))) != SSD_OK) return st;
-    return cuda_status(launch_chunk_grads(c, cs));
+    return guarded([&] {
+        if (halves(c)) return backward_halves(c, cs);
+        cudaError_t e = launch_chunk_prep(c, p.b, cs);
+        for (auto step : {launch_chunk_forward, launch_chunk_reverse, launch_chunk_grads})
+            if (e == cudaSuccess) e = step(c, cs);
+        return e;
+    });
 }
 
 ssd_status delta_step(const delta_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,

@@ -173,6 +173,58 @@ def test_halves_of_the_batch_on_two_streams(dl):
             assert torch.equal(out[k], got[k]), k
 
 
+def large(b, L, H, P, N, G, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    def unit(x):
+        return torch.nn.functional.normalize(x, dim=-1)
+
+    return dict(q=unit(rand(b, L, G, N)), k=unit(rand(b, L, G, N)), v=rand(b, L, H, P),
+                g=-torch.rand(b, H, L, generator=g, device="cuda"), beta=torch.rand(b, H, L, generator=g, device="cuda"))
+
+
+def near(a, b, bar):
+    """Rows that take another grid: the same sums, grouped differently."""
+    assert a.shape == b.shape and torch.isfinite(a).all()
+    assert float((a.float() - b.float()).norm()) <= bar * float(b.float().norm())
+
+
+def test_offsets_past_32_bits(dl):
+    """The last rows of tensors with more than 2^31 elements, and of workspaces past 4 GB, against the rows alone."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    t = large(3, 131072, 64, 128, 32, 1, 1)
+    assert t["v"].numel() > 2 ** 31
+    o, fin = dl.delta_forward(*t.values())
+    last = {k: x[2:].contiguous() for k, x in t.items()}
+    del t
+    o, fin = o[2:].clone(), fin[2:].clone()
+    ro, rf = dl.delta_forward(*last.values())
+    near(o, ro, BF16_BAR)
+    near(fin, rf, SPLIT_BAR)
+    del o, ro, last
+    t = large(2, 32768, 80, 64, 128, 16, 2)
+    do = torch.randn_like(t["v"])
+    out = dl.delta_backward(*t.values(), do)
+    ref = dl.delta_backward(*(x[1:].contiguous() for x in t.values()), do[1:].contiguous())
+    for k in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(out[k][1:], ref[k]), k  # halves of the batch: the same kernels
+    del out, ref, do, t
+    slots, H, P, N = 4200, 80, 64, 128
+    pool = torch.zeros(slots, H, P, N, device="cuda")
+    assert pool.numel() > 2 ** 31
+    x = large(2, 1, H, P, N, 16, 3)
+    pool[-1], pool[1] = 0.25, 0.25
+    index = torch.tensor([slots - 1, 1], dtype=torch.int32, device="cuda")
+    one = [y[:1].expand_as(y).squeeze(2 if n in ("g", "beta") else 1).contiguous() for n, y in x.items()]
+    o = dl.delta_step(*one, pool, state_index=index)
+    assert torch.equal(o[0], o[1]) and torch.equal(pool[-1], pool[1]) and float((pool[1] - 0.25).abs().max()) > 1e-3
+    assert float(pool[2:-1].abs().max()) == 0 and float(pool[0].abs().max()) == 0
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_no_state_no_final_gradient(dl, bf16):
     x = draw(2, 129, 2, 64, 128, 1, seed=5, bf16=bf16)

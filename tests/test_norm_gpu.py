@@ -114,6 +114,24 @@ def test_fp8_scales_at_the_ends_of_fp32(nm, group, top):
         assert torch.all(q[:, 1::2] == 448)
 
 
+def test_offsets_past_32_bits(nm):
+    """The last rows of a tensor with more than 2^31 elements, against the rows alone."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    rows, D = 1100000, 2048
+    x = torch.randn(rows, D, device="cuda", dtype=torch.bfloat16)
+    w = 1 + 0.1 * torch.randn(D, device="cuda")
+    y, stream = nm.add_rms_norm(x, w, residual=x)
+    y8, s, _ = nm.add_rms_norm_fp8(x, w, residual=x, group=128)
+    dx, _ = nm.add_rms_norm_backward(y, stream, w, d_stream=x)
+    tail = x[-50:].contiguous()
+    ty, ts = nm.add_rms_norm(tail, w, residual=tail)
+    t8, tsc, _ = nm.add_rms_norm_fp8(tail, w, residual=tail, group=128)
+    tdx, _ = nm.add_rms_norm_backward(ty, ts, w, d_stream=tail)
+    assert torch.equal(y[-50:], ty) and torch.equal(stream[-50:], ts) and torch.equal(s[-50:], tsc)
+    assert torch.equal(y8[-50:].view(torch.uint8), t8.view(torch.uint8)) and torch.equal(dx[-50:], tdx)
+
+
 def test_in_place_stream_and_fixed_order(nm):
     import ctypes
     from state_space_model_mamba_gb300 import ssd
