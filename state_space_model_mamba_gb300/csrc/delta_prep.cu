@@ -13,13 +13,14 @@
 // columns before them on the tensor cores (beta y and E as hi + lo bf16 parts), which add it
 // to the right-hand sides where these lie in tensor memory.  Substitution stays accurate for repeated keys, where a
 // power series of the triangle would lose every digit.
-// What bounds it is the chain of those steps, each behind a barrier, and 8200 warp
-// instructions a head and chunk: 40 % of the issue slots are used with six blocks on an SM
+// What bounds it is the chain of those steps, each behind a barrier, and 7000 warp
+// instructions a head and chunk (8200 before decays and triangles went in pairs, at 40 % of
+// the issue slots and 11 % more time) with six blocks on an SM
 // (tensor memory would hold eight, shared memory six), four where several heads share a
 // block's products.  With the shares in fp32 registers too a head took twice the
 // instructions; the whole substitution unrolled waited for instructions half of the time.
 // Which warps get the long rows changes from block to block.
-// Measured: 13.4 ns a head and chunk (1 x 131072 x 32 heads: 878 us; 4 x 2048 x 24: 52 us, 2.5 TB/s).
+// Measured: 12.3 ns a head and chunk (1 x 131072 x 32 heads: 806 us; 4 x 2048 x 24: 47.5 us, 2.7 TB/s).
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -36,7 +37,7 @@ constexpr int kLdD = 16;              // floats per row of E's diagonal blocks
 constexpr uint32_t kOffE = 0, kOffZ = 16384, kOffSmall = 32768;
 struct Small {
     float d[kChunk * kLdD];
-    float2 gam[kChunk];   // gamma log2(e), hi and lo
+    float gam[2][kChunk]; // gamma log2(e): hi, lo
     float beta[kChunk];
     uint64_t load, mma, step;
     uint32_t tmem;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
     Small &sm = *(Small *)(smem_raw + kOffSmall);
     uint64_t &bar_load = sm.load, &bar_mma = sm.mma, &bar_step = sm.step;
     float *const s_d = sm.d, *const s_beta = sm.beta;
-    float2 *const s_gam = sm.gam;
+    float *const s_gh = sm.gam[0], *const s_gl = sm.gam[1];
     // the products, then the right-hand sides
     constexpr uint32_t kAccCols = ALONE ? 64 : 128, kRhs = ALONE ? 0 : 64;
     const DeltaParams &p = cp.p;
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
             const Pair c0 = add(sum, Pair{-g1, 0.f}), c1 = sum;
             const Pair total{__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
             const Pair l0 = times_log2e(c0), l1 = times_log2e(c1);
-            s_gam[i0] = make_float2(l0.hi, l0.lo);
-            s_gam[i0 + 1] = make_float2(l1.hi, l1.lo);
+            *(float2 *)(s_gh + i0) = make_float2(l0.hi, l1.hi);
+            *(float2 *)(s_gl + i0) = make_float2(l0.lo, l1.lo);
             *(float2 *)(s_beta + i0) = beta;
             float *gates = (float *)img;
             *(float2 *)(gates + i0) = make_float2(expf(c0.hi), expf(c1.hi));
@@ -162,21 +163,32 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
             tc_fence_after();
         }
         if (__syncthreads_and(ok) == 0) break;
-        const float2 gi = s_gam[i];
+        const float gh = s_gh[i], gl = s_gl[i];
         const int last = i >> 4 | 1;      // warps of rows 0 .. 31 have two blocks of columns
-        // 16 columns of D o (row of K K^T or Q K^T), zero where j >= i (keys) or j > i
-        auto decayed = [&](int jb, float f, float (&r)[16]) {
-            float a[16];
+        const int limit = live ? (keys ? i : i + 1) : 0;  // the row's columns that count
+        const bool all = t0 + kChunk <= V;
+        // 16 columns of f D o (row of K K^T or Q K^T), zero from column `limit` on
+        auto decayed = [&](int jb, float f, float2 (&r)[8]) {
             __syncwarp();  // the lanes' rows end at different columns
-            tmem_ld16(tmem_addr(tm, 32 * warp, (16 * jb) ^ (32 * flip)), a);
-            const bool whole = 16 * jb + 15 < (i & ~31);  // the same for the warp
+            tmem_ld16(tmem_addr(tm, 32 * warp, (16 * jb) ^ (32 * flip)), (float *)r);
+            const bool whole = all && 16 * jb + 15 < (i & ~31);  // the same for the warp
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int j = 16 * jb + e;
-                const float2 gj = s_gam[j];
-                const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y));
-                r[e] = whole || j < i || (j == i && !keys) ? f * d * a[e] : 0.f;
-                if (!live) r[e] = 0.f;
+            for (int c = 0; c < 4; ++c) {
+                const float4 h = *(const float4 *)(s_gh + 16 * jb + 4 * c), l = *(const float4 *)(s_gl + 16 * jb + 4 * c);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float2 minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
+                    const float2 x = ffma2(u ? make_float2(h.z, h.w) : make_float2(h.x, h.y), minus, make_float2(gh, gh)),
+                                 y = ffma2(u ? make_float2(l.z, l.w) : make_float2(l.x, l.y), minus, make_float2(gl, gl)),
+                                 d = ffma2(x, one, y);
+                    float2 v = fmul2(fmul2(r[2 * c + u], make_float2(f, f)), make_float2(exp2_approx(d.x), exp2_approx(d.y)));
+                    if (!whole) {
+                        const int j = 16 * jb + 4 * c + 2 * u;
+                        v.x = j < limit ? v.x : 0.f;
+                        v.y = j + 1 < limit ? v.y : 0.f;
+                    }
+                    r[2 * c + u] = v;
+                }
             }
         };
         const bool bwd = cp.w.states != nullptr, solves = keys || !bwd;
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
         if (solves)
             for (int jb = 0; jb <= last; ++jb) {
                 float2 r[8];
-                decayed(jb, keys ? -1.f : p.scale, (float(&)[16])r);
+                decayed(jb, keys ? -1.f : p.scale, r);
                 __syncwarp();
                 tmem_st16(tmem_addr(rhs(jb), 32 * warp, 0), (const float *)r);
                 if (keys) {  // -E
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
         if (bwd && !keys)                 // the backward takes A itself
             for (int jb = 0; jb <= last; ++jb) {
                 float2 y[8];
-                decayed(jb, p.scale, (float(&)[16])y);
+                decayed(jb, p.scale, y);
                 if (jb <= (i >> 4)) store_block(jb, y);
             }
         const uint32_t zt = kq + kOffZ + (tid >> 3) * 128 + (tid & 7) * 16;
@@ -233,22 +245,19 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
                 __syncwarp();
                 tmem_ld16(tmem_addr(rhs(jb), 32 * warp, 0), (float *)y);
                 // the triangle of the block: from the last column, each solved one taken off those before it
-                float *yy = (float *)y;
+                // (pairs of columns; the triangle holds zeros from its diagonal on)
                 const float *e0 = s_d + 16 * jb * kLdD;
                 float2 z[8];
-                float *zz = (float *)z;
 #pragma unroll
                 for (int m = 15; m >= 0; --m) {
-                    const float zm = s_beta[16 * jb + m] * yy[m];
-                    zz[m] = zm;
+                    const float zm = s_beta[16 * jb + m] * (m & 1 ? y[m / 2].y : y[m / 2].x);
+                    (m & 1 ? z[m / 2].y : z[m / 2].x) = zm;
                     const float4 *w = (const float4 *)(e0 + m * kLdD);
 #pragma unroll
                     for (int e = 0; e < (m + 3) / 4; ++e) {
                         const float4 v = w[e];
-                        yy[4 * e] = fmaf(zm, v.x, yy[4 * e]);
-                        if (4 * e + 1 < m) yy[4 * e + 1] = fmaf(zm, v.y, yy[4 * e + 1]);
-                        if (4 * e + 2 < m) yy[4 * e + 2] = fmaf(zm, v.z, yy[4 * e + 2]);
-                        if (4 * e + 3 < m) yy[4 * e + 3] = fmaf(zm, v.w, yy[4 * e + 3]);
+                        y[2 * e] = ffma2(make_float2(zm, zm), make_float2(v.x, v.y), y[2 * e]);
+                        if (4 * e + 2 < m) y[2 * e + 1] = ffma2(make_float2(zm, zm), make_float2(v.z, v.w), y[2 * e + 1]);
                     }
                 }
                 if (jb > 0) {
@@ -315,7 +324,7 @@ cudaError_t launch_chunk_prep(const ChunkParams &c, int status_rows, cudaStream_
     if ((e = same_tiles(&maps.q, maps.k, p.q)) != cudaSuccess) return e;
     // A block's heads share the two products: equal shares of a group, up to 6 heads (80 heads in 16 groups: one block of
     // 5 took 275 us where blocks of 4 and 1 took 292; 64 heads in 8 groups: 281 us in fours, 284 in eights,
-    // 329 alone), but one by one while all of them have a place at once.
+    // 329 alone; all before the arithmetic went in pairs), but one by one while all of them have a place at once.
     const int shares = (p.hpg + kHeadsPer - 1) / kHeadsPer;
     const int per = (long long)c.n * p.b * p.H <= 6 * kSMs ? 1 : (p.hpg + shares - 1) / shares;
     const unsigned grid = (unsigned)c.n * ((p.hpg + per - 1) / per) * p.b * p.G;
