@@ -19,9 +19,9 @@
 // dV (beside dO Z^T and dV Z^T), W and dS are rounded once, as dk is.
 // Two blocks share an SM, hide each other's copies and passes, and stay for the whole
 // pass.  What bounds it: an item is 2.9 us of products (40 steps of 128 rows and columns, 20
-// narrow ones) and five hand-overs, 4.3 to 6.7 us an item and SM measured with two in flight
-// (20480 items of 80 heads, 2 x 8192: 578 us; 3072 of 24 heads, 4 x 2048: 135 us, 3.1 TB/s).
-// The sums in registers spilled (64 a thread of 96): 619 and 150 us.
+// narrow ones) and five hand-overs, 6 us an item and SM with two in flight (3072 items of 24 heads,
+// 4 x 2048: 122 us, 3.4 TB/s).  The sums in registers spilled (64 a thread of 96) and took 150 us,
+// masks a column at a time 135.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 
@@ -36,7 +36,7 @@ constexpr int kCompute = 256, kThreads = kCompute + 32;
 // S lo, then dS; dO and dV (then [Nm; M] lo); Q and K
 constexpr uint32_t kOffZero = 0, kOffW = 8192, kOffSZ = 16384, kOffZ = kOffSZ + 16384, kOffP = kOffSZ, kOffZlo = 40960,
                    kOffDS = 49152, kOffDV = 65536, kOffPlo = kOffDV, kOffQK = 81920, kOffSmall = 114688;
-struct Small {
+struct alignas(16) Small {
     float beta[kChunk];  // as the image has them, one copy
     float2 gam[kChunk];
     uint64_t qk, in, ds, x, p, m[3];
@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar_qk, u & 1));
                     for (int x = tid; x < 4 * kChunk * 8; x += kCompute)
                         if (((x >> 3) & 63) >= live_n) st_shared_v4(base + kOffQK + x * 16u, 0, 0, 0, 0);
+                    fence_async_smem();  // before the products with them: what is masked below has to be finite
                 }
                 for (int it = 0; it < items && ok; ++it, ++n) {
                     const uint32_t ph = n & 1;
@@ -305,26 +306,34 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                         const uint4 o = pack8(w);
                         st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
                     }
-                    float rs = 0.f, cs_[32];
+                    float2 rs2 = make_float2(0.f, 0.f);
+                    float cs_[32];
+                    const int limit = live ? (keys ? i : i + 1) : 0;  // the row's columns that count
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        float a[16], b[16];
+                        float2 a[8], b[8];
                         __syncwarp();
                         tmem_ld16x2(tmem_addr(tm, 32 * quarter, 32 * half + 16 * q),
-                                    tmem_addr(tm, 32 * quarter, 64 + 32 * half + 16 * q), a, b);
+                                    tmem_addr(tm, 32 * quarter, 64 + 32 * half + 16 * q), (float *)a, (float *)b);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int j = 32 * half + 16 * q + e;
-                            const float2 gj = sm.gam[j];
-                            const float d = exp2_approx((gi.x - gj.x) + (gi.y - gj.y)) * sm.beta[j];
-                            const bool in = live && (j < i || (j == i && !keys));
-                            a[e] = in ? f * d * a[e] : 0.f;
-                            cs_[16 * q + e] = in ? a[e] * b[e] : 0.f;
-                            rs += cs_[16 * q + e];
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = 32 * half + 16 * q + 2 * e;
+                            const float4 gj = *(const float4 *)(sm.gam + j);
+                            const float2 minus = make_float2(-1.f, -1.f), x = ffma2(make_float2(gj.x, gj.y), minus, gi),
+                                         y = ffma2(make_float2(gj.z, gj.w), minus, gi);
+                            const float2 d = fmul2(make_float2(exp2_approx(x.x + x.y), exp2_approx(y.x + y.y)), *(const float2 *)(sm.beta + j));
+                            float2 v = fmul2(fmul2(a[e], make_float2(f, f)), d);
+                            v.x = j < limit ? v.x : 0.f;
+                            v.y = j + 1 < limit ? v.y : 0.f;
+                            a[e] = v;
+                            const float2 c = fmul2(v, b[e]);
+                            rs2 = ffma2(c, make_float2(1.f, 1.f), rs2);
+                            cs_[16 * q + 2 * e] = c.x;
+                            cs_[16 * q + 2 * e + 1] = c.y;
                         }
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            store_parts8(base + kOffP, base + kOffPlo, row, 4 * half + 2 * q + c, (const float2 *)a + 4 * c);
+                            store_parts8(base + kOffP, base + kOffPlo, row, 4 * half + 2 * q + c, a + 4 * c);
                     }
                     fence_async_smem();
                     tc_fence_before();
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                             }
                     }
                     float *pe = cp.w.pe + (cs * cp.n + chunk) * 512;
-                    pe[half * 128 + row] = rs;
+                    pe[half * 128 + row] = rs2.x + rs2.y;
                     pe[256 + quarter * 64 + 32 * half + lane] = cs_[0];
                 }
                 ++u;
