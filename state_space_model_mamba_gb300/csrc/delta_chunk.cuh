@@ -92,8 +92,6 @@ cudaError_t encode_tiles(CUtensorMap *m, const void *base, int rank, const cuuin
                          const cuuint32_t *box);
 // The map `like` of a tensor with the same shape at another address.
 cudaError_t same_tiles(CUtensorMap *m, const CUtensorMap &like, const void *base);
-// Dynamic shared memory of a kernel, asked for once per thread, device and size: a short call is mostly its launches.
-cudaError_t allow_shared(const void *kernel, int bytes);
 // [b, L, heads, width] bf16: boxes of 64 columns of one head x a chunk's (or fewer) tokens
 inline cudaError_t map_chunk_tokens(CUtensorMap *m, const void *ptr, int b, int L, int heads, int width,
                                     int tokens = kChunk) {

@@ -48,6 +48,10 @@ __device__ __forceinline__ void write_status(const DeltaParams &p, int rows) {
 }
 __device__ __forceinline__ float clamp_log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
 
+// Dynamic shared memory of a kernel, asked for once per thread, device and size: a short call is mostly its launches
+// (delta_maps.cu).
+cudaError_t allow_shared(const void *kernel, int bytes);
+
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
 template <>

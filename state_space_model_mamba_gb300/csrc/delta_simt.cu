@@ -47,31 +47,61 @@ struct Stage {
     float a[kTok], beta[kTok];
 };
 
+// A stage on its way to shared memory: a thread's pieces in registers, loaded while the stage before is worked on.
 template <typename T, int NC, bool BWD>
-__device__ __forceinline__ void load_stage(Stage<NC, BWD> &s, const DeltaParams &p, int bi, int h, int row0, int t0,
-                                           int nt) {
-    const int g = h / p.hpg, nq = p.N / 4;
-    const T *q = (const T *)p.q, *k = (const T *)p.k, *v = (const T *)p.v;
-    for (int i = threadIdx.x; i < nt * NC * kLanes; i += kThreads) {
-        const int t = i / (NC * kLanes), c = i % (NC * kLanes);
-        const long long at = (((long long)bi * p.L + t0 + t) * p.G + g) * p.N + 4 * c;
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        s.q[t][c] = c < nq ? load4(q + at) : z;
-        s.k[t][c] = c < nq ? load4(k + at) : z;
+struct Fetch {
+    static constexpr int kTok = tok_of(NC), kKeys = (kTok * NC * kLanes + kThreads - 1) / kThreads,
+                         kVals = kTok * kRows / kThreads;
+    float4 q[kKeys], k[kKeys];
+    float v[kVals], dO[BWD ? kVals : 1], a, beta;
+    __device__ __forceinline__ void load(const DeltaParams &p, int bi, int h, int row0, int t0, int nt) {
+        const int g = h / p.hpg, nq = p.N / 4;
+#pragma unroll
+        for (int x = 0; x < kKeys; ++x) {
+            const int i = threadIdx.x + x * kThreads, t = i / (NC * kLanes), c = i % (NC * kLanes);
+            const long long at = (((long long)bi * p.L + t0 + t) * p.G + g) * p.N + 4 * c;
+            q[x] = k[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < nt && c < nq) {
+                q[x] = load4((const T *)p.q + at);
+                k[x] = load4((const T *)p.k + at);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kVals; ++x) {
+            const int i = threadIdx.x + x * kThreads, t = i / kRows, r = i % kRows;
+            const long long at = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r;
+            const bool in = t < nt && row0 + r < p.P;
+            v[x] = in ? load1((const T *)p.v + at) : 0.f;
+            if (BWD) dO[x] = in ? p.scale * load1((const T *)p.d_o + at) : 0.f;
+        }
+        a = beta = 0.f;
+        if (threadIdx.x < nt) {
+            const long long at = ((long long)bi * p.H + h) * p.L + t0 + threadIdx.x;
+            a = expf(clamp_log_decay(p.g[at]));
+            beta = p.beta[at];
+        }
     }
-    for (int i = threadIdx.x; i < nt * kRows; i += kThreads) {
-        const int t = i / kRows, r = i % kRows;
-        const long long at = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r;
-        const bool in = row0 + r < p.P;
-        s.v[t][r] = in ? load1(v + at) : 0.f;
-        if (BWD) s.dO[t][r] = in ? p.scale * load1((const T *)p.d_o + at) : 0.f;
+    __device__ __forceinline__ void store(Stage<NC, BWD> &s) const {
+#pragma unroll
+        for (int x = 0; x < kKeys; ++x) {
+            const int i = threadIdx.x + x * kThreads;
+            if (i < kTok * NC * kLanes) {
+                (&s.q[0][0])[i] = q[x];
+                (&s.k[0][0])[i] = k[x];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kVals; ++x) {
+            const int i = threadIdx.x + x * kThreads;
+            (&s.v[0][0])[i] = v[x];
+            if (BWD) (&s.dO[0][0])[i] = dO[x];
+        }
+        if (threadIdx.x < kTok) {
+            s.a[threadIdx.x] = a;
+            s.beta[threadIdx.x] = beta;
+        }
     }
-    if (threadIdx.x < nt) {
-        const long long at = ((long long)bi * p.H + h) * p.L + t0 + threadIdx.x;
-        s.a[threadIdx.x] = expf(clamp_log_decay(p.g[at]));
-        s.beta[threadIdx.x] = p.beta[at];
-    }
-}
+};
 
 template <int NC>
 __device__ __forceinline__ void load_row(float4 (&s)[NC], const float *src, bool in, int N, int lane) {
@@ -97,8 +127,8 @@ __device__ __forceinline__ void store_row(const float4 (&s)[NC], float *dst, boo
 template <typename T, int NC>
 __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float *kept, int nseg) {
     constexpr int kTok = tok_of(NC);
-    __shared__ Stage<NC, false> st;
-    __shared__ float out[kTok][kRows];
+    __shared__ Stage<NC, false> stages[2];
+    __shared__ float outs[2][kTok][kRows];
     const int nblk = (p.P + kRows - 1) / kRows, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H;
     const int row0 = (blockIdx.x % nblk) * kRows;
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -108,28 +138,58 @@ __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float 
     const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
     float4 s[NC];
     load_row(s, p.init ? p.init + srow : nullptr, in, p.N, lane);
-    for (int t0 = 0; t0 < V; t0 += kTok) {
+    Fetch<T, NC, false> next;
+    if (V > 0) {
+        next.load(p, bi, h, row0, 0, min(kTok, V));
+        next.store(stages[0]);
+    }
+    __syncthreads();
+    for (int t0 = 0, cur = 0; t0 < V; t0 += kTok, cur ^= 1) {
         const int nt = min(kTok, V - t0);
-        __syncthreads();
-        load_stage<T>(st, p, bi, h, row0, t0, nt);
+        const Stage<NC, false> &st = stages[cur];
+        float(*out)[kRows] = outs[cur];
+        if (t0 + kTok < V) next.load(p, bi, h, row0, t0 + kTok, min(kTok, V - t0 - kTok));
         if (kept)
             store_row(s, kept + (((long long)bh * nseg + t0 / kTok) * p.P + row0 + row) * p.N, in, p.N, lane);
-        __syncthreads();
+        // what token t reads of the state is summed over the lanes beside the next token's s.k: one chain of shuffles a token
+        float od = 0.f;
+#pragma unroll 4
         for (int t = 0; t < nt; ++t) {
-            float d = 0.f;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) d += dot4(s[i], st.k[t][i * kLanes + lane]);
-            const float a = st.a[t];
-            const float u = st.beta[t] * (st.v[t][row] - a * sum8(d));
-            float od = 0.f;
+            float4 k[NC];
+            float d0 = 0.f, d1 = 0.f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                s[i] = axpy4(u, st.k[t][i * kLanes + lane], scale4(a, s[i]));
-                od += dot4(s[i], st.q[t][i * kLanes + lane]);
+                k[i] = st.k[t][i * kLanes + lane];
+                if (i & 1)
+                    d1 += dot4(s[i], k[i]);
+                else
+                    d0 += dot4(s[i], k[i]);
             }
-            od = sum8(od);
-            if (lane == 0) out[t][row] = p.scale * od;
+            float d = d0 + d1;
+            const float a = st.a[t], be = st.beta[t], v = st.v[t][row];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) s[i] = scale4(a, s[i]);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) {
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+                od += __shfl_xor_sync(0xffffffffu, od, o);
+            }
+            if (lane == 0 && t > 0) out[t - 1][row] = p.scale * od;
+            const float u = be * (v - a * d);
+            float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                s[i] = axpy4(u, k[i], s[i]);
+                if (i & 1)
+                    o1 += dot4(s[i], st.q[t][i * kLanes + lane]);
+                else
+                    o0 += dot4(s[i], st.q[t][i * kLanes + lane]);
+            }
+            od = o0 + o1;
         }
+        od = sum8(od);
+        if (lane == 0) out[nt - 1][row] = p.scale * od;
+        if (t0 + kTok < V) next.store(stages[cur ^ 1]);
         __syncthreads();
         if (p.o)
             for (int i = threadIdx.x; i < nt * kRows; i += kThreads) {
@@ -161,13 +221,21 @@ struct BwdBuffers {
     int nseg, nblk, items;
 };
 
+// shared memory of a block: two stages, and a segment's sums over each warp's rows
+template <int NC>
+struct BwdShared {
+    Stage<NC, true> stage[2];
+    float zs[tok_of(NC)][kRows];
+    float4 red[2][tok_of(NC)][kThreads / 32][NC * kLanes];
+    float red1[2][tok_of(NC)][kThreads / 32];
+};
+static_assert(sizeof(BwdShared<4>) <= 232448 && sizeof(BwdShared<8>) <= 232448, "shared memory of a block");
+
 template <typename T, int NC>
 __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
     constexpr int kSegTok = tok_of(NC);
-    __shared__ Stage<NC, true> st;
-    __shared__ float zs[kSegTok][kRows];
-    __shared__ float4 red[2][kThreads / 32][NC * kLanes];
-    __shared__ float red1[2][kThreads / 32];
+    extern __shared__ __align__(16) char smem[];
+    BwdShared<NC> &sm = *(BwdShared<NC> *)smem;
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, warp = threadIdx.x / 32;
     float4 *hist = (float4 *)w.hist + (size_t)blockIdx.x * kSegTok * NC * kThreads + threadIdx.x;
     for (int item = blockIdx.x; item < w.items; item += gridDim.x) {
@@ -175,48 +243,76 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
         const bool in = row0 + row < p.P;
         const int V = valid_tokens(p, bi);
         const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
-        float4 D[NC], s[NC];
+        const int nseg = (V + kSegTok - 1) / kSegTok;
+        float4 D[NC], s[NC], sn[NC];
         load_row(D, p.d_final ? p.d_final + srow : nullptr, in, p.N, lane);
-        for (int seg = (V + kSegTok - 1) / kSegTok - 1; seg >= 0; --seg) {
+        Fetch<T, NC, true> next;
+        auto fetch = [&](int seg) {
+            next.load(p, bi, h, row0, seg * kSegTok, min(kSegTok, V - seg * kSegTok));
+            load_row(sn, w.kept + (((long long)bh * w.nseg + seg) * p.P + row0 + row) * p.N, in, p.N, lane);
+        };
+        __syncthreads();  // the item before is done with the stages
+        if (nseg > 0) {
+            fetch(nseg - 1);
+            next.store(sm.stage[0]);
+        }
+        __syncthreads();
+        for (int seg = nseg - 1, cur = 0; seg >= 0; --seg, cur ^= 1) {
             const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
-            __syncthreads();
-            load_stage<T>(st, p, bi, h, row0, t0, nt);
-            load_row(s, w.kept + (((long long)bh * w.nseg + seg) * p.P + row0 + row) * p.N, in, p.N, lane);
-            __syncthreads();
+            const Stage<NC, true> &st = sm.stage[cur];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) s[i] = sn[i];
+            if (seg > 0) fetch(seg - 1);
+#pragma unroll 2
             for (int t = 0; t < nt; ++t) {
-                float d = 0.f;
+                const float a = st.a[t], be = st.beta[t], v = st.v[t][row];
+                float4 k[NC];
+                float d0 = 0.f, d1 = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    s[i] = scale4(st.a[t], s[i]);
+                    k[i] = st.k[t][i * kLanes + lane];
+                    s[i] = scale4(a, s[i]);
                     hist[(t * NC + i) * kThreads] = s[i];
-                    d += dot4(s[i], st.k[t][i * kLanes + lane]);
+                    if (i & 1)
+                        d1 += dot4(s[i], k[i]);
+                    else
+                        d0 += dot4(s[i], k[i]);
                 }
-                const float z = st.v[t][row] - sum8(d);
-                if (lane == 0) zs[t][row] = z;
+                const float z = v - sum8(d0 + d1);
+                if (lane == 0) sm.zs[t][row] = z;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) s[i] = axpy4(st.beta[t] * z, st.k[t][i * kLanes + lane], s[i]);
+                for (int i = 0; i < NC; ++i) s[i] = axpy4(be * z, k[i], s[i]);
             }
             __syncwarp();
+            float4 sd[NC], sd_next[NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) sd_next[i] = hist[((nt - 1) * NC + i) * kThreads];
             for (int t = nt - 1; t >= 0; --t) {
-                const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = zs[t][row];
-                float d = 0.f;
+                const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = sm.zs[t][row];
+                float4 k[NC];
+                float d0 = 0.f, d1 = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
+                    sd[i] = sd_next[i];
+                    if (t > 0) sd_next[i] = hist[((t - 1) * NC + i) * kThreads];
+                    k[i] = st.k[t][i * kLanes + lane];
                     D[i] = axpy4(dO, st.q[t][i * kLanes + lane], D[i]);
-                    d += dot4(D[i], st.k[t][i * kLanes + lane]);
+                    if (i & 1)
+                        d1 += dot4(D[i], k[i]);
+                    else
+                        d0 += dot4(D[i], k[i]);
                 }
-                d = sum8(d);
+                const float d = sum8(d0 + d1);
                 const float dz = be * d, bz = be * z;
                 if (lane == 0 && in)
                     store1((T *)p.dv + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + row, dz);
                 float dg = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    const float4 sd = hist[(t * NC + i) * kThreads], kk = st.k[t][i * kLanes + lane];
-                    float4 dq = scale4(dO, axpy4(bz, kk, sd));
-                    float4 dk = axpy4(bz, D[i], scale4(-dz, sd));
-                    D[i] = axpy4(-dz, kk, D[i]);
-                    dg += dot4(D[i], sd);
+                    float4 dq = scale4(dO, axpy4(bz, k[i], sd[i]));
+                    float4 dk = axpy4(bz, D[i], scale4(-dz, sd[i]));
+                    D[i] = axpy4(-dz, k[i], D[i]);
+                    dg += dot4(D[i], sd[i]);
                     D[i] = scale4(a, D[i]);
                     // the warp's four rows
 #pragma unroll
@@ -231,8 +327,8 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
                         dk.w += __shfl_xor_sync(0xffffffffu, dk.w, o);
                     }
                     if ((threadIdx.x & 31) < kLanes) {
-                        red[0][warp][i * kLanes + lane] = dq;
-                        red[1][warp][i * kLanes + lane] = dk;
+                        sm.red[0][t][warp][i * kLanes + lane] = dq;
+                        sm.red[1][t][warp][i * kLanes + lane] = dk;
                     }
                 }
                 // over the warp: every lane has its share of dg, lane 0 of each row its dbeta
@@ -243,28 +339,31 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
                     db += __shfl_xor_sync(0xffffffffu, db, o);
                 }
                 if ((threadIdx.x & 31) == 0) {
-                    red1[0][warp] = dg;
-                    red1[1][warp] = db;
+                    sm.red1[0][t][warp] = dg;
+                    sm.red1[1][t][warp] = db;
                 }
-                __syncthreads();
-                const long long tok = ((long long)blk * p.b * p.H + bh) * p.L + t0 + t;
-                for (int i = threadIdx.x; i < 2 * NC * kLanes; i += kThreads) {
-                    const int which = i / (NC * kLanes), c = i % (NC * kLanes);
-                    float4 acc = red[which][0][c];
-                    for (int x = 1; x < kThreads / 32; ++x) {
-                        const float4 r = red[which][x][c];
-                        acc = make_float4(acc.x + r.x, acc.y + r.y, acc.z + r.z, acc.w + r.w);
-                    }
-                    if (4 * c < p.N) *(float4 *)((which ? w.part_k : w.part_q) + tok * p.N + 4 * c) = acc;
-                }
-                if (threadIdx.x >= kThreads - 2) {
-                    const int which = threadIdx.x - (kThreads - 2);
-                    float acc = 0.f;
-                    for (int x = 0; x < kThreads / 32; ++x) acc += red1[which][x];
-                    (which ? w.part_b : w.part_g)[tok] = acc;
-                }
-                __syncthreads();
             }
+            if (seg > 0) next.store(sm.stage[cur ^ 1]);
+            __syncthreads();
+            // the segment's sums over the warps, in order
+            const long long tok = ((long long)blk * p.b * p.H + bh) * p.L + t0;
+            for (int i = threadIdx.x; i < 2 * nt * NC * kLanes; i += kThreads) {
+                const int c = i % (NC * kLanes), t = i / (NC * kLanes) % nt, which = i / (NC * kLanes) / nt;
+                float4 acc = sm.red[which][t][0][c];
+#pragma unroll
+                for (int x = 1; x < kThreads / 32; ++x) {
+                    const float4 r = sm.red[which][t][x][c];
+                    acc = make_float4(acc.x + r.x, acc.y + r.y, acc.z + r.z, acc.w + r.w);
+                }
+                if (4 * c < p.N) *(float4 *)((which ? w.part_k : w.part_q) + (tok + t) * p.N + 4 * c) = acc;
+            }
+            for (int i = threadIdx.x; i < 2 * nt; i += kThreads) {
+                const int which = i / nt, t = i % nt;
+                float acc = 0.f;
+                for (int x = 0; x < kThreads / 32; ++x) acc += sm.red1[which][t][x];
+                (which ? w.part_b : w.part_g)[tok + t] = acc;
+            }
+            __syncthreads();
         }
         store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
         for (int i = threadIdx.x; i < (p.L - V) * kRows; i += kThreads) {
@@ -353,7 +452,7 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaParams p, flo
 }
 
 int row_blocks(int P) { return (P + kRows - 1) / kRows; }
-constexpr int kBwdBlocks = 304;  // two per SM: bounds the history buffer
+constexpr int kBwdBlocks = 304;  // bounds the history buffer
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 struct BwdSizes {
@@ -414,7 +513,12 @@ cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
     f.final_state = nullptr;
     cudaError_t e = fwd<T>(f, w.kept, w.nseg, s);
     if (e != cudaSuccess) return e;
-#define CALL(NC) delta_rows_bwd<T, NC><<<z.grid, kThreads, 0, s>>>(p, w)
+#define CALL(NC)                                                                                          \
+    do {                                                                                                  \
+        const int bytes = (int)sizeof(BwdShared<NC>);                                                     \
+        if ((e = allow_shared((const void *)delta_rows_bwd<T, NC>, bytes)) != cudaSuccess) return e;      \
+        delta_rows_bwd<T, NC><<<z.grid, kThreads, bytes, s>>>(p, w);                                      \
+    } while (0)
     DELTA_BY_NC(CALL)
 #undef CALL
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
