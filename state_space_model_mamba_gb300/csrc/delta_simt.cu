@@ -17,12 +17,14 @@ namespace ssd {
 namespace delta {
 namespace {
 
-constexpr int kRows = 32;   // state rows per block
 constexpr int kLanes = 8;   // lanes per row
-constexpr int kThreads = kRows * kLanes;
-// Tokens staged in shared memory at a time, also the tokens between kept states of the backward
-// (8 for wide keys: the backward's stage and reduction buffers stay within 48 KB).
-constexpr int tok_of(int nc) { return nc > 4 ? 8 : 16; }
+// State rows R per block: 32, or 8 where blocks of 32 would leave SMs without one.  A block's warps read the same
+// keys, and four tokens of them are 100 cycles of the shared memory's for every warp: 2 x 515 tokens of 4 heads,
+// 32 rows each, took 92 us in 8 blocks, PUT us in 32.
+inline int rows_of(long long heads, int P) { return heads * ((P + 31) / 32) < 152 ? 8 : 32; }
+// Tokens staged in shared memory at a time, also the tokens between kept states of the backward, whose
+// states inside a segment have to fit in shared memory too.
+constexpr int tok_of(int nc) { return nc > 4 ? 4 : (nc > 2 ? 8 : 16); }
 
 __device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -38,20 +40,20 @@ __device__ __forceinline__ float4 scale4(float a, float4 x) { return make_float4
 
 // Tokens [t0, t0 + nt) of one (b, h, row block) in shared memory: q and k rows
 // (N, zero-padded to 32 NC), v (and do) of the block's rows, decay and beta.
-template <int NC, bool BWD>
+template <int NC, bool BWD, int R>
 struct Stage {
     static constexpr int kTok = tok_of(NC);
     float4 q[kTok][NC * kLanes], k[kTok][NC * kLanes];
-    float v[kTok][kRows];
-    float dO[BWD ? kTok : 1][kRows];
+    float v[kTok][R];
+    float dO[BWD ? kTok : 1][R];
     float a[kTok], beta[kTok];
 };
 
 // A stage on its way to shared memory: a thread's pieces in registers, loaded while the stage before is worked on.
-template <typename T, int NC, bool BWD>
+template <typename T, int NC, bool BWD, int R>
 struct Fetch {
-    static constexpr int kTok = tok_of(NC), kKeys = (kTok * NC * kLanes + kThreads - 1) / kThreads,
-                         kVals = kTok * kRows / kThreads;
+    static constexpr int kThreads = R * kLanes, kTok = tok_of(NC), kKeys = (kTok * NC * kLanes + kThreads - 1) / kThreads,
+                         kVals = (kTok * R + kThreads - 1) / kThreads;
     float4 q[kKeys], k[kKeys];
     float v[kVals], dO[BWD ? kVals : 1], a, beta;
     __device__ __forceinline__ void load(const DeltaParams &p, int bi, int h, int row0, int t0, int nt) {
@@ -68,20 +70,20 @@ struct Fetch {
         }
 #pragma unroll
         for (int x = 0; x < kVals; ++x) {
-            const int i = threadIdx.x + x * kThreads, t = i / kRows, r = i % kRows;
+            const int i = threadIdx.x + x * kThreads, t = i / R, r = i % R;
             const long long at = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r;
             const bool in = t < nt && row0 + r < p.P;
             v[x] = in ? load1((const T *)p.v + at) : 0.f;
             if (BWD) dO[x] = in ? p.scale * load1((const T *)p.d_o + at) : 0.f;
         }
-        a = beta = 0.f;
+        a = 1.f, beta = 0.f;  // an absent token leaves the state as it is
         if (threadIdx.x < nt) {
             const long long at = ((long long)bi * p.H + h) * p.L + t0 + threadIdx.x;
             a = expf(clamp_log_decay(p.g[at]));
             beta = p.beta[at];
         }
     }
-    __device__ __forceinline__ void store(Stage<NC, BWD> &s) const {
+    __device__ __forceinline__ void store(Stage<NC, BWD, R> &s) const {
 #pragma unroll
         for (int x = 0; x < kKeys; ++x) {
             const int i = threadIdx.x + x * kThreads;
@@ -93,8 +95,10 @@ struct Fetch {
 #pragma unroll
         for (int x = 0; x < kVals; ++x) {
             const int i = threadIdx.x + x * kThreads;
-            (&s.v[0][0])[i] = v[x];
-            if (BWD) (&s.dO[0][0])[i] = dO[x];
+            if (i < kTok * R) {
+                (&s.v[0][0])[i] = v[x];
+                if (BWD) (&s.dO[0][0])[i] = dO[x];
+            }
         }
         if (threadIdx.x < kTok) {
             s.a[threadIdx.x] = a;
@@ -124,13 +128,13 @@ __device__ __forceinline__ void store_row(const float4 (&s)[NC], float *dst, boo
 // ------------------------------------------------------------------ forward
 // Grid: one block per (b, h, row block).  `kept`, when given, gets the state before
 // every segment of tok_of(NC) tokens ([b, H, segments, P, N]), for the backward.
-template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float *kept, int nseg) {
-    constexpr int kTok = tok_of(NC);
-    __shared__ Stage<NC, false> stages[2];
-    __shared__ float outs[2][kTok][kRows];
-    const int nblk = (p.P + kRows - 1) / kRows, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H;
-    const int row0 = (blockIdx.x % nblk) * kRows;
+template <typename T, int NC, int R>
+__global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, float *kept, int nseg) {
+    constexpr int kTok = tok_of(NC), kThreads = R * kLanes;
+    __shared__ Stage<NC, false, R> stages[2];
+    __shared__ float outs[2][kTok][R], gram[kTok / 4][8];
+    const int nblk = (p.P + R - 1) / R, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H;
+    const int row0 = (blockIdx.x % nblk) * R;
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const bool in = row0 + row < p.P;
     const int V = valid_tokens(p, bi);
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float 
     const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
     float4 s[NC];
     load_row(s, p.init ? p.init + srow : nullptr, in, p.N, lane);
-    Fetch<T, NC, false> next;
+    Fetch<T, NC, false, R> next;
     if (V > 0) {
         next.load(p, bi, h, row0, 0, min(kTok, V));
         next.store(stages[0]);
@@ -146,61 +150,79 @@ __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float 
     __syncthreads();
     for (int t0 = 0, cur = 0; t0 < V; t0 += kTok, cur ^= 1) {
         const int nt = min(kTok, V - t0);
-        const Stage<NC, false> &st = stages[cur];
-        float(*out)[kRows] = outs[cur];
+        const Stage<NC, false, R> &st = stages[cur];
+        float(*out)[R] = outs[cur];
         if (t0 + kTok < V) next.load(p, bi, h, row0, t0 + kTok, min(kTok, V - t0 - kTok));
         if (kept)
             store_row(s, kept + (((long long)bh * nseg + t0 / kTok) * p.P + row0 + row) * p.N, in, p.N, lane);
-        // what token t reads of the state is summed over the lanes beside the next token's s.k: one chain of shuffles a token
-        float od = 0.f;
-#pragma unroll 4
-        for (int t = 0; t < nt; ++t) {
-            float4 k[NC];
-            float d0 = 0.f, d1 = 0.f;
+        // k_i.k_j inside each four tokens, a pair per row of lanes
+        constexpr int kPairs = kTok / 4 * 6;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                k[i] = st.k[t][i * kLanes + lane];
-                if (i & 1)
-                    d1 += dot4(s[i], k[i]);
-                else
-                    d0 += dot4(s[i], k[i]);
-            }
-            float d = d0 + d1;
-            const float a = st.a[t], be = st.beta[t], v = st.v[t][row];
+        for (int y = 0; y < (kPairs + R - 1) / R; ++y) {  // by whole warps: rows past the last pair take it again
+            const int x = min(row + y * R, kPairs - 1);
+            const int pair = x % 6, i = pair < 3 ? 0 : (pair < 5 ? 1 : 2), j = pair < 3 ? pair + 1 : (pair < 5 ? pair - 1 : 3);
+            float g = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) s[i] = scale4(a, s[i]);
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) {
-                d += __shfl_xor_sync(0xffffffffu, d, o);
-                od += __shfl_xor_sync(0xffffffffu, od, o);
-            }
-            if (lane == 0 && t > 0) out[t - 1][row] = p.scale * od;
-            const float u = be * (v - a * d);
-            float o0 = 0.f, o1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                s[i] = axpy4(u, k[i], s[i]);
-                if (i & 1)
-                    o1 += dot4(s[i], st.q[t][i * kLanes + lane]);
-                else
-                    o0 += dot4(s[i], st.q[t][i * kLanes + lane]);
-            }
-            od = o0 + o1;
+            for (int c = 0; c < NC; ++c) g += dot4(st.k[x / 6 * 4 + i][c * kLanes + lane], st.k[x / 6 * 4 + j][c * kLanes + lane]);
+            g = sum8(g);
+            if (lane == 0) gram[x / 6][pair] = g;
         }
-        od = sum8(od);
-        if (lane == 0) out[nt - 1][row] = p.scale * od;
+        __syncthreads();
+        // Four tokens a time: the sums s.k of all four from the state before them, one chain of shuffles (beside it
+        // those of what the four before have read); what the tokens between write comes in by the pairs' products.
+        float od[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < nt; t += 4) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < NC; ++i) d[j] += dot4(s[i], st.k[t + j][i * kLanes + lane]);
+            const float4 a = *(const float4 *)(st.a + t), be = *(const float4 *)(st.beta + t);
+            const float *g = gram[t / 4];
+            const float g01 = g[0], g02 = g[1], g03 = g[2], g12 = g[3], g13 = g[4], g23 = g[5];
+            const float v0 = st.v[t][row], v1 = st.v[t + 1][row], v2 = st.v[t + 2][row], v3 = st.v[t + 3][row];
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
+                    od[j] += __shfl_xor_sync(0xffffffffu, od[j], o);
+                }
+            if (t > 0 && lane < 4) out[t - 4 + lane][row] = p.scale * (lane < 2 ? (lane ? od[1] : od[0]) : (lane == 2 ? od[2] : od[3]));
+            float u[4];
+            u[0] = be.x * (v0 - a.x * d[0]);
+            u[1] = be.y * (v1 - a.y * fmaf(u[0], g01, a.x * d[1]));
+            u[2] = be.z * (v2 - a.z * fmaf(u[1], g12, a.y * fmaf(u[0], g02, a.x * d[2])));
+            u[3] = be.w * (v3 - a.w * fmaf(u[2], g23, a.z * fmaf(u[1], g13, a.y * fmaf(u[0], g03, a.x * d[3]))));
+            const float al[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                od[j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    s[i] = axpy4(u[j], st.k[t + j][i * kLanes + lane], scale4(al[j], s[i]));
+                    od[j] += dot4(s[i], st.q[t + j][i * kLanes + lane]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            od[j] = sum8(od[j]);
+            const int t = (nt - 1) / 4 * 4 + j;
+            if (lane == 0 && t < nt) out[t][row] = p.scale * od[j];
+        }
         if (t0 + kTok < V) next.store(stages[cur ^ 1]);
         __syncthreads();
         if (p.o)
-            for (int i = threadIdx.x; i < nt * kRows; i += kThreads) {
-                const int t = i / kRows, r = i % kRows;
+            for (int i = threadIdx.x; i < nt * R; i += kThreads) {
+                const int t = i / R, r = i % R;
                 if (row0 + r < p.P)
                     store1((T *)p.o + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r, out[t][r]);
             }
     }
     if (p.o)
-        for (int i = threadIdx.x; i < (p.L - V) * kRows; i += kThreads) {
-            const int t = V + i / kRows, r = i % kRows;
+        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads) {
+            const int t = V + i / R, r = i % R;
             if (row0 + r < p.P) store1((T *)p.o + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
         }
     store_row(s, p.final_state ? p.final_state + srow : nullptr, in, p.N, lane);
@@ -212,41 +234,44 @@ __global__ void __launch_bounds__(kThreads) delta_rows_fwd(DeltaParams p, float 
 //     D += do q^T;   dbeta = (D k).z;   dz = beta D k = dv;
 //     dk = beta z^T D - dz^T Sd;   dq = do^T S_t;   D -= dz k^T;
 //     dg = <D, Sd>;   D *= a.
-// The states inside a segment are formed again from the kept one and stored
-// per block in `hist` (each element written and read by one thread).  Sums over
+// The states inside a segment are formed again from the kept one and held in
+// shared memory (each element written and read by one thread).  Sums over
 // the rows (dq, dk, dbeta, dg) go to per-row-block partials, which
 // delta_rows_reduce adds in a fixed order.
 struct BwdBuffers {
-    float *kept, *hist, *part_q, *part_k, *part_g, *part_b;
+    float *kept, *part_q, *part_k, *part_g, *part_b;
     int nseg, nblk, items;
 };
 
 // shared memory of a block: two stages, and a segment's sums over each warp's rows
-template <int NC>
+template <int NC, int R>
 struct BwdShared {
-    Stage<NC, true> stage[2];
-    float zs[tok_of(NC)][kRows];
+    static constexpr int kThreads = R * kLanes;
+    Stage<NC, true, R> stage[2];
+    float zs[tok_of(NC)][R];
+    float4 hist[tok_of(NC)][NC][kThreads];
     float4 red[2][tok_of(NC)][kThreads / 32][NC * kLanes];
     float red1[2][tok_of(NC)][kThreads / 32];
 };
-static_assert(sizeof(BwdShared<4>) <= 232448 && sizeof(BwdShared<8>) <= 232448, "shared memory of a block");
+static_assert(sizeof(BwdShared<2, 32>) <= 232448 && sizeof(BwdShared<4, 32>) <= 232448 && sizeof(BwdShared<8, 32>) <= 232448,
+              "shared memory of a block");
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
-    constexpr int kSegTok = tok_of(NC);
+template <typename T, int NC, int R>
+__global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
+    constexpr int kSegTok = tok_of(NC), kThreads = R * kLanes;
     extern __shared__ __align__(16) char smem[];
-    BwdShared<NC> &sm = *(BwdShared<NC> *)smem;
+    BwdShared<NC, R> &sm = *(BwdShared<NC, R> *)smem;
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, warp = threadIdx.x / 32;
-    float4 *hist = (float4 *)w.hist + (size_t)blockIdx.x * kSegTok * NC * kThreads + threadIdx.x;
+    auto hist = [&](int t, int i) -> float4 & { return sm.hist[t][i][threadIdx.x]; };
     for (int item = blockIdx.x; item < w.items; item += gridDim.x) {
-        const int bh = item / w.nblk, blk = item % w.nblk, bi = bh / p.H, h = bh % p.H, row0 = blk * kRows;
+        const int bh = item / w.nblk, blk = item % w.nblk, bi = bh / p.H, h = bh % p.H, row0 = blk * R;
         const bool in = row0 + row < p.P;
         const int V = valid_tokens(p, bi);
         const long long srow = ((long long)bh * p.P + row0 + row) * p.N;
         const int nseg = (V + kSegTok - 1) / kSegTok;
         float4 D[NC], s[NC], sn[NC];
         load_row(D, p.d_final ? p.d_final + srow : nullptr, in, p.N, lane);
-        Fetch<T, NC, true> next;
+        Fetch<T, NC, true, R> next;
         auto fetch = [&](int seg) {
             next.load(p, bi, h, row0, seg * kSegTok, min(kSegTok, V - seg * kSegTok));
             load_row(sn, w.kept + (((long long)bh * w.nseg + seg) * p.P + row0 + row) * p.N, in, p.N, lane);
@@ -259,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
         __syncthreads();
         for (int seg = nseg - 1, cur = 0; seg >= 0; --seg, cur ^= 1) {
             const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
-            const Stage<NC, true> &st = sm.stage[cur];
+            const Stage<NC, true, R> &st = sm.stage[cur];
 #pragma unroll
             for (int i = 0; i < NC; ++i) s[i] = sn[i];
             if (seg > 0) fetch(seg - 1);
@@ -272,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
                 for (int i = 0; i < NC; ++i) {
                     k[i] = st.k[t][i * kLanes + lane];
                     s[i] = scale4(a, s[i]);
-                    hist[(t * NC + i) * kThreads] = s[i];
+                    hist(t, i) = s[i];
                     if (i & 1)
                         d1 += dot4(s[i], k[i]);
                     else
@@ -284,17 +309,13 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
                 for (int i = 0; i < NC; ++i) s[i] = axpy4(be * z, k[i], s[i]);
             }
             __syncwarp();
-            float4 sd[NC], sd_next[NC];
-#pragma unroll
-            for (int i = 0; i < NC; ++i) sd_next[i] = hist[((nt - 1) * NC + i) * kThreads];
             for (int t = nt - 1; t >= 0; --t) {
                 const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = sm.zs[t][row];
-                float4 k[NC];
+                float4 k[NC], sd[NC];
                 float d0 = 0.f, d1 = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    sd[i] = sd_next[i];
-                    if (t > 0) sd_next[i] = hist[((t - 1) * NC + i) * kThreads];
+                    sd[i] = hist(t, i);
                     k[i] = st.k[t][i * kLanes + lane];
                     D[i] = axpy4(dO, st.q[t][i * kLanes + lane], D[i]);
                     if (i & 1)
@@ -366,8 +387,8 @@ __global__ void __launch_bounds__(kThreads) delta_rows_bwd(DeltaParams p, BwdBuf
             __syncthreads();
         }
         store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
-        for (int i = threadIdx.x; i < (p.L - V) * kRows; i += kThreads) {
-            const int t = V + i / kRows, r = i % kRows;
+        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads) {
+            const int t = V + i / R, r = i % R;
             if (row0 + r < p.P) store1((T *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
         }
     }
@@ -409,6 +430,7 @@ __global__ void delta_rows_reduce(DeltaParams p, BwdBuffers w) {
 }
 
 // ------------------------------------------------------------------ one token
+constexpr int kRows = 32, kThreads = kRows * kLanes;  // of a block
 // Grid: one block per (b, h, row block).  Each state element is read and written once, in
 // 16-byte pieces, NC of them in flight per thread.
 template <typename T, int NC>
@@ -451,27 +473,27 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaParams p, flo
     if (in && lane == 0) store1((T *)p.o + vat, p.scale * od);
 }
 
-int row_blocks(int P) { return (P + kRows - 1) / kRows; }
-constexpr int kBwdBlocks = 304;  // bounds the history buffer
+int row_blocks(int P, int R) { return (P + R - 1) / R; }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 struct BwdSizes {
-    size_t kept, hist, part, gate, total;
-    int nseg, nblk, grid;
+    size_t kept, part, gate, total;
+    int nseg, nblk, grid, rows;
 };
 BwdSizes bwd_sizes(long long b, long long L, long long H, long long P, long long N) {
     BwdSizes z;
     const size_t nc = (size_t)(N + 31) / 32;
     const int seg = tok_of((int)nc);
     z.nseg = (int)((L + seg - 1) / seg);
-    z.nblk = row_blocks((int)P);
+    z.rows = rows_of(b * H, (int)P);
+    z.nblk = row_blocks((int)P, z.rows);
     const long long items = b * H * z.nblk;
-    z.grid = (int)(items < kBwdBlocks ? items : kBwdBlocks);
+    const long long most = z.rows == 32 ? 152 : 456;  // a block of 32 rows has an SM to itself
+    z.grid = (int)(items < most ? items : most);
     z.kept = up256(4ull * b * H * z.nseg * P * N);
-    z.hist = up256(16ull * z.grid * seg * nc * kThreads);
     z.part = up256(4ull * z.nblk * b * H * L * N);
     z.gate = up256(4ull * z.nblk * b * H * L);
-    z.total = z.kept + z.hist + 2 * z.part + 2 * z.gate;
+    z.total = z.kept + 2 * z.part + 2 * z.gate;
     return z;
 }
 
@@ -487,37 +509,36 @@ BwdSizes bwd_sizes(long long b, long long L, long long H, long long P, long long
         default: CALL(8); break;       \
     }
 
-template <typename T>
+template <typename T, int R>
 cudaError_t fwd(const DeltaParams &p, float *kept, int nseg, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P));
-#define CALL(NC) delta_rows_fwd<T, NC><<<grid, kThreads, 0, s>>>(p, kept, nseg)
+    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P, R));
+#define CALL(NC) delta_rows_fwd<T, NC, R><<<grid, R * kLanes, 0, s>>>(p, kept, nseg)
     DELTA_BY_NC(CALL)
 #undef CALL
     return cudaGetLastError();
 }
-template <typename T>
+template <typename T, int R>
 cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
     const BwdSizes z = bwd_sizes(p.b, p.L, p.H, p.P, p.N);
     BwdBuffers w;
     w.kept = (float *)ws;
-    w.hist = (float *)(ws + z.kept);
-    w.part_q = (float *)(ws + z.kept + z.hist);
-    w.part_k = (float *)(ws + z.kept + z.hist + z.part);
-    w.part_g = (float *)(ws + z.kept + z.hist + 2 * z.part);
-    w.part_b = (float *)(ws + z.kept + z.hist + 2 * z.part + z.gate);
+    w.part_q = (float *)(ws + z.kept);
+    w.part_k = (float *)(ws + z.kept + z.part);
+    w.part_g = (float *)(ws + z.kept + 2 * z.part);
+    w.part_b = (float *)(ws + z.kept + 2 * z.part + z.gate);
     w.nseg = z.nseg;
     w.nblk = z.nblk;
     w.items = p.b * p.H * z.nblk;
     DeltaParams f = p;
     f.o = nullptr;
     f.final_state = nullptr;
-    cudaError_t e = fwd<T>(f, w.kept, w.nseg, s);
+    cudaError_t e = fwd<T, R>(f, w.kept, w.nseg, s);
     if (e != cudaSuccess) return e;
 #define CALL(NC)                                                                                          \
     do {                                                                                                  \
-        const int bytes = (int)sizeof(BwdShared<NC>);                                                     \
-        if ((e = allow_shared((const void *)delta_rows_bwd<T, NC>, bytes)) != cudaSuccess) return e;      \
-        delta_rows_bwd<T, NC><<<z.grid, kThreads, bytes, s>>>(p, w);                                      \
+        const int bytes = (int)sizeof(BwdShared<NC, R>);                                                  \
+        if ((e = allow_shared((const void *)delta_rows_bwd<T, NC, R>, bytes)) != cudaSuccess) return e;   \
+        delta_rows_bwd<T, NC, R><<<z.grid, R * kLanes, bytes, s>>>(p, w);                                 \
     } while (0)
     DELTA_BY_NC(CALL)
 #undef CALL
@@ -529,7 +550,7 @@ cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t step(const DeltaParams &p, float *state, long long slots, const int32_t *index, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P));
+    const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P, kRows));
 #define CALL(NC) delta_step_kernel<T, NC><<<grid, kThreads, 0, s>>>(p, state, slots, index)
     DELTA_BY_NC(CALL)
 #undef CALL
@@ -541,10 +562,12 @@ cudaError_t step(const DeltaParams &p, float *state, long long slots, const int3
 size_t simt_backward_bytes(const delta_dims &d) { return bwd_sizes(d.batch, d.seqlen, d.nheads, d.headdim, d.dstate).total; }
 
 cudaError_t launch_simt_forward(const DeltaParams &p, bool is_bf16, cudaStream_t s) {
-    return is_bf16 ? fwd<bf16>(p, nullptr, 0, s) : fwd<float>(p, nullptr, 0, s);
+    if (rows_of((long long)p.b * p.H, p.P) == 8) return is_bf16 ? fwd<bf16, 8>(p, nullptr, 0, s) : fwd<float, 8>(p, nullptr, 0, s);
+    return is_bf16 ? fwd<bf16, 32>(p, nullptr, 0, s) : fwd<float, 32>(p, nullptr, 0, s);
 }
 cudaError_t launch_simt_backward(const DeltaParams &p, bool is_bf16, char *ws, cudaStream_t s) {
-    return is_bf16 ? bwd<bf16>(p, ws, s) : bwd<float>(p, ws, s);
+    if (rows_of((long long)p.b * p.H, p.P) == 8) return is_bf16 ? bwd<bf16, 8>(p, ws, s) : bwd<float, 8>(p, ws, s);
+    return is_bf16 ? bwd<bf16, 32>(p, ws, s) : bwd<float, 32>(p, ws, s);
 }
 cudaError_t launch_step(const DeltaParams &p, bool is_bf16, float *state, long long slots, const int32_t *index,
                         cudaStream_t s) {

@@ -115,6 +115,12 @@ def test_f32_forward_backward(dl, shape, init):
     compare(run(dl, x, False, 0.5, init=init), x, False, 0.5, init=init)
 
 
+@pytest.mark.parametrize("shape, valid", [((2, 37, 80, 8, 12, 4), [37, 5]), ((1, 21, 80, 40, 196, 2), None), ((4, 18, 40, 12, 100, 5), [0, 18, 1, 17])])
+def test_f32_more_heads_than_blocks_of_few_rows(dl, shape, valid):
+    x = draw(*shape, seed=sum(shape), bf16=False)
+    compare(run(dl, x, False, 0.5, valid=valid), x, False, 0.5, valid=valid)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("valid", [[150, 0, 1], [64, 128, 149], [63, 65, 2]])
 def test_valid_len_and_garbage_past_it(dl, bf16, valid):
