@@ -5,22 +5,26 @@
 //     s <- a s + beta (v_p - a s.k) k,   o_p = scale s.q,
 // so rows are spread over the grid: 8 lanes hold one row (N / 8 elements each
 // in registers, 4-element pieces interleaved over the lanes so that a row's
-// load is one 128-byte line per piece), 32 rows a block.  What bounds the
-// sequence kernels is the latency of one token (two dependent 8-lane sums),
-// about 150 cycles; the step kernel reads and writes each state once and is
-// bound by HBM: 192 requests of 80 heads, 64 x 128, 1.01 GB in 151 us, 6.7 TB/s, as a copy.
+// load is one 128-byte line per piece), 32 or 8 rows a block.  What bounds the
+// sequence kernels is a warp's own instructions, some 70 a token and three cycles each, in the
+// token's order: the sums over the lanes are taken four tokens at a time, and the next tokens are
+// loaded meanwhile.  Measured in fp32: 2 x 515 tokens, 4 heads of 32 x 48: 71 us (token by token, without
+// loads ahead: 174); its backward, 2 x 129: 19 + 66 + 4 us (44 + 118 + 3).  The step kernel
+// reads and writes each state once and is bound by HBM: 192 requests of 80 heads, 64 x 128, 1.01 GB in
+// 150 us, 6.7 TB/s, as a copy.
 #include <stdio.h>
 
 #include "delta_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace delta {
 namespace {
 
 constexpr int kLanes = 8;   // lanes per row
-// State rows R per block: 32, or 8 where blocks of 32 would leave SMs without one.  A block's warps read the same
-// keys, and four tokens of them are 100 cycles of the shared memory's for every warp: 2 x 515 tokens of 4 heads,
-// 32 rows each, took 92 us in 8 blocks, PUT us in 32.
+// State rows R per block: 32, or 8 where blocks of 32 would leave SMs without one.  A block's warps share its
+// schedulers and shared memory (four tokens' keys are 100 of its cycles for every warp): 2 x 515 tokens of 4 heads,
+// 32 rows each, took 92 us in 8 blocks, 74 in 32.
 inline int rows_of(long long heads, int P) { return heads * ((P + 31) / 32) < 152 ? 8 : 32; }
 // Tokens staged in shared memory at a time, also the tokens between kept states of the backward, whose
 // states inside a segment have to fit in shared memory too.
@@ -32,11 +36,20 @@ __device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 4);
     return x;
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+// in pairs: a warp has a scheduler to itself where heads are few, and each instruction costs it three cycles
+using tc::ffma2;
+using tc::fmul2;
+__device__ __forceinline__ float2 lo2(float4 x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi2(float4 x) { return make_float2(x.z, x.w); }
+__device__ __forceinline__ float2 dot4(float4 a, float4 b, float2 acc) { return ffma2(hi2(a), hi2(b), ffma2(lo2(a), lo2(b), acc)); }
 __device__ __forceinline__ float4 axpy4(float a, float4 x, float4 y) {
-    return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+    const float2 aa = make_float2(a, a), l = ffma2(aa, lo2(x), lo2(y)), h = ffma2(aa, hi2(x), hi2(y));
+    return make_float4(l.x, l.y, h.x, h.y);
 }
-__device__ __forceinline__ float4 scale4(float a, float4 x) { return make_float4(a * x.x, a * x.y, a * x.z, a * x.w); }
+__device__ __forceinline__ float4 scale4(float a, float4 x) {
+    const float2 aa = make_float2(a, a), l = fmul2(aa, lo2(x)), h = fmul2(aa, hi2(x));
+    return make_float4(l.x, l.y, h.x, h.y);
+}
 
 // Tokens [t0, t0 + nt) of one (b, h, row block) in shared memory: q and k rows
 // (N, zero-padded to 32 NC), v (and do) of the block's rows, decay and beta.
@@ -161,10 +174,10 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
         for (int y = 0; y < (kPairs + R - 1) / R; ++y) {  // by whole warps: rows past the last pair take it again
             const int x = min(row + y * R, kPairs - 1);
             const int pair = x % 6, i = pair < 3 ? 0 : (pair < 5 ? 1 : 2), j = pair < 3 ? pair + 1 : (pair < 5 ? pair - 1 : 3);
-            float g = 0.f;
+            float2 g2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) g += dot4(st.k[x / 6 * 4 + i][c * kLanes + lane], st.k[x / 6 * 4 + j][c * kLanes + lane]);
-            g = sum8(g);
+            for (int c = 0; c < NC; ++c) g2 = dot4(st.k[x / 6 * 4 + i][c * kLanes + lane], st.k[x / 6 * 4 + j][c * kLanes + lane], g2);
+            const float g = sum8(g2.x + g2.y);
             if (lane == 0) gram[x / 6][pair] = g;
         }
         __syncthreads();
@@ -172,11 +185,14 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
         // those of what the four before have read); what the tokens between write comes in by the pairs' products.
         float od[4] = {0.f, 0.f, 0.f, 0.f};
         for (int t = 0; t < nt; t += 4) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            float d[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                float2 d2 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) d[j] += dot4(s[i], st.k[t + j][i * kLanes + lane]);
+                for (int i = 0; i < NC; ++i) d2 = dot4(s[i], st.k[t + j][i * kLanes + lane], d2);
+                d[j] = d2.x + d2.y;
+            }
             const float4 a = *(const float4 *)(st.a + t), be = *(const float4 *)(st.beta + t);
             const float *g = gram[t / 4];
             const float g01 = g[0], g02 = g[1], g03 = g[2], g12 = g[3], g13 = g[4], g23 = g[5];
@@ -197,12 +213,13 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
             const float al[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                od[j] = 0.f;
+                float2 o2 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     s[i] = axpy4(u[j], st.k[t + j][i * kLanes + lane], scale4(al[j], s[i]));
-                    od[j] += dot4(s[i], st.q[t + j][i * kLanes + lane]);
+                    o2 = dot4(s[i], st.q[t + j][i * kLanes + lane], o2);
                 }
+                od[j] = o2.x + o2.y;
             }
         }
 #pragma unroll
@@ -246,11 +263,11 @@ struct BwdBuffers {
 // shared memory of a block: two stages, and a segment's sums over each warp's rows
 template <int NC, int R>
 struct BwdShared {
-    static constexpr int kThreads = R * kLanes;
+    static constexpr int kThreads = R * kLanes, kParts = R == 8 ? R : R / 4;  // sums of a row, or of a warp's four
     Stage<NC, true, R> stage[2];
     float zs[tok_of(NC)][R];
     float4 hist[tok_of(NC)][NC][kThreads];
-    float4 red[2][tok_of(NC)][kThreads / 32][NC * kLanes];
+    float4 red[2][tok_of(NC)][kParts][NC * kLanes];
     float red1[2][tok_of(NC)][kThreads / 32];
 };
 static_assert(sizeof(BwdShared<2, 32>) <= 232448 && sizeof(BwdShared<4, 32>) <= 232448 && sizeof(BwdShared<8, 32>) <= 232448,
@@ -258,7 +275,7 @@ static_assert(sizeof(BwdShared<2, 32>) <= 232448 && sizeof(BwdShared<4, 32>) <= 
 
 template <typename T, int NC, int R>
 __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
-    constexpr int kSegTok = tok_of(NC), kThreads = R * kLanes;
+    constexpr int kSegTok = tok_of(NC), kThreads = R * kLanes, kParts = BwdShared<NC, R>::kParts;
     extern __shared__ __align__(16) char smem[];
     BwdShared<NC, R> &sm = *(BwdShared<NC, R> *)smem;
     const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, warp = threadIdx.x / 32;
@@ -292,18 +309,15 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
             for (int t = 0; t < nt; ++t) {
                 const float a = st.a[t], be = st.beta[t], v = st.v[t][row];
                 float4 k[NC];
-                float d0 = 0.f, d1 = 0.f;
+                float2 d2 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     k[i] = st.k[t][i * kLanes + lane];
                     s[i] = scale4(a, s[i]);
                     hist(t, i) = s[i];
-                    if (i & 1)
-                        d1 += dot4(s[i], k[i]);
-                    else
-                        d0 += dot4(s[i], k[i]);
+                    d2 = dot4(s[i], k[i], d2);
                 }
-                const float z = v - sum8(d0 + d1);
+                const float z = v - sum8(d2.x + d2.y);
                 if (lane == 0) sm.zs[t][row] = z;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) s[i] = axpy4(be * z, k[i], s[i]);
@@ -312,52 +326,49 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
             for (int t = nt - 1; t >= 0; --t) {
                 const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = sm.zs[t][row];
                 float4 k[NC], sd[NC];
-                float d0 = 0.f, d1 = 0.f;
+                float2 d2 = make_float2(0.f, 0.f), dg2 = d2;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     sd[i] = hist(t, i);
                     k[i] = st.k[t][i * kLanes + lane];
                     D[i] = axpy4(dO, st.q[t][i * kLanes + lane], D[i]);
-                    if (i & 1)
-                        d1 += dot4(D[i], k[i]);
-                    else
-                        d0 += dot4(D[i], k[i]);
+                    d2 = dot4(D[i], k[i], d2);
                 }
-                const float d = sum8(d0 + d1);
+                const float d = sum8(d2.x + d2.y);
                 const float dz = be * d, bz = be * z;
                 if (lane == 0 && in)
                     store1((T *)p.dv + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + row, dz);
-                float dg = 0.f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     float4 dq = scale4(dO, axpy4(bz, k[i], sd[i]));
                     float4 dk = axpy4(bz, D[i], scale4(-dz, sd[i]));
                     D[i] = axpy4(-dz, k[i], D[i]);
-                    dg += dot4(D[i], sd[i]);
+                    dg2 = dot4(D[i], sd[i], dg2);
                     D[i] = scale4(a, D[i]);
-                    // the warp's four rows
+                    if (kParts == R / 4) {  // over the warp's four rows
 #pragma unroll
-                    for (int o = 8; o <= 16; o <<= 1) {
-                        dq.x += __shfl_xor_sync(0xffffffffu, dq.x, o);
-                        dq.y += __shfl_xor_sync(0xffffffffu, dq.y, o);
-                        dq.z += __shfl_xor_sync(0xffffffffu, dq.z, o);
-                        dq.w += __shfl_xor_sync(0xffffffffu, dq.w, o);
-                        dk.x += __shfl_xor_sync(0xffffffffu, dk.x, o);
-                        dk.y += __shfl_xor_sync(0xffffffffu, dk.y, o);
-                        dk.z += __shfl_xor_sync(0xffffffffu, dk.z, o);
-                        dk.w += __shfl_xor_sync(0xffffffffu, dk.w, o);
+                        for (int o = 8; o <= 16; o <<= 1) {
+                            dq.x += __shfl_xor_sync(0xffffffffu, dq.x, o);
+                            dq.y += __shfl_xor_sync(0xffffffffu, dq.y, o);
+                            dq.z += __shfl_xor_sync(0xffffffffu, dq.z, o);
+                            dq.w += __shfl_xor_sync(0xffffffffu, dq.w, o);
+                            dk.x += __shfl_xor_sync(0xffffffffu, dk.x, o);
+                            dk.y += __shfl_xor_sync(0xffffffffu, dk.y, o);
+                            dk.z += __shfl_xor_sync(0xffffffffu, dk.z, o);
+                            dk.w += __shfl_xor_sync(0xffffffffu, dk.w, o);
+                        }
                     }
-                    if ((threadIdx.x & 31) < kLanes) {
-                        sm.red[0][t][warp][i * kLanes + lane] = dq;
-                        sm.red[1][t][warp][i * kLanes + lane] = dk;
+                    if (kParts == R || (threadIdx.x & 31) < kLanes) {
+                        sm.red[0][t][kParts == R ? row : warp][i * kLanes + lane] = dq;
+                        sm.red[1][t][kParts == R ? row : warp][i * kLanes + lane] = dk;
                     }
                 }
-                // over the warp: every lane has its share of dg, lane 0 of each row its dbeta
-                float db = lane == 0 ? d * z : 0.f;
+                // every lane has its share of dg, lane 0 of each row its dbeta
+                float dg = dg2.x + dg2.y, db = lane == 0 ? d * z : 0.f;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) {
                     dg += __shfl_xor_sync(0xffffffffu, dg, o);
-                    db += __shfl_xor_sync(0xffffffffu, db, o);
+                    if (o >= 8) db += __shfl_xor_sync(0xffffffffu, db, o);
                 }
                 if ((threadIdx.x & 31) == 0) {
                     sm.red1[0][t][warp] = dg;
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
                 const int c = i % (NC * kLanes), t = i / (NC * kLanes) % nt, which = i / (NC * kLanes) / nt;
                 float4 acc = sm.red[which][t][0][c];
 #pragma unroll
-                for (int x = 1; x < kThreads / 32; ++x) {
+                for (int x = 1; x < kParts; ++x) {
                     const float4 r = sm.red[which][t][x][c];
                     acc = make_float4(acc.x + r.x, acc.y + r.y, acc.z + r.z, acc.w + r.w);
                 }
@@ -458,17 +469,16 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaParams p, flo
     }
     const float a = expf(clamp_log_decay(p.g[bi * (long long)p.H + h])), be = p.beta[bi * (long long)p.H + h];
     const float v = in ? load1((const T *)p.v + vat) : 0.f;
-    float d = 0.f;
+    float2 d = make_float2(0.f, 0.f), od2 = d;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) d += dot4(s[i], k[i]);
-    const float u = be * (v - a * sum8(d));
-    float od = 0.f;
+    for (int i = 0; i < NC; ++i) d = dot4(s[i], k[i], d);
+    const float u = be * (v - a * sum8(d.x + d.y));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         s[i] = axpy4(u, k[i], scale4(a, s[i]));
-        od += dot4(s[i], q[i]);
+        od2 = dot4(s[i], q[i], od2);
     }
-    od = sum8(od);
+    const float od = sum8(od2.x + od2.y);
     store_row(s, srow, in, p.N, lane);
     if (in && lane == 0) store1((T *)p.o + vat, p.scale * od);
 }
