@@ -4,8 +4,8 @@
 //
 // All three are streams bound by HBM.  A row is held by TPR threads with NV vectors of
 // VEC columns each, vector j of thread t at columns (j TPR + t) VEC, so that every load
-// of a warp is contiguous (512 bytes at VEC = 8 in bf16).  VEC is 8 where D is a multiple of
-// 8, else 2 or 1: rows then start on the vector's alignment.  The blocks that the SMs hold at
+// of a warp is contiguous.  A vector has 16 bytes where D allows (8 columns in bf16, 4 in
+// fp32), else VEC is 2 or 1: rows then start on the vector's alignment.  The blocks that the SMs hold at
 // once walk the rows: the weight stays in registers (read again for every row it is as much L2
 // traffic as half the row), and the next row is loaded, as it is stored, before the sums of this
 // one are waited for.  The arithmetic is in pairs, and the residual is added in bf16 itself: at
@@ -128,6 +128,8 @@ __device__ __forceinline__ void st_e4m3(uint8_t *p, const float2 *f, float inv) 
             h[i] = __nv_cvt_float2_to_fp8x2(fmul2(f[i], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
         if constexpr (VEC == 2)
             *(uint16_t *)p = h[0];
+        else if constexpr (VEC == 4)
+            *(uint32_t *)p = h[0] | (uint32_t)h[1] << 16;
         else
             *(uint2 *)p = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
     }
@@ -253,10 +255,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
                 for (int i = 0; i < PAIRS; ++i) y.set(i, f[j][i]);
                 y.store((T *)a.y + at + c);
             }
-            if constexpr (FP8 && VEC == 8) {
-                if (a.group) {  // group / 8 neighbouring lanes hold a group's columns of vector j
+            if constexpr (FP8 && VEC >= 4) {
+                if (a.group) {  // group / VEC neighbouring lanes hold a group's columns of vector j
                     float m = amax[0];
-                    for (int o = a.group / 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int o = a.group / (2 * VEC); o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     amax[0] = 0.f;
                     if (live && c < a.D) {
                         st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], e4m3_gain(m));
@@ -456,32 +458,38 @@ ssd_status norm_cuda(cudaError_t e) {
     snprintf(msg, sizeof(msg), "launch failed: %s", cudaGetErrorString(e));
     return norm_fail(SSD_ERR_CUDA, msg);
 }
-int vec_of(int64_t D) { return D % 8 == 0 ? 8 : (D % 2 == 0 ? 2 : 1); }
 
-// Calls f<VEC, TPR, NV> with a row's threads: the fewest of 32 .. 1024 that hold D columns in two vectors of
-// 8 (four where that passes 1024 threads), or in up to 16 of the narrow vectors.
+// Calls F(VEC, TPR, NV) with a row's threads: the fewest of 32 .. 1024 that hold D columns in two vectors of 16 bytes (as
+// many more as a row past 1024 threads needs), or in four narrow ones.
 #define NORM_BY_D(F)                                                         \
     do {                                                                     \
-        const int vec_ = vec_of(D);                                          \
-        const int64_t n_ = D / vec_;                                         \
-        if (vec_ == 8) {                                                     \
-            if (n_ <= 32) F(8, 32, 1);                                       \
-            else if (n_ <= 64) F(8, 32, 2);                                  \
-            else if (n_ <= 128) F(8, 64, 2);                                 \
-            else if (n_ <= 256) F(8, 128, 2);                                \
-            else if (n_ <= 320) F(8, 160, 2);                                \
-            else if (n_ <= 512) F(8, 256, 2);                                \
-            else if (n_ <= 1024) F(8, 512, 2);                               \
-            else F(8, 1024, 2);                                              \
-        } else if (vec_ == 2) {                                              \
-            if (n_ <= 512) F(2, 128, 4);                                     \
-            else if (n_ <= 2048) F(2, 256, 8);                               \
-            else F(2, 1024, 8);                                              \
+        constexpr int kWide = 16 / (int)sizeof(T);                           \
+        const int64_t n_ = D % kWide == 0 ? D / kWide : (D % 2 == 0 ? D / 2 : D); \
+        if (D % kWide == 0) {                                                \
+            if (n_ <= 32) F(kWide, 32, 1);                                   \
+            else if (n_ <= 64) F(kWide, 32, 2);                              \
+            else if (n_ <= 128) F(kWide, 64, 2);                             \
+            else if (n_ <= 256) F(kWide, 128, 2);                            \
+            else if (n_ <= 320) F(kWide, 160, 2);                            \
+            else if (n_ <= 512) F(kWide, 256, 2);                            \
+            else if (n_ <= 640) F(kWide, 320, 2);                            \
+            else if (n_ <= 1024) F(kWide, 512, 2);                           \
+            else if (n_ <= 2048) F(kWide, 1024, 2);                          \
+            else F(kWide, 1024, 4);                                          \
+        } else if (D % 2 == 0) {                                             \
+            NORM_NARROW(F, 2);                                               \
         } else {                                                             \
-            if (n_ <= 512) F(1, 128, 4);                                     \
-            else if (n_ <= 4096) F(1, 512, 8);                               \
-            else F(1, 1024, 16);                                             \
+            NORM_NARROW(F, 1);                                               \
         }                                                                    \
+    } while (0)
+#define NORM_NARROW(F, VEC)                                                  \
+    do {                                                                     \
+        if (n_ <= 512) F(VEC, 128, 4);                                       \
+        else if (n_ <= 1024) F(VEC, 256, 4);                                 \
+        else if (n_ <= 2048) F(VEC, 512, 4);                                 \
+        else if (n_ <= 4096) F(VEC, 1024, 4);                                \
+        else if (n_ <= 8192) F(VEC, 1024, 8);                                \
+        else F(VEC, 1024, 16);                                               \
     } while (0)
 
 template <typename T, bool FP8>
