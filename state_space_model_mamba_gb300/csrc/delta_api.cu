@@ -185,7 +185,7 @@ cudaError_t side_stream(cudaStream_t caller, SideStream **out) {
 
 // The backward of two halves of the batch, each on its own stream.  The scans are serial in the chunks, so a last
 // wave of few chains leaves most SMs to themselves for as long as a full one; the other half's kernels fill them,
-// those of the gradients above all.  2 x 8192 x 80 heads (160 chains on 152 SMs): 2.11 ms for 2.54; 3 x 4096 x 64: 1.28 for
+// those of the gradients above all.  2 x 8192 x 80 heads (160 chains on 152 SMs): 2.11 ms for 2.54 when it was added; 3 x 4096 x 64: 1.28 for
 // 1.39; 4 x 8192 x 80: 4.28 for 4.45.  Chains that all run at once anyway gain nothing (4 x 2048 x 24: 453 us for
 // 440), short ones not the launches.
 bool halves(const ChunkParams &c) {

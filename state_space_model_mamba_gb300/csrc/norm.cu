@@ -67,7 +67,7 @@ struct Vec {
         for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
     // elements 2 i and 2 i + 1 (VEC = 1: the element and 0)
-    static constexpr int PAIRS = (VEC + 1) / 2;
+    [[maybe_unused]] static constexpr int PAIRS = (VEC + 1) / 2;
     __device__ __forceinline__ float2 get(int i) const {
         if constexpr (sizeof(T) == 4)
             return make_float2(__uint_as_float(w[2 * i]), VEC > 1 ? __uint_as_float(w[2 * i + (VEC > 1)]) : 0.f);
