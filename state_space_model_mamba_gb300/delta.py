@@ -82,12 +82,16 @@ def _check_tokens(q, k, v, g, beta, lead):
     H, P = vs[-2:]
     if G < 1 or H % G:
         raise ValueError(f"heads ({H}) must be a multiple of key groups ({G})")
-    keys = vs[:lead] + (G, N)
     gate = (vs[0], H) if lead == 1 else (vs[0], H, vs[1])
-    _want("q", q, keys, dtype, device)
-    _want("k", k, keys, dtype, device)
-    _want("g", g, gate, _F32, device)
-    _want("beta", beta, gate, _F32, device)
+    if not (q.dtype is dtype and k.dtype is dtype and g.dtype is _F32 and beta.dtype is _F32
+            and qs[:lead] == vs[:lead] and k.shape == qs and g.shape == gate and beta.shape == gate
+            and q.device == device and k.device == device and g.device == device and beta.device == device
+            and q.is_contiguous() and k.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
+        keys = vs[:lead] + (G, N)
+        _want("q", q, keys, dtype, device)
+        _want("k", k, keys, dtype, device)
+        _want("g", g, gate, _F32, device)
+        _want("beta", beta, gate, _F32, device)
     return code, G, N, H, P
 
 
@@ -128,8 +132,8 @@ def delta_forward(q, k, v, g, beta, scale=None, init_state=None, valid_len=None,
     fin = torch.empty(b, H, P, N, device=v.device, dtype=_F32) if return_final_state else None
     ws = torch.empty(workspace_bytes(dims, code, False), dtype=torch.uint8, device=v.device)
     ssd._check(_lib().delta_forward(
-        ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
-        _ptr(init_state), _ptr(valid_len), _ptr(o), _ptr(fin), _ptr(ws), ws.numel(), _raw_stream(v.device.index)))
+        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
+        _ptr(init_state), _ptr(valid_len), o.data_ptr(), _ptr(fin), ws.data_ptr(), ws.numel(), _raw_stream(v.device.index)))
     if check_status:
         ssd.workspace_status(ws)
     return o, fin
@@ -151,7 +155,7 @@ def delta_backward(q, k, v, g, beta, do, scale=None, d_final_state=None, init_st
                d_init=torch.empty(b, H, P, N, device=v.device, dtype=_F32) if want_d_init else None)
     ws = torch.empty(workspace_bytes(dims, code, True), dtype=torch.uint8, device=v.device)
     ssd._check(_lib().delta_backward(
-        ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
+        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
         _ptr(init_state), _ptr(valid_len), _ptr(do), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
         _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["d_init"]), _ptr(ws), ws.numel(),
         _raw_stream(v.device.index)))
@@ -178,6 +182,6 @@ def delta_step(q, k, v, g, beta, state, scale=None, state_index=None):
     dims = _dims(b, 1, H, P, N, G)
     o = torch.empty_like(v)
     ssd._check(_lib().delta_step(
-        ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), N ** -0.5 if scale is None else scale,
-        _ptr(state), state.shape[0], _ptr(state_index), _ptr(o), _raw_stream(v.device.index)))
+        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
+        state.data_ptr(), state.shape[0], _ptr(state_index), o.data_ptr(), _raw_stream(v.device.index)))
     return o
