@@ -9,7 +9,7 @@
 // sequence kernels is a warp's own instructions, some 70 a token and three cycles each, in the
 // token's order: the sums over the lanes are taken four tokens at a time, and the next tokens are
 // loaded meanwhile.  Measured in fp32: 2 x 515 tokens, 4 heads of 32 x 48: 71 us (token by token, without
-// loads ahead: 174); its backward, 2 x 129: 19 + 66 + 4 us (44 + 118 + 3).  The step kernel
+// loads ahead: 174); its backward, 2 x 129: 15 + 66 + 3 us (44 + 118 + 3).  The step kernel
 // reads and writes each state once and is bound by HBM: 192 requests of 80 heads, 64 x 128, 1.01 GB in
 // 150 us, 6.7 TB/s, as a copy.
 #include <stdio.h>
@@ -139,9 +139,9 @@ __device__ __forceinline__ void store_row(const float4 (&s)[NC], float *dst, boo
 }
 
 // ------------------------------------------------------------------ forward
-// Grid: one block per (b, h, row block).  `kept`, when given, gets the state before
-// every segment of tok_of(NC) tokens ([b, H, segments, P, N]), for the backward.
-template <typename T, int NC, int R>
+// Grid: one block per (b, h, row block).  Without outputs it is the backward's recompute: `kept` gets the
+// state before every segment of tok_of(NC) tokens ([b, H, segments, P, N]).
+template <typename T, int NC, int R, bool OUT>
 __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, float *kept, int nseg) {
     constexpr int kTok = tok_of(NC), kThreads = R * kLanes;
     __shared__ Stage<NC, false, R> stages[2];
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
         const Stage<NC, false, R> &st = stages[cur];
         float(*out)[R] = outs[cur];
         if (t0 + kTok < V) next.load(p, bi, h, row0, t0 + kTok, min(kTok, V - t0 - kTok));
-        if (kept)
+        if (!OUT)
             store_row(s, kept + (((long long)bh * nseg + t0 / kTok) * p.P + row0 + row) * p.N, in, p.N, lane);
         // k_i.k_j inside each four tokens, a pair per row of lanes
         constexpr int kPairs = kTok / 4 * 6;
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
-                    od[j] += __shfl_xor_sync(0xffffffffu, od[j], o);
+                    if (OUT) od[j] += __shfl_xor_sync(0xffffffffu, od[j], o);
                 }
-            if (t > 0 && lane < 4) out[t - 4 + lane][row] = p.scale * (lane < 2 ? (lane ? od[1] : od[0]) : (lane == 2 ? od[2] : od[3]));
+            if (OUT && t > 0 && lane < 4) out[t - 4 + lane][row] = p.scale * (lane < 2 ? (lane ? od[1] : od[0]) : (lane == 2 ? od[2] : od[3]));
             float u[4];
             u[0] = be.x * (v0 - a.x * d[0]);
             u[1] = be.y * (v1 - a.y * fmaf(u[0], g01, a.x * d[1]));
@@ -217,27 +217,27 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     s[i] = axpy4(u[j], st.k[t + j][i * kLanes + lane], scale4(al[j], s[i]));
-                    o2 = dot4(s[i], st.q[t + j][i * kLanes + lane], o2);
+                    if (OUT) o2 = dot4(s[i], st.q[t + j][i * kLanes + lane], o2);
                 }
                 od[j] = o2.x + o2.y;
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4 && OUT; ++j) {
             od[j] = sum8(od[j]);
             const int t = (nt - 1) / 4 * 4 + j;
             if (lane == 0 && t < nt) out[t][row] = p.scale * od[j];
         }
         if (t0 + kTok < V) next.store(stages[cur ^ 1]);
         __syncthreads();
-        if (p.o)
+        if (OUT)
             for (int i = threadIdx.x; i < nt * R; i += kThreads) {
                 const int t = i / R, r = i % R;
                 if (row0 + r < p.P)
                     store1((T *)p.o + (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r, out[t][r]);
             }
     }
-    if (p.o)
+    if (OUT)
         for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads) {
             const int t = V + i / R, r = i % R;
             if (row0 + r < p.P) store1((T *)p.o + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
@@ -519,10 +519,10 @@ BwdSizes bwd_sizes(long long b, long long L, long long H, long long P, long long
         default: CALL(8); break;       \
     }
 
-template <typename T, int R>
+template <typename T, int R, bool OUT>
 cudaError_t fwd(const DeltaParams &p, float *kept, int nseg, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.b * p.H * row_blocks(p.P, R));
-#define CALL(NC) delta_rows_fwd<T, NC, R><<<grid, R * kLanes, 0, s>>>(p, kept, nseg)
+#define CALL(NC) delta_rows_fwd<T, NC, R, OUT><<<grid, R * kLanes, 0, s>>>(p, kept, nseg)
     DELTA_BY_NC(CALL)
 #undef CALL
     return cudaGetLastError();
@@ -539,10 +539,7 @@ cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
     w.nseg = z.nseg;
     w.nblk = z.nblk;
     w.items = p.b * p.H * z.nblk;
-    DeltaParams f = p;
-    f.o = nullptr;
-    f.final_state = nullptr;
-    cudaError_t e = fwd<T, R>(f, w.kept, w.nseg, s);
+    cudaError_t e = fwd<T, R, false>(p, w.kept, w.nseg, s);
     if (e != cudaSuccess) return e;
 #define CALL(NC)                                                                                          \
     do {                                                                                                  \
@@ -572,8 +569,8 @@ cudaError_t step(const DeltaParams &p, float *state, long long slots, const int3
 size_t simt_backward_bytes(const delta_dims &d) { return bwd_sizes(d.batch, d.seqlen, d.nheads, d.headdim, d.dstate).total; }
 
 cudaError_t launch_simt_forward(const DeltaParams &p, bool is_bf16, cudaStream_t s) {
-    if (rows_of((long long)p.b * p.H, p.P) == 8) return is_bf16 ? fwd<bf16, 8>(p, nullptr, 0, s) : fwd<float, 8>(p, nullptr, 0, s);
-    return is_bf16 ? fwd<bf16, 32>(p, nullptr, 0, s) : fwd<float, 32>(p, nullptr, 0, s);
+    if (rows_of((long long)p.b * p.H, p.P) == 8) return is_bf16 ? fwd<bf16, 8, true>(p, nullptr, 0, s) : fwd<float, 8, true>(p, nullptr, 0, s);
+    return is_bf16 ? fwd<bf16, 32, true>(p, nullptr, 0, s) : fwd<float, 32, true>(p, nullptr, 0, s);
 }
 cudaError_t launch_simt_backward(const DeltaParams &p, bool is_bf16, char *ws, cudaStream_t s) {
     if (rows_of((long long)p.b * p.H, p.P) == 8) return is_bf16 ? bwd<bf16, 8>(p, ws, s) : bwd<float, 8>(p, ws, s);
