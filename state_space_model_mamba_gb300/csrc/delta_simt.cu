@@ -9,7 +9,7 @@
 // sequence kernels is a warp's own instructions, some 70 a token and three cycles each, in the
 // token's order: the sums over the lanes are taken four tokens at a time, and the next tokens are
 // loaded meanwhile.  Measured in fp32: 2 x 515 tokens, 4 heads of 32 x 48: 71 us (token by token, without
-// loads ahead: 174); its backward, 2 x 129: 15 + 66 + 3 us (44 + 118 + 3).  The step kernel
+// loads ahead: 174); its backward, 2 x 129: 15 + 50 + 3 us (44 + 118 + 3).  The step kernel
 // reads and writes each state once and is bound by HBM: 192 requests of 80 heads, 64 x 128, 1.01 GB in
 // 150 us, 6.7 TB/s, as a copy.
 #include <stdio.h>
@@ -70,10 +70,11 @@ struct Fetch {
     float4 q[kKeys], k[kKeys];
     float v[kVals], dO[BWD ? kVals : 1], a, beta;
     __device__ __forceinline__ void load(const DeltaParams &p, int bi, int h, int row0, int t0, int nt) {
+        const int tid = threadIdx.x % kThreads;
         const int g = h / p.hpg, nq = p.N / 4;
 #pragma unroll
         for (int x = 0; x < kKeys; ++x) {
-            const int i = threadIdx.x + x * kThreads, t = i / (NC * kLanes), c = i % (NC * kLanes);
+            const int i = tid + x * kThreads, t = i / (NC * kLanes), c = i % (NC * kLanes);
             const long long at = (((long long)bi * p.L + t0 + t) * p.G + g) * p.N + 4 * c;
             q[x] = k[x] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t < nt && c < nq) {
@@ -83,23 +84,24 @@ struct Fetch {
         }
 #pragma unroll
         for (int x = 0; x < kVals; ++x) {
-            const int i = threadIdx.x + x * kThreads, t = i / R, r = i % R;
+            const int i = tid + x * kThreads, t = i / R, r = i % R;
             const long long at = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + row0 + r;
             const bool in = t < nt && row0 + r < p.P;
             v[x] = in ? load1((const T *)p.v + at) : 0.f;
             if (BWD) dO[x] = in ? p.scale * load1((const T *)p.d_o + at) : 0.f;
         }
         a = 1.f, beta = 0.f;  // an absent token leaves the state as it is
-        if (threadIdx.x < nt) {
-            const long long at = ((long long)bi * p.H + h) * p.L + t0 + threadIdx.x;
+        if (tid < nt) {
+            const long long at = ((long long)bi * p.H + h) * p.L + t0 + tid;
             a = expf(clamp_log_decay(p.g[at]));
             beta = p.beta[at];
         }
     }
     __device__ __forceinline__ void store(Stage<NC, BWD, R> &s) const {
+        const int tid = threadIdx.x % kThreads;
 #pragma unroll
         for (int x = 0; x < kKeys; ++x) {
-            const int i = threadIdx.x + x * kThreads;
+            const int i = tid + x * kThreads;
             if (i < kTok * NC * kLanes) {
                 (&s.q[0][0])[i] = q[x];
                 (&s.k[0][0])[i] = k[x];
@@ -107,15 +109,15 @@ struct Fetch {
         }
 #pragma unroll
         for (int x = 0; x < kVals; ++x) {
-            const int i = threadIdx.x + x * kThreads;
+            const int i = tid + x * kThreads;
             if (i < kTok * R) {
                 (&s.v[0][0])[i] = v[x];
                 if (BWD) (&s.dO[0][0])[i] = dO[x];
             }
         }
-        if (threadIdx.x < kTok) {
-            s.a[threadIdx.x] = a;
-            s.beta[threadIdx.x] = beta;
+        if (tid < kTok) {
+            s.a[tid] = a;
+            s.beta[tid] = beta;
         }
     }
 };
@@ -252,7 +254,8 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
 //     dk = beta z^T D - dz^T Sd;   dq = do^T S_t;   D -= dz k^T;
 //     dg = <D, Sd>;   D *= a.
 // The states inside a segment are formed again from the kept one and held in
-// shared memory (each element written and read by one thread).  Sums over
+// shared memory, by a second group of threads while the first is on the segment behind where a
+// block has few rows (50 us for 66), else by the same threads.  Sums over
 // the rows (dq, dk, dbeta, dg) go to per-row-block partials, which
 // delta_rows_reduce adds in a fixed order.
 struct BwdBuffers {
@@ -264,22 +267,25 @@ struct BwdBuffers {
 template <int NC, int R>
 struct BwdShared {
     static constexpr int kThreads = R * kLanes, kParts = R == 8 ? R : R / 4;  // sums of a row, or of a warp's four
+    static constexpr int kGroups = R == 8 ? 2 : 1;  // of threads: one a segment ahead with its states, where they fit twice
     Stage<NC, true, R> stage[2];
-    float zs[tok_of(NC)][R];
-    float4 hist[tok_of(NC)][NC][kThreads];
+    float zs[kGroups][tok_of(NC)][R];
+    float4 hist[kGroups][tok_of(NC)][NC][kThreads];
     float4 red[2][tok_of(NC)][kParts][NC * kLanes];
     float red1[2][tok_of(NC)][kThreads / 32];
 };
-static_assert(sizeof(BwdShared<2, 32>) <= 232448 && sizeof(BwdShared<4, 32>) <= 232448 && sizeof(BwdShared<8, 32>) <= 232448,
+static_assert(sizeof(BwdShared<2, 8>) <= 232448 && sizeof(BwdShared<4, 8>) <= 232448 && sizeof(BwdShared<8, 8>) <= 232448 &&
+                  sizeof(BwdShared<2, 32>) <= 232448 && sizeof(BwdShared<4, 32>) <= 232448 && sizeof(BwdShared<8, 32>) <= 232448,
               "shared memory of a block");
 
 template <typename T, int NC, int R>
-__global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
-    constexpr int kSegTok = tok_of(NC), kThreads = R * kLanes, kParts = BwdShared<NC, R>::kParts;
+__global__ void __launch_bounds__(R * kLanes * BwdShared<NC, R>::kGroups) delta_rows_bwd(DeltaParams p, BwdBuffers w) {
+    constexpr int kSegTok = tok_of(NC), kThreads = R * kLanes, kParts = BwdShared<NC, R>::kParts,
+                  kGroups = BwdShared<NC, R>::kGroups;
     extern __shared__ __align__(16) char smem[];
     BwdShared<NC, R> &sm = *(BwdShared<NC, R> *)smem;
-    const int row = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, warp = threadIdx.x / 32;
-    auto hist = [&](int t, int i) -> float4 & { return sm.hist[t][i][threadIdx.x]; };
+    const int tid = threadIdx.x % kThreads, row = tid / kLanes, lane = tid % kLanes, warp = tid / 32;
+    const bool ahead = kGroups == 1 || (int)threadIdx.x >= kThreads, back = kGroups == 1 || (int)threadIdx.x < kThreads;
     for (int item = blockIdx.x; item < w.items; item += gridDim.x) {
         const int bh = item / w.nblk, blk = item % w.nblk, bi = bh / p.H, h = bh % p.H, row0 = blk * R;
         const bool in = row0 + row < p.P;
@@ -293,15 +299,10 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
             next.load(p, bi, h, row0, seg * kSegTok, min(kSegTok, V - seg * kSegTok));
             load_row(sn, w.kept + (((long long)bh * w.nseg + seg) * p.P + row0 + row) * p.N, in, p.N, lane);
         };
-        __syncthreads();  // the item before is done with the stages
-        if (nseg > 0) {
-            fetch(nseg - 1);
-            next.store(sm.stage[0]);
-        }
-        __syncthreads();
-        for (int seg = nseg - 1, cur = 0; seg >= 0; --seg, cur ^= 1) {
-            const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
-            const Stage<NC, true, R> &st = sm.stage[cur];
+        // the states of a segment, from the one kept before it
+        auto states = [&](int seg, int buf, int hb) {
+            const int nt = min(kSegTok, V - seg * kSegTok);
+            const Stage<NC, true, R> &st = sm.stage[buf];
 #pragma unroll
             for (int i = 0; i < NC; ++i) s[i] = sn[i];
             if (seg > 0) fetch(seg - 1);
@@ -314,22 +315,25 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
                 for (int i = 0; i < NC; ++i) {
                     k[i] = st.k[t][i * kLanes + lane];
                     s[i] = scale4(a, s[i]);
-                    hist(t, i) = s[i];
+                    sm.hist[hb][t][i][tid] = s[i];
                     d2 = dot4(s[i], k[i], d2);
                 }
                 const float z = v - sum8(d2.x + d2.y);
-                if (lane == 0) sm.zs[t][row] = z;
+                if (lane == 0) sm.zs[hb][t][row] = z;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) s[i] = axpy4(be * z, k[i], s[i]);
             }
-            __syncwarp();
+        };
+        auto reverse = [&](int seg, int buf, int hb) {
+            const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
+            const Stage<NC, true, R> &st = sm.stage[buf];
             for (int t = nt - 1; t >= 0; --t) {
-                const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = sm.zs[t][row];
+                const float dO = st.dO[t][row], be = st.beta[t], a = st.a[t], z = sm.zs[hb][t][row];
                 float4 k[NC], sd[NC];
                 float2 d2 = make_float2(0.f, 0.f), dg2 = d2;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    sd[i] = hist(t, i);
+                    sd[i] = sm.hist[hb][t][i][tid];
                     k[i] = st.k[t][i * kLanes + lane];
                     D[i] = axpy4(dO, st.q[t][i * kLanes + lane], D[i]);
                     d2 = dot4(D[i], k[i], d2);
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
                             dk.w += __shfl_xor_sync(0xffffffffu, dk.w, o);
                         }
                     }
-                    if (kParts == R || (threadIdx.x & 31) < kLanes) {
+                    if (kParts == R || (tid & 31) < kLanes) {
                         sm.red[0][t][kParts == R ? row : warp][i * kLanes + lane] = dq;
                         sm.red[1][t][kParts == R ? row : warp][i * kLanes + lane] = dk;
                     }
@@ -370,16 +374,17 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
                     dg += __shfl_xor_sync(0xffffffffu, dg, o);
                     if (o >= 8) db += __shfl_xor_sync(0xffffffffu, db, o);
                 }
-                if ((threadIdx.x & 31) == 0) {
+                if ((tid & 31) == 0) {
                     sm.red1[0][t][warp] = dg;
                     sm.red1[1][t][warp] = db;
                 }
             }
-            if (seg > 0) next.store(sm.stage[cur ^ 1]);
-            __syncthreads();
-            // the segment's sums over the warps, in order
+        };
+        // the segment's sums over its parts, in order
+        auto sums = [&](int seg) {
+            const int t0 = seg * kSegTok, nt = min(kSegTok, V - t0);
             const long long tok = ((long long)blk * p.b * p.H + bh) * p.L + t0;
-            for (int i = threadIdx.x; i < 2 * nt * NC * kLanes; i += kThreads) {
+            for (int i = threadIdx.x; i < 2 * nt * NC * kLanes; i += kThreads * kGroups) {
                 const int c = i % (NC * kLanes), t = i / (NC * kLanes) % nt, which = i / (NC * kLanes) / nt;
                 float4 acc = sm.red[which][t][0][c];
 #pragma unroll
@@ -389,16 +394,49 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_bwd(DeltaParams p, BwdB
                 }
                 if (4 * c < p.N) *(float4 *)((which ? w.part_k : w.part_q) + (tok + t) * p.N + 4 * c) = acc;
             }
-            for (int i = threadIdx.x; i < 2 * nt; i += kThreads) {
+            for (int i = threadIdx.x; i < 2 * nt; i += kThreads * kGroups) {
                 const int which = i / nt, t = i % nt;
                 float acc = 0.f;
                 for (int x = 0; x < kThreads / 32; ++x) acc += sm.red1[which][t][x];
                 (which ? w.part_b : w.part_g)[tok + t] = acc;
             }
-            __syncthreads();
+        };
+        __syncthreads();  // the item before is done with the stages
+        if (nseg > 0 && ahead) {
+            fetch(nseg - 1);
+            next.store(sm.stage[0]);
         }
-        store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
-        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads) {
+        __syncthreads();
+        if constexpr (kGroups == 1) {
+            for (int seg = nseg - 1, cur = 0; seg >= 0; --seg, cur ^= 1) {
+                states(seg, cur, 0);
+                __syncwarp();
+                reverse(seg, cur, 0);
+                if (seg > 0) next.store(sm.stage[cur ^ 1]);
+                __syncthreads();
+                sums(seg);
+                __syncthreads();
+            }
+        } else {
+            // stage[cur] has segment seg, stage[cur ^ 1] the one before it, whose states are formed meanwhile
+            if (nseg > 0 && ahead) {
+                states(nseg - 1, 0, 0);
+                if (nseg > 1) next.store(sm.stage[1]);
+            }
+            __syncthreads();
+            for (int seg = nseg - 1, cur = 0; seg >= 0; --seg, cur ^= 1) {
+                if (back)
+                    reverse(seg, cur, cur);
+                else if (seg > 0)
+                    states(seg - 1, cur ^ 1, cur ^ 1);
+                __syncthreads();
+                if (ahead && seg > 1) next.store(sm.stage[cur]);
+                sums(seg);
+                __syncthreads();
+            }
+        }
+        if (back) store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
+        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads * kGroups) {
             const int t = V + i / R, r = i % R;
             if (row0 + r < p.P) store1((T *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
         }
@@ -545,7 +583,7 @@ cudaError_t bwd(const DeltaParams &p, char *ws, cudaStream_t s) {
     do {                                                                                                  \
         const int bytes = (int)sizeof(BwdShared<NC, R>);                                                  \
         if ((e = allow_shared((const void *)delta_rows_bwd<T, NC, R>, bytes)) != cudaSuccess) return e;   \
-        delta_rows_bwd<T, NC, R><<<z.grid, R * kLanes, bytes, s>>>(p, w);                                 \
+        delta_rows_bwd<T, NC, R><<<z.grid, R * kLanes * BwdShared<NC, R>::kGroups, bytes, s>>>(p, w);                               \
     } while (0)
     DELTA_BY_NC(CALL)
 #undef CALL
