@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(R * kLanes) delta_rows_fwd(DeltaParams p, floa
             }
     }
     if (OUT)
-        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads) {
-            const int t = V + i / R, r = i % R;
+        for (long long i = threadIdx.x; i < (long long)(p.L - V) * R; i += kThreads) {  // past 32 bits from 2^28 tokens on
+            const int t = V + (int)(i / R), r = (int)(i % R);
             if (row0 + r < p.P) store1((T *)p.o + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
         }
     store_row(s, p.final_state ? p.final_state + srow : nullptr, in, p.N, lane);
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(R * kLanes * BwdShared<NC, R>::kGroups) delta_
             }
         }
         if (back) store_row(D, p.d_init ? p.d_init + srow : nullptr, in, p.N, lane);
-        for (int i = threadIdx.x; i < (p.L - V) * R; i += kThreads * kGroups) {
-            const int t = V + i / R, r = i % R;
+        for (long long i = threadIdx.x; i < (long long)(p.L - V) * R; i += kThreads * kGroups) {  // past 32 bits from 2^28 tokens on
+            const int t = V + (int)(i / R), r = (int)(i % R);
             if (row0 + r < p.P) store1((T *)p.dv + (((long long)bi * p.L + t) * p.H + h) * p.P + row0 + r, 0.f);
         }
     }

@@ -365,3 +365,45 @@ def test_refusals(dl):
         dl.delta_backward(**a, do=x["do"].float())
     with pytest.raises(ValueError):
         dl.delta_step(x["q"][:, 0], x["k"][:, 0], x["v"][:, 0].contiguous(), x["g"][:, :, 0], x["beta"][:, :, 0], x["init"])
+
+
+def test_more_absent_tokens_than_32_bits_count(dl):
+    """Token by token a block makes the absent tokens of its rows zero: 8 rows of 2^28 tokens and more."""
+    import ctypes
+    from state_space_model_mamba_gb300 import ssd
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB")
+    L, valid, W = 2 ** 28 + 70, 5, 4
+    x = draw(1, valid, 1, W, W, 1, seed=9, bf16=False)
+    d = dev(x, False)
+
+    def padded(t, axis):
+        shape = list(t.shape)
+        shape[axis] = L
+        out = torch.zeros(shape, device="cuda")
+        out.narrow(axis, 0, valid).copy_(t)
+        return out
+
+    q, k, v, do = (padded(d[n], 1) for n in ("q", "k", "v", "do"))
+    g, beta = padded(d["g"], 2), padded(d["beta"], 2)
+    vl = torch.tensor([valid], dtype=torch.int32, device="cuda")
+    dims = dl.DeltaDims(1, L, 1, W, W, 1, 0, 0)
+    nan = float("nan")
+    stream = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(dl.workspace_bytes(dims, 0, True), dtype=torch.uint8, device="cuda")
+    o, dv = torch.full_like(v, nan), torch.full_like(v, nan)
+    five = [t.data_ptr() for t in (q, k, v, g, beta)]
+    ssd._check(dl._lib().delta_forward(ctypes.byref(dims), 0, *five, 0.5, None, vl.data_ptr(), o.data_ptr(), None, ws.data_ptr(),
+                                       ws.numel(), stream))
+    ro, _ = od.delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.5)
+    check(o[:, :valid], ro, F32_BAR, "o", 2)
+    assert int(torch.count_nonzero(o[:, valid:])) == 0  # NaN counts
+    del o
+    dq, dk, dg, dbeta = torch.full_like(q, nan), torch.full_like(k, nan), torch.full_like(g, nan), torch.full_like(beta, nan)
+    ssd._check(dl._lib().delta_backward(ctypes.byref(dims), 0, *five, 0.5, None, vl.data_ptr(), do.data_ptr(), None, dq.data_ptr(),
+                                        dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), None, ws.data_ptr(),
+                                        ws.numel(), stream))
+    ref = od.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.5, x["do"])
+    for name, t, axis in (("dq", dq, 1), ("dk", dk, 1), ("dv", dv, 1), ("dg", dg, 2), ("dbeta", dbeta, 2)):
+        check(t.narrow(axis, 0, valid), ref[name], F32_BAR, name, 2)
+        assert int(torch.count_nonzero(t.narrow(axis, valid, L - valid))) == 0, name
