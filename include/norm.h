@@ -30,7 +30,8 @@ ssd_status norm_add_rms(ssd_dtype dtype, const void *x, const void *residual, co
 
 /* The same with y in e4m3 (one byte each) and fp32 scales [rows, D / group]
  * (group 0: one scale a row): scale = max |y| / 448 over the group, y8 the
- * e4m3 value nearest to y / scale; a group of zeros has scale 0 and zeros.
+ * e4m3 value nearest to y / scale (448 at most, where a scale below fp32's
+ * normal numbers was rounded down); a group whose scale is 0 has zeros.
  * group is 0, 32, 64 or 128 and divides D. */
 ssd_status norm_add_rms_fp8(ssd_dtype dtype, const void *x, const void *residual, const float *weight, float eps,
                             void *y8, float *scales, void *stream_out, int64_t rows, int64_t D, int64_t group,

@@ -141,13 +141,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-// what brings a maximum of m to e4m3's largest value.  The reciprocal is off by one unit in the last place at most;
-// for m too small to have one in range it stops at the largest float, so that zeros stay zeros.
-__device__ __forceinline__ float e4m3_gain(float m) {
+// A group's scale, and what its values are multiplied with to come out as y / scale: the reciprocal, off by one unit
+// in the last place at most.  Where that would leave fp32, or the scale is no normal number and so is rounded, values
+// and scale go up by 2^64 first, and the reciprocal is that of the scale as it is stored.  Scales that round to 0
+// (maxima below 448 halves of the smallest float) come with zeros.
+constexpr float kTinyMax = 1e-30f, kUp = 18446744073709551616.f;
+__device__ __forceinline__ float reciprocal(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
-    r *= kE4m3Max;
-    return m == 0.f ? 0.f : (r > 3.4e38f ? 3.4e38f : r);
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ float e4m3_gain(float m, float &scale, float2 (&f)[N]) {
+    scale = m * (1.f / kE4m3Max);
+    if (!(m < kTinyMax)) return reciprocal(m) * kE4m3Max;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fmul2(f[i], make_float2(kUp, kUp));
+    return scale == 0.f ? 0.f : reciprocal(scale * kUp);
 }
 struct Sum {
     static __device__ __forceinline__ float op(float a, float b) { return a + b; }
@@ -260,9 +270,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
                     float m = amax[0];
                     for (int o = a.group / (2 * VEC); o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     amax[0] = 0.f;
+                    float scale;
+                    const float gain = e4m3_gain(m, scale, f[j]);
                     if (live && c < a.D) {
-                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], e4m3_gain(m));
-                        if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = m * (1.f / kE4m3Max);
+                        st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], gain);
+                        if (c % a.group == 0) a.scales[row * (a.D / a.group) + c / a.group] = scale;
                     }
                 }
             }
@@ -270,13 +282,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rms_kernel(NormArgs
         if constexpr (FP8) {
             if (!a.group) {
                 row_reduce<Max, TPR, 1>(amax, buf, turn);
-                const float m = amax[0], inv = e4m3_gain(m);
+                float scale;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int c = (j * TPR + t) * VEC;
-                    if (live && c < a.D) st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], inv);
+                    const float gain = e4m3_gain(amax[0], scale, f[j]);
+                    if (live && c < a.D) st_e4m3<VEC>((uint8_t *)a.y + at + c, f[j], gain);
                 }
-                if (live && t == 0) a.scales[row] = m * (1.f / kE4m3Max);
+                if (live && t == 0) a.scales[row] = scale;
             }
         }
     }

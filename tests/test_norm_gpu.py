@@ -158,3 +158,23 @@ def test_refusals(nm):
     from state_space_model_mamba_gb300 import ssd
     with pytest.raises(ssd.SsdError):
         nm.add_rms_norm_fp8(x, w, group=48)
+
+
+@pytest.mark.parametrize("group,D", [(0, 256), (128, 256), (0, 255), (0, 250), (32, 1024)])
+@pytest.mark.parametrize("top", [1e-41, 1e-38, 3e-37, 1.2e-36, 6e-36, 1e-33, 0.99e-30, 1.01e-30, 1e-20])
+def test_fp8_of_tiny_maxima_multiplies_back(nm, group, D, top):
+    """y8 is nearest to y / scale also where the maximum's reciprocal leaves fp32 or the scale is rounded as a
+    subnormal.  Half a step of e4m3 (2^-4 of the value, half of 2^-9 below 2^-6), and the two roundings on the way
+    (2^-22 of the value) where that decides a tie."""
+    x, _, _, _, w = make(5, D, torch.float32, D + group)
+    x[3] = 0
+    w = w * top
+    y, _ = nm.add_rms_norm(x, w, 1e-5)
+    y8, s, _ = nm.add_rms_norm_fp8(x, w, 1e-5, group=group)
+    y, q, s = (t.double().cpu().numpy() for t in (y.view(5, s.shape[1], -1), y8.float().view(5, s.shape[1], -1), s))
+    m = np.abs(y).max(-1)
+    assert np.all(np.abs(s - m / 448) <= 2.0 ** -23 * m / 448 + 2.0 ** -150) and np.all(s[:3] > 0)
+    assert np.all(q[3] == 0) and np.all(s[3] == 0)
+    r = np.clip(y[:3] / s[:3, :, None], -448, 448)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(r), 2.0 ** -6))) - 3)
+    assert np.all(np.abs(q[:3] - r) <= 0.5 * step + 2.0 ** -22 * np.abs(r))
