@@ -429,14 +429,17 @@ __global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
         if (lane + o < 32) suffix += dn;
         if (lane >= o) prefix += up;
     }
-    prefix -= to.x + to.y;  // before token 2 l
+    // the sums without this lane's tokens are its neighbours': its own may be larger by any factor, and would not come off again
+    const float after = __shfl_down_sync(0xffffffffu, suffix, 1), before = __shfl_up_sync(0xffffffffu, prefix, 1);
+    const float next = (lane < 31 ? after : 0.f) + from.y;
+    prefix = lane ? before : 0.f;
     const long long at = bh * p.L + t;
     if (t < p.L) {
         p.dg[at] = t < V ? ss + prefix + suffix : 0.f;
         p.dbeta[at] = t < V ? db.x : 0.f;
     }
     if (t + 1 < p.L) {
-        p.dg[at + 1] = t + 1 < V ? ss + (prefix + to.x) + (suffix - from.x) : 0.f;
+        p.dg[at + 1] = t + 1 < V ? ss + (prefix + to.x) + next : 0.f;
         p.dbeta[at + 1] = t + 1 < V ? db.y : 0.f;
     }
 }

@@ -407,3 +407,24 @@ def test_more_absent_tokens_than_32_bits_count(dl):
     for name, t, axis in (("dq", dq, 1), ("dk", dk, 1), ("dv", dv, 1), ("dg", dg, 2), ("dbeta", dbeta, 2)):
         check(t.narrow(axis, 0, valid), ref[name], F32_BAR, name, 2)
         assert int(torch.count_nonzero(t.narrow(axis, valid, L - valid))) == 0, name
+
+
+def strong_decay(L, zero_do, seed):
+    """Heads that forget at one rate throughout."""
+    x = draw(2, L, 4, 64, 128, 2, seed=seed)
+    x["g"][:] = -np.array([6.0, 8.0, 10.0, 12.0], np.float32)[None, :, None]
+    if zero_do:
+        x["do"][:] = 0
+    return x
+
+
+@pytest.mark.parametrize("L", [64, 190])
+def test_gate_gradients_under_strong_decay(dl, L):
+    """A gradient of the final state alone: the last tokens' shares of dg are exp(6 .. 12) times those of the tokens
+    before them.  Every head by its own norm; the bar is that of slices."""
+    x = strong_decay(L, True, 71)
+    out = run(dl, x, True, 0.4)
+    ref = od.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.4, x["do"], x["d_final"], x["init"])
+    for name in ("dg", "dbeta"):
+        e = np.linalg.norm(out[name].double().cpu().numpy() - ref[name], axis=2) / np.linalg.norm(ref[name], axis=2)
+        assert e.max() <= 4 * SPLIT_BAR, (name, e)
