@@ -120,7 +120,7 @@ size_t carve(const delta_dims &d, bool backward, char *ws, ChunkParams *c) {
         w.ss = (float *)take(cs * n * 16 * 4);
         for (float **x : {&w.ww, &w.zx}) *x = (float *)take(cs * 4 * n * kChunk * 4);
         for (float **x : {&w.fq, &w.fk}) *x = (float *)take(cs * 2 * n * kChunk * 4);
-        w.pe = (float *)take(cs * n * 512 * 4);
+        w.pe = (float *)take(cs * n * kCrossSums * 4);
     }
     if (c) {
         c->n = (int)n;
@@ -153,7 +153,7 @@ ChunkParams batch_part(const ChunkParams &all, int b0, int nb) {
     move(w.ss, cs * c.n * 16 * 4);
     move(w.ww, cs * 4 * c.n * kChunk * 4), move(w.zx, cs * 4 * c.n * kChunk * 4);
     move(w.fq, cs * 2 * c.n * kChunk * 4), move(w.fk, cs * 2 * c.n * kChunk * 4);
-    move(w.pe, cs * c.n * 512 * 4);
+    move(w.pe, cs * c.n * kCrossSums * 4);
     return c;
 }
 

@@ -58,12 +58,14 @@ constexpr int kImgMat = kGates, kImgFwd = kGates + 2 * kPart, kImgBwd = kGates +
 //   dv_lo  [cs, n]          what dV lost to its rounding: [64 tokens][64] (8 KB)
 // dg is the sum of everything that crosses its token inside the chunk, so that no term carries
 // less decay than the result (products of whole rows, do.o - dv.v and <S, dS>, would be the same sum
-// but cancel where a head forgets fast):
-//     dg_t = ss + sum_{j < t} ww_j + sum_{i >= t} (fq_i + fk_i + pe_i)
+// but cancel where a head forgets fast, and so would sums that a token's own share is taken off again):
+//     dg_t = ss + sum_{j < t} ww_j + sum_{i >= t} (fq_i + fk_i) + sum_{i >= t} sum_{j < t} P_ij
 //     ss = e^gamma_C <S, dS>            S before, dS after the chunk    [cs, n, 16], a share of each warp
 //     ww = beta Z.(e^(gamma_C - gamma) K dS),  zx = Z.X                 [cs, 4, n * 64], sums over 16 columns
 //     fq = q.(scale e^gamma dO S^T),  fk = -k.(e^gamma dV S^T)          [cs, 2, n * 64], over 64 of the keys' columns
-//     pe = row sum - column sum of (Nm o Q K^T + M o K K^T)             [cs, n, 512], the sums in pieces
+//     P = Nm o Q K^T + M o K K^T, as pe                                 [cs, n, 384]:
+//       0 .. 127: each row's sum over columns 0 .. 31 (Nm, then M)
+//       128 + 64 r + t: over the rows i >= t of quarter r (Nm, Nm, M, M), the columns before t of t's own half
 // and dbeta = zx.
 struct ChunkBackward {
     char *states, *dstates, *errs, *dv_lo;
@@ -78,6 +80,7 @@ struct ChunkParams {
     ChunkBackward w; // pointers are null in the forward
     __host__ __device__ char *image(long long bh, int chunk) const { return img + (bh * n + chunk) * (long long)img_bytes; }
 };
+constexpr int kCrossSums = 384;
 constexpr int kStateTile = 32768, kDStateTile = 16384, kErrTile = 16384, kDvLoTile = 8192;
 __host__ __device__ __forceinline__ int slices_of(const DeltaParams &p) { return (p.P + 63) / 64; }
 

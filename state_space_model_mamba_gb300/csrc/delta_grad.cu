@@ -14,8 +14,10 @@
 // group are walked by one block, which adds them up in tensor memory: dq and dk are written
 // once, in a fixed order.  Z, S, Nm and M come as hi + lo parts: what a token reads of S and
 // what the chunk has written over it cancel, and the share of dg that passes between tokens
-// of the chunk is made here,
-//     pe_i = sum_j P_ij - sum_j P_ji,   P = Nm o Q K^T + M o K K^T;
+// of the chunk is made here, as the sums that cross each token,
+//     sum_{i >= t} sum_{j < t} P_ij,   P = Nm o Q K^T + M o K K^T:
+// row sums less column sums would add up to the same, but leave the rounding of pairs that do not cross t, above
+// all of the diagonal, which no decay makes small (heads at g = -8 and -12 throughout: dg 1e-3 and 5e-2 off);
 // dV (beside dO Z^T and dV Z^T), W and dS are rounded once, as dk is.
 // Two blocks share an SM, hide each other's copies and passes, and stay for the whole
 // pass.  What bounds it: an item is 2.9 us of products (40 steps of 128 rows and columns, 20
@@ -306,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                         const uint4 o = pack8(w);
                         st_shared_v4(base + kOffW + off, o.x, o.y, o.z, o.w);
                     }
-                    float2 rs2 = make_float2(0.f, 0.f);
-                    float cs_[32];
+                    float before = 0.f, cs_[32];  // the row's sum so far; for t a column, what row i >= t has before t
                     const int limit = live ? (keys ? i : i + 1) : 0;  // the row's columns that count
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -327,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                             v.y = j + 1 < limit ? v.y : 0.f;
                             a[e] = v;
                             const float2 c = fmul2(v, b[e]);
-                            rs2 = ffma2(c, make_float2(1.f, 1.f), rs2);
-                            cs_[16 * q + 2 * e] = c.x;
-                            cs_[16 * q + 2 * e + 1] = c.y;
+                            cs_[16 * q + 2 * e] = j <= i ? before : 0.f;
+                            cs_[16 * q + 2 * e + 1] = j < i ? before + c.x : 0.f;
+                            before += c.x + c.y;
                         }
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
@@ -350,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
                                 cs_[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                             }
                     }
-                    float *pe = cp.w.pe + (cs * cp.n + chunk) * 512;
-                    pe[half * 128 + row] = rs2.x + rs2.y;
-                    pe[256 + quarter * 64 + 32 * half + lane] = cs_[0];
+                    float *pe = cp.w.pe + (cs * cp.n + chunk) * kCrossSums;
+                    if (half == 0) pe[row] = before;
+                    pe[128 + quarter * 64 + 32 * half + lane] = cs_[0];
                 }
                 ++u;
             }
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
     const long long bh = w / cp.n;
     const int V = valid_tokens(p, (int)(bh / p.H)), t = chunk * kChunk + 2 * lane;
     float2 from = make_float2(0.f, 0.f), to = from, db = from;  // what tokens read, what they write
+    float2 cross = from, first = from;  // pairs across a token; what the later half's rows read of the first half
     float ss = 0.f;
     if (chunk * kChunk < V) {
         for (int x = 0; x < 4 * nsl; ++x) {
@@ -409,37 +411,49 @@ __global__ void __launch_bounds__(256) delta_gate_grads(const ChunkParams cp) {
             from.y += fq.y + fk.y;
         }
         for (int x = 0; x < nsl; ++x) {
-            // row sums of Nm and of M, each over two halves of the columns; column sums, over four quarters of the rows
-            const float *pe = cp.w.pe + ((bh * nsl + x) * cp.n + chunk) * 512 + 2 * lane;
+            // the crossing pairs of rows in four quarters, columns of t's own half; the rows' sums over the first half
+            const float *pe = cp.w.pe + ((bh * nsl + x) * cp.n + chunk) * kCrossSums + 2 * lane;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const float2 r = *(const float2 *)(pe + 64 * y), c = *(const float2 *)(pe + 256 + 64 * y);
-                from.x += r.x - c.x;
-                from.y += r.y - c.y;
+                const float2 c = *(const float2 *)(pe + 128 + 64 * y);
+                cross.x += c.x;
+                cross.y += c.y;
+            }
+            if (lane >= 16) {
+                const float2 n = *(const float2 *)pe, m = *(const float2 *)(pe + 64);
+                first.x += n.x + m.x;
+                first.y += n.y + m.y;
             }
             if (lane < 16) ss += cp.w.ss[((bh * nsl + x) * cp.n + chunk) * 16 + lane];
         }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    float suffix = from.x + from.y, prefix = to.x + to.y;
+    float suffix = from.x + from.y, prefix = to.x + to.y, over = first.x + first.y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const float dn = __shfl_down_sync(0xffffffffu, suffix, o), up = __shfl_up_sync(0xffffffffu, prefix, o);
-        if (lane + o < 32) suffix += dn;
+        const float dn = __shfl_down_sync(0xffffffffu, suffix, o), up = __shfl_up_sync(0xffffffffu, prefix, o),
+                    ov = __shfl_down_sync(0xffffffffu, over, o);
+        if (lane + o < 32) suffix += dn, over += ov;
         if (lane >= o) prefix += up;
     }
     // the sums without this lane's tokens are its neighbours': its own may be larger by any factor, and would not come off again
-    const float after = __shfl_down_sync(0xffffffffu, suffix, 1), before = __shfl_up_sync(0xffffffffu, prefix, 1);
-    const float next = (lane < 31 ? after : 0.f) + from.y;
-    prefix = lane ? before : 0.f;
+    float next = __shfl_down_sync(0xffffffffu, suffix, 1), next_over = __shfl_down_sync(0xffffffffu, over, 1);
+    prefix = __shfl_up_sync(0xffffffffu, prefix, 1);
+    if (lane == 31) next = next_over = 0.f;
+    if (lane == 0) prefix = 0.f;
+    next += from.y;
+    if (lane >= 16) {  // a token of the second half is crossed by all that the rows from it on have in the first
+        cross.x += over;
+        cross.y += next_over + first.y;
+    }
     const long long at = bh * p.L + t;
     if (t < p.L) {
-        p.dg[at] = t < V ? ss + prefix + suffix : 0.f;
+        p.dg[at] = t < V ? ss + prefix + suffix + cross.x : 0.f;
         p.dbeta[at] = t < V ? db.x : 0.f;
     }
     if (t + 1 < p.L) {
-        p.dg[at + 1] = t + 1 < V ? ss + (prefix + to.x) + next : 0.f;
+        p.dg[at + 1] = t + 1 < V ? ss + (prefix + to.x) + next + cross.y : 0.f;
         p.dbeta[at + 1] = t + 1 < V ? db.y : 0.f;
     }
 }

@@ -428,3 +428,16 @@ def test_gate_gradients_under_strong_decay(dl, L):
     for name in ("dg", "dbeta"):
         e = np.linalg.norm(out[name].double().cpu().numpy() - ref[name], axis=2) / np.linalg.norm(ref[name], axis=2)
         assert e.max() <= 4 * SPLIT_BAR, (name, e)
+
+
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("L", [64, 190])
+def test_gradients_under_strong_decay(dl, L, simt):
+    """All that crosses a token is made small by its decay, and so is dg: what does not cross it must not be in the
+    sum.  Every head by its own norm, not floored by those of others; the bars are those of slices."""
+    x = strong_decay(L, False, 72)
+    out = run(dl, x, True, 0.4, simt=simt)
+    ref = od.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.4, x["do"], x["d_final"], x["init"])
+    for name, axes, bar in (("dg", 2, SPLIT_BAR), ("dbeta", 2, SPLIT_BAR), ("dv", (1, 3), BF16_BAR), ("d_init", (2, 3), SPLIT_BAR)):
+        e = np.linalg.norm(out[name].double().cpu().numpy() - ref[name], axis=axes) / np.linalg.norm(ref[name], axis=axes)
+        assert e.max() <= 4 * bar, (name, e)
