@@ -73,7 +73,10 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
         mbar_fence_init();
         sm.err = (base & 1023u) ? 1 : 0;
     }
-    if (warp == 0) tmem_alloc(&sm.tmem, 256);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_alloc(&sm.tmem, 256);
+    }
     for (int i = tid; i < 8192 / 16; i += kThreads) st_shared_v4(base + kOffZero + 16 * i, 0, 0, 0, 0);
     fence_async_smem();
     tc_fence_before();
@@ -381,7 +384,10 @@ __global__ void __launch_bounds__(kThreads, 2) delta_grad_kernel(const ChunkPara
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && sm.err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, 256);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_dealloc(tm, 256);
+    }
 }
 
 // dg and dbeta from the sums (delta_chunk.cuh): a warp per (b, h, chunk), lane l tokens 2 l and 2 l + 1.

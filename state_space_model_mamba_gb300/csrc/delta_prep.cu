@@ -103,7 +103,10 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
                 tma_tile(kq + kb * 16384u + (k_off ^ 8192u) + 4096u * x, &maps.q, &bar_load, 64 * kb, grp, tok, bi);
             }
     }
-    if (warp == 0) tmem_alloc(&sm.tmem, kAccCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_alloc(&sm.tmem, kAccCols);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -311,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 6 : 4) delta_prep_kernel(con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tm, kAccCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_dealloc(tm, kAccCols);
+    }
 }
 
 }  // namespace

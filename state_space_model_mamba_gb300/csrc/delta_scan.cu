@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         mbar_fence_init();
         s_err = 0;
     }
-    if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_alloc(&s_tmem, kTmemCols);
+    }
     // the row octets of Tt that no copy writes are zero
     for (int i = tid; !BWD && i < 32768 / 16; i += kScanThreads) st_shared_v4(base + kOffTri + 16 * i, 0, 0, 0, 0);
     fence_async_smem();
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] = fmul2(a[e], make_float2(f, f));
                 }
+                __syncwarp();  // lanes of absent tokens may come from a branch of their own
                 tmem_st16(ta, (const float *)a);
                 if (kBeside) {
                     const float zero[16] = {};
@@ -451,7 +455,10 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, kTmemCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_dealloc(tm, kTmemCols);
+    }
 }
 
 // ------------------------------------------------------------------ reverse
@@ -507,7 +514,10 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
         s_err = 0;
     }
     constexpr uint32_t kCols = 512, kAcc3 = 256;
-    if (warp == 0) tmem_alloc(&s_tmem, kCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_alloc(&s_tmem, kCols);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -859,7 +869,10 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_err) atomicExch(p.status + kStatusCode, (int)SSD_ERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, kCols);
+    if (warp == 0) {
+        __syncwarp();  // lane 0 may come from a branch of its own
+        tmem_dealloc(tm, kCols);
+    }
 }
 
 }  // namespace
