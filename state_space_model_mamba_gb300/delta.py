@@ -131,9 +131,12 @@ def delta_forward(q, k, v, g, beta, scale=None, init_state=None, valid_len=None,
     o = torch.empty_like(v)
     fin = torch.empty(b, H, P, N, device=v.device, dtype=_F32) if return_final_state else None
     ws = torch.empty(workspace_bytes(dims, code, False), dtype=torch.uint8, device=v.device)
-    ssd._check(_lib().delta_forward(
-        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
-        _ptr(init_state), _ptr(valid_len), o.data_ptr(), _ptr(fin), ws.data_ptr(), ws.numel(), _raw_stream(v.device.index)))
+    index = v.device.index
+    with ssd.on_device(index):
+        ssd._check(_lib().delta_forward(
+            ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            N ** -0.5 if scale is None else scale, _ptr(init_state), _ptr(valid_len), o.data_ptr(), _ptr(fin), ws.data_ptr(),
+            ws.numel(), _raw_stream(index)))
     if check_status:
         ssd.workspace_status(ws)
     return o, fin
@@ -154,11 +157,13 @@ def delta_backward(q, k, v, g, beta, do, scale=None, d_final_state=None, init_st
                dbeta=torch.empty_like(beta),
                d_init=torch.empty(b, H, P, N, device=v.device, dtype=_F32) if want_d_init else None)
     ws = torch.empty(workspace_bytes(dims, code, True), dtype=torch.uint8, device=v.device)
-    ssd._check(_lib().delta_backward(
-        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
-        _ptr(init_state), _ptr(valid_len), _ptr(do), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
-        _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["d_init"]), _ptr(ws), ws.numel(),
-        _raw_stream(v.device.index)))
+    index = v.device.index
+    with ssd.on_device(index):
+        ssd._check(_lib().delta_backward(
+            ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            N ** -0.5 if scale is None else scale, _ptr(init_state), _ptr(valid_len), _ptr(do), _ptr(d_final_state),
+            _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["d_init"]),
+            _ptr(ws), ws.numel(), _raw_stream(index)))
     if check_status:
         ssd.workspace_status(ws)
     return out
@@ -181,7 +186,10 @@ def delta_step(q, k, v, g, beta, state, scale=None, state_index=None):
         _want("state_index", state_index, (b,), _I32, v.device)
     dims = _dims(b, 1, H, P, N, G)
     o = torch.empty_like(v)
-    ssd._check(_lib().delta_step(
-        ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else scale,
-        state.data_ptr(), state.shape[0], _ptr(state_index), o.data_ptr(), _raw_stream(v.device.index)))
+    index = v.device.index
+    with ssd.on_device(index):
+        ssd._check(_lib().delta_step(
+            ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            N ** -0.5 if scale is None else scale, state.data_ptr(), state.shape[0], _ptr(state_index), o.data_ptr(),
+            _raw_stream(index)))
     return o

@@ -71,8 +71,9 @@ def quat_cumprod(q: torch.Tensor, init: torch.Tensor | None = None) -> torch.Ten
     b, L, H, J, _ = q.shape
     cum = torch.empty_like(q)
     ws = quat_workspace(q, False)
-    ssd._check(_lib().m3_quat_cumprod(_ptr(q), _ptr(init), _ptr(cum), b, L, H, J, _ptr(ws), ws.numel(),
-                                      _stream(q.device)))
+    with ssd.on_device(q.device.index):
+        ssd._check(_lib().m3_quat_cumprod(_ptr(q), _ptr(init), _ptr(cum), b, L, H, J, _ptr(ws), ws.numel(),
+                                          _stream(q.device)))
     return cum
 
 
@@ -85,8 +86,9 @@ def quat_cumprod_backward(q, init, d_cum, want_d_init=True):
     d_q = torch.empty_like(q)
     d_init = torch.empty(b, H, J, 4, device=q.device, dtype=torch.float32) if want_d_init else None
     ws = quat_workspace(q, True)
-    ssd._check(_lib().m3_quat_cumprod_backward(_ptr(q), _ptr(init), _ptr(d_cum), _ptr(d_q), _ptr(d_init),
-                                               b, L, H, J, _ptr(ws), ws.numel(), _stream(q.device)))
+    with ssd.on_device(q.device.index):
+        ssd._check(_lib().m3_quat_cumprod_backward(_ptr(q), _ptr(init), _ptr(d_cum), _ptr(d_q), _ptr(d_init),
+                                                   b, L, H, J, _ptr(ws), ws.numel(), _stream(q.device)))
     return d_q, d_init
 
 
@@ -110,8 +112,9 @@ def y_diag(V, B, C, gamma):
     T, m, H, P = V.shape
     N = B.shape[3]
     y = torch.empty_like(V)
-    ssd._check(_lib().m3_y_diag(code, _ptr(V), _ptr(B), _ptr(C), _ptr(gamma), _ptr(y), T, m, H, P, N,
-                                _stream(V.device)))
+    with ssd.on_device(V.device.index):
+        ssd._check(_lib().m3_y_diag(code, _ptr(V), _ptr(B), _ptr(C), _ptr(gamma), _ptr(y), T, m, H, P, N,
+                                    _stream(V.device)))
     return y
 
 
@@ -124,6 +127,7 @@ def y_diag_backward(dY, V, B, C, gamma):
     N = B.shape[3]
     dV, dB, dC = torch.empty_like(V), torch.empty_like(B), torch.empty_like(C)
     dg = torch.empty_like(gamma)
-    ssd._check(_lib().m3_y_diag_backward(code, _ptr(dY), _ptr(V), _ptr(B), _ptr(C), _ptr(gamma), _ptr(dV),
-                                         _ptr(dB), _ptr(dC), _ptr(dg), T, m, H, P, N, _stream(V.device)))
+    with ssd.on_device(V.device.index):
+        ssd._check(_lib().m3_y_diag_backward(code, _ptr(dY), _ptr(V), _ptr(B), _ptr(C), _ptr(gamma), _ptr(dV),
+                                             _ptr(dB), _ptr(dC), _ptr(dg), T, m, H, P, N, _stream(V.device)))
     return dV, dB, dC, dg

@@ -71,8 +71,9 @@ def add_rms_norm(x, weight, eps=1e-5, residual=None):
     code, rows, D, index = _check(x, weight, ("residual",), residual)
     y = torch.empty_like(x)
     stream = x if residual is None else torch.empty_like(x)
-    ssd._check(_lib().norm_add_rms(code, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, y.data_ptr(),
-                                   None if residual is None else _ptr(stream), rows, D, _raw_stream(index)))
+    with ssd.on_device(index):
+        ssd._check(_lib().norm_add_rms(code, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, y.data_ptr(),
+                                       None if residual is None else _ptr(stream), rows, D, _raw_stream(index)))
     return y, stream
 
 
@@ -83,9 +84,10 @@ def add_rms_norm_fp8(x, weight, eps=1e-5, residual=None, group=0):
     y8 = torch.empty(x.shape, device=x.device, dtype=torch.float8_e4m3fn)
     scales = torch.empty(*x.shape[:-1], D // group if group else 1, device=x.device, dtype=torch.float32)
     stream = x if residual is None else torch.empty_like(x)
-    ssd._check(_lib().norm_add_rms_fp8(code, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, y8.data_ptr(), scales.data_ptr(),
-                                       None if residual is None else _ptr(stream), rows, D, group,
-                                       _raw_stream(index)))
+    with ssd.on_device(index):
+        ssd._check(_lib().norm_add_rms_fp8(code, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, y8.data_ptr(),
+                                           scales.data_ptr(), None if residual is None else _ptr(stream), rows, D, group,
+                                           _raw_stream(index)))
     return y8, scales, stream
 
 
@@ -98,6 +100,7 @@ def add_rms_norm_backward(dy, stream, weight, eps=1e-5, d_stream=None):
     dw = torch.empty_like(weight)
     lib = _lib()
     ws = torch.empty(lib.norm_backward_workspace_bytes(rows, D), dtype=torch.uint8, device=stream.device)
-    ssd._check(lib.norm_add_rms_backward(code, _ptr(dy), _ptr(stream), _ptr(weight), eps, _ptr(d_stream), _ptr(dx),
-                                         _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(index)))
+    with ssd.on_device(index):
+        ssd._check(lib.norm_add_rms_backward(code, _ptr(dy), _ptr(stream), _ptr(weight), eps, _ptr(d_stream), _ptr(dx),
+                                             _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(index)))
     return dx, dw

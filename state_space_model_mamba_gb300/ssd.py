@@ -9,6 +9,7 @@ call fails, a RuntimeError is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -166,6 +167,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The library launches on the current device, and the default stream's handle is the same on every one: a call on
+# another device's tensors has to make that device current first.
+_get_device = torch._C._cuda_getDevice
+_here = contextlib.nullcontext()
+
+
+def on_device(index):
+    """Context in which CUDA device ``index`` is the current one (nothing is done where it already is)."""
+    return _here if index == _get_device() else torch.cuda.device(index)
+
+
 def _stream_ptr(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -193,21 +205,23 @@ def forward_into(dims: Dims, x, dt, A, B, C, D, init_state, valid_len, y, final_
                  workspace: torch.Tensor):
     """ssd_forward on caller-provided outputs and workspace (no allocation)."""
     code = _dtype_code(x)
-    _check(load_library().ssd_forward(
-        ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-        _ptr(init_state), _ptr(valid_len), _ptr(y), _ptr(final_state), _ptr(workspace),
-        workspace.numel(), _stream_ptr(x.device)))
+    with on_device(x.device.index):
+        _check(load_library().ssd_forward(
+            ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+            _ptr(init_state), _ptr(valid_len), _ptr(y), _ptr(final_state), _ptr(workspace),
+            workspace.numel(), _stream_ptr(x.device)))
 
 
 def backward_into(dims: Dims, x, dt, A, B, C, D, init_state, valid_len, dy, d_final, dx, ddt,
                   dA, dB, dC, dD, d_init, workspace: torch.Tensor):
     """ssd_backward on caller-provided gradients and workspace (no allocation)."""
     code = _dtype_code(x)
-    _check(load_library().ssd_backward(
-        ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-        _ptr(init_state), _ptr(valid_len), _ptr(dy), _ptr(d_final), _ptr(dx), _ptr(ddt), _ptr(dA),
-        _ptr(dB), _ptr(dC), _ptr(dD), _ptr(d_init), _ptr(workspace), workspace.numel(),
-        _stream_ptr(x.device)))
+    with on_device(x.device.index):
+        _check(load_library().ssd_backward(
+            ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+            _ptr(init_state), _ptr(valid_len), _ptr(dy), _ptr(d_final), _ptr(dx), _ptr(ddt), _ptr(dA),
+            _ptr(dB), _ptr(dC), _ptr(dD), _ptr(d_init), _ptr(workspace), workspace.numel(),
+            _stream_ptr(x.device)))
 
 
 def ssd_forward(x, dt, A, B, C, D, chunk_len, init_state=None, valid_len=None,
@@ -278,9 +292,10 @@ def state_moments(x, dt, A, B, init_state=None, valid_len=None, check_status=Fal
     if n == 0:
         _check(lib.ssd_supported(ctypes.byref(dims.c()), code) or SSD_ERR_UNSUPPORTED)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _check(lib.ssd_state_moments(ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B),
-                                 _ptr(init_state), _ptr(valid_len), _ptr(m2), _ptr(m1), _ptr(count),
-                                 _ptr(ws), ws.numel(), _stream_ptr(dev)))
+    with on_device(dev.index):
+        _check(lib.ssd_state_moments(ctypes.byref(dims.c()), code, _ptr(x), _ptr(dt), _ptr(A), _ptr(B),
+                                     _ptr(init_state), _ptr(valid_len), _ptr(m2), _ptr(m1), _ptr(count),
+                                     _ptr(ws), ws.numel(), _stream_ptr(dev)))
     if check_status:
         workspace_status(ws)
     return m2, m1, count
@@ -292,8 +307,9 @@ def state_pr(m2, m1, count, center=False, pairing=SSD_PAIR_REAL, num=0, pool_bat
     nb = 1 if pool_batch else b
     pr = torch.empty(nb, H, device=m2.device, dtype=torch.float32)
     tr = torch.empty(nb, H, device=m2.device, dtype=torch.float32)
-    _check(load_library().ssd_state_pr(_ptr(m2), _ptr(m1), _ptr(count), b, H, N, int(center), int(pairing),
-                                       int(num), int(pool_batch), _ptr(pr), _ptr(tr), _stream_ptr(m2.device)))
+    with on_device(m2.device.index):
+        _check(load_library().ssd_state_pr(_ptr(m2), _ptr(m1), _ptr(count), b, H, N, int(center), int(pairing),
+                                           int(num), int(pool_batch), _ptr(pr), _ptr(tr), _stream_ptr(m2.device)))
     return pr, tr
 
 
@@ -301,8 +317,9 @@ def workspace_status(workspace: torch.Tensor) -> None:
     """Raise SsdError if the last call on ``workspace`` recorded a device-side
     condition: a timeout, non-finite values (SSD_FLAG_CHECK_FINITE) or clamped
     valid_len entries.  Synchronises the current stream."""
-    _check(load_library().ssd_workspace_status(_ptr(workspace), workspace.numel(),
-                                               _stream_ptr(workspace.device)))
+    with on_device(workspace.device.index):
+        _check(load_library().ssd_workspace_status(_ptr(workspace), workspace.numel(),
+                                                   _stream_ptr(workspace.device)))
 
 
 def wait_selftest(workspace: torch.Tensor, limit_us: int, arrive: bool) -> None:
@@ -310,8 +327,9 @@ def wait_selftest(workspace: torch.Tensor, limit_us: int, arrive: bool) -> None:
     completes (``arrive``) or that nothing completes, giving up after
     ``limit_us`` microseconds; :func:`workspace_status` then reports the
     timeout (ssd_wait_selftest)."""
-    _check(load_library().ssd_wait_selftest(_ptr(workspace), workspace.numel(), int(limit_us), int(arrive),
-                                            _stream_ptr(workspace.device)))
+    with on_device(workspace.device.index):
+        _check(load_library().ssd_wait_selftest(_ptr(workspace), workspace.numel(), int(limit_us), int(arrive),
+                                                _stream_ptr(workspace.device)))
 
 
 def noalloc_status(device=None) -> None:
