@@ -53,7 +53,7 @@ constexpr int kImgMat = kGates, kImgFwd = kGates + 2 * kPart, kImgBwd = kGates +
 // What the backward's kernels keep, per (b, h) chain and slice of 64 columns of P (chain-slice
 // cs = bh * nsl + slice).  Tiles are in the 128-byte swizzle, ready as operands.
 //   states [cs, n]          S before every chunk: hi, lo parts [128 n][64] (32 KB)
-//   dstates [cs, n]         dS after every chunk: [128 n][64] (16 KB)
+//   dstates [cs, n]         dS after every chunk: hi, lo parts [128 n][64] (32 KB)
 //   errs   [cs, n]          Z: hi, lo parts [64 tokens][64] (16 KB)
 //   dv_lo  [cs, n]          what dV lost to its rounding: [64 tokens][64] (8 KB)
 // dg is the sum of everything that crosses its token inside the chunk, so that no term carries
@@ -81,7 +81,7 @@ struct ChunkParams {
     __host__ __device__ char *image(long long bh, int chunk) const { return img + (bh * n + chunk) * (long long)img_bytes; }
 };
 constexpr int kCrossSums = 384;
-constexpr int kStateTile = 32768, kDStateTile = 16384, kErrTile = 16384, kDvLoTile = 8192;
+constexpr int kStateTile = 32768, kDStateTile = 32768, kErrTile = 16384, kDvLoTile = 8192;
 __host__ __device__ __forceinline__ int slices_of(const DeltaParams &p) { return (p.P + 63) / 64; }
 
 inline bool chunk_supported(const delta_dims &d, ssd_dtype t) {

@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
         for (int r = 0; r < 2 && r < nv; ++r) load(r);
         if (nv > 0) load_z(0);
         bool ok = true;
-        auto keep = [&](int r) {  // the hi part of dS after the chunk, from the operand
+        auto keep = [&](int r) {  // dS after the chunk, from the operand
             if (!__all_sync(0xffffffffu, mbar_wait(&bar_s, r & 1))) return false;
             if (lane == 0) {
                 bulk_store(cp.w.dstates + ((long long)blockIdx.x * cp.n + nv - 1 - r) * kDStateTile, base + kOffS, kDStateTile);

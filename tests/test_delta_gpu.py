@@ -441,3 +441,15 @@ def test_gradients_under_strong_decay(dl, L, simt):
     for name, axes, bar in (("dg", 2, SPLIT_BAR), ("dbeta", 2, SPLIT_BAR), ("dv", (1, 3), BF16_BAR), ("d_init", (2, 3), SPLIT_BAR)):
         e = np.linalg.norm(out[name].double().cpu().numpy() - ref[name], axis=axes) / np.linalg.norm(ref[name], axis=axes)
         assert e.max() <= 4 * bar, (name, e)
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 4, 64, 128, 4), (1, 450, 6, 128, 128, 2), (2, 200, 4, 64, 64, 1), (1, 333, 2, 96, 80, 2),
+                                   (2, 130, 3, 64, 128, 1)])
+def test_key_gradients_are_rounded_once(dl, shape):
+    """dq, dk and dv in bf16: one rounding is 1.5e-3 to 1.7e-3 root-mean-square of values spread over a power of two
+    or normal ones, and operands in two parts add nothing to it in quadrature: 2^-9."""
+    x = draw(*shape, seed=80 + sum(shape))
+    out = run(dl, x, True, 0.5)
+    ref = od.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.5, x["do"], x["d_final"], x["init"])
+    for name in ("dq", "dk", "dv"):
+        check(out[name], ref[name], 2.0 ** -9, name, 2)
