@@ -99,6 +99,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = tc::pack_bf2(r.x, r.y);
 }
 
+// and what the two parts leave: x = hi + lo + rest up to 2^-25 of x
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &lo, uint32_t &rest) {
+    const float2 minus = make_float2(-1.f, -1.f);
+    hi = tc::pack_bf2(x, y);
+    const float2 r = tc::ffma2(tc::bf2_to_f2(hi), minus, make_float2(x, y));
+    lo = tc::pack_bf2(r.x, r.y);
+    const float2 e = tc::ffma2(tc::bf2_to_f2(lo), minus, r);
+    rest = tc::pack_bf2(e.x, e.y);
+}
+
 // 8 values as one 16-byte piece of row `row` of a hi and of a lo tile (SW128)
 __device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, int row, int piece, const float2 *x) {
     uint32_t h[4], l[4];
@@ -106,6 +116,16 @@ __device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile,
     for (int e = 0; e < 4; ++e) split2(x[e].x, x[e].y, h[e], l[e]);
     tc::st_shared_v4(hi_tile + tc::sw128_chunk(row, piece), h[0], h[1], h[2], h[3]);
     tc::st_shared_v4(lo_tile + tc::sw128_chunk(row, piece), l[0], l[1], l[2], l[3]);
+}
+// in three parts
+__device__ __forceinline__ void store_parts8(uint32_t hi_tile, uint32_t lo_tile, uint32_t rest_tile, int row, int piece, const float2 *x) {
+    uint32_t h[4], l[4], r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split3(x[e].x, x[e].y, h[e], l[e], r[e]);
+    const uint32_t at = tc::sw128_chunk(row, piece);
+    tc::st_shared_v4(hi_tile + at, h[0], h[1], h[2], h[3]);
+    tc::st_shared_v4(lo_tile + at, l[0], l[1], l[2], l[3]);
+    tc::st_shared_v4(rest_tile + at, r[0], r[1], r[2], r[3]);
 }
 // the same to global memory, the lo tile `lo_off` bytes behind the hi one
 __device__ __forceinline__ void store_parts8(char *tile, int lo_off, int row, int piece, const float2 *x) {

@@ -13,7 +13,8 @@
 // bf16 parts, the hi and lo parts of S and W side by side as one operand of twice the
 // columns, so that the left operand is read once.  The state itself stays in fp32, in
 // tensor memory beside the accumulators, and is added to by the threads with rounding to
-// nearest.
+// nearest.  What the forward adds to it, W, comes in a third part too (2^-25 of a value): two leave
+// 2.5e-6 of the final state, nearly all of its error, where the other operands' second roundings leave 7e-7.
 //
 // What bounds it is the latency of the chain of three products and three passes of
 // the threads.  The rows that carry the chain (K tokens) lie in two of the four lane
@@ -65,6 +66,22 @@ __device__ __forceinline__ void store_operand8(uint32_t tile, uint32_t lo, int r
     const uint32_t at = tile + sw128_chunk(row, piece), al = W == 64 ? at + lo : tile + sw128_chunk(row, piece + W / 8);
     st_shared_v4(at, h[0], h[1], h[2], h[3]);
     st_shared_v4(al, l[0], l[1], l[2], l[3]);
+}
+// and a third part: in a tile of its own (W = 64), or in the columns behind the lo ones, 64 columns a tile
+template <int W>
+__device__ __forceinline__ void store_operand8(uint32_t tile, uint32_t lo, uint32_t rest, int row, int piece, const float2 *x) {
+    if constexpr (W == 64) {
+        store_parts8(tile, tile + lo, rest, row, piece, x);
+    } else {
+        uint32_t h[4], l[4], r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split3(x[e].x, x[e].y, h[e], l[e], r[e]);
+        const uint32_t at = tile + sw128_chunk(row, piece), al = tile + sw128_chunk(row, piece + W / 8),
+                       ar = W == 32 ? at + lo : tile + sw128_chunk(row, piece + W / 4);
+        st_shared_v4(at, h[0], h[1], h[2], h[3]);
+        st_shared_v4(al, l[0], l[1], l[2], l[3]);
+        st_shared_v4(ar, r[0], r[1], r[2], r[3]);
+    }
 }
 // 16 columns of row `row` of the state
 template <int W>
@@ -119,6 +136,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     constexpr int kCompute = compute_threads(W), kScanThreads = scan_threads(W);
     static_assert(!BWD || W == 64, "the backward's tiles have 64 columns");
     constexpr bool kBeside = NB > 1;
+    constexpr bool kThird = !BWD && W < 64;  // W's third part has columns of its own
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nsl = (p.P + W - 1) / W, slice = blockIdx.x % nsl, unit = blockIdx.x / nsl, h = unit % p.H;
     const int bi = NB == 1 && !BWD ? longest_first(p, unit / p.H, lane) : unit / p.H, bh = bi * p.H + h;
@@ -151,7 +169,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     if (warp == kCompute / 32) {
         // ---- products
         const uint32_t i1 = idesc_bf16(128, 2 * W, false, true), i2 = idesc_bf16(128, W, false, true),
-                       i3 = idesc_bf16(128, 2 * W, true, true);
+                       i3 = idesc_bf16(128, kThird ? 3 * W : 2 * W, true, true), i4 = idesc_bf16(128, W, true, true);
         const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
                        dW = sdesc(base + kOffW, 8192, 1024), dT = BWD ? sdesc_plain(base + kOffTri, 1024, 128) : sdesc_plain(base + kOffTri, 128, 256);
         bool ok = true;
@@ -191,6 +209,9 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             if (lane == 0) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)  // W's third part, where X was, on top of its second
+                    if (!BWD && !kThird) mma_bf16(tm + W, sdesc_add(dKt, ks * 2048), sdesc_add(dX, ks * 2048), i4, true);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
@@ -404,7 +425,10 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
                             if (partial && !live) a[4 * u + e] = make_float2(0.f, 0.f);
                             w[e] = fmul2(a[4 * u + e], make_float2(f, f));
                         }
-                        store_operand8<W>(base + kOffW, 8192, i, 2 * group + u, w);
+                        if (BWD)
+                            store_operand8<W>(base + kOffW, 8192, i, 2 * group + u, w);
+                        else
+                            store_operand8<W>(base + kOffW, 8192, base + kOffX, i, 2 * group + u, w);
                     }
                     fence_async_smem();
                 }
@@ -423,12 +447,24 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
                         if (tok < p.L && col + 8 * u < p.P) *(uint4 *)(dst + 8 * u) = live ? pack8(a + 4 * u) : make_uint4(0, 0, 0, 0);
                 }
             }
+            float2 S[8];
+            if (kThird) {
+                __syncwarp();  // lanes store rows of their own
+                tmem_ld16(ts, (float *)S);
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar_m[2], ph));
             if (!ok) break;
             tc_fence_after();
             {
-                float2 a[8], b[8], S[8];
-                tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
+                float2 a[8], b[8];
+                if (kThird) {
+                    float2 r[8];
+                    tmem_ld16x3(ta, tb, tb + W, (float *)a, (float *)b, (float *)r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) b[e] = ffma2(r[e], one, b[e]);
+                } else {
+                    tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
                 if (c + 1 < nv) publish_piece<W>(base + kOffS, row, group, S);
@@ -469,7 +505,8 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 //   2.  Tt^T (beta dU)                  -> X = dU + Tt^T (beta dU),  dV = beta X
 //   3.  K^T (-e^gamma dV) + Q^T D       -> dS = e^gamma_C dS + ...
 // and, with what the forward kept, the sums that the gates' gradients are made of
-// (delta_chunk.cuh).
+// (delta_chunk.cuh).  D and e^gamma dV, which dS takes up, come in three parts as W does in the forward:
+// two left 2.5e-6 of the initial state's gradient.
 // One block per SM, with everything that a step reads in flight a step ahead: two sets of
 // every tile, D in a place of its own, and Q^T D in an accumulator of its own, formed
 // while the chain waits for its threads.  Two blocks per SM (single tiles, 56 registers a
@@ -478,7 +515,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 // Measured: 4.1 us a chunk (4 x 2048 x 24 heads: 136 us; 160 chains of 128 chunks on 152 SMs by themselves: 1049 us, two
 // waves, which is why the backward runs halves of the batch on two streams).
 constexpr uint32_t kOffX2 = 0, kOffW2 = 16384;                   // in the state's place, as in the forward
-constexpr uint32_t kRevTri = 32768, kRevDO = kRevTri + 2 * 32768, kRevD = kRevDO + 2 * 8192, kRevKQ = kRevD + 16384,
+constexpr uint32_t kRevTri = 32768, kRevDO = kRevTri + 2 * 32768, kRevD = kRevDO + 2 * 8192, kRevKQ = kRevD + 24576,
                    kRevZ = kRevKQ + 2 * kKQBytes, kRevBytes = kRevZ + kErrTile;
 static_assert(kRevBytes + 2048 <= 232448, "shared memory of the reverse scan");
 struct RevMaps {
@@ -560,7 +597,9 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
             tc_fence_after();
             if (lane == 0)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + kAcc3, sdesc_add(dQt, ks * 2048), sdesc_add(dD, ks * 2048), i3, ks > 0);
+                for (int ks = 0; ks < 8; ++ks)  // the third part on top of the second
+                    mma_bf16(tm + kAcc3 + (ks >> 2) * 64, sdesc_add(dQt, (ks & 3) * 2048), sdesc_add(dD, (ks >> 2) * 16384 + (ks & 3) * 2048),
+                             ks < 4 ? i3 : i0, ks > 0);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -578,6 +617,9 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16(tm + kAcc3, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, true);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)  // the third part, where X was
+                    mma_bf16(tm + kAcc3 + 64, sdesc_add(dKt, ks * 2048), sdesc_add(dX, ks * 2048), i0, true);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
@@ -734,7 +776,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
                     float2 d[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) d[e] = fmul2(bf2_to_f2(v[e]), make_float2(f, f));
-                    store_parts8(base + kRevD, base + kRevD + 8192, i, 2 * group + x, d);
+                    store_parts8(base + kRevD, base + kRevD + 8192, base + kRevD + 16384, i, 2 * group + x, d);
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -806,7 +848,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
                     float2 w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * x + e], make_float2(f, f));
-                    store_parts8(base + kOffW2, base + kOffW2 + 8192, i, 2 * group + x, w);
+                    store_parts8(base + kOffW2, base + kOffW2 + 8192, base + kOffX2, i, 2 * group + x, w);
                 }
                 fence_async_smem();
                 tc_fence_before();
