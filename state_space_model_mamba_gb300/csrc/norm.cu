@@ -472,8 +472,10 @@ ssd_status norm_cuda(cudaError_t e) {
     return norm_fail(SSD_ERR_CUDA, msg);
 }
 
-// Calls F(VEC, TPR, NV) with a row's threads: the fewest of 32 .. 1024 that hold D columns in two vectors of 16 bytes (as
-// many more as a row past 1024 threads needs), or in four narrow ones.
+// Calls F(VEC, TPR, NV) with a row's threads: of the counts below the fewest that hold D columns in two vectors of 16 bytes, or
+// in four narrow ones; rows too long for 1024 threads of that take more vectors a thread.  The counts are powers of two, and 160
+// and 320 for 2560 and 5120 columns in bf16 (1280 and 2560 in fp32): widths between two of them leave threads without a
+// column (a quarter of 256 at 1536 columns of fp32, say).
 #define NORM_BY_D(F)                                                         \
     do {                                                                     \
         constexpr int kWide = 16 / (int)sizeof(T);                           \
@@ -488,7 +490,7 @@ ssd_status norm_cuda(cudaError_t e) {
             else if (n_ <= 640) F(kWide, 320, 2);                            \
             else if (n_ <= 1024) F(kWide, 512, 2);                           \
             else if (n_ <= 2048) F(kWide, 1024, 2);                          \
-            else F(kWide, 1024, 4);                                          \
+            else if constexpr (kMaxD > 2048 * kWide) F(kWide, 1024, 4);      \
         } else if (D % 2 == 0) {                                             \
             NORM_NARROW(F, 2);                                               \
         } else {                                                             \
@@ -502,7 +504,7 @@ ssd_status norm_cuda(cudaError_t e) {
         else if (n_ <= 2048) F(VEC, 512, 4);                                 \
         else if (n_ <= 4096) F(VEC, 1024, 4);                                \
         else if (n_ <= 8192) F(VEC, 1024, 8);                                \
-        else F(VEC, 1024, 16);                                               \
+        else if constexpr (kMaxD > 8192 * VEC) F(VEC, 1024, 16);             \
     } while (0)
 
 template <typename T, bool FP8>

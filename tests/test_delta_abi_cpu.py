@@ -103,3 +103,30 @@ def test_bindings_refuse_wrong_tensors(lib):
         delta.delta_forward(**ok)
     with pytest.raises(ValueError, match="CUDA"):
         norm.add_rms_norm(torch.zeros(2, 8), torch.ones(8))
+
+
+def test_norm_kernels_are_those_that_some_row_takes(lib):
+    """Every variant that the library holds is reached by a row of 1 .. 16384 columns, and every one reached is there."""
+    import shutil
+    import subprocess
+    if shutil.which("nm") is None:
+        pytest.skip("needs nm")
+    names = subprocess.run(["nm", "-C", ssd.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    held = {(m[1], m[2]) + tuple(int(x) for x in m[3].split(", "))
+            for m in re.finditer(r"\b(add_rms|rms_bwd)_kernel<(float|__nv_bfloat16), (\d+, \d+, \d+)[,>]", names)}
+    reached = set()
+    for t, wide in (("float", 4), ("__nv_bfloat16", 8)):
+        for D in range(1, 16385):
+            vec = wide if D % wide == 0 else 2 - D % 2
+            n = D // vec
+            if vec == wide:
+                if n <= 32:
+                    tpr, nv = 32, 1
+                else:
+                    tpr = next((x for x in (32, 64, 128, 160, 256, 320, 512, 1024) if n <= 2 * x), 1024)
+                    nv = 2 if n <= 2048 else 4
+            else:
+                tpr = next((x for x in (128, 256, 512, 1024) if n <= 4 * x), 1024)
+                nv = 4 if n <= 4096 else (8 if n <= 8192 else 16)
+            reached |= {("add_rms", t, vec, tpr, nv), ("rms_bwd", t, vec, tpr, nv)}
+    assert held == reached, (sorted(held - reached), sorted(reached - held))
