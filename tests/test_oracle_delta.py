@@ -69,3 +69,20 @@ def test_norm_gradient_against_central_differences():
     f = lambda hh, ww: (od.add_rms_norm(hh, ww, 1e-5) * dy).sum() + (ds * hh).sum()  # noqa: E731
     assert abs((f(h + e * u, w) - f(h - e * u, w)) / (2 * e) - (dx * u).sum()) < 1e-7
     assert abs((f(h, w + e * uw) - f(h, w - e * uw)) / (2 * e) - (dw * uw).sum()) < 1e-7
+
+
+def test_steps_through_slots_in_any_order():
+    """Requests keep their slots of a larger pool, one is absent at every step; the other slots are left alone."""
+    x = inputs(7)
+    o, S = od.delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], 0.5, x["init"])
+    r = np.random.default_rng(8)
+    state = r.standard_normal((5,) + x["init"].shape[1:])
+    state[3], state[0] = x["init"][0], x["init"][1]
+    before = state.copy()
+    for t in range(7):
+        order, index = (np.array([1, 0, 0]), np.array([0, 3, -1])) if t % 2 else (np.array([0, 1, 1]), np.array([3, 0, 5]))
+        step = od.delta_step(*(x[n][order, t] for n in ("q", "k", "v")), *(x[n][order, :, t] for n in ("g", "beta")), 0.5, state, index)
+        np.testing.assert_allclose(step[:2], o[order[:2], t], atol=1e-12)
+        assert np.all(step[2] == 0)
+    np.testing.assert_allclose(state[[3, 0]], S, atol=1e-12)
+    np.testing.assert_array_equal(state[[1, 2, 4]], before[[1, 2, 4]])
