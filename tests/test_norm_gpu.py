@@ -178,3 +178,19 @@ def test_fp8_of_tiny_maxima_multiplies_back(nm, group, D, top):
     r = np.clip(y[:3] / s[:3, :, None], -448, 448)
     step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(r), 2.0 ** -6))) - 3)
     assert np.all(np.abs(q[:3] - r) <= 0.5 * step + 2.0 ** -22 * np.abs(r))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [1e-5, 0.1])
+def test_backward_of_one_column(nm, dtype, eps):
+    """dx = dy w rstd (1 - (h rstd)^2), the difference of two nearly equal terms: each within 2^-20 of dy w rstd (rstd
+    within two units of the last place, its square twice as far), then the result's own rounding."""
+    x, _, dy, _, w = make(300, 1, dtype, 4)
+    dx, dw = nm.add_rms_norm_backward(dy, x, w, eps)
+    h, d, ww = (t.double().cpu().numpy() for t in (x, dy, w))
+    r = 1 / np.sqrt(h * h + eps)
+    ref = d * ww * eps * r ** 3
+    err = np.abs(dx.double().cpu().numpy() - ref)
+    assert np.all(err <= 2.0 ** -20 * np.abs(d * ww * r) + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23) * np.abs(ref))
+    assert np.linalg.norm(ref) > 20 * 2.0 ** -20 * np.linalg.norm(d * ww * r)  # zeros would not do
+    assert rel(dw, od.add_rms_norm_backward(d, h, ww, eps)[1]) <= 1e-5
