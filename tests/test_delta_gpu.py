@@ -468,3 +468,10 @@ def test_states_take_up_what_is_written_in_three_parts(dl, shape):
     for name, r in (("final", S), ("d_init", ref["d_init"])):
         e = np.linalg.norm(out[name].double().cpu().numpy() - r) / np.linalg.norm(r)
         assert e <= 1.5e-6, (name, e)
+
+
+@pytest.mark.parametrize("shape, valid", [((2, 965, 39, 128, 8, 3), None), ((3, 970, 26, 96, 8, 13), [970, 100, 961])])
+def test_halves_of_the_batch_with_two_slices_a_head(dl, shape, valid):
+    """More chain slices than SMs over 16 chunks: each half's share of the workspace begins after whole heads of two slices."""
+    x = draw(*shape, seed=sum(shape))
+    compare(run(dl, x, True, 0.3, valid=valid), x, True, 0.3, valid=valid)
