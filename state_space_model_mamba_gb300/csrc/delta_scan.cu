@@ -67,17 +67,17 @@ __device__ __forceinline__ void store_operand8(uint32_t tile, uint32_t lo, int r
     st_shared_v4(at, h[0], h[1], h[2], h[3]);
     st_shared_v4(al, l[0], l[1], l[2], l[3]);
 }
-// and a third part: in a tile of its own (W = 64), or in the columns behind the lo ones, 64 columns a tile
+// in three parts side by side, 64 columns a tile of 8 KB
 template <int W>
-__device__ __forceinline__ void store_operand8(uint32_t tile, uint32_t lo, uint32_t rest, int row, int piece, const float2 *x) {
+__device__ __forceinline__ void store_operand8x3(uint32_t tile, int row, int piece, const float2 *x) {
     if constexpr (W == 64) {
-        store_parts8(tile, tile + lo, rest, row, piece, x);
+        store_parts8(tile, tile + 8192, tile + 16384, row, piece, x);
     } else {
         uint32_t h[4], l[4], r[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split3(x[e].x, x[e].y, h[e], l[e], r[e]);
         const uint32_t at = tile + sw128_chunk(row, piece), al = tile + sw128_chunk(row, piece + W / 8),
-                       ar = W == 32 ? at + lo : tile + sw128_chunk(row, piece + W / 4);
+                       ar = W == 32 ? at + 8192 : tile + sw128_chunk(row, piece + W / 4);
         st_shared_v4(at, h[0], h[1], h[2], h[3]);
         st_shared_v4(al, l[0], l[1], l[2], l[3]);
         st_shared_v4(ar, r[0], r[1], r[2], r[3]);
@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     constexpr int kCompute = compute_threads(W), kScanThreads = scan_threads(W);
     static_assert(!BWD || W == 64, "the backward's tiles have 64 columns");
     constexpr bool kBeside = NB > 1;
-    constexpr bool kThird = !BWD && W < 64;  // W's third part has columns of its own
+    // W's parts side by side, in the place of X lo too where they take 24 KB; the state behind their accumulators
+    constexpr int kParts = BWD ? 2 : 3;
+    constexpr uint32_t kAtW = kParts * W > 128 ? kOffX + 8192 : kOffW, kStateCol = kParts * W > 128 ? 192 : 128;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nsl = (p.P + W - 1) / W, slice = blockIdx.x % nsl, unit = blockIdx.x / nsl, h = unit % p.H;
     const int bi = NB == 1 && !BWD ? longest_first(p, unit / p.H, lane) : unit / p.H, bh = bi * p.H + h;
@@ -169,9 +171,9 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
     if (warp == kCompute / 32) {
         // ---- products
         const uint32_t i1 = idesc_bf16(128, 2 * W, false, true), i2 = idesc_bf16(128, W, false, true),
-                       i3 = idesc_bf16(128, kThird ? 3 * W : 2 * W, true, true), i4 = idesc_bf16(128, W, true, true);
+                       i3 = idesc_bf16(128, kParts * W, true, true);
         const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX, 8192, 1024),
-                       dW = sdesc(base + kOffW, 8192, 1024), dT = BWD ? sdesc_plain(base + kOffTri, 1024, 128) : sdesc_plain(base + kOffTri, 128, 256);
+                       dW = sdesc(base + kAtW, 8192, 1024), dT = BWD ? sdesc_plain(base + kOffTri, 1024, 128) : sdesc_plain(base + kOffTri, 128, 256);
         bool ok = true;
         int done = 0;
         for (int c = 0; c < nv; ++c) {
@@ -209,9 +211,6 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             if (lane == 0) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_bf16(tm, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, ks > 0);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)  // W's third part, where X was, on top of its second
-                    if (!BWD && !kThird) mma_bf16(tm + W, sdesc_add(dKt, ks * 2048), sdesc_add(dX, ks * 2048), i4, true);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
         const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
         const bool keys = quarter < 2;       // rows 0 .. 63: K tokens, 64 .. 127: Q tokens
         const int i = row & 63, col = slice * W + 16 * group;
-        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + W, ts = ta + 128;
+        const uint32_t ta = tmem_addr(tm, 32 * quarter, 16 * group), tb = ta + W, ts = ta + kStateCol;
         const float2 one = make_float2(1.f, 1.f);
         bool ok = true;
         // the state operand of chunk c is written; before the last chunk, K rows of absent tokens are made zero
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
                         if (BWD)
                             store_operand8<W>(base + kOffW, 8192, i, 2 * group + u, w);
                         else
-                            store_operand8<W>(base + kOffW, 8192, base + kOffX, i, 2 * group + u, w);
+                            store_operand8x3<W>(base + kAtW, i, 2 * group + u, w);
                     }
                     fence_async_smem();
                 }
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
                 }
             }
             float2 S[8];
-            if (kThird) {
+            if (kParts == 3 && kBeside) {
                 __syncwarp();  // lanes store rows of their own
                 tmem_ld16(ts, (float *)S);
             }
@@ -457,11 +456,15 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
             tc_fence_after();
             {
                 float2 a[8], b[8];
-                if (kThird) {
+                if (kParts == 3) {
                     float2 r[8];
-                    tmem_ld16x3(ta, tb, tb + W, (float *)a, (float *)b, (float *)r);
+                    if (kBeside)
+                        tmem_ld16x3(ta, tb, tb + W, (float *)a, (float *)b, (float *)r);
+                    else
+                        tmem_ld16x2(tb, tb + W, (float *)b, (float *)r);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) b[e] = ffma2(r[e], one, b[e]);
+                    if (!kBeside) tmem_ld16x2(ta, ts, (float *)a, (float *)S);  // fewer registers at once
                 } else {
                     tmem_ld16x3(ta, tb, ts, (float *)a, (float *)b, (float *)S);
                 }
