@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 // read where they are used cost 2 us of a step's 5: Z comes by copy, S into registers, a step ahead.
 // Measured: 4.1 us a chunk (4 x 2048 x 24 heads: 136 us; 160 chains of 128 chunks on 152 SMs by themselves: 1049 us, two
 // waves, which is why the backward runs halves of the batch on two streams).
-constexpr uint32_t kOffX2 = 0, kOffW2 = 16384;                   // in the state's place, as in the forward
+constexpr uint32_t kOffX2 = 0, kOffW2 = 8192;                    // in the state's place, as in the forward
 constexpr uint32_t kRevTri = 32768, kRevDO = kRevTri + 2 * 32768, kRevD = kRevDO + 2 * 8192, kRevKQ = kRevD + 24576,
                    kRevZ = kRevKQ + 2 * kKQBytes, kRevBytes = kRevZ + kErrTile;
 static_assert(kRevBytes + 2048 <= 232448, "shared memory of the reverse scan");
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
     if (warp == kCompute / 32) {
         // ---- products; step r is chunk nv - 1 - r
         const uint32_t i0 = idesc_bf16(128, 64, true, true), i1 = idesc_bf16(128, 128, false, true),
-                       i3 = idesc_bf16(128, 128, true, true);
+                       i2 = idesc_bf16(128, 128, true, true), i3 = idesc_bf16(128, 192, true, true);
         const uint64_t dS = sdesc(base + kOffS, 16384, 1024), dX = sdesc(base + kOffX2, 8192, 1024),
                        dW = sdesc(base + kOffW2, 8192, 1024), dD = sdesc(base + kRevD, 8192, 1024);
         bool ok = true;
@@ -600,9 +600,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
             tc_fence_after();
             if (lane == 0)
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)  // the third part on top of the second
-                    mma_bf16(tm + kAcc3 + (ks >> 2) * 64, sdesc_add(dQt, (ks & 3) * 2048), sdesc_add(dD, (ks >> 2) * 16384 + (ks & 3) * 2048),
-                             ks < 4 ? i3 : i0, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_bf16(tm + kAcc3, sdesc_add(dQt, ks * 2048), sdesc_add(dD, ks * 2048), i3, ks > 0);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_x, ph)))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm, sdesc_add(dT, part * kSquare + ks * 256), sdesc_add(dX, ks * 2048), part ? i0 : i3, true);
+                        mma_bf16(tm, sdesc_add(dT, part * kSquare + ks * 256), sdesc_add(dX, ks * 2048), part ? i0 : i2, true);
                 mma_commit(&bar_m[1]);
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar_w, ph)))) break;
@@ -620,9 +618,6 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16(tm + kAcc3, sdesc_add(dKt, ks * 2048), sdesc_add(dW, ks * 2048), i3, true);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)  // the third part, where X was
-                    mma_bf16(tm + kAcc3 + 64, sdesc_add(dKt, ks * 2048), sdesc_add(dX, ks * 2048), i0, true);
                 mma_commit(&bar_m[2]);
             }
             __syncwarp();
@@ -851,7 +846,7 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
                     float2 w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = fmul2(a[4 * x + e], make_float2(f, f));
-                    store_parts8(base + kOffW2, base + kOffW2 + 8192, base + kOffX2, i, 2 * group + x, w);
+                    store_parts8(base + kOffW2, base + kOffW2 + 8192, base + kOffW2 + 16384, i, 2 * group + x, w);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -885,8 +880,11 @@ __global__ void __launch_bounds__(scan_threads(64), 1)
             if (!ok) break;
             tc_fence_after();
             {
-                float2 a[8], b[8], S[8];
-                tmem_ld16x3(t3, t3 + 64, ts, (float *)a, (float *)b, (float *)S);
+                float2 a[8], b[8], S[8], rest[8];
+                tmem_ld16x2(t3 + 64, t3 + 128, (float *)b, (float *)rest);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[e] = ffma2(rest[e], one, b[e]);
+                tmem_ld16x2(t3, ts, (float *)a, (float *)S);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[e] = ffma2(S[e], make_float2(ec, ec), ffma2(b[e], one, a[e]));
                 if (r + 1 < nv) publish_piece<64>(base + kOffS, row, group, S);
