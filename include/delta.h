@@ -12,6 +12,9 @@
  * where V = valid_len[b] (default L).  Tokens t >= V are absent: no state
  * update, o = 0, and every per-token gradient there is 0; their q, k, v, g,
  * beta and do values are not used (NaN and infinities there do no harm).
+ * A NaN or an infinity in a present token's q, k, v, g, beta or do makes no promise for its
+ * sequence and key group: the chunked kernels multiply it by stored zeros, so that tokens before it
+ * in its chunk (64 tokens) may become NaN too, where the token-by-token kernels leave them alone.
  * Keys are used as given: a layer normalises q and k to unit length before
  * the call, with beta in [0, 1] the recurrence then contracts.
  *
@@ -25,6 +28,12 @@
  * T is fp32 for SSD_F32 and bf16 for SSD_BF16.  g is the log of the decay,
  * g <= 0 (values below -1000 act as -1000: a decay of exactly 0); beta is
  * used as given and may be 0.
+ *
+ * Precision of SSD_BF16: outputs in bf16 are rounded once (1.7e-3 of an output's norm).  The
+ * chunked kernels feed fp32 values to the tensor cores as two bf16 parts (2^-17 of a value at most) and what a
+ * state takes up as three; of an fp32 output's norm final_state and d_init are below 1e-6 off, dg and dbeta
+ * 2e-6 to 5e-6.  DELTA_FLAG_SIMT keeps every operand in fp32: 1e-7 to 3e-7, at the token-by-token
+ * kernels' speed.  So does SSD_F32.
  *
  * Memory, streams, errors: as in ssd.h.  The caller owns every buffer, the
  * workspace is sized by delta_workspace_bytes, work is enqueued on `stream`
@@ -72,7 +81,9 @@ typedef struct {
 ssd_status delta_supported(const delta_dims *dims, ssd_dtype dtype);
 
 /* Bytes of workspace delta_forward (backward = 0) or delta_backward
- * (backward = 1) needs; 0 when the arguments are invalid. */
+ * (backward = 1) needs; 0 when the arguments are invalid.  The backward keeps a state
+ * every 64 tokens (chunked), or every 16, 8 or 4 (token by token, dstate up to 64, 128 or 256), and token by token
+ * its key gradients' sums per 32 rows of a head, 8 where heads are few: 0.26 MB a token at 4 heads of 128 x 256. */
 size_t delta_workspace_bytes(const delta_dims *dims, ssd_dtype dtype, int backward);
 
 /* Forward: o (and optionally final_state).  init_state may be NULL (zeros),

@@ -19,10 +19,10 @@
 // row sums less column sums would add up to the same, but leave the rounding of pairs that do not cross t, above
 // all of the diagonal, which no decay makes small (heads at g = -8 and -12 throughout: dg 1e-3 and 5e-2 off).
 // Two blocks share an SM, hide each other's copies and passes, and stay for the whole
-// pass.  What bounds it: an item is 2.9 us of products (40 steps of 128 rows and columns, 20
-// narrow ones) and five hand-overs, 6 us an item and SM with two in flight (3072 items of 24 heads,
-// 4 x 2048: 122 us, 3.4 TB/s).  The sums in registers spilled (64 a thread of 96) and took 150 us,
-// masks a column at a time 135.
+// pass.  What bounds it: an item is 3.4 us of products (48 steps of 128 rows and columns, 20
+// narrow ones) and six hand-overs, 7.2 us an item and SM with two in flight (3072 items of 24 heads,
+// 4 x 2048: 145 us, 3.2 TB/s).  With W and dS rounded once and crossing sums as differences it took 122; against that,
+// sums in registers spilled (64 a thread of 96) and took 150, masks a column at a time 135.
 #include "delta_chunk.cuh"
 #include "delta_mma.cuh"
 

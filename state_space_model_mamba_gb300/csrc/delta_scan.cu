@@ -26,10 +26,11 @@
 // passes and products: they repeat the loads of K and Q and waste part of the
 // instruction, so they are taken only where every slice still has an SM of its own.
 //
-// Measured a chunk: 1.53 us in slices of 16 columns (1 x 131072 x 32 heads, 3.14 ms), 3.0 us
+// Measured a chunk: 1.56 us in slices of 16 columns (1 x 131072 x 32 heads, 3.19 ms), 3.1 us
 // for the backward's recompute, which also keeps S and Z (4 x 2048 x 24: 99 us); two blocks
-// per SM, 8 ragged rows of up to 4096 tokens and 64 heads: 341 us.  Tried and slower: threads
-// that wait for a block's barrier instead of arriving at one the products' warp waits for.
+// per SM, 8 ragged rows of up to 4096 tokens and 64 heads: 365 us (W in two parts: 341).  The third part in product
+// steps of its own, on top of the second's accumulators, took 8 % of a narrow slice's chunk and 33 us of
+// the ragged batch; columns of its own, 2 % and 23.  Tried and slower: threads that wait for a block's barrier instead of arriving at one the products' warp waits for.
 #include <cuda.h>
 
 #include "delta_chunk.cuh"
@@ -106,7 +107,7 @@ struct ScanMaps {
 };
 
 // The batch row whose length has this rank, longest first: blocks that wait for a place should be the short ones
-// (8 rows of 1024 .. 4096 tokens, 64 heads, two blocks per SM: 341 us for 365 in the order given).
+// (8 rows of 1024 .. 4096 tokens, 64 heads, two blocks per SM: 341 us for 365 in the order given, W in two parts).
 __device__ __forceinline__ int longest_first(const DeltaParams &p, int rank, int lane) {
     if (!p.valid_len || p.b > 64) return rank;
     const int v0 = lane < p.b ? valid_tokens(p, lane) : -1, v1 = lane + 32 < p.b ? valid_tokens(p, lane + 32) : -1;
@@ -515,8 +516,8 @@ __global__ void __launch_bounds__(scan_threads(W), NB == 1 ? 2 : 1)
 // while the chain waits for its threads.  Two blocks per SM (single tiles, 56 registers a
 // thread) took as long for two chains as this takes for two in turn.  The forward's S and Z
 // read where they are used cost 2 us of a step's 5: Z comes by copy, S into registers, a step ahead.
-// Measured: 4.1 us a chunk (4 x 2048 x 24 heads: 136 us; 160 chains of 128 chunks on 152 SMs by themselves: 1049 us, two
-// waves, which is why the backward runs halves of the batch on two streams).
+// Measured: 4.4 us a chunk (4 x 2048 x 24 heads: 145 us, 136 with D and dV in two parts and dS kept in one; 80 chains of 128
+// chunks: 564 us; 160 chains on 152 SMs by themselves are two waves, which is why the backward runs halves of the batch on two streams).
 constexpr uint32_t kOffX2 = 0, kOffW2 = 8192;                    // in the state's place, as in the forward
 constexpr uint32_t kRevTri = 32768, kRevDO = kRevTri + 2 * 32768, kRevD = kRevDO + 2 * 8192, kRevKQ = kRevD + 24576,
                    kRevZ = kRevKQ + 2 * kKQBytes, kRevBytes = kRevZ + kErrTile;

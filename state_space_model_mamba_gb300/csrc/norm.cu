@@ -13,9 +13,10 @@
 // bf16 one, which writes more, took 57.
 //
 // Measured at 16384 x 2560 in bf16, of a measured copy's 6.69 TB/s:
-//   bf16 output 52.6 us (6.4 TB/s), e4m3 with a scale per 128 columns 47.8 us (6.2 TB/s),
-//   backward 59 us (5.7 TB/s), of which the second kernel is 4;
-// 24 x 2560: 2 us, below a launch.
+//   bf16 output 51.9 us (6.5 TB/s), e4m3 with a scale per 128 columns 47.3 us (6.2 TB/s),
+//   backward 54.5 us, and 3.9 for dweight's second kernel (5.7 TB/s over both, 0.86 of the copy);
+// 24 x 2560: 1.9 us, below a launch.  At 16384 columns, where a row's registers leave no room for the next one, and at
+// widths that are no multiple of 16 bytes the rates are lower (backward 3.5 TB/s in bf16, odd widths 1.5 to 5).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdio.h>
