@@ -1,6 +1,7 @@
-/* norm.h -- C ABI of the block's entry norm, in the same library (libssd.so):
- * the residual addition and root-mean-square norm in one pass, its output in
- * the stream's type or in 8 bits with scales, and the backward.
+/* norm.h -- C ABI of a block's norms, in the same library (libssd.so): at its
+ * entry the residual addition and root-mean-square norm in one pass, its output in
+ * the stream's type or in 8 bits with scales, and the backward; at its exit (end of
+ * this file) the group norm of a mixer's output with its gate.
  *
  * Per row of D columns:
  *     stream = x + residual            (rounded to T; x itself without a residual)
@@ -46,6 +47,31 @@ size_t norm_backward_workspace_bytes(int64_t rows, int64_t D);
 ssd_status norm_add_rms_backward(ssd_dtype dtype, const void *dy, const void *h, const float *weight, float eps,
                                  const void *d_stream, void *dx, float *dweight, int64_t rows, int64_t D,
                                  void *workspace, size_t workspace_bytes, void *stream_);
+
+/* The mixers' exit norm: group norm per token, channels last, with an activation or a gate.  A row's
+ * D columns are `groups` groups of D / groups neighbouring ones (a group for each head, say); per row and group
+ *     u = x,  or x act(gate) with NORM_GATE_FIRST
+ *     n = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps)  with NORM_CENTER,
+ *         u / sqrt(mean(u^2) + eps)                          without
+ *     y = n weight + bias,  then times act(gate) with a gate that is not first, or act(y) without a gate.
+ * x, gate, y [rows, D] (T); weight and bias [D] fp32, bias may be NULL (zeros), gate may be NULL.
+ * Statistics are fp32, y is rounded once.  y may alias x or gate. */
+#define NORM_ACT_NONE 0    /* act(z) = z */
+#define NORM_ACT_SILU 1    /* z / (1 + exp(-z)) */
+#define NORM_ACT_SIGMOID 2 /* 1 / (1 + exp(-z)) */
+#define NORM_CENTER 1u
+#define NORM_GATE_FIRST 2u
+ssd_status norm_group_gated(ssd_dtype dtype, const void *x, const void *gate, const float *weight, const float *bias, float eps,
+                            int activation, uint32_t flags, void *y, int64_t rows, int64_t D, int64_t groups, void *stream_);
+
+/* Gradients for dy [rows, D] (T) from the forward's inputs (nothing is saved between the two): dx and, with a
+ * gate, dgate [rows, D] (T); dweight and dbias [D] fp32, summed over the rows in a fixed order, each may be
+ * NULL (with both NULL no workspace is needed).  dx and dgate may alias dy, x or gate (not each other). */
+size_t norm_group_workspace_bytes(ssd_dtype dtype, int64_t rows, int64_t D, int64_t groups);
+ssd_status norm_group_gated_backward(ssd_dtype dtype, const void *dy, const void *x, const void *gate, const float *weight,
+                                     const float *bias, float eps, int activation, uint32_t flags, void *dx, void *dgate,
+                                     float *dweight, float *dbias, int64_t rows, int64_t D, int64_t groups, void *workspace,
+                                     size_t workspace_bytes, void *stream_);
 
 #ifdef __cplusplus
 }

@@ -171,6 +171,21 @@ ssd_status ssd_backward(const ssd_dims *dims, ssd_dtype dtype,
                         float *d_init_state,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* One token of decoding for each of `batch` requests (no counterpart on the pages, whose scan
+ * is whole sequences): the recurrence above, states updated in place.
+ *     x, y [batch, nheads, headdim]; B, C [batch, ngroups, dstate]      (T)
+ *     dt [batch, nheads]; A, D [nheads]                                 (fp32)
+ *     state [slots, nheads, headdim, dstate]                            (fp32)
+ *     state_index [batch] (int32) or NULL: the slot of each request (NULL: slot i,
+ *         then slots >= batch)
+ * A request whose slot is outside [0, slots) is absent (padding of a captured batch): y = 0, no
+ * state is touched.  Two requests must not name one slot.  dims->seqlen must be 1;
+ * chunk_len (any that ssd_supported takes) and flags have no effect.
+ *   Errors: SSD_ERR_INVALID_ARG / _UNSUPPORTED before any work; SSD_ERR_CUDA if the launch fails. */
+ssd_status ssd_step(const ssd_dims *dims, ssd_dtype dtype, const void *x, const float *dt, const float *A,
+                    const void *B, const void *C, const float *D, float *state, int64_t slots,
+                    const int32_t *state_index, void *y, void *stream);
+
 /* Reads (synchronously, on `stream`) the status words that the last call on
  * this workspace left and returns, in this order of precedence:
  * SSD_ERR_TIMEOUT, SSD_ERR_NONFINITE (with the count in ssd_last_error()),

@@ -8,7 +8,9 @@ a missing library raises immediately (there is no fallback path).
 
 Beside the scan, with the same conventions: :mod:`mamba3` (``include/mamba3.h``),
 :mod:`delta`, the gated delta rule over sequences, its backward and its one-token
-step (``include/delta.h``), and :mod:`norm`, the entry norm with the residual's
-addition, its e4m3 output and its backward (``include/norm.h``).
+step (``include/delta.h``), :mod:`window`, attention with a sliding window and sinks, its
+backward, and its ring for decoding (``include/window.h``), and :mod:`norm`, the entry norm
+with the residual's addition, its e4m3 output and its backward, and the exit norm of a
+mixer's output with its gate (``include/norm.h``).
 """
-__all__ = ["ssd", "mamba3", "delta", "norm", "inputs"]
+__all__ = ["ssd", "mamba3", "delta", "window", "norm", "inputs"]

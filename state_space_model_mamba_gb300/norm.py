@@ -1,6 +1,7 @@
-"""Thin Python binding of the entry norm of ``libssd.so`` (``include/norm.h``):
-residual addition and root-mean-square norm in one pass, with the output in
-the stream's type or in e4m3 with scales, and the backward.
+"""Thin Python binding of the norms of ``libssd.so`` (``include/norm.h``): at a block's
+entry residual addition and root-mean-square norm in one pass, with the output in
+the stream's type or in e4m3 with scales, and the backward; at its exit the group norm
+of a mixer's output with an activation or a gate, and the backward.
 
 Argument marshalling only, as :mod:`ssd`.  ``x`` may have any number of leading
 axes; its last axis is the row.
@@ -14,7 +15,10 @@ import torch
 
 from . import ssd
 
-EXPORTED = ("norm_add_rms", "norm_add_rms_fp8", "norm_backward_workspace_bytes", "norm_add_rms_backward")
+EXPORTED = ("norm_add_rms", "norm_add_rms_fp8", "norm_backward_workspace_bytes", "norm_add_rms_backward",
+            "norm_group_gated", "norm_group_workspace_bytes", "norm_group_gated_backward")
+ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+NORM_CENTER, NORM_GATE_FIRST = 1, 2
 
 _lock = threading.Lock()
 _bound = None
@@ -36,6 +40,13 @@ def _lib():
             lib.norm_backward_workspace_bytes.restype = sz
             lib.norm_add_rms_backward.argtypes = [i32, vp, vp, vp, f32, vp, vp, vp, i64, i64, vp, sz, vp]
             lib.norm_add_rms_backward.restype = i32
+            u32 = ctypes.c_uint32
+            lib.norm_group_gated.argtypes = [i32, vp, vp, vp, vp, f32, i32, u32, vp, i64, i64, i64, vp]
+            lib.norm_group_gated.restype = i32
+            lib.norm_group_workspace_bytes.argtypes = [i32, i64, i64, i64]
+            lib.norm_group_workspace_bytes.restype = sz
+            lib.norm_group_gated_backward.argtypes = [i32] + [vp] * 5 + [f32, i32, u32] + [vp] * 4 + [i64, i64, i64, vp, sz, vp]
+            lib.norm_group_gated_backward.restype = i32
             _bound = lib
     return _bound
 
@@ -104,3 +115,50 @@ def add_rms_norm_backward(dy, stream, weight, eps=1e-5, d_stream=None):
         ssd._check(lib.norm_add_rms_backward(code, _ptr(dy), _ptr(stream), _ptr(weight), eps, _ptr(d_stream), _ptr(dx),
                                              _ptr(dw), rows, D, _ptr(ws), ws.numel(), _raw_stream(index)))
     return dx, dw
+
+
+def _check_group(x, weight, bias, gate, groups, center, activation, gate_first, dy=None):
+    code, rows, D, index = _check(x, weight, ("gate", "dy"), gate, dy)
+    if bias is not None and (bias.shape != (D,) or bias.dtype is not _F32 or bias.device != x.device or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous ({D},) float32 tensor on {x.device}")
+    if groups < 1 or D % groups:
+        raise ValueError(f"columns ({D}) must be a multiple of groups ({groups})")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}")
+    if gate_first and gate is None:
+        raise ValueError("gate_first without a gate")
+    flags = (NORM_CENTER if center else 0) | (NORM_GATE_FIRST if gate_first else 0)
+    return code, rows, D, index, ACTIVATIONS[activation], flags
+
+
+def group_norm_gated(x, weight, bias=None, gate=None, groups=1, eps=1e-5, center=True, activation="silu", gate_first=False):
+    """Group norm over the last axis, per token, with an activation or a gate.  Returns y in x's type.
+
+    x [.., D] in fp32 or bf16, weight and bias fp32 [D] (bias may be None), gate like x or None; the D columns
+    are ``groups`` groups.  ``gate_first`` norms x * act(gate); else the normed value times weight plus bias is
+    multiplied by act(gate), or without a gate put through the activation itself ("silu", "sigmoid"
+    or None for act(z) = z).  ``center`` takes the group's mean off (without it: root-mean-square norm).
+    """
+    code, rows, D, index, act, flags = _check_group(x, weight, bias, gate, groups, center, activation, gate_first)
+    y = torch.empty_like(x)
+    with ssd.on_device(index):
+        ssd._check(_lib().norm_group_gated(code, x.data_ptr(), _ptr(gate), weight.data_ptr(), _ptr(bias), eps, act, flags,
+                                           y.data_ptr(), rows, D, groups, _raw_stream(index)))
+    return y
+
+
+def group_norm_gated_backward(dy, x, weight, bias=None, gate=None, groups=1, eps=1e-5, center=True, activation="silu",
+                              gate_first=False):
+    """Gradients of :func:`group_norm_gated` for dy, from its inputs: a dict with dx, dgate (None without a gate),
+    dweight and dbias (None without a bias)."""
+    code, rows, D, index, act, flags = _check_group(x, weight, bias, gate, groups, center, activation, gate_first, dy)
+    out = dict(dx=torch.empty_like(x), dgate=None if gate is None else torch.empty_like(x), dweight=torch.empty_like(weight),
+               dbias=None if bias is None else torch.empty_like(weight))
+    lib = _lib()
+    ws = torch.empty(lib.norm_group_workspace_bytes(code, rows, D, groups), dtype=torch.uint8, device=x.device)
+    with ssd.on_device(index):
+        ssd._check(lib.norm_group_gated_backward(
+            code, dy.data_ptr(), x.data_ptr(), _ptr(gate), weight.data_ptr(), _ptr(bias), eps, act, flags, _ptr(out["dx"]),
+            _ptr(out["dgate"]), _ptr(out["dweight"]), _ptr(out["dbias"]), rows, D, groups, ws.data_ptr(), ws.numel(),
+            _raw_stream(index)))
+    return out

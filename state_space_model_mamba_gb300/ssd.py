@@ -32,7 +32,8 @@ EXPORTED = ("ssd_supported", "ssd_workspace_bytes", "ssd_forward", "ssd_backward
             "ssd_workspace_status", "ssd_status_str", "ssd_last_error", "ssd_version",
             "ssd_last_launch_count", "ssd_profile_begin", "ssd_profile_end", "ssd_profile_name",
             "ssd_profile_only", "ssd_forward_noalloc", "ssd_noalloc_status",
-            "ssd_moments_workspace_bytes", "ssd_state_moments", "ssd_state_pr", "ssd_wait_selftest")
+            "ssd_moments_workspace_bytes", "ssd_state_moments", "ssd_state_pr", "ssd_wait_selftest",
+            "ssd_step")
 SSD_PAIR_REAL, SSD_PAIR_COMPLEX_INTERLEAVED, SSD_PAIR_COMPLEX_HALF_HALF, SSD_PAIR_QUATERNION = 0, 1, 2, 3
 
 
@@ -101,6 +102,8 @@ def load_library(path: str | None = None):
         lib.ssd_state_moments.argtypes = [dims_p, i32] + [vp] * 9 + [vp, sz, vp]
         lib.ssd_state_moments.restype = i32
         i64 = ctypes.c_int64
+        lib.ssd_step.argtypes = [dims_p, i32] + [vp] * 7 + [i64] + [vp] * 3
+        lib.ssd_step.restype = i32
         lib.ssd_state_pr.argtypes = [vp] * 3 + [i64] * 3 + [i32, i32, i64, i32, vp, vp, vp]
         lib.ssd_state_pr.restype = i32
         if path is None:
@@ -273,6 +276,41 @@ def ssd_backward(x, dt, A, B, C, D, chunk_len, dy, d_final_state=None, init_stat
     if check_finite or check_status:
         workspace_status(ws)
     return out
+
+
+def ssd_step(x, dt, A, B, C, D, state, state_index=None):
+    """One decoded token per request; ``state`` is updated in place.  Returns y.
+
+    x [b,H,P] and B, C [b,G,N] (fp32 or bf16), dt [b,H], A and D [H] fp32, state
+    [slots,H,P,N] fp32, state_index int32 [b] (each request's slot; a slot outside
+    the pool marks an absent request, whose y is 0) or None (slot i).  No two
+    requests may name the same slot.
+    """
+    code, dev = _dtype_code(x), x.device
+    if x.dim() != 3 or B.dim() != 3 or state.dim() != 4:
+        raise ValueError("x must be [b, H, P], B and C [b, G, N], state [slots, H, P, N]")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    b, H, P = x.shape
+    G, N = B.shape[1:]
+    exp = [("dt", dt, (b, H), torch.float32), ("A", A, (H,), torch.float32), ("B", B, (b, G, N), x.dtype),
+           ("C", C, (b, G, N), x.dtype), ("D", D, (H,), torch.float32),
+           ("state", state, (state.shape[0], H, P, N), torch.float32)]
+    if state_index is not None:
+        exp.append(("state_index", state_index, (b,), torch.int32))
+    for name, t, shape, dtype in exp:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{name}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    dims = SsdDims(b, 1, H, P, N, G, 64, 0, 0)
+    y = torch.empty_like(x)
+    with on_device(dev.index):
+        _check(load_library().ssd_step(
+            ctypes.byref(dims), code, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), D.data_ptr(),
+            state.data_ptr(), state.shape[0], None if state_index is None else state_index.data_ptr(), y.data_ptr(),
+            torch._C._cuda_getCurrentRawStream(dev.index)))
+    return y
 
 
 def state_moments(x, dt, A, B, init_state=None, valid_len=None, check_status=False, split_scan=False):
