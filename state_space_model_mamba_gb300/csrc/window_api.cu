@@ -4,7 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "window_internal.cuh"
+#include "window_tile.cuh"
 
 namespace ssd {
 namespace window {
@@ -163,7 +163,10 @@ ssd_status window_forward(const window_dims *dims, ssd_dtype dtype, const void *
     WindowParams p = base_params(*dims, q, k, v, scale, valid_len, workspace);
     p.o = o;
     p.lse = lse;
-    return guarded([&] { return launch_simt_forward(p, dtype == SSD_BF16, (cudaStream_t)stream); });
+    return guarded([&] {
+        if (tile_supported(*dims, dtype)) return launch_tile_forward(p, (cudaStream_t)stream);
+        return launch_simt_forward(p, dtype == SSD_BF16, (cudaStream_t)stream);
+    });
 }
 
 ssd_status window_backward(const window_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,

@@ -63,6 +63,9 @@ __device__ __forceinline__ void store4<bf16>(bf16 *p, float4 v) {
 cudaError_t launch_simt_forward(const WindowParams &p, bool is_bf16, cudaStream_t s);
 cudaError_t launch_simt_backward(const WindowParams &p, bool is_bf16, cudaStream_t s);
 
+// ---- tensor-core kernels (window_fwd.cu)
+cudaError_t launch_tile_forward(const WindowParams &p, cudaStream_t s);
+
 // ---- the ring (window_step.cu)
 struct RingParams {
     int b, L, H, P, G, hpg, W, sinks;
