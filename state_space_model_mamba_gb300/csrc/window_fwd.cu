@@ -53,7 +53,7 @@ struct Item {
         const int T = tile_tokens(p), t0 = index % per_row * 2 * T;
         g = index / per_row % p.G;
         bi = index / per_row / p.G;
-        V = valid_tokens(p, bi);
+        V = __shfl_sync(0xffffffffu, valid_tokens(p, bi), 0);
         end = min(t0 + 2 * T, V);
         lo = max(0, t0 - p.W + 1);
         head = min(p.sinks, lo);
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     extern __shared__ __align__(1024) char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     Bars &sm = *(Bars *)(smem_raw + Lay::kOffBars);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tm = sm.tmem;  // S (and P) of tile i at column 128 i, O at 256 + 128 i
+    const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);  // S (and P) of tile i at column 128 i, O at 256 + 128 i
     bool ok = sm.err == 0;
 
     if (warp >= kSoftmax / 32) {
@@ -162,6 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             // ---- products
             const uint32_t i_pv = tc::idesc_bf16(128, (p.P + 15) / 16 * 16, false, true);
             const int ksteps = (p.P + 15) / 16;
+            // operands are the same for the whole warp and their descriptors differ by constants: an instruction then takes its
+            // 64 cycles (measured; with addresses that the compiler takes for a lane's own it takes 104)
+            const uint64_t d_q = tc::sdesc_kmajor(base, 0, 16384), d_k = tc::sdesc_kmajor(base + Lay::kOffRing, 0, 16384),
+                           d_v = tc::sdesc_mnmajor(base + Lay::kOffRing, 0, 16384);
             int n = 0, nq[2] = {0, 0}, np[2] = {0, 0};
             for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
                 const Item it(p, index, per_row);
@@ -182,10 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                             tc::tc_fence_after();
                             if (ok && lane == 0) {
                                 const int steps = (it.count(j - 1) + 15) / 16;
-                                const uint32_t v = base + Lay::kOffRing + vslot * Lay::kTile;
-                                for (int ks = 0; ks < steps; ++ks)
-                                    tc::mma_bf16_tmem_a(tm + 256 + 128 * i, tm + 128 * i + 8 * ks, tc::sdesc_mnmajor(v, ks, 16384), i_pv,
-                                                        begun[i] || ks > 0);
+                                const uint64_t v = delta::sdesc_add(d_v, vslot * Lay::kTile);
+#pragma unroll
+                                for (int ks = 0; ks < 8; ++ks)
+                                    if (ks < steps)
+                                        tc::mma_bf16_tmem_a(tm + 256 + 128 * i, tm + 128 * i + 8 * ks, delta::sdesc_add(v, ks * 2048), i_pv,
+                                                            begun[i] || ks > 0);
                                 if (j - 1 == it.last[i]) tc::mma_commit(&sm.o_full[i]);
                             }
                             __syncwarp();
@@ -197,9 +203,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                             loaded[i] = true;
                             tc::tc_fence_after();
                             if (ok && lane == 0) {
-                                const uint32_t q = base + i * Lay::kTile, k = base + Lay::kOffRing + kslot * Lay::kTile;
-                                for (int ks = 0; ks < ksteps; ++ks)
-                                    tc::mma_bf16(tm + 128 * i, tc::sdesc_kmajor(q, ks, 16384), tc::sdesc_kmajor(k, ks, 16384), i_s, ks > 0);
+                                const uint64_t q = delta::sdesc_add(d_q, i * Lay::kTile), k = delta::sdesc_add(d_k, kslot * Lay::kTile);
+#pragma unroll
+                                for (int ks = 0; ks < 4 * KB; ++ks)
+                                    if (ks < ksteps)
+                                        tc::mma_bf16(tm + 128 * i, delta::sdesc_add(q, (ks >> 2) * 16384 + (ks & 3) * 32),
+                                                     delta::sdesc_add(k, (ks >> 2) * 16384 + (ks & 3) * 32), i_s, ks > 0);
                                 tc::mma_commit(&sm.s_full[i]);
                                 if (j == it.last[i]) tc::mma_commit(&sm.q_empty[i]);
                             }
