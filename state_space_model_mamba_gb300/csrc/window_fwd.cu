@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 auto load_q = [&](int i) {
                     if (!it.on[i] || !ok) return;
                     ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[i], (nq[i] & 1) ^ 1));
-                    if (ok && lane == 0) {
+                    if (ok && elect()) {
                         mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
                         for (int kb = 0; kb < KB; ++kb)
                             tma_tile(base + i * Lay::kTile + kb * 16384, &maps.q, &sm.q_full[i], 64 * kb, it.g * p.hpg, it.ta[i], it.bi);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     if (!ok) return;
                     const int slot = n % Lay::kSlots;
                     ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[slot], ((n / Lay::kSlots) & 1) ^ 1));
-                    if (ok && lane == 0) {
+                    if (ok && elect()) {
                         mbar_arrive_expect_tx(&sm.kv_full[slot], Lay::kTile);
                         for (int kb = 0; kb < KB; ++kb)
                             tma_tile(base + Lay::kOffRing + slot * Lay::kTile + kb * 16384, map, &sm.kv_full[slot], 64 * kb, it.g,
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                                                              mbar_wait(&sm.kv_full[vslot], ((n - 1) / Lay::kSlots) & 1));
                             ++np[i];
                             tc::tc_fence_after();
-                            if (ok && lane == 0) {
+                            if (ok && elect()) {
                                 const int steps = (it.count(j - 1) + 15) / 16;
                                 const uint64_t v = delta::sdesc_add(d_v, vslot * Lay::kTile);
 #pragma unroll
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                             if (!loaded[i]) ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[i], nq[i] & 1));
                             loaded[i] = true;
                             tc::tc_fence_after();
-                            if (ok && lane == 0) {
+                            if (ok && elect()) {
                                 const uint64_t q = delta::sdesc_add(d_q, i * Lay::kTile), k = delta::sdesc_add(d_k, kslot * Lay::kTile);
 #pragma unroll
                                 for (int ks = 0; ks < 4 * KB; ++ks)
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                             pending[i] = true;
                         }
                     }
-                    if (ok && lane == 0) {
+                    if (ok && elect()) {
                         if (j > 0) tc::mma_commit(&sm.kv_empty[vslot]);
                         if (more) tc::mma_commit(&sm.kv_empty[kslot]);
                     }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 for (int i = 0; i < 2; ++i) nq[i] += it.on[i];
             }
             if (!ok) sm.err = 1;
-            if (lane == 0) tc::mma_commit(&sm.drain);
+            if (elect()) tc::mma_commit(&sm.drain);
             __syncwarp();
             mbar_wait(&sm.drain, 0);
         }
