@@ -1,10 +1,13 @@
 // window_fwd.cu -- window attention, forward, on tcgen05.
 //
 // Blocks stay on their SM and take items in turn: two query tiles (window_tile.cuh) of one key group
-// and the key tiles that they see.  Per tile pair S = Q K^T (128 x 128, fp32, tensor memory), the
-// softmax's step, and O += P V.  One warp copies (TMA), one issues products, and two groups of four warps, a
-// thread per row, take the softmax of one query tile each: while a group works on its S, the tensor core works on
-// the other's.  P goes to tensor memory over the S that it came from, as the A operand; O stays there.
+// and the key tiles that they see.  Per pair of tiles S = Q K^T (fp32, tensor memory), the softmax's
+// step, and O += P V.  One warp copies (TMA), one issues products, and two groups of four warps, a
+// thread per row, take the softmax of one query tile each.  S and P have columns of their own, so a
+// group's next S is made as soon as it has its last one in registers, and the tensor core does not wait for the
+// softmax's chain of instructions: 512 columns hold two S, two P and two O with 80 keys a tile where O
+// has 128 columns, and 128 keys where it has 64.  (With P in place of S, 128 keys a tile, the products of a
+// query tile waited for its softmax: 3570 cycles for 2 x 128 x 128 scores at P = 128, of which 2048 are products.)
 // The row maximum is followed lazily: a row's reference only moves, and O is only rescaled, where the maximum
 // has grown by 2^8 over it, so P <= 256 and the passes over O are rare; sums are fp32 and do not care.
 // P is rounded to bf16 (2^-8 of each at most), the sum it is divided by is not.
@@ -20,8 +23,9 @@ using tc::ffma2;
 using tc::fmul2;
 using tc::tmem_addr;
 
-// Threads: two groups of softmax, then a group whose first two warps copy and issue.  That group gives up registers
-// for a softmax thread's 128 scores: 2 * 128 * 216 + 128 * 72 = 384 * 168, what the block is launched with.
+// Threads: two groups of softmax, then a group whose first warp copies, whose second issues S and whose others issue O.  An
+// instruction costs its issuing thread some 55 cycles and a wait 100, so one thread could not keep the tensor core in work.
+// That group gives up registers for a softmax thread's scores: 2 * 128 * 216 + 128 * 72 = 384 * 168, what the block is launched with.
 constexpr int kSoftmax = 256, kThreads = 384, kRegsSoftmax = 216, kRegsIssue = 72;
 static_assert(kSoftmax * kRegsSoftmax + (kThreads - kSoftmax) * kRegsIssue <= kThreads * 168, "registers of the launch");
 constexpr float kLazy = 8.f;  // log2 of what P may grow to
@@ -33,47 +37,58 @@ struct Maps {
 // KB = ceil(P / 64) blocks of 64 columns a tile.
 template <int KB>
 struct Layout {
-    static constexpr int kTile = KB * 16384, kSlots = KB == 2 ? 5 : 8;
-    static constexpr int kOffRing = 2 * kTile, kOffBars = kOffRing + kSlots * kTile;
-    static constexpr int kBytes = kOffBars + 1024;
+    static constexpr int kKeys = KB == 2 ? 80 : 128;                            // of a tile
+    static constexpr int kBlock = kKeys * 128, kTile = KB * kBlock, kSlots = 6;  // ring of K and V tiles
+    static constexpr int kQTile = KB * 16384;
+    static constexpr int kOffRing = 2 * kQTile, kOffStage = kOffRing + kSlots * kTile;  // stage: 8 warps x 32 rows x 64 columns
+    static constexpr int kOffBars = kOffStage + 8 * 4096, kBytes = kOffBars + 1024;
+    // columns of tensor memory: S, P, O of tile i
+    static constexpr int kS = 0, kP = 2 * kKeys, kO = 512 - 2 * 64 * KB, kOCols = 64 * KB;
+    static_assert(kP + kKeys <= kO, "tensor memory");
+    static_assert(kBytes <= 232448 && kSlots % 2 == 0, "shared memory; K in the even slots");
 };
 struct Bars {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain, kv_full[8], kv_empty[8];
+    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], p_free[2], o_empty[2], drain, kv_full[8], kv_empty[8];
     uint32_t tmem;
     int err;
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
-// Two query tiles and their keys.
+// Two query tiles and their keys: tiles [0, tiles_a) are sinks in front of the window, [tiles_a, tiles) the window.
+template <int KEYS>
 struct Item {
     int bi, g, V, head, lo, end, tiles_a, tiles;
-    int ta[2], tb[2], first[2], last[2];
-    bool on[2];
+    int ta[2], from[2], last[2];  // first token; first and last window tile that is seen (none: last < from)
     __device__ __forceinline__ Item(const WindowParams &p, int index, int per_row) {
         const int T = tile_tokens(p), t0 = index % per_row * 2 * T;
         g = index / per_row % p.G;
         bi = index / per_row / p.G;
-        V = __shfl_sync(0xffffffffu, valid_tokens(p, bi), 0);
+        V = valid_tokens(p, bi);
         end = min(t0 + 2 * T, V);
         lo = max(0, t0 - p.W + 1);
         head = min(p.sinks, lo);
-        tiles_a = (head + 127) / 128;
-        tiles = t0 < V ? tiles_a + (end - lo + 127) / 128 : 0;
+        tiles_a = (head + KEYS - 1) / KEYS;
+        tiles = t0 < V ? tiles_a + (end - lo + KEYS - 1) / KEYS : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             ta[i] = t0 + i * T;
-            tb[i] = min(ta[i] + T, V);
-            on[i] = ta[i] < V;
-            first[i] = max(0, ta[i] - p.W + 1);
-            last[i] = on[i] ? tiles_a + (tb[i] - 1 - lo) / 128 : -1;
+            // sinks inside the window's first tiles: all of them are taken, the masks do the rest
+            from[i] = tiles_a + (lo < p.sinks ? 0 : (max(0, ta[i] - p.W + 1) - lo) / KEYS);
+            last[i] = on(i) ? tiles_a + (min(ta[i] + T, V) - 1 - lo) / KEYS : -1;
         }
     }
-    __device__ __forceinline__ int start(int j) const { return j < tiles_a ? j * 128 : lo + (j - tiles_a) * 128; }
-    __device__ __forceinline__ int count(int j) const { return min(128, (j < tiles_a ? head : end) - start(j)); }
-    __device__ __forceinline__ bool need(const WindowParams &p, int i, int j) const {
-        if (j > last[i]) return false;
-        const int s = start(j);
-        return s + count(j) > first[i] || s < p.sinks;
+    __device__ __forceinline__ bool on(int i) const { return ta[i] < V; }
+    __device__ __forceinline__ int start(int j) const { return j < tiles_a ? j * KEYS : lo + (j - tiles_a) * KEYS; }
+    __device__ __forceinline__ int count(int j) const { return min(KEYS, (j < tiles_a ? head : end) - start(j)); }
+    __device__ __forceinline__ bool need(int i, int j) const { return j <= last[i] && (j < tiles_a || j >= from[i]); }
+};
+// A place in a ring of SLOTS and the parity of its phase.
+template <int SLOTS>
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == SLOTS) slot = 0, phase ^= 1;
     }
 };
 
@@ -81,6 +96,8 @@ template <int KB>
 __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_constant__ Maps maps, WindowParams p, float c,
                                                                  uint32_t negate, int items, int per_row) {
     using Lay = Layout<KB>;
+    constexpr int KEYS = Lay::kKeys, SLOTS = Lay::kSlots;
+    using It = Item<KEYS>;
     extern __shared__ __align__(1024) char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     Bars &sm = *(Bars *)(smem_raw + Lay::kOffBars);
@@ -90,15 +107,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
             mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.p_free[i], 1);
             mbar_init(&sm.o_empty[i], 4);
         }
-        for (int i = 0; i < Lay::kSlots; ++i) {
+        for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&sm.kv_full[i], 1);
-            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.kv_empty[i], i & 1 ? 2 : 1);  // K: the thread of S; V: both threads of O
         }
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain, 3);
         tc::mbar_fence_init();
         sm.err = (base & 1023u) ? 1 : 0;
     }
@@ -110,162 +128,170 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);  // S (and P) of tile i at column 128 i, O at 256 + 128 i
+    const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
     bool ok = sm.err == 0;
 
     if (warp >= kSoftmax / 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == kSoftmax / 32) {
-            // ---- copies
-            const uint32_t q_bytes = (uint32_t)(tile_tokens(p) * p.hpg) * 128u * KB;
-            int n = 0, nq[2] = {0, 0};
-            for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-                const Item it(p, index, per_row);
-                auto load_q = [&](int i) {
-                    if (!it.on[i] || !ok) return;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[i], (nq[i] & 1) ^ 1));
-                    if (ok && elect()) {
+            // ---- copies, one thread
+            if (elect()) {
+                const uint32_t q_bytes = (uint32_t)(tile_tokens(p) * p.hpg) * 128u * KB;
+                Place<SLOTS> at;
+                uint32_t nq[2] = {0, 0};
+                int loaded = 0;
+                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+                    const It it(p, index, per_row);
+                    if (it.tiles == 0) continue;
+                    auto load_q = [&](int i) {
+                        if (!it.on(i) || !ok) return;
+                        if (!(ok = wait_bar(&sm.q_empty[i], (nq[i] & 1) ^ 1))) return;
                         mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
                         for (int kb = 0; kb < KB; ++kb)
-                            tma_tile(base + i * Lay::kTile + kb * 16384, &maps.q, &sm.q_full[i], 64 * kb, it.g * p.hpg, it.ta[i], it.bi);
-                    }
-                    if (ok) ++nq[i];
-                };
-                auto load_kv = [&](const CUtensorMap *map, int j) {
-                    if (!ok) return;
-                    const int slot = n % Lay::kSlots;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[slot], ((n / Lay::kSlots) & 1) ^ 1));
-                    if (ok && elect()) {
-                        mbar_arrive_expect_tx(&sm.kv_full[slot], Lay::kTile);
+                            tma_tile(base + i * Lay::kQTile + kb * 16384, &maps.q, &sm.q_full[i], 64 * kb, it.g * p.hpg, it.ta[i], it.bi);
+                        ++nq[i];
+                    };
+                    for (int x = 0; x < 2 * it.tiles && ok; ++x) {
+                        if (x < 2) load_q(x);
+                        if (!ok || !(ok = wait_bar(&sm.kv_empty[at.slot], at.phase ^ 1))) break;
+                        mbar_arrive_expect_tx(&sm.kv_full[at.slot], Lay::kTile);
                         for (int kb = 0; kb < KB; ++kb)
-                            tma_tile(base + Lay::kOffRing + slot * Lay::kTile + kb * 16384, map, &sm.kv_full[slot], 64 * kb, it.g,
-                                     it.start(j), it.bi);
+                            tma_tile(base + Lay::kOffRing + at.slot * Lay::kTile + kb * Lay::kBlock, x & 1 ? &maps.v : &maps.k,
+                                     &sm.kv_full[at.slot], 64 * kb, it.g, it.start(x >> 1), it.bi);
+                        at.next();
+                        ++loaded;
                     }
-                    if (ok) ++n;
-                };
-                if (it.tiles == 0) continue;
-                load_q(0);
-                load_kv(&maps.k, 0);
-                load_q(1);
-                load_kv(&maps.v, 0);
-                for (int j = 1; j < it.tiles; ++j) {
-                    load_kv(&maps.k, j);
-                    load_kv(&maps.v, j);
                 }
+                if (!ok) sm.err = 1;
+                // copies in flight land before the block ends
+                for (int x = max(0, loaded - SLOTS); x < loaded; ++x) wait_bar(&sm.kv_full[x % SLOTS], (x / SLOTS) & 1);
+                for (int i = 0; i < 2; ++i)
+                    if (nq[i]) wait_bar(&sm.q_full[i], (nq[i] - 1) & 1);
             }
-            if (!ok) sm.err = 1;
-            // copies in flight land before the block ends
-            for (int x = max(0, n - Lay::kSlots); x < n; ++x) mbar_wait(&sm.kv_full[x % Lay::kSlots], (x / Lay::kSlots) & 1);
-            for (int i = 0; i < 2; ++i)
-                if (nq[i]) mbar_wait(&sm.q_full[i], (nq[i] - 1) & 1);
-        } else if (warp == kSoftmax / 32 + 1) {
-            // ---- products
-            const uint32_t i_pv = tc::idesc_bf16(128, (p.P + 15) / 16 * 16, false, true);
-            const int ksteps = (p.P + 15) / 16;
-            // operands are the same for the whole warp and their descriptors differ by constants: an instruction then takes its
-            // 64 cycles (measured; with addresses that the compiler takes for a lane's own it takes 104)
-            const uint64_t d_q = tc::sdesc_kmajor(base, 0, 16384), d_k = tc::sdesc_kmajor(base + Lay::kOffRing, 0, 16384),
-                           d_v = tc::sdesc_mnmajor(base + Lay::kOffRing, 0, 16384);
-            int n = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-                const Item it(p, index, per_row);
-                bool pending[2] = {false, false}, begun[2] = {false, false}, loaded[2] = {false, false};
-                for (int j = 0; j <= it.tiles && ok && it.tiles; ++j) {
-                    const int kslot = n % Lay::kSlots, vslot = (n + Lay::kSlots - 1) % Lay::kSlots;  // K of j, V of j - 1
-                    const bool more = j < it.tiles;
-                    if (more) ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[kslot], (n / Lay::kSlots) & 1));
-                    const int nk = more ? (it.count(j) + 15) / 16 * 16 : 0;
-                    const uint32_t i_s = tc::idesc_bf16(128, nk, false, false) | negate;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (pending[i] && ok) {
-                            if (!begun[i]) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_empty[i], (nq[i] & 1) ^ 1));
-                            ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.p_full[i], np[i] & 1) &&
-                                                             mbar_wait(&sm.kv_full[vslot], ((n - 1) / Lay::kSlots) & 1));
-                            ++np[i];
-                            tc::tc_fence_after();
-                            if (ok && elect()) {
-                                const int steps = (it.count(j - 1) + 15) / 16;
-                                const uint64_t v = delta::sdesc_add(d_v, vslot * Lay::kTile);
-#pragma unroll
-                                for (int ks = 0; ks < 8; ++ks)
-                                    if (ks < steps)
-                                        tc::mma_bf16_tmem_a(tm + 256 + 128 * i, tm + 128 * i + 8 * ks, delta::sdesc_add(v, ks * 2048), i_pv,
-                                                            begun[i] || ks > 0);
-                                if (j - 1 == it.last[i]) tc::mma_commit(&sm.o_full[i]);
-                            }
-                            __syncwarp();
-                            begun[i] = true;
-                            pending[i] = false;
-                        }
-                        if (more && ok && it.need(p, i, j)) {
-                            if (!loaded[i]) ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[i], nq[i] & 1));
-                            loaded[i] = true;
-                            tc::tc_fence_after();
-                            if (ok && elect()) {
-                                const uint64_t q = delta::sdesc_add(d_q, i * Lay::kTile), k = delta::sdesc_add(d_k, kslot * Lay::kTile);
-#pragma unroll
-                                for (int ks = 0; ks < 4 * KB; ++ks)
-                                    if (ks < ksteps)
-                                        tc::mma_bf16(tm + 128 * i, delta::sdesc_add(q, (ks >> 2) * 16384 + (ks & 3) * 32),
-                                                     delta::sdesc_add(k, (ks >> 2) * 16384 + (ks & 3) * 32), i_s, ks > 0);
-                                tc::mma_commit(&sm.s_full[i]);
-                                if (j == it.last[i]) tc::mma_commit(&sm.q_empty[i]);
-                            }
-                            __syncwarp();
-                            pending[i] = true;
-                        }
-                    }
-                    if (ok && elect()) {
-                        if (j > 0) tc::mma_commit(&sm.kv_empty[vslot]);
-                        if (more) tc::mma_commit(&sm.kv_empty[kslot]);
-                    }
-                    __syncwarp();
-                    if (more) n += 2;
-                }
-                for (int i = 0; i < 2; ++i) nq[i] += it.on[i];
-            }
-            if (!ok) sm.err = 1;
-            if (elect()) tc::mma_commit(&sm.drain);
             __syncwarp();
-            mbar_wait(&sm.drain, 0);
+        } else if (warp == kSoftmax / 32 + 1) {
+            // ---- products S = Q K^T, one thread
+            if (elect()) {
+                const uint32_t i_s0 = tc::idesc_bf16(128, 0, false, false) | negate;
+                const int ksteps = (p.P + 15) / 16;
+                const uint64_t d_q = tc::sdesc(base, 16, 1024), d_k = tc::sdesc(base + Lay::kOffRing, 16, 1024);
+                Place<SLOTS> at;
+                uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};
+                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+                    const It it(p, index, per_row);
+                    bool loaded[2] = {false, false};
+                    for (int j = 0; j < it.tiles && ok; ++j) {
+                        if (!(ok = wait_bar(&sm.kv_full[at.slot], at.phase))) break;
+                        const uint32_t i_s = i_s0 | (uint32_t)((it.count(j) + 15) >> 4) << 18;  // N / 8 from bit 17
+                        const uint64_t k = delta::sdesc_add(d_k, at.slot * Lay::kTile);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!ok || !it.need(i, j)) continue;
+                            if (!loaded[i]) ok = wait_bar(&sm.q_full[i], nq[i] & 1);
+                            loaded[i] = true;
+                            if (!ok || !(ok = wait_bar(&sm.s_free[i], (ns[i] & 1) ^ 1))) continue;
+                            ++ns[i];
+                            tc::tc_fence_after();
+                            const uint64_t q = delta::sdesc_add(d_q, i * Lay::kQTile);
+#pragma unroll
+                            for (int ks = 0; ks < 4 * KB; ++ks)
+                                if (ks < ksteps)
+                                    tc::mma_bf16(tm + Lay::kS + KEYS * i, delta::sdesc_add(q, (ks >> 2) * 16384 + (ks & 3) * 32),
+                                                 delta::sdesc_add(k, (ks >> 2) * Lay::kBlock + (ks & 3) * 32), i_s, ks > 0);
+                            tc::mma_commit(&sm.s_full[i]);
+                            if (j == it.last[i]) tc::mma_commit(&sm.q_empty[i]);
+                        }
+                        tc::mma_commit(&sm.kv_empty[at.slot]);
+                        at.next(), at.next();
+                    }
+                    for (int i = 0; i < 2; ++i) nq[i] += it.on(i) && it.tiles;
+                }
+                if (!ok) sm.err = 1;
+                tc::mma_commit(&sm.drain);
+                wait_bar(&sm.drain, 0);
+            }
+            __syncwarp();
+        } else {
+            // ---- products O += P V of query tile i, one thread
+            if (elect()) {
+                const int i = warp - (kSoftmax / 32 + 2);
+                const uint32_t i_pv = tc::idesc_bf16(128, (p.P + 15) / 16 * 16, false, true);
+                const uint64_t d_v = tc::sdesc(base + Lay::kOffRing, Lay::kBlock, 1024);
+                const uint32_t to = tm + Lay::kO + Lay::kOCols * i, tp = tm + Lay::kP + KEYS / 2 * i;
+                Place<SLOTS> at;
+                at.next();
+                uint32_t no = 0, np = 0;
+                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+                    const It it(p, index, per_row);
+                    bool begun = false;
+                    for (int j = 0; j < it.tiles && ok; ++j) {
+                        if (!(ok = wait_bar(&sm.kv_full[at.slot], at.phase))) break;
+                        if (it.need(i, j)) {
+                            if (!begun && !(ok = wait_bar(&sm.o_empty[i], (no & 1) ^ 1))) break;
+                            if (!(ok = wait_bar(&sm.p_full[i], np & 1))) break;
+                            ++np;
+                            tc::tc_fence_after();
+                            const int steps = (it.count(j) + 15) >> 4;
+                            const uint64_t v = delta::sdesc_add(d_v, at.slot * Lay::kTile);
+#pragma unroll
+                            for (int ks = 0; ks < KEYS / 16; ++ks)
+                                if (ks < steps) tc::mma_bf16_tmem_a(to, tp + 8 * ks, delta::sdesc_add(v, ks * 2048), i_pv, begun || ks > 0);
+                            tc::mma_commit(&sm.p_free[i]);
+                            tc::mma_commit(&sm.kv_empty[at.slot]);
+                            begun = true;
+                        } else {
+                            mbar_arrive(&sm.kv_empty[at.slot]);
+                        }
+                        at.next(), at.next();
+                    }
+                    no += it.on(i) && it.tiles;
+                }
+                if (!ok) sm.err = 1;
+                tc::mma_commit(&sm.drain);
+                wait_bar(&sm.drain, 0);
+            }
+            __syncwarp();
         }
     } else {
         // ---- softmax of query tile i
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int i = warp >> 2, row = tid & 127, quarter = warp & 3, R = p.hpg, T = tile_tokens(p);
-        const uint32_t ts = tmem_addr(tm, 32 * quarter, 128 * i), to = ts + 256;
-        int n = 0, ns = 0, no = 0;
+        const uint32_t magic = row_magic(R), stage = base + Lay::kOffStage + warp * 4096;
+        const uint32_t ts = tmem_addr(tm, 32 * quarter, Lay::kS + KEYS * i), tp = tmem_addr(tm, 32 * quarter, Lay::kP + KEYS / 2 * i),
+                       to = tmem_addr(tm, 32 * quarter, Lay::kO + Lay::kOCols * i);
+        int n = 0, ns = 0;
         for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-            const Item it(p, index, per_row);
-            const int t = it.ta[i] + row / R, h = it.g * R + row % R;
+            const It it(p, index, per_row);
+            const int token = row_token(row, magic), t = it.ta[i] + token, h = it.g * R + row - token * R;
             const bool in = row < T * R && t < p.L, live = in && t < it.V;
             float m = -INFINITY, l = 0.f;
-            if (it.on[i]) {
+            if (it.on(i)) {
                 const int tq = live ? t : it.ta[i];
                 bool begun = false;
                 for (int j = 0; j < it.tiles && ok; ++j, n += 2) {
-                    if (!it.need(p, i, j)) continue;
+                    if (!it.need(i, j)) continue;
                     const int s0 = it.start(j), nk = it.count(j);
                     // keys that every row sees: none behind the tile's first token, none in front of its last one's window
-                    const bool plain = nk == 128 && s0 + 127 <= it.ta[i] && (s0 > it.tb[i] - 1 - p.W || s0 + 128 <= p.sinks);
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[i], ns & 1));
-                    if (!ok) break;
+                    const bool plain = nk == KEYS && s0 + KEYS - 1 <= it.ta[i] && (s0 > it.ta[i] + T - 1 - p.W || s0 + KEYS <= p.sinks);
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[i], ns & 1)))) break;
                     tc::tc_fence_after();
-                    ++ns;
-                    const bool two = nk > 64;
-                    float2 x[64];
-                    tc::tmem_ld64(ts, (float *)x);
-                    if (two) tc::tmem_ld64(ts + 64, (float *)(x + 32));
+                    float2 x[KEYS / 2];
+                    if constexpr (KEYS == 80)
+                        tmem_ld80(ts, (float *)x);
+                    else
+                        tmem_ld128(ts, (float *)x);
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.s_free[i]);
                     if (!plain) {
                         const int hi = min(nk, tq - s0 + 1), from = tq - p.W + 1 - s0, sk = p.sinks - s0;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q >= 2 && !two) break;
+                        for (int q = 0; q < (KEYS + 31) / 32; ++q) {
                             const uint32_t see = bits_between(-32, hi - 32 * q) &
                                                  (bits_between(from - 32 * q, 32) | bits_between(-32, sk - 32 * q));
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
+                                if (16 * q + e >= KEYS / 2) break;
                                 float2 &y = x[16 * q + e];
                                 y.x = see >> (2 * e) & 1 ? y.x : -INFINITY;
                                 y.y = see >> (2 * e + 1) & 1 ? y.y : -INFINITY;
@@ -274,16 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x[e].x, x[e].y));
-                    if (two)
-#pragma unroll
-                        for (int e = 32; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x[e].x, x[e].y));
+                    for (int e = 0; e < KEYS / 2; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x[e].x, x[e].y));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // the product with the last P is done: P and O are this group's
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[i], (ns & 1) ^ 1)))) break;
+                    tc::tc_fence_after();
+                    ++ns;
                     const bool grows = top > m && (m == -INFINITY || (top - m) * c > kLazy);
                     if (!begun) {
                         m = top;
                         begun = true;
-                    } else if (__any_sync(0xffffffffu, grows)) {  // products up to the last tile's are done: S came behind them
+                    } else if (__any_sync(0xffffffffu, grows)) {
                         const float f = grows ? (m == -INFINITY ? 0.f : exp2_approx((m - top) * c)) : 1.f;
                         if (grows) m = top;
                         l *= f;
@@ -300,29 +327,34 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     const float ref = m == -INFINITY ? 0.f : -m * c;
                     const float2 cc = make_float2(c, c), rr = make_float2(ref, ref), one = make_float2(1.f, 1.f);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (q >= 2 && !two) break;
+                    for (int q = 0; q < (KEYS + 31) / 32; ++q) {
+                        constexpr int kLast = KEYS % 32 ? KEYS % 32 / 2 : 16;  // pairs of the last chunk
+                        if (32 * q >= nk) break;
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
+                            if (q == KEYS / 32 && e >= kLast) break;
                             float2 y = ffma2(x[16 * q + e], cc, rr);
                             y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                             sum[e & 1] = ffma2(y, one, sum[e & 1]);
                             pk[e] = tc::pack_bf2(y.x, y.y);
                         }
-                        __syncwarp();
-                        delta::tmem_st16(ts + 16 * q, (const float *)pk);
+                        if (q == KEYS / 32)
+                            tmem_st8(tp + 16 * q, pk);
+                        else
+                            delta::tmem_st16(tp + 16 * q, (const float *)pk);
                     }
                     delta::tmem_wait_st();
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    if ((nk & 15) && (i == 0 || !it.need(p, 0, j))) {
+                    if ((nk & 15) && (i == 0 || !it.need(0, j))) {
                         // rows of V up to the product's step of 16: their probabilities are 0, so they have to be finite
-                        const int slot = (n + 1) % Lay::kSlots, rows = 16 - (nk & 15);
-                        ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[slot], ((n + 1) / Lay::kSlots) & 1));
+                        const int slot = (n + 1) % SLOTS, rows = 16 - (nk & 15);
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[slot], ((n + 1) / SLOTS) & 1)))) break;
                         const uint32_t v = base + Lay::kOffRing + slot * Lay::kTile;
                         for (int e = row; e < rows * 8 * KB; e += 128)
-                            tc::st_shared_v4(v + (e / (8 * rows)) * 16384 + (nk + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
+                            tc::st_shared_v4(v + (e / (8 * rows)) * Lay::kBlock + (nk + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
                         tc::fence_async_smem();
                     }
                     tc::tc_fence_before();
@@ -330,37 +362,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     if (lane == 0) mbar_arrive(&sm.p_full[i]);
                 }
                 if (!ok) break;
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[i], no & 1));
-                if (!ok) break;
+                // the last product: p_free's phase that the next item's first tile waits for too
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[i], (ns & 1) ^ 1)))) break;
                 tc::tc_fence_after();
-                ++no;
             } else {
                 n += 2 * it.tiles;
             }
+            if (in && p.lse) p.lse[((long long)it.bi * p.H + h) * p.L + t] = live ? (m * c + log2f(l)) * kLn2 : 0.f;
             const float inv = live ? 1.f / l : 0.f;
-            bf16 *o = (bf16 *)p.o + (((long long)it.bi * p.L + t) * p.H + h) * p.P;
-            for (int q = 0; q < (p.P + 31) / 32; ++q) {
-                float v[32];
-                if (it.on[i]) {
+            // O in bf16, 64 columns at a time through the warp's stage, so that a row leaves as whole lines
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[16];
+                    if (it.on(i))
+                        tc::tmem_ld16(to + 64 * kb + 16 * q, v);
+                    else
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = live ? tc::pack_bf2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+                    tc::st_shared_v4(stage + tc::sw128_chunk(lane, 2 * q), y[0], y[1], y[2], y[3]);
+                    tc::st_shared_v4(stage + tc::sw128_chunk(lane, 2 * q + 1), y[4], y[5], y[6], y[7]);
                     __syncwarp();
-                    tc::tmem_ld32u(to + 32 * q, (uint32_t *)v);
+                }
+                if (kb == KB - 1 && it.on(i)) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_empty[i]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = 32 * q + 8 * e;
-                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                    if (live)
-                        y = make_uint4(tc::pack_bf2(v[8 * e] * inv, v[8 * e + 1] * inv), tc::pack_bf2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                       tc::pack_bf2(v[8 * e + 4] * inv, v[8 * e + 5] * inv), tc::pack_bf2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
-                    if (in && col < p.P) *(uint4 *)(o + col) = y;
+                for (int e = 0; e < 8; ++e) {
+                    const int r = 4 * e + (lane >> 3), rr = 32 * quarter + r, tok = row_token(rr, magic), col = 64 * kb + 8 * (lane & 7);
+                    const uint4 y = tc::ld_shared_v4(stage + tc::sw128_chunk(r, lane & 7));
+                    if (rr < T * R && it.ta[i] + tok < p.L && col < p.P)
+                        *(uint4 *)((bf16 *)p.o + (((long long)it.bi * p.L + it.ta[i] + tok) * p.H + it.g * R + rr - tok * R) * p.P + col) = y;
                 }
             }
-            if (it.on[i]) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.o_empty[i]);
-            }
-            if (in && p.lse) p.lse[((long long)it.bi * p.H + h) * p.L + t] = live ? (m * c + log2f(l)) * kLn2 : 0.f;
         }
         if (!ok) sm.err = 1;
     }
@@ -380,7 +421,7 @@ cudaError_t forward(const WindowParams &p, cudaStream_t s) {
     const int T = tile_tokens(p);
     cudaError_t e;
     if ((e = map_tokens(&maps.q, p.q, p, p.H, p.hpg, T)) != cudaSuccess) return e;
-    if ((e = map_tokens(&maps.k, p.k, p, p.G, 1, 128)) != cudaSuccess) return e;
+    if ((e = map_tokens(&maps.k, p.k, p, p.G, 1, Layout<KB>::kKeys)) != cudaSuccess) return e;
     if ((e = delta::same_tiles(&maps.v, maps.k, p.v)) != cudaSuccess) return e;
     if ((e = delta::allow_shared((const void *)window_fwd_kernel<KB>, Layout<KB>::kBytes)) != cudaSuccess) return e;
     const int per_row = (p.L + 2 * T - 1) / (2 * T), items = per_row * p.G * p.b;
