@@ -59,10 +59,10 @@ template <int KEYS>
 struct Item {
     int bi, g, V, head, lo, end, tiles_a, tiles;
     int ta[2], from[2], last[2];  // first token; first and last window tile that is seen (none: last < from)
-    __device__ __forceinline__ Item(const WindowParams &p, int index, int per_row) {
-        const int T = tile_tokens(p), t0 = index % per_row * 2 * T;
-        g = index / per_row % p.G;
-        bi = index / per_row / p.G;
+    __device__ __forceinline__ Item(const WindowParams &p, const Cursor &c, int T) {
+        const int t0 = c.x * 2 * T;
+        g = c.g;
+        bi = c.b;
         V = valid_tokens(p, bi);
         end = min(t0 + 2 * T, V);
         lo = max(0, t0 - p.W + 1);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         }
         mbar_init(&sm.drain, 3);
         tc::mbar_fence_init();
-        sm.err = (base & 1023u) ? 1 : 0;
+        sm.err = 0;
     }
     if (blockIdx.x == 0) write_status(p);
     if (warp == 0) {
@@ -129,31 +129,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
-    bool ok = sm.err == 0;
+    const int T = tile_tokens(p);
+    int *const err = &sm.err;
 
     if (warp >= kSoftmax / 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == kSoftmax / 32) {
             // ---- copies, one thread
             if (elect()) {
-                const uint32_t q_bytes = (uint32_t)(tile_tokens(p) * p.hpg) * 128u * KB;
+                const uint32_t q_bytes = (uint32_t)(T * p.hpg) * 128u * KB;
                 Place<SLOTS> at;
                 uint32_t nq[2] = {0, 0};
                 int loaded = 0;
-                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-                    const It it(p, index, per_row);
+                for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+                    const It it(p, cur, T);
                     if (it.tiles == 0) continue;
                     auto load_q = [&](int i) {
-                        if (!it.on(i) || !ok) return;
-                        if (!(ok = wait_bar(&sm.q_empty[i], (nq[i] & 1) ^ 1))) return;
+                        if (!it.on(i)) return;
+                        wait_bar(&sm.q_empty[i], (nq[i] & 1) ^ 1, err);
                         mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
                         for (int kb = 0; kb < KB; ++kb)
                             tma_tile(base + i * Lay::kQTile + kb * 16384, &maps.q, &sm.q_full[i], 64 * kb, it.g * p.hpg, it.ta[i], it.bi);
                         ++nq[i];
                     };
-                    for (int x = 0; x < 2 * it.tiles && ok; ++x) {
+                    for (int x = 0; x < 2 * it.tiles; ++x) {
                         if (x < 2) load_q(x);
-                        if (!ok || !(ok = wait_bar(&sm.kv_empty[at.slot], at.phase ^ 1))) break;
+                        wait_bar(&sm.kv_empty[at.slot], at.phase ^ 1, err);
                         mbar_arrive_expect_tx(&sm.kv_full[at.slot], Lay::kTile);
                         for (int kb = 0; kb < KB; ++kb)
                             tma_tile(base + Lay::kOffRing + at.slot * Lay::kTile + kb * Lay::kBlock, x & 1 ? &maps.v : &maps.k,
@@ -162,11 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                         ++loaded;
                     }
                 }
-                if (!ok) sm.err = 1;
                 // copies in flight land before the block ends
-                for (int x = max(0, loaded - SLOTS); x < loaded; ++x) wait_bar(&sm.kv_full[x % SLOTS], (x / SLOTS) & 1);
+                for (int x = max(0, loaded - SLOTS); x < loaded; ++x) mbar_wait(&sm.kv_full[x % SLOTS], (x / SLOTS) & 1);
                 for (int i = 0; i < 2; ++i)
-                    if (nq[i]) wait_bar(&sm.q_full[i], (nq[i] - 1) & 1);
+                    if (nq[i]) mbar_wait(&sm.q_full[i], (nq[i] - 1) & 1);
             }
             __syncwarp();
         } else if (warp == kSoftmax / 32 + 1) {
@@ -177,19 +177,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 const uint64_t d_q = tc::sdesc(base, 16, 1024), d_k = tc::sdesc(base + Lay::kOffRing, 16, 1024);
                 Place<SLOTS> at;
                 uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};
-                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-                    const It it(p, index, per_row);
+                for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+                    const It it(p, cur, T);
                     bool loaded[2] = {false, false};
-                    for (int j = 0; j < it.tiles && ok; ++j) {
-                        if (!(ok = wait_bar(&sm.kv_full[at.slot], at.phase))) break;
+                    for (int j = 0; j < it.tiles; ++j) {
+                        wait_bar(&sm.kv_full[at.slot], at.phase, err);
                         const uint32_t i_s = i_s0 | (uint32_t)((it.count(j) + 15) >> 4) << 18;  // N / 8 from bit 17
                         const uint64_t k = delta::sdesc_add(d_k, at.slot * Lay::kTile);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            if (!ok || !it.need(i, j)) continue;
-                            if (!loaded[i]) ok = wait_bar(&sm.q_full[i], nq[i] & 1);
+                            if (!it.need(i, j)) continue;
+                            if (!loaded[i]) wait_bar(&sm.q_full[i], nq[i] & 1, err);
                             loaded[i] = true;
-                            if (!ok || !(ok = wait_bar(&sm.s_free[i], (ns[i] & 1) ^ 1))) continue;
+                            wait_bar(&sm.s_free[i], (ns[i] & 1) ^ 1, err);
                             ++ns[i];
                             tc::tc_fence_after();
                             const uint64_t q = delta::sdesc_add(d_q, i * Lay::kQTile);
@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     }
                     for (int i = 0; i < 2; ++i) nq[i] += it.on(i) && it.tiles;
                 }
-                if (!ok) sm.err = 1;
                 tc::mma_commit(&sm.drain);
-                wait_bar(&sm.drain, 0);
+                mbar_wait(&sm.drain, 0);
             }
             __syncwarp();
         } else {
@@ -221,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 Place<SLOTS> at;
                 at.next();
                 uint32_t no = 0, np = 0;
-                for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-                    const It it(p, index, per_row);
+                for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+                    const It it(p, cur, T);
                     bool begun = false;
-                    for (int j = 0; j < it.tiles && ok; ++j) {
-                        if (!(ok = wait_bar(&sm.kv_full[at.slot], at.phase))) break;
+                    for (int j = 0; j < it.tiles; ++j) {
+                        wait_bar(&sm.kv_full[at.slot], at.phase, err);
                         if (it.need(i, j)) {
-                            if (!begun && !(ok = wait_bar(&sm.o_empty[i], (no & 1) ^ 1))) break;
-                            if (!(ok = wait_bar(&sm.p_full[i], np & 1))) break;
+                            if (!begun) wait_bar(&sm.o_empty[i], (no & 1) ^ 1, err);
+                            wait_bar(&sm.p_full[i], np & 1, err);
                             ++np;
                             tc::tc_fence_after();
                             const int steps = (it.count(j) + 15) >> 4;
@@ -246,34 +245,33 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     }
                     no += it.on(i) && it.tiles;
                 }
-                if (!ok) sm.err = 1;
                 tc::mma_commit(&sm.drain);
-                wait_bar(&sm.drain, 0);
+                mbar_wait(&sm.drain, 0);
             }
             __syncwarp();
         }
     } else {
         // ---- softmax of query tile i
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int i = warp >> 2, row = tid & 127, quarter = warp & 3, R = p.hpg, T = tile_tokens(p);
+        const int i = warp >> 2, row = tid & 127, quarter = warp & 3, R = p.hpg;
         const uint32_t magic = row_magic(R), stage = base + Lay::kOffStage + warp * 4096;
         const uint32_t ts = tmem_addr(tm, 32 * quarter, Lay::kS + KEYS * i), tp = tmem_addr(tm, 32 * quarter, Lay::kP + KEYS / 2 * i),
                        to = tmem_addr(tm, 32 * quarter, Lay::kO + Lay::kOCols * i);
         int n = 0, ns = 0;
-        for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
-            const It it(p, index, per_row);
+        for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+            const It it(p, cur, T);
             const int token = row_token(row, magic), t = it.ta[i] + token, h = it.g * R + row - token * R;
             const bool in = row < T * R && t < p.L, live = in && t < it.V;
             float m = -INFINITY, l = 0.f;
             if (it.on(i)) {
                 const int tq = live ? t : it.ta[i];
                 bool begun = false;
-                for (int j = 0; j < it.tiles && ok; ++j, n += 2) {
+                for (int j = 0; j < it.tiles; ++j) {
                     if (!it.need(i, j)) continue;
                     const int s0 = it.start(j), nk = it.count(j);
                     // keys that every row sees: none behind the tile's first token, none in front of its last one's window
                     const bool plain = nk == KEYS && s0 + KEYS - 1 <= it.ta[i] && (s0 > it.ta[i] + T - 1 - p.W || s0 + KEYS <= p.sinks);
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[i], ns & 1)))) break;
+                    wait_warp(&sm.s_full[i], ns & 1, err);
                     tc::tc_fence_after();
                     float2 x[KEYS / 2];
                     if constexpr (KEYS == 80)
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     if (!plain) {
                         const int hi = min(nk, tq - s0 + 1), from = tq - p.W + 1 - s0, sk = p.sinks - s0;
 #pragma unroll
-                        for (int q = 0; q < (KEYS + 31) / 32; ++q) {
+                        for (int q = 0; q < (KEYS + 31) / 32; ++q) {  // past nk all of them
                             const uint32_t see = bits_between(-32, hi - 32 * q) &
                                                  (bits_between(from - 32 * q, 32) | bits_between(-32, sk - 32 * q));
 #pragma unroll
@@ -303,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     for (int e = 0; e < KEYS / 2; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x[e].x, x[e].y));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     // the product with the last P is done: P and O are this group's
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[i], (ns & 1) ^ 1)))) break;
+                    wait_warp(&sm.p_free[i], (ns & 1) ^ 1, err);
                     tc::tc_fence_after();
                     ++ns;
                     const bool grows = top > m && (m == -INFINITY || (top - m) * c > kLazy);
@@ -350,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     if ((nk & 15) && (i == 0 || !it.need(0, j))) {
                         // rows of V up to the product's step of 16: their probabilities are 0, so they have to be finite
-                        const int slot = (n + 1) % SLOTS, rows = 16 - (nk & 15);
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[slot], ((n + 1) / SLOTS) & 1)))) break;
+                        const int slot = (n + 2 * j + 1) % SLOTS, rows = 16 - (nk & 15);
+                        wait_warp(&sm.kv_full[slot], ((n + 2 * j + 1) / SLOTS) & 1, err);
                         const uint32_t v = base + Lay::kOffRing + slot * Lay::kTile;
                         for (int e = row; e < rows * 8 * KB; e += 128)
                             tc::st_shared_v4(v + (e / (8 * rows)) * Lay::kBlock + (nk + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
@@ -361,49 +359,50 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[i]);
                 }
-                if (!ok) break;
                 // the last product: p_free's phase that the next item's first tile waits for too
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[i], (ns & 1) ^ 1)))) break;
+                wait_warp(&sm.p_free[i], (ns & 1) ^ 1, err);
                 tc::tc_fence_after();
-            } else {
-                n += 2 * it.tiles;
             }
+            n += 2 * it.tiles;
             if (in && p.lse) p.lse[((long long)it.bi * p.H + h) * p.L + t] = live ? (m * c + log2f(l)) * kLn2 : 0.f;
             const float inv = live ? 1.f / l : 0.f;
             // O in bf16, 64 columns at a time through the warp's stage, so that a row leaves as whole lines
+            bf16 *const o = (bf16 *)p.o + (((long long)it.bi * p.L + it.ta[i]) * p.H + it.g * R) * p.P;
+            const int rows = min(T, p.L - it.ta[i]) * R;  // of the tile that there are
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[16];
-                    if (it.on(i))
-                        tc::tmem_ld16(to + 64 * kb + 16 * q, v);
-                    else
+                for (int q = 0; q < 2; ++q) {
+                    float v[32];
+                    if (it.on(i)) {
+                        tc::tmem_ld32u(to + 64 * kb + 32 * q, (uint32_t *)v);
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    uint32_t y[8];
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    }
+                    uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = live ? tc::pack_bf2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
-                    tc::st_shared_v4(stage + tc::sw128_chunk(lane, 2 * q), y[0], y[1], y[2], y[3]);
-                    tc::st_shared_v4(stage + tc::sw128_chunk(lane, 2 * q + 1), y[4], y[5], y[6], y[7]);
-                    __syncwarp();
+                    for (int e = 0; e < 16; ++e) y[e] = live ? tc::pack_bf2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        tc::st_shared_v4(stage + tc::sw128_chunk(lane, 4 * q + e), y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                 }
+                __syncwarp();
                 if (kb == KB - 1 && it.on(i)) {
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.o_empty[i]);
                 }
+                const int col = 64 * kb + 8 * (lane & 7);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int r = 4 * e + (lane >> 3), rr = 32 * quarter + r, tok = row_token(rr, magic), col = 64 * kb + 8 * (lane & 7);
+                    const int r = 4 * e + (lane >> 3), rr = 32 * quarter + r;
                     const uint4 y = tc::ld_shared_v4(stage + tc::sw128_chunk(r, lane & 7));
-                    if (rr < T * R && it.ta[i] + tok < p.L && col < p.P)
-                        *(uint4 *)((bf16 *)p.o + (((long long)it.bi * p.L + it.ta[i] + tok) * p.H + it.g * R + rr - tok * R) * p.P + col) = y;
+                    if (rr < rows && col < p.P) *(uint4 *)(o + row_token(rr, magic) * (p.H - R) * p.P + rr * p.P + col) = y;
                 }
             }
         }
-        if (!ok) sm.err = 1;
     }
     tc::tc_fence_before();
     __syncthreads();

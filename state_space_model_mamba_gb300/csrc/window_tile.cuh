@@ -46,12 +46,44 @@ __device__ __forceinline__ bool elect() {
     return one != 0;
 }
 
-// The wait of the issuing threads: what waits for nothing is a few instructions in line (their code is walked through once
-// per tile, past the instruction caches that the softmax's fills), the rest is called.  False after 2 s.
-__device__ __noinline__ inline bool wait_long(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity); }
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
-    return tc::mbar_try_wait(bar, parity) || wait_long(bar, parity);
+// A wait in two parts: what is over already is a few instructions in line, the rest a loop.  After 2 s, or once any wait
+// of the block has given up, it gives up and says so in `err`; the caller goes on, with values that nobody will use, and
+// every later wait of the block ends at once.
+__device__ __forceinline__ void wait_loop(uint64_t *bar, uint32_t parity, int *err) {
+    const uint64_t t0 = tc::global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (tc::mbar_try_wait(bar, parity)) return;
+        if ((it & 63u) == 0u && (*(volatile int *)err || tc::global_timer_ns() - t0 > tc::kWaitLimitNs)) {
+            *(volatile int *)err = 1;
+            return;
+        }
+    }
 }
+__device__ __noinline__ inline void wait_long(uint64_t *bar, uint32_t parity, int *err) { wait_loop(bar, parity, err); }
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, int *err) {
+    if (!tc::mbar_try_wait(bar, parity)) wait_long(bar, parity, err);
+}
+// The same for whole warps with registers full of values, that a call would have to put away.
+__device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, int *err) {
+    if (!tc::mbar_try_wait(bar, parity)) wait_loop(bar, parity, err);
+    __syncwarp();
+}
+
+// The items (batch row, key group, place in the row) of a block: from the block's number on in steps of the grid, without
+// divisions after the first.
+struct Cursor {
+    int x, g, b, dx, dg, db, left;
+    __device__ __forceinline__ Cursor(int items, int per_row, int G) {
+        x = blockIdx.x % per_row, g = blockIdx.x / per_row % G, b = blockIdx.x / per_row / G;
+        dx = gridDim.x % per_row, dg = gridDim.x / per_row % G, db = gridDim.x / per_row / G;
+        left = (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;
+    }
+    __device__ __forceinline__ void next(int per_row, int G) {
+        x += dx, g += dg, b += db, --left;
+        if (x >= per_row) x -= per_row, ++g;
+        if (g >= G) g -= G, ++b;
+    }
+};
 
 // bits [lo, hi) of 32, either may be out of range
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
