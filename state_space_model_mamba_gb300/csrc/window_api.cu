@@ -70,10 +70,14 @@ constexpr size_t kStatusBytes = 1024;  // status words, then the backward's buff
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // The backward's buffers behind the status words.
-size_t carve(const window_dims &d, char *ws, WindowParams *p) {
+size_t carve(const window_dims &d, ssd_dtype dt, char *ws, WindowParams *p, float **parts) {
     const size_t delta = up256(4ull * d.batch * d.nheads * d.seqlen);
-    if (p) p->delta = (float *)(ws + kStatusBytes);
-    return kStatusBytes + delta;
+    if (p) {
+        p->delta = (float *)(ws + kStatusBytes);
+        *parts = (float *)(ws + kStatusBytes + delta);
+    }
+    if (!tile_supported(d, dt, true)) return kStatusBytes + delta;
+    return kStatusBytes + delta + 4 * tile_backward_floats(d.batch, d.seqlen, d.ngroups, d.headdim, d.window, d.sinks);
 }
 
 WindowParams base_params(const window_dims &d, const void *q, const void *k, const void *v, float scale,
@@ -145,7 +149,7 @@ ssd_status window_supported(const window_dims *dims, ssd_dtype dtype) {
 size_t window_workspace_bytes(const window_dims *dims, ssd_dtype dtype, int backward) {
     record_error("");
     if (validate(dims, dtype) != SSD_OK) return 0;
-    return backward ? carve(*dims, nullptr, nullptr) : kStatusBytes;
+    return backward ? carve(*dims, dtype, nullptr, nullptr, nullptr) : kStatusBytes;
 }
 
 ssd_status window_forward(const window_dims *dims, ssd_dtype dtype, const void *q, const void *k, const void *v,
@@ -164,7 +168,7 @@ ssd_status window_forward(const window_dims *dims, ssd_dtype dtype, const void *
     p.o = o;
     p.lse = lse;
     return guarded([&] {
-        if (tile_supported(*dims, dtype)) return launch_tile_forward(p, (cudaStream_t)stream);
+        if (tile_supported(*dims, dtype, false)) return launch_tile_forward(p, (cudaStream_t)stream);
         return launch_simt_forward(p, dtype == SSD_BF16, (cudaStream_t)stream);
     });
 }
@@ -182,14 +186,18 @@ ssd_status window_backward(const window_dims *dims, ssd_dtype dtype, const void 
     if (workspace_bytes < need)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
     WindowParams p = base_params(*dims, q, k, v, scale, valid_len, workspace);
-    carve(*dims, (char *)workspace, &p);
+    float *parts = nullptr;
+    carve(*dims, dtype, (char *)workspace, &p, &parts);
     p.o = const_cast<void *>(o);
     p.lse = const_cast<float *>(lse);
     p.d_o = d_o;
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    return guarded([&] { return launch_simt_backward(p, dtype == SSD_BF16, (cudaStream_t)stream); });
+    return guarded([&] {
+        if (tile_supported(*dims, dtype, true)) return launch_tile_backward(p, parts, (cudaStream_t)stream);
+        return launch_simt_backward(p, dtype == SSD_BF16, (cudaStream_t)stream);
+    });
 }
 
 ssd_status window_fill(const window_dims *dims, ssd_dtype dtype, const void *k, const void *v, const int32_t *valid_len,

@@ -82,16 +82,6 @@ struct Item {
     __device__ __forceinline__ int count(int j) const { return min(KEYS, (j < tiles_a ? head : end) - start(j)); }
     __device__ __forceinline__ bool need(int i, int j) const { return j <= last[i] && (j < tiles_a || j >= from[i]); }
 };
-// A place in a ring of SLOTS and the parity of its phase.
-template <int SLOTS>
-struct Place {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == SLOTS) slot = 0, phase ^= 1;
-    }
-};
-
 template <int KB>
 __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_constant__ Maps maps, WindowParams p, float c,
                                                                  uint32_t negate, int items, int per_row) {

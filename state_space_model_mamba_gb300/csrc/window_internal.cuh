@@ -63,8 +63,10 @@ __device__ __forceinline__ void store4<bf16>(bf16 *p, float4 v) {
 cudaError_t launch_simt_forward(const WindowParams &p, bool is_bf16, cudaStream_t s);
 cudaError_t launch_simt_backward(const WindowParams &p, bool is_bf16, cudaStream_t s);
 
-// ---- tensor-core kernels (window_fwd.cu)
+// ---- tensor-core kernels (window_fwd.cu, window_bwd.cu); the backward's share of the workspace in floats
 cudaError_t launch_tile_forward(const WindowParams &p, cudaStream_t s);
+size_t tile_backward_floats(long long batch, long long L, long long G, long long P, long long W, long long sinks);
+cudaError_t launch_tile_backward(const WindowParams &p, float *parts, cudaStream_t s);
 
 // ---- the ring (window_step.cu)
 struct RingParams {
