@@ -70,6 +70,9 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
 
 template <int TPR>
 constexpr int kBlock = TPR < 256 ? 256 : TPR;
+// Rows in flight ahead of the one in work.
+template <int NV>
+constexpr int kAhead = NV == 1 ? 2 : 1;
 
 // What both kernels hold of a short row: vectors j of thread t at columns (j TPR + t) VEC.
 template <int VEC, int TPR, int NV>
@@ -133,8 +136,9 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
             if (a.bias) b[j].load(a.bias + off + at.col(j));
         }
     }
-    Vec<T, VEC> x[NV], z[NV];
-    auto load = [&](long long row) {
+    constexpr int A = kAhead<NV>;
+    Vec<T, VEC> xs[A][NV], zs[A][NV];
+    auto load = [&](long long row, Vec<T, VEC> *x, Vec<T, VEC> *z) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             x[j].zero();
@@ -145,8 +149,10 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
             }
         }
     };
-    load(at.mine);
-    for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
+#pragma unroll
+    for (int k = 0; k < A; ++k) load(at.mine + k * at.step, xs[k], zs[k]);
+    long long row = at.mine;
+    auto one = [&](Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV]) {
         float2 u[NV][PAIRS], s[NV][PAIRS];  // s: what the normed value is multiplied with
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
                 if (a.gate) s[j][i] = act2<T>(a.act, z[j].get(i));
                 if (a.first) u[j][i] = fmul2(u[j][i], s[j][i]);
             }
-        load(row + at.step);
+        load(row + A * at.step, x, z);
         normalise(u, a, at, buf, turn);
         if (row < a.rows)
 #pragma unroll
@@ -174,7 +180,11 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
                 }
                 y.store((T *)a.y + row * a.w + at.col(j));
             }
-    }
+        row += at.step;
+    };
+    for (long long base = row - threadIdx.x / TPR; base < a.rows; base += A * at.step)
+#pragma unroll
+        for (int k = 0; k < A; ++k) one(xs[k], zs[k]);  // past the last row nothing is read or written
 }
 
 // ------------------------------------------------------------------ backward
@@ -198,8 +208,9 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) dw[j][i] = db[j][i] = make_float2(0.f, 0.f);
     }
-    Vec<T, VEC> x[NV], z[NV], dy[NV];
-    auto load = [&](long long row) {
+    constexpr int A = kAhead<NV>;
+    Vec<T, VEC> xs[A][NV], zs[A][NV], dys[A][NV];
+    auto load = [&](long long row, Vec<T, VEC> *x, Vec<T, VEC> *z, Vec<T, VEC> *dy) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             x[j].zero();
@@ -212,9 +223,11 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
             }
         }
     };
-    load(at.mine);
+#pragma unroll
+    for (int k = 0; k < A; ++k) load(at.mine + k * at.step, xs[k], zs[k], dys[k]);
     const float inv = 1.f / (float)a.w;
-    for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
+    long long row = at.mine;
+    auto one = [&](Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV], Vec<T, VEC>(&dy)[NV]) {
         // u, then n;  g the gradient of y;  s the gate's activation, d what dgate is multiplied with
         float2 u[NV][PAIRS], g[NV][PAIRS], s[NV][PAIRS], d[NV][PAIRS];
 #pragma unroll
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                     }
                 }
             }
-        load(row + at.step);
+        load(row + A * at.step, x, z, dy);
         const float rstd = normalise(u, a, at, buf, turn);
         float2 t1 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
         const bool live = row < a.rows;
@@ -278,7 +291,11 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                 dx.store((T *)a.dx + row * a.w + at.col(j));
                 if (a.gate) dz.store((T *)a.dgate + row * a.w + at.col(j));
             }
-    }
+        row += at.step;
+    };
+    for (long long base = row - threadIdx.x / TPR; base < a.rows; base += A * at.step)
+#pragma unroll
+        for (int k = 0; k < A; ++k) one(xs[k], zs[k], dys[k]);  // past the last row nothing is read, written or added
     if (a.part) {
         const long long D = (long long)a.groups * a.w, slots = at.step / a.groups, slot = at.mine / a.groups;
 #pragma unroll

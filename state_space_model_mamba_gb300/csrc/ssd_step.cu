@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = 4 * (i * kLanes + lane);
-        s[i] = in && c < p.N ? __ldcs((const float4 *)(srow + c)) : zero;
+        s[i] = in && c < p.N ? *(const float4 *)(srow + c) : zero;
         B[i] = c < p.N ? load4((const T *)p.B + key + c) : zero;
         C[i] = c < p.N ? load4((const T *)p.C + key + c) : zero;
     }
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
                            fmaf(u, B[i].w, a * s[i].w));
         y = fmaf(s[i].x, C[i].x, fmaf(s[i].y, C[i].y, fmaf(s[i].z, C[i].z, fmaf(s[i].w, C[i].w, y))));
         const int c = 4 * (i * kLanes + lane);
-        if (in && c < p.N) __stcs((float4 *)(srow + c), s[i]);
+        if (in && c < p.N) *(float4 *)(srow + c) = s[i];
     }
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);

@@ -15,6 +15,7 @@
 // races with nobody.
 #include <cooperative_groups.h>
 
+#include "tc_ptx.cuh"
 #include "window_internal.cuh"
 
 namespace cg = cooperative_groups;
@@ -23,7 +24,7 @@ namespace ssd {
 namespace window {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ prompts into the ring
@@ -153,6 +154,17 @@ __device__ __forceinline__ float quad_max(float x) {
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
+// A lane's 16-byte pieces on their way to shared memory, in groups that are waited for in order; what a lane copies it reads
+// itself, so that a warp's stages need no barrier.  Rows that are not there become zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // bf16.  NI = ceil(P / 32).  A fragment of m16n8k16 wants inner indices 2c, 2c + 1, 2c + 8, 2c + 9 of lane 4 r + c; it is
 // given elements 32 i + 8 c + (0 .. 3) for step 2 i and + (4 .. 7) for step 2 i + 1, of q and k alike.
 // A column tile's column n of the second product is column 64 v + 8 n + j of v for tile (v, j).
@@ -190,23 +202,51 @@ __global__ void __launch_bounds__(kThreads) ring_step_mma(RingParams p, int spli
         for (int j = 0; j < 8; ++j) o[v][j][0] = o[v][j][1] = o[v][j][2] = o[v][j][3] = 0.f;
     const int tiles = (r.n + 15) / 16, per = (tiles + splits - 1) / splits, last = min(tiles, (r.split + 1) * per);
     const bf16 *kown = (const bf16 *)p.k + r.own(p), *vown = (const bf16 *)p.v + r.own(p);
-    for (int tile = r.split * per + warp; tile < last; tile += kThreads / 32) {
+    // tiles ahead of the one in work, each 2 NI + 4 NV pieces a lane
+    constexpr int kPieces = 2 * NI + 4 * NV;
+    const uint32_t ring = tc::smem_u32(smem4) + (uint32_t)(warp * kStages * kPieces * 32 + lane) * 16u;
+    auto fetch = [&](int tile, int stage) {
+        if (tile < last) {
+            const int j0 = tile * 16;
+            uint32_t to = ring + (uint32_t)(stage * kPieces * 32) * 16u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = j0 + 8 * x + row;
+                const bf16 *src = j == r.at ? kown : (const bf16 *)p.k_cache + r.entry(p, min(j, r.n - 1));
+#pragma unroll
+                for (int i = 0; i < NI; ++i, to += 512) {
+                    const bool in = j < r.n && 32 * i + 8 * c < p.P;
+                    copy16(to, src + (in ? 32 * i + 8 * c : 0), in);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = j0 + 8 * (x >> 1) + 2 * c + (x & 1);
+                const bf16 *src = j == r.at ? vown : (const bf16 *)p.v_cache + r.entry(p, min(j, r.n - 1));
+#pragma unroll
+                for (int v = 0; v < NV; ++v, to += 512) {
+                    const bool in = j < r.n && 64 * v + 8 * row < p.P;
+                    copy16(to, src + (in ? 64 * v + 8 * row : 0), in);
+                }
+            }
+        }
+        copy_commit();
+    };
+    constexpr int kStep = kThreads / 32;
+    int stage = 0, ahead = r.split * per + warp;
+#pragma unroll
+    for (int x = 0; x < kStages - 1; ++x, ahead += kStep) fetch(ahead, x);
+    for (int tile = r.split * per + warp; tile < last; tile += kStep, ahead += kStep) {
         const int j0 = tile * 16;
+        fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+        copy_wait<kStages - 1>();
+        const uint32_t from = ring + (uint32_t)(stage * kPieces * 32) * 16u;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         uint4 kr[2][NI], vr[4][NV];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int j = j0 + 8 * x + row;
-            const bf16 *src = j == r.at ? kown : (const bf16 *)p.k_cache + r.entry(p, j);
+        for (int x = 0; x < 2 * NI; ++x) kr[x / NI][x % NI] = tc::ld_shared_v4(from + x * 512);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) kr[x][i] = j < r.n && 32 * i + 8 * c < p.P ? __ldcs((const uint4 *)(src + 32 * i + 8 * c)) : zero;
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int j = j0 + 8 * (x >> 1) + 2 * c + (x & 1);
-            const bf16 *src = j == r.at ? vown : (const bf16 *)p.v_cache + r.entry(p, j);
-#pragma unroll
-            for (int v = 0; v < NV; ++v) vr[x][v] = j < r.n && 64 * v + 8 * row < p.P ? __ldcs((const uint4 *)(src + 64 * v + 8 * row)) : zero;
-        }
+        for (int x = 0; x < 4 * NV; ++x) vr[x / NV][x % NV] = tc::ld_shared_v4(from + (2 * NI + x) * 512);
         float s[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -246,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) ring_step_mma(RingParams p, int spli
             }
         }
     }
+    copy_wait<0>();
+    __syncthreads();  // the shares take the stages' place
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -375,6 +417,14 @@ cudaError_t step_rows(const RingParams &p, cudaStream_t s) {
     }
 }
 
+template <int NI>
+cudaError_t step_mma(const RingParams &p, cudaStream_t s) {
+    constexpr int ring = kThreads * kStages * (2 * NI + 4 * ((NI + 1) / 2)) * 16, join = shared_bytes<4, 16>(32 * NI);
+    constexpr int shared = ring > join ? ring : join;
+    const cudaError_t e = delta::allow_shared((const void *)ring_step_mma<NI>, shared);
+    return e != cudaSuccess ? e : launch_clusters(ring_step_mma<NI>, p, 16, shared, s);
+}
+
 }  // namespace
 
 cudaError_t launch_fill(const RingParams &p, bool is_bf16, cudaStream_t s) {
@@ -391,12 +441,11 @@ cudaError_t launch_fill(const RingParams &p, bool is_bf16, cudaStream_t s) {
 cudaError_t launch_step(const RingParams &p, bool is_bf16, cudaStream_t s) {
     if (!is_bf16) return step_rows<float>(p, s);
     if (p.P % 8) return step_rows<bf16>(p, s);
-    const int shared = shared_bytes<4, 16>(p.P);
     switch ((p.P + 31) / 32) {
-        case 1: return launch_clusters(ring_step_mma<1>, p, 16, shared, s);
-        case 2: return launch_clusters(ring_step_mma<2>, p, 16, shared, s);
-        case 3: return launch_clusters(ring_step_mma<3>, p, 16, shared, s);
-        default: return launch_clusters(ring_step_mma<4>, p, 16, shared, s);
+        case 1: return step_mma<1>(p, s);
+        case 2: return step_mma<2>(p, s);
+        case 3: return step_mma<3>(p, s);
+        default: return step_mma<4>(p, s);
     }
 }
 
