@@ -70,9 +70,6 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
 
 template <int TPR>
 constexpr int kBlock = TPR < 256 ? 256 : TPR;
-// Rows in flight ahead of the one in work.
-template <int NV>
-constexpr int kAhead = NV == 1 ? 2 : 1;
 
 // What both kernels hold of a short row: vectors j of thread t at columns (j TPR + t) VEC.
 template <int VEC, int TPR, int NV>
@@ -88,6 +85,38 @@ template <int VEC, int TPR, int NV, int PAIRS>
 __device__ __forceinline__ float normalise(float2 (&u)[NV][PAIRS], const GroupArgs &a, const Place<VEC, TPR, NV> &at,
                                            float (*buf)[32][1], int &turn) {
     const float inv = 1.f / (float)a.w;
+    if (TPR <= 32 && a.center && a.w == TPR * NV * VEC) {
+        // every lane has as many columns: its own mean and squares about it, then lanes in pairs, whose squares about the common
+        // mean are the sum of theirs and n / 2 times the difference's; one chain of shuffles in place of two
+        constexpr float n = (float)(NV * VEC);
+        float2 s2 = make_float2(0.f, 0.f), q2 = s2;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) s2 = make_float2(s2.x + u[j][i].x, s2.y + u[j][i].y);
+        float mean = (s2.x + s2.y) * (1.f / n);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const float2 d = make_float2(u[j][i].x - mean, VEC > 1 ? u[j][i].y - mean : 0.f);
+                q2 = ffma2(d, d, q2);
+            }
+        float squares = q2.x + q2.y, half = 0.5f * n;
+#pragma unroll
+        for (int o = 1; o < TPR; o <<= 1) {
+            const float m = __shfl_xor_sync(0xffffffffu, mean, o), q = __shfl_xor_sync(0xffffffffu, squares, o), d = m - mean;
+            squares = (squares + q) + half * d * d;
+            mean = 0.5f * (mean + m);
+            half += half;
+        }
+        const float rstd = rsqrtf(squares * inv + a.eps), off = -mean * rstd;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) u[j][i] = ffma2(u[j][i], make_float2(rstd, rstd), make_float2(off, VEC > 1 ? off : 0.f));
+        return rstd;
+    }
     if (a.center) {
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -136,9 +165,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
             if (a.bias) b[j].load(a.bias + off + at.col(j));
         }
     }
-    constexpr int A = kAhead<NV>;
-    Vec<T, VEC> xs[A][NV], zs[A][NV];
-    auto load = [&](long long row, Vec<T, VEC> *x, Vec<T, VEC> *z) {
+    Vec<T, VEC> x[NV], z[NV];
+    auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             x[j].zero();
@@ -149,10 +177,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
             }
         }
     };
-#pragma unroll
-    for (int k = 0; k < A; ++k) load(at.mine + k * at.step, xs[k], zs[k]);
-    long long row = at.mine;
-    auto one = [&](Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV]) {
+    load(at.mine);
+    for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
         float2 u[NV][PAIRS], s[NV][PAIRS];  // s: what the normed value is multiplied with
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -162,7 +188,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
                 if (a.gate) s[j][i] = act2<T>(a.act, z[j].get(i));
                 if (a.first) u[j][i] = fmul2(u[j][i], s[j][i]);
             }
-        load(row + A * at.step, x, z);
+        load(row + at.step);
         normalise(u, a, at, buf, turn);
         if (row < a.rows)
 #pragma unroll
@@ -180,11 +206,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
                 }
                 y.store((T *)a.y + row * a.w + at.col(j));
             }
-        row += at.step;
-    };
-    for (long long base = row - threadIdx.x / TPR; base < a.rows; base += A * at.step)
-#pragma unroll
-        for (int k = 0; k < A; ++k) one(xs[k], zs[k]);  // past the last row nothing is read or written
+    }
 }
 
 // ------------------------------------------------------------------ backward
@@ -208,9 +230,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) dw[j][i] = db[j][i] = make_float2(0.f, 0.f);
     }
-    constexpr int A = kAhead<NV>;
-    Vec<T, VEC> xs[A][NV], zs[A][NV], dys[A][NV];
-    auto load = [&](long long row, Vec<T, VEC> *x, Vec<T, VEC> *z, Vec<T, VEC> *dy) {
+    Vec<T, VEC> x[NV], z[NV], dy[NV];
+    auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             x[j].zero();
@@ -223,11 +244,9 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
             }
         }
     };
-#pragma unroll
-    for (int k = 0; k < A; ++k) load(at.mine + k * at.step, xs[k], zs[k], dys[k]);
+    load(at.mine);
     const float inv = 1.f / (float)a.w;
-    long long row = at.mine;
-    auto one = [&](Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV], Vec<T, VEC>(&dy)[NV]) {
+    for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
         // u, then n;  g the gradient of y;  s the gate's activation, d what dgate is multiplied with
         float2 u[NV][PAIRS], g[NV][PAIRS], s[NV][PAIRS], d[NV][PAIRS];
 #pragma unroll
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                     }
                 }
             }
-        load(row + A * at.step, x, z, dy);
+        load(row + at.step);
         const float rstd = normalise(u, a, at, buf, turn);
         float2 t1 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
         const bool live = row < a.rows;
@@ -291,11 +310,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                 dx.store((T *)a.dx + row * a.w + at.col(j));
                 if (a.gate) dz.store((T *)a.dgate + row * a.w + at.col(j));
             }
-        row += at.step;
-    };
-    for (long long base = row - threadIdx.x / TPR; base < a.rows; base += A * at.step)
-#pragma unroll
-        for (int k = 0; k < A; ++k) one(xs[k], zs[k], dys[k]);  // past the last row nothing is read, written or added
+    }
     if (a.part) {
         const long long D = (long long)a.groups * a.w, slots = at.step / a.groups, slot = at.mine / a.groups;
 #pragma unroll

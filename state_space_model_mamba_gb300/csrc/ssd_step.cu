@@ -47,10 +47,14 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
     for (int i = 0; i < NC; ++i) {
         const int c = 4 * (i * kLanes + lane);
         s[i] = in && c < p.N ? *(const float4 *)(srow + c) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 4 * (i * kLanes + lane);
         B[i] = c < p.N ? load4((const T *)p.B + key + c) : zero;
         C[i] = c < p.N ? load4((const T *)p.C + key + c) : zero;
     }
-    const float dt = p.dt[(long long)bi * p.H + h], a = expf(dt * p.A[h]);
+    const float dt = __ldg(p.dt + (long long)bi * p.H + h), a = expf(dt * __ldg(p.A + h)), D = __ldg(p.D + h);
     const float x = in ? load1((const T *)p.x + at) : 0.f, u = dt * x;
     float y = 0.f;
 #pragma unroll
@@ -58,12 +62,15 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
         s[i] = make_float4(fmaf(u, B[i].x, a * s[i].x), fmaf(u, B[i].y, a * s[i].y), fmaf(u, B[i].z, a * s[i].z),
                            fmaf(u, B[i].w, a * s[i].w));
         y = fmaf(s[i].x, C[i].x, fmaf(s[i].y, C[i].y, fmaf(s[i].z, C[i].z, fmaf(s[i].w, C[i].w, y))));
-        const int c = 4 * (i * kLanes + lane);
-        if (in && c < p.N) *(float4 *)(srow + c) = s[i];
     }
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (in && lane == 0) store1((T *)p.y + at, fmaf(p.D[h], x, y));
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 4 * (i * kLanes + lane);
+        if (in && c < p.N) *(float4 *)(srow + c) = s[i];
+    }
+    if (in && lane == 0) store1((T *)p.y + at, fmaf(D, x, y));
 }
 
 template <typename T>

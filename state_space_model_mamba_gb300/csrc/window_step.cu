@@ -24,7 +24,7 @@ namespace ssd {
 namespace window {
 namespace {
 
-constexpr int kThreads = 128, kStages = 3;
+constexpr int kThreads = 128, kStages = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ prompts into the ring
@@ -169,7 +169,7 @@ __device__ __forceinline__ void copy_wait() {
 // given elements 32 i + 8 c + (0 .. 3) for step 2 i and + (4 .. 7) for step 2 i + 1, of q and k alike.
 // A column tile's column n of the second product is column 64 v + 8 n + j of v for tile (v, j).
 template <int NI>
-__global__ void __launch_bounds__(kThreads) ring_step_mma(RingParams p, int splits, int chunks) {
+__global__ void __launch_bounds__(kThreads, 3) ring_step_mma(RingParams p, int splits, int chunks) {
     extern __shared__ float4 smem4[];
     Shares<4, 16> *sh = (Shares<4, 16> *)smem4;
     constexpr int NV = (NI + 1) / 2;
