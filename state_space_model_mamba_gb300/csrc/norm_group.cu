@@ -39,15 +39,26 @@ struct GroupArgs {
 };
 
 // The activation and its derivative; for silu x s and s (1 + x (1 - s)) with s the logistic function of x.
+// 1 / (1 + exp(-x)) of a pair.  fp32 takes expf; bf16 the approximations of 2^x and of the reciprocal, off by some
+// 2^-21 of the result where its rounding is 2^-9.  exp(-x) past fp32 is infinite and the result 0.
 template <typename T>
-__device__ __forceinline__ float logistic(float x) {
-    const float e = sizeof(T) == 4 ? expf(-x) : __expf(-x);  // __expf: some 2^-21 of the value, bf16 keeps 2^-9
-    return __fdividef(1.f, 1.f + e);
+__device__ __forceinline__ float2 logistic(float2 x) {
+    if constexpr (sizeof(T) == 4) {
+        return make_float2(__fdividef(1.f, 1.f + expf(-x.x)), __fdividef(1.f, 1.f + expf(-x.y)));
+    } else {
+        float2 e = fmul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        e = fadd2(e, make_float2(1.f, 1.f));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        return e;
+    }
 }
 template <typename T>
 __device__ __forceinline__ float2 act2(int act, float2 x) {
     if (act == NORM_ACT_NONE) return x;
-    const float2 s = make_float2(logistic<T>(x.x), logistic<T>(x.y));
+    const float2 s = logistic<T>(x);
     return act == NORM_ACT_SILU ? fmul2(x, s) : s;
 }
 template <typename T>
@@ -58,7 +69,7 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
         d = one;
         return;
     }
-    const float2 s = make_float2(logistic<T>(x.x), logistic<T>(x.y)), r = ffma2(s, minus, one);  // 1 - s
+    const float2 s = logistic<T>(x), r = ffma2(s, minus, one);  // 1 - s
     if (act == NORM_ACT_SILU) {
         a = fmul2(x, s);
         d = fmul2(s, ffma2(x, r, one));
@@ -93,13 +104,13 @@ __device__ __forceinline__ float normalise(float2 (&u)[NV][PAIRS], const GroupAr
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < PAIRS; ++i) s2 = make_float2(s2.x + u[j][i].x, s2.y + u[j][i].y);
+            for (int i = 0; i < PAIRS; ++i) s2 = fadd2(s2, u[j][i]);
         float mean = (s2.x + s2.y) * (1.f / n);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
-                const float2 d = make_float2(u[j][i].x - mean, VEC > 1 ? u[j][i].y - mean : 0.f);
+                const float2 d = fadd2(u[j][i], make_float2(-mean, VEC > 1 ? -mean : 0.f));
                 q2 = ffma2(d, d, q2);
             }
         float squares = q2.x + q2.y, half = 0.5f * n;
@@ -122,7 +133,7 @@ __device__ __forceinline__ float normalise(float2 (&u)[NV][PAIRS], const GroupAr
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < PAIRS; ++i) s2 = make_float2(s2.x + u[j][i].x, s2.y + u[j][i].y);
+            for (int i = 0; i < PAIRS; ++i) s2 = fadd2(s2, u[j][i]);
         float s[1] = {s2.x + s2.y};
         row_reduce<Sum, TPR, 1>(s, buf, turn);
         const float mean = s[0] * inv;
@@ -130,7 +141,7 @@ __device__ __forceinline__ float normalise(float2 (&u)[NV][PAIRS], const GroupAr
         for (int j = 0; j < NV; ++j)
             if (at.col(j) < a.w)
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) u[j][i] = make_float2(u[j][i].x - mean, VEC > 1 ? u[j][i].y - mean : 0.f);
+                for (int i = 0; i < PAIRS; ++i) u[j][i] = fadd2(u[j][i], make_float2(-mean, VEC > 1 ? -mean : 0.f));
     }
     float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -284,9 +295,9 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                     d[j][i] = fmul2(d[j][i], y);  // dgate
                 }
                 dw[j][i] = ffma2(g[j][i], u[j][i], dw[j][i]);
-                db[j][i] = make_float2(db[j][i].x + g[j][i].x, db[j][i].y + g[j][i].y);
+                db[j][i] = fadd2(db[j][i], g[j][i]);
                 g[j][i] = fmul2(g[j][i], w[j].get(i));
-                t1 = make_float2(t1.x + g[j][i].x, t1.y + g[j][i].y);
+                t1 = fadd2(t1, g[j][i]);
                 t2 = ffma2(g[j][i], u[j][i], t2);
             }
         float t[2] = {t1.x + t1.y, t2.x + t2.y};

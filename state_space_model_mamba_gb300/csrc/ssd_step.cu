@@ -1,7 +1,7 @@
 // ssd_step.cu -- one decoded token of the selective scan (ssd_step, include/ssd.h).
 //
 // Row p of a state is a recurrence of its own, s <- exp(dt A) s + dt x_p B, y_p = s.C + D x_p.
-// 8 lanes hold a row in 16-byte pieces interleaved over the lanes, 32 rows a block; every state element
+// 8 lanes hold a row in 16-byte pieces interleaved over the lanes, 16 rows a block; every state element
 // is read and written once, and that is what bounds it: HBM.
 #include <stdarg.h>
 #include <stdio.h>
@@ -15,7 +15,7 @@ using delta::load1;
 using delta::load4;
 using delta::store1;
 
-constexpr int kLanes = 8, kRows = 32, kThreads = kRows * kLanes;
+constexpr int kLanes = 8, kRows = 16, kThreads = kRows * kLanes;
 
 struct StepParams {
     int b, H, P, N, G, hpg;
@@ -27,7 +27,7 @@ struct StepParams {
     void *y;
 };
 
-// NC = ceil(N / 32) pieces a lane.  Grid: one block per (b, h, 32 rows).
+// NC = ceil(N / 32) pieces a lane.  Grid: one block per (b, h, 16 rows).
 template <typename T, int NC>
 __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
     const int nblk = (p.P + kRows - 1) / kRows, bh = blockIdx.x / nblk, bi = bh / p.H, h = bh % p.H, g = h / p.hpg;
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = 4 * (i * kLanes + lane);
-        s[i] = in && c < p.N ? *(const float4 *)(srow + c) : zero;
+        s[i] = in && c < p.N ? __ldcs((const float4 *)(srow + c)) : zero;
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) ssd_step_kernel(StepParams p) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = 4 * (i * kLanes + lane);
-        if (in && c < p.N) *(float4 *)(srow + c) = s[i];
+        if (in && c < p.N) __stcs((float4 *)(srow + c), s[i]);
     }
     if (in && lane == 0) store1((T *)p.y + at, fmaf(D, x, y));
 }
