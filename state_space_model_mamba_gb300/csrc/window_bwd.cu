@@ -316,8 +316,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
                 float2 x[24], y[24];
                 tmem_ld48x2(ts + b * kDqKeys, tp + b * kDqKeys, (float *)x, (float *)y);
                 tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.dp_free[b]);
+                arrive_first(&sm.dp_free[b], lane);
 #pragma unroll
                 for (int e = 0; e < 24; ++e) {
                     float2 u = ffma2(x[e], cc, ll);
@@ -340,7 +339,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
                 uint32_t pk[24];
 #pragma unroll
                 for (int e = 0; e < 24; ++e) pk[e] = tc::pack_bf2(x[e].x, x[e].y);
-                __syncwarp();
                 delta::tmem_st16(ts + b * kDqKeys, (const float *)pk);
                 tmem_st8(ts + b * kDqKeys + 16, pk + 16);
                 delta::tmem_wait_st();
@@ -351,10 +349,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
                     for (int e = tid; e < rows * 8 * KB; e += kDqCompute)
                         tc::st_shared_v4(k + (e / (8 * rows)) * Lay::kBlock + (nk + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
                     tc::fence_async_smem();
+                    __syncwarp();
                 }
                 tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.ds_full[b]);
+                arrive_first(&sm.ds_full[b], lane);
             }
             if (it.tiles) {
                 wait_warp(&sm.dq_full, ni++ & 1, err);
@@ -667,7 +665,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                     pk[e] = tc::pack_bf2(x[e].x, x[e].y);
                     dk[e] = tc::pack_bf2(y[e].x, y[e].y);
                 }
-                __syncwarp();
                 delta::tmem_st16(ts + 128 * b, (const float *)pk);
                 delta::tmem_st16(ts + 128 * b + 64, (const float *)dk);
                 delta::tmem_wait_st();
@@ -678,10 +675,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                     for (int e = tid; e < rows * 8 * 2 * KB; e += kDkvCompute)
                         tc::st_shared_v4(q + (e / (8 * rows)) * Lay::kBlock + (from + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
                     tc::fence_async_smem();
+                    __syncwarp();
                 }
                 tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[b]);
+                arrive_first(&sm.p_full[b], lane);
                 at.next();
             }
             if (it.tiles) {

@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             if (it.on(i)) {
                 const int tq = live ? t : it.ta[i];
                 bool begun = false;
-                for (int j = 0; j < it.tiles; ++j) {
-                    if (!it.need(i, j)) continue;
+                for (int j = it.tiles_a ? 0 : it.from[i]; j <= it.last[i]; j = j + 1 == it.tiles_a ? it.from[i] : j + 1) {
                     const int s0 = it.start(j), nk = it.count(j);
                     // keys that every row sees: none behind the tile's first token, none in front of its last one's window
                     const bool plain = nk == KEYS && s0 + KEYS - 1 <= it.ta[i] && (s0 > it.ta[i] + T - 1 - p.W || s0 + KEYS <= p.sinks);
@@ -269,8 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     else
                         tmem_ld128(ts, (float *)x);
                     tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.s_free[i]);
+                    arrive_first(&sm.s_free[i], lane);
                     if (!plain) {
                         const int hi = min(nk, tq - s0 + 1), from = tq - p.W + 1 - s0, sk = p.sinks - s0;
 #pragma unroll
@@ -295,31 +293,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                     tc::tc_fence_after();
                     ++ns;
                     const bool grows = top > m && (m == -INFINITY || (top - m) * c > kLazy);
-                    if (!begun) {
-                        m = top;
-                        begun = true;
-                    } else if (__any_sync(0xffffffffu, grows)) {
-                        const float f = grows ? (m == -INFINITY ? 0.f : exp2_approx((m - top) * c)) : 1.f;
-                        if (grows) m = top;
-                        l *= f;
+                    const float f = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
+                    m = grows ? top : m;
+                    l = grows ? l * f : l;
+                    if (begun && __any_sync(0xffffffffu, grows)) {
+                        const float g = grows ? f : 1.f;
                         for (int q = 0; q < (p.P + 15) / 16; ++q) {
                             float o[16];
                             __syncwarp();
                             tc::tmem_ld16(to + 16 * q, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            for (int e = 0; e < 16; ++e) o[e] *= g;
                             delta::tmem_st16(to + 16 * q, o);
                         }
                         delta::tmem_wait_st();
                     }
+                    begun = true;
                     const float ref = m == -INFINITY ? 0.f : -m * c;
                     const float2 cc = make_float2(c, c), rr = make_float2(ref, ref), one = make_float2(1.f, 1.f);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    __syncwarp();
 #pragma unroll
                     for (int q = 0; q < (KEYS + 31) / 32; ++q) {
                         constexpr int kLast = KEYS % 32 ? KEYS % 32 / 2 : 16;  // pairs of the last chunk
-                        if (32 * q >= nk) break;
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -344,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                         for (int e = row; e < rows * 8 * KB; e += 128)
                             tc::st_shared_v4(v + (e / (8 * rows)) * Lay::kBlock + (nk + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
                         tc::fence_async_smem();
+                        __syncwarp();
                     }
                     tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[i]);
+                    arrive_first(&sm.p_full[i], lane);
                 }
                 // the last product: p_free's phase that the next item's first tile waits for too
                 wait_warp(&sm.p_free[i], (ns & 1) ^ 1, err);
