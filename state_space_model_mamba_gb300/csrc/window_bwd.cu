@@ -61,39 +61,6 @@ struct Maps {
     CUtensorMap q, d_o, k, v;
 };
 
-// A warp's 32 rows x 64 columns in bf16 from its stage to rows of global memory, as whole lines: row r of the tile
-// goes to dst + off(r) where r < rows.
-template <class F>
-__device__ __forceinline__ void store_lines(uint32_t stage, int quarter, int lane, bf16 *dst, int rows, int col, int P, F off) {
-    const int c = col + 8 * (lane & 7);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int r = 4 * e + (lane >> 3), rr = 32 * quarter + r;
-        const uint4 y = tc::ld_shared_v4(stage + tc::sw128_chunk(r, lane & 7));
-        if (rr < rows && c < P) *(uint4 *)(dst + off(rr) + c) = y;
-    }
-}
-// Columns [at, at + 64) of a warp's accumulator rows times f, rounded, to the warp's stage; zeros where f is 0 or none is filled.
-__device__ __forceinline__ void stage_rows(uint32_t stage, uint32_t at, int lane, float f, bool filled) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float v[32];
-        if (filled) {
-            __syncwarp();
-            tc::tmem_ld32u(at + 32 * q, (uint32_t *)v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        }
-        uint32_t y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = f != 0.f ? tc::pack_bf2(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            tc::st_shared_v4(stage + tc::sw128_chunk(lane, 4 * q + e), y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-    }
-}
-
 // ------------------------------------------------------------------ dq
 constexpr int kDqCompute = 256, kDqThreads = 384, kDqKeys = 96, kDqK = 3, kDqV = 2;  // slots of the rings of K and V tiles
 template <int KB>
@@ -113,23 +80,7 @@ struct DqBars {
 };
 static_assert(sizeof(DqBars) <= 1024, "barriers");
 
-// A query tile and its keys: tiles [0, tiles_a) are sinks in front of the window, [tiles_a, tiles) the window.
-struct DqItem {
-    int bi, g, V, head, lo, end, tiles_a, tiles, ta;
-    __device__ __forceinline__ DqItem(const WindowParams &p, const Cursor &c, int T) {
-        ta = c.x * T;
-        g = c.g;
-        bi = c.b;
-        V = valid_tokens(p, bi);
-        end = min(ta + T, V);
-        lo = max(0, ta - p.W + 1);
-        head = min(p.sinks, lo);
-        tiles_a = (head + kDqKeys - 1) / kDqKeys;
-        tiles = ta < V ? tiles_a + (end - lo + kDqKeys - 1) / kDqKeys : 0;
-    }
-    __device__ __forceinline__ int start(int j) const { return j < tiles_a ? j * kDqKeys : lo + (j - tiles_a) * kDqKeys; }
-    __device__ __forceinline__ int count(int j) const { return min(kDqKeys, (j < tiles_a ? head : end) - start(j)); }
-};
+using DqItem = QueryItem<kDqKeys>;
 
 // The thread of one of the two products of a pair of tiles: A from `a` (the query tile's rows), B from a ring of SLOTS tiles.
 template <int KB, int SLOTS>
@@ -213,24 +164,28 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
             const uint32_t q_bytes = (uint32_t)(2 * T * R) * 128u * KB;
             Place<kDqK> ak;
             Place<kDqV> av;
-            uint32_t nq = 0, n = 0;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+            uint32_t nq = 0, nk = 0, nv = 0;
+            bool ok = true;
+            for (Cursor cur(items, per_row, p.G); cur.left > 0 && ok; cur.next(per_row, p.G)) {
                 const DqItem it(p, cur, T);
                 if (it.tiles) {
-                    wait_bar(&sm.q_empty, (nq++ & 1) ^ 1, err);
+                    if (!(ok = wait_copy(&sm.q_empty, (nq & 1) ^ 1, err))) break;
+                    ++nq;
                     mbar_arrive_expect_tx(&sm.q_full, q_bytes);
                     for (int kb = 0; kb < KB; ++kb) {
                         tma_tile(base + kb * 16384, &maps.q, &sm.q_full, 64 * kb, it.g * R, it.ta, it.bi);
                         tma_tile(base + Lay::kOffDO + kb * 16384, &maps.d_o, &sm.q_full, 64 * kb, it.g * R, it.ta, it.bi);
                     }
                 }
-                for (int j = 0; j < it.tiles; ++j, ++n) {
-                    wait_bar(&sm.k_empty[ak.slot], ak.phase ^ 1, err);
+                for (int j = 0; j < it.tiles; ++j) {
+                    if (!(ok = wait_copy(&sm.k_empty[ak.slot], ak.phase ^ 1, err))) break;
+                    ++nk;
                     mbar_arrive_expect_tx(&sm.k_full[ak.slot], Lay::kTile);
                     for (int kb = 0; kb < KB; ++kb)
                         tma_tile(base + Lay::kOffK + ak.slot * Lay::kTile + kb * Lay::kBlock, &maps.k, &sm.k_full[ak.slot], 64 * kb, it.g,
                                  it.start(j), it.bi);
-                    wait_bar(&sm.v_empty[av.slot], av.phase ^ 1, err);
+                    if (!(ok = wait_copy(&sm.v_empty[av.slot], av.phase ^ 1, err))) break;
+                    ++nv;
                     mbar_arrive_expect_tx(&sm.v_full[av.slot], Lay::kTile);
                     for (int kb = 0; kb < KB; ++kb)
                         tma_tile(base + Lay::kOffV + av.slot * Lay::kTile + kb * Lay::kBlock, &maps.v, &sm.v_full[av.slot], 64 * kb, it.g,
@@ -239,8 +194,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
                 }
             }
             // copies in flight land before the block ends
-            for (uint32_t x = n > kDqK ? n - kDqK : 0; x < n; ++x) mbar_wait(&sm.k_full[x % kDqK], (x / kDqK) & 1);
-            for (uint32_t x = n > kDqV ? n - kDqV : 0; x < n; ++x) mbar_wait(&sm.v_full[x % kDqV], (x / kDqV) & 1);
+            for (uint32_t x = nk > kDqK ? nk - kDqK : 0; x < nk; ++x) mbar_wait(&sm.k_full[x % kDqK], (x / kDqK) & 1);
+            for (uint32_t x = nv > kDqV ? nv - kDqV : 0; x < nv; ++x) mbar_wait(&sm.v_full[x % kDqV], (x / kDqV) & 1);
             if (nq) mbar_wait(&sm.q_full, (nq - 1) & 1);
         }
         __syncwarp();
@@ -310,7 +265,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
             const float2 cc = make_float2(c, c), ll = make_float2(lse2, lse2), DD = make_float2(D, D), one = make_float2(1.f, 1.f);
             for (int j = 0; j < it.tiles; ++j, ++n) {
                 const int b = n & 1, nk = it.count(j), s0 = it.start(j), mine = s0 + 48 * half;
-                const bool plain = nk == kDqKeys && s0 + kDqKeys - 1 <= it.ta && (s0 > it.ta + T - 1 - p.W || s0 + kDqKeys <= p.sinks);
+                const bool plain = it.plain(p, T, s0, nk);
                 wait_warp(&sm.full[b], (n >> 1) & 1, err);
                 tc::tc_fence_after();
                 float2 x[24], y[24];
@@ -335,6 +290,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
                             x[16 * q + e].y = see >> (2 * e + 1) & 1 ? x[16 * q + e].y : 0.f;
                         }
                     }
+                    __syncwarp();
                 }
                 uint32_t pk[24];
 #pragma unroll
@@ -497,10 +453,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             const uint32_t bytes = (uint32_t)(2 * T * R) * 128u * KB;
             Place<SLOTS> at;
             uint32_t nk = 0, n = 0;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+            bool ok = true;
+            for (Cursor cur(items, per_row, p.G); cur.left > 0 && ok; cur.next(per_row, p.G)) {
                 const DkvItem it(p, cur, T, ktiles, cut);
                 if (it.tiles) {
-                    wait_bar(&sm.kv_empty, (nk++ & 1) ^ 1, err);
+                    if (!(ok = wait_copy(&sm.kv_empty, (nk & 1) ^ 1, err))) break;
+                    ++nk;
                     mbar_arrive_expect_tx(&sm.kv_full, 2 * Lay::kKTile);
                     for (int kb = 0; kb < KB; ++kb) {
                         tma_tile(base + kb * 16384, &maps.k, &sm.kv_full, 64 * kb, it.g, it.k0, it.bi);
@@ -508,7 +466,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                     }
                 }
                 for (int j = 0; j < it.tiles; ++j, ++n) {
-                    wait_bar(&sm.in_empty[at.slot], at.phase ^ 1, err);
+                    if (!(ok = wait_copy(&sm.in_empty[at.slot], at.phase ^ 1, err))) break;
                     mbar_arrive_expect_tx(&sm.in_full[at.slot], bytes);
                     const uint32_t to = base + Lay::kOffRing + at.slot * 2 * Lay::kTile;
                     for (int kb = 0; kb < KB; ++kb) {
@@ -658,6 +616,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                         x[e] = make_float2(a ? x[e].x : 0.f, d ? x[e].y : 0.f);
                         y[e] = make_float2(a ? y[e].x : 0.f, d ? y[e].y : 0.f);
                     }
+                    __syncwarp();
                 }
                 uint32_t pk[16], dk[16];
 #pragma unroll

@@ -63,6 +63,12 @@ __device__ __noinline__ inline void wait_long(uint64_t *bar, uint32_t parity, in
 __device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, int *err) {
     if (!tc::mbar_try_wait(bar, parity)) wait_long(bar, parity, err);
 }
+// The copying threads' wait: false once a wait of the block has given up, and then nothing more is copied (a barrier that
+// nobody waits for would count bytes past its range).
+__device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t parity, int *err) {
+    wait_bar(bar, parity, err);
+    return *(volatile int *)err == 0;
+}
 // The same for whole warps with registers full of values, that a call would have to put away.
 __device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, int *err) {
     if (!tc::mbar_try_wait(bar, parity)) wait_loop(bar, parity, err);
@@ -96,6 +102,28 @@ struct Cursor {
     }
 };
 
+// A query tile of T tokens and its keys in tiles of KEYS: [0, tiles_a) are sinks in front of the window, [tiles_a, tiles) the window.
+template <int KEYS>
+struct QueryItem {
+    int bi, g, V, head, lo, end, tiles_a, tiles, ta;
+    __device__ __forceinline__ QueryItem(const WindowParams &p, const Cursor &c, int T) {
+        ta = c.x * T;
+        g = c.g;
+        bi = c.b;
+        V = valid_tokens(p, bi);
+        end = min(ta + T, V);
+        lo = max(0, ta - p.W + 1);
+        head = min(p.sinks, lo);
+        tiles_a = (head + KEYS - 1) / KEYS;
+        tiles = ta < V ? tiles_a + (end - lo + KEYS - 1) / KEYS : 0;
+    }
+    __device__ __forceinline__ int start(int j) const { return j < tiles_a ? j * KEYS : lo + (j - tiles_a) * KEYS; }
+    __device__ __forceinline__ int count(int j) const { return min(KEYS, (j < tiles_a ? head : end) - start(j)); }
+    // whether every row sees every key of tile j: none behind the first token, none in front of the last one's window
+    __device__ __forceinline__ bool plain(const WindowParams &p, int T, int s0, int nk) const {
+        return nk == KEYS && s0 + KEYS - 1 <= ta && (s0 > ta + T - 1 - p.W || s0 + KEYS <= p.sinks);
+    }
+};
 // A place in a ring of SLOTS and the parity of its phase.
 template <int SLOTS>
 struct Place {
@@ -174,6 +202,39 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// A warp's 32 rows x 64 columns in bf16 from its stage to rows of global memory, as whole lines: row r of the tile
+// goes to dst + off(r) where r < rows.
+template <class F>
+__device__ __forceinline__ void store_lines(uint32_t stage, int quarter, int lane, bf16 *dst, int rows, int col, int P, F off) {
+    const int c = col + 8 * (lane & 7);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int r = 4 * e + (lane >> 3), rr = 32 * quarter + r;
+        const uint4 y = tc::ld_shared_v4(stage + tc::sw128_chunk(r, lane & 7));
+        if (rr < rows && c < P) *(uint4 *)(dst + off(rr) + c) = y;
+    }
+}
+// Columns [at, at + 64) of a warp's accumulator rows times f, rounded, to the warp's stage; zeros where f is 0 or none is filled.
+__device__ __forceinline__ void stage_rows(uint32_t stage, uint32_t at, int lane, float f, bool filled) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float v[32];
+        if (filled) {
+            __syncwarp();
+            tc::tmem_ld32u(at + 32 * q, (uint32_t *)v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+        uint32_t y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = f != 0.f ? tc::pack_bf2(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            tc::st_shared_v4(stage + tc::sw128_chunk(lane, 4 * q + e), y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    }
 }
 
 // Tensor maps of [b, L, heads, P] in bf16, 64 columns (128 bytes, swizzled) x `nheads` heads x `tokens` tokens a box.
