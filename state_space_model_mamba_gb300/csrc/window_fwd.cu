@@ -7,7 +7,7 @@
 // other's softmax, first tiles and last stores (one block with two query tiles that share the copies of
 // their keys came to the end of both at once, and stood still for a fifth of an item).  S and P have columns of their own in
 // a block's half of tensor memory, so that the next S is made as soon as the last one is in registers: 256 columns hold S, P and
-// O with 80 keys a tile where O has 128 columns, and 128 keys where it has 64.
+// O with 80 keys a tile where O has 128 columns, and 96 keys where it has 64.
 // The row maximum is followed lazily: a row's reference only moves, and O is only rescaled, where the maximum
 // has grown by 2^8 over it, so P <= 256 and the passes over O are rare; sums are fp32 and do not care.
 // P is rounded to bf16 (2^-8 of each at most), the sum it is divided by is not.
@@ -38,13 +38,13 @@ struct Maps {
 // KB = ceil(P / 64) blocks of 64 columns a tile.
 template <int KB>
 struct Layout {
-    static constexpr int kKeys = KB == 2 ? 80 : 128;                                           // of a tile
+    static constexpr int kKeys = KB == 2 ? 80 : 96;                                            // of a tile
     // Rings of K and of V tiles, apart: a waiting thread tells a phase of a slot from the next one only, so it has to see
     // every use of the slots it waits for (a ring of three slots for both let S begin on a K that had not landed).
-    static constexpr int kBlock = kKeys * 128, kTile = KB * kBlock, kK = 2, kV = KB == 2 ? 1 : 2;
+    static constexpr int kBlock = kKeys * 128, kTile = KB * kBlock, kK = 2, kV = 2;
     static constexpr int kQTile = KB * 16384;
-    static constexpr int kOffK = kQTile, kOffV = kOffK + kK * kTile, kOffStage = kOffV + kV * kTile;  // stage: 4 warps x 32 rows x 64 columns
-    static constexpr int kOffBars = kOffStage + 4 * 4096, kBytes = kOffBars + 1024;
+    static constexpr int kOffK = kQTile, kOffV = kOffK + kK * kTile;
+    static constexpr int kOffBars = kOffV + kV * kTile, kBytes = kOffBars + 1024;
     static constexpr int kS = 0, kP = kKeys, kO = 256 - 64 * KB;  // columns of tensor memory
     static_assert(kP + kKeys / 2 <= kO, "tensor memory");
     static_assert(2 * (kBytes + 1024) <= 233472, "shared memory of two blocks");
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
         // ---- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int row = tid, R = p.hpg;
-        const uint32_t magic = row_magic(R), stage = base + Lay::kOffStage + warp * 4096;
+        const uint32_t magic = row_magic(R);
         const uint32_t ts = tmem_addr(tm, 32 * warp, Lay::kS), tp = tmem_addr(tm, 32 * warp, Lay::kP), to = tmem_addr(tm, 32 * warp, Lay::kO);
         const int token = row_token(row, magic), head = row - token * R;
         uint32_t ns = 0;  // tiles before
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 else if constexpr (COLS == 80)
                     tmem_ld80(ts, (float *)x);
                 else
-                    tmem_ld128(ts, (float *)x);
+                    tmem_ld96(ts, (float *)x);
                 tc::tc_fence_before();
                 arrive_first(&sm.s_free, lane);
                 if (!plain) {
@@ -246,50 +246,51 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                         }
                     }
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // The exponents are taken with the reference of the tiles before, while the maximum is looked for; where that
+                // has grown too far, which is rare past the first tiles, again with the new one.
+                const float2 cc = make_float2(c, c), one = make_float2(1.f, 1.f);
+                uint32_t pk[COLS / 2];
+                float2 sum[2];
+                for (;;) {
+                    const float ref = m == -INFINITY ? 0.f : -m * c;
+                    const float2 rr = make_float2(ref, ref);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < COLS / 2; ++e) mx[e & 3] = fmaxf(mx[e & 3], fmaxf(x[e].x, x[e].y));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grows = top > m && (m == -INFINITY || (top - m) * c > kLazy);
-                const float f = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
-                m = grows ? top : m;
-                l = grows ? l * f : l;
-                const float ref = m == -INFINITY ? 0.f : -m * c;
-                const float2 cc = make_float2(c, c), rr = make_float2(ref, ref), one = make_float2(1.f, 1.f);
-                // the product with the last P is done: P and O are this thread's
-                wait_warp(&sm.p_free, (ns & 1) ^ 1, err);
-                tc::tc_fence_after();
-                ++ns;
-                if (j > 0 && __any_sync(0xffffffffu, grows)) {
-                    const float g = grows ? f : 1.f;
-                    for (int q = 0; q < (p.P + 15) / 16; ++q) {
-                        float o[16];
-                        __syncwarp();
-                        tc::tmem_ld16(to + 16 * q, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= g;
-                        delta::tmem_st16(to + 16 * q, o);
-                    }
-                    delta::tmem_wait_st();
-                }
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int q = 0; q < (COLS + 31) / 32; ++q) {
-                    constexpr int kLast = COLS % 32 ? COLS % 32 / 2 : 16;  // pairs of the last chunk
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (q == COLS / 32 && e >= kLast) break;
-                        float2 y = ffma2(x[16 * q + e], cc, rr);
+                    for (int e = 0; e < COLS / 2; ++e) {
+                        float2 y = ffma2(x[e], cc, rr);
                         y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                        mx[e & 3] = max3(mx[e & 3], x[e].x, x[e].y);
                         sum[e & 1] = ffma2(y, one, sum[e & 1]);
                         pk[e] = tc::pack_bf2(y.x, y.y);
                     }
-                    if (q == COLS / 32)
-                        tmem_st8(tp + 16 * q, pk);
-                    else
-                        delta::tmem_st16(tp + 16 * q, (const float *)pk);
+                    const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    const bool grows = top > m && (m == -INFINITY || (top - m) * c > kLazy);
+                    if (!__any_sync(0xffffffffu, grows)) break;
+                    const float f = grows ? (m == -INFINITY ? 0.f : exp2_approx((m - top) * c)) : 1.f;
+                    m = grows ? top : m;
+                    l *= f;
+                    if (j > 0) {
+                        wait_warp(&sm.p_free, (ns & 1) ^ 1, err);
+                        tc::tc_fence_after();
+                        for (int q = 0; q < (p.P + 15) / 16; ++q) {
+                            float o[16];
+                            __syncwarp();
+                            tc::tmem_ld16(to + 16 * q, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            delta::tmem_st16(to + 16 * q, o);
+                        }
+                        delta::tmem_wait_st();
+                    }
                 }
+                // the product with the last P is done
+                wait_warp(&sm.p_free, (ns & 1) ^ 1, err);
+                tc::tc_fence_after();
+                ++ns;
+                if constexpr (COLS >= 80) tmem_st32(tp, pk);
+                if constexpr (COLS == 96) delta::tmem_st16(tp + 32, (const float *)(pk + 32));
+                if constexpr (COLS % 32 == 16) tmem_st8(tp + COLS / 2 - 8, pk + COLS / 2 - 8);
                 delta::tmem_wait_st();
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 if (nk & 15) {
@@ -321,19 +322,29 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
             }
             if (in && p.lse) p.lse[((long long)it.bi * p.H + h) * p.L + t] = live ? (m * c + log2f(l)) * kLn2 : 0.f;
             const float inv = live ? 1.f / l : 0.f;
-            // O in bf16, 64 columns at a time through the warp's stage, so that a row leaves as whole lines
-            bf16 *const o = (bf16 *)p.o + (((long long)it.bi * p.L + it.ta) * p.H + it.g * R) * p.P;
-            const int rows = min(T, p.L - it.ta) * R;  // of the tile that there are
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                __syncwarp();
-                stage_rows(stage, to + 64 * kb, lane, inv, it.tiles > 0);
-                if (kb == KB - 1 && it.tiles) {
-                    tc::tc_fence_before();
-                    arrive_first(&sm.o_empty, lane);
+            // O in bf16, a thread its row's next 64 bytes at a time.  The loop stays one: code that runs once an item is fetched from
+            // past the instruction caches, and costs more than what it does.
+            bf16 *const o = (bf16 *)p.o + (((long long)it.bi * p.L + t) * p.H + h) * p.P;
+#pragma unroll 1
+            for (int q = 0; q < p.P; q += 32) {
+                float v[32];
+                if (it.tiles) {
+                    __syncwarp();
+                    tc::tmem_ld32u(to + q, (uint32_t *)v);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (live)
+                        y = make_uint4(tc::pack_bf2(v[8 * e] * inv, v[8 * e + 1] * inv), tc::pack_bf2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                       tc::pack_bf2(v[8 * e + 4] * inv, v[8 * e + 5] * inv), tc::pack_bf2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    if (in && q + 8 * e < p.P) *(uint4 *)(o + q + 8 * e) = y;
+                }
+            }
+            if (it.tiles) {
+                tc::tc_fence_before();
                 __syncwarp();
-                store_lines(stage, warp, lane, o, rows, 64 * kb, p.P, [&](int r) { return row_token(r, magic) * (p.H - R) * p.P + r * p.P; });
+                arrive_first(&sm.o_empty, lane);
             }
         }
     }
