@@ -56,6 +56,13 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
+// 32 bytes to an address that is a multiple of 32: a whole sector, where two stores of 16 bytes would be half ones each
+__device__ __forceinline__ void store32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <int KB>
 __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_constant__ Maps maps, WindowParams p, float c,
                                                                  uint32_t negate, int items, int per_row) {
@@ -325,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
             // O in bf16, a thread its row's next 64 bytes at a time.  The loop stays one: code that runs once an item is fetched from
             // past the instruction caches, and costs more than what it does.
             bf16 *const o = (bf16 *)p.o + (((long long)it.bi * p.L + t) * p.H + h) * p.P;
+            const bool wide = p.P % 16 == 0 && ((uintptr_t)p.o & 31) == 0;
 #pragma unroll 1
             for (int q = 0; q < p.P; q += 32) {
                 float v[32];
@@ -332,13 +340,16 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                     __syncwarp();
                     tc::tmem_ld32u(to + q, (uint32_t *)v);
                 }
+                uint32_t y[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                    if (live)
-                        y = make_uint4(tc::pack_bf2(v[8 * e] * inv, v[8 * e + 1] * inv), tc::pack_bf2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                       tc::pack_bf2(v[8 * e + 4] * inv, v[8 * e + 5] * inv), tc::pack_bf2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
-                    if (in && q + 8 * e < p.P) *(uint4 *)(o + q + 8 * e) = y;
+                for (int e = 0; e < 16; ++e) y[e] = live ? tc::pack_bf2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+                if (wide) {
+                    if (in && q < p.P) store32(o + q, y);
+                    if (in && q + 16 < p.P) store32(o + q + 16, y + 8);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (in && q + 8 * e < p.P) *(uint4 *)(o + q + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                 }
             }
             if (it.tiles) {
