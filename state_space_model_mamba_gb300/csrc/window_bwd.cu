@@ -91,7 +91,7 @@ __device__ __forceinline__ void dq_scores(const WindowParams &p, int items, int 
     const uint32_t idesc0 = tc::idesc_bf16(128, 0, false, false);
     Place<SLOTS> at;
     uint32_t nq = 0, n = 0;
-    for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+    for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
         const DqItem it(p, cur, T);
         if (it.tiles) wait_bar(&sm.q_full, nq++ & 1, &sm.err);
         for (int j = 0; j < it.tiles; ++j, ++n) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
             Place<kDqV> av;
             uint32_t nq = 0, nk = 0, nv = 0;
             bool ok = true;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0 && ok; cur.next(per_row, p.G)) {
+            for (Cursor cur(items, per_row, p); cur.left > 0 && ok; cur.next()) {
                 const DqItem it(p, cur, T);
                 if (it.tiles) {
                     if (!(ok = wait_copy(&sm.q_empty, (nq & 1) ^ 1, err))) break;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
             const uint64_t d_k = tc::sdesc(base + Lay::kOffK, Lay::kBlock, 1024);
             Place<kDqK> at;
             uint32_t ni = 0, n = 0;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+            for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
                 const DqItem it(p, cur, T);
                 for (int j = 0; j < it.tiles; ++j, ++n) {
                     if (j == 0) wait_bar(&sm.dq_empty, (ni++ & 1) ^ 1, err);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) window_dq_kernel(const __grid_c
         const int token = row_token(row, magic), head = row - token * R;
         const float c = p.scale * kLog2e;
         uint32_t n = 0, ni = 0;
-        for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+        for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
             const DqItem it(p, cur, T);
             const int t = it.ta + token, h = it.g * R + head;
             const bool live = row < T * R && t < it.V;
@@ -381,21 +381,29 @@ __host__ __device__ inline size_t sink_floats(const SinkCut &c, long long groups
     return c.segments ? (size_t)groups * c.tiles * (c.segments + 1) * 2 * 128 * P : 0;
 }
 
-// 128 keys from k0 and the query tokens [tb, te) that see them.
+// 128 keys from k0 and the query tokens [tb, te) that see them: first the sinks' segments, then the rows' tiles, every row's first
+// before any other, so that those at a row's end, which fewer tokens see, come last.
 struct DkvItem {
     int bi, g, V, k0, tb, te, tiles, part;  // part: the sinks' share that this is, or -1
-    __device__ __forceinline__ DkvItem(const WindowParams &p, const Cursor &c, int T, int ktiles, const SinkCut &cut) {
-        g = c.g;
-        bi = c.b;
+    __device__ __forceinline__ DkvItem(const WindowParams &p, int index, int T, const SinkCut &cut) {
+        const int rows = p.b * p.G, sinks = rows * cut.tiles * cut.segments;
+        int tile, segment = 0, row;
+        if (index < sinks) {
+            row = index % rows;
+            tile = index / rows / cut.segments;
+            segment = index / rows % cut.segments + 1;
+        } else {
+            row = (index - sinks) % rows;
+            tile = (index - sinks) / rows;
+        }
+        g = row % p.G;
+        bi = row / p.G;
         V = valid_tokens(p, bi);
-        int tile = c.x, segment = 0;
-        if (c.x < ktiles) {
-            k0 = tb = 128 * c.x;
+        k0 = 128 * tile;
+        if (segment == 0) {
+            tb = k0;
             te = min(V, k0 + 127 + p.W);
         } else {
-            tile = (c.x - ktiles) / cut.segments;
-            segment = (c.x - ktiles) % cut.segments + 1;
-            k0 = 128 * tile;
             const long long from = k0 + 127ll + p.W + (segment - 1ll) * cut.length;
             tb = (int)min(from, (long long)V);
             te = (int)min(from + cut.length, (long long)V);
@@ -407,7 +415,7 @@ struct DkvItem {
 
 template <int KB>
 __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid_constant__ Maps maps, WindowParams p, SinkCut cut, float *parts,
-                                                                    int items, int per_row, int ktiles) {
+                                                                    int items) {
     using Lay = DkvLayout<KB>;
     constexpr int SLOTS = Lay::kSlots;
     extern __shared__ __align__(1024) char smem_raw[];
@@ -454,8 +462,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             Place<SLOTS> at;
             uint32_t nk = 0, n = 0;
             bool ok = true;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0 && ok; cur.next(per_row, p.G)) {
-                const DkvItem it(p, cur, T, ktiles, cut);
+            for (int index = blockIdx.x; index < items && ok; index += gridDim.x) {
+                const DkvItem it(p, index, T, cut);
                 if (it.tiles) {
                     if (!(ok = wait_copy(&sm.kv_empty, (nk & 1) ^ 1, err))) break;
                     ++nk;
@@ -490,8 +498,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             const uint64_t d_a = tc::sdesc(base + second * Lay::kOffV, 16, 1024), d_b = tc::sdesc(base + Lay::kOffRing + second * Lay::kTile, 16, 1024);
             Place<SLOTS> at;
             uint32_t nk = 0, n = 0;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
-                const DkvItem it(p, cur, T, ktiles, cut);
+            for (int index = blockIdx.x; index < items; index += gridDim.x) {
+                const DkvItem it(p, index, T, cut);
                 if (it.tiles) wait_bar(&sm.kv_full, nk++ & 1, err);
                 for (int j = 0; j < it.tiles; ++j, ++n) {
                     wait_bar(&sm.in_full[at.slot], at.phase, err);
@@ -519,8 +527,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             const uint64_t d_q = tc::sdesc(base + Lay::kOffRing, Lay::kBlock, 1024);
             Place<SLOTS> at;
             uint32_t ni = 0, n = 0;
-            for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
-                const DkvItem it(p, cur, T, ktiles, cut);
+            for (int index = blockIdx.x; index < items; index += gridDim.x) {
+                const DkvItem it(p, index, T, cut);
                 for (int j = 0; j < it.tiles; ++j, ++n) {
                     if (j == 0) wait_bar(&sm.acc_empty, (ni++ & 1) ^ 1, err);
                     wait_bar(&sm.p_full[n & 1], (n >> 1) & 1, err);
@@ -552,8 +560,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
         // ---- the rows' statistics: -lse log2(e) (so low where there is no row that p is 0) and -D
         const uint32_t magic = row_magic(R);
         Place<SLOTS> at;
-        for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
-            const DkvItem it(p, cur, T, ktiles, cut);
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const DkvItem it(p, index, T, cut);
             for (int j = 0; j < it.tiles; ++j) {
                 float ll[2] = {-INFINITY, -INFINITY}, dd[2] = {0.f, 0.f};
 #pragma unroll
@@ -582,8 +590,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
         const float2 cc = make_float2(c, c);
         Place<SLOTS> at;
         uint32_t n = 0, ni = 0;
-        for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
-            const DkvItem it(p, cur, T, ktiles, cut);
+        for (int index = blockIdx.x; index < items; index += gridDim.x) {
+            const DkvItem it(p, index, T, cut);
             const int s = it.k0 + key;
             for (int j = 0; j < it.tiles; ++j, ++n) {
                 const int b = n & 1, t0 = it.tb + j * T;
@@ -730,13 +738,13 @@ cudaError_t backward(const WindowParams &p, float *parts, cudaStream_t s) {
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const SinkCut cut = sink_cut(p.L, p.W, p.sinks);
-    const int T = kDkvRows / p.hpg, ktiles = (p.L + 127) / 128, per_row = ktiles + cut.tiles * cut.segments, items = per_row * p.G * p.b;
+    const int T = kDkvRows / p.hpg, items = ((p.L + 127) / 128 + cut.tiles * cut.segments) * p.G * p.b;
     if ((e = map_tokens(&maps.q, p.q, p, p.H, p.hpg, T)) != cudaSuccess) return e;
     if ((e = delta::same_tiles(&maps.d_o, maps.q, p.d_o)) != cudaSuccess) return e;
     if ((e = map_tokens(&maps.k, p.k, p, p.G, 1, 128)) != cudaSuccess) return e;
     if ((e = delta::same_tiles(&maps.v, maps.k, p.v)) != cudaSuccess) return e;
     if ((e = delta::allow_shared((const void *)window_dkv_kernel<KB>, DkvLayout<KB>::kBytes)) != cudaSuccess) return e;
-    window_dkv_kernel<KB><<<items < kSMs ? items : kSMs, kDkvThreads, DkvLayout<KB>::kBytes, s>>>(maps, p, cut, parts, items, per_row, ktiles);
+    window_dkv_kernel<KB><<<items < kSMs ? items : kSMs, kDkvThreads, DkvLayout<KB>::kBytes, s>>>(maps, p, cut, parts, items);
     if ((e = cudaGetLastError()) != cudaSuccess || !cut.segments) return e;
     const long long n = (long long)p.b * p.G * 2 * 128 * cut.tiles * (p.P / 4);
     window_sinks_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, cut, parts, n);

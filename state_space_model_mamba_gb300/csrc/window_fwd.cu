@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 Place<Lay::kV> av;
                 uint32_t nq = 0, nk = 0, nv = 0;
                 bool ok = true;
-                for (Cursor cur(items, per_row, p.G); cur.left > 0 && ok; cur.next(per_row, p.G)) {
+                for (Cursor cur(items, per_row, p); cur.left > 0 && ok; cur.next()) {
                     const It it(p, cur, T);
                     auto load_k = [&](int j) {
                         if (!(ok = wait_copy(&sm.k_empty[ak.slot], ak.phase ^ 1, err))) return;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 const uint64_t d_q = tc::sdesc(base, 16, 1024), d_k = tc::sdesc(base + Lay::kOffK, 16, 1024);
                 Place<Lay::kK> at;
                 uint32_t nq = 0, ns = 0;
-                for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+                for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
                     const It it(p, cur, T);
                     if (it.tiles) wait_bar(&sm.q_full, nq++ & 1, err);
                     for (int j = 0; j < it.tiles; ++j, ++ns) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 const uint64_t d_v = tc::sdesc(base + Lay::kOffV, Lay::kBlock, 1024);
                 Place<Lay::kV> at;
                 uint32_t no = 0, np = 0;
-                for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+                for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
                     const It it(p, cur, T);
                     if (it.tiles) wait_bar(&sm.o_empty, (no++ & 1) ^ 1, err);
                     for (int j = 0; j < it.tiles; ++j, ++np) {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
         const uint32_t ts = tmem_addr(tm, 32 * warp, Lay::kS), tp = tmem_addr(tm, 32 * warp, Lay::kP), to = tmem_addr(tm, 32 * warp, Lay::kO);
         const int token = row_token(row, magic), head = row - token * R;
         uint32_t ns = 0;  // tiles before
-        for (Cursor cur(items, per_row, p.G); cur.left > 0; cur.next(per_row, p.G)) {
+        for (Cursor cur(items, per_row, p); cur.left > 0; cur.next()) {
             const It it(p, cur, T);
             const int t = it.ta + token, h = it.g * R + head;
             const bool in = row < T * R && t < p.L, live = in && t < it.V;

@@ -86,19 +86,21 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar, int lane) {
         : "memory");
 }
 
-// The items (batch row, key group, place in the row) of a block: from the block's number on in steps of the grid, without
-// divisions after the first.
+// The query tiles (place x in the row, key group g, batch row b) of a block: numbers blockIdx.x, + gridDim.x, ... of all of them, counted
+// from the rows' ends, every row's last tile before any other: rows advance together, so their windows stay in the L2
+// cache, and the tiles at a row's start, which see few keys, come last, where blocks run out of work.  No divisions after the first.
 struct Cursor {
-    int x, g, b, dx, dg, db, left;
-    __device__ __forceinline__ Cursor(int items, int per_row, int G) {
-        x = blockIdx.x % per_row, g = blockIdx.x / per_row % G, b = blockIdx.x / per_row / G;
-        dx = gridDim.x % per_row, dg = gridDim.x / per_row % G, db = gridDim.x / per_row / G;
+    int x, g, b, dx, dg, db, G, B, left;
+    __device__ __forceinline__ Cursor(int items, int per_row, const WindowParams &p) : G(p.G), B(p.b) {
+        const int rows = G * B;
+        x = per_row - 1 - (int)blockIdx.x / rows, g = blockIdx.x % rows % G, b = blockIdx.x % rows / G;
+        dx = gridDim.x / rows, dg = gridDim.x % rows % G, db = gridDim.x % rows / G;
         left = (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;
     }
-    __device__ __forceinline__ void next(int per_row, int G) {
-        x += dx, g += dg, b += db, --left;
-        if (x >= per_row) x -= per_row, ++g;
+    __device__ __forceinline__ void next() {
+        x -= dx, g += dg, b += db, --left;
         if (g >= G) g -= G, ++b;
+        if (b >= B) b -= B, --x;
     }
 };
 
