@@ -355,7 +355,7 @@ struct DkvLayout {
     static_assert(kBytes <= 232448, "shared memory");
 };
 struct DkvBars {
-    uint64_t kv_full, kv_empty, full[2], p_full[2], free[2], acc_full, acc_empty, drain, in_full[6], in_empty[6], stats_full[6];
+    uint64_t kv_full, kv_empty, s_full[2], dp_full[2], p_full[2], dx_full[2], s_free[2], dp_free[2], acc_full, acc_empty, drain, in_full[6], in_empty[6], stats_full[6];
     uint32_t tmem;
     int err;
 };
@@ -424,20 +424,23 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         mbar_init(&sm.kv_full, 1);
-        mbar_init(&sm.kv_empty, 1);
+        mbar_init(&sm.kv_empty, 2);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sm.full[b], 2);  // S^T and dP^T
+            mbar_init(&sm.s_full[b], 1);
+            mbar_init(&sm.dp_full[b], 1);
             mbar_init(&sm.p_full[b], 8);
-            mbar_init(&sm.free[b], 1);
+            mbar_init(&sm.dx_full[b], 8);
+            mbar_init(&sm.s_free[b], 1);
+            mbar_init(&sm.dp_free[b], 1);
         }
-        mbar_init(&sm.acc_full, 1);
+        mbar_init(&sm.acc_full, 2);  // dV and dK
         mbar_init(&sm.acc_empty, 8);
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&sm.in_full[i], 1);
-            mbar_init(&sm.in_empty[i], 1);
+            mbar_init(&sm.in_empty[i], 2);  // dV and dK, which come behind S^T and dP^T
             mbar_init(&sm.stats_full[i], 1);
         }
-        mbar_init(&sm.drain, 3);
+        mbar_init(&sm.drain, 4);
         tc::mbar_fence_init();
         sm.err = 0;
     }
@@ -496,6 +499,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             const uint32_t idesc = tc::idesc_bf16(128, kDkvRows, false, false);
             const int ksteps = (p.P + 15) / 16;
             const uint64_t d_a = tc::sdesc(base + second * Lay::kOffV, 16, 1024), d_b = tc::sdesc(base + Lay::kOffRing + second * Lay::kTile, 16, 1024);
+            uint64_t *const full = second ? sm.dp_full : sm.s_full, *const free = second ? sm.dp_free : sm.s_free;
             Place<SLOTS> at;
             uint32_t nk = 0, n = 0;
             for (int index = blockIdx.x; index < items; index += gridDim.x) {
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                 if (it.tiles) wait_bar(&sm.kv_full, nk++ & 1, err);
                 for (int j = 0; j < it.tiles; ++j, ++n) {
                     wait_bar(&sm.in_full[at.slot], at.phase, err);
-                    wait_bar(&sm.free[n & 1], ((n >> 1) & 1) ^ 1, err);
+                    wait_bar(&free[n & 1], ((n >> 1) & 1) ^ 1, err);
                     tc::tc_fence_after();
                     const uint64_t b = delta::sdesc_add(d_b, at.slot * 2 * Lay::kTile);
                     const uint32_t d = tm + 128 * (n & 1) + 64 * second;
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                         if (ks < ksteps)
                             tc::mma_bf16(d, delta::sdesc_add(d_a, (ks >> 2) * 16384 + (ks & 3) * 32),
                                          delta::sdesc_add(b, (ks >> 2) * Lay::kBlock + (ks & 3) * 32), idesc, ks > 0);
-                    tc::mma_commit(&sm.full[n & 1]);
+                    tc::mma_commit(&full[n & 1]);
                     at.next();
                 }
             }
@@ -520,30 +524,27 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
             mbar_wait(&sm.drain, 0);
         }
         __syncwarp();
-    } else if (warp == kDkvCompute / 32 + 3) {
-        // ---- dV += P^T dO, dK += dX^T Q
+    } else if (warp == kDkvCompute / 32 + 3 || warp == kDkvCompute / 32 + 5) {
+        // ---- dV += P^T dO (first thread), dK += dX^T Q (second)
         if (elect()) {
-            const uint32_t idesc = tc::idesc_bf16(128, (p.P + 15) / 16 * 16, false, true);
-            const uint64_t d_q = tc::sdesc(base + Lay::kOffRing, Lay::kBlock, 1024);
+            const uint32_t second = warp == kDkvCompute / 32 + 5;
+            const uint32_t idesc = tc::idesc_bf16(128, (p.P + 15) / 16 * 16, false, true), to = tm + (second ? Lay::kDK : Lay::kDV);
+            const uint64_t d_b = tc::sdesc(base + Lay::kOffRing + (second ? 0 : Lay::kTile), Lay::kBlock, 1024);
+            uint64_t *const in = second ? sm.dx_full : sm.p_full, *const free = second ? sm.dp_free : sm.s_free;
             Place<SLOTS> at;
             uint32_t ni = 0, n = 0;
             for (int index = blockIdx.x; index < items; index += gridDim.x) {
                 const DkvItem it(p, index, T, cut);
                 for (int j = 0; j < it.tiles; ++j, ++n) {
                     if (j == 0) wait_bar(&sm.acc_empty, (ni++ & 1) ^ 1, err);
-                    wait_bar(&sm.p_full[n & 1], (n >> 1) & 1, err);
+                    wait_bar(&in[n & 1], (n >> 1) & 1, err);
                     tc::tc_fence_after();
-                    const uint64_t q = delta::sdesc_add(d_q, at.slot * 2 * Lay::kTile);
-                    const uint32_t a = tm + 128 * (n & 1);
+                    const uint64_t b = delta::sdesc_add(d_b, at.slot * 2 * Lay::kTile);
+                    const uint32_t a = tm + 128 * (n & 1) + 64 * second;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)  // the second 32 rows' p starts where their scores did
-                        tc::mma_bf16_tmem_a(tm + Lay::kDV, a + (ks & 2) * 16 + (ks & 1) * 8, delta::sdesc_add(q, Lay::kTile + ks * 2048), idesc,
-                                            j > 0 || ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc::mma_bf16_tmem_a(tm + Lay::kDK, a + 64 + (ks & 2) * 16 + (ks & 1) * 8, delta::sdesc_add(q, ks * 2048), idesc,
-                                            j > 0 || ks > 0);
-                    tc::mma_commit(&sm.free[n & 1]);
+                    for (int ks = 0; ks < 4; ++ks)  // the second 32 rows' values start where their scores did
+                        tc::mma_bf16_tmem_a(to, a + (ks & 2) * 16 + (ks & 1) * 8, delta::sdesc_add(b, ks * 2048), idesc, j > 0 || ks > 0);
+                    tc::mma_commit(&free[n & 1]);
                     tc::mma_commit(&sm.in_empty[at.slot]);
                     if (j == it.tiles - 1) {
                         tc::mma_commit(&sm.kv_empty);
@@ -597,55 +598,69 @@ __global__ void __launch_bounds__(kDkvThreads, 1) window_dkv_kernel(const __grid
                 const int b = n & 1, t0 = it.tb + j * T;
                 const bool plain = it.k0 + 127 <= t0 && (t0 + T - 1 - it.k0 < p.W || it.k0 + 128 <= p.sinks) && t0 + T <= it.V;
                 wait_warp(&sm.stats_full[at.slot], at.phase, err);
-                wait_warp(&sm.full[b], (n >> 1) & 1, err);
+                wait_warp(&sm.s_full[b], (n >> 1) & 1, err);
                 tc::tc_fence_after();
                 float2 x[16], y[16];
-                tmem_ld32x2(ts + 128 * b, ts + 128 * b + 64, (float *)x, (float *)y);
+                uint32_t pk[16], see = 0xffffffffu;
+                tc::tmem_ld32u(ts + 128 * b, (uint32_t *)x);
                 const uint32_t st = base + Lay::kOffStats + at.slot * 512 + half * 128;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint4 l4 = tc::ld_shared_v4(st + 16 * e), d4 = tc::ld_shared_v4(st + 256 + 16 * e);
+                    const uint4 l4 = tc::ld_shared_v4(st + 16 * e);
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        const float2 ll = make_float2(__uint_as_float(z ? l4.z : l4.x), __uint_as_float(z ? l4.w : l4.y)),
-                                     dd = make_float2(__uint_as_float(z ? d4.z : d4.x), __uint_as_float(z ? d4.w : d4.y));
-                        float2 u = ffma2(x[2 * e + z], cc, ll);
-                        u = make_float2(exp2_approx(u.x), exp2_approx(u.y));
-                        x[2 * e + z] = u;
-                        y[2 * e + z] = fmul2(u, ffma2(y[2 * e + z], make_float2(1.f, 1.f), dd));
+                        const float2 ll = make_float2(__uint_as_float(z ? l4.z : l4.x), __uint_as_float(z ? l4.w : l4.y));
+                        const float2 u = ffma2(x[2 * e + z], cc, ll);
+                        x[2 * e + z] = make_float2(exp2_approx(u.x), exp2_approx(u.y));
                     }
                 }
                 if (!plain) {
                     const int first = max(0, s - t0) * R, last = min(it.te - t0, s < p.sinks ? T : min(T, s + p.W - t0)) * R;
-                    const uint32_t see = bits_between(first - 32 * half, last - 32 * half);
+                    see = bits_between(first - 32 * half, last - 32 * half);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const bool a = see >> (2 * e) & 1, d = see >> (2 * e + 1) & 1;
-                        x[e] = make_float2(a ? x[e].x : 0.f, d ? x[e].y : 0.f);
-                        y[e] = make_float2(a ? y[e].x : 0.f, d ? y[e].y : 0.f);
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = make_float2(see & (1u << (2 * e)) ? x[e].x : 0.f, see & (2u << (2 * e)) ? x[e].y : 0.f);
+                    if (t0 + T > it.V) {
+                        // rows of absent tokens: their p and dx are 0, so q and do have to be finite (dP^T has read them)
+                        wait_warp(&sm.dp_full[b], (n >> 1) & 1, err);
+                        const int from = (it.V - t0) * R, rows = T * R - from;
+                        const uint32_t q = base + Lay::kOffRing + at.slot * 2 * Lay::kTile;
+                        for (int e = tid; e < rows * 8 * 2 * KB; e += kDkvCompute)
+                            tc::st_shared_v4(q + (e / (8 * rows)) * Lay::kBlock + (from + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
+                        tc::fence_async_smem();
                     }
                     __syncwarp();
                 }
-                uint32_t pk[16], dk[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    pk[e] = tc::pack_bf2(x[e].x, x[e].y);
-                    dk[e] = tc::pack_bf2(y[e].x, y[e].y);
-                }
+                for (int e = 0; e < 16; ++e) pk[e] = tc::pack_bf2(x[e].x, x[e].y);
                 delta::tmem_st16(ts + 128 * b, (const float *)pk);
-                delta::tmem_st16(ts + 128 * b + 64, (const float *)dk);
                 delta::tmem_wait_st();
-                if (t0 + T > it.V) {
-                    // rows of absent tokens: their p and dx are 0, so q and do have to be finite
-                    const int from = (it.V - t0) * R, rows = T * R - from;
-                    const uint32_t q = base + Lay::kOffRing + at.slot * 2 * Lay::kTile;
-                    for (int e = tid; e < rows * 8 * 2 * KB; e += kDkvCompute)
-                        tc::st_shared_v4(q + (e / (8 * rows)) * Lay::kBlock + (from + e / 8 % rows) * 128 + (e & 7) * 16, 0, 0, 0, 0);
-                    tc::fence_async_smem();
-                    __syncwarp();
-                }
                 tc::tc_fence_before();
                 arrive_first(&sm.p_full[b], lane);
+                wait_warp(&sm.dp_full[b], (n >> 1) & 1, err);
+                tc::tc_fence_after();
+                tc::tmem_ld32u(ts + 128 * b + 64, (uint32_t *)y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 d4 = tc::ld_shared_v4(st + 256 + 16 * e);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const float2 dd = make_float2(__uint_as_float(z ? d4.z : d4.x), __uint_as_float(z ? d4.w : d4.y));
+                        y[2 * e + z] = fmul2(x[2 * e + z], ffma2(y[2 * e + z], make_float2(1.f, 1.f), dd));
+                    }
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = make_float2(see & (1u << (2 * e)) ? y[e].x : 0.f, see & (2u << (2 * e)) ? y[e].y : 0.f);
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = tc::pack_bf2(y[e].x, y[e].y);
+                delta::tmem_st16(ts + 128 * b + 64, (const float *)pk);
+                delta::tmem_wait_st();
+                tc::tc_fence_before();
+                arrive_first(&sm.dx_full[b], lane);
                 at.next();
             }
             if (it.tiles) {
