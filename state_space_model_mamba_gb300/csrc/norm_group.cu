@@ -82,6 +82,24 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
 template <int TPR>
 constexpr int kBlock = TPR < 256 ? 256 : TPR;
 
+// Blocks of an SM: what the registers of short rows allow, and for long ones that many threads.
+template <int TPR, int NV, int VEC>
+constexpr int kFwdBlocks = kBlock<TPR> == 256 ? (NV == 1 ? 4 : 2) : (kBlock<TPR> == 512 && NV == 1 ? 2 : 1);
+template <int TPR, int NV, int VEC>
+constexpr int kBwdBlocks = kBlock<TPR> == 256 && NV == 1 ? 2 : 1;
+
+// The gate's place, known to the compiler for short rows, whose kernels are bound by their instructions (16384 x 5120 in heads of
+// 64: 89 us with the place looked up, 83 us known; backward 170 and 139, with three rows ahead).
+constexpr int kNoGate = 0, kGateAfter = 1, kGateFirst = 2, kAnyGate = 3;
+template <int MODE>
+__device__ __forceinline__ bool gated(const GroupArgs &a) {
+    return MODE == kAnyGate ? a.gate != nullptr : MODE != kNoGate;
+}
+template <int MODE>
+__device__ __forceinline__ bool gate_first(const GroupArgs &a) {
+    return MODE == kAnyGate ? a.first : MODE == kGateFirst;
+}
+
 // What both kernels hold of a short row: vectors j of thread t at columns (j TPR + t) VEC.
 template <int VEC, int TPR, int NV>
 struct Place {
@@ -159,8 +177,8 @@ __device__ __forceinline__ float normalise(float2 (&u)[NV][PAIRS], const GroupAr
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
+template <typename T, int VEC, int TPR, int NV, int MODE>
+__global__ void __launch_bounds__(kBlock<TPR>, kFwdBlocks<TPR, NV, VEC>) group_norm_kernel(GroupArgs a) {
     __shared__ float buf[2][32][1];
     constexpr int PAIRS = Vec<T, VEC>::PAIRS;
     const Place<VEC, TPR, NV> at;
@@ -176,19 +194,24 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
             if (a.bias) b[j].load(a.bias + off + at.col(j));
         }
     }
+    // columns outside stay 0; past the last row the row before stays, and nothing is made of it
     Vec<T, VEC> x[NV], z[NV];
-    auto load = [&](long long row) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            x[j].zero();
-            z[j].zero();
-            if (row < a.rows && at.col(j) < a.w) {
-                x[j].template load<true>((const T *)a.x + row * a.w + at.col(j));
-                if (a.gate) z[j].template load<true>((const T *)a.gate + row * a.w + at.col(j));
-            }
-        }
+    for (int j = 0; j < NV; ++j) x[j].zero(), z[j].zero();
+    const T *px = (const T *)a.x + at.mine * a.w, *pz = (const T *)a.gate + at.mine * a.w;
+    const long long move = at.step * a.w;
+    auto load = [&](long long row) {
+        if (row < a.rows)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (at.col(j) < a.w) {
+                    x[j].template load<true>(px + at.col(j));
+                    if (gated<MODE>(a)) z[j].template load<true>(pz + at.col(j));
+                }
+        px += move, pz += move;
     };
     load(at.mine);
+    T *py = (T *)a.y + at.mine * a.w;
     for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
         float2 u[NV][PAIRS], s[NV][PAIRS];  // s: what the normed value is multiplied with
 #pragma unroll
@@ -196,8 +219,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
                 u[j][i] = x[j].get(i);
-                if (a.gate) s[j][i] = act2<T>(a.act, z[j].get(i));
-                if (a.first) u[j][i] = fmul2(u[j][i], s[j][i]);
+                if (gated<MODE>(a)) s[j][i] = act2<T>(a.act, z[j].get(i));
+                if (gate_first<MODE>(a)) u[j][i] = fmul2(u[j][i], s[j][i]);
             }
         load(row + at.step);
         normalise(u, a, at, buf, turn);
@@ -209,20 +232,21 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_kernel(GroupArgs a) {
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) {
                     float2 v = ffma2(u[j][i], w[j].get(i), b[j].get(i));
-                    if (!a.gate)
+                    if (!gated<MODE>(a))
                         v = act2<T>(a.act, v);
-                    else if (!a.first)
+                    else if (!gate_first<MODE>(a))
                         v = fmul2(v, s[j][i]);
                     y.set(i, v);
                 }
-                y.store((T *)a.y + row * a.w + at.col(j));
+                y.store(py + at.col(j));
             }
+        py += move;
     }
 }
 
 // ------------------------------------------------------------------ backward
-template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a) {
+template <typename T, int VEC, int TPR, int NV, int MODE>
+__global__ void __launch_bounds__(kBlock<TPR>, kBwdBlocks<TPR, NV, VEC>) group_norm_bwd_kernel(GroupArgs a) {
     __shared__ float buf[2][32][1], buf2[2][32][2];
     constexpr int PAIRS = Vec<T, VEC>::PAIRS;
     const Place<VEC, TPR, NV> at;
@@ -241,23 +265,35 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) dw[j][i] = db[j][i] = make_float2(0.f, 0.f);
     }
-    Vec<T, VEC> x[NV], z[NV], dy[NV];
-    auto load = [&](long long row) {
+    // columns outside stay 0; past the last row dy is 0, so that nothing is added to the weights' gradients
+    constexpr int A = TPR <= 32 && NV == 1 && VEC > 1 ? 3 : 1;  // rows ahead of the one in work
+    Vec<T, VEC> xs[A][NV], zs[A][NV], dys[A][NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            x[j].zero();
-            z[j].zero();
-            dy[j].zero();
-            if (row < a.rows && at.col(j) < a.w) {
-                x[j].template load<true>((const T *)a.x + row * a.w + at.col(j));
-                dy[j].template load<true>((const T *)a.dy + row * a.w + at.col(j));
-                if (a.gate) z[j].template load<true>((const T *)a.gate + row * a.w + at.col(j));
+    for (int k = 0; k < A; ++k)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) xs[k][j].zero(), zs[k][j].zero(), dys[k][j].zero();
+    const T *px = (const T *)a.x + at.mine * a.w, *pz = (const T *)a.gate + at.mine * a.w, *pdy = (const T *)a.dy + at.mine * a.w;
+    const long long move = at.step * a.w;
+    auto load = [&](long long row, Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV], Vec<T, VEC>(&dy)[NV]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (at.col(j) < a.w) {
+                if (row < a.rows) {
+                    x[j].template load<true>(px + at.col(j));
+                    dy[j].template load<true>(pdy + at.col(j));
+                    if (gated<MODE>(a)) z[j].template load<true>(pz + at.col(j));
+                } else {
+                    dy[j].zero();
+                }
             }
-        }
+        px += move, pz += move, pdy += move;
     };
-    load(at.mine);
+#pragma unroll
+    for (int k = 0; k < A; ++k) load(at.mine + k * at.step, xs[k], zs[k], dys[k]);
+    T *pdx = (T *)a.dx + at.mine * a.w, *pdz = (T *)a.dgate + at.mine * a.w;
     const float inv = 1.f / (float)a.w;
-    for (long long row = at.mine, base = row - threadIdx.x / TPR; base < a.rows; row += at.step, base += at.step) {
+    long long row = at.mine;
+    auto one = [&](Vec<T, VEC>(&x)[NV], Vec<T, VEC>(&z)[NV], Vec<T, VEC>(&dy)[NV]) {
         // u, then n;  g the gradient of y;  s the gate's activation, d what dgate is multiplied with
         float2 u[NV][PAIRS], g[NV][PAIRS], s[NV][PAIRS], d[NV][PAIRS];
 #pragma unroll
@@ -267,9 +303,9 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                 const float2 v = x[j].get(i);
                 g[j][i] = dy[j].get(i);
                 u[j][i] = v;
-                if (a.gate) {
+                if (gated<MODE>(a)) {
                     act2<T>(a.act, z[j].get(i), s[j][i], d[j][i]);
-                    if (a.first) {
+                    if (gate_first<MODE>(a)) {
                         u[j][i] = fmul2(v, s[j][i]);
                         d[j][i] = fmul2(d[j][i], v);
                     } else {
@@ -278,7 +314,7 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
                     }
                 }
             }
-        load(row + at.step);
+        load(row + A * at.step, x, z, dy);
         const float rstd = normalise(u, a, at, buf, turn);
         float2 t1 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
         const bool live = row < a.rows;
@@ -287,11 +323,11 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
                 const float2 y = ffma2(u[j][i], w[j].get(i), b[j].get(i));
-                if (!a.gate) {
+                if (!gated<MODE>(a)) {
                     float2 act, slope;
                     act2<T>(a.act, y, act, slope);
                     g[j][i] = fmul2(g[j][i], slope);
-                } else if (!a.first) {
+                } else if (!gate_first<MODE>(a)) {
                     d[j][i] = fmul2(d[j][i], y);  // dgate
                 }
                 dw[j][i] = ffma2(g[j][i], u[j][i], dw[j][i]);
@@ -311,17 +347,22 @@ __global__ void __launch_bounds__(kBlock<TPR>) group_norm_bwd_kernel(GroupArgs a
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) {
                     float2 du = ffma2(g[j][i], make_float2(rstd, rstd), ffma2(u[j][i], make_float2(m2, m2), make_float2(m1, m1)));
-                    if (a.first) {
+                    if (gate_first<MODE>(a)) {
                         d[j][i] = fmul2(d[j][i], du);
                         du = fmul2(du, s[j][i]);
                     }
                     dx.set(i, du);
-                    if (a.gate) dz.set(i, d[j][i]);
+                    if (gated<MODE>(a)) dz.set(i, d[j][i]);
                 }
-                dx.store((T *)a.dx + row * a.w + at.col(j));
-                if (a.gate) dz.store((T *)a.dgate + row * a.w + at.col(j));
+                dx.store(pdx + at.col(j));
+                if (gated<MODE>(a)) dz.store(pdz + at.col(j));
             }
-    }
+        pdx += move, pdz += move;
+        row += at.step;
+    };
+    for (long long base = row - threadIdx.x / TPR; base < a.rows; base += A * at.step)
+#pragma unroll
+        for (int k = 0; k < A; ++k) one(xs[k], zs[k], dys[k]);
     if (a.part) {
         const long long D = (long long)a.groups * a.w, slots = at.step / a.groups, slot = at.mine / a.groups;
 #pragma unroll
@@ -360,7 +401,7 @@ __global__ void __launch_bounds__(256) group_norm_sum_kernel(const float *part, 
 
 // ------------------------------------------------------------------ launches
 // The variant of a width, as a call F(VEC, TPR, NV): 16-byte vectors where the width allows, else single
-// elements; as few threads as hold the row in one vector each up to a warp, then in up to four (16).
+// elements; as few threads as hold the row in one vector each up to 512, then in two or four (single elements: up to 16).
 #define GROUP_BY_WIDTH(T, w, F)                                      \
     {                                                                \
         constexpr int kWide = 16 / (int)sizeof(T);                   \
@@ -370,10 +411,13 @@ __global__ void __launch_bounds__(256) group_norm_sum_kernel(const float *part, 
             else if (n <= 8) F(kWide, 8, 1);                         \
             else if (n <= 16) F(kWide, 16, 1);                       \
             else if (n <= 32) F(kWide, 32, 1);                       \
-            else if (n <= 64) F(kWide, 32, 2);                       \
+            else if (n <= 64) F(kWide, 64, 1);                       \
             else if (n <= 128) F(kWide, 128, 1);                     \
-            else if (n <= 512) F(kWide, 256, 2);                     \
-            else if (n <= 2048) F(kWide, 512, 4);                    \
+            else if (n <= 256) F(kWide, 256, 1);                     \
+            else if (n <= 512) F(kWide, 512, 1);                     \
+            else if (n <= 768) F(kWide, 384, 2);                     \
+            else if (n <= 1024) F(kWide, 512, 2);                    \
+            else if (n <= 2048) F(kWide, 1024, 2);                   \
             else if constexpr (kMaxD > 2048 * kWide) F(kWide, 1024, 4); \
         } else {                                                     \
             if (n <= 128) F(1, 32, 4);                               \
@@ -385,22 +429,34 @@ __global__ void __launch_bounds__(256) group_norm_sum_kernel(const float *part, 
 
 long long gcd(long long a, long long b) { return b ? gcd(b, a % b) : a; }
 // Blocks: a multiple of what makes the stride a multiple of the groups, as near as that goes to the
-// blocks that the SMs hold at once (1024 threads an SM), and no more than there are rows for.
+// blocks that the SMs hold at once, and no more than there are rows for.
 template <int TPR>
-long long grid_of(long long rows, int groups) {
+long long grid_of(long long rows, int groups, int per_sm) {
     constexpr long long RPB = kBlock<TPR> / TPR;
-    const long long unit = groups / gcd(groups, RPB), held = kSMs * (1024 / kBlock<TPR>);
+    const long long unit = groups / gcd(groups, RPB), held = kSMs * per_sm;
     const long long most = (rows + unit * RPB - 1) / (unit * RPB), fit = held / unit;
     return unit * (most < (fit < 1 ? 1 : fit) ? most : (fit < 1 ? 1 : fit));
 }
 template <int TPR>
-long long slots_of(long long rows, int groups) {
-    return grid_of<TPR>(rows, groups) * (kBlock<TPR> / TPR) / groups;
+long long slots_of(long long rows, int groups, int per_sm) {
+    return grid_of<TPR>(rows, groups, per_sm) * (kBlock<TPR> / TPR) / groups;
 }
 
+// K<..., MODE> for the gate's place, where a row is held by a warp or less in whole vectors.
+#define GROUP_LAUNCH(K, BLOCKS, VEC, TPR, NV)                                                                       \
+    do {                                                                                                    \
+        const unsigned grid = (unsigned)grid_of<TPR>(a.rows, a.groups, BLOCKS<TPR, NV, VEC>);               \
+        if constexpr (TPR <= 32 && VEC > 1) {                                                               \
+            if (!a.gate) K<T, VEC, TPR, NV, kNoGate><<<grid, kBlock<TPR>, 0, s>>>(a);                       \
+            else if (a.first) K<T, VEC, TPR, NV, kGateFirst><<<grid, kBlock<TPR>, 0, s>>>(a);               \
+            else K<T, VEC, TPR, NV, kGateAfter><<<grid, kBlock<TPR>, 0, s>>>(a);                            \
+        } else {                                                                                            \
+            K<T, VEC, TPR, NV, kAnyGate><<<grid, kBlock<TPR>, 0, s>>>(a);                                   \
+        }                                                                                                   \
+    } while (0)
 template <typename T>
 cudaError_t forward(const GroupArgs &a, cudaStream_t s) {
-#define CALL(VEC, TPR, NV) group_norm_kernel<T, VEC, TPR, NV><<<(unsigned)grid_of<TPR>(a.rows, a.groups), kBlock<TPR>, 0, s>>>(a)
+#define CALL(VEC, TPR, NV) GROUP_LAUNCH(group_norm_kernel, kFwdBlocks, VEC, TPR, NV)
     GROUP_BY_WIDTH(T, a.w, CALL)
 #undef CALL
     return cudaGetLastError();
@@ -408,15 +464,14 @@ cudaError_t forward(const GroupArgs &a, cudaStream_t s) {
 template <typename T>
 long long slots(long long rows, int groups, int w) {
     long long out = 0;
-#define CALL(VEC, TPR, NV) out = slots_of<TPR>(rows, groups)
+#define CALL(VEC, TPR, NV) out = slots_of<TPR>(rows, groups, kBwdBlocks<TPR, NV, VEC>)
     GROUP_BY_WIDTH(T, w, CALL)
 #undef CALL
     return out;
 }
 template <typename T>
 cudaError_t backward(const GroupArgs &a, float *dweight, float *dbias, cudaStream_t s) {
-#define CALL(VEC, TPR, NV) \
-    group_norm_bwd_kernel<T, VEC, TPR, NV><<<(unsigned)grid_of<TPR>(a.rows, a.groups), kBlock<TPR>, 0, s>>>(a)
+#define CALL(VEC, TPR, NV) GROUP_LAUNCH(group_norm_bwd_kernel, kBwdBlocks, VEC, TPR, NV)
     GROUP_BY_WIDTH(T, a.w, CALL)
 #undef CALL
     cudaError_t e = cudaGetLastError();
