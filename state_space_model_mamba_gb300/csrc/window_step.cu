@@ -180,20 +180,7 @@ __global__ void __launch_bounds__(kThreads, 3) ring_step_mma(RingParams p, int s
         return;
     }
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
-    write_entry<bf16>(p, r);
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t qa[2 * NI][4];
-    {
-        const bf16 *q = (const bf16 *)p.q + ((long long)r.bi * p.H + r.g * p.hpg + r.chunk * 16) * p.P;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int col = 32 * i + 8 * c;
-            const uint4 x = row < heads && col < p.P ? __ldg((const uint4 *)(q + row * p.P + col)) : zero;
-            const uint4 y = row + 8 < heads && col < p.P ? __ldg((const uint4 *)(q + (row + 8) * p.P + col)) : zero;
-            qa[2 * i][0] = x.x, qa[2 * i][1] = y.x, qa[2 * i][2] = x.y, qa[2 * i][3] = y.y;
-            qa[2 * i + 1][0] = x.z, qa[2 * i + 1][1] = y.z, qa[2 * i + 1][2] = x.w, qa[2 * i + 1][3] = y.w;
-        }
-    }
     const float f = p.scale * kLog2e;
     float o[NV][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -236,6 +223,18 @@ __global__ void __launch_bounds__(kThreads, 3) ring_step_mma(RingParams p, int s
     int stage = 0, ahead = r.split * per + warp;
 #pragma unroll
     for (int x = 0; x < kStages - 1; ++x, ahead += kStep) fetch(ahead, x);
+    uint32_t qa[2 * NI][4];
+    {
+        const bf16 *q = (const bf16 *)p.q + ((long long)r.bi * p.H + r.g * p.hpg + r.chunk * 16) * p.P;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int col = 32 * i + 8 * c;
+            const uint4 x = row < heads && col < p.P ? __ldg((const uint4 *)(q + row * p.P + col)) : zero;
+            const uint4 y = row + 8 < heads && col < p.P ? __ldg((const uint4 *)(q + (row + 8) * p.P + col)) : zero;
+            qa[2 * i][0] = x.x, qa[2 * i][1] = y.x, qa[2 * i][2] = x.y, qa[2 * i][3] = y.y;
+            qa[2 * i + 1][0] = x.z, qa[2 * i + 1][1] = y.z, qa[2 * i + 1][2] = x.w, qa[2 * i + 1][3] = y.w;
+        }
+    }
     for (int tile = r.split * per + warp; tile < last; tile += kStep, ahead += kStep) {
         const int j0 = tile * 16;
         fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
@@ -287,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 3) ring_step_mma(RingParams p, int s
         }
     }
     copy_wait<0>();
+    write_entry<bf16>(p, r);  // last: a store waits for its load, and what comes behind it with it
     __syncthreads();  // the shares take the stages' place
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -386,7 +386,9 @@ template <class K>
 cudaError_t launch_clusters(K kernel, const RingParams &p, int heads_a_block, int shared, cudaStream_t s) {
     int chunks = (p.hpg + heads_a_block - 1) / heads_a_block, splits = 1;
     const long long units = (long long)p.b * p.G * chunks, entries = (long long)p.sinks + p.W;
-    // two blocks a SM while each keeps 64 rows
+    // Two blocks a SM while each keeps 64 rows.  A block's beginning and end are some 7 us, so that halves of full ones do not pay
+    // (192 requests of up to 1028 rows: 127 us, in halves 151), nor do blocks of two warps (144) or one (142), nor
+    // clusters of 16 for one request.
     while (splits < 8 && units * splits < 304 && entries / (2 * splits) >= 64) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * splits));
