@@ -114,6 +114,15 @@ def test_f32(wd, b, L, H, G, P, W, sinks):
     compare(run(wd, x, W, sinks, False), x, W, sinks, False)
 
 
+@pytest.mark.parametrize("b,L,H,G,P,W,sinks", [(2, 650, 8, 8, 20, 100, 0), (1, 700, 12, 2, 64, 33, 3), (3, 333, 16, 16, 128, 50, 0),
+                                               (2, 900, 8, 4, 36, 20, 5)])
+def test_f32_blocks_on_every_sm(wd, b, L, H, G, P, W, sinks):
+    """Enough blocks of 32 rows for the form with four rows a warp; narrow heads; sinks far behind the window."""
+    x = draw(b, L, H, G, P, L + P, False)
+    valid = [L] + [L // 2 + 7 * i for i in range(b - 1)]
+    compare(run(wd, x, W, sinks, False, valid=valid), x, W, sinks, False, valid=valid)
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 def test_a_token_that_sees_itself_alone(wd, bf16):
     """window 1 without sinks: o = v exactly, lse the score, gradients of q and k only what do.o loses to o's rounding."""
