@@ -278,6 +278,14 @@ def ssd_backward(x, dt, A, B, C, D, chunk_len, dy, d_final_state=None, init_stat
     return out
 
 
+def _want(name, t, shape, dtype, index):
+    """Refuses a tensor that is not contiguous, of that shape and type and on CUDA device ``index``."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{index}")
+
+
 def ssd_step(x, dt, A, B, C, D, state, state_index=None):
     """One decoded token per request; ``state`` is updated in place.  Returns y.
 
@@ -286,30 +294,30 @@ def ssd_step(x, dt, A, B, C, D, state, state_index=None):
     the pool marks an absent request, whose y is 0) or None (slot i).  No two
     requests may name the same slot.
     """
-    code, dev = _dtype_code(x), x.device
-    if x.dim() != 3 or B.dim() != 3 or state.dim() != 4:
+    code, f32 = _dtype_code(x), torch.float32
+    xs, Bs, ss = x.shape, B.shape, state.shape
+    if len(xs) != 3 or len(Bs) != 3 or len(ss) != 4:
         raise ValueError("x must be [b, H, P], B and C [b, G, N], state [slots, H, P, N]")
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor")
-    b, H, P = x.shape
-    G, N = B.shape[1:]
-    exp = [("dt", dt, (b, H), torch.float32), ("A", A, (H,), torch.float32), ("B", B, (b, G, N), x.dtype),
-           ("C", C, (b, G, N), x.dtype), ("D", D, (H,), torch.float32),
-           ("state", state, (state.shape[0], H, P, N), torch.float32)]
+    b, H, P = xs
+    G, N = Bs[1:]
+    index = x.get_device()
+    _want("dt", dt, (b, H), f32, index)
+    _want("A", A, (H,), f32, index)
+    _want("B", B, (b, G, N), x.dtype, index)
+    _want("C", C, Bs, x.dtype, index)
+    _want("D", D, (H,), f32, index)
+    _want("state", state, (ss[0], H, P, N), f32, index)
     if state_index is not None:
-        exp.append(("state_index", state_index, (b,), torch.int32))
-    for name, t, shape, dtype in exp:
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError(f"{name}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+        _want("state_index", state_index, (b,), torch.int32, index)
     dims = SsdDims(b, 1, H, P, N, G, 64, 0, 0)
     y = torch.empty_like(x)
-    with on_device(dev.index):
+    with on_device(index):
         _check(load_library().ssd_step(
             ctypes.byref(dims), code, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), D.data_ptr(),
-            state.data_ptr(), state.shape[0], None if state_index is None else state_index.data_ptr(), y.data_ptr(),
-            torch._C._cuda_getCurrentRawStream(dev.index)))
+            state.data_ptr(), ss[0], None if state_index is None else state_index.data_ptr(), y.data_ptr(),
+            torch._C._cuda_getCurrentRawStream(index)))
     return y
 
 

@@ -62,11 +62,7 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _want(name, t, shape, dtype, device):
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+_want = ssd._want
 
 
 def _check_keys(k, v, lead):
@@ -77,31 +73,31 @@ def _check_keys(k, v, lead):
     if not k.is_cuda or not k.is_contiguous():
         raise ValueError("k must be a contiguous CUDA tensor")
     code = ssd.SSD_BF16 if k.dtype is _BF16 else ssd._dtype_code(k)
-    _want("v", v, ks, k.dtype, k.device)
-    return code, ks[-2], ks[-1]
+    index = k.get_device()
+    _want("v", v, ks, k.dtype, index)
+    return code, ks, index
 
 
 def _check_queries(q, k, v, lead):
-    code, G, P = _check_keys(k, v, lead)
-    qs, ks = q.shape, k.shape
-    if len(qs) != lead + 2 or qs[:lead] != ks[:lead] or qs[-1] != P:
+    code, ks, index = _check_keys(k, v, lead)
+    qs = q.shape
+    if len(qs) != lead + 2 or qs[:lead] != ks[:lead] or qs[-1] != ks[-1]:
         raise ValueError("q [.., H, P] and k, v [.., G, P] need the same leading axes and width")
-    H = qs[-2]
-    if G < 1 or H % G:
-        raise ValueError(f"heads ({H}) must be a multiple of key groups ({G})")
-    _want("q", q, qs, k.dtype, k.device)
-    return code, H, G, P
+    if ks[-2] < 1 or qs[-2] % ks[-2]:
+        raise ValueError(f"heads ({qs[-2]}) must be a multiple of key groups ({ks[-2]})")
+    _want("q", q, qs, k.dtype, index)
+    return code, qs, ks[-2], index
 
 
-def _check_ring(k_cache, v_cache, k, G, P, window, sinks, b, cache_index):
-    if k_cache.dim() != 4:
+def _check_ring(k_cache, v_cache, dtype, G, P, window, sinks, b, cache_index, index):
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache and v_cache must be [slots, sinks + window, G, P]")
-    slots = k_cache.shape[0]
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _want(name, t, (slots, sinks + window, G, P), k.dtype, k.device)
+    _want("k_cache", k_cache, (shape[0], sinks + window, G, P), dtype, index)
+    _want("v_cache", v_cache, shape, dtype, index)
     if cache_index is not None:
-        _want("cache_index", cache_index, (b,), _I32, k.device)
-    return slots
+        _want("cache_index", cache_index, (b,), _I32, index)
+    return shape[0]
 
 
 def workspace_bytes(dims: WindowDims, dtype_code: int, backward: bool) -> int:
@@ -112,11 +108,10 @@ def workspace_bytes(dims: WindowDims, dtype_code: int, backward: bool) -> int:
 
 
 def _sequence(q, k, v, window, sinks, valid_len, simt):
-    code, H, G, P = _check_queries(q, k, v, 2)
-    b, L = q.shape[:2]
+    code, (b, L, H, P), G, index = _check_queries(q, k, v, 2)
     if valid_len is not None:
-        _want("valid_len", valid_len, (b,), _I32, q.device)
-    return code, WindowDims(b, L, H, P, G, window, sinks, WINDOW_FLAG_SIMT if simt else 0, 0)
+        _want("valid_len", valid_len, (b,), _I32, index)
+    return code, WindowDims(b, L, H, P, G, window, sinks, WINDOW_FLAG_SIMT if simt else 0, 0), b, L, H, P, index
 
 
 def window_forward(q, k, v, window, sinks=0, scale=None, valid_len=None, return_lse=True, simt=False, check_status=False):
@@ -128,12 +123,10 @@ def window_forward(q, k, v, window, sinks=0, scale=None, valid_len=None, return_
     ``simt`` keeps fp32 operands in bf16 too, on CUDA cores; ``check_status`` synchronises and raises
     SsdError when valid_len entries had to be clamped.
     """
-    code, dims = _sequence(q, k, v, window, sinks, valid_len, simt)
-    b, L, H, P = q.shape
+    code, dims, b, L, H, P, index = _sequence(q, k, v, window, sinks, valid_len, simt)
     o = torch.empty_like(q)
     lse = torch.empty(b, H, L, device=q.device, dtype=_F32) if return_lse else None
     ws = torch.empty(workspace_bytes(dims, code, False), dtype=torch.uint8, device=q.device)
-    index = q.device.index
     with ssd.on_device(index):
         ssd._check(_lib().window_forward(
             ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), P ** -0.5 if scale is None else scale,
@@ -145,14 +138,12 @@ def window_forward(q, k, v, window, sinks=0, scale=None, valid_len=None, return_
 
 def window_backward(q, k, v, o, lse, do, window, sinks=0, scale=None, valid_len=None, simt=False, check_status=False):
     """Gradients for ``do`` at the forward's ``o`` and ``lse``: a dict with dq, dk and dv."""
-    code, dims = _sequence(q, k, v, window, sinks, valid_len, simt)
-    b, L, H, P = q.shape
-    _want("o", o, q.shape, q.dtype, q.device)
-    _want("do", do, q.shape, q.dtype, q.device)
-    _want("lse", lse, (b, H, L), _F32, q.device)
+    code, dims, b, L, H, P, index = _sequence(q, k, v, window, sinks, valid_len, simt)
+    _want("o", o, q.shape, q.dtype, index)
+    _want("do", do, q.shape, q.dtype, index)
+    _want("lse", lse, (b, H, L), _F32, index)
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
     ws = torch.empty(workspace_bytes(dims, code, True), dtype=torch.uint8, device=q.device)
-    index = q.device.index
     with ssd.on_device(index):
         ssd._check(_lib().window_backward(
             ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
@@ -167,13 +158,11 @@ def window_fill(k, v, k_cache, v_cache, window, sinks=0, valid_len=None, cache_i
     """Writes the tokens of prompts k, v [b, L, G, P] that later tokens see into rings
     k_cache, v_cache [slots, sinks + window, G, P]: row i's into slot cache_index[i] (int32 [b]; a slot
     outside the pool marks a row that is not kept) or slot i.  No two rows may name the same slot."""
-    code, G, P = _check_keys(k, v, 2)
-    b, L = k.shape[:2]
-    slots = _check_ring(k_cache, v_cache, k, G, P, window, sinks, b, cache_index)
+    code, (b, L, G, P), index = _check_keys(k, v, 2)
+    slots = _check_ring(k_cache, v_cache, k.dtype, G, P, window, sinks, b, cache_index, index)
     if valid_len is not None:
-        _want("valid_len", valid_len, (b,), _I32, k.device)
+        _want("valid_len", valid_len, (b,), _I32, index)
     dims = WindowDims(b, L, G, P, G, window, sinks, WINDOW_FLAG_SIMT, 0)
-    index = k.device.index
     with ssd.on_device(index):
         ssd._check(_lib().window_fill(
             ctypes.byref(dims), code, k.data_ptr(), v.data_ptr(), _ptr(valid_len), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -188,13 +177,11 @@ def window_step(q, k, v, k_cache, v_cache, position, window, sinks=0, scale=None
     slot outside the pool, or a negative position, marks an absent request, whose o is 0) or None (slot i).
     No two requests may name the same slot.
     """
-    code, H, G, P = _check_queries(q, k, v, 1)
-    b = q.shape[0]
-    slots = _check_ring(k_cache, v_cache, k, G, P, window, sinks, b, cache_index)
-    _want("position", position, (b,), _I32, q.device)
+    code, (b, H, P), G, index = _check_queries(q, k, v, 1)
+    slots = _check_ring(k_cache, v_cache, k.dtype, G, P, window, sinks, b, cache_index, index)
+    _want("position", position, (b,), _I32, index)
     dims = WindowDims(b, 1, H, P, G, window, sinks, WINDOW_FLAG_SIMT, 0)
     o = torch.empty_like(q)
-    index = q.device.index
     with ssd.on_device(index):
         ssd._check(_lib().window_step(
             ctypes.byref(dims), code, q.data_ptr(), k.data_ptr(), v.data_ptr(), position.data_ptr(),
