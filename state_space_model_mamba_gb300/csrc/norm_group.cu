@@ -330,8 +330,10 @@ __global__ void __launch_bounds__(kBlock<TPR>, kBwdBlocks<TPR, NV, VEC>) group_n
                 } else if (!gate_first<MODE>(a)) {
                     d[j][i] = fmul2(d[j][i], y);  // dgate
                 }
-                dw[j][i] = ffma2(g[j][i], u[j][i], dw[j][i]);
-                db[j][i] = fadd2(db[j][i], g[j][i]);
+                if (live) {  // past the last row n may be NaN (no columns loaded, eps of 0), which dy = 0 does not take out
+                    dw[j][i] = ffma2(g[j][i], u[j][i], dw[j][i]);
+                    db[j][i] = fadd2(db[j][i], g[j][i]);
+                }
                 g[j][i] = fmul2(g[j][i], w[j].get(i));
                 t1 = fadd2(t1, g[j][i]);
                 t2 = ffma2(g[j][i], u[j][i], t2);
