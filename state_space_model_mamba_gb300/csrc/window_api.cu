@@ -1,5 +1,6 @@
 // window_api.cu -- the C ABI declared in include/window.h: argument checks,
 // workspace carving and the launches of window attention.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -51,6 +52,10 @@ ssd_status check_pointers(const void *const *req, const char *const *names, int 
         if (!aligned16(req[i])) return fail(SSD_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
     }
     return SSD_OK;
+}
+
+ssd_status check_scale(float scale) {
+    return isfinite(scale) ? SSD_OK : fail(SSD_ERR_INVALID_ARG, "scale %g is not finite", (double)scale);
 }
 
 ssd_status cuda_status(cudaError_t e) {
@@ -161,6 +166,7 @@ ssd_status window_forward(const window_dims *dims, ssd_dtype dtype, const void *
     const void *req[] = {q, k, v, o, workspace};
     static const char *const names[] = {"q", "k", "v", "o", "workspace"};
     if ((st = check_pointers(req, names, 5)) != SSD_OK) return st;
+    if ((st = check_scale(scale)) != SSD_OK) return st;
     if (lse && !aligned16(lse)) return fail(SSD_ERR_INVALID_ARG, "lse is not 16-byte aligned");
     if (workspace_bytes < kStatusBytes)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, kStatusBytes);
@@ -182,6 +188,7 @@ ssd_status window_backward(const window_dims *dims, ssd_dtype dtype, const void 
     const void *req[] = {q, k, v, o, lse, d_o, dq, dk, dv, workspace};
     static const char *const names[] = {"q", "k", "v", "o", "lse", "do", "dq", "dk", "dv", "workspace"};
     if ((st = check_pointers(req, names, 10)) != SSD_OK) return st;
+    if ((st = check_scale(scale)) != SSD_OK) return st;
     const size_t need = window_workspace_bytes(dims, dtype, 1);
     if (workspace_bytes < need)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
@@ -224,6 +231,7 @@ ssd_status window_step(const window_dims *dims, ssd_dtype dtype, const void *q, 
     const void *req[] = {q, k, v, k_cache, v_cache, o};
     static const char *const names[] = {"q", "k", "v", "k_cache", "v_cache", "o"};
     if ((st = check_pointers(req, names, 6)) != SSD_OK) return st;
+    if ((st = check_scale(scale)) != SSD_OK) return st;
     if (!position) return fail(SSD_ERR_INVALID_ARG, "position is NULL");
     if ((st = check_ring(dims, slots, cache_index)) != SSD_OK) return st;
     RingParams p = ring_params(*dims, k, v, k_cache, v_cache, slots, cache_index);

@@ -130,3 +130,12 @@ def test_bindings_refuse_wrong_tensors(lib):
     with pytest.raises(ValueError, match="CUDA"):
         ssd.ssd_step(torch.zeros(1, 4, 8), torch.zeros(1, 4), torch.zeros(4), torch.zeros(1, 2, 8), torch.zeros(1, 2, 8),
                      torch.zeros(4), torch.zeros(1, 4, 8, 8))
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_scales_that_are_not_finite_are_refused(lib, scale):
+    big = 1 << 40
+    assert lib.window_forward(dims(), 1, BUF, BUF, BUF, scale, None, BUF, None, BUF, big, None) == ssd.SSD_ERR_INVALID_ARG
+    assert b"finite" in lib.ssd_last_error()
+    assert lib.window_backward(dims(), 1, *([BUF] * 6 + [scale, None] + [BUF] * 4 + [big, None])) == ssd.SSD_ERR_INVALID_ARG
+    assert lib.window_step(dims(seqlen=1), 1, BUF, BUF, BUF, BUF, scale, BUF, BUF, 2, None, BUF, None) == ssd.SSD_ERR_INVALID_ARG
