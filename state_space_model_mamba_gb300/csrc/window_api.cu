@@ -74,6 +74,12 @@ ssd_status guarded(F launches) {
 constexpr size_t kStatusBytes = 1024;  // status words, then the backward's buffers
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+// Window and sinks as the kernels take them: at most L, and plain causal where both together leave nobody out.
+void fit_window(const window_dims &d, int *W, int *sinks) {
+    const bool all = d.window + d.sinks >= d.seqlen;
+    *W = (int)(all ? d.seqlen : d.window);
+    *sinks = (int)(all ? 0 : d.sinks);
+}
 // The backward's buffers behind the status words.
 size_t carve(const window_dims &d, ssd_dtype dt, char *ws, WindowParams *p, float **parts) {
     const size_t delta = up256(4ull * d.batch * d.nheads * d.seqlen);
@@ -82,7 +88,9 @@ size_t carve(const window_dims &d, ssd_dtype dt, char *ws, WindowParams *p, floa
         *parts = (float *)(ws + kStatusBytes + delta);
     }
     if (!tile_supported(d, dt, true)) return kStatusBytes + delta;
-    return kStatusBytes + delta + 4 * tile_backward_floats(d.batch, d.seqlen, d.ngroups, d.headdim, d.window, d.sinks);
+    int W, sinks;
+    fit_window(d, &W, &sinks);
+    return kStatusBytes + delta + 4 * tile_backward_floats(d.batch, d.seqlen, d.ngroups, d.headdim, W, sinks);
 }
 
 WindowParams base_params(const window_dims &d, const void *q, const void *k, const void *v, float scale,
@@ -95,8 +103,7 @@ WindowParams base_params(const window_dims &d, const void *q, const void *k, con
     p.P = (int)d.headdim;
     p.G = (int)d.ngroups;
     p.hpg = p.H / p.G;
-    p.W = (int)(d.window < d.seqlen ? d.window : d.seqlen);
-    p.sinks = (int)(d.sinks < d.seqlen ? d.sinks : d.seqlen);
+    fit_window(d, &p.W, &p.sinks);
     p.scale = scale;
     p.q = q;
     p.k = k;

@@ -367,13 +367,13 @@ struct SinkCut {
 };
 inline SinkCut sink_cut(long long L, long long W, long long sinks) {
     SinkCut c = {0, 0, 0};
-    W = W < L ? W : L;
-    sinks = sinks < L ? sinks : L;
     const long long behind = L - 127 - W;
     if (sinks < 1 || behind < 1) return c;
-    // as long as a window item, but no shorter than 1024 tokens
-    c.length = (int)(W + 127 < 1024 ? 1024 : W + 127);
+    // as long as a window item, but no shorter than 1024 tokens, and in all no more than 1024 shares a group: their place is
+    // 1 KB a column each, and many tiles of sinks fill the SMs without being cut
     c.tiles = (int)((sinks + 127) / 128);
+    const long long most = c.tiles < 1024 ? 1024 / c.tiles : 1, even = (behind + most - 1) / most, least = W + 127 < 1024 ? 1024 : W + 127;
+    c.length = (int)(even < least ? least : even);
     c.segments = (int)((behind + c.length - 1) / c.length);
     return c;
 }

@@ -20,7 +20,7 @@ using delta::store1;
 struct WindowParams {
     int b, L, H, P, G, hpg;
     int W;      // window, at most L
-    int sinks;  // at most L
+    int sinks;  // none where W is L
     float scale;
     const void *q, *k, *v;
     const int32_t *valid_len;

@@ -139,3 +139,19 @@ def test_scales_that_are_not_finite_are_refused(lib, scale):
     assert b"finite" in lib.ssd_last_error()
     assert lib.window_backward(dims(), 1, *([BUF] * 6 + [scale, None] + [BUF] * 4 + [big, None])) == ssd.SSD_ERR_INVALID_ARG
     assert lib.window_step(dims(seqlen=1), 1, BUF, BUF, BUF, BUF, scale, BUF, BUF, 2, None, BUF, None) == ssd.SSD_ERR_INVALID_ARG
+
+
+def test_the_workspace_of_many_sinks_is_bounded(lib):
+    """Half the tokens as sinks: the shares of their gradients stay below 2048 tiles of 128 x headdim pairs of fp32 a group;
+    where everybody is seen nothing is kept at all."""
+    L, groups = 131072, 2 * 2
+    delta = 4 * 2 * 4 * L
+
+    def size(**kw):
+        return lib.window_workspace_bytes(dims(seqlen=L, **kw), 1, 1)
+
+    for window_, sinks in ((1024, 4), (1024, 200), (1, 40000), (1024, L // 2), (3000, L - 4000)):
+        assert delta < size(window=window_, sinks=sinks) <= delta + 2048 + groups * 2048 * 2 * 128 * 64 * 4
+    none = size(window=1024, sinks=0)
+    assert none <= delta + 2048
+    assert size(window=1024, sinks=L) == size(window=1, sinks=L - 1) == size(window=L, sinks=4) == none

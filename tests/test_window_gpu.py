@@ -381,3 +381,13 @@ def test_refusals(wd):
         wd.window_fill(k, v, kc[:1], kc[:1], 4, 2)
     with pytest.raises(ValueError, match="position"):
         wd.window_step(q[:, 0].contiguous(), k[:, 0].contiguous(), v[:, 0].contiguous(), kc, kc.clone(), ints([0]), 4, 2)
+
+
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("b,L,H,G,P,W,sinks", [(1, 300, 2, 1, 64, 20, 280), (2, 257, 4, 2, 128, 1, 1000), (1, 1500, 2, 2, 64, 30, 900),
+                                               (1, 300, 2, 1, 64, 20, 279), (1, 2700, 1, 1, 8, 40, 300)])
+def test_many_sinks(wd, b, L, H, G, P, W, sinks, simt):
+    """Sinks that with the window cover the row (plain causal attention), all but cover it, take many tiles."""
+    x = draw(b, L, H, G, P, L + sinks)
+    valid = [L - 3 * i for i in range(b)]
+    compare(run(wd, x, W, sinks, True, valid=valid, simt=simt), x, W, sinks, True, valid=valid)
