@@ -7,7 +7,8 @@
 // other's softmax, first tiles and last stores (one block with two query tiles that share the copies of
 // their keys came to the end of both at once, and stood still for a fifth of an item).  S and P have columns of their own in
 // a block's half of tensor memory, so that the next S is made as soon as the last one is in registers: 256 columns hold S, P and
-// O with 80 keys a tile where O has 128 columns, and 96 keys where it has 64.
+// O with 80 keys a tile where O has 128 columns.  Where it has 64 there would be room for more, but a thread's 96 scores leave
+// it too few registers (8 padded rows of up to 4096, 64 heads of 64: 526 us with 96 keys, 469 with 80).
 // The row maximum is followed lazily: a row's reference only moves, and O is only rescaled, where the maximum
 // has grown by 2^8 over it, so P <= 256 and the passes over O are rare; sums are fp32 and do not care.
 // P is rounded to bf16 (2^-8 of each at most), the sum it is divided by is not.
@@ -38,7 +39,7 @@ struct Maps {
 // KB = ceil(P / 64) blocks of 64 columns a tile.
 template <int KB>
 struct Layout {
-    static constexpr int kKeys = KB == 2 ? 80 : 96;                                            // of a tile
+    static constexpr int kKeys = 80;  // of a tile
     // Rings of K and of V tiles, apart: a waiting thread tells a phase of a slot from the next one only, so it has to see
     // every use of the slots it waits for (a ring of three slots for both let S begin on a K that had not landed).
     static constexpr int kBlock = kKeys * 128, kTile = KB * kBlock, kK = 2, kV = 2;
@@ -233,10 +234,8 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 float2 x[COLS / 2];
                 if constexpr (COLS == 16)
                     tc::tmem_ld16(ts, (float *)x);
-                else if constexpr (COLS == 80)
-                    tmem_ld80(ts, (float *)x);
                 else
-                    tmem_ld96(ts, (float *)x);
+                    tmem_ld80(ts, (float *)x);
                 tc::tc_fence_before();
                 arrive_first(&sm.s_free, lane);
                 if (!plain) {
@@ -295,9 +294,8 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
                 wait_warp(&sm.p_free, (ns & 1) ^ 1, err);
                 tc::tc_fence_after();
                 ++ns;
-                if constexpr (COLS >= 80) tmem_st32(tp, pk);
-                if constexpr (COLS == 96) delta::tmem_st16(tp + 32, (const float *)(pk + 32));
-                if constexpr (COLS % 32 == 16) tmem_st8(tp + COLS / 2 - 8, pk + COLS / 2 - 8);
+                if constexpr (COLS == 80) tmem_st32(tp, pk);
+                tmem_st8(tp + COLS / 2 - 8, pk + COLS / 2 - 8);
                 delta::tmem_wait_st();
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 if (nk & 15) {
