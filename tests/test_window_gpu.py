@@ -391,3 +391,22 @@ def test_many_sinks(wd, b, L, H, G, P, W, sinks, simt):
     x = draw(b, L, H, G, P, L + sinks)
     valid = [L - 3 * i for i in range(b)]
     compare(run(wd, x, W, sinks, True, valid=valid, simt=simt), x, W, sinks, True, valid=valid)
+
+
+@pytest.mark.parametrize("H,G,P", [(2, 2, 64), (4, 1, 128)])
+@pytest.mark.parametrize("rise", [0.02, 0.3, -0.3, 8.0])
+def test_scores_that_rise_and_fall_along_the_row(wd, H, G, P, rise):
+    """Each tile's scores lie above (below) those of the tiles before, so that the softmax's reference has to move (stays) from tile
+    to tile.  Tolerances as for scores of every size: a score is off by its length's sum times 2^-24 of it."""
+    L, W, sinks = 700, 400, 3
+    x = draw(1, L, H, G, P, 21)
+    u = np.zeros(P, np.float32)
+    u[0] = 1.0
+    ramp = (np.arange(L, dtype=np.float32) - L / 2) * rise
+    x["q"] = store(0.3 * x["q"] + u, True)
+    x["k"] = store(0.3 * x["k"] + ramp[None, :, None, None] * u, True)
+    out = run(wd, x, W, sinks, True, scale=1.0, backward=False)
+    o, lse = ow.window_forward(x["q"], x["k"], x["v"], W, sinks, 1.0)
+    s = max(1.0, np.abs(lse).max())
+    check(out["lse"], lse, F32_BAR, "lse", 2)
+    check(out["o"], o, BF16_BAR + 8 * s * 2.0 ** -23, "o", 3)
