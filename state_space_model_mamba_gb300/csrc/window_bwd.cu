@@ -749,7 +749,7 @@ cudaError_t backward(const WindowParams &p, float *parts, cudaStream_t s) {
         if ((e = map_tokens(&maps.k, p.k, p, p.G, 1, kDqKeys)) != cudaSuccess) return e;
         if ((e = delta::same_tiles(&maps.v, maps.k, p.v)) != cudaSuccess) return e;
         if ((e = delta::allow_shared((const void *)window_dq_kernel<KB>, DqLayout<KB>::kBytes)) != cudaSuccess) return e;
-        window_dq_kernel<KB><<<items < kSMs ? items : kSMs, kDqThreads, DqLayout<KB>::kBytes, s>>>(maps, p, items, per_row);
+        window_dq_kernel<KB><<<tile_grid(p, items, kSMs), kDqThreads, DqLayout<KB>::kBytes, s>>>(maps, p, items, per_row);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const SinkCut cut = sink_cut(p.L, p.W, p.sinks);
@@ -759,7 +759,7 @@ cudaError_t backward(const WindowParams &p, float *parts, cudaStream_t s) {
     if ((e = map_tokens(&maps.k, p.k, p, p.G, 1, 128)) != cudaSuccess) return e;
     if ((e = delta::same_tiles(&maps.v, maps.k, p.v)) != cudaSuccess) return e;
     if ((e = delta::allow_shared((const void *)window_dkv_kernel<KB>, DkvLayout<KB>::kBytes)) != cudaSuccess) return e;
-    window_dkv_kernel<KB><<<items < kSMs ? items : kSMs, kDkvThreads, DkvLayout<KB>::kBytes, s>>>(maps, p, cut, parts, items);
+    window_dkv_kernel<KB><<<tile_grid(p, items, kSMs), kDkvThreads, DkvLayout<KB>::kBytes, s>>>(maps, p, cut, parts, items);
     if ((e = cudaGetLastError()) != cudaSuccess || !cut.segments) return e;
     const long long n = (long long)p.b * p.G * 2 * 128 * cut.tiles * (p.P / 4);
     window_sinks_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, cut, parts, n);

@@ -384,7 +384,7 @@ cudaError_t forward(const WindowParams &p, cudaStream_t s) {
     // the sign of the scale goes into the product, so that the largest score is the largest exponent; a scale of 0 is
     // kept off 0 for the masked ones
     const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-    window_fwd_kernel<KB><<<items < 2 * kSMs ? items : 2 * kSMs, kThreads, Layout<KB>::kBytes, s>>>(maps, p, c, p.scale < 0.f ? 1u << 13 : 0u,
+    window_fwd_kernel<KB><<<tile_grid(p, items, 2 * kSMs), kThreads, Layout<KB>::kBytes, s>>>(maps, p, c, p.scale < 0.f ? 1u << 13 : 0u,
                                                                                                items, per_row);
     return cudaGetLastError();
 }

@@ -105,6 +105,21 @@ struct Cursor {
     }
 };
 
+// Blocks for `items` tiles, at most `most`.  Block i takes tiles i, i + grid, ..., tile n is of batch row n % (G b) / G: where the rows differ
+// in length the grid's common divisor with G b is at most G, so that every block comes round all of them (8 padded rows of 8 groups,
+// whose 304 blocks met either the even rows or the odd; 16 rows of up to 2048, 32 heads of 128 over 4: 195 us, 187 now).
+inline int tile_grid(const WindowParams &p, int items, int most) {
+    if (items <= most || !p.valid_len) return items < most ? items : most;
+    for (;; --most) {
+        int a = p.G * p.b, c = most;
+        while (c) {
+            const int r = a % c;
+            a = c, c = r;
+        }
+        if (a <= p.G) return most;
+    }
+}
+
 // A query tile of T tokens and its keys in tiles of KEYS: [0, tiles_w) the window, [tiles_w, tiles) the sinks in front of it.
 template <int KEYS>
 struct QueryItem {
