@@ -98,11 +98,15 @@ __global__ void __launch_bounds__(kThreads, 2) window_fwd_kernel(const __grid_co
         __syncwarp();
         tc::tmem_alloc(&sm.tmem, 256);
     }
+    const int T = tile_tokens(p);
+    // rows past the tokens' of a query tile are never copied: zeros, so that their sums never ask for a maximum
+    for (int e = tid; e < (128 - T * p.hpg) * 8 * KB; e += kThreads)
+        tc::st_shared_v4(base + (e % KB) * 16384 + (T * p.hpg) * 128 + e / KB * 16, 0, 0, 0, 0);
+    tc::fence_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
-    const int T = tile_tokens(p);
     int *const err = &sm.err;
 
     if (warp >= kSoftmax / 32) {
