@@ -31,29 +31,45 @@ using tc::fmul2;
 using tc::tmem_addr;
 
 // ------------------------------------------------------------------ D = do . o
-// 8 lanes a row of P (8 columns each in turn), rows in the order of the tensors.
-__global__ void __launch_bounds__(256) window_delta_kernel(WindowParams p, long long rows) {
-    const long long row = (blockIdx.x * 256ll + threadIdx.x) >> 3;
+// 8 lanes a row of P (8 columns each in turn), rows in the order of the tensors, 4 a thread whose loads go ahead of the sums
+// (one row a thread, numbered in 64 bits: the 130M layer's backward 175 us, so 172; 8 padded rows of up to 4096 tokens of 64 heads of 64
+// 1502 and 1474).  The API takes up to 3.2e9 rows, which 32 bits number.
+constexpr int kDeltaRows = 4;
+template <int KB>
+__global__ void __launch_bounds__(256) window_delta_kernel(WindowParams p, uint32_t rows) {
+    const uint32_t first = blockIdx.x * (32u * kDeltaRows) + (threadIdx.x >> 3);
     const int lane = threadIdx.x & 7;
     if (blockIdx.x == 0) write_status(p);
-    float s = 0.f;
-    if (row < rows) {
-        const bf16 *o = (const bf16 *)p.o + row * p.P, *d = (const bf16 *)p.d_o + row * p.P;
+    uint4 a[kDeltaRows][KB], b[kDeltaRows][KB];
+#pragma unroll
+    for (int i = 0; i < kDeltaRows; ++i)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int c = 8 * lane + 64 * kb;
+            a[i][kb] = b[i][kb] = make_uint4(0u, 0u, 0u, 0u);
+            if (first + 32 * i < rows && c < p.P) {
+                const long long at = (long long)(first + 32 * i) * p.P + c;
+                a[i][kb] = __ldg((const uint4 *)((const bf16 *)p.o + at));
+                b[i][kb] = __ldg((const uint4 *)((const bf16 *)p.d_o + at));
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < kDeltaRows; ++i) {
         float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 2
-        for (int c = 8 * lane; c < p.P; c += 64) {
-            const uint4 a = __ldg((const uint4 *)(o + c)), b = __ldg((const uint4 *)(d + c));
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const uint32_t x[4] = {a[i][kb].x, a[i][kb].y, a[i][kb].z, a[i][kb].w}, y[4] = {b[i][kb].x, b[i][kb].y, b[i][kb].z, b[i][kb].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc = ffma2(tc::bf2_to_f2(x[e]), tc::bf2_to_f2(y[e]), acc);
         }
-        s = acc.x + acc.y;
-    }
+        float s = acc.x + acc.y;
 #pragma unroll
-    for (int x = 4; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (row < rows && lane == 0) {
-        const int h = (int)(row % p.H), t = (int)(row / p.H % p.L);
-        p.delta[(row / p.H / p.L * p.H + h) * p.L + t] = s;
+        for (int x = 4; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        const uint32_t row = first + 32 * i;
+        if (row < rows && lane == 0) {
+            const uint32_t token = row / (uint32_t)p.H, h = row - token * p.H, bi = token / (uint32_t)p.L, t = token - bi * p.L;
+            p.delta[((long long)bi * p.H + h) * p.L + t] = s;
+        }
     }
 }
 
@@ -739,7 +755,7 @@ template <int KB>
 cudaError_t backward(const WindowParams &p, float *parts, cudaStream_t s) {
     cudaError_t e;
     const long long rows = (long long)p.b * p.L * p.H;
-    window_delta_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, s>>>(p, rows);
+    window_delta_kernel<KB><<<(unsigned)((rows + 32 * kDeltaRows - 1) / (32 * kDeltaRows)), 256, 0, s>>>(p, (uint32_t)rows);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     Maps maps;
     {
