@@ -34,9 +34,11 @@ def window_forward(q, k, v, window, sinks, scale, valid_len=None):
     return o, lse
 
 
-def window_backward(q, k, v, do, window, sinks, scale, valid_len=None):
-    """dict(dq, dk, dv) for the gradient do of o."""
+def window_backward(q, k, v, do, window, sinks, scale, valid_len=None, o=None):
+    """dict(dq, dk, dv) for the gradient do of o.  With `o`, do . o takes that in place of the exact outputs, as a kernel does
+    that is given outputs as they were stored."""
     q, k, v, do = (np.asarray(x, np.float64) for x in (q, k, v, do))
+    o = None if o is None else np.asarray(o, np.float64)
     b, L, H, P = q.shape
     G = k.shape[2]
     dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
@@ -49,7 +51,8 @@ def window_backward(q, k, v, do, window, sinks, scale, valid_len=None):
                 p = np.exp(x - x.max(-1, keepdims=True))
                 p /= p.sum(-1, keepdims=True)
                 dp = do[i, t, hs] @ v[i, s, g].T
-                dx = scale * p * (dp - (p * dp).sum(-1, keepdims=True))
+                D = (p * dp).sum(-1, keepdims=True) if o is None else (do[i, t, hs] * o[i, t, hs]).sum(-1, keepdims=True)
+                dx = scale * p * (dp - D)
                 dq[i, t, hs] = dx @ k[i, s, g]
                 dk[i, s, g] += dx.T @ q[i, t, hs]
                 dv[i, s, g] += p.T @ do[i, t, hs]
