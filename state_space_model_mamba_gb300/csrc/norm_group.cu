@@ -69,13 +69,13 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
         d = one;
         return;
     }
-    const float2 s = logistic<T>(x), r = ffma2(s, minus, one);  // 1 - s
+    const float2 s = logistic<T>(x);
     if (act == NORM_ACT_SILU) {
         a = fmul2(x, s);
-        d = fmul2(s, ffma2(x, r, one));
-    } else {
+        d = fmul2(s, ffma2(x, ffma2(s, minus, one), one));
+    } else {  // 1 - s is the logistic function of -x; the difference would have no bits left where s is next to 1
         a = s;
-        d = fmul2(s, r);
+        d = fmul2(s, logistic<T>(fmul2(x, minus)));
     }
 }
 
