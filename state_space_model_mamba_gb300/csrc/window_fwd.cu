@@ -13,6 +13,8 @@
 // more than 2^8, so P <= 256 and the passes over O are rare; sums are fp32 and do not care.  Other tiles do not
 // look for their maximum (2 x 8192 tokens of 40 heads of 128, window 2048: 437 us, 413 without).
 // P is rounded to bf16 (2^-8 of each at most), the sum it is divided by is not.
+#include <float.h>
+
 #include <type_traits>
 
 #include "window_tile.cuh"
@@ -386,8 +388,8 @@ cudaError_t forward(const WindowParams &p, cudaStream_t s) {
     if ((e = delta::allow_shared((const void *)window_fwd_kernel<KB>, Layout<KB>::kBytes)) != cudaSuccess) return e;
     const int per_row = (p.L + T - 1) / T, items = per_row * p.G * p.b;
     // the sign of the scale goes into the product, so that the largest score is the largest exponent; a scale of 0 is
-    // kept off 0 for the masked ones
-    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+    // kept off 0 for the masked ones, by the smallest number there is: no finite score makes more than 2^-20 of it
+    const float c = fmaxf(fabsf(p.scale) * kLog2e, FLT_TRUE_MIN);
     window_fwd_kernel<KB><<<tile_grid(p, items, 2 * kSMs), kThreads, Layout<KB>::kBytes, s>>>(maps, p, c, p.scale < 0.f ? 1u << 13 : 0u,
                                                                                                items, per_row);
     return cudaGetLastError();

@@ -103,3 +103,21 @@ def test_offsets_past_32_bits(wd, bf16, G):
     for n in alone:
         assert torch.equal(last[n], alone[n]), n
     assert alone["dq"][0, 1:valid[-1]].abs().amax((1, 2)).min() > 0  # every token that sees another has a gradient
+
+
+def scaled_alike(wd, bf16, simt, power):
+    """The outputs at q, k and a scale, and at q and k times 2^power and the scale times 2^-2power: the same scores, exactly."""
+    x = wu.draw(1, 300, 4, 2, 64, 31, bf16)
+    big = dict(x, q=x["q"] * np.float32(2.0 ** power), k=x["k"] * np.float32(2.0 ** power))
+    for sign in (1, -1):
+        yield [train(wd, {n: dev(t, bf16) for n, t in y.items()}, 70, 3, scale=sign * s, simt=simt)
+               for y, s in ((x, 0.125), (big, 2.0 ** (-3 - 2 * power)))]
+
+
+@pytest.mark.parametrize("bf16,simt", FORMS)
+@pytest.mark.parametrize("power", [53, 60])
+def test_tiny_scales_of_large_scores(wd, bf16, simt, power):
+    """o, lse and dv are the same bit for bit."""
+    for a, b in scaled_alike(wd, bf16, simt, power):
+        for n in ("o", "lse", "dv"):
+            assert torch.equal(a[n], b[n]), n
