@@ -34,6 +34,8 @@ __device__ __forceinline__ float4 fma4(float a, float4 x, float4 y) {
 __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
     return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
 }
+// The scale enters after the sums of dq and dk: before them it would take the terms of a tiny one below the normal numbers.
+__device__ __forceinline__ float4 scaled(float a, float4 x) { return make_float4(a * x.x, a * x.y, a * x.z, a * x.w); }
 // Rows [first, first + n) of head `head` of a [b, L, heads, P] tensor; rows at or past `end` become zeros.
 template <typename T>
 __device__ __forceinline__ void load_rows(float *dst, int pitch, const void *src, int bi, int L, int heads, int head, int P,
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) window_rows_dq(Windo
 #pragma unroll
             for (int i = 0; i < WR; ++i) {
                 const int t = t0 + warp * WR + i, s = s0 + lane;
-                x[i] = t < t1 && s < end && sees(p, t, s) ? p.scale * expf(p.scale * x[i] - lse[i]) * (dp[i] - D[i]) : 0.f;
+                x[i] = t < t1 && s < end && sees(p, t, s) ? expf(p.scale * x[i] - lse[i]) * (dp[i] - D[i]) : 0.f;
             }
             sums(x, K, pitch, at, dq);
         }
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) window_rows_dq(Windo
 #pragma unroll
     for (int i = 0; i < WR; ++i) {
         const int t = t0 + warp * WR + i;
-        const float4 y = at.total(dq[i]);
+        const float4 y = scaled(p.scale, at.total(dq[i]));
         if (t < p.L && at.leads()) store4((T *)p.dq + (((long long)bi * p.L + t) * p.H + h) * p.P + at.c, y);
     }
 }
@@ -309,14 +311,14 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) window_rows_dkv(Wind
             for (int i = 0; i < WR; ++i) {
                 const int s = s0 + warp * WR + i;
                 x[i] = t < last && s < s1 && sees(p, t, s) ? expf(p.scale * x[i] - lse_t) : 0.f;
-                dp[i] = x[i] != 0.f ? p.scale * x[i] * (dp[i] - D_t) : 0.f;
+                dp[i] = x[i] != 0.f ? x[i] * (dp[i] - D_t) : 0.f;
             }
             sums(x, dO, pitch, at, dv);
             sums(dp, Q, pitch, at, dk);
         }
     }
 #pragma unroll
-    for (int i = 0; i < WR; ++i) dk[i] = at.total(dk[i]), dv[i] = at.total(dv[i]);
+    for (int i = 0; i < WR; ++i) dk[i] = scaled(p.scale, at.total(dk[i])), dv[i] = at.total(dv[i]);
     if (splits == 1) {
 #pragma unroll
         for (int i = 0; i < WR; ++i) {

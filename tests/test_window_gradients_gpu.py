@@ -121,3 +121,13 @@ def test_tiny_scales_of_large_scores(wd, bf16, simt, power):
     for a, b in scaled_alike(wd, bf16, simt, power):
         for n in ("o", "lse", "dv"):
             assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("bf16,simt", FORMS)
+@pytest.mark.parametrize("power", [53, 60])
+def test_gradients_at_tiny_scales(wd, bf16, simt, power):
+    """dq and dk are the same times 2^-power, bit for bit while that is a normal number."""
+    for a, b in scaled_alike(wd, bf16, simt, power):
+        for n in ("dq", "dk"):
+            ok = a[n].float().abs() >= 2.0 ** (power - 120)
+            assert torch.equal((a[n].float() * 2.0 ** -power)[ok], b[n].float()[ok]), n
