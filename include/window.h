@@ -10,7 +10,8 @@
  *     p[t,s]    = softmax over the s that t sees of scale q[b,t,h,:] . k[b,s,g,:]
  *     o[b,t,h]  = sum_s p[t,s] v[b,s,g,:]
  *     lse[b,h,t] = log sum_s exp(scale q . k)
- * window >= seqlen is plain causal attention.  scale is finite, of either sign.  Tokens t >= V are absent:
+ * window >= seqlen is plain causal attention.  scale is of either sign; it and the scores scale q . k are finite, times log2(e) too.
+ * Tokens t >= V are absent:
  * nobody sees them, o, lse and every gradient there are 0, and their q, k, v, o, lse and do values are not
  * used (NaN and infinities there do no harm).  A NaN or an infinity in a present token's
  * k or v makes no promise for the tokens of its row up to 255 before it, which the tensor-core

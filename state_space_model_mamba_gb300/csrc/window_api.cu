@@ -54,8 +54,9 @@ ssd_status check_pointers(const void *const *req, const char *const *names, int 
     return SSD_OK;
 }
 
+// The kernels' exponents are of base 2: the scale has to stay finite times log2(e).
 ssd_status check_scale(float scale) {
-    return isfinite(scale) ? SSD_OK : fail(SSD_ERR_INVALID_ARG, "scale %g is not finite", (double)scale);
+    return isfinite(scale * kLog2e) ? SSD_OK : fail(SSD_ERR_INVALID_ARG, "scale %g is not finite in base 2", (double)scale);
 }
 
 ssd_status cuda_status(cudaError_t e) {

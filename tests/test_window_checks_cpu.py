@@ -50,3 +50,18 @@ def test_a_given_o_is_used():
     a, b = (ow.window_backward(x["q"], x["k"], x["v"], x["do"], 4, 1, 0.3, **kw) for kw in ({}, dict(o=o)))
     for name in a:
         np.testing.assert_allclose(a[name], b[name], rtol=0, atol=1e-13)
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38])
+def test_scales_past_fp32_in_base_2_are_refused(scale):
+    """A scale whose product with log2(e) overflows would make every score infinite."""
+    import ctypes
+    from state_space_model_mamba_gb300 import build, ssd, window
+    build.build()
+    lib, buf = window._lib(), ctypes.c_void_p(1 << 20)  # never dereferenced: the calls fail before a launch
+    d = [ctypes.byref(window.WindowDims(2, n, 4, 64, 2, 16, 4, 0, 0)) for n in (100, 1)]
+    for code in (0, 1):
+        assert lib.window_forward(d[0], code, buf, buf, buf, scale, None, buf, None, buf, 1 << 40, None) == ssd.SSD_ERR_INVALID_ARG
+        assert b"finite" in lib.ssd_last_error()
+        assert lib.window_backward(d[0], code, *([buf] * 6 + [scale, None] + [buf] * 4 + [1 << 40, None])) == ssd.SSD_ERR_INVALID_ARG
+        assert lib.window_step(d[1], code, buf, buf, buf, buf, scale, buf, buf, 2, None, buf, None) == ssd.SSD_ERR_INVALID_ARG
