@@ -38,9 +38,10 @@ struct GroupArgs {
     int groups, w;
 };
 
-// The activation and its derivative; for silu x s and s (1 + x (1 - s)) with s the logistic function of x.
-// 1 / (1 + exp(-x)) of a pair.  fp32 takes expf; bf16 the approximations of 2^x and of the reciprocal, off by some
-// 2^-21 of the result where its rounding is 2^-9.  exp(-x) past fp32 is infinite and the result 0.
+// The activation and its derivative; for silu x s and s (1 + x (1 - s)), for sigmoid s and s (1 - s), with s the logistic function of x.
+// s = 1 / (1 + exp(-x)) of a pair.  fp32 takes expf; bf16 the approximations of 2^x and of the reciprocal, off by some
+// 2^-21 of the result (2^-17 where exp(-x) is 10^35: x log2(e) as rounded) where its rounding is up to 2^-8.  exp(-x) past fp32 is infinite
+// and the result 0.
 template <typename T>
 __device__ __forceinline__ float2 logistic(float2 x) {
     if constexpr (sizeof(T) == 4) {
@@ -69,13 +70,15 @@ __device__ __forceinline__ void act2(int act, float2 x, float2 &a, float2 &d) {
         d = one;
         return;
     }
-    const float2 s = logistic<T>(x);
     if (act == NORM_ACT_SILU) {
+        const float2 s = logistic<T>(x), r = ffma2(s, minus, one);  // 1 - s
         a = fmul2(x, s);
-        d = fmul2(s, ffma2(x, ffma2(s, minus, one), one));
-    } else {  // 1 - s is the logistic function of -x; the difference would have no bits left where s is next to 1
-        a = s;
-        d = fmul2(s, logistic<T>(fmul2(x, minus)));
+        d = fmul2(s, ffma2(x, r, one));
+    } else {
+        // s of -|x|, so that 1 - s keeps its bits (where s is next to 1 the difference has none left); of x it is one of the two
+        const float2 s = logistic<T>(make_float2(-fabsf(x.x), -fabsf(x.y))), r = ffma2(s, minus, one);
+        a = make_float2(x.x > 0.f ? r.x : s.x, x.y > 0.f ? r.y : s.y);
+        d = fmul2(s, r);
     }
 }
 
