@@ -33,7 +33,6 @@ namespace ssd {
 namespace delta {
 
 constexpr int kChunk = 64;
-constexpr int kSMs = 152;
 // e^gamma, e^(gamma_C - gamma), beta; then pairs gamma log2(e) as hi and lo
 constexpr int kGates = 5 * kChunk * 4;
 // forward: run ks of a part: its first byte and its length; the 16-byte piece of row i (0 .. 127), columns 8 c .. + 7

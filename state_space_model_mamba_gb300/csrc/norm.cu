@@ -319,7 +319,6 @@ __global__ void __launch_bounds__(1024) rms_dweight_reduce(const float *part, fl
 
 // ------------------------------------------------------------------ host side
 constexpr long long kMaxD = 16384;
-constexpr int kSMs = 152;
 constexpr int kBwdBlocks = 4 * kSMs;  // the most whose partial rows the workspace holds
 
 // Blocks of a kernel that the SMs hold at once.  A grid of just these walks the rows: one of 8 blocks per SM where

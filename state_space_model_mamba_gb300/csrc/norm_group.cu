@@ -21,7 +21,6 @@ namespace {
 
 using namespace norm_rows;
 
-constexpr int kSMs = 152;
 constexpr long long kMaxD = 16384;
 
 struct GroupArgs {

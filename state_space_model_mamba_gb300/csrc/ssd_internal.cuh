@@ -71,6 +71,7 @@ struct Params {
 //   [kStatusValidLen]  number of valid_len entries outside [0, seqlen] (clamped)
 //   [kStatusNonFinite] non-finite elements seen by the SSD_FLAG_CHECK_FINITE check
 constexpr int kStatusCode = 0, kStatusValidLen = 1, kStatusNonFinite = 2, kStatusWords = 4;
+constexpr int kSMs = 152;  // of the GPU: what grids and shares are cut for
 
 // ---------------------------------------------------------------- small helpers
 // valid_len[bi] clamped to [0, L] (an entry outside is counted by K1, below).

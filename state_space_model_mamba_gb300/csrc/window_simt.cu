@@ -360,7 +360,7 @@ long long blocks(const WindowParams &p, int heads, int rows) { return (long long
 // Four rows a warp read a tile for twice as many, and take twice as long over it: where they leave a block for every SM
 // (fp32, heads of 64, window 256, forward, two and four rows: 1200 tokens of 24 heads 144 and 115 us, 600 of 8 heads 28 and
 // 26.5, of 4 heads 18 and 26).
-bool four_rows(const WindowParams &p, int heads) { return blocks(p, heads, 32) >= 152; }
+bool four_rows(const WindowParams &p, int heads) { return blocks(p, heads, 32) >= kSMs; }
 constexpr int most_bytes(int rows) { return (rows + kTile) * 2 * 132 * 4; }  // asked for once, for every width
 
 template <typename T, int WR>
@@ -389,7 +389,7 @@ cudaError_t backward_kv(const WindowParams &p, cudaStream_t s) {
     const long long units = blocks(p, p.G, rows), seen = p.sinks || p.L - p.W < rows ? p.L : p.W + rows;
     const long long tiles = p.hpg * ((seen + kTile - 1) / kTile);
     int splits = 1;
-    while (splits < 8 && 2 * splits <= tiles && (units * splits < 304 || tiles >= 128 * splits)) splits *= 2;
+    while (splits < 8 && 2 * splits <= tiles && (units * splits < 2 * kSMs || tiles >= 128 * splits)) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute cluster = {};
     cluster.id = cudaLaunchAttributeClusterDimension;

@@ -8,9 +8,9 @@
 // them), its warps take tiles of 16 rows.  In bf16 the products run on mma.sync.m16n8k16
 // straight from the loaded registers: the order of a product's inner index is free, so a thread's
 // fragments are the 16-byte pieces that it loads, and the scores' accumulators are the next product's
-// operand.  Probabilities are rounded to bf16 there (2^-9 of each, averaged over the rows; sums stay
-// fp32).  Few requests are split over the blocks of a cluster, which join their sums through
-// distributed shared memory in the cluster's order: one launch, no workspace, fixed order of sums.
+// operand.  Probabilities are rounded to bf16 there (2^-8 of each at most; sums stay fp32).  Few
+// requests are split over the blocks of a cluster, which join their sums through distributed
+// shared memory in the cluster's order: one launch, no workspace, fixed order of sums.
 // The new token's own row is taken from the arguments by every block, so the write of its entry
 // races with nobody.
 #include <cooperative_groups.h>
@@ -389,7 +389,7 @@ cudaError_t launch_clusters(K kernel, const RingParams &p, int heads_a_block, in
     // Two blocks a SM while each keeps 64 rows.  A block's beginning and end are some 7 us, so that halves of full ones do not pay
     // (192 requests of up to 1028 rows: 127 us, in halves 151), nor do blocks of two warps (144) or one (142), nor
     // clusters of 16 for one request.
-    while (splits < 8 && units * splits < 304 && entries / (2 * splits) >= 64) splits *= 2;
+    while (splits < 8 && units * splits < 2 * kSMs && entries / (2 * splits) >= 64) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * splits));
     cfg.blockDim = dim3(kThreads);

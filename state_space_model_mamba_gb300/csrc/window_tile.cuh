@@ -9,7 +9,7 @@
 #pragma once
 #include <cuda.h>
 
-#include "delta_chunk.cuh"  // encode_tiles, kSMs
+#include "delta_chunk.cuh"  // encode_tiles
 #include "delta_mma.cuh"
 #include "window_internal.cuh"
 
@@ -23,7 +23,6 @@ using tc::mbar_wait;
 using tc::smem_u32;
 
 constexpr int kTileRows = 128;
-using delta::kSMs;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 inline bool tile_supported(const window_dims &d, ssd_dtype t, bool backward) {
@@ -35,8 +34,8 @@ __device__ __forceinline__ int row_token(int r, uint32_t m) { return (int)((r * 
 __host__ __device__ __forceinline__ uint32_t row_magic(int R) { return (65536u + R - 1) / R; }
 
 // True in one lane of a converged warp.  Where products and copies are issued behind this instruction the compiler knows
-// that one lane is left and takes their operands as they are; behind `lane == 0` it wraps each product in some 400
-// bytes of code, and the issuing warp took 104 to 150 cycles for what the tensor core does in 64.
+// that one lane is left and takes their operands as they are; behind `lane == 0` the issuing warp took 104 to 150 cycles for
+// a product that the tensor core does in 64.
 __device__ __forceinline__ bool elect() {
     uint32_t one;
     asm volatile(
