@@ -8,7 +8,7 @@
 // their keys came to the end of both at once, and stood still for a fifth of an item).  S and P have columns of their own in
 // a block's half of tensor memory, so that the next S is made as soon as the last one is in registers: 256 columns hold S, P and
 // O with 80 keys a tile where O has 128 columns.  Where it has 64 there would be room for more, but a thread's 96 scores leave
-// it too few registers (8 padded rows of up to 4096, 64 heads of 64: 526 us with 96 keys, 469 with 80).
+// it too few registers (8 padded rows of 1024 to 4096, 64 heads of 64: 481 us of kernel with 80 keys, a tenth more with 96).
 // The row maximum is followed lazily: a row's reference only moves to it, and O is only rescaled, where a tile's P add up to
 // more than 2^8, so P <= 256 and the passes over O are rare; sums are fp32 and do not care.  Other tiles do not
 // look for their maximum (2 x 8192 tokens of 40 heads of 128, window 2048: 437 us, 413 without).

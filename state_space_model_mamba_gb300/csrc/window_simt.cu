@@ -12,7 +12,7 @@
 // among the blocks of a cluster, whose sums are added in the blocks' order).
 // Every sum has one order.  What bounds them at the sizes that fp32 is for (gradient checks) is
 // the chain of a tile's scores, shuffles and sums: at 129 tokens of 4 heads of 32, window 48, 8 us forward and 22 backward in two
-// kernels; at 2 x 4096 tokens of 8 heads of 64, window 1024, 0.82 ms and 2.7, a quarter of the fp32 rate.
+// kernels; at 2 x 4096 tokens of 8 heads of 64, window 1024, 0.81 ms and 2.6, a quarter of the fp32 rate.
 #include <cooperative_groups.h>
 
 #include "window_internal.cuh"
